@@ -71,7 +71,10 @@ enum {
   PA_DEVERR_CONTEXT_LEN = 2,  /* context length < 0 or > max_blocks_per_seq*block_size */
   PA_DEVERR_SLOT = 3,         /* slot_mapping entry >= num_blocks*block_size            */
   PA_DEVERR_TIMEOUT = 4,      /* a bounded wait on a shared-memory barrier expired      */
-  PA_DEVERR_QUERY_RANGE = 5   /* bad q_start / chunk length in chunked prefill          */
+  PA_DEVERR_QUERY_RANGE = 5,  /* bad q_start / chunk length in chunked prefill          */
+  PA_DEVERR_POSITION = 6,     /* rotary position outside [0, max_position)              */
+  PA_DEVERR_SCORE_ROW = 7,    /* score row outside the score array, or used twice       */
+  PA_DEVERR_KEEP = 8          /* keep list: bad count, base, or an entry out of range   */
 };
 
 typedef struct CUstream_st* pa_stream; /* identical to cudaStream_t */
@@ -481,6 +484,172 @@ int pa_decode_noalloc(const void* q, const void* k_cache, const void* v_cache, c
                       int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int q_heads,
                       int kv_heads, int head_dim, int block_size, int num_blocks, float scale,
                       int split_tokens, void* out, pa_dtype dtype, pa_stream stream);
+
+/* ----------------------------------------------------------------------------
+ * pa_norm_rope_and_cache - what stands between the query/key/value projection
+ * and the cache, in one pass: per-head norm, rotary position, and the writes of
+ * pa_reshape_and_cache.
+ *
+ * For token i, every query head x = q[i][h] and key head x = k[i][g]:
+ *   norm   (weight not NULL)  x_d <- x_d * rsqrt(mean_d(x_d^2) + eps) * weight_d
+ *   rotate the first rot_dim elements: pair p of rot_dim/2 is elements
+ *          (p, p + rot_dim/2), or (2p, 2p+1) if interleaved != 0;
+ *          (a, b) <- (a cos - b sin, b cos + a sin) with
+ *          cos = cos_sin[pos][p], sin = cos_sin[pos][rot_dim/2 + p],
+ *          pos = positions[axis(p)][i]
+ * computed in fp32 and rounded once.  Queries go to q_out, keys and values
+ * (values bit-exactly) to slot slot_mapping[i] of the caches.  A position is
+ * any number of the table, not the slot's place in its sequence: the nodes of
+ * a drafted tree at one depth share it, and a cache whose tokens were moved
+ * (pa_compact_kv) keeps the rotations its keys were written with.
+ *   q, k, v       [num_tokens][heads][head_dim], each token's heads
+ *                 contiguous, tokens *_stride elements apart (a multiple of 8,
+ *                 at least heads*head_dim): rows of one fused projection will do
+ *   q_weight, k_weight  [head_dim] in dtype, or NULL: no norm
+ *   positions     int32 [num_axes][num_tokens], num_axes 1 to 3 (for images and
+ *                 video: time, height, width)
+ *   sections      HOST int [num_axes], sum rot_dim/2: pairs [0, s0) turn by axis
+ *                 0, the next s1 by axis 1, ...; NULL with one axis
+ *   cos_sin       fp32 [max_position][rot_dim]: cosines, then sines
+ *   rot_dim       a multiple of 16, 16 <= rot_dim <= head_dim
+ *   slot_mapping  int32 [num_tokens] as pa_reshape_and_cache (distinct, < 0: the
+ *                 token's K/V are not written; its query still is)
+ *   q_out         [num_tokens][q_heads][head_dim]; may be q itself when q's
+ *                 rows are contiguous, else it must not overlap the inputs
+ * A position outside the table records PA_DEVERR_POSITION (unless the slot is
+ * negative: padding) and nothing of that token is written.  A slot past the
+ * pool records PA_DEVERR_SLOT and the token's K/V are skipped.  num_tokens == 0
+ * is a no-op.
+ * ------------------------------------------------------------------------- */
+int pa_norm_rope_and_cache(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, const void* q_weight, const void* k_weight, float eps,
+                           const int32_t* positions, int num_axes, const int32_t* sections, const float* cos_sin,
+                           int max_position, int rot_dim, int interleaved, const int32_t* slot_mapping,
+                           int num_tokens, int q_heads, void* q_out, void* k_cache, void* v_cache, int num_blocks,
+                           int block_size, int kv_heads, int head_dim, pa_dtype dtype, pa_stream stream);
+
+/* ----------------------------------------------------------------------------
+ * pa_verify_tree - the verify attention when the draft is a tree.
+ *
+ * Request r drafted n = q_start[r+1] - q_start[r] tokens (at most 64), node j's
+ * K/V in the cache as token context_lens[r] - n + j.  Row i = q_start[r] + j
+ * (node j) attends
+ *     every token t < context_lens[r] - n, and
+ *     node m (token context_lens[r] - n + m) for each bit m < n of tree_mask[i]
+ * - for a drafted tree the node itself and its ancestors - and no other; bits
+ * from n on are ignored.  A row that sees nothing gives zeros.  A node's K/V
+ * never reach a row that does not see it, whatever they hold (stale slots of
+ * padding nodes may hold NaN).  Ragged batches are packed: a request may have
+ * no rows.  pa_verify_decode is the chain (mask bits 0..j).
+ *   q, out        [total_q][q_heads][head_dim]
+ *   q_start       int32 [num_reqs + 1], non-decreasing, q_start[num_reqs] <= total_q
+ *   tree_mask     uint64 [total_q]
+ *   max_q_len     host-side bound of n, 1..64 (sizes the grid and the scratch)
+ *   split_tokens  0 = the library's choice; else a multiple of 128: the context
+ *                 is attended in partitions of that size, merged by log-sum-exp
+ *   workspace     at least pa_verify_tree_workspace_size(...) bytes (may be NULL
+ *                 when that is 0)
+ * q_heads / kv_heads up to 16.  Rows of q past q_start[num_reqs] are left as
+ * they were in out.  A q_start that decreases or passes total_q, n > max_q_len
+ * or a context shorter than n records PA_DEVERR_QUERY_RANGE, a context past the
+ * table PA_DEVERR_CONTEXT_LEN; the request is skipped.
+ * pa_verify_tree_split_tokens: the partition size of such a call (negative: a
+ * pa_status error).
+ * ------------------------------------------------------------------------- */
+int pa_verify_tree_split_tokens(int num_reqs, int max_q_len, int q_heads, int kv_heads, int max_blocks_per_seq,
+                                int block_size, int split_tokens);
+
+size_t pa_verify_tree_workspace_size(int num_reqs, int total_q, int max_q_len, int q_heads, int kv_heads,
+                                     int head_dim, int max_blocks_per_seq, int block_size, int split_tokens);
+
+int pa_verify_tree(const void* q, const int32_t* q_start, const uint64_t* tree_mask, const int32_t* context_lens,
+                   const void* k_cache, const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
+                   int num_reqs, int total_q, int max_q_len, int q_heads, int kv_heads, int head_dim, int block_size,
+                   int num_blocks, float scale, int split_tokens, void* workspace, size_t workspace_bytes, void* out,
+                   pa_dtype dtype, pa_stream stream);
+
+/* ----------------------------------------------------------------------------
+ * pa_decode_accumulate - pa_decode that also adds up the attention each cached
+ * token receives, the score by which pa_evict_select later chooses.
+ *
+ * out as pa_decode; and for every token t < context_lens[r] and KV head g
+ *     scores_out[row][g][t] = scores[row][g][t] + sum over the query heads h of
+ *                             group g of softmax(s_h)_t,   row = score_rows[r]
+ * in fp32, each entry by one thread in a fixed order (repeatable bit for bit).
+ * Entries of other rows and from context_lens[r] on are left as they were; a
+ * token appended to a sequence must find zero there (a new sequence's row is
+ * zeroed by the caller; pa_compact_kv leaves zeros behind what it keeps).
+ *   scores, scores_out  fp32 [num_rows][kv_heads][score_len]; the same array or
+ *                 not overlapping; score_len >= max_blocks_per_seq * block_size
+ *                 or at least every context (a longer one records
+ *                 PA_DEVERR_CONTEXT_LEN, and its tokens from score_len on get no
+ *                 score)
+ *   score_rows    int32 [num_seqs], or NULL: row r.  A negative row: the request
+ *                 keeps no score.  A row >= num_rows, or one that an earlier
+ *                 request of the call has, records PA_DEVERR_SCORE_ROW and the
+ *                 request keeps no score either.
+ *   workspace     at least pa_decode_accumulate_workspace_size(...) bytes: the
+ *                 partials, and the logits of the call
+ * Everything else as pa_decode.
+ * ------------------------------------------------------------------------- */
+size_t pa_decode_accumulate_workspace_size(int num_seqs, int q_heads, int kv_heads, int head_dim,
+                                           int max_blocks_per_seq, int block_size, int split_tokens);
+
+int pa_decode_accumulate(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                         int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int q_heads, int kv_heads,
+                         int head_dim, int block_size, int num_blocks, float scale, int split_tokens,
+                         const float* scores, const int32_t* score_rows, int num_rows, int score_len,
+                         float* scores_out, void* workspace, size_t workspace_bytes, void* out, pa_dtype dtype,
+                         pa_stream stream);
+
+/* ----------------------------------------------------------------------------
+ * pa_evict_select - which tokens a budget keeps, per request and KV head.
+ *
+ * With L = context_lens[r] and budget = sink + heavy + recent: all L tokens if
+ * L <= budget; else the first `sink`, the last `recent`, and of those between
+ * the `heavy` with the largest scores[row][g][t] (equal scores: the lower t
+ * first; a NaN counts below every number), in ascending order of t.
+ *   keep          int32 [num_seqs][kv_heads][budget]; entries from keep_lens[r]
+ *                 on are -1
+ *   keep_lens     int32 [num_seqs]: min(L, budget), 0 for a refused request
+ *   scores, score_rows, num_rows, score_len as pa_decode_accumulate, but rows
+ *                 may repeat; a row outside [0, num_rows) records
+ *                 PA_DEVERR_SCORE_ROW, a context outside [0, score_len]
+ *                 PA_DEVERR_CONTEXT_LEN, and the request keeps nothing
+ * sink, heavy, recent >= 0, budget >= 1.
+ * ------------------------------------------------------------------------- */
+int pa_evict_select(const float* scores, const int32_t* score_rows, int num_rows, int kv_heads, int score_len,
+                    const int32_t* context_lens, int num_seqs, int sink, int heavy, int recent, int32_t* keep,
+                    int32_t* keep_lens, pa_stream stream);
+
+/* ----------------------------------------------------------------------------
+ * pa_compact_kv - move the kept tokens of each sequence together, in place.
+ *
+ * For request r, KV head g and i < n = keep_lens[r], with b = base[r]:
+ *     token b + i of the sequence becomes token b + keep[r][g][i]
+ * (K and V, bit-exactly, and its score), all moves of a head as if at once.
+ * After an eviction b = 0 and keep is pa_evict_select's, each head its own
+ * list; after a tree's verify b = L - n_drafted and keep is the accepted path,
+ * one list for all heads.  Then the sequence has b + n tokens
+ * (pa_alloc_compact does the bookkeeping; block_tables are those of before it).
+ *   keep          int32 [num_seqs][keep_heads][max_keep], keep_heads 1 (one list
+ *                 for all heads) or kv_heads; i <= keep[i] < context_lens[r] - b
+ *                 (any ascending list of tokens is)
+ *   base          int32 [num_seqs], or NULL: 0
+ *   scores        fp32 [num_rows][kv_heads][score_len] or NULL; entries
+ *                 [b + n, context_lens[r]) of the row become 0.  score_rows as
+ *                 pa_decode_accumulate.
+ * The blocks of tokens [b, b + n) must be private to their sequence (copy
+ * shared ones first: pa_alloc_cow, pa_copy_blocks).  An entry out of range
+ * records PA_DEVERR_KEEP and is skipped (a count outside [0, max_keep], a base
+ * outside [0, L] or base + count > L: the request), a bad block id
+ * PA_DEVERR_BLOCK_ID, a context outside the table PA_DEVERR_CONTEXT_LEN.
+ * ------------------------------------------------------------------------- */
+int pa_compact_kv(void* k_cache, void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
+                  const int32_t* context_lens, const int32_t* keep, int keep_heads, int max_keep,
+                  const int32_t* keep_lens, const int32_t* base, int num_seqs, int num_blocks, int block_size,
+                  int kv_heads, int head_dim, pa_dtype dtype, float* scores, const int32_t* score_rows, int num_rows,
+                  int score_len, pa_stream stream);
 
 /* Read and clear the calling device's error word.  Synchronises `stream`.
  * *host_code receives the PA_DEVERR_* code (0 = none).  Returns

@@ -32,6 +32,9 @@ PA_DEVERR_CONTEXT_LEN = 2
 PA_DEVERR_SLOT = 3
 PA_DEVERR_TIMEOUT = 4
 PA_DEVERR_QUERY_RANGE = 5
+PA_DEVERR_POSITION = 6
+PA_DEVERR_SCORE_ROW = 7
+PA_DEVERR_KEEP = 8
 
 
 class LibraryMissing(RuntimeError):
@@ -97,6 +100,16 @@ PROTOTYPES = {
     "pa_decode_shared_prefix_split_tokens": (_I, [_I, _I, _I, _I]),
     "pa_decode_shared_prefix": (_I, [_P, _P, _P, _P, _I, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P, _I,
                                      _P, _P]),
+    "pa_norm_rope_and_cache": (_I, [_P, _P, _P, C.c_int64, C.c_int64, C.c_int64, _P, _P, _F, _P, _I, _I32P, _P, _I, _I,
+                                    _I, _P, _I, _I, _P, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "pa_verify_tree_split_tokens": (_I, [_I, _I, _I, _I, _I, _I, _I]),
+    "pa_verify_tree_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),
+    "pa_verify_tree": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P, _I, _P]),
+    "pa_decode_accumulate_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
+    "pa_decode_accumulate": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _I, _I, _P, _P, _SZ,
+                                  _P, _I, _P]),
+    "pa_evict_select": (_I, [_P, _P, _I, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P]),
+    "pa_compact_kv": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I, _I, _P]),
     "pa_get_device_error": (_I, [_I32P, _P]),
     "pa_alloc_create": (_I, [_I, _I, _I32P, C.POINTER(_P)]),
     "pa_alloc_destroy": (None, [_P]),

@@ -44,6 +44,12 @@
 // tile, no Block Table.  Only tokens below the slot's mapped bound
 // (slot_tokens[slot], a multiple of 16) are ever loaded; a context past it
 // records PA_DEVERR_CONTEXT_LEN and the rest counts as empty.
+//
+// Logits (LOGITS, q_len = 1): each scaled score is also stored, fp32 in log2
+// units, token-major with the group's heads together ([token][group]), for the
+// pass that turns them into weights once the row's sum is known; that sum is
+// taken over the unrounded probabilities (the output's own sum is over those
+// rounded for the P.V product, up to 2^-9 off where one token takes most).
 #include <cuda_pipeline.h>
 #include <float.h>
 
@@ -78,7 +84,7 @@ struct DecodeSmem {
   static constexpr int MAX_BYTES = TAB_OFF + UNITS * kMaxTableEntries * 4 + 1024;
 };
 
-template <int D, int BSUB, int NT, typename T, int WARPS, int STAGES, bool CONTIG, int CW>
+template <int D, int BSUB, int NT, typename T, int WARPS, int STAGES, bool CONTIG, int CW, bool LOGITS>
 __global__ void __launch_bounds__(WARPS * 32)
     decode_partial_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                           const DecodeParams p) {
@@ -248,6 +254,7 @@ __global__ void __launch_bounds__(WARPS * 32)
   };
 
   float m[NT][2], lp[NT][2];
+  float lx[LOGITS ? NT : 1][2] = {};  // LOGITS: the sum of the probabilities before they are rounded
   float acc[NT][KSTEPS][4];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -318,6 +325,20 @@ __global__ void __launch_bounds__(WARPS * 32)
       const float s1 = t0 < lim[nt][1] ? sacc[nt][1] * sl2 : -INFINITY;
       const float s2 = t0 + 8 < lim[nt][0] ? sacc[nt][2] * sl2 : -INFINITY;
       const float s3 = t0 + 8 < lim[nt][1] ? sacc[nt][3] * sl2 : -INFINITY;
+      if constexpr (LOGITS) {
+        // columns n, n+1 (heads of the group) of tokens t0 and t0 + 8
+        const int n = col0 + nt * 8 + 2 * (lane & 3);
+        float* lg = p.logits + (((size_t)r * p.kv_heads + h) * cap + t0) * G + n;
+        if (n + 1 < G && (G & 1) == 0) {
+          if (t0 < tok1) *reinterpret_cast<float2*>(lg) = make_float2(s0, s1);
+          if (t0 + 8 < tok1) *reinterpret_cast<float2*>(lg + 8 * G) = make_float2(s2, s3);
+        } else {
+          if (n < G && t0 < tok1) lg[0] = s0;
+          if (n + 1 < G && t0 < tok1) lg[1] = s1;
+          if (n < G && t0 + 8 < tok1) lg[8 * G] = s2;
+          if (n + 1 < G && t0 + 8 < tok1) lg[8 * G + 1] = s3;
+        }
+      }
       float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) {
@@ -341,6 +362,10 @@ __global__ void __launch_bounds__(WARPS * 32)
         m[nt][1] = up1 ? mx1 : m[nt][1];
         lp[nt][0] *= al0;
         lp[nt][1] *= al1;
+        if constexpr (LOGITS) {
+          lx[nt][0] *= al0;
+          lx[nt][1] *= al1;
+        }
 #pragma unroll
         for (int mt = 0; mt < KSTEPS; ++mt) {
           acc[nt][mt][0] *= al0;
@@ -358,6 +383,10 @@ __global__ void __launch_bounds__(WARPS * 32)
       const uint32_t pk01 = Elem<T>::pack(p0, p1), pk23 = Elem<T>::pack(p2, p3);
       lp[nt][0] += Elem<T>::lo(pk01) + Elem<T>::lo(pk23);
       lp[nt][1] += Elem<T>::hi(pk01) + Elem<T>::hi(pk23);
+      if constexpr (LOGITS) {
+        lx[nt][0] += p0 + p2;
+        lx[nt][1] += p1 + p3;
+      }
       pb0[nt] = movmatrix_trans(pk01);
       pb1[nt] = movmatrix_trans(pk23);
     }
@@ -404,6 +433,13 @@ __global__ void __launch_bounds__(WARPS * 32)
       l += __shfl_xor_sync(0xffffffffu, l, 8);
       l += __shfl_xor_sync(0xffffffffu, l, 16);
       lp[nt][e] = l;
+      if constexpr (LOGITS) {
+        float x = lx[nt][e];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        lx[nt][e] = x;
+      }
     }
 
   if (nsplit == 1 && !p.always_partial) {
@@ -440,6 +476,7 @@ __global__ void __launch_bounds__(WARPS * 32)
           if (r0 == 0) {
             p.part_m[row * p.max_splits + slot] = m[nt][e];
             p.part_l[row * p.max_splits + slot] = lp[nt][e];
+            if constexpr (LOGITS) p.part_w[row * p.max_splits + slot] = lx[nt][e];
           }
         }
       }
@@ -590,12 +627,12 @@ __global__ void __launch_bounds__(256) lse_merge_warp_kernel(const MergeParams p
   }
 }
 
-template <int D, int BSUB, int NT, typename T, bool CONTIG = false, int CW = 1>
+template <int D, int BSUB, int NT, typename T, bool CONTIG = false, int CW = 1, bool LOGITS = false>
 cudaError_t launch_decode_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p,
                             cudaStream_t stream) {
   constexpr int W = kDecodeWarps, S = kDecodeStages;
   using L = DecodeSmem<D, BSUB, NT, T, W, S, CW>;
-  auto kern = decode_partial_kernel<D, BSUB, NT, T, W, S, CONTIG, CW>;
+  auto kern = decode_partial_kernel<D, BSUB, NT, T, W, S, CONTIG, CW, LOGITS>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -633,6 +670,25 @@ cudaError_t launch_decode_nt(const CUtensorMap& kmap, const CUtensorMap& vmap, c
   return cudaErrorInvalidValue;
 }
 
+template <int D, int BSUB, typename T>
+cudaError_t launch_logits_nt(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p,
+                             cudaStream_t stream) {
+  if (p.group <= 8) return launch_decode_t<D, BSUB, 1, T, false, 1, true>(kmap, vmap, p, stream);
+  if (p.group <= 16) return launch_decode_t<D, BSUB, 2, T, false, 1, true>(kmap, vmap, p, stream);
+  return cudaErrorInvalidValue;
+}
+
+template <int D, typename T>
+cudaError_t launch_logits_bs(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p, int bsub,
+                             cudaStream_t stream) {
+  switch (bsub) {
+    case 4: return launch_logits_nt<D, 4, T>(kmap, vmap, p, stream);
+    case 8: return launch_logits_nt<D, 8, T>(kmap, vmap, p, stream);
+    case 16: return launch_logits_nt<D, 16, T>(kmap, vmap, p, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
 template <int D, typename T>
 cudaError_t launch_decode_bs(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p, int bsub,
                              cudaStream_t stream) {
@@ -656,6 +712,18 @@ cudaError_t launch_decode_partial(const CUtensorMap& kmap, const CUtensorMap& vm
     return dt == PA_BF16 ? launch_decode_bs<64, __nv_bfloat16>(kmap, vmap, p, bsub, stream)
                          : launch_decode_bs<64, __half>(kmap, vmap, p, bsub, stream);
   }
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_decode_logits(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p, int head_dim,
+                                 int bsub, pa_dtype dt, cudaStream_t stream) {
+  if (p.q_len != 1 || !p.always_partial || !p.logits) return cudaErrorInvalidValue;
+  if (head_dim == 128)
+    return dt == PA_BF16 ? launch_logits_bs<128, __nv_bfloat16>(kmap, vmap, p, bsub, stream)
+                         : launch_logits_bs<128, __half>(kmap, vmap, p, bsub, stream);
+  if (head_dim == 64)
+    return dt == PA_BF16 ? launch_logits_bs<64, __nv_bfloat16>(kmap, vmap, p, bsub, stream)
+                         : launch_logits_bs<64, __half>(kmap, vmap, p, bsub, stream);
   return cudaErrorInvalidValue;
 }
 

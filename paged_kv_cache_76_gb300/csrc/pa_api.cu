@@ -830,6 +830,384 @@ int pa_decode_shared_prefix(const void* q, const void* k_cache, const void* v_ca
   return cuda_status(launch_lse_merge(mp, head_dim, dtype, cs));
 }
 
+int pa_norm_rope_and_cache(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride,
+                           int64_t v_stride, const void* q_weight, const void* k_weight, float eps,
+                           const int32_t* positions, int num_axes, const int32_t* sections, const float* cos_sin,
+                           int max_position, int rot_dim, int interleaved, const int32_t* slot_mapping,
+                           int num_tokens, int q_heads, void* q_out, void* k_cache, void* v_cache, int num_blocks,
+                           int block_size, int kv_heads, int head_dim, pa_dtype dtype, pa_stream stream) {
+  int st = check_kv_shape(num_blocks, block_size, kv_heads, head_dim, dtype);
+  if (st != PA_OK) return st;
+  if (num_tokens < 0 || q_heads <= 0 || q_heads > 16384 || !(eps >= 0.f) || !std::isfinite(eps)) return PA_ERR_INVALID;
+  if (rot_dim < 16 || rot_dim % 16 != 0 || rot_dim > head_dim || max_position <= 0) return PA_ERR_INVALID;
+  if (num_axes < 1 || num_axes > 3 || (num_axes > 1 && !sections)) return PA_ERR_INVALID;
+  const int64_t qrow = (int64_t)q_heads * head_dim, krow = (int64_t)kv_heads * head_dim;
+  if (q_stride < qrow || k_stride < krow || v_stride < krow || q_stride % 8 || k_stride % 8 || v_stride % 8)
+    return PA_ERR_INVALID;
+  NormRopeParams p{};
+  p.sec_end[0] = p.sec_end[1] = rot_dim / 2;
+  if (sections) {
+    int64_t sum = 0;
+    for (int a = 0; a < num_axes; ++a) {
+      if (sections[a] < 0) return PA_ERR_INVALID;
+      sum += sections[a];
+      if (a < 2) p.sec_end[a] = (int)(sum < rot_dim / 2 ? sum : rot_dim / 2);
+    }
+    if (sum != rot_dim / 2) return PA_ERR_INVALID;
+  }
+  if (num_tokens == 0) return PA_OK;
+  if (!q || !k || !v || !positions || !cos_sin || !slot_mapping || !q_out || !k_cache || !v_cache)
+    return PA_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(cos_sin) || !aligned16(q_out) ||
+      !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(q_weight) || !aligned16(k_weight))
+    return PA_ERR_INVALID;
+  if (q_out == q && q_stride != qrow) return PA_ERR_INVALID;
+  int* err = device_error_ptr();
+  if (!err) return PA_ERR_CUDA;
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q_weight = q_weight;
+  p.k_weight = k_weight;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.slots = slot_mapping;
+  p.q_out = q_out;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.err = err;
+  p.num_slots = (int64_t)num_blocks * block_size;
+  p.num_tokens = num_tokens;
+  p.q_heads = q_heads;
+  p.kv_heads = kv_heads;
+  p.num_axes = num_axes;
+  p.max_position = max_position;
+  p.rot_dim = rot_dim;
+  p.interleaved = interleaved != 0;
+  p.eps = eps;
+  return cuda_status(launch_norm_rope(p, head_dim, dtype, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+// Workspace of pa_decode_accumulate: the partials of every partition (and the
+// sums of their unrounded probabilities), then the logits [num_seqs][kv_heads][cap][group].
+struct AccumulateSetup {
+  int split, max_splits, cap;
+  DecodeWorkspace ws;
+  size_t w_off, logits_off, bytes;
+};
+
+int accumulate_setup(int num_seqs, int q_heads, int kv_heads, int head_dim, int max_blocks_per_seq, int block_size,
+                     int split_tokens, AccumulateSetup* s) {
+  if (num_seqs < 0 || num_seqs > 65535 || kv_heads <= 0 || q_heads <= 0 || q_heads % kv_heads != 0 || head_dim <= 0)
+    return PA_ERR_INVALID;
+  DecodeSetup d;
+  const int st = decode_setup(num_seqs, q_heads, head_dim, max_blocks_per_seq, block_size, split_tokens, &d);
+  if (st != PA_OK) return st;
+  s->split = d.split;
+  s->max_splits = d.max_splits;
+  s->cap = max_blocks_per_seq * block_size;
+  s->ws = decode_workspace_layout(num_seqs, q_heads, head_dim, d.max_splits);
+  s->w_off = s->ws.bytes;
+  s->logits_off = s->w_off + (((size_t)num_seqs * q_heads * d.max_splits * sizeof(float) + 255) & ~size_t(255));
+  s->bytes = s->logits_off + (size_t)num_seqs * q_heads * s->cap * sizeof(float);
+  return PA_OK;
+}
+
+}  // namespace
+
+size_t pa_decode_accumulate_workspace_size(int num_seqs, int q_heads, int kv_heads, int head_dim,
+                                           int max_blocks_per_seq, int block_size, int split_tokens) {
+  AccumulateSetup s;
+  if (accumulate_setup(num_seqs, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size, split_tokens, &s) !=
+      PA_OK)
+    return 0;
+  return s.bytes;
+}
+
+int pa_decode_accumulate(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                         int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int q_heads, int kv_heads,
+                         int head_dim, int block_size, int num_blocks, float scale, int split_tokens,
+                         const float* scores, const int32_t* score_rows, int num_rows, int score_len,
+                         float* scores_out, void* workspace, size_t workspace_bytes, void* out, pa_dtype dtype,
+                         pa_stream stream) {
+  int st = check_kv_shape(num_blocks, block_size, kv_heads, head_dim, dtype);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || num_seqs > 65535 || q_heads <= 0 || q_heads % kv_heads != 0 || q_heads / kv_heads > 16)
+    return PA_ERR_INVALID;
+  if (max_blocks_per_seq <= 0 || !std::isfinite(scale) || num_rows <= 0 || score_len <= 0) return PA_ERR_INVALID;
+  if ((int64_t)num_seqs * q_heads > (int64_t)INT32_MAX - 8) return PA_ERR_INVALID;
+  if (!score_rows && num_rows < num_seqs) return PA_ERR_INVALID;
+  AccumulateSetup s;
+  st = accumulate_setup(num_seqs, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size, split_tokens, &s);
+  if (st != PA_OK) return st;
+  if ((int64_t)s.max_splits * kv_heads > (int64_t)INT32_MAX) return PA_ERR_INVALID;
+  if (num_seqs == 0) return PA_OK;
+  if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out || !scores || !scores_out)
+    return PA_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(scores) ||
+      !aligned16(scores_out))
+    return PA_ERR_INVALID;
+  if (!workspace || workspace_bytes < s.bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+  CUtensorMap km, vm;
+  if (!kv_map(k_cache, num_blocks, block_size, kv_heads, head_dim, dtype, &km) ||
+      !kv_map(v_cache, num_blocks, block_size, kv_heads, head_dim, dtype, &vm))
+    return PA_ERR_CUDA;
+  int* err = device_error_ptr();
+  if (!err) return PA_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  DecodeParams p{};
+  p.q = q;
+  p.tables = block_tables;
+  p.lens = context_lens;
+  p.out = out;
+  p.part_o = reinterpret_cast<float*>(ws + s.ws.o_off);
+  p.part_m = reinterpret_cast<float*>(ws + s.ws.m_off);
+  p.part_l = reinterpret_cast<float*>(ws + s.ws.l_off);
+  p.part_w = reinterpret_cast<float*>(ws + s.w_off);
+  p.logits = reinterpret_cast<float*>(ws + s.logits_off);
+  p.err = err;
+  p.maxblk = max_blocks_per_seq;
+  p.num_seqs = num_seqs;
+  p.q_heads = q_heads;
+  p.kv_heads = kv_heads;
+  p.group = q_heads / kv_heads;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.split_tokens = s.split;
+  p.max_splits = s.max_splits;
+  p.grid_splits = s.max_splits;
+  p.tab_entries = s.split / block_size;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.q_len = 1;
+  p.always_partial = 1;
+  st = cuda_status(launch_decode_logits(km, vm, p, head_dim, block_size < 16 ? block_size : 16, dtype, cs));
+  if (st != PA_OK) return st;
+  MergeParams mp{};
+  mp.part_o = p.part_o;
+  mp.part_m = p.part_m;
+  mp.part_l = p.part_l;
+  mp.lens = context_lens;
+  mp.out = out;
+  mp.num_seqs = num_seqs;
+  mp.q_heads = q_heads;
+  mp.max_splits = s.max_splits;
+  mp.split_tokens = s.split;
+  mp.cap = s.cap;
+  mp.always = 1;
+  mp.q_len = 1;
+  st = cuda_status(launch_lse_merge(mp, head_dim, dtype, cs));
+  if (st != PA_OK) return st;
+  AccumulateParams ap{};
+  ap.logits = p.logits;
+  ap.part_m = p.part_m;
+  ap.part_w = p.part_w;
+  ap.lens = context_lens;
+  ap.scores = scores;
+  ap.scores_out = scores_out;
+  ap.score_rows = score_rows;
+  ap.err = err;
+  ap.num_seqs = num_seqs;
+  ap.q_heads = q_heads;
+  ap.kv_heads = kv_heads;
+  ap.group = p.group;
+  ap.max_splits = s.max_splits;
+  ap.split_tokens = s.split;
+  ap.cap = s.cap;
+  ap.num_rows = num_rows;
+  ap.score_len = score_len;
+  return cuda_status(launch_accumulate(ap, cs));
+}
+
+int pa_evict_select(const float* scores, const int32_t* score_rows, int num_rows, int kv_heads, int score_len,
+                    const int32_t* context_lens, int num_seqs, int sink, int heavy, int recent, int32_t* keep,
+                    int32_t* keep_lens, pa_stream stream) {
+  if (num_rows <= 0 || kv_heads <= 0 || kv_heads > 1024 || score_len <= 0 || num_seqs < 0 || num_seqs > 65535)
+    return PA_ERR_INVALID;
+  if (sink < 0 || heavy < 0 || recent < 0) return PA_ERR_INVALID;
+  const int64_t budget = (int64_t)sink + heavy + recent;
+  if (budget < 1 || budget > INT32_MAX) return PA_ERR_INVALID;
+  if (!score_rows && num_rows < num_seqs) return PA_ERR_INVALID;
+  if (num_seqs == 0) return PA_OK;
+  if (!scores || !context_lens || !keep || !keep_lens || !aligned16(scores) || !aligned16(keep)) return PA_ERR_INVALID;
+  int* err = device_error_ptr();
+  if (!err) return PA_ERR_CUDA;
+  EvictSelectParams p{};
+  p.scores = scores;
+  p.score_rows = score_rows;
+  p.lens = context_lens;
+  p.keep = keep;
+  p.keep_lens = keep_lens;
+  p.err = err;
+  p.num_rows = num_rows;
+  p.kv_heads = kv_heads;
+  p.score_len = score_len;
+  p.sink = sink;
+  p.heavy = heavy;
+  p.recent = recent;
+  return cuda_status(launch_evict_select(p, num_seqs, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+int pa_compact_kv(void* k_cache, void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
+                  const int32_t* context_lens, const int32_t* keep, int keep_heads, int max_keep,
+                  const int32_t* keep_lens, const int32_t* base, int num_seqs, int num_blocks, int block_size,
+                  int kv_heads, int head_dim, pa_dtype dtype, float* scores, const int32_t* score_rows, int num_rows,
+                  int score_len, pa_stream stream) {
+  int st = check_kv_shape(num_blocks, block_size, kv_heads, head_dim, dtype);
+  if (st != PA_OK) return st;
+  if (num_seqs < 0 || num_seqs > 65535 || max_blocks_per_seq <= 0 || max_keep <= 0) return PA_ERR_INVALID;
+  if (keep_heads != 1 && keep_heads != kv_heads) return PA_ERR_INVALID;
+  if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX) return PA_ERR_INVALID;
+  if (scores && (num_rows <= 0 || score_len <= 0 || (!score_rows && num_rows < num_seqs) || !aligned16(scores)))
+    return PA_ERR_INVALID;
+  if (num_seqs == 0) return PA_OK;
+  if (!k_cache || !v_cache || !block_tables || !context_lens || !keep || !keep_lens) return PA_ERR_INVALID;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return PA_ERR_INVALID;
+  int* err = device_error_ptr();
+  if (!err) return PA_ERR_CUDA;
+  CompactParams p{};
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.tables = block_tables;
+  p.lens = context_lens;
+  p.keep = keep;
+  p.keep_lens = keep_lens;
+  p.base = base;
+  p.scores = scores;
+  p.score_rows = score_rows;
+  p.err = err;
+  p.maxblk = max_blocks_per_seq;
+  p.cap = max_blocks_per_seq * block_size;
+  p.keep_heads = keep_heads;
+  p.max_keep = max_keep;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.kv_heads = kv_heads;
+  p.num_rows = num_rows;
+  p.score_len = score_len;
+  p.row_vecs = head_dim / 8;
+  return cuda_status(launch_compact_kv(p, num_seqs, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+
+constexpr int kTreeMaxNodes = 64;    // one mask word per node
+constexpr int kTreeSplitUnit = 128;  // partitions are whole key tiles
+constexpr int kTreeSplitMin = 512;
+
+struct TreeSetup {
+  int split, max_splits;
+  DecodeWorkspace ws;
+};
+
+int tree_setup(int num_reqs, int total_q, int max_q_len, int q_heads, int kv_heads, int head_dim,
+               int max_blocks_per_seq, int block_size, int split_tokens, TreeSetup* s) {
+  if (num_reqs < 0 || num_reqs > 65535 || total_q < 0 || max_q_len < 1 || max_q_len > kTreeMaxNodes || q_heads <= 0 ||
+      kv_heads <= 0 || q_heads % kv_heads != 0 || q_heads / kv_heads > 16 || head_dim <= 0 ||
+      max_blocks_per_seq <= 0 || block_size <= 0)
+    return PA_ERR_INVALID;
+  const int64_t cap = (int64_t)max_blocks_per_seq * block_size;
+  if (cap > INT32_MAX - kTreeSplitUnit || (int64_t)total_q * q_heads > INT32_MAX) return PA_ERR_INVALID;
+  const int64_t whole = (cap + kTreeSplitUnit - 1) / kTreeSplitUnit * kTreeSplitUnit;
+  int64_t split = split_tokens;
+  if (split_tokens == 0) {
+    // enough partitions that every SM has two CTAs of 64 rows
+    const int64_t units = (int64_t)num_reqs * kv_heads * (((int64_t)max_q_len * (q_heads / kv_heads) + 63) / 64);
+    const int64_t sms = sm_count() > 0 ? sm_count() : 152;
+    const int64_t want = units > 0 ? (2 * sms + units - 1) / units : 1;
+    split = ((cap + want - 1) / want + kTreeSplitUnit - 1) / kTreeSplitUnit * kTreeSplitUnit;
+    if (split < kTreeSplitMin) split = kTreeSplitMin;
+  }
+  if (split <= 0 || split % kTreeSplitUnit != 0) return PA_ERR_INVALID;
+  if (split > whole) split = whole;
+  s->split = (int)split;
+  s->max_splits = (int)((cap + split - 1) / split);
+  s->ws = s->max_splits > 1 ? decode_workspace_layout(total_q, q_heads, head_dim, s->max_splits)
+                            : DecodeWorkspace{0, 0, 0, 0};
+  return PA_OK;
+}
+
+}  // namespace
+
+int pa_verify_tree_split_tokens(int num_reqs, int max_q_len, int q_heads, int kv_heads, int max_blocks_per_seq,
+                                int block_size, int split_tokens) {
+  TreeSetup s;
+  const int st = tree_setup(num_reqs, 0, max_q_len, q_heads, kv_heads, 64, max_blocks_per_seq, block_size,
+                            split_tokens, &s);
+  return st != PA_OK ? st : s.split;
+}
+
+size_t pa_verify_tree_workspace_size(int num_reqs, int total_q, int max_q_len, int q_heads, int kv_heads,
+                                     int head_dim, int max_blocks_per_seq, int block_size, int split_tokens) {
+  TreeSetup s;
+  if (tree_setup(num_reqs, total_q, max_q_len, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size,
+                 split_tokens, &s) != PA_OK)
+    return 0;
+  return s.ws.bytes;
+}
+
+int pa_verify_tree(const void* q, const int32_t* q_start, const uint64_t* tree_mask, const int32_t* context_lens,
+                   const void* k_cache, const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq,
+                   int num_reqs, int total_q, int max_q_len, int q_heads, int kv_heads, int head_dim, int block_size,
+                   int num_blocks, float scale, int split_tokens, void* workspace, size_t workspace_bytes, void* out,
+                   pa_dtype dtype, pa_stream stream) {
+  int st = check_kv_shape(num_blocks, block_size, kv_heads, head_dim, dtype);
+  if (st != PA_OK) return st;
+  if (!std::isfinite(scale)) return PA_ERR_INVALID;
+  TreeSetup s;
+  st = tree_setup(num_reqs, total_q, max_q_len, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size,
+                  split_tokens, &s);
+  if (st != PA_OK) return st;
+  if (num_reqs == 0 || total_q == 0) return PA_OK;
+  if (!q || !q_start || !tree_mask || !context_lens || !k_cache || !v_cache || !block_tables || !out)
+    return PA_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) ||
+      (reinterpret_cast<uintptr_t>(tree_mask) & 7u))
+    return PA_ERR_INVALID;
+  if (s.ws.bytes > 0 && (!workspace || workspace_bytes < s.ws.bytes || !aligned16(workspace)))
+    return PA_ERR_WORKSPACE;
+  CUtensorMap km, vm;
+  if (!kv_map(k_cache, num_blocks, block_size, kv_heads, head_dim, dtype, &km) ||
+      !kv_map(v_cache, num_blocks, block_size, kv_heads, head_dim, dtype, &vm))
+    return PA_ERR_CUDA;
+  int* err = device_error_ptr();
+  if (!err) return PA_ERR_CUDA;
+  TreeParams p{};
+  p.q = q;
+  p.v_cache = v_cache;
+  p.q_start = q_start;
+  p.mask = tree_mask;
+  p.lens = context_lens;
+  p.tables = block_tables;
+  p.out = out;
+  p.err = err;
+  p.maxblk = max_blocks_per_seq;
+  p.num_reqs = num_reqs;
+  p.total_q = total_q;
+  p.max_q_len = max_q_len;
+  p.q_heads = q_heads;
+  p.kv_heads = kv_heads;
+  p.group = q_heads / kv_heads;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.split_tokens = s.split;
+  p.max_splits = s.max_splits;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (s.ws.bytes) {
+    p.part_o = reinterpret_cast<float*>(ws + s.ws.o_off);
+    p.part_m = reinterpret_cast<float*>(ws + s.ws.m_off);
+    p.part_l = reinterpret_cast<float*>(ws + s.ws.l_off);
+  }
+  return cuda_status(launch_verify_tree(km, vm, p, head_dim, block_size < 16 ? block_size : 16, dtype,
+                                        reinterpret_cast<cudaStream_t>(stream)));
+}
+
 int pa_selftest_wait_timeout(int wait_ms, pa_stream stream) {
   if (wait_ms < 1 || wait_ms > 2000) return PA_ERR_INVALID;
   int* err = device_error_ptr();

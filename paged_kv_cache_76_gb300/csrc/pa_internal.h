@@ -66,6 +66,11 @@ struct DecodeParams {
   const int32_t* slot_ids;
   const int32_t* slot_tokens;
   int num_slots, contig_len;
+  // launch_decode_logits: every column's scaled score (log2 units) of every
+  // token of the partition, [num_seqs][kv_heads][cap][group], and the sums of
+  // the unrounded probabilities, laid out as part_l
+  float* logits;
+  float* part_w;
 };
 
 struct MergeParams {
@@ -125,6 +130,9 @@ cudaError_t launch_decode_partial(const CUtensorMap& kmap, const CUtensorMap& vm
 cudaError_t launch_lse_merge(const MergeParams& p, int head_dim, pa_dtype dt, cudaStream_t stream);
 cudaError_t launch_decode_contig(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p,
                                  int head_dim, pa_dtype dt, cudaStream_t stream);
+// The decode partition pass (q_len 1, always_partial) that also stores p.logits.
+cudaError_t launch_decode_logits(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeParams& p,
+                                 int head_dim, int bsub, pa_dtype dt, cudaStream_t stream);
 cudaError_t launch_chunked_prefill(const CUtensorMap& kmap, const CUtensorMap& vmap, const PrefillParams& p,
                                    int head_dim, int bsub, pa_dtype dt, cudaStream_t stream);
 // tcgen05/TMEM kernel for blocks of >= 8 tokens (bsub >= 8): chunked prefill
@@ -160,5 +168,91 @@ cudaError_t launch_swap_blocks(const void* src_k, const void* src_v, void* dst_k
                                cudaStream_t stream);
 cudaError_t launch_copy_blocks(void* k_cache, void* v_cache, const int32_t* pairs, int num_pairs,
                                int num_blocks, int64_t block_bytes, int* err, cudaStream_t stream);
+
+
+// Norm, rotation and cache write of new tokens (pa_norm_rope_and_cache).
+struct NormRopeParams {
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_stride, k_stride, v_stride;  // elements between tokens
+  const void* q_weight;                  // null: no norm
+  const void* k_weight;
+  const int32_t* positions;  // [num_axes][num_tokens]
+  const float* cos_sin;      // [max_position][rot_dim]
+  const int32_t* slots;
+  void* q_out;
+  void* k_cache;
+  void* v_cache;
+  int* err;
+  int64_t num_slots;
+  int num_tokens, q_heads, kv_heads, num_axes, max_position, rot_dim, interleaved;
+  int sec_end[2];  // pairs before sec_end[0] turn by axis 0, before sec_end[1] by axis 1, the rest by axis 2
+  float eps;
+};
+cudaError_t launch_norm_rope(const NormRopeParams& p, int head_dim, pa_dtype dt, cudaStream_t stream);
+
+// Attention of drafted trees (pa_verify_tree).
+struct TreeParams {
+  const void* q;
+  const void* v_cache;  // for the rare nodes whose V is not finite
+  const int32_t* q_start;
+  const uint64_t* mask;  // [total_q]
+  const int32_t* lens;
+  const int32_t* tables;
+  void* out;
+  int* err;
+  int maxblk, num_reqs, total_q, max_q_len, q_heads, kv_heads, group, num_blocks, block_size;
+  int split_tokens, max_splits;  // partitions of the context; one: no scratch
+  float scale_log2;
+  float* part_o;  // [total_q * q_heads][max_splits][head_dim], as the decode partials
+  float* part_m;
+  float* part_l;
+};
+cudaError_t launch_verify_tree(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int head_dim,
+                               int bsub, pa_dtype dt, cudaStream_t stream);
+
+struct EvictSelectParams {
+  const float* scores;  // [num_rows][kv_heads][score_len]
+  const int32_t* score_rows;
+  const int32_t* lens;
+  int32_t* keep;  // [num_seqs][kv_heads][sink + heavy + recent]
+  int32_t* keep_lens;
+  int* err;
+  int num_rows, kv_heads, score_len, sink, heavy, recent;
+};
+cudaError_t launch_evict_select(const EvictSelectParams& p, int num_seqs, cudaStream_t stream);
+
+struct CompactParams {
+  void* k_cache;
+  void* v_cache;
+  const int32_t* tables;
+  const int32_t* lens;
+  const int32_t* keep;  // [num_seqs][keep_heads][max_keep]
+  const int32_t* keep_lens;
+  const int32_t* base;  // null: 0
+  float* scores;        // null: none
+  const int32_t* score_rows;
+  int* err;
+  int maxblk, cap, keep_heads, max_keep, num_blocks, block_size, kv_heads, num_rows, score_len;
+  int row_vecs;  // 16-byte vectors of one head's row
+  int columns;   // set by the launcher
+};
+cudaError_t launch_compact_kv(const CompactParams& p, int num_seqs, cudaStream_t stream);
+
+// pa_decode_accumulate: what the partition pass leaves of the logits, and the
+// pass that turns them into weights (after the merge's inputs are complete).
+struct AccumulateParams {
+  const float* logits;  // [num_seqs][kv_heads][cap][group], log2 units
+  const float* part_m;  // as MergeParams
+  const float* part_w;  // sums of the unrounded probabilities
+  const int32_t* lens;
+  const float* scores;
+  float* scores_out;
+  const int32_t* score_rows;
+  int* err;
+  int num_seqs, q_heads, kv_heads, group, max_splits, split_tokens, cap, num_rows, score_len;
+};
+cudaError_t launch_accumulate(const AccumulateParams& p, cudaStream_t stream);
 
 }  // namespace pa

@@ -1,0 +1,71 @@
+// What the two attention kernels of pa_verify_tree share: the geometry of a
+// work unit, and the care that a drafted node's values reach only the rows
+// that see the node.
+#pragma once
+
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+// A request's part of the batch.  Row i*G + g is query i (node i), head g of
+// the group; keys [0, hist) are seen by every row, key hist + j by the rows
+// whose mask has bit j.
+struct TreeReq {
+  int qs, n, ctx, hist;
+};
+
+// The request from immutable inputs; 0, or the error code of a request that is
+// skipped.
+__device__ __forceinline__ int tree_request(const TreeParams& p, int r, TreeReq& q) {
+  q.qs = __ldg(p.q_start + r);
+  const int qe = __ldg(p.q_start + r + 1);
+  q.n = qe - q.qs;
+  q.ctx = __ldg(p.lens + r);
+  q.hist = q.ctx - q.n;
+  if (q.qs < 0 || qe < q.qs || qe > p.total_q || q.n > p.max_q_len || q.hist < 0) return PA_DEVERR_QUERY_RANGE;
+  if (q.ctx > p.maxblk * p.block_size) return PA_DEVERR_CONTEXT_LEN;
+  return 0;
+}
+
+// P.V multiplies a masked node's V by exactly zero, which is NaN where V holds
+// an infinity or a NaN (a padding node's stale slot).  So the non-finite
+// elements of drafted V rows are replaced by zero in shared memory, the row's
+// bit is noted, and a row that does see such a node adds the elements back at
+// the end (tree_restore): they decide the result there whatever their weight.
+// Returns true if v held a non-finite element.
+template <typename T> __device__ __forceinline__ bool scrub8(uint4& v) {
+  constexpr uint32_t E = std::is_same<T, __half>::value ? 0x7C00u : 0x7F80u;
+  uint32_t* u = reinterpret_cast<uint32_t*>(&v);
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool lo = (u[i] & E) == E, hi = ((u[i] >> 16) & E) == E;
+    if (lo) u[i] &= 0xFFFF0000u;
+    if (hi) u[i] &= 0x0000FFFFu;
+    any |= lo || hi;
+  }
+  return any;
+}
+
+// What the noted nodes `bits` (non-finite V, seen by the row) add to element d
+// of the row: the sum of their non-finite elements, else 0.
+template <typename T>
+__device__ __forceinline__ float tree_restore(const TreeParams& p, int r, int h, int head_dim, int hist, uint64_t bits,
+                                              int d) {
+  float add = 0.f;
+  while (bits) {
+    const int j = __ffsll((long long)bits) - 1;
+    bits &= bits - 1;
+    const int t = hist + j;
+    const int b = __ldg(p.tables + (size_t)r * p.maxblk + t / p.block_size);
+    if (b < 0 || b >= p.num_blocks) continue;
+    const T x = reinterpret_cast<const T*>(
+        p.v_cache)[(((size_t)b * p.block_size + t % p.block_size) * p.kv_heads + h) * head_dim + d];
+    const float f = static_cast<float>(x);
+    if (!isfinite(f)) add += f;
+  }
+  return add;
+}
+
+}  // namespace pa

@@ -31,6 +31,16 @@ __all__ = [
     "verify_decode",
     "verify_split_tokens",
     "verify_workspace_size",
+    "rope_table",
+    "norm_rope_and_cache",
+    "tree_mask",
+    "verify_tree",
+    "verify_tree_split_tokens",
+    "verify_tree_workspace_size",
+    "decode_accumulate",
+    "decode_accumulate_workspace_size",
+    "evict_select",
+    "compact_kv",
     "get_device_error",
     "selftest_wait_timeout",
     "launch_count",
@@ -417,6 +427,255 @@ def chunked_prefill(q, q_start, context_lens, k_cache, v_cache, block_tables, sc
         int(max_q_len), int(max_ctas), hq, hkv, d, bs, nb, float(scale), _dev(out, "out"), dtype_code(q.dtype),
         _stream(stream))
     return out
+
+
+def _check_current(t: torch.Tensor):
+    """The library launches on the current device: a tensor elsewhere would be another GPU's memory."""
+    if t.is_cuda and t.device.index != torch.cuda.current_device():
+        raise ValueError(f"tensors are on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+
+
+def rope_table(max_position: int, rot_dim: int, base: float = 10000.0, device=None) -> torch.Tensor:
+    """fp32 [max_position, rot_dim], cosines then sines of ``position * base^(-2j/rot_dim)``: the table
+    :func:`norm_rope_and_cache` reads.  The angles are taken in 64 bits: in 32 those of far positions lose the
+    digits that matter."""
+    j = torch.arange(rot_dim // 2, dtype=torch.float64, device=device)
+    angle = torch.arange(max_position, dtype=torch.float64, device=device)[:, None] * base ** (-2.0 * j / rot_dim)
+    return torch.cat([angle.cos(), angle.sin()], 1).to(torch.float32)
+
+
+def _token_rows(t: torch.Tensor, name: str, cache: torch.Tensor):
+    """Pointer and token stride (elements) of [num_tokens, heads, head_dim] whose heads are contiguous."""
+    if t.dim() != 3 or t.shape[2] != cache.shape[3]:
+        raise ValueError(f"{name} is [num_tokens, heads, head_dim] of the cache's head_dim")
+    if t.dtype != cache.dtype:
+        raise TypeError(f"{name} ({t.dtype}) must have the cache's dtype ({cache.dtype})")
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, not {cache.device}")
+    row = t.shape[1] * t.shape[2]
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    stride = t.stride(0) if t.shape[0] > 1 else row
+    if stride < row or stride % 8:
+        raise ValueError(f"{name}: tokens must be at least a row, and a multiple of 8 elements, apart")
+    return stride
+
+
+def norm_rope_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight=None, k_weight=None,
+                        eps=1e-6, sections=None, interleaved=False, out=None, stream=None):
+    """pa_norm_rope_and_cache: per-head norm (with ``q_weight``/``k_weight``) and rotary position of new queries and
+    keys, keys and values into their slots; returns the queries.
+
+    ``q``/``k``/``v`` may be views of one projection's rows.  ``positions``: int32 [num_tokens], or
+    [axes, num_tokens] with ``sections`` (pairs per axis).  ``out`` may be ``q`` if that is contiguous."""
+    nb, bs, hkv, d = _cache_dims(k_cache)
+    _check_caches(k_cache, v_cache)
+    strides = [_token_rows(t, n, k_cache) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
+    T, hq = int(q.shape[0]), int(q.shape[1])
+    if k.shape != (T, hkv, d) or v.shape != (T, hkv, d):
+        raise ValueError("k and v are [num_tokens, kv_heads, head_dim] of the cache, as many tokens as q")
+    axes = 1 if positions.dim() == 1 else int(positions.shape[0]) if positions.dim() == 2 else 0
+    if not 1 <= axes <= 3 or positions.shape[-1] != T or positions.device != q.device:
+        raise ValueError("positions is [num_tokens] or [1 to 3 axes, num_tokens] on q's device")
+    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or cos_sin.device != q.device:
+        raise ValueError("cos_sin is fp32 [max_position, rot_dim] on q's device")
+    rot = int(cos_sin.shape[1])
+    if sections is None:
+        if axes > 1:
+            raise ValueError("several axes need their sections")
+    elif len(sections) != axes or min(sections) < 0 or sum(sections) != rot // 2:
+        raise ValueError(f"sections are {axes} counts of pairs, rot_dim / 2 = {rot // 2} together")
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None and (w.shape != (d,) or w.dtype != q.dtype or w.device != q.device):
+            raise ValueError(f"{n} is [head_dim] of q's dtype and device")
+    _check_index(q, "slot_mapping", slot_mapping, T)
+    if out is None:
+        out = torch.empty((T, hq, d), dtype=q.dtype, device=q.device)
+    elif out.shape != (T, hq, d) or out.dtype != q.dtype or out.device != q.device:
+        raise ValueError("out must have q's shape, dtype and device")
+    _check_current(q)
+    import ctypes as C
+    sec = (C.c_int32 * axes)(*[int(x) for x in sections]) if sections is not None else None
+    _keep(out)
+    _launch(
+        "pa_norm_rope_and_cache", _dev_rows(q, "q"), _dev_rows(k, "k"), _dev_rows(v, "v"), *strides,
+        _dev(q_weight, "q_weight") if q_weight is not None else None,
+        _dev(k_weight, "k_weight") if k_weight is not None else None, float(eps), _i32(positions, "positions"), axes,
+        sec, _dev(cos_sin, "cos_sin"), int(cos_sin.shape[0]), rot, int(bool(interleaved)),
+        _i32(slot_mapping, "slot_mapping"), T, hq, _dev(out, "out"), _dev(k_cache, "k_cache"),
+        _dev(v_cache, "v_cache"), nb, bs, hkv, d, dtype_code(q.dtype), _stream(stream))
+    return out
+
+
+def _dev_rows(t: torch.Tensor, name: str):
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.data_ptr()
+
+
+def tree_mask(parents) -> torch.Tensor:
+    """int64 [n] (host): node i sees itself and its ancestors.  ``parents[i]`` < i, or -1 for a child of the context."""
+    words = []
+    for i, p in enumerate(parents):
+        p = int(p)
+        if not -1 <= p < i or i >= 64:
+            raise ValueError("parents come before their children, at most 64 nodes")
+        words.append((words[p] if p >= 0 else 0) | 1 << i)
+    return torch.tensor([w - (1 << 64) if w >> 63 else w for w in words], dtype=torch.int64)
+
+
+def verify_tree_split_tokens(num_reqs, max_q_len, q_heads, kv_heads, max_blocks_per_seq, block_size,
+                             split_tokens=0) -> int:
+    return check(_lib.lib().pa_verify_tree_split_tokens(int(num_reqs), int(max_q_len), int(q_heads), int(kv_heads),
+                                                        int(max_blocks_per_seq), int(block_size), int(split_tokens)),
+                 "pa_verify_tree_split_tokens")
+
+
+def verify_tree_workspace_size(num_reqs, total_q, max_q_len, q_heads, kv_heads, head_dim, max_blocks_per_seq,
+                               block_size, split_tokens=0) -> int:
+    return int(_lib.lib().pa_verify_tree_workspace_size(num_reqs, total_q, max_q_len, q_heads, kv_heads, head_dim,
+                                                        max_blocks_per_seq, block_size, split_tokens))
+
+
+def verify_tree(q, q_start, tree_mask, context_lens, k_cache, v_cache, block_tables, scale, max_q_len, out=None,
+                split_tokens=0, workspace=None, stream=None):
+    """pa_verify_tree: ``q`` is [total_q, q_heads, head_dim], packed by ``q_start``; bit m of ``tree_mask[i]`` (int64)
+    lets row i see its request's node m.  Every row sees the context before the draft."""
+    nb, bs, hkv, d = _cache_dims(k_cache)
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q is [total_q, q_heads, head_dim] of the cache's head_dim")
+    T, hq, _ = q.shape
+    R = int(context_lens.shape[0])
+    if out is None:
+        out = torch.empty_like(q)
+    _check_attention(q, k_cache, v_cache, out)
+    _check_index(q, "context_lens", context_lens, R)
+    _check_index(q, "q_start", q_start, R + 1)
+    _check_index(q, "block_tables", block_tables, R, table=True)
+    _check_index(q, "tree_mask", tree_mask, T)
+    if tree_mask.dtype != torch.int64:
+        raise TypeError("tree_mask must be int64")
+    _check_current(q)
+    maxblk = int(block_tables.shape[1])
+    if workspace is None:
+        n = verify_tree_workspace_size(R, T, int(max_q_len), hq, hkv, d, maxblk, bs, split_tokens)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+    ws_ptr, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
+        if workspace is not None else (None, 0)
+    _keep(out, workspace)
+    _launch(
+        "pa_verify_tree", _dev(q, "q"), _i32(q_start, "q_start"), _dev(tree_mask, "tree_mask"),
+        _i32(context_lens, "context_lens"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+        _i32(block_tables, "block_tables"), maxblk, R, T, int(max_q_len), hq, hkv, d, bs, nb, float(scale),
+        int(split_tokens), ws_ptr, ws_bytes, _dev(out, "out"), dtype_code(q.dtype), _stream(stream))
+    return out
+
+
+def decode_accumulate_workspace_size(num_seqs, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size,
+                                     split_tokens=0) -> int:
+    return int(_lib.lib().pa_decode_accumulate_workspace_size(num_seqs, q_heads, kv_heads, head_dim,
+                                                              max_blocks_per_seq, block_size, split_tokens))
+
+
+def _check_scores(ref, scores, hkv: int, score_rows, num_seqs: int, name="scores"):
+    if scores.dim() != 3 or scores.shape[1] != hkv or scores.dtype != torch.float32 or scores.device != ref.device:
+        raise ValueError(f"{name} is fp32 [rows, kv_heads, length] on {ref.device}")
+    if score_rows is not None:
+        _check_index(ref, "score_rows", score_rows, num_seqs)
+    elif scores.shape[0] < num_seqs:
+        raise ValueError(f"{name} has fewer rows than there are requests")
+
+
+def decode_accumulate(q, k_cache, v_cache, block_tables, context_lens, scale, scores, score_rows=None,
+                      scores_out=None, out=None, split_tokens=0, workspace=None, stream=None):
+    """pa_decode_accumulate: :func:`decode`, and each cached token's attention weight (summed over the query heads of
+    its KV head) added to its score.  ``scores``: fp32 [rows, kv_heads, length], request r's row is ``score_rows[r]``
+    (None: r; negative: no score).  ``scores_out`` None: in place.  Returns (out, scores_out)."""
+    nb, bs, hkv, d = _cache_dims(k_cache)
+    if out is None:
+        out = torch.empty_like(q)
+    _check_decode(q, k_cache, v_cache, block_tables, context_lens, out)
+    B, hq, _ = q.shape
+    if scores_out is None:
+        scores_out = scores
+    _check_scores(q, scores, hkv, score_rows, B)
+    if scores_out.shape != scores.shape:
+        raise ValueError("scores_out must have scores' shape")
+    _check_scores(q, scores_out, hkv, score_rows, B, "scores_out")
+    _check_current(q)
+    maxblk = int(block_tables.shape[1])
+    if workspace is None:
+        n = decode_accumulate_workspace_size(B, hq, hkv, d, maxblk, bs, split_tokens)
+        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+    _keep(out, workspace)
+    _launch(
+        "pa_decode_accumulate", _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
+        _i32(block_tables, "block_tables"), maxblk, _i32(context_lens, "context_lens"), B, hq, hkv, d, bs, nb,
+        float(scale), int(split_tokens), _dev(scores, "scores"),
+        _i32(score_rows, "score_rows") if score_rows is not None else None, int(scores.shape[0]),
+        int(scores.shape[2]), _dev(scores_out, "scores_out"), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _dev(out, "out"), dtype_code(q.dtype), _stream(stream))
+    return out, scores_out
+
+
+def evict_select(scores, context_lens, sink, heavy, recent, score_rows=None, keep=None, keep_lens=None, stream=None):
+    """pa_evict_select: per request and KV head the tokens a budget of ``sink + heavy + recent`` keeps, ascending:
+    the first, the last, and the best scored between.  Returns (keep int32 [num_seqs, kv_heads, budget], -1 behind;
+    keep_lens int32 [num_seqs])."""
+    if scores.dim() != 3:
+        raise ValueError("scores is fp32 [rows, kv_heads, length]")
+    B, hkv = int(context_lens.shape[0]), int(scores.shape[1])
+    _check_scores(scores, scores, hkv, score_rows, B)
+    _check_index(scores, "context_lens", context_lens, B)
+    if min(sink, heavy, recent) < 0 or sink + heavy + recent < 1:
+        raise ValueError("sink, heavy and recent are counts, at least one token together")
+    budget = int(sink) + int(heavy) + int(recent)
+    if keep is None:
+        keep = torch.empty((B, hkv, budget), dtype=torch.int32, device=scores.device)
+    elif keep.shape != (B, hkv, budget) or keep.device != scores.device:
+        raise ValueError(f"keep is [{B}, {hkv}, {budget}] on {scores.device}")
+    if keep_lens is None:
+        keep_lens = torch.empty(B, dtype=torch.int32, device=scores.device)
+    _check_index(scores, "keep_lens", keep_lens, B)
+    _check_current(scores)
+    _keep(keep, keep_lens)
+    _launch(
+        "pa_evict_select", _dev(scores, "scores"), _i32(score_rows, "score_rows") if score_rows is not None else None,
+        int(scores.shape[0]), hkv, int(scores.shape[2]), _i32(context_lens, "context_lens"), B, int(sink), int(heavy),
+        int(recent), _i32(keep, "keep"), _i32(keep_lens, "keep_lens"), _stream(stream))
+    return keep, keep_lens
+
+
+def compact_kv(k_cache, v_cache, block_tables, context_lens, keep, keep_lens, base=None, scores=None, score_rows=None,
+               stream=None):
+    """pa_compact_kv: token ``base[r] + i`` of each sequence becomes its token ``base[r] + keep[r, g, i]``, in place
+    (``keep``: int32 [num_seqs, 1 or kv_heads, max_keep], ``i <= keep[i]``); with ``scores``, those too, and zeros
+    behind them."""
+    nb, bs, hkv, d = _cache_dims(k_cache)
+    _check_caches(k_cache, v_cache)
+    B = int(context_lens.shape[0])
+    _check_index(k_cache, "block_tables", block_tables, B, table=True)
+    _check_index(k_cache, "context_lens", context_lens, B)
+    if keep.dim() != 3 or keep.shape[0] != B or keep.shape[1] not in (1, hkv) or keep.device != k_cache.device:
+        raise ValueError("keep is int32 [num_seqs, 1 or kv_heads, max_keep] on the cache's device")
+    _check_index(k_cache, "keep_lens", keep_lens, B)
+    if base is not None:
+        _check_index(k_cache, "base", base, B)
+    if scores is not None:
+        _check_scores(k_cache, scores, hkv, score_rows, B)
+    _check_current(k_cache)
+    if keep.shape[2] == 0:
+        if scores is not None:
+            raise ValueError("keep has no entries")
+        return
+    with_rows = scores is not None and score_rows is not None
+    _launch(
+        "pa_compact_kv", _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _i32(block_tables, "block_tables"),
+        int(block_tables.shape[1]), _i32(context_lens, "context_lens"), _i32(keep, "keep"), int(keep.shape[1]),
+        int(keep.shape[2]), _i32(keep_lens, "keep_lens"), _i32(base, "base") if base is not None else None, B, nb, bs,
+        hkv, d, dtype_code(k_cache.dtype), _dev(scores, "scores") if scores is not None else None,
+        _i32(score_rows, "score_rows") if with_rows else None, int(scores.shape[0]) if scores is not None else 0,
+        int(scores.shape[2]) if scores is not None else 0, _stream(stream))
 
 
 def selftest_wait_timeout(wait_ms: int = 50, stream=None) -> None:
