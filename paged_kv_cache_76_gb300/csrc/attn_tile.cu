@@ -55,10 +55,20 @@
 // issuing thread each.)  K is K-major and V MN-major in the canonical
 // 128-byte-swizzled shared-memory layouts that the TMA boxes write.  Every
 // mbarrier wait is bounded.
+//
+// Drafted trees (TREE, pa_verify_tree): the rows of a ragged batch, packed by
+// q_start, in tiles of 128; row (query i, head g) sees the context before the
+// draft and the drafted keys of its 64-bit mask.  Only tiles that reach the
+// draft are masked: the row's visible keys of the tile are one or two words,
+// the mask shifted to where the draft starts in it.  In those tiles the warps
+// that zero V rows past the keys also clean the drafted V rows of non-finite
+// elements (tree.cuh).  A context may be cut into partitions of split_tokens
+// keys, a unit each, whose partials a merge combines.  One unit per CTA.
 #include <float.h>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "tree.cuh"
 
 namespace pa {
 
@@ -81,7 +91,7 @@ __device__ __forceinline__ uint8_t* align1024_tc(uint8_t* p) {
   return reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(p) + 1023) & ~uintptr_t(1023));
 }
 
-template <int D, int BSUB, bool SPREAD>
+template <int D, int BSUB, bool SPREAD, bool TREE>
 struct TcSmem {
   using Tile = KvTile<D, BSUB, kKeys>;  // D/64 halves x 128 rows x 128 B
   static constexpr int K_OFF = 0;
@@ -93,7 +103,8 @@ struct TcSmem {
   static constexpr int BAR_OFF = L_OFF + (SPREAD ? 3 : 2) * kRows * 4;
   static constexpr int NBARS = 4 * 3 + 2 + 2 + 6;
   static constexpr int SLOT_OFF = BAR_OFF + NBARS * 8;
-  static constexpr int BYTES = SLOT_OFF + 16 + 1024;
+  static constexpr int BAD_OFF = SLOT_OFF + 16;  // TREE: drafted nodes with non-finite V (2 words)
+  static constexpr int BYTES = SLOT_OFF + 16 + (TREE ? 16 : 0) + 1024;
   static_assert(BSUB * 128 >= 1024, "needs blocks of at least 8 tokens (one 8-row swizzle atom per box)");
   static_assert(BYTES <= 227 * 1024, "shared memory per CTA");
   static_assert((kKeys / BSUB) * (D / 64) <= 32, "a producer warp issues one box per lane");
@@ -120,6 +131,7 @@ static_assert(B_MMADONE + 1 == 4 * 3 + 2 + 2 + 6, "barrier count");
 // q_len * group to 128).  Units are numbered request-major, then head.
 struct TcUnit {
   int z, h, row0, r, qs, chunk, p0, k0, kend, rows, ntiles;
+  int part;  // TREE: partition of the context; p0 is then the draft's first key
 };
 
 // Geometry of unit u from immutable inputs only: row (query i, head g) sees
@@ -150,11 +162,44 @@ __device__ __forceinline__ bool tc_unit(const PrefillParams& p, int u, int row_t
   return true;
 }
 
-template <int D, int BSUB, typename T, bool SPREAD>
+// TREE: units numbered request, partition, KV head, row tile (row tiles of the
+// same keys next to one another: the second finds them in L2).
+__device__ __forceinline__ int tree_unit(const PrefillParams& p, const TreeParams& tp, int u, int row_tiles,
+                                         TcUnit& w) {
+  const int per_z = row_tiles * p.kv_heads;
+  w.z = u / per_z;
+  const int rem = u - w.z * per_z;
+  w.h = rem / row_tiles;
+  w.row0 = (rem - w.h * row_tiles) * kRows;
+  w.r = w.z / tp.max_splits;
+  w.part = w.z - w.r * tp.max_splits;
+  w.ntiles = 0;
+  TreeReq q;
+  const int code = tree_request(tp, w.r, q);
+  if (code) return code;
+  w.qs = q.qs;
+  w.chunk = q.n;
+  w.p0 = q.hist;
+  w.rows = q.n * p.group;
+  w.k0 = w.part * tp.split_tokens;
+  w.kend = min(q.ctx, w.k0 + tp.split_tokens);
+  if (w.row0 < w.rows && w.k0 < w.kend) w.ntiles = (w.kend - w.k0 + kKeys - 1) / kKeys;
+  return 0;
+}
+
+// Which of the 64 keys from `rel` past the draft's start on (before it:
+// negative) a row with this mask sees.
+__device__ __forceinline__ uint64_t tree_window(uint64_t mask, int rel) {
+  if (rel <= -64) return ~0ull;
+  if (rel < 0) return (mask << -rel) | ((1ull << -rel) - 1);
+  return rel < 64 ? mask >> rel : 0ull;
+}
+
+template <int D, int BSUB, typename T, bool SPREAD, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                   const PrefillParams p) {
-  using L = TcSmem<D, BSUB, SPREAD>;
+                   const PrefillParams p, const TreeParams tp) {
+  using L = TcSmem<D, BSUB, SPREAD, TREE>;
   using Tile = typename L::Tile;
   constexpr int NH = D / 64;
   constexpr int KSTEPS = D / 16;      // S = Q K^T: K dimension = head_dim
@@ -178,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = p.group;
   // CTA b (linear block index) takes units b, b + nctas, ...
   const int row_tiles = (p.max_q_len * G + kRows - 1) / kRows;
-  const int nunits = row_tiles * p.kv_heads * p.num_reqs;
+  const int nunits = row_tiles * p.kv_heads * p.num_reqs * (TREE ? tp.max_splits : 1);
   const int cta0 = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
   const int nctas = gridDim.x * gridDim.y * gridDim.z;
   // the spread form keeps its epilogue's partial outputs in V stages that
@@ -191,6 +236,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // the first unit >= u (in this CTA's stride) that has key tiles, or nunits
   auto next_unit = [&](int u, TcUnit& w, bool report) -> int {
+    if constexpr (TREE) {  // one unit per CTA, which has keys (see below)
+      if (u < nunits) tree_unit(p, tp, u, row_tiles, w);
+      return u < nunits ? u : nunits;
+    }
     for (; u < nunits; u += nctas) {
       if (!tc_unit(p, u, row_tiles, w)) {
         if (report) {
@@ -203,6 +252,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     return nunits;
   };
+
+  uint32_t* bad = reinterpret_cast<uint32_t*>(smem + L::BAD_OFF);
+  if constexpr (TREE) {
+    // a ragged batch's units without rows or keys, and refused requests
+    TcUnit w;
+    const int code = tree_unit(p, tp, cta0, row_tiles, w);
+    if (code || w.ntiles == 0) {
+      griddep_wait();
+      if (code && w.h == 0 && w.row0 == 0 && w.part == 0 && threadIdx.x == 0) record_error(p.err, code);
+      return;
+    }
+    if (threadIdx.x == 0) bad[0] = bad[1] = 0;
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKStages; ++i) {
@@ -435,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // units whose rows see no key at all (a verify request shorter than its
     // queries) are skipped by every role; their rows are written as zeros here
     // (spread: by the first lane quarter)
-    {
+    if constexpr (!TREE) {
       TcUnit z;
       for (int uz = cta0; uz < nunits; uz += nctas) {
         if (!tc_unit(p, uz, row_tiles, z) || z.ntiles > 0 || z.row0 >= z.rows) continue;
@@ -449,6 +511,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
     }
+
+    // this thread's V row of a tile whose keys end at nvalid: zeroed behind
+    // them; (TREE) a drafted row loses its non-finite elements
+    auto clean_v = [&](uint8_t* vt, int nvalid, int ts, const TcUnit& w) {
+      if (vrow >= nvalid) {
+#pragma unroll
+        for (int hf = 0; hf < NH; ++hf)
+#pragma unroll
+          for (int c = 0; c < 8; ++c)
+            *reinterpret_cast<uint4*>(vt + Tile::line(hf, vrow) + c * 16) = make_uint4(0, 0, 0, 0);
+      } else if (TREE && ts + vrow >= w.p0) {
+        bool any = false;
+#pragma unroll
+        for (int hf = 0; hf < NH; ++hf)
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            uint4* at = reinterpret_cast<uint4*>(vt + Tile::line(hf, vrow) + c * 16);
+            uint4 x = *at;
+            if (scrub8<T>(x)) {
+              *at = x;
+              any = true;
+            }
+          }
+        const int node = ts + vrow - w.p0;
+        if (any) atomicOr(&bad[node >> 5], 1u << (node & 31));
+      }
+    };
 
     bool ok = true;
     int gt = 0;  // key tiles processed by this CTA
@@ -467,6 +556,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       const bool valid = grow < w.rows;
       const int qi = grow / G, g = grow % G;
       const int lim = !valid ? -1 : w.p0 + qi;  // last key this row may see
+      uint64_t mask = 0;                        // TREE: the drafted nodes it sees
+      if constexpr (TREE) {
+        if (valid) mask = __ldg(tp.mask + w.qs + qi) & (w.chunk >= 64 ? ~0ull : (1ull << w.chunk) - 1);
+      }
       const bool wvalid = __any_sync(kAll, valid);  // else: only keep the barrier phases
       float m = -INFINITY, l = 0.f;  // running (possibly stale) max in log2 units, sum of this warp's keys
       for (int j = 0; j < w.ntiles; ++j, ++gt) {
@@ -477,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ts = w.k0 + j * kKeys;
         const int nvis = lim - ts + 1 - s_key0;  // keys of this warp's S window the row may see (<= 0: none)
         // rows past the unit (whose output is never read) do not force the masking pass
-        const bool all_full = __all_sync(kAll, nvis >= KS || !valid);
+        const bool all_full = TREE ? ts + s_key0 + KS <= w.p0 : __all_sync(kAll, nvis >= KS || !valid);
 
         // the warp's S window in registers (one TMEM round trip); then the
         // buffer may take S(gt + 2)
@@ -513,21 +606,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(B_SFREE + b));
         if (j == w.ntiles - 1 && un < nunits) q_to_tmem();  // the unit's last S done: the next unit's Q
         const int nvalid = min(kKeys, w.kend - ts);
+        // V rows to clean before P.V: past the keys, and (TREE) drafted ones
+        const bool unclean = nvalid < kKeys || (TREE && ts + kKeys > w.p0);
         if (!wvalid) {
           // rows all past the unit: no P (its rows of O are never read), but
           // the zeroing of V rows past the keys is this warp's share
-          if (kh == 0 && nvalid < kKeys) {
+          if (kh == 0 && unclean) {
             const int s = gt % kVStages;
             ok = __all_sync(kAll, mbar_wait(bar(B_VFULL + s), (gt / kVStages) & 1));
             if (!ok) break;
-            if (vrow >= nvalid) {
-              uint8_t* vt = smem + L::V_OFF + s * Tile::BYTES;
-#pragma unroll
-              for (int hf = 0; hf < NH; ++hf)
-#pragma unroll
-                for (int c = 0; c < 8; ++c)
-                  *reinterpret_cast<uint4*>(vt + Tile::line(hf, vrow) + c * 16) = make_uint4(0, 0, 0, 0);
-            }
+            clean_v(smem + L::V_OFF + s * Tile::BYTES, nvalid, ts, w);
             fence_proxy_async_smem();
           }
           // P(gt)'s barrier counts one arrival per warp and tile: like every
@@ -543,8 +631,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 
         if (!all_full) {
+          if constexpr (TREE) {
+            const int rel = ts + s_key0 - w.p0;
 #pragma unroll
-          for (int e = 0; e < KS; ++e) sv[e] = e < nvis ? sv[e] : -INFINITY;
+            for (int c = 0; c < (KS + 63) / 64; ++c) {
+              const uint64_t see = tree_window(mask, rel + 64 * c);
+#pragma unroll
+              for (int e = 0; e < (KS < 64 ? KS : 64); ++e)
+                sv[64 * c + e] = (see >> e) & 1 ? sv[64 * c + e] : -INFINITY;
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < KS; ++e) sv[e] = e < nvis ? sv[e] : -INFINITY;
+          }
         }
         float mraw;
         if constexpr (SPREAD) mraw = max32(sv);
@@ -595,20 +694,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16u(tl + O_COL + 16 * c, *reinterpret_cast<const uint32_t(*)[16]>(ov));
           }
         }
-        if (kh == 0 && nvalid < kKeys) {
+        if (kh == 0 && unclean) {
           // last key tile: keys past kend came from stale slots (or were not
           // loaded); zero their V rows so that p = 0 never meets NaN/Inf
           const int s = gt % kVStages;
           ok = __all_sync(kAll, mbar_wait(bar(B_VFULL + s), (gt / kVStages) & 1));
           if (!ok) break;
-          if (vrow >= nvalid) {
-            uint8_t* vt = smem + L::V_OFF + s * Tile::BYTES;
-#pragma unroll
-            for (int hf = 0; hf < NH; ++hf)
-#pragma unroll
-              for (int c = 0; c < 8; ++c)
-                *reinterpret_cast<uint4*>(vt + Tile::line(hf, vrow) + c * 16) = make_uint4(0, 0, 0, 0);
-          }
+          clean_v(smem + L::V_OFF + s * Tile::BYTES, nvalid, ts, w);
           fence_proxy_async_smem();
         }
         if constexpr (SPREAD) {
@@ -673,9 +765,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             f[qq] = mv == -INFINITY ? 0.f : ex2_approx(mv - mmax);
             lt += f[qq] * (lq[(qq * 2) * 32 + r] + lq[(qq * 2 + 1) * 32 + r]);
           }
-          const float inv = lt > 0.f ? 1.f / lt : 0.f;
+          const float inv = TREE ? tree_inverse(lt) : lt > 0.f ? 1.f / lt : 0.f;
           const int rr = w.row0 + r;
-          T* orow = reinterpret_cast<T*>(p.out) + ((size_t)(w.qs + rr / G) * p.q_heads + w.h * G + rr % G) * D;
+          const size_t orow_i = (size_t)(w.qs + rr / G) * p.q_heads + w.h * G + rr % G;
+          T* orow = reinterpret_cast<T*>(p.out) + orow_i * D;
+          uint64_t fix = 0;
+          if constexpr (TREE) fix = __ldg(tp.mask + w.qs + rr / G) & ((uint64_t)bad[0] | ((uint64_t)bad[1] << 32));
 #pragma unroll
           for (int i = 0; i < D / 32; ++i) {
             const int ch = c0 + 8 * i;  // 16-byte chunk of the fp32 row = 4 output elements
@@ -684,6 +779,23 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int qq = 0; qq < 4; ++qq) {
               const float4 x = *part(qq, r, ch);
               a.x += f[qq] * x.x, a.y += f[qq] * x.y, a.z += f[qq] * x.z, a.w += f[qq] * x.w;
+            }
+            if constexpr (TREE) {
+              if (fix) {
+                a.x += tree_restore<T>(tp, w.r, w.h, D, w.p0, fix, 4 * ch);
+                a.y += tree_restore<T>(tp, w.r, w.h, D, w.p0, fix, 4 * ch + 1);
+                a.z += tree_restore<T>(tp, w.r, w.h, D, w.p0, fix, 4 * ch + 2);
+                a.w += tree_restore<T>(tp, w.r, w.h, D, w.p0, fix, 4 * ch + 3);
+              }
+              if (w.p0 + w.chunk > tp.split_tokens) {  // one of several partitions
+                const size_t pr = orow_i * tp.max_splits + w.part;
+                *reinterpret_cast<float4*>(tp.part_o + pr * D + 4 * ch) = a;
+                if (ch == 0) {
+                  tp.part_m[pr] = mmax;
+                  tp.part_l[pr] = lt;
+                }
+                continue;
+              }
             }
             *reinterpret_cast<uint2*>(orow + 4 * ch) =
                 make_uint2(Elem<T>::pack(a.x * inv, a.y * inv), Elem<T>::pack(a.z * inv, a.w * inv));
@@ -703,14 +815,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float lt = lsum[row] + lsum[kRows + row];
         asm volatile("bar.sync %0, %1;\n" ::"r"(1 + quarter), "r"(64) : "memory");
         if (wvalid) {
-          const float inv = lt > 0.f ? 1.f / lt : 0.f;
-          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) +
-                                                ((size_t)(w.qs + qi) * p.q_heads + w.h * G + g) * D + kh * DH);
+          const float inv = TREE ? tree_inverse(lt) : lt > 0.f ? 1.f / lt : 0.f;
+          const size_t orow_i = (size_t)(w.qs + qi) * p.q_heads + w.h * G + g;
+          uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + orow_i * D + kh * DH);
+          uint64_t fix = 0;
+          if constexpr (TREE) fix = mask & ((uint64_t)bad[0] | ((uint64_t)bad[1] << 32));
 #pragma unroll
           for (int c = 0; c < DH / 32; ++c) {
             float ov[32];
             tmem_ld32(tl + O_COL + kh * DH + 32 * c, ov);  // warp-collective: every lane loads, valid rows store
             tmem_wait_ld();
+            if constexpr (TREE) {
+              if (fix) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) ov[e] += tree_restore<T>(tp, w.r, w.h, D, w.p0, fix, kh * DH + 32 * c + e);
+              }
+              if (w.p0 + w.chunk > tp.split_tokens) {  // one of several partitions
+                const size_t pr = orow_i * tp.max_splits + w.part;
+                if (valid) {
+                  float4* po = reinterpret_cast<float4*>(tp.part_o + pr * D + kh * DH + 32 * c);
+#pragma unroll
+                  for (int q = 0; q < 8; ++q)
+                    po[q] = make_float4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+                  if (kh == 0 && c == 0) {
+                    tp.part_m[pr] = m;
+                    tp.part_l[pr] = lt;
+                  }
+                }
+                continue;
+              }
+            }
             if (valid) {
 #pragma unroll
               for (int q = 0; q < 4; ++q)
@@ -749,8 +883,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int D, int BSUB, typename T, bool SPREAD>
 cudaError_t launch_tc_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const PrefillParams& p,
                          cudaStream_t stream) {
-  using L = TcSmem<D, BSUB, SPREAD>;
-  auto kern = attn_tile_kernel<D, BSUB, T, SPREAD>;
+  using L = TcSmem<D, BSUB, SPREAD, false>;
+  auto kern = attn_tile_kernel<D, BSUB, T, SPREAD, false>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -770,7 +904,55 @@ cudaError_t launch_tc_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const 
   // one CTA per unit: a (row tile, head, request) grid, whose linear order is
   // the unit order; capped: a 1-D grid of max_ctas persistent CTAs
   const dim3 grid = p.max_ctas > 0 && p.max_ctas < nunits ? dim3(p.max_ctas) : dim3(row_tiles, p.kv_heads, zdim);
-  return launch_pdl(kern, grid, dim3(kThreads), L::BYTES, stream, kmap, vmap, p);
+  return launch_pdl(kern, grid, dim3(kThreads), L::BYTES, stream, kmap, vmap, p, TreeParams{});
+}
+
+template <int D, int BSUB, typename T, bool SPREAD>
+cudaError_t launch_tree_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& tp, cudaStream_t stream) {
+  using L = TcSmem<D, BSUB, SPREAD, true>;
+  auto kern = attn_tile_kernel<D, BSUB, T, SPREAD, true>;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && !attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  PrefillParams p{};
+  p.q = tp.q;
+  p.q_start = tp.q_start;
+  p.lens = tp.lens;
+  p.tables = tp.tables;
+  p.out = tp.out;
+  p.err = tp.err;
+  p.maxblk = tp.maxblk;
+  p.num_reqs = tp.num_reqs;
+  p.total_q = tp.total_q;
+  p.max_q_len = tp.max_q_len;
+  p.q_heads = tp.q_heads;
+  p.kv_heads = tp.kv_heads;
+  p.group = tp.group;
+  p.num_blocks = tp.num_blocks;
+  p.block_size = tp.block_size;
+  p.scale_log2 = tp.scale_log2;
+  const long long row_tiles = (tp.max_q_len * tp.group + kRows - 1) / kRows;
+  const long long nunits = row_tiles * tp.kv_heads * tp.num_reqs * tp.max_splits;
+  if (nunits > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_pdl(kern, dim3((unsigned)nunits), dim3(kThreads), L::BYTES, stream, kmap, vmap, p, tp);
+}
+
+template <int D, typename T>
+cudaError_t launch_tree_bs(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int bsub,
+                           cudaStream_t stream) {
+  const bool spread = p.max_q_len * p.group <= 32;
+  switch (bsub) {
+    case 8: return spread ? launch_tree_t<D, 8, T, true>(kmap, vmap, p, stream)
+                          : launch_tree_t<D, 8, T, false>(kmap, vmap, p, stream);
+    case 16: return spread ? launch_tree_t<D, 16, T, true>(kmap, vmap, p, stream)
+                           : launch_tree_t<D, 16, T, false>(kmap, vmap, p, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 template <int D, typename T>
@@ -791,6 +973,17 @@ cudaError_t launch_tc_bs(const CUtensorMap& kmap, const CUtensorMap& vmap, const
 }
 
 }  // namespace
+
+cudaError_t launch_tree_tile(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int head_dim,
+                             int bsub, pa_dtype dt, cudaStream_t stream) {
+  if (head_dim == 128)
+    return dt == PA_BF16 ? launch_tree_bs<128, __nv_bfloat16>(kmap, vmap, p, bsub, stream)
+                         : launch_tree_bs<128, __half>(kmap, vmap, p, bsub, stream);
+  if (head_dim == 64)
+    return dt == PA_BF16 ? launch_tree_bs<64, __nv_bfloat16>(kmap, vmap, p, bsub, stream)
+                         : launch_tree_bs<64, __half>(kmap, vmap, p, bsub, stream);
+  return cudaErrorInvalidValue;
+}
 
 cudaError_t launch_attn_tile(const CUtensorMap& kmap, const CUtensorMap& vmap, const PrefillParams& p, int head_dim,
                             int bsub, pa_dtype dt, cudaStream_t stream) {

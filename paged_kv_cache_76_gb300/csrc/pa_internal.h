@@ -209,6 +209,9 @@ struct TreeParams {
   float* part_m;
   float* part_l;
 };
+// blocks of >= 8 tokens: the tcgen05 kernel of attn_tile.cu (no merge)
+cudaError_t launch_tree_tile(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int head_dim,
+                             int bsub, pa_dtype dt, cudaStream_t stream);
 cudaError_t launch_verify_tree(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int head_dim,
                                int bsub, pa_dtype dt, cudaStream_t stream);
 

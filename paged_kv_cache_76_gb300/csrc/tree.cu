@@ -315,7 +315,7 @@ __global__ void __launch_bounds__((kTreeConsumers + 1) * 32)
     const float l = x ? lb : la, m = x ? mb : ma;
     const size_t orow = (size_t)(rq.qs + (x ? qib : qia)) * p.q_heads + h * G + row % G;
     if (direct) {
-      const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;  // a NaN among the scores stays one
+      const float inv = tree_inverse(l);
       T* o = reinterpret_cast<T*>(p.out) + orow * D + 2 * (lane & 3);
 #pragma unroll
       for (int i = 0; i < DT8; ++i)
@@ -373,7 +373,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
       }
     }
   }
-  const float inv = den > 0.f ? 1.f / den : den == 0.f ? 0.f : den;
+  const float inv = tree_inverse(den);
   T* o = reinterpret_cast<T*>(p.out) + orow * D + lane * V;
 #pragma unroll
   for (int i = 0; i < V; i += 2)
@@ -405,8 +405,7 @@ cudaError_t launch_tree_dt(const CUtensorMap& kmap, const CUtensorMap& vmap, con
   cudaError_t e = cudaErrorInvalidValue;
   switch (bsub) {
     case 4: e = launch_mma_t<D, 4, T>(kmap, vmap, p, stream); break;
-    case 8: e = launch_mma_t<D, 8, T>(kmap, vmap, p, stream); break;
-    case 16: e = launch_mma_t<D, 16, T>(kmap, vmap, p, stream); break;
+    default: e = launch_tree_tile(kmap, vmap, p, D, bsub, std::is_same<T, __half>::value ? PA_FP16 : PA_BF16, stream);
   }
   if (e != cudaSuccess || p.max_splits == 1) return e;
   const unsigned gx = (unsigned)(((int64_t)p.max_q_len * p.q_heads + 7) / 8);

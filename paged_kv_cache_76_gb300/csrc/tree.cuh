@@ -28,6 +28,9 @@ __device__ __forceinline__ int tree_request(const TreeParams& p, int r, TreeReq&
   return 0;
 }
 
+// 1 / l; a row that sees nothing (l = 0) is zero, a NaN among its scores stays one.
+__device__ __forceinline__ float tree_inverse(float l) { return l > 0.f ? 1.f / l : l == 0.f ? 0.f : l; }
+
 // P.V multiplies a masked node's V by exactly zero, which is NaN where V holds
 // an infinity or a NaN (a padding node's stale slot).  So the non-finite
 // elements of drafted V rows are replaced by zero in shared memory, the row's
