@@ -50,10 +50,20 @@
 //               exact.
 // Q and K are K-major and V is MN-major in the canonical 128-byte-swizzled
 // shared-memory layouts.  Every mbarrier wait is bounded.
+//
+// Drafted trees (TREE, pa_verify_tree with more than 128 rows per KV head):
+// rows packed by q_start in units of 256, one unit per CTA; row (query i,
+// head g) sees the context before the draft and the drafted keys of its 64-bit
+// mask, which in a tile that reaches the draft is the mask shifted to where
+// the draft starts in it.  The drafted V rows of such a tile are cleaned of
+// non-finite elements (tree.cuh).  A context may be cut into partitions of
+// split_tokens keys, a unit each, whose partials a merge combines.  A unit of
+// at most 128 rows leaves tile B alone: its issuer only frees the stages.
 #include <float.h>
 
 #include "pa_device.cuh"
 #include "pa_internal.h"
+#include "tree.cuh"
 
 namespace pa {
 
@@ -89,6 +99,7 @@ struct TcSmem {
   static constexpr int BAR_OFF = V_OFF + kVStages * Tile::BYTES;
   static constexpr int NBARS = 2 * kKStages + 2 * kVStages + 15;
   static constexpr int SLOT_OFF = BAR_OFF + NBARS * 8;
+  static constexpr int BAD_OFF = SLOT_OFF + 8;  // TREE: drafted nodes with non-finite V (2 words)
   static constexpr int BYTES = SLOT_OFF + 16 + 1024;
   static_assert(BSUB * 128 >= 1024, "needs blocks of at least 8 tokens (one 8-row swizzle atom per box)");
   static_assert(BYTES <= 227 * 1024, "shared memory per CTA");
@@ -114,6 +125,7 @@ static_assert(B_MMADONE + 1 == 2 * kKStages + 2 * kVStages + 15, "barrier count"
 // order starts the longest units of every head first.
 struct TcUnit {
   int z, h, row0, r, qs, chunk, p0, k0, kend, rows, ntiles;
+  int part;  // TREE: partition of the context; p0 is then the draft's first key
 };
 
 // Geometry of unit u from immutable inputs only.  false: the request's
@@ -160,10 +172,35 @@ __device__ __forceinline__ bool tc_unit(const PrefillParams& p, int u, int row_t
   return true;
 }
 
-template <int D, int BSUB, typename T>
+// TREE: units numbered request, partition, KV head, row tile.  0, or the error
+// code of a refused request.
+__device__ __forceinline__ int tree_unit(const PrefillParams& p, const TreeParams& tp, int u, int row_tiles,
+                                         TcUnit& w) {
+  const int per_z = row_tiles * p.kv_heads;
+  w.z = u / per_z;
+  const int rem = u - w.z * per_z;
+  w.h = rem / row_tiles;
+  w.row0 = (rem - w.h * row_tiles) * 2 * kRows;
+  w.r = w.z / tp.max_splits;
+  w.part = w.z - w.r * tp.max_splits;
+  w.ntiles = 0;
+  TreeReq q;
+  const int code = tree_request(tp, w.r, q);
+  if (code) return code;
+  w.qs = q.qs;
+  w.chunk = q.n;
+  w.p0 = q.hist;
+  w.rows = q.n * p.group;
+  w.k0 = w.part * tp.split_tokens;
+  w.kend = min(q.ctx, w.k0 + tp.split_tokens);
+  if (w.row0 < w.rows && w.k0 < w.kend) w.ntiles = (w.kend - w.k0 + kKeys - 1) / kKeys;
+  return 0;
+}
+
+template <int D, int BSUB, typename T, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                    const PrefillParams p) {
+                    const PrefillParams p, const TreeParams tp) {
   using L = TcSmem<D, BSUB>;
   using Tile = typename L::Tile;
   constexpr int NH = D / 64;
@@ -185,9 +222,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int G = p.group;
   // CTA b (linear block index) takes units b, b + nctas, ...
   const int row_tiles = (p.max_q_len * G + 2 * kRows - 1) / (2 * kRows);
-  const int nunits = row_tiles * p.kv_heads * (p.causal ? p.num_reqs : (p.prefix_len + p.key_split - 1) / p.key_split);
+  const int nunits =
+      row_tiles * p.kv_heads *
+      (TREE ? p.num_reqs * tp.max_splits : p.causal ? p.num_reqs : (p.prefix_len + p.key_split - 1) / p.key_split);
   const int cta0 = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
   const int nctas = gridDim.x * gridDim.y * gridDim.z;
+  auto unit = [&](int u, TcUnit& w) -> bool {
+    if constexpr (TREE) return tree_unit(p, tp, u, row_tiles, w) == 0;
+    return tc_unit(p, u, row_tiles, w);
+  };
+
+  uint32_t* bad = reinterpret_cast<uint32_t*>(smem + L::BAD_OFF);
+  if constexpr (TREE) {
+    // a ragged batch's units without rows or keys, and refused requests
+    TcUnit w;
+    const int code = tree_unit(p, tp, cta0, row_tiles, w);
+    if (code || w.ntiles == 0) {
+      griddep_wait();
+      if (code && w.h == 0 && w.row0 == 0 && w.part == 0 && threadIdx.x == 0) record_error(p.err, code);
+      return;
+    }
+    if (threadIdx.x == 0) bad[0] = bad[1] = 0;
+  }
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKStages; ++i) {
@@ -228,14 +284,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const CUtensorMap* map = isv ? &vmap : &kmap;
     const int full0 = isv ? B_VFULL : B_KFULL, empty0 = isv ? B_VEMPTY : B_KEMPTY;
     const uint32_t base = smem_u32(smem + (isv ? L::V_OFF : L::K_OFF));
-    const uint64_t pol = policy_evict_last();  // K/V tiles are re-read by the other row tiles
+    // K/V tiles are re-read by the other row tiles (a tree's rows mostly fit one)
+    const uint64_t pol = TREE && row_tiles == 1 ? policy_evict_first() : policy_evict_last();
     const int nst = isv ? kVStages : kKStages;
     int gt = 0;  // K/V tiles issued by this CTA (ring position and phase)
     bool failed = false;
     griddep_wait();  // the cache (this step's reshape_and_cache) comes from the kernel before
     for (int u = cta0; u < nunits && !failed; u += nctas) {
       TcUnit w;
-      if (!tc_unit(p, u, row_tiles, w) || w.ntiles <= 0) continue;
+      if (!unit(u, w) || w.ntiles <= 0) continue;
       const int32_t* trow = p.tables + (size_t)w.r * p.maxblk;
       for (int j = 0; j < w.ntiles; ++j, ++gt) {
         const int s = gt % nst;
@@ -302,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int u = cta0; ok && u < nunits; u += nctas) {
         TcUnit w;
-        if (!tc_unit(p, u, row_tiles, w)) {
+        if (!unit(u, w)) {
           if (x == 0) {
             griddep_wait();
             if (lane == 0) record_error(p.err, PA_DEVERR_QUERY_RANGE);
@@ -310,6 +367,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
         if (w.ntiles <= 0) continue;
+        if (TREE && x == 1 && w.row0 + kRows >= w.rows) {
+          // no rows in tile B: this issuer only gives its share of every stage back
+          for (int j = 0; j < w.ntiles; ++j, ++gt) {
+            const int sk = gt % kKStages, sv = gt % kVStages;
+            ok = __all_sync(kAll, mbar_wait(bar(B_KFULL + sk), (gt / kKStages) & 1) &&
+                                      mbar_wait(bar(B_VFULL + sv), (gt / kVStages) & 1));
+            if (!ok) break;
+            if (lane == 0) {
+              mbar_arrive(bar(B_KEMPTY + sk));
+              mbar_arrive(bar(B_VEMPTY + sv));
+            }
+          }
+          continue;
+        }
         // Q_x of this unit is in smem; the softmax warps have also finished
         // the previous unit (its last P.V completed and O_x was read out).
         if (!__all_sync(kAll, mbar_wait(bar(B_QFULL + x), nu & 1))) { ok = false; break; }
@@ -361,11 +432,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     int gt = 0;  // key tiles processed by this CTA
     for (int u = cta0; ok && u < nunits; u += nctas) {
       TcUnit w;
-      if (!tc_unit(p, u, row_tiles, w) || w.ntiles <= 0) continue;
+      if (!unit(u, w) || w.ntiles <= 0) continue;
+      if (TREE && x == 1 && w.row0 + kRows >= w.rows) continue;
       const int grow = w.row0 + x * kRows + row;
       const bool valid = grow < w.rows;
       const int qi = grow / G, g = grow % G;
       const int lim = !valid ? -1 : (p.causal ? w.p0 + qi : w.kend - 1);  // last key this row may see
+      uint64_t mask = 0;                                                  // TREE: the drafted nodes it sees
+      if constexpr (TREE) {
+        if (valid) mask = __ldg(tp.mask + w.qs + qi) & (w.chunk >= 64 ? ~0ull : (1ull << w.chunk) - 1);
+      }
       {
         // Q row -> shared memory (K-major, 128-byte swizzle); padding rows are
         // zero.  The previous unit's S MMAs have completed (its last P.V did).
@@ -391,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
         const int ts = w.k0 + j * kKeys;
         const int nvis = lim - ts + 1;  // keys of this tile the row may see (<= 0: none)
-        const bool all_full = __all_sync(0xffffffffu, nvis >= kKeys);
+        const bool all_full = TREE ? ts + kKeys <= w.p0 : __all_sync(0xffffffffu, nvis >= kKeys);
 
         // the whole S row in registers: one TMEM round trip
         float sv[kKeys];
@@ -399,8 +475,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(scol + 32 * c, *reinterpret_cast<float(*)[32]>(&sv[32 * c]));
         tmem_wait_ld();
         if (!all_full) {
+          if constexpr (TREE) {
+            const uint64_t see = tree_window(mask, ts - w.p0);
 #pragma unroll
-          for (int e = 0; e < kKeys; ++e) sv[e] = e < nvis ? sv[e] : -INFINITY;
+            for (int e = 0; e < kKeys; ++e) sv[e] = (see >> e) & 1 ? sv[e] : -INFINITY;
+          } else {
+#pragma unroll
+            for (int e = 0; e < kKeys; ++e) sv[e] = e < nvis ? sv[e] : -INFINITY;
+          }
         }
         // row maximum: four independent chains of three-input max
         float ma = -INFINITY, mb = -INFINITY, mc = -INFINITY, md = -INFINITY;
@@ -458,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tmem_st16u(ocol + 16 * c, *reinterpret_cast<const uint32_t(*)[16]>(ov));
           }
         }
-        if (nvalid < kKeys) {
+        if (nvalid < kKeys || (TREE && !all_full)) {
           // last key tile: keys past kend came from stale slots (or were
           // not loaded); zero their V rows so that p = 0 never meets
           // NaN/Inf.  Both Q tiles' softmax warps write the same zeros
@@ -474,6 +556,24 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int c = 0; c < 8; ++c)
                 *reinterpret_cast<uint4*>(vrow + hf * Tile::HALF + c * 16) = make_uint4(0, 0, 0, 0);
+          } else if (TREE && row < kKeys && ts + row >= w.p0) {
+            // a drafted row loses its non-finite elements (both groups find
+            // and write the same, or the second finds none left)
+            uint8_t* vrow = smem + L::V_OFF + s * Tile::BYTES + row * 128;
+            bool any = false;
+#pragma unroll
+            for (int hf = 0; hf < NH; ++hf)
+#pragma unroll
+              for (int c = 0; c < 8; ++c) {
+                uint4* at = reinterpret_cast<uint4*>(vrow + hf * Tile::HALF + c * 16);
+                uint4 v = *at;
+                if (scrub8<T>(v)) {
+                  *at = v;
+                  any = true;
+                }
+              }
+            const int node = ts + row - w.p0;
+            if (any) atomicOr(&bad[node >> 5], 1u << (node & 31));
           }
           fence_proxy_async_smem();
         }
@@ -493,7 +593,41 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = bar_red_and(1 + x, 128, ofull);
       if (!ok) break;
       tc_fence_after();
-      if (p.causal) {
+      if constexpr (TREE) {
+        const size_t orow = (size_t)(w.qs + qi) * p.q_heads + w.h * G + g;
+        const bool whole = w.p0 + w.chunk <= tp.split_tokens;  // the request's only partition
+        const size_t pr = orow * tp.max_splits + w.part;
+        const float inv = tree_inverse(l);
+        const uint64_t fix = mask & ((uint64_t)bad[0] | ((uint64_t)bad[1] << 32));
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float ov[32];
+          tmem_ld32(ocol + 32 * c, ov);
+          tmem_wait_ld();
+          if (fix) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) ov[e] += tree_restore<T>(tp, w.r, w.h, D, w.p0, fix, 32 * c + e);
+          }
+          if (!valid) continue;
+          if (whole) {
+            uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) + orow * D) + 4 * c;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              dst[q] = make_uint4(Elem<T>::pack(ov[8 * q] * inv, ov[8 * q + 1] * inv),
+                                  Elem<T>::pack(ov[8 * q + 2] * inv, ov[8 * q + 3] * inv),
+                                  Elem<T>::pack(ov[8 * q + 4] * inv, ov[8 * q + 5] * inv),
+                                  Elem<T>::pack(ov[8 * q + 6] * inv, ov[8 * q + 7] * inv));
+          } else {
+            float4* po = reinterpret_cast<float4*>(tp.part_o + pr * D) + 8 * c;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) po[q] = make_float4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+          }
+        }
+        if (valid && !whole) {
+          tp.part_m[pr] = m;
+          tp.part_l[pr] = l;
+        }
+      } else if (p.causal) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
         uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<T*>(p.out) +
                                               ((size_t)(w.qs + qi) * p.q_heads + w.h * G + g) * D);
@@ -550,7 +684,7 @@ template <int D, int BSUB, typename T>
 cudaError_t launch_tc_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const PrefillParams& p,
                          cudaStream_t stream) {
   using L = TcSmem<D, BSUB>;
-  auto kern = attn_tc_kernel<D, BSUB, T>;
+  auto kern = attn_tc_kernel<D, BSUB, T, false>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -567,7 +701,36 @@ cudaError_t launch_tc_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const 
   // one CTA per unit: a (row tile, head, request) grid, whose linear order is
   // the unit order; capped: a 1-D grid of max_ctas persistent CTAs
   const dim3 grid = p.max_ctas > 0 && p.max_ctas < nunits ? dim3(p.max_ctas) : dim3(row_tiles, p.kv_heads, zdim);
-  return launch_pdl(kern, grid, dim3(kThreads), L::BYTES, stream, kmap, vmap, p);
+  return launch_pdl(kern, grid, dim3(kThreads), L::BYTES, stream, kmap, vmap, p, TreeParams{});
+}
+
+template <int D, int BSUB, typename T>
+cudaError_t launch_tree_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const PrefillParams& p,
+                          const TreeParams& tp, cudaStream_t stream) {
+  using L = TcSmem<D, BSUB>;
+  auto kern = attn_tc_kernel<D, BSUB, T, true>;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && !attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  const long long row_tiles = (tp.max_q_len * tp.group + 2 * kRows - 1) / (2 * kRows);
+  const long long nunits = row_tiles * tp.kv_heads * tp.num_reqs * tp.max_splits;
+  if (nunits > INT32_MAX) return cudaErrorInvalidValue;
+  return launch_pdl(kern, dim3((unsigned)nunits), dim3(kThreads), L::BYTES, stream, kmap, vmap, p, tp);
+}
+
+template <int D, typename T>
+cudaError_t launch_tree_bs(const CUtensorMap& kmap, const CUtensorMap& vmap, const PrefillParams& p,
+                           const TreeParams& tp, int bsub, cudaStream_t stream) {
+  switch (bsub) {
+    case 8: return launch_tree_t<D, 8, T>(kmap, vmap, p, tp, stream);
+    case 16: return launch_tree_t<D, 16, T>(kmap, vmap, p, tp, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 template <int D, typename T>
@@ -581,6 +744,18 @@ cudaError_t launch_tc_bs(const CUtensorMap& kmap, const CUtensorMap& vmap, const
 }
 
 }  // namespace
+
+cudaError_t launch_tree_pair(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& tp, int head_dim,
+                             int bsub, pa_dtype dt, cudaStream_t stream) {
+  const PrefillParams p = tree_prefill_params(tp);
+  if (head_dim == 128)
+    return dt == PA_BF16 ? launch_tree_bs<128, __nv_bfloat16>(kmap, vmap, p, tp, bsub, stream)
+                         : launch_tree_bs<128, __half>(kmap, vmap, p, tp, bsub, stream);
+  if (head_dim == 64)
+    return dt == PA_BF16 ? launch_tree_bs<64, __nv_bfloat16>(kmap, vmap, p, tp, bsub, stream)
+                         : launch_tree_bs<64, __half>(kmap, vmap, p, tp, bsub, stream);
+  return cudaErrorInvalidValue;
+}
 
 cudaError_t launch_attn_tc(const CUtensorMap& kmap, const CUtensorMap& vmap, const PrefillParams& p, int head_dim,
                             int bsub, pa_dtype dt, cudaStream_t stream) {

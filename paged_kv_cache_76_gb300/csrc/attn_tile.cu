@@ -187,14 +187,6 @@ __device__ __forceinline__ int tree_unit(const PrefillParams& p, const TreeParam
   return 0;
 }
 
-// Which of the 64 keys from `rel` past the draft's start on (before it:
-// negative) a row with this mask sees.
-__device__ __forceinline__ uint64_t tree_window(uint64_t mask, int rel) {
-  if (rel <= -64) return ~0ull;
-  if (rel < 0) return (mask << -rel) | ((1ull << -rel) - 1);
-  return rel < 64 ? mask >> rel : 0ull;
-}
-
 template <int D, int BSUB, typename T, bool SPREAD, bool TREE>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -919,23 +911,7 @@ cudaError_t launch_tree_t(const CUtensorMap& kmap, const CUtensorMap& vmap, cons
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  PrefillParams p{};
-  p.q = tp.q;
-  p.q_start = tp.q_start;
-  p.lens = tp.lens;
-  p.tables = tp.tables;
-  p.out = tp.out;
-  p.err = tp.err;
-  p.maxblk = tp.maxblk;
-  p.num_reqs = tp.num_reqs;
-  p.total_q = tp.total_q;
-  p.max_q_len = tp.max_q_len;
-  p.q_heads = tp.q_heads;
-  p.kv_heads = tp.kv_heads;
-  p.group = tp.group;
-  p.num_blocks = tp.num_blocks;
-  p.block_size = tp.block_size;
-  p.scale_log2 = tp.scale_log2;
+  const PrefillParams p = tree_prefill_params(tp);
   const long long row_tiles = (tp.max_q_len * tp.group + kRows - 1) / kRows;
   const long long nunits = row_tiles * tp.kv_heads * tp.num_reqs * tp.max_splits;
   if (nunits > INT32_MAX) return cudaErrorInvalidValue;

@@ -209,7 +209,10 @@ struct TreeParams {
   float* part_m;
   float* part_l;
 };
-// blocks of >= 8 tokens: the tcgen05 kernel of attn_tile.cu (no merge)
+// blocks of >= 8 tokens, no merge: the tcgen05 kernels of attn_tile.cu (128
+// rows per CTA) and attn_tc.cu (256)
+cudaError_t launch_tree_pair(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int head_dim,
+                             int bsub, pa_dtype dt, cudaStream_t stream);
 cudaError_t launch_tree_tile(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int head_dim,
                              int bsub, pa_dtype dt, cudaStream_t stream);
 cudaError_t launch_verify_tree(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int head_dim,

@@ -405,7 +405,11 @@ cudaError_t launch_tree_dt(const CUtensorMap& kmap, const CUtensorMap& vmap, con
   cudaError_t e = cudaErrorInvalidValue;
   switch (bsub) {
     case 4: e = launch_mma_t<D, 4, T>(kmap, vmap, p, stream); break;
-    default: e = launch_tree_tile(kmap, vmap, p, D, bsub, std::is_same<T, __half>::value ? PA_FP16 : PA_BF16, stream);
+    default: {
+      const pa_dtype dt = std::is_same<T, __half>::value ? PA_FP16 : PA_BF16;
+      e = p.max_q_len * p.group <= 128 ? launch_tree_tile(kmap, vmap, p, D, bsub, dt, stream)
+                                       : launch_tree_pair(kmap, vmap, p, D, bsub, dt, stream);
+    }
   }
   if (e != cudaSuccess || p.max_splits == 1) return e;
   const unsigned gx = (unsigned)(((int64_t)p.max_q_len * p.q_heads + 7) / 8);

@@ -15,6 +15,28 @@ struct TreeReq {
   int qs, n, ctx, hist;
 };
 
+// The fields that the tcgen05 kernels read as they do a prefill's.
+inline PrefillParams tree_prefill_params(const TreeParams& tp) {
+  PrefillParams p{};
+  p.q = tp.q;
+  p.q_start = tp.q_start;
+  p.lens = tp.lens;
+  p.tables = tp.tables;
+  p.out = tp.out;
+  p.err = tp.err;
+  p.maxblk = tp.maxblk;
+  p.num_reqs = tp.num_reqs;
+  p.total_q = tp.total_q;
+  p.max_q_len = tp.max_q_len;
+  p.q_heads = tp.q_heads;
+  p.kv_heads = tp.kv_heads;
+  p.group = tp.group;
+  p.num_blocks = tp.num_blocks;
+  p.block_size = tp.block_size;
+  p.scale_log2 = tp.scale_log2;
+  return p;
+}
+
 // The request from immutable inputs; 0, or the error code of a request that is
 // skipped.
 __device__ __forceinline__ int tree_request(const TreeParams& p, int r, TreeReq& q) {
@@ -26,6 +48,14 @@ __device__ __forceinline__ int tree_request(const TreeParams& p, int r, TreeReq&
   if (q.qs < 0 || qe < q.qs || qe > p.total_q || q.n > p.max_q_len || q.hist < 0) return PA_DEVERR_QUERY_RANGE;
   if (q.ctx > p.maxblk * p.block_size) return PA_DEVERR_CONTEXT_LEN;
   return 0;
+}
+
+// Which of the 64 keys from `rel` past the draft's start on (before it:
+// negative) a row with this mask sees.
+__device__ __forceinline__ uint64_t tree_window(uint64_t mask, int rel) {
+  if (rel <= -64) return ~0ull;
+  if (rel < 0) return (mask << -rel) | ((1ull << -rel) - 1);
+  return rel < 64 ? mask >> rel : 0ull;
 }
 
 // 1 / l; a row that sees nothing (l = 0) is zero, a NaN among its scores stays one.
