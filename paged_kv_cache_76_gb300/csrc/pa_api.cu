@@ -1098,7 +1098,7 @@ namespace {
 
 constexpr int kTreeMaxNodes = 64;    // one mask word per node
 constexpr int kTreeSplitUnit = 128;  // partitions are whole key tiles
-constexpr int kTreeSplitMin = 512;
+constexpr int kTreeSplitMin = 256;
 
 struct TreeSetup {
   int split, max_splits;
@@ -1116,12 +1116,25 @@ int tree_setup(int num_reqs, int total_q, int max_q_len, int q_heads, int kv_hea
   const int64_t whole = (cap + kTreeSplitUnit - 1) / kTreeSplitUnit * kTreeSplitUnit;
   int64_t split = split_tokens;
   if (split_tokens == 0) {
-    // enough partitions that every SM has two CTAs of 64 rows
-    const int64_t units = (int64_t)num_reqs * kv_heads * (((int64_t)max_q_len * (q_heads / kv_heads) + 63) / 64);
+    // Units (requests x KV heads x tiles of 128 or 256 rows) that give every
+    // SM two run whole: a partition's partials (a kilobyte written and read
+    // per row) then cost more than the balance brings.  Measured on GB300, 64
+    // requests of <= 4096 tokens, 8 KV heads: whole 132 us, 2048-token
+    // partitions 153 us (80..128 rows); 162 and 190 us (104..240 rows).  Fewer
+    // units are cut into about four per SM, but no smaller than the partials
+    // are worth (twice the rows): 8 contexts of 33..131 thousand tokens, 128
+    // rows: 65536 tokens 649 us, 32768 568, 12288 462, 4096 507; one of 8060,
+    // 240 rows: 1024 tokens 25.7 us, 512 24.0, 256 37.8.
+    const int64_t rows = (int64_t)max_q_len * (q_heads / kv_heads);
+    const int64_t units = (int64_t)num_reqs * kv_heads * (rows <= 128 ? 1 : (rows + 255) / 256);
     const int64_t sms = sm_count() > 0 ? sm_count() : 152;
-    const int64_t want = units > 0 ? (2 * sms + units - 1) / units : 1;
-    split = ((cap + want - 1) / want + kTreeSplitUnit - 1) / kTreeSplitUnit * kTreeSplitUnit;
-    if (split < kTreeSplitMin) split = kTreeSplitMin;
+    split = whole;
+    if (units < 2 * sms) {
+      split = cap * (units > 0 ? units : 1) / (4 * sms);
+      split = split > 2 * rows ? split : 2 * rows;
+      split = (split + kTreeSplitUnit - 1) / kTreeSplitUnit * kTreeSplitUnit;
+      if (split < kTreeSplitMin) split = kTreeSplitMin;
+    }
   }
   if (split <= 0 || split % kTreeSplitUnit != 0) return PA_ERR_INVALID;
   if (split > whole) split = whole;
