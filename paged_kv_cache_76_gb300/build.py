@@ -21,8 +21,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpa.so")
 SOURCES = ["pa_api.cu", "decode.cu", "prefill.cu", "cache_ops.cu", "block_alloc.cpp", "decode_noalloc.cu", "attn_tc.cu",
-           "attn_tile.cu", "vkv.cpp", "rope.cu", "evict.cu", "accumulate.cu",
-           "tree.cu"]
+           "attn_tile.cu", "vkv.cpp", "rope.cu", "evict.cu", "tree.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

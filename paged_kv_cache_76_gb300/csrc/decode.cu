@@ -489,15 +489,12 @@ __global__ void __launch_bounds__(WARPS * 32)
 // the four partial sums are added in warp order, so the result depends only on
 // logical positions.
 template <int D, typename T>
-__global__ void __launch_bounds__(128) lse_merge_kernel(const MergeParams p) {
+__device__ __forceinline__ void merge_row_by_cta(const MergeParams& p, int row) {
   constexpr int V = D / 32;
   constexpr int NW = 4;
   __shared__ float s_max[NW];
   __shared__ float s_den[NW];
   __shared__ __align__(16) float s_acc[NW][D];
-  griddep_wait();  // the partials come from the kernel before this one
-  griddep_launch_dependents();
-  const int row = blockIdx.x;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (row >= p.num_seqs * p.q_len * p.q_heads) return;
   const int r = row / (p.q_heads * p.q_len);
@@ -548,18 +545,22 @@ __global__ void __launch_bounds__(128) lse_merge_kernel(const MergeParams p) {
     o[d] = Elem<T>::from((((s_acc[0][d] + s_acc[1][d]) + s_acc[2][d]) + s_acc[3][d]) * inv);
 }
 
+template <int D, typename T>
+__global__ void __launch_bounds__(128) lse_merge_kernel(const MergeParams p) {
+  griddep_wait();  // the partials come from the kernel before this one
+  griddep_launch_dependents();
+  merge_row_by_cta<D, T>(p, blockIdx.x);
+}
+
 // The same merge with one warp per row, for at most 32 partitions: lane c
 // holds m_c and l_c, each lane owns D/32 output dims, and the o partials are
 // loaded eight partitions at a time ahead of the sums, so a row costs about
 // one round trip to L2.  Partitions are added in order (deterministic).
 template <int D, typename T>
-__global__ void __launch_bounds__(256) lse_merge_warp_kernel(const MergeParams p) {
+__device__ __forceinline__ void merge_row_by_warp(const MergeParams& p, int row) {
   constexpr int V = D / 32;
   constexpr int CH = 8;  // o partials in flight per lane
-  griddep_wait();        // the partials come from the kernel before this one
-  griddep_launch_dependents();
   const int lane = threadIdx.x & 31;
-  const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= p.num_seqs * p.q_len * p.q_heads) return;
   const int r = row / (p.q_heads * p.q_len);
   int ctx = __ldg(p.lens + r);
@@ -625,6 +626,135 @@ __global__ void __launch_bounds__(256) lse_merge_warp_kernel(const MergeParams p
   } else {
     *reinterpret_cast<uint32_t*>(o) = Elem<T>::pack(a[0] * inv, a[1] * inv);
   }
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(256) lse_merge_warp_kernel(const MergeParams p) {
+  griddep_wait();  // the partials come from the kernel before this one
+  griddep_launch_dependents();
+  merge_row_by_warp<D, T>(p, blockIdx.x * 8 + (threadIdx.x >> 5));
+}
+
+// ----------------------------------------------------------------------------
+// The second half of pa_decode_accumulate, one launch: the first merge_ctas
+// CTAs merge the rows as the kernels above do; the others turn the logits that
+// the partition pass stored into attention weights and add them to the scores:
+//
+//   scores_out[row][g][t] = scores[row][g][t] + sum_h 2^(s_h,t - M_h) / W_h
+//
+// with s in log2 units, M_h the largest partition reference and W_h the
+// partitions' sums of unrounded probabilities brought to it, which every CTA
+// computes for its own heads.  One thread owns a token and adds its heads in
+// order, so the result is the same bits on every run; nothing is atomic.
+//
+// Bound by memory: 4 * group bytes of logits (just written, mostly still in
+// L2) and 8 bytes of score per token and KV head, beside the 4 * head_dim
+// bytes of K and V that the partition pass reads.  A CTA takes p.chunk tokens:
+// enough that the partials it reads for M and W stay below a quarter of its
+// logits.
+constexpr int kMaxGroup = 16;
+
+// Sum over the group of one token's weights; lg: its `G` logits.
+template <int GV>
+__device__ __forceinline__ float token_weight(const float* lg, int G, const float* s_m, const float* s_inv) {
+  float w = 0.f;
+  for (int g = 0; g < G; g += GV) {
+    float x[GV];
+    if constexpr (GV == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(lg + g);
+      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
+    } else {
+      x[0] = lg[g];
+    }
+#pragma unroll
+    for (int e = 0; e < GV; ++e) w += exp2f(x[e] - s_m[g + e]) * s_inv[g + e];
+  }
+  return w;
+}
+
+template <int GV>
+__device__ __forceinline__ void add_weights(const AccumulateParams& p, int part) {
+  __shared__ float s_m[kMaxGroup], s_inv[kMaxGroup];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
+  const int chunk = part % p.chunks, rh = part / p.chunks;
+  const int h = rh % p.kv_heads, r = rh / p.kv_heads;
+  int ctx = __ldg(p.lens + r);
+  ctx = ctx < 0 ? 0 : min(ctx, p.cap);
+  const int row = p.score_rows ? __ldg(p.score_rows + r) : r;
+  const int t0 = chunk * p.chunk;
+  if (row < 0 || t0 >= ctx) {
+    if (row >= p.num_rows && t0 == 0 && tid == 0) record_error(p.err, PA_DEVERR_SCORE_ROW);
+    return;
+  }
+  const int G = p.group;
+  const int nsplit = (ctx + p.split_tokens - 1) / p.split_tokens;
+  for (int g = warp; g < G; g += threads / 32) {
+    const size_t prow = ((size_t)r * p.q_heads + h * G + g) * p.max_splits;
+    float M = -INFINITY;
+    for (int c = lane; c < nsplit; c += 32) M = fmaxf(M, p.part_m[prow + c]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (M == -INFINITY) M = 0.f;
+    float l = 0.f;
+    for (int c = lane; c < nsplit; c += 32) l += exp2f(p.part_m[prow + c] - M) * p.part_w[prow + c];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) {
+      s_m[g] = M;
+      s_inv[g] = l > 0.f ? 1.f / l : 0.f;
+    }
+  }
+  bool twice = false;  // an earlier request has this row: it alone keeps score
+  if (p.score_rows)
+    for (int i = tid; i < r; i += threads) twice |= __ldg(p.score_rows + i) == row;
+  if (__syncthreads_or(twice) || row >= p.num_rows) {
+    if (tid == 0) record_error(p.err, PA_DEVERR_SCORE_ROW);
+    return;
+  }
+  if (ctx > p.score_len) {
+    if (tid == 0) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
+    ctx = p.score_len;
+  }
+  const int t1 = min(t0 + p.chunk, ctx);
+  const size_t at = ((size_t)row * p.kv_heads + h) * p.score_len;
+  const float* lg = p.logits + ((size_t)r * p.kv_heads + h) * p.cap * G;
+#pragma unroll 2
+  for (int t = t0 + tid; t < t1; t += threads)
+    p.scores_out[at + t] = p.scores[at + t] + token_weight<GV>(lg + (size_t)t * G, G, s_m, s_inv);
+}
+
+// THREADS 256: a warp per row (at most 32 partitions); 128: the CTA per row.
+template <int D, typename T, int THREADS, int GV>
+__global__ void __launch_bounds__(THREADS)
+    merge_accumulate_kernel(const MergeParams mp, const AccumulateParams ap, int merge_ctas) {
+  griddep_wait();
+  griddep_launch_dependents();
+  if ((int)blockIdx.x < merge_ctas) {
+    if constexpr (THREADS == 256) merge_row_by_warp<D, T>(mp, blockIdx.x * 8 + (threadIdx.x >> 5));
+    else merge_row_by_cta<D, T>(mp, blockIdx.x);
+  } else {
+    add_weights<GV>(ap, blockIdx.x - merge_ctas);
+  }
+}
+
+template <int D, typename T>
+cudaError_t launch_merge_accumulate_t(const MergeParams& mp, const AccumulateParams& p0, cudaStream_t stream) {
+  AccumulateParams ap = p0;
+  const int64_t least = 8 * (int64_t)ap.max_splits;
+  ap.chunk = (int)((least > 512 ? least : 512) + 255) / 256 * 256;
+  ap.chunks = (ap.cap - 1) / ap.chunk + 1;
+  const int64_t rows = (int64_t)mp.num_seqs * mp.q_heads;
+  const bool warps = mp.max_splits <= 32;
+  const int64_t merge_ctas = warps ? (rows + 7) / 8 : rows;
+  const int64_t grid = merge_ctas + (int64_t)ap.chunks * ap.kv_heads * ap.num_seqs;
+  if (grid > INT32_MAX) return cudaErrorInvalidValue;
+  const bool v4 = ap.group % 4 == 0;  // a token's logits are whole 16-byte vectors
+  const dim3 g((unsigned)grid);
+  if (warps)
+    return v4 ? launch_pdl(merge_accumulate_kernel<D, T, 256, 4>, g, dim3(256), 0, stream, mp, ap, (int)merge_ctas)
+              : launch_pdl(merge_accumulate_kernel<D, T, 256, 1>, g, dim3(256), 0, stream, mp, ap, (int)merge_ctas);
+  return v4 ? launch_pdl(merge_accumulate_kernel<D, T, 128, 4>, g, dim3(128), 0, stream, mp, ap, (int)merge_ctas)
+            : launch_pdl(merge_accumulate_kernel<D, T, 128, 1>, g, dim3(128), 0, stream, mp, ap, (int)merge_ctas);
 }
 
 template <int D, int BSUB, int NT, typename T, bool CONTIG = false, int CW = 1, bool LOGITS = false>
@@ -735,6 +865,18 @@ cudaError_t launch_decode_contig(const CUtensorMap& kmap, const CUtensorMap& vma
   if (head_dim == 64)
     return dt == PA_BF16 ? launch_decode_contig_t<64, __nv_bfloat16>(kmap, vmap, p, stream)
                          : launch_decode_contig_t<64, __half>(kmap, vmap, p, stream);
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_merge_accumulate(const MergeParams& mp, const AccumulateParams& ap, int head_dim, pa_dtype dt,
+                                    cudaStream_t stream) {
+  if (!mp.always || mp.q_len != 1 || mp.tok_begin || mp.extra_slots) return cudaErrorInvalidValue;
+  if (head_dim == 128)
+    return dt == PA_BF16 ? launch_merge_accumulate_t<128, __nv_bfloat16>(mp, ap, stream)
+                         : launch_merge_accumulate_t<128, __half>(mp, ap, stream);
+  if (head_dim == 64)
+    return dt == PA_BF16 ? launch_merge_accumulate_t<64, __nv_bfloat16>(mp, ap, stream)
+                         : launch_merge_accumulate_t<64, __half>(mp, ap, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -1001,8 +1001,6 @@ int pa_decode_accumulate(const void* q, const void* k_cache, const void* v_cache
   mp.cap = s.cap;
   mp.always = 1;
   mp.q_len = 1;
-  st = cuda_status(launch_lse_merge(mp, head_dim, dtype, cs));
-  if (st != PA_OK) return st;
   AccumulateParams ap{};
   ap.logits = p.logits;
   ap.part_m = p.part_m;
@@ -1021,7 +1019,7 @@ int pa_decode_accumulate(const void* q, const void* k_cache, const void* v_cache
   ap.cap = s.cap;
   ap.num_rows = num_rows;
   ap.score_len = score_len;
-  return cuda_status(launch_accumulate(ap, cs));
+  return cuda_status(launch_merge_accumulate(mp, ap, head_dim, dtype, cs));
 }
 
 int pa_evict_select(const float* scores, const int32_t* score_rows, int num_rows, int kv_heads, int score_len,
@@ -1060,7 +1058,9 @@ int pa_compact_kv(void* k_cache, void* v_cache, const int32_t* block_tables, int
                   int score_len, pa_stream stream) {
   int st = check_kv_shape(num_blocks, block_size, kv_heads, head_dim, dtype);
   if (st != PA_OK) return st;
-  if (num_seqs < 0 || num_seqs > 65535 || max_blocks_per_seq <= 0 || max_keep <= 0) return PA_ERR_INVALID;
+  if (num_seqs < 0 || num_seqs > 65535 || max_blocks_per_seq <= 0 || max_keep <= 0 ||
+      max_keep > INT32_MAX - (1 << 16))
+    return PA_ERR_INVALID;
   if (keep_heads != 1 && keep_heads != kv_heads) return PA_ERR_INVALID;
   if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX) return PA_ERR_INVALID;
   if (scores && (num_rows <= 0 || score_len <= 0 || (!score_rows && num_rows < num_seqs) || !aligned16(scores)))

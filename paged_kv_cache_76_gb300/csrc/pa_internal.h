@@ -282,7 +282,9 @@ struct AccumulateParams {
   const int32_t* score_rows;
   int* err;
   int num_seqs, q_heads, kv_heads, group, max_splits, split_tokens, cap, num_rows, score_len;
+  int chunk, chunks;  // set by the launcher: tokens of a CTA, CTAs of a (request, KV head)
 };
-cudaError_t launch_accumulate(const AccumulateParams& p, cudaStream_t stream);
+cudaError_t launch_merge_accumulate(const MergeParams& mp, const AccumulateParams& ap, int head_dim, pa_dtype dt,
+                                    cudaStream_t stream);
 
 }  // namespace pa

@@ -6,13 +6,18 @@
 // (of up to three axes); queries go to q_out, keys and values to their cache
 // slots.  Everything between the one load and the one store is fp32.
 //
-// Bound by HBM: 2 bytes read and 2 written per element.  D/8 threads hold a
-// head row, and each thread holds four whole pairs of it (elements 4s.. and
-// rot_dim/2 + 4s.., two 8-byte vectors; eight neighbours if interleaved), so a
-// rotation needs no other thread, the norm's sum is the only shuffle, and the
-// thread keeps its four cosines and sines over all heads of its token.  The
-// rows of a token that a thread takes are loaded together, before any is used,
-// and a CTA's next token while it works on this one's.
+// Bound by HBM: 2 bytes read and 2 written per element; what it takes to get
+// there is bytes in flight and few instructions per element.
+//  * A warp's work item is up to 2 KB of one token's query, key or value heads
+//    (8 heads of 128): one bulk copy (cp.async.bulk) into the warp's own ring
+//    in shared memory, kRopeStages items ahead, so loads in flight cost no
+//    registers and no address arithmetic.  Warps share nothing and never meet.
+//  * D/8 threads hold a head row, and each thread four whole pairs of it
+//    (elements 4s.. and rot_dim/2 + 4s..; eight neighbours if interleaved), so
+//    a rotation needs no other thread and the norm's sum is the only shuffle.
+//    The thread keeps its four cosines and sines for the item's heads.
+//  * The chain slot/position -> table row runs ahead of the items: positions
+//    two items, cosines one.
 #include "pa_device.cuh"
 #include "pa_internal.h"
 
@@ -20,173 +25,252 @@ namespace pa {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeStages = 3;
+constexpr int kItemBytes = 2048;
+constexpr int kRopeMaxWarps = 8;  // of a CTA
 constexpr unsigned kAll = 0xffffffffu;
 
-// Heads of a token in the order queries, keys, values; a CTA takes a token and
-// the rows group + ROWS * (share, share + shares, ...) of it, kRopeRows of them
-// at a time.
-constexpr int kRopeRows = 4;
+// A token's place: its slot and its positions on the axes.
+struct Place {
+  int slot, pos[3];
+};
 
 template <int D, typename T, bool INTER>
-__global__ void __launch_bounds__(kRopeThreads) norm_rope_kernel(const NormRopeParams p) {
-  constexpr int LPH = D / 8;                // threads per head row
-  constexpr int ROWS = kRopeThreads / LPH;  // head rows in flight
-  const int sub = threadIdx.x % LPH, group = threadIdx.x / LPH;
+__global__ void __launch_bounds__(32 * kRopeMaxWarps, 4) norm_rope_kernel(const NormRopeParams p) {
+  constexpr int LPH = D / 8;                       // threads per head row
+  constexpr int GROUPS = 32 / LPH;                 // head rows side by side
+  constexpr int HEADS = kItemBytes / (2 * D);      // heads of an item
+  constexpr int RPT = HEADS / GROUPS;              // rows of a thread
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, nwarps = blockDim.x >> 5;
+  uint8_t* ring = smem + warp * kRopeStages * kItemBytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + nwarps * kRopeStages * kItemBytes) + warp * kRopeStages;
+  if (lane == 0) {
+    for (int s = 0; s < kRopeStages; ++s) mbar_init(smem_u32(&bars[s]), 1);
+    fence_mbar_init();
+  }
+  __syncwarp();
+  const int sub = lane % LPH, group = lane / LPH;
   const int half = p.rot_dim / 2;
   const bool rotated = sub < p.rot_dim / 8;
   // this thread's two runs of four elements; behind rot_dim, eight neighbours
   const int lo = INTER || !rotated ? 8 * sub : 4 * sub;
   const int hi = INTER || !rotated ? 8 * sub + 4 : half + 4 * sub;
-  const int heads = p.q_heads + 2 * p.kv_heads;
-  const int share0 = blockIdx.y * ROWS + group, step = gridDim.y * ROWS;
+  // blocks of a token: queries, keys, values
+  const int qb = (p.q_heads + HEADS - 1) / HEADS, kb = (p.kv_heads + HEADS - 1) / HEADS;
+  const int bpt = qb + 2 * kb;
+  // items of this warp: gw, gw + W, ... of num_tokens * bpt, as (token, block)
+  const int W = gridDim.x * nwarps, gw = blockIdx.x * nwarps + warp;
+  const int dt = W / bpt, db = W % bpt;
+  auto advance = [&](int& t, int& b) {
+    t += dt;
+    b += db;
+    if (b >= bpt) {
+      b -= bpt;
+      ++t;
+    }
+  };
 
   // the whole kernel after the one before it: its inputs may come from there,
   // and q_out may still be read there.  No early launch of the next kernel,
   // which may read q_out in its set-up.
   griddep_wait();
 
-  // token t's slot and positions
-  auto place = [&](int t, int& slot, int (&pos)[3]) {
-    slot = __ldg(p.slots + t);
-#pragma unroll
-    for (int a = 0; a < 3; ++a) pos[a] = a < p.num_axes ? __ldg(p.positions + (size_t)a * p.num_tokens + t) : 0;
+  // heads [h0, h0 + n) of block b's kind
+  auto heads_of = [&](int b, int& h0) {
+    const int all = b < qb ? p.q_heads : p.kv_heads;
+    h0 = (b < qb ? b : b < qb + kb ? b - qb : b - qb - kb) * HEADS;
+    return min(HEADS, all - h0);
   };
-  int slot_next, pos_next[3];
-  if (blockIdx.x < p.num_tokens) place(blockIdx.x, slot_next, pos_next);
-
-  for (int t = blockIdx.x; t < p.num_tokens; t += gridDim.x) {
-    const int slot = slot_next;
-    const int pos[3] = {pos_next[0], pos_next[1], pos_next[2]};
-    if (t + (int)gridDim.x < p.num_tokens) place(t + gridDim.x, slot_next, pos_next);
-    bool bad_pos = false;
-#pragma unroll
-    for (int a = 0; a < 3; ++a) bad_pos |= pos[a] < 0 || pos[a] >= p.max_position;
-    if (bad_pos) {  // CTA-uniform
-      if (slot >= 0 && threadIdx.x == 0) record_error(p.err, PA_DEVERR_POSITION);
-      continue;
+  auto issue = [&](int t, int b, int s) {
+    int h0;
+    const int n = heads_of(b, h0);
+    const T* src = reinterpret_cast<const T*>(b < qb ? p.q : b < qb + kb ? p.k : p.v) +
+                   (b < qb ? p.q_stride : b < qb + kb ? p.k_stride : p.v_stride) * (int64_t)t + (int64_t)h0 * D;
+    fence_proxy_async_smem();  // this warp's reads of the stage before the copy's writes
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive_expect_tx(smem_u32(&bars[s]), n * D * 2);
+      bulk_load(smem_u32(ring + s * kItemBytes), src, n * D * 2, smem_u32(&bars[s]));
     }
-    const bool write_kv = slot >= 0 && slot < p.num_slots;
-    if (slot >= p.num_slots && threadIdx.x == 0) record_error(p.err, PA_DEVERR_SLOT);
+  };
+  auto place_of = [&](int t) {
+    Place w;
+    w.slot = __ldg(p.slots + t);
+#pragma unroll
+    for (int a = 0; a < 3; ++a) w.pos[a] = a < p.num_axes ? __ldg(p.positions + (size_t)a * p.num_tokens + t) : 0;
+    return w;
+  };
+  auto outside = [&](const Place& w) {
+    bool bad = false;
+#pragma unroll
+    for (int a = 0; a < 3; ++a) bad |= w.pos[a] < 0 || w.pos[a] >= p.max_position;
+    return bad;
+  };
+  // this thread's four cosines and sines at a place inside the table
+  auto turn = [&](const Place& w, bool want, float4& c, float4& s) {
+    c = make_float4(1.f, 1.f, 1.f, 1.f);
+    s = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (!rotated || !want) return;
+    const int j = 4 * sub;  // its pairs
+    auto axis = [&](int jj) { return jj < p.sec_end[0] ? w.pos[0] : jj < p.sec_end[1] ? w.pos[1] : w.pos[2]; };
+    if ((j >= p.sec_end[0] || j + 3 < p.sec_end[0]) && (j >= p.sec_end[1] || j + 3 < p.sec_end[1])) {
+      const float* row = p.cos_sin + (size_t)axis(j) * p.rot_dim + j;  // all four turn by one axis
+      c = __ldg(reinterpret_cast<const float4*>(row));
+      s = __ldg(reinterpret_cast<const float4*>(row + half));
+    } else {
+      auto at = [&](int i) { return p.cos_sin + (size_t)axis(j + i) * p.rot_dim + j + i; };
+      c = make_float4(__ldg(at(0)), __ldg(at(1)), __ldg(at(2)), __ldg(at(3)));
+      s = make_float4(__ldg(at(0) + half), __ldg(at(1) + half), __ldg(at(2) + half), __ldg(at(3) + half));
+    }
+  };
 
-    float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-    if (rotated) {
-      const int j = 4 * sub;  // this thread's pairs
-      auto axis = [&](int jj) { return jj < p.sec_end[0] ? pos[0] : jj < p.sec_end[1] ? pos[1] : pos[2]; };
-      const bool one = (j >= p.sec_end[0] || j + 3 < p.sec_end[0]) && (j >= p.sec_end[1] || j + 3 < p.sec_end[1]);
-      if (one) {  // all four turn by one axis
-        const float* row = p.cos_sin + (size_t)axis(j) * p.rot_dim + j;
-        const float4 cv = __ldg(reinterpret_cast<const float4*>(row));
-        const float4 sv = __ldg(reinterpret_cast<const float4*>(row + half));
-        c[0] = cv.x, c[1] = cv.y, c[2] = cv.z, c[3] = cv.w;
-        s[0] = sv.x, s[1] = sv.y, s[2] = sv.z, s[3] = sv.w;
+  int t = gw / bpt, b = gw % bpt;  // the item at hand
+  int ti = t, bi = b;              // the next to load
+  for (int s = 0; s < kRopeStages; ++s) {
+    if (ti < p.num_tokens) issue(ti, bi, s);
+    advance(ti, bi);
+  }
+  int t1 = t, b1 = b;  // the item after this one
+  advance(t1, b1);
+  Place w{}, w1{};
+  if (t < p.num_tokens) w = place_of(t);
+  if (t1 < p.num_tokens) w1 = place_of(t1);
+  float4 c4, s4;
+  turn(w, t < p.num_tokens && b < qb + kb && !outside(w), c4, s4);
+
+  for (int k = 0; t < p.num_tokens; ++k) {
+    int t2 = t1, b2 = b1;
+    advance(t2, b2);
+    Place w2{};
+    if (t2 < p.num_tokens) w2 = place_of(t2);
+    float4 c4n, s4n;
+    turn(w1, t1 < p.num_tokens && b1 < qb + kb && !outside(w1), c4n, s4n);
+
+    const int s = k % kRopeStages;
+    if (!mbar_wait(smem_u32(&bars[s]), (k / kRopeStages) & 1)) {
+      if (lane == 0) record_error(p.err, PA_DEVERR_TIMEOUT);
+      // copies in flight land before exit (bounded)
+      for (int j = k + 1; j < k + kRopeStages && t1 < p.num_tokens; ++j, advance(t1, b1))
+        mbar_wait(smem_u32(&bars[j % kRopeStages]), (j / kRopeStages) & 1);
+      return;
+    }
+    const bool skip = outside(w);
+    if (b == 0 && lane == 0) {
+      if (skip && w.slot >= 0) record_error(p.err, PA_DEVERR_POSITION);
+      if (!skip && w.slot >= p.num_slots) record_error(p.err, PA_DEVERR_SLOT);
+    }
+    const bool is_q = b < qb, is_v = b >= qb + kb;
+    if (!skip && (is_q || (w.slot >= 0 && w.slot < p.num_slots))) {
+      int h0;
+      const int n = heads_of(b, h0);
+      const uint8_t* from = ring + s * kItemBytes;
+      T* dst = is_q ? reinterpret_cast<T*>(p.q_out) + ((size_t)t * p.q_heads + h0) * D
+                    : reinterpret_cast<T*>(is_v ? p.v_cache : p.k_cache) + ((size_t)w.slot * p.kv_heads + h0) * D;
+      if (is_v) {
+        for (int i = lane; i < n * (D / 8); i += 32)
+          reinterpret_cast<uint4*>(dst)[i] = reinterpret_cast<const uint4*>(from)[i];
       } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float* row = p.cos_sin + (size_t)axis(j + i) * p.rot_dim + j + i;
-          c[i] = __ldg(row);
-          s[i] = __ldg(row + half);
+        const T* wt = reinterpret_cast<const T*>(is_q ? p.q_weight : p.k_weight);
+        uint2 wx = make_uint2(0u, 0u), wy = wx;
+        if (wt) {
+          wx = __ldg(reinterpret_cast<const uint2*>(wt + lo));
+          wy = __ldg(reinterpret_cast<const uint2*>(wt + hi));
         }
-      }
-    }
-
-    for (int h0 = share0; h0 - group < heads; h0 += step * kRopeRows) {
-      uint2 x[kRopeRows], y[kRopeRows];
+        // pair i of two packed runs: (a[i], b[i])
+        auto pairs = [](const uint2& x, const uint2& y, float (&a)[4], float (&bb)[4]) {
+          if constexpr (INTER) {
+            a[0] = Elem<T>::lo(x.x), bb[0] = Elem<T>::hi(x.x), a[1] = Elem<T>::lo(x.y), bb[1] = Elem<T>::hi(x.y);
+            a[2] = Elem<T>::lo(y.x), bb[2] = Elem<T>::hi(y.x), a[3] = Elem<T>::lo(y.y), bb[3] = Elem<T>::hi(y.y);
+          } else {
+            a[0] = Elem<T>::lo(x.x), a[1] = Elem<T>::hi(x.x), a[2] = Elem<T>::lo(x.y), a[3] = Elem<T>::hi(x.y);
+            bb[0] = Elem<T>::lo(y.x), bb[1] = Elem<T>::hi(y.x), bb[2] = Elem<T>::lo(y.y), bb[3] = Elem<T>::hi(y.y);
+          }
+        };
+        float wa[4], wb[4];
+        pairs(wx, wy, wa, wb);
+        const float c[4] = {c4.x, c4.y, c4.z, c4.w}, sn[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-      for (int u = 0; u < kRopeRows; ++u) {
-        const int hh = h0 + u * step;
-        x[u] = y[u] = make_uint2(0u, 0u);
-        if (hh < p.q_heads || (hh < heads && write_kv)) {
-          const bool is_q = hh < p.q_heads, is_k = hh < p.q_heads + p.kv_heads;
-          const int h = is_q ? hh : is_k ? hh - p.q_heads : hh - p.q_heads - p.kv_heads;
-          const T* src = reinterpret_cast<const T*>(is_q ? p.q : is_k ? p.k : p.v) +
-                         (is_q ? p.q_stride : is_k ? p.k_stride : p.v_stride) * (int64_t)t + (int64_t)h * D;
-          x[u] = __ldg(reinterpret_cast<const uint2*>(src + lo));
-          y[u] = __ldg(reinterpret_cast<const uint2*>(src + hi));
-        }
-      }
+        for (int u = 0; u < RPT; ++u) {
+          const int row = u * GROUPS + group;  // rows behind n hold an earlier item: not stored
+          const T* src = reinterpret_cast<const T*>(from) + row * D;
+          const uint2 x = *reinterpret_cast<const uint2*>(src + lo), y = *reinterpret_cast<const uint2*>(src + hi);
+          float a[4], bb[4];
+          pairs(x, y, a, bb);
+          if (wt) {  // warp-uniform
+            float sx = 0.f, sy = 0.f;
 #pragma unroll
-      for (int u = 0; u < kRopeRows; ++u) {
-        const int hh = h0 + u * step;
-        if (hh - group >= heads) break;  // CTA-uniform
-        const bool is_q = hh < p.q_heads, is_k = !is_q && hh < p.q_heads + p.kv_heads;
-        const int h = is_q ? hh : is_k ? hh - p.q_heads : hh - p.q_heads - p.kv_heads;
-        // pair i: (a[i], b[i])
-        float a[4], b[4];
-        if constexpr (INTER) {
-          a[0] = Elem<T>::lo(x[u].x), b[0] = Elem<T>::hi(x[u].x), a[1] = Elem<T>::lo(x[u].y), b[1] = Elem<T>::hi(x[u].y);
-          a[2] = Elem<T>::lo(y[u].x), b[2] = Elem<T>::hi(y[u].x), a[3] = Elem<T>::lo(y[u].y), b[3] = Elem<T>::hi(y[u].y);
-        } else {
-          a[0] = Elem<T>::lo(x[u].x), a[1] = Elem<T>::hi(x[u].x), a[2] = Elem<T>::lo(x[u].y), a[3] = Elem<T>::hi(x[u].y);
-          b[0] = Elem<T>::lo(y[u].x), b[1] = Elem<T>::hi(y[u].x), b[2] = Elem<T>::lo(y[u].y), b[3] = Elem<T>::hi(y[u].y);
-        }
-        if (p.q_weight || p.k_weight) {
-          float sum = 0.f;
+            for (int i = 0; i < 4; ++i) ffma2(sx, sy, a[i], bb[i], a[i], bb[i], sx, sy);
+            float sum = sx + sy;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) sum += a[i] * a[i] + b[i] * b[i];
-#pragma unroll
-          for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
-          const T* w = reinterpret_cast<const T*>(is_q ? p.q_weight : is_k ? p.k_weight : nullptr);
-          if (w) {
+            for (int o = LPH / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(kAll, sum, o);
             const float f = rsqrtf(sum * (1.f / D) + p.eps);
-            const uint2 wx = __ldg(reinterpret_cast<const uint2*>(w + lo)), wy = __ldg(reinterpret_cast<const uint2*>(w + hi));
-            const float wl[4] = {Elem<T>::lo(wx.x), Elem<T>::hi(wx.x), Elem<T>::lo(wx.y), Elem<T>::hi(wx.y)};
-            const float wh[4] = {Elem<T>::lo(wy.x), Elem<T>::hi(wy.x), Elem<T>::lo(wy.y), Elem<T>::hi(wy.y)};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              a[i] *= f * (INTER ? (i < 2 ? wl[2 * i] : wh[2 * i - 4]) : wl[i]);
-              b[i] *= f * (INTER ? (i < 2 ? wl[2 * i + 1] : wh[2 * i - 3]) : wh[i]);
+              a[i] *= f * wa[i];
+              bb[i] *= f * wb[i];
             }
           }
-        }
-        uint2 xo = x[u], yo = y[u];  // values: as they are
-        if (is_q || is_k) {
           float za[4], zb[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            za[i] = a[i] * c[i] - b[i] * s[i];
-            zb[i] = b[i] * c[i] + a[i] * s[i];
+            za[i] = a[i] * c[i] - bb[i] * sn[i];
+            zb[i] = bb[i] * c[i] + a[i] * sn[i];
           }
-          if constexpr (INTER) {
-            xo = make_uint2(Elem<T>::pack(za[0], zb[0]), Elem<T>::pack(za[1], zb[1]));
-            yo = make_uint2(Elem<T>::pack(za[2], zb[2]), Elem<T>::pack(za[3], zb[3]));
-          } else {
-            xo = make_uint2(Elem<T>::pack(za[0], za[1]), Elem<T>::pack(za[2], za[3]));
-            yo = make_uint2(Elem<T>::pack(zb[0], zb[1]), Elem<T>::pack(zb[2], zb[3]));
+          if (row < n) {
+            T* to = dst + row * D;
+            if constexpr (INTER) {
+              *reinterpret_cast<uint2*>(to + lo) = make_uint2(Elem<T>::pack(za[0], zb[0]), Elem<T>::pack(za[1], zb[1]));
+              *reinterpret_cast<uint2*>(to + hi) = make_uint2(Elem<T>::pack(za[2], zb[2]), Elem<T>::pack(za[3], zb[3]));
+            } else {
+              *reinterpret_cast<uint2*>(to + lo) = make_uint2(Elem<T>::pack(za[0], za[1]), Elem<T>::pack(za[2], za[3]));
+              *reinterpret_cast<uint2*>(to + hi) = make_uint2(Elem<T>::pack(zb[0], zb[1]), Elem<T>::pack(zb[2], zb[3]));
+            }
           }
-        }
-        if (is_q || (hh < heads && write_kv)) {
-          T* dst = is_q ? reinterpret_cast<T*>(p.q_out) + ((size_t)t * p.q_heads + h) * D
-                        : reinterpret_cast<T*>(is_k ? p.k_cache : p.v_cache) + ((size_t)slot * p.kv_heads + h) * D;
-          *reinterpret_cast<uint2*>(dst + lo) = xo;
-          *reinterpret_cast<uint2*>(dst + hi) = yo;
         }
       }
     }
+    if (ti < p.num_tokens) issue(ti, bi, s);
+    advance(ti, bi);
+    t = t1, b = b1, w = w1, c4 = c4n, s4 = s4n;
+    t1 = t2, b1 = b2, w1 = w2;
   }
 }
 
-template <int D, typename T>
+template <int D, typename T, bool INTER>
 cudaError_t launch_t(const NormRopeParams& p, cudaStream_t stream) {
-  constexpr int ROWS = kRopeThreads / (D / 8);
-  const int heads = p.q_heads + 2 * p.kv_heads;
-  const int shares = (heads + ROWS - 1) / ROWS;
-  // few tokens: a CTA per share of the heads, so that the loads of a token
-  // are all in flight at once
-  const int sms = num_sms() > 0 ? num_sms() : 1;
-  const int gy = (int64_t)p.num_tokens * shares <= 4 * (int64_t)sms ? shares : 1;
-  const int64_t cap = 8 * (int64_t)sms;  // 8 CTAs of 256 threads per SM
-  const unsigned gx = (unsigned)(p.num_tokens < cap ? p.num_tokens : cap);
-  return p.interleaved ? launch_pdl(norm_rope_kernel<D, T, true>, dim3(gx, gy), dim3(kRopeThreads), 0, stream, p)
-                       : launch_pdl(norm_rope_kernel<D, T, false>, dim3(gx, gy), dim3(kRopeThreads), 0, stream, p);
+  constexpr int HEADS = kItemBytes / (2 * D);
+  auto kern = norm_rope_kernel<D, T, INTER>;
+  auto bytes = [](int warps) { return warps * kRopeStages * (kItemBytes + 8); };
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && !attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes(kRopeMaxWarps));
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  const int64_t bpt = (p.q_heads + HEADS - 1) / HEADS + 2 * ((p.kv_heads + HEADS - 1) / HEADS);
+  const int64_t items = p.num_tokens * bpt, sms = num_sms() > 0 ? num_sms() : 1;
+  // few items: two warps a CTA, so that they spread over the SMs; many: 32
+  // warps an SM (192 KB of rings) that walk the items
+  const int warps = items <= 2 * kRopeMaxWarps * sms ? 2 : kRopeMaxWarps;
+  const int64_t want = (items + warps - 1) / warps, cap = 4 * sms;
+  const unsigned grid = (unsigned)(warps == 2 || want < cap ? want : cap);
+  return launch_pdl(kern, dim3(grid), dim3(32 * warps), bytes(warps), stream, p);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const NormRopeParams& p, int head_dim, pa_dtype dt, cudaStream_t stream) {
   if (p.num_tokens == 0) return cudaSuccess;
-  if (head_dim == 128) return dt == PA_BF16 ? launch_t<128, __nv_bfloat16>(p, stream) : launch_t<128, __half>(p, stream);
-  if (head_dim == 64) return dt == PA_BF16 ? launch_t<64, __nv_bfloat16>(p, stream) : launch_t<64, __half>(p, stream);
+  const bool b = dt == PA_BF16, i = p.interleaved != 0;
+  if (head_dim == 128)
+    return b ? (i ? launch_t<128, __nv_bfloat16, true>(p, stream) : launch_t<128, __nv_bfloat16, false>(p, stream))
+             : (i ? launch_t<128, __half, true>(p, stream) : launch_t<128, __half, false>(p, stream));
+  if (head_dim == 64)
+    return b ? (i ? launch_t<64, __nv_bfloat16, true>(p, stream) : launch_t<64, __nv_bfloat16, false>(p, stream))
+             : (i ? launch_t<64, __half, true>(p, stream) : launch_t<64, __half, false>(p, stream));
   return cudaErrorInvalidValue;
 }
 
