@@ -590,8 +590,15 @@ int pa_verify_tree(const void* q, const int32_t* q_start, const uint64_t* tree_m
  *                 request keeps no score either.
  *   workspace     at least pa_decode_accumulate_workspace_size(...) bytes: the
  *                 partials, and the logits of the call
- * Everything else as pa_decode.
+ *   split_tokens  as pa_decode; 0 = the library's choice for this call, which
+ *                 also depends on num_seqs and kv_heads
+ *                 (pa_decode_accumulate_split_tokens tells it)
+ * Everything else as pa_decode, whose output it equals bit for bit at the same
+ * partition size.
  * ------------------------------------------------------------------------- */
+int pa_decode_accumulate_split_tokens(int num_seqs, int q_heads, int kv_heads, int max_blocks_per_seq, int block_size,
+                                      int split_tokens);
+
 size_t pa_decode_accumulate_workspace_size(int num_seqs, int q_heads, int kv_heads, int head_dim,
                                            int max_blocks_per_seq, int block_size, int split_tokens);
 

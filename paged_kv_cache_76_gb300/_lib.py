@@ -105,6 +105,7 @@ PROTOTYPES = {
     "pa_verify_tree_split_tokens": (_I, [_I, _I, _I, _I, _I, _I, _I]),
     "pa_verify_tree_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),
     "pa_verify_tree": (_I, [_P, _P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P, _I, _P]),
+    "pa_decode_accumulate_split_tokens": (_I, [_I, _I, _I, _I, _I, _I]),
     "pa_decode_accumulate_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
     "pa_decode_accumulate": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _F, _I, _P, _P, _I, _I, _P, _P, _SZ,
                                   _P, _I, _P]),

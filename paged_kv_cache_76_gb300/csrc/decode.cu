@@ -46,7 +46,7 @@
 // records PA_DEVERR_CONTEXT_LEN and the rest counts as empty.
 //
 // Logits (LOGITS, q_len = 1): each scaled score is also stored, fp32 in log2
-// units, token-major with the group's heads together ([token][group]), for the
+// units, token-major with the group's heads together ([token][group_pad]), for the
 // pass that turns them into weights once the row's sum is known; that sum is
 // taken over the unrounded probabilities (the output's own sum is over those
 // rounded for the P.V product, up to 2^-9 off where one token takes most).
@@ -328,15 +328,14 @@ __global__ void __launch_bounds__(WARPS * 32)
       if constexpr (LOGITS) {
         // columns n, n+1 (heads of the group) of tokens t0 and t0 + 8
         const int n = col0 + nt * 8 + 2 * (lane & 3);
-        float* lg = p.logits + (((size_t)r * p.kv_heads + h) * cap + t0) * G + n;
-        if (n + 1 < G && (G & 1) == 0) {
+        const int gp = p.group_pad;
+        float* lg = p.logits + (((size_t)r * p.kv_heads + h) * cap + t0) * gp + n;
+        if (n + 1 < gp) {
           if (t0 < tok1) *reinterpret_cast<float2*>(lg) = make_float2(s0, s1);
-          if (t0 + 8 < tok1) *reinterpret_cast<float2*>(lg + 8 * G) = make_float2(s2, s3);
-        } else {
-          if (n < G && t0 < tok1) lg[0] = s0;
-          if (n + 1 < G && t0 < tok1) lg[1] = s1;
-          if (n < G && t0 + 8 < tok1) lg[8 * G] = s2;
-          if (n + 1 < G && t0 + 8 < tok1) lg[8 * G + 1] = s3;
+          if (t0 + 8 < tok1) *reinterpret_cast<float2*>(lg + 8 * gp) = make_float2(s2, s3);
+        } else if (n < gp) {  // one head
+          if (t0 < tok1) lg[0] = s0;
+          if (t0 + 8 < tok1) lg[8 * gp] = s2;
         }
       }
       float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
@@ -647,58 +646,71 @@ __global__ void __launch_bounds__(256) lse_merge_warp_kernel(const MergeParams p
 // computes for its own heads.  One thread owns a token and adds its heads in
 // order, so the result is the same bits on every run; nothing is atomic.
 //
-// Bound by memory: 4 * group bytes of logits (just written, mostly still in
-// L2) and 8 bytes of score per token and KV head, beside the 4 * head_dim
-// bytes of K and V that the partition pass reads.  A CTA takes p.chunk tokens:
+// Bound by memory: 4 bytes of logits per head of the group (just written,
+// mostly still in L2) and 8 bytes of score per token and KV head, beside the
+// 4 * head_dim bytes of K and V that the partition pass reads - if enough loads
+// are under way: each thread takes the logits of 16 / GP tokens at a time, and
+// its first ones while the CTA works out M and W.  A CTA takes p.chunk tokens,
 // enough that the partials it reads for M and W stay below a quarter of its
 // logits.
 constexpr int kMaxGroup = 16;
 
-// Sum over the group of one token's weights; lg: its `G` logits.
-template <int GV>
-__device__ __forceinline__ float token_weight(const float* lg, int G, const float* s_m, const float* s_inv) {
-  float w = 0.f;
-  for (int g = 0; g < G; g += GV) {
-    float x[GV];
-    if constexpr (GV == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(lg + g);
-      x[0] = v.x, x[1] = v.y, x[2] = v.z, x[3] = v.w;
-    } else {
-      x[0] = lg[g];
-    }
-#pragma unroll
-    for (int e = 0; e < GV; ++e) w += exp2f(x[e] - s_m[g + e]) * s_inv[g + e];
-  }
-  return w;
-}
-
-template <int GV>
+// GP: floats between tokens (the group rounded up to 1, 2 or a multiple of 4).
+template <int GP>
 __device__ __forceinline__ void add_weights(const AccumulateParams& p, int part) {
+  constexpr int U = kMaxGroup / GP;  // tokens of a thread at a time
   __shared__ float s_m[kMaxGroup], s_inv[kMaxGroup];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x;
   const int chunk = part % p.chunks, rh = part / p.chunks;
   const int h = rh % p.kv_heads, r = rh / p.kv_heads;
-  int ctx = __ldg(p.lens + r);
-  ctx = ctx < 0 ? 0 : min(ctx, p.cap);
+  const int ctx = min(max(__ldg(p.lens + r), 0), p.cap);
   const int row = p.score_rows ? __ldg(p.score_rows + r) : r;
   const int t0 = chunk * p.chunk;
-  if (row < 0 || t0 >= ctx) {
+  if (row < 0 || row >= p.num_rows || t0 >= ctx) {
     if (row >= p.num_rows && t0 == 0 && tid == 0) record_error(p.err, PA_DEVERR_SCORE_ROW);
     return;
   }
+  const int end = min(ctx, p.score_len), t1 = min(t0 + p.chunk, end);
+  const size_t at = ((size_t)row * p.kv_heads + h) * p.score_len;
+  const float* lg = p.logits + ((size_t)r * p.kv_heads + h) * p.cap * GP;
+  float x[U][GP], old[U];
+  auto load = [&](int tb) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = tb + u * threads + tid;
+      if (t < t1) {
+        const float* src = lg + (size_t)t * GP;
+        old[u] = p.scores[at + t];
+        if constexpr (GP >= 4) {
+#pragma unroll
+          for (int g = 0; g < GP; g += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(src + g);
+            x[u][g] = v.x, x[u][g + 1] = v.y, x[u][g + 2] = v.z, x[u][g + 3] = v.w;
+          }
+        } else if constexpr (GP == 2) {
+          const float2 v = *reinterpret_cast<const float2*>(src);
+          x[u][0] = v.x, x[u][1] = v.y;
+        } else {
+          x[u][0] = *src;
+        }
+      }
+    }
+  };
+  load(t0);
   const int G = p.group;
   const int nsplit = (ctx + p.split_tokens - 1) / p.split_tokens;
-  for (int g = warp; g < G; g += threads / 32) {
+  for (int g = warp; g < GP; g += threads / 32) {
     const size_t prow = ((size_t)r * p.q_heads + h * G + g) * p.max_splits;
-    float M = -INFINITY;
-    for (int c = lane; c < nsplit; c += 32) M = fmaxf(M, p.part_m[prow + c]);
+    float M = -INFINITY, l = 0.f;
+    if (g < G) {  // heads that pad the group weigh nothing
+      for (int c = lane; c < nsplit; c += 32) M = fmaxf(M, p.part_m[prow + c]);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    if (M == -INFINITY) M = 0.f;
-    float l = 0.f;
-    for (int c = lane; c < nsplit; c += 32) l += exp2f(p.part_m[prow + c] - M) * p.part_w[prow + c];
+      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      if (M == -INFINITY) M = 0.f;
+      for (int c = lane; c < nsplit; c += 32) l += exp2f(p.part_m[prow + c] - M) * p.part_w[prow + c];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    }
     if (lane == 0) {
       s_m[g] = M;
       s_inv[g] = l > 0.f ? 1.f / l : 0.f;
@@ -707,24 +719,29 @@ __device__ __forceinline__ void add_weights(const AccumulateParams& p, int part)
   bool twice = false;  // an earlier request has this row: it alone keeps score
   if (p.score_rows)
     for (int i = tid; i < r; i += threads) twice |= __ldg(p.score_rows + i) == row;
-  if (__syncthreads_or(twice) || row >= p.num_rows) {
+  if (__syncthreads_or(twice)) {
     if (tid == 0) record_error(p.err, PA_DEVERR_SCORE_ROW);
     return;
   }
-  if (ctx > p.score_len) {
-    if (tid == 0) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
-    ctx = p.score_len;
+  if (ctx > p.score_len && t0 == 0 && tid == 0) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
+  for (int tb = t0; tb < t1; tb += U * threads) {
+    if (tb > t0) load(tb);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int t = tb + u * threads + tid;
+      if (t < t1) {
+        float w = 0.f;
+#pragma unroll
+        for (int g = 0; g < GP; ++g)
+          if (g < G) w += exp2f(x[u][g] - s_m[g]) * s_inv[g];
+        p.scores_out[at + t] = old[u] + w;
+      }
+    }
   }
-  const int t1 = min(t0 + p.chunk, ctx);
-  const size_t at = ((size_t)row * p.kv_heads + h) * p.score_len;
-  const float* lg = p.logits + ((size_t)r * p.kv_heads + h) * p.cap * G;
-#pragma unroll 2
-  for (int t = t0 + tid; t < t1; t += threads)
-    p.scores_out[at + t] = p.scores[at + t] + token_weight<GV>(lg + (size_t)t * G, G, s_m, s_inv);
 }
 
 // THREADS 256: a warp per row (at most 32 partitions); 128: the CTA per row.
-template <int D, typename T, int THREADS, int GV>
+template <int D, typename T, int THREADS>
 __global__ void __launch_bounds__(THREADS)
     merge_accumulate_kernel(const MergeParams mp, const AccumulateParams ap, int merge_ctas) {
   griddep_wait();
@@ -733,28 +750,34 @@ __global__ void __launch_bounds__(THREADS)
     if constexpr (THREADS == 256) merge_row_by_warp<D, T>(mp, blockIdx.x * 8 + (threadIdx.x >> 5));
     else merge_row_by_cta<D, T>(mp, blockIdx.x);
   } else {
-    add_weights<GV>(ap, blockIdx.x - merge_ctas);
+    const int part = blockIdx.x - merge_ctas;
+    switch (ap.group_pad) {
+      case 1: add_weights<1>(ap, part); break;
+      case 2: add_weights<2>(ap, part); break;
+      case 4: add_weights<4>(ap, part); break;
+      case 8: add_weights<8>(ap, part); break;
+      case 12: add_weights<12>(ap, part); break;
+      default: add_weights<16>(ap, part); break;
+    }
   }
 }
 
 template <int D, typename T>
 cudaError_t launch_merge_accumulate_t(const MergeParams& mp, const AccumulateParams& p0, cudaStream_t stream) {
   AccumulateParams ap = p0;
-  const int64_t least = 8 * (int64_t)ap.max_splits;
-  ap.chunk = (int)((least > 512 ? least : 512) + 255) / 256 * 256;
-  ap.chunks = (ap.cap - 1) / ap.chunk + 1;
   const int64_t rows = (int64_t)mp.num_seqs * mp.q_heads;
   const bool warps = mp.max_splits <= 32;
+  const int threads = warps ? 256 : 128;
   const int64_t merge_ctas = warps ? (rows + 7) / 8 : rows;
+  // tokens: whole rounds of the CTA's threads, at least eight per partition
+  const int round = threads * (kMaxGroup / ap.group_pad);
+  ap.chunk = (8 * ap.max_splits + round - 1) / round * round;
+  ap.chunks = (ap.cap - 1) / ap.chunk + 1;
   const int64_t grid = merge_ctas + (int64_t)ap.chunks * ap.kv_heads * ap.num_seqs;
   if (grid > INT32_MAX) return cudaErrorInvalidValue;
-  const bool v4 = ap.group % 4 == 0;  // a token's logits are whole 16-byte vectors
   const dim3 g((unsigned)grid);
-  if (warps)
-    return v4 ? launch_pdl(merge_accumulate_kernel<D, T, 256, 4>, g, dim3(256), 0, stream, mp, ap, (int)merge_ctas)
-              : launch_pdl(merge_accumulate_kernel<D, T, 256, 1>, g, dim3(256), 0, stream, mp, ap, (int)merge_ctas);
-  return v4 ? launch_pdl(merge_accumulate_kernel<D, T, 128, 4>, g, dim3(128), 0, stream, mp, ap, (int)merge_ctas)
-            : launch_pdl(merge_accumulate_kernel<D, T, 128, 1>, g, dim3(128), 0, stream, mp, ap, (int)merge_ctas);
+  return warps ? launch_pdl(merge_accumulate_kernel<D, T, 256>, g, dim3(256), 0, stream, mp, ap, (int)merge_ctas)
+               : launch_pdl(merge_accumulate_kernel<D, T, 128>, g, dim3(128), 0, stream, mp, ap, (int)merge_ctas);
 }
 
 template <int D, int BSUB, int NT, typename T, bool CONTIG = false, int CW = 1, bool LOGITS = false>

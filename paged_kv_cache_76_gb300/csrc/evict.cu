@@ -12,52 +12,72 @@ constexpr unsigned kAll = 0xffffffffu;
 
 // Order-preserving map of fp32 to uint32 (-0 equals +0, NaN below everything).
 __device__ __forceinline__ uint32_t score_key(float x) {
-  if (x != x) return 0u;
-  const uint32_t b = x == 0.f ? 0u : __float_as_uint(x);
-  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+  const uint32_t b = __float_as_uint(x + 0.f);  // -0 + 0 is +0
+  const uint32_t k = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return x == x ? k : 0u;
 }
 
-// A cluster of CTAs takes one (KV head, request): each holds its part of the
-// row's keys in shared memory, read once.  The heavy-th largest key of the
-// candidates [sink, L - recent) is found digit by digit (11, 11 and 10 bits
-// from the top): a histogram per CTA, then the digit at which the count from
-// above passes what is still wanted.  The 2048 digits are 16 slices.  In a
-// cluster each slice has an owner to which the others add their non-empty
-// digits (few: scores share a handful of exponents, and later digits only
-// count keys of the chosen prefix), and every CTA adds its 16 slice sums to
-// every other's, so one cluster barrier per digit does: each CTA then finds the
-// slice in its own sums and reads that slice's 128 digits from the owner.
-// Then every warp counts its run of keys above and equal to the result, the
-// counts before a warp give its place in the list, and it writes the indices
-// in order by ballots; of the equal keys the first ones.
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
+// A cluster of CTAs takes one (KV head, request), a CTA a run of its candidates
+// [sink, L - recent), a warp a run of that.  The heavy-th largest key is found
+// digit by digit (11, 11 and 10 bits from the top): a histogram per CTA, then
+// the digit at which the count from above passes what is still wanted.  The
+// 2048 digits are 16 slices.  In a cluster each slice has an owner to which the
+// others add their non-empty digits (few: scores share a handful of exponents,
+// and later digits only count keys of the chosen prefix), and every CTA adds
+// its 16 slice sums to every other's, so one cluster barrier per digit does:
+// a warp finds the slice in its CTA's sums and reads that slice's 128 digits
+// from the owner.
+//
+// The keys are gone over three times: for the first digit; to list the keys of
+// the chosen first digit (a few in a hundred: the other digits, and the counts
+// of keys above and equal to the result, come from the list; should it not
+// hold them, from all keys); and to write the indices in order, by ballots,
+// each warp from the counts before it - of the equal keys the first ones.
+// Bound by the instructions and atomics per key and the latency of the steps
+// between (memory is 4 bytes per candidate): keys stay in shared memory as far
+// as that leaves every CTA resident at once, and the rest are read again from
+// L2.  Measured on GB300: 512 rows of 2300 keys 15.5 us, 64 of 85000 30 us, 8
+// of 131000 18 us.  A range for the threshold from a sample of the row, which
+// saves most atomics, measured slower (25, 36 and 21 us): the sample's own
+// steps cost more.
 constexpr int kSelBins = 2048;
-constexpr int kSelSlices = 16;                       // one per warp
-constexpr int kSelSlice = kSelBins / kSelSlices;     // four digits per lane
-static_assert(kSelSlices == kSelWarps && kSelSlice == 128, "a warp sums a slice");
-constexpr int kSelMaxHeld = 40960;  // keys of a CTA in shared memory; the rest are read again
+constexpr int kSelSlices = 16;
+constexpr int kSelSlice = kSelBins / kSelSlices;     // 128 digits, four per lane
+constexpr int kSelList = 1024;
+constexpr int kSelBatch = 8;                         // keys of a lane loaded together
 
-__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictSelectParams p) {
+// Shared memory in words before the keys, for a cluster of C.
+__host__ __device__ constexpr int select_words(int C) {
+  return kSelBins + (C == 1 ? kSelBins : 3 * kSelBins / C) + 2 * kSelList;
+}
+
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictSelectParams p) {
+  constexpr int NW = THREADS / 32;
   extern __shared__ uint4 smem_raw[];
+  const int C = (int)cluster_size(), rank = (int)cluster_rank();
   uint32_t* hist = reinterpret_cast<uint32_t*>(smem_raw);  // [kSelBins] this CTA's digits
-  uint32_t* sums = hist + kSelBins;                        // [3][kSelBins] the cluster's, of the slices it owns
-  uint32_t* keys = sums + 3 * kSelBins;                    // [held]
+  uint32_t* sums = hist + kSelBins;                        // the cluster's, of the slices it owns, per digit
+  const int sums_stride = C == 1 ? 0 : kSelBins / C;
+  uint2* list = reinterpret_cast<uint2*>(sums + (C == 1 ? kSelBins : 3 * sums_stride));  // (key, place in the run)
+  uint32_t* keys = reinterpret_cast<uint32_t*>(list + kSelList);                        // [p.held]
   __shared__ uint32_t slices[3][kSelSlices];               // the cluster's slice sums
-  __shared__ __align__(16) uint32_t s_count[4];            // this CTA's keys above and equal to the threshold
-  __shared__ uint32_t w_above[kSelWarps], w_equal[kSelWarps];
+  __shared__ __align__(16) uint32_t s_count[4];            // this CTA's keys above and equal to the result
+  __shared__ uint32_t w_above[NW], w_equal[NW];
+  __shared__ uint32_t s_listed, s_want, s_prefix, s_before[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  for (int i = tid; i < kSelBins; i += kSelThreads) smem_raw[i] = make_uint4(0, 0, 0, 0);  // hist and sums
+  const int zero = (kSelBins + (C == 1 ? 0 : 3 * sums_stride)) / 4;
+  for (int i = tid; i < zero; i += THREADS) smem_raw[i] = make_uint4(0, 0, 0, 0);
   if (tid < 3 * kSelSlices) (&slices[0][0])[tid] = 0;
+  if (tid == 0) s_listed = 0;
   griddep_wait();
   griddep_launch_dependents();
-  const int C = (int)cluster_size(), rank = (int)cluster_rank();
   const int r = blockIdx.y, g = blockIdx.x / C;
   const int budget = p.sink + p.heavy + p.recent;
   int32_t* keep = p.keep + ((size_t)r * p.kv_heads + g) * budget;
   const int row = p.score_rows ? __ldg(p.score_rows + r) : r;
   const int L = __ldg(p.lens + r);
-  const int t0 = rank * kSelThreads + tid, tn = C * kSelThreads;  // this thread among the cluster's
+  const int t0 = rank * THREADS + tid, tn = C * THREADS;  // this thread among the cluster's
   if (row < 0 || row >= p.num_rows || L < 0 || L > p.score_len) {
     if (t0 == 0) {
       record_error(p.err, row < 0 || row >= p.num_rows ? PA_DEVERR_SCORE_ROW : PA_DEVERR_CONTEXT_LEN);
@@ -77,24 +97,33 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictSe
   const float* sc = p.scores + ((size_t)row * p.kv_heads + g) * p.score_len + p.sink;
   const int n = L - p.sink - p.recent;  // > heavy
   // this CTA's run of candidates, and each warp's run of it (whole warps wide)
-  const int run = ((n - 1) / (C * kSelThreads) + 1) * kSelThreads;
+  const int run = ((n - 1) / (C * THREADS) + 1) * THREADS;
   const int c0 = (int)min((int64_t)rank * run, (int64_t)n), m = min(run, n - c0);
   sc += c0;
-  auto key = [&](int i) { return i < p.held ? keys[i] : score_key(__ldg(sc + i)); };
+  const int wrun = ((m + THREADS - 1) / THREADS) * 32;
+  const int w0 = min(warp * wrun, m), w1 = min(w0 + wrun, m);
+  // a lane's keys i0 + lane + 32 u; behind the run's end 0
+  auto batch = [&](int i0, uint32_t (&k)[kSelBatch]) {
+#pragma unroll
+    for (int u = 0; u < kSelBatch; ++u) {
+      const int i = i0 + 32 * u + lane;
+      k[u] = i >= w1 ? 0u : i < p.held ? keys[i] : score_key(__ldg(sc + i));
+    }
+  };
   if (C == 1) __syncthreads();  // the counts are zero, in every CTA
   else cluster_sync();
 
   // first digit while the keys come in
-  constexpr int U = 8;
-  for (int i0 = tid; i0 < m; i0 += U * kSelThreads) {
-    float x[U];
+  for (int i0 = w0; i0 < w1; i0 += 32 * kSelBatch) {
+    float x[kSelBatch];
 #pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (i0 + u * kSelThreads < m) x[u] = __ldg(sc + i0 + u * kSelThreads);
+    for (int u = 0; u < kSelBatch; ++u)
+      if (i0 + 32 * u + lane < w1) x[u] = __ldg(sc + i0 + 32 * u + lane);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kSelThreads;
-      if (i < m) {
+    for (int u = 0; u < kSelBatch; ++u) {
+      if (i0 + 32 * u >= w1) break;
+      const int i = i0 + 32 * u + lane;
+      if (i < w1) {
         const uint32_t k = score_key(x[u]);
         if (i < p.held) keys[i] = k;
         atomicAdd(&hist[k >> 21], 1u);
@@ -102,123 +131,211 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const EvictSe
     }
   }
   uint32_t prefix = 0, want = p.heavy;  // of the keys with this prefix, `want` are still to be chosen
+  uint32_t gt = 0;                      // this lane's keys above the first digit
 #pragma unroll 1
   for (int d = 0; d < 3; ++d) {
     const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bits = d == 2 ? 10 : 11;
-    if (d > 0) {
-      for (int i = tid; i < m; i += kSelThreads) {
-        const uint32_t k = key(i);
-        if ((k >> (shift + bits)) == prefix) atomicAdd(&hist[(k >> shift) & ((1u << bits) - 1)], 1u);
+    const uint32_t digits = (1u << bits) - 1;
+    if (d == 1) {
+      for (int i0 = w0; i0 < w1; i0 += 32 * kSelBatch) {
+        uint32_t k[kSelBatch];
+        batch(i0, k);
+#pragma unroll
+        for (int u = 0; u < kSelBatch; ++u) {
+          if (i0 + 32 * u >= w1) break;
+          const int i = i0 + 32 * u + lane;
+          gt += (k[u] >> 21) > prefix;  // a key behind the end is 0: not above anything
+          const bool same = i < w1 && (k[u] >> 21) == prefix;
+          const uint32_t eq = __ballot_sync(kAll, same);
+          if (eq) {
+            if (same) atomicAdd(&hist[(k[u] >> shift) & digits], 1u);
+            uint32_t at = 0;
+            if (lane == 0) at = atomicAdd(&s_listed, (uint32_t)__popc(eq));
+            at = __shfl_sync(kAll, at, 0) + __popc(eq & ((1u << lane) - 1));
+            if (same && at < kSelList) list[at] = make_uint2(k[u], i);
+          }
+        }
       }
-    }
-    __syncthreads();
-    // slice `warp` of this CTA's digits, four of them in each lane
-    uint32_t* mine = hist + warp * kSelSlice + 4 * lane;
-    const uint4 v = *reinterpret_cast<const uint4*>(mine);
-    *reinterpret_cast<uint4*>(mine) = make_uint4(0, 0, 0, 0);  // for the next digit
-    const uint32_t sum = __reduce_add_sync(kAll, v.x + v.y + v.z + v.w);
-    uint32_t* total = sums + d * kSelBins;  // [kSelBins]
-    if (C == 1) {
-      *reinterpret_cast<uint4*>(total + warp * kSelSlice + 4 * lane) = v;
-      if (lane == 0) slices[d][warp] = sum;
-      __syncthreads();
-    } else {
-      const uint32_t at = smem_u32(total + warp * kSelSlice + 4 * lane), owner = warp % C;
-      if (v.x) cluster_add(at, owner, v.x);
-      if (v.y) cluster_add(at + 4, owner, v.y);
-      if (v.z) cluster_add(at + 8, owner, v.z);
-      if (v.w) cluster_add(at + 12, owner, v.w);
-      if (lane < C && sum) cluster_add(smem_u32(&slices[d][warp]), lane, sum);
-      cluster_sync();
-    }
-    // every warp: lane l holds slice 15 - l, so that a scan counts from the top
-    const uint32_t sl = lane < kSelSlices ? slices[d][kSelSlices - 1 - lane] : 0u;
-    uint32_t upto = sl;
+    } else if (d == 2) {
+      if (s_listed <= kSelList) {
+        for (int j = tid; j < (int)s_listed; j += THREADS)
+          if ((list[j].x >> 10) == prefix) atomicAdd(&hist[list[j].x & digits], 1u);
+      } else {
+        for (int i0 = w0; i0 < w1; i0 += 32 * kSelBatch) {
+          uint32_t k[kSelBatch];
+          batch(i0, k);
 #pragma unroll
-    for (int o = 1; o < kSelSlices; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(kAll, upto, o);
-      if (lane >= o) upto += y;
-    }
-    const int hit = __ffs(__ballot_sync(kAll, upto >= want)) - 1;  // one of the 16: they hold all
-    want -= __shfl_sync(kAll, upto - sl, hit);
-    const int slice = kSelSlices - 1 - hit;
-    // its digits, lane l: the four below 128 - 4 l
-    const uint32_t q0 = smem_u32(total + slice * kSelSlice + kSelSlice - 4 * (lane + 1));
-    const uint4 q = C == 1 ? *reinterpret_cast<const uint4*>(total + slice * kSelSlice + kSelSlice - 4 * (lane + 1))
-                           : cluster_ld4(q0, slice % C);
-    const uint32_t four = q.x + q.y + q.z + q.w;
-    upto = four;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(kAll, upto, o);
-      if (lane >= o) upto += y;
-    }
-    const int at = __ffs(__ballot_sync(kAll, upto >= want)) - 1;
-    uint32_t above = upto - four, digit = slice * kSelSlice + kSelSlice - 1 - 4 * lane;  // lane `at`'s are wanted
-    if (above + q.w < want) {
-      above += q.w;
-      --digit;
-      if (above + q.z < want) {
-        above += q.z;
-        --digit;
-        if (above + q.y < want) {
-          above += q.y;
-          --digit;
+          for (int u = 0; u < kSelBatch; ++u)
+            if (i0 + 32 * u + lane < w1 && (k[u] >> 10) == prefix) atomicAdd(&hist[k[u] & digits], 1u);
         }
       }
     }
-    want -= __shfl_sync(kAll, above, at);
-    prefix = (prefix << bits) | __shfl_sync(kAll, digit, at);
+    __syncthreads();
+    // a warp's slices of this CTA's digits, four of them in each lane
+    for (int sl = warp; sl < kSelSlices; sl += NW) {
+      uint4* mine = reinterpret_cast<uint4*>(hist + sl * kSelSlice) + lane;
+      const uint4 v = *mine;
+      *mine = make_uint4(0, 0, 0, 0);  // for the next digit
+      const uint32_t sum = __reduce_add_sync(kAll, v.x + v.y + v.z + v.w);
+      uint32_t* total = sums + d * sums_stride + sl / C * kSelSlice + 4 * lane;
+      if (C == 1) {
+        *reinterpret_cast<uint4*>(total) = v;
+        if (lane == 0) slices[d][sl] = sum;
+      } else {
+        const uint32_t at = smem_u32(total), owner = sl % C;
+        if (v.x) cluster_add(at, owner, v.x);
+        if (v.y) cluster_add(at + 4, owner, v.y);
+        if (v.z) cluster_add(at + 8, owner, v.z);
+        if (v.w) cluster_add(at + 12, owner, v.w);
+        if (lane < C && sum) cluster_add(smem_u32(&slices[d][sl]), lane, sum);
+      }
+    }
+    if (C == 1) __syncthreads();
+    else cluster_sync();
+    // one warp (all of them would meet at the slice's owner): lane l holds slice
+    // 15 - l, so that a scan counts from the top
+    if (warp == 0) {
+      const uint32_t sl = lane < kSelSlices ? slices[d][kSelSlices - 1 - lane] : 0u;
+      uint32_t upto = sl;
+#pragma unroll
+      for (int o = 1; o < kSelSlices; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(kAll, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const int hit = __ffs(__ballot_sync(kAll, upto >= want)) - 1;  // one of the 16: they hold all
+      want -= __shfl_sync(kAll, upto - sl, hit);
+      const int slice = kSelSlices - 1 - hit;
+      // its digits, lane l: the four below 128 - 4 l
+      const uint32_t* from = sums + d * sums_stride + slice / C * kSelSlice + kSelSlice - 4 * (lane + 1);
+      const uint4 q = C == 1 ? *reinterpret_cast<const uint4*>(from) : cluster_ld4(smem_u32(from), slice % C);
+      const uint32_t four = q.x + q.y + q.z + q.w;
+      upto = four;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(kAll, upto, o);
+        if (lane >= o) upto += y;
+      }
+      const int at = __ffs(__ballot_sync(kAll, upto >= want)) - 1;
+      uint32_t above = upto - four, digit = slice * kSelSlice + kSelSlice - 1 - 4 * lane;  // lane `at`'s are wanted
+      if (above + q.w < want) {
+        above += q.w;
+        --digit;
+        if (above + q.z < want) {
+          above += q.z;
+          --digit;
+          if (above + q.y < want) {
+            above += q.y;
+            --digit;
+          }
+        }
+      }
+      if (lane == at) {
+        s_want = want - above;
+        s_prefix = (prefix << bits) | digit;
+      }
+    }
+    __syncthreads();
+    want = s_want;
+    prefix = s_prefix;
   }
   // prefix: the heavy-th largest key; `want` of the equal ones are taken
-  const int wrun = ((m + kSelThreads - 1) / kSelThreads) * 32;
-  const int w0 = min(warp * wrun, m), w1 = min(w0 + wrun, m);
-  uint32_t gt = 0, eq = 0;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const uint32_t k = i0 + lane < w1 ? key(i0 + lane) : 0u;
-    gt += __popc(__ballot_sync(kAll, i0 + lane < w1 && k > prefix));
-    eq += __popc(__ballot_sync(kAll, i0 + lane < w1 && k == prefix));
-  }
-  if (lane == 0) {
-    w_above[warp] = gt;
-    w_equal[warp] = eq;
+  if (s_listed <= kSelList) {
+    gt = __reduce_add_sync(kAll, gt);
+    if (lane == 0) {
+      w_above[warp] = gt;
+      w_equal[warp] = 0;
+    }
+    __syncthreads();
+    for (int j = tid; j < (int)s_listed; j += THREADS) {
+      const uint2 e = list[j];
+      if (e.x > prefix) atomicAdd(&w_above[e.y / wrun], 1u);
+      if (e.x == prefix) atomicAdd(&w_equal[e.y / wrun], 1u);
+    }
+  } else {
+    uint32_t eq = 0;
+    gt = 0;
+    for (int i0 = w0; i0 < w1; i0 += 32 * kSelBatch) {
+      uint32_t k[kSelBatch];
+      batch(i0, k);
+#pragma unroll
+      for (int u = 0; u < kSelBatch; ++u) {
+        const bool in = i0 + 32 * u + lane < w1;
+        gt += __popc(__ballot_sync(kAll, in && k[u] > prefix));
+        eq += __popc(__ballot_sync(kAll, in && k[u] == prefix));
+      }
+    }
+    if (lane == 0) {
+      w_above[warp] = gt;
+      w_equal[warp] = eq;
+    }
   }
   __syncthreads();
-  uint32_t above = 0, equal = 0;  // keys before this warp's run
+  // keys before this warp's run: lane w holds warp w's, then lane q CTA q's
+  const uint32_t wa = lane < NW ? w_above[lane] : 0u, we = lane < NW ? w_equal[lane] : 0u;
+  uint32_t above = __reduce_add_sync(kAll, lane < warp ? wa : 0u);
+  uint32_t equal = __reduce_add_sync(kAll, lane < warp ? we : 0u);
   if (C > 1) {
+    const uint32_t a = __reduce_add_sync(kAll, wa), e = __reduce_add_sync(kAll, we);
     if (tid == 0) {
-      uint32_t a = 0, e = 0;
-      for (int w = 0; w < kSelWarps; ++w) a += w_above[w], e += w_equal[w];
       s_count[0] = a;
       s_count[1] = e;
     }
     cluster_sync();
-    if (lane < rank) {  // C <= 16: a lane per CTA before this one
-      const uint4 v = cluster_ld4(smem_u32(s_count), lane);
-      above = v.x;
-      equal = v.y;
+    if (warp == 0) {
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (lane < rank) v = cluster_ld4(smem_u32(s_count), lane);
+      v.x = __reduce_add_sync(kAll, v.x);
+      v.y = __reduce_add_sync(kAll, v.y);
+      if (lane == 0) s_before[0] = v.x, s_before[1] = v.y;
     }
-    above = __reduce_add_sync(kAll, above);
-    equal = __reduce_add_sync(kAll, equal);
     cluster_sync();  // no CTA leaves while another reads its counts
-  }
-  for (int w = 0; w < warp; ++w) {
-    above += w_above[w];
-    equal += w_equal[w];
+    above += s_before[0];
+    equal += s_before[1];
   }
   uint32_t out = above + min(equal, want);
   const uint32_t before = (1u << lane) - 1;
   int32_t* to = keep + p.sink;
-  for (int i0 = w0; i0 < w1; i0 += 32) {
-    const bool in = i0 + lane < w1;
-    const uint32_t k = in ? key(i0 + lane) : 0u;
-    const uint32_t beq = __ballot_sync(kAll, in && k == prefix);
-    const bool take = in && (k > prefix || (k == prefix && equal + __popc(beq & before) < want));
-    const uint32_t bt = __ballot_sync(kAll, take);
-    if (take) to[out + __popc(bt & before)] = p.sink + c0 + i0 + lane;
-    out += __popc(bt);
-    equal += __popc(beq);
+  for (int i0 = w0; i0 < w1; i0 += 32 * kSelBatch) {
+    uint32_t k[kSelBatch];
+    batch(i0, k);
+#pragma unroll
+    for (int u = 0; u < kSelBatch; ++u) {
+      if (i0 + 32 * u >= w1) break;
+      const int i = i0 + 32 * u + lane;
+      uint32_t bt = __ballot_sync(kAll, k[u] > prefix);
+      const uint32_t beq = __ballot_sync(kAll, i < w1 && k[u] == prefix);
+      if (beq) {  // the first ones of the equal keys
+        bt |= __ballot_sync(kAll, ((beq >> lane) & 1) && equal + __popc(beq & before) < want);
+        equal += __popc(beq);
+      }
+      if ((bt >> lane) & 1) to[out + __popc(bt & before)] = p.sink + c0 + i;
+      out += __popc(bt);
+    }
   }
+}
+
+template <int THREADS>
+cudaError_t launch_select_t(EvictSelectParams& p, int cluster, int num_seqs, cudaStream_t stream) {
+  auto kern = evict_select_kernel<THREADS>;
+  constexpr int kMost = 224 * 1024;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && !attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  // keys held: as many as leave room for every CTA at once
+  const int64_t sms = num_sms() > 0 ? num_sms() : 152;
+  int64_t per_sm = ((int64_t)p.kv_heads * num_seqs * cluster + sms - 1) / sms;
+  if (per_sm > 2048 / THREADS) per_sm = 2048 / THREADS;
+  const int64_t room = (kMost / per_sm - 4096) / 4 - select_words(cluster);
+  const int64_t run = ((int64_t)p.score_len / ((int64_t)cluster * THREADS) + 1) * THREADS;
+  p.held = (int)(room < 0 ? 0 : run < room ? run : room);
+  const size_t smem = (size_t)(select_words(cluster) + p.held) * 4;
+  return launch_pdl_cluster(kern, cluster, dim3((unsigned)(p.kv_heads * cluster), num_seqs), dim3(THREADS), smem,
+                            stream, p);
 }
 
 // ----------------------------------------------------------------------------
@@ -472,29 +589,19 @@ __global__ void __launch_bounds__(kMoveThreads) compact_small_kernel(const Compa
 cudaError_t launch_evict_select(const EvictSelectParams& p0, int num_seqs, cudaStream_t stream) {
   if (num_seqs == 0) return cudaSuccess;
   EvictSelectParams p = p0;
-  // CTAs per row: enough that each holds 8192 keys or fewer, as long as that
-  // leaves no more than about four CTAs per SM in all (16: opt-in, for the few
-  // long rows that would leave SMs idle)
+  // One CTA per SM: clusters of up to 8 share a row while there are SMs for
+  // them and a thousand keys for each CTA.  A second CTA on an SM only halves
+  // both (64 rows of 85000 keys: clusters of 2, 4, 8 of 1024 threads 30, 42, 80
+  // us; of 512 threads 41, 34, 56).  More rows than SMs: small CTAs, the steps
+  // between the keys cost what short rows do (512 rows of 2300: 256 threads
+  // 15.5 us, 512 17.2, 1024 32.3).
   const int64_t rows = (int64_t)p.kv_heads * num_seqs, sms = num_sms() > 0 ? num_sms() : 152;
   int cluster = 1;
-  while (cluster < 16 && (int64_t)cluster * 8192 < p.score_len && rows * cluster * 2 <= 4 * sms) cluster *= 2;
-  while (cluster < 8 && (int64_t)cluster * kSelMaxHeld < p.score_len) cluster *= 2;
-  const int64_t run = ((int64_t)p.score_len / ((int64_t)cluster * kSelThreads) + 1) * kSelThreads;
-  p.held = (int)(run < kSelMaxHeld ? run : kSelMaxHeld);
-  const size_t smem = (size_t)(4 * kSelBins + p.held) * 4;
-  static bool attr_set[64] = {};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && !attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (4 * kSelBins + kSelMaxHeld) * 4);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    attr_set[dev] = true;
-  }
-  return launch_pdl_cluster(evict_select_kernel, cluster, dim3((unsigned)(p.kv_heads * cluster), num_seqs),
-                            dim3(kSelThreads), smem, stream, p);
+  while (cluster < 8 && rows * cluster * 2 <= sms && (int64_t)cluster * 1024 < p.score_len) cluster *= 2;
+  const int64_t per_cta = (p.score_len + cluster - 1) / cluster;
+  if (rows * cluster > sms && per_cta <= 8192) return launch_select_t<256>(p, cluster, num_seqs, stream);
+  return per_cta <= 2048 ? launch_select_t<512>(p, cluster, num_seqs, stream)
+                         : launch_select_t<1024>(p, cluster, num_seqs, stream);
 }
 
 cudaError_t launch_compact_kv(const CompactParams& p0, int num_seqs, cudaStream_t stream) {

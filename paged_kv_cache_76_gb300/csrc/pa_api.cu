@@ -894,9 +894,10 @@ int pa_norm_rope_and_cache(const void* q, const void* k, const void* v, int64_t 
 namespace {
 
 // Workspace of pa_decode_accumulate: the partials of every partition (and the
-// sums of their unrounded probabilities), then the logits [num_seqs][kv_heads][cap][group].
+// sums of their unrounded probabilities), then the logits
+// [num_seqs][kv_heads][cap][group_pad].
 struct AccumulateSetup {
-  int split, max_splits, cap;
+  int split, max_splits, cap, group_pad;
   DecodeWorkspace ws;
   size_t w_off, logits_off, bytes;
 };
@@ -905,20 +906,46 @@ int accumulate_setup(int num_seqs, int q_heads, int kv_heads, int head_dim, int 
                      int split_tokens, AccumulateSetup* s) {
   if (num_seqs < 0 || num_seqs > 65535 || kv_heads <= 0 || q_heads <= 0 || q_heads % kv_heads != 0 || head_dim <= 0)
     return PA_ERR_INVALID;
+  const int group = q_heads / kv_heads;
+  if (group > 16) return PA_ERR_INVALID;
+  int split = pa_decode_split_tokens(max_blocks_per_seq, block_size, split_tokens);
+  if (split <= 0) return PA_ERR_INVALID;
+  if (split_tokens == 0) {
+    // A warp takes a partition.  Too few of them leave SMs without their 12
+    // warps each: 256, 128 or 64 tokens then.  More than about 54 per SM only
+    // add partials, which every CTA of the second pass reads: doubled.
+    // Measured on GB300 (us; 4 requests of <= 1500 tokens, 28/4 heads): 384
+    // tokens 28.8, 256 20.7, 128 13.1, 64 9.7; 8 of 33..131 thousand, 64/8
+    // heads: 256 523, 512 509, 1024 514, 2048 521.
+    const int64_t sms = sm_count() > 0 ? sm_count() : 152;
+    const int64_t cap = (int64_t)max_blocks_per_seq * block_size, lists = (int64_t)num_seqs * kv_heads;
+    auto units = [&](int sp) { return lists * ((cap + sp - 1) / sp); };
+    if (units(split) < 12 * sms)
+      for (split = 256; split > 64 && units(split) < 12 * sms;) split /= 2;
+    while (units(split) > 54 * sms && split * 2 <= 256 * block_size) split *= 2;
+  }
   DecodeSetup d;
-  const int st = decode_setup(num_seqs, q_heads, head_dim, max_blocks_per_seq, block_size, split_tokens, &d);
+  const int st = decode_setup(num_seqs, q_heads, head_dim, max_blocks_per_seq, block_size, split, &d);
   if (st != PA_OK) return st;
+  s->group_pad = group <= 2 ? group : (group + 3) / 4 * 4;
   s->split = d.split;
   s->max_splits = d.max_splits;
   s->cap = max_blocks_per_seq * block_size;
   s->ws = decode_workspace_layout(num_seqs, q_heads, head_dim, d.max_splits);
   s->w_off = s->ws.bytes;
   s->logits_off = s->w_off + (((size_t)num_seqs * q_heads * d.max_splits * sizeof(float) + 255) & ~size_t(255));
-  s->bytes = s->logits_off + (size_t)num_seqs * q_heads * s->cap * sizeof(float);
+  s->bytes = s->logits_off + (size_t)num_seqs * kv_heads * s->group_pad * s->cap * sizeof(float);
   return PA_OK;
 }
 
 }  // namespace
+
+int pa_decode_accumulate_split_tokens(int num_seqs, int q_heads, int kv_heads, int max_blocks_per_seq, int block_size,
+                                      int split_tokens) {
+  AccumulateSetup s;
+  const int st = accumulate_setup(num_seqs, q_heads, kv_heads, 64, max_blocks_per_seq, block_size, split_tokens, &s);
+  return st != PA_OK ? st : s.split;
+}
 
 size_t pa_decode_accumulate_workspace_size(int num_seqs, int q_heads, int kv_heads, int head_dim,
                                            int max_blocks_per_seq, int block_size, int split_tokens) {
@@ -971,6 +998,7 @@ int pa_decode_accumulate(const void* q, const void* k_cache, const void* v_cache
   p.part_l = reinterpret_cast<float*>(ws + s.ws.l_off);
   p.part_w = reinterpret_cast<float*>(ws + s.w_off);
   p.logits = reinterpret_cast<float*>(ws + s.logits_off);
+  p.group_pad = s.group_pad;
   p.err = err;
   p.maxblk = max_blocks_per_seq;
   p.num_seqs = num_seqs;
@@ -1014,6 +1042,7 @@ int pa_decode_accumulate(const void* q, const void* k_cache, const void* v_cache
   ap.q_heads = q_heads;
   ap.kv_heads = kv_heads;
   ap.group = p.group;
+  ap.group_pad = s.group_pad;
   ap.max_splits = s.max_splits;
   ap.split_tokens = s.split;
   ap.cap = s.cap;

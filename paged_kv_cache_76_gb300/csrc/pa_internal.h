@@ -90,10 +90,11 @@ struct DecodeParams {
   const int32_t* slot_tokens;
   int num_slots, contig_len;
   // launch_decode_logits: every column's scaled score (log2 units) of every
-  // token of the partition, [num_seqs][kv_heads][cap][group], and the sums of
-  // the unrounded probabilities, laid out as part_l
+  // token of the partition, [num_seqs][kv_heads][cap][group_pad], and the sums
+  // of the unrounded probabilities, laid out as part_l
   float* logits;
   float* part_w;
+  int group_pad;
 };
 
 struct MergeParams {
@@ -273,7 +274,7 @@ cudaError_t launch_compact_kv(const CompactParams& p, int num_seqs, cudaStream_t
 // pa_decode_accumulate: what the partition pass leaves of the logits, and the
 // pass that turns them into weights (after the merge's inputs are complete).
 struct AccumulateParams {
-  const float* logits;  // [num_seqs][kv_heads][cap][group], log2 units
+  const float* logits;  // [num_seqs][kv_heads][cap][group_pad], log2 units
   const float* part_m;  // as MergeParams
   const float* part_w;  // sums of the unrounded probabilities
   const int32_t* lens;
@@ -281,7 +282,7 @@ struct AccumulateParams {
   float* scores_out;
   const int32_t* score_rows;
   int* err;
-  int num_seqs, q_heads, kv_heads, group, max_splits, split_tokens, cap, num_rows, score_len;
+  int num_seqs, q_heads, kv_heads, group, group_pad, max_splits, split_tokens, cap, num_rows, score_len;
   int chunk, chunks;  // set by the launcher: tokens of a CTA, CTAs of a (request, KV head)
 };
 cudaError_t launch_merge_accumulate(const MergeParams& mp, const AccumulateParams& ap, int head_dim, pa_dtype dt,

@@ -38,6 +38,7 @@ __all__ = [
     "verify_tree_split_tokens",
     "verify_tree_workspace_size",
     "decode_accumulate",
+    "decode_accumulate_split_tokens",
     "decode_accumulate_workspace_size",
     "evict_select",
     "compact_kv",
@@ -569,6 +570,13 @@ def verify_tree(q, q_start, tree_mask, context_lens, k_cache, v_cache, block_tab
         _i32(block_tables, "block_tables"), maxblk, R, T, int(max_q_len), hq, hkv, d, bs, nb, float(scale),
         int(split_tokens), ws_ptr, ws_bytes, _dev(out, "out"), dtype_code(q.dtype), _stream(stream))
     return out
+
+
+def decode_accumulate_split_tokens(num_seqs, q_heads, kv_heads, max_blocks_per_seq, block_size, split_tokens=0) -> int:
+    """Partition size such a pa_decode_accumulate call uses (0: its automatic choice)."""
+    return check(_lib.lib().pa_decode_accumulate_split_tokens(int(num_seqs), int(q_heads), int(kv_heads),
+                                                              int(max_blocks_per_seq), int(block_size),
+                                                              int(split_tokens)), "pa_decode_accumulate_split_tokens")
 
 
 def decode_accumulate_workspace_size(num_seqs, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size,

@@ -74,7 +74,8 @@ def test_accumulate_matches_float64_and_decode(case):
     before, scale = scores.clone(), 1 / np.sqrt(d)
     out, into = ops().decode_accumulate(q, kc, vc, tables, lens_t, scale, scores, score_rows=rows, split_tokens=split)
     assert into is scores and ops().get_device_error() == 0
-    assert torch.equal(out, ops().decode(q, kc, vc, tables, lens_t, scale, split_tokens=split))
+    same = ops().decode_accumulate_split_tokens(len(lens), hq, hkv, tables.shape[1], bs, split)
+    assert torch.equal(out, ops().decode(q, kc, vc, tables, lens_t, scale, split_tokens=same))
     apart = torch.full_like(scores, 9.0)
     ops().decode_accumulate(q, kc, vc, tables, lens_t, scale, before, score_rows=rows, scores_out=apart,
                             split_tokens=split)
@@ -101,7 +102,8 @@ def test_accumulate_rows_that_are_refused_or_absent():
     lens = [100, 90, 80, 70]
     kc, vc, tables, lens_t, rng, g = cache(2, lens, 2, 128, 16, "bf16")
     q = torch.randn(4, 8, 128, generator=g, device="cuda").to(torch.bfloat16)
-    plain = ops().decode(q, kc, vc, tables, lens_t, 0.1)
+    plain = ops().decode(q, kc, vc, tables, lens_t, 0.1,
+                         split_tokens=ops().decode_accumulate_split_tokens(4, 8, 2, tables.shape[1], 16))
 
     def run(rows, width=128, n=4):
         s = torch.zeros(n, 2, width, device="cuda")
