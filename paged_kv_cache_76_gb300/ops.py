@@ -7,6 +7,7 @@ documented shapes; int32 index tensors live on the same device.
 """
 from __future__ import annotations
 
+import ctypes as C
 import math
 import threading
 
@@ -118,9 +119,17 @@ def _launch(name: str, *args) -> None:
     check(fn(*args), name)
 
 
+# the current stream's handle, without the Stream object that
+# torch.cuda.current_stream() builds around it (3 us of a call's 15)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream=None):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(torch.cuda.current_device())
+    return torch.cuda.current_stream().cuda_stream
 
 
 def _dev(t: torch.Tensor, name: str):
@@ -445,21 +454,26 @@ def rope_table(max_position: int, rot_dim: int, base: float = 10000.0, device=No
     return torch.cat([angle.cos(), angle.sin()], 1).to(torch.float32)
 
 
-def _token_rows(t: torch.Tensor, name: str, cache: torch.Tensor):
-    """Pointer and token stride (elements) of [num_tokens, heads, head_dim] whose heads are contiguous."""
-    if t.dim() != 3 or t.shape[2] != cache.shape[3]:
-        raise ValueError(f"{name} is [num_tokens, heads, head_dim] of the cache's head_dim")
-    if t.dtype != cache.dtype:
-        raise TypeError(f"{name} ({t.dtype}) must have the cache's dtype ({cache.dtype})")
-    if t.device != cache.device:
-        raise ValueError(f"{name} is on {t.device}, not {cache.device}")
-    row = t.shape[1] * t.shape[2]
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    stride = t.stride(0) if t.shape[0] > 1 else row
+def _token_rows(t: torch.Tensor, name: str, heads: int, d: int, dtype, device) -> int:
+    """Token stride (elements) of [num_tokens, heads, head_dim] whose heads are contiguous."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} ({t.dtype}) must have the cache's dtype ({dtype})")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, not {device}")
+    row = heads * d
+    if t.is_contiguous():
+        stride = row
+    else:
+        s0, s1, s2 = t.stride()
+        if s2 != 1 or (heads > 1 and s1 != d):
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        stride = s0 if t.shape[0] > 1 else row
     if stride < row or stride % 8:
         raise ValueError(f"{name}: tokens must be at least a row, and a multiple of 8 elements, apart")
     return stride
+
+
+_Sections = C.c_int32 * 3
 
 
 def norm_rope_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight=None, k_weight=None,
@@ -471,40 +485,47 @@ def norm_rope_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
     [axes, num_tokens] with ``sections`` (pairs per axis).  ``out`` may be ``q`` if that is contiguous."""
     nb, bs, hkv, d = _cache_dims(k_cache)
     _check_caches(k_cache, v_cache)
-    strides = [_token_rows(t, n, k_cache) for t, n in ((q, "q"), (k, "k"), (v, "v"))]
-    T, hq = int(q.shape[0]), int(q.shape[1])
+    dtype, device = k_cache.dtype, k_cache.device
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q is [num_tokens, q_heads, head_dim] of the cache's head_dim")
+    T, hq, _ = q.shape
     if k.shape != (T, hkv, d) or v.shape != (T, hkv, d):
         raise ValueError("k and v are [num_tokens, kv_heads, head_dim] of the cache, as many tokens as q")
-    axes = 1 if positions.dim() == 1 else int(positions.shape[0]) if positions.dim() == 2 else 0
-    if not 1 <= axes <= 3 or positions.shape[-1] != T or positions.device != q.device:
+    qs = _token_rows(q, "q", hq, d, dtype, device)
+    ks = _token_rows(k, "k", hkv, d, dtype, device)
+    vs = _token_rows(v, "v", hkv, d, dtype, device)
+    pshape = positions.shape
+    axes = 1 if len(pshape) == 1 else pshape[0] if len(pshape) == 2 else 0
+    if not 1 <= axes <= 3 or pshape[-1] != T or positions.device != device:
         raise ValueError("positions is [num_tokens] or [1 to 3 axes, num_tokens] on q's device")
-    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or cos_sin.device != q.device:
+    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or cos_sin.device != device:
         raise ValueError("cos_sin is fp32 [max_position, rot_dim] on q's device")
-    rot = int(cos_sin.shape[1])
+    max_pos, rot = cos_sin.shape
+    sec = None
     if sections is None:
         if axes > 1:
             raise ValueError("several axes need their sections")
     elif len(sections) != axes or min(sections) < 0 or sum(sections) != rot // 2:
         raise ValueError(f"sections are {axes} counts of pairs, rot_dim / 2 = {rot // 2} together")
+    else:
+        sec = _Sections(*sections)
     for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.shape != (d,) or w.dtype != q.dtype or w.device != q.device):
+        if w is not None and (w.shape != (d,) or w.dtype != dtype or w.device != device):
             raise ValueError(f"{n} is [head_dim] of q's dtype and device")
-    _check_index(q, "slot_mapping", slot_mapping, T)
+    _check_index(k_cache, "slot_mapping", slot_mapping, T)
     if out is None:
-        out = torch.empty((T, hq, d), dtype=q.dtype, device=q.device)
-    elif out.shape != (T, hq, d) or out.dtype != q.dtype or out.device != q.device:
+        out = torch.empty((T, hq, d), dtype=dtype, device=device)
+    elif out.shape != (T, hq, d) or out.dtype != dtype or out.device != device:
         raise ValueError("out must have q's shape, dtype and device")
     _check_current(q)
-    import ctypes as C
-    sec = (C.c_int32 * axes)(*[int(x) for x in sections]) if sections is not None else None
     _keep(out)
     _launch(
-        "pa_norm_rope_and_cache", _dev_rows(q, "q"), _dev_rows(k, "k"), _dev_rows(v, "v"), *strides,
+        "pa_norm_rope_and_cache", _dev_rows(q, "q"), _dev_rows(k, "k"), _dev_rows(v, "v"), qs, ks, vs,
         _dev(q_weight, "q_weight") if q_weight is not None else None,
-        _dev(k_weight, "k_weight") if k_weight is not None else None, float(eps), _i32(positions, "positions"), axes,
-        sec, _dev(cos_sin, "cos_sin"), int(cos_sin.shape[0]), rot, int(bool(interleaved)),
-        _i32(slot_mapping, "slot_mapping"), T, hq, _dev(out, "out"), _dev(k_cache, "k_cache"),
-        _dev(v_cache, "v_cache"), nb, bs, hkv, d, dtype_code(q.dtype), _stream(stream))
+        _dev(k_weight, "k_weight") if k_weight is not None else None, eps, _i32(positions, "positions"), axes, sec,
+        _dev(cos_sin, "cos_sin"), max_pos, rot, 1 if interleaved else 0, _i32(slot_mapping, "slot_mapping"), T, hq,
+        _dev(out, "out"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), nb, bs, hkv, d, dtype_code(dtype),
+        _stream(stream))
     return out
 
 
@@ -694,7 +715,6 @@ def selftest_wait_timeout(wait_ms: int = 50, stream=None) -> None:
 
 def get_device_error(stream=None) -> int:
     """Read and clear the device error word (synchronises the stream)."""
-    import ctypes as C
     code = C.c_int32(0)
     st = _lib.lib().pa_get_device_error(C.byref(code), _stream(stream))
     if st not in (_lib.PA_OK, _lib.PA_ERR_DEVICE_CHECK):
