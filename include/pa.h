@@ -727,6 +727,18 @@ int pa_alloc_cow(pa_alloc* a, int seq_id, int logical_block, int32_t* src_dst_ou
 
 int pa_alloc_free_seq(pa_alloc* a, int seq_id);
 
+/* seq_id shrinks to its first n_tokens tokens, of which those from first_token
+ * on are rewritten by a pa_compact_kv on the stream (first_token == n_tokens:
+ * none, a plain truncation, as after rejected drafts).  Blocks behind the last
+ * token are released as pa_alloc_free_seq does, so build the tables that
+ * pa_compact_kv reads before this call and launch it before anything writes
+ * the released blocks.  Blocks with rewritten tokens must be private
+ * (PA_ERR_SHARED_BLOCK: pa_alloc_cow first) and leave the prefix cache, as does
+ * a private block whose tail is cut off; the sequence registers nothing more
+ * where its tokens are no longer known.  PA_ERR_INVALID unless
+ * 0 <= first_token <= n_tokens <= its length, or while it is swapped out. */
+int pa_alloc_compact(pa_alloc* a, int seq_id, int64_t first_token, int64_t n_tokens);
+
 /* Copy seq_id's Block Table into out[0..cap); *n_out = its length.
  * PA_ERR_INVALID if cap is too small (nothing written). */
 int pa_alloc_block_table(const pa_alloc* a, int seq_id, int32_t* out, int cap, int* n_out);

@@ -78,6 +78,11 @@ of CPU blocks is set up:
   queue in reverse order.  Both return the (source, destination) pairs the
   caller copies with swap_blocks before reusing the source blocks.
 * free_seq on a swapped-out request returns its CPU blocks.
+
+Compaction (the pages have no counterpart): a request keeps its first n
+tokens, those from a given one on rewritten in place.  Blocks with rewritten
+tokens have to be private and leave the cache; so does a private last block
+that is cut; the blocks behind are freed as at a request's end.
 """
 from __future__ import annotations
 
@@ -461,6 +466,38 @@ class SequenceManager:
         table[logical_block] = nb
         self.cow_copies += 1
         return (b, nb)
+
+    def compact(self, seq, first_token, n_tokens):
+        self._resident(seq)
+        L, bs = self.num_tokens[seq], self.block_size
+        if not 0 <= first_token <= n_tokens <= L:
+            raise AllocError("0 <= first_token <= n_tokens <= length")
+        table = self.tables[seq]
+        kept = -(-n_tokens // bs)
+        touched = table[first_token // bs:kept] if first_token < n_tokens else []
+        if any(self.pool.ref_cnt[b] > 1 for b in touched):
+            raise AllocError("rewritten blocks must be private")
+        gone = set(touched)
+        if n_tokens % bs and n_tokens < L and self.pool.ref_cnt[table[kept - 1]] == 1:
+            gone.add(table[kept - 1])
+        for b in gone:
+            h, self.pool.block_hash[b] = self.pool.block_hash[b], None
+            if h is not None and self.pool.cached_block_hash_to_block.get(h) == b:
+                del self.pool.cached_block_hash_to_block[h]
+        if first_token < n_tokens:
+            self.pending[seq] = None
+        elif n_tokens == 0:
+            self.parent[seq], self.pending[seq] = self.salt[seq], []
+        elif n_tokens // bs == L // bs:
+            if self.pending[seq] is not None:
+                self.pending[seq] = self.pending[seq][:n_tokens % bs]
+        elif n_tokens % bs == 0 and self.pool.block_hash[table[kept - 1]] is not None:
+            self.parent[seq], self.pending[seq] = self.pool.block_hash[table[kept - 1]], []
+        else:
+            self.pending[seq] = None
+        self.pool.free_blocks(list(reversed(table[kept:])))
+        self.tables[seq] = table[:kept]
+        self.num_tokens[seq] = n_tokens
 
     def free_seq(self, seq):
         """Release ``seq``: its blocks in reverse order, tail block first."""

@@ -119,6 +119,7 @@ PROTOTYPES = {
     "pa_alloc_share": (_I, [_P, _I, _I, _I]),
     "pa_alloc_cow": (_I, [_P, _I, _I, _I32P]),
     "pa_alloc_free_seq": (_I, [_P, _I]),
+    "pa_alloc_compact": (_I, [_P, _I, C.c_int64, C.c_int64]),
     "pa_alloc_block_table": (_I, [_P, _I, _I32P, _I, C.POINTER(_I)]),
     "pa_alloc_build_tables": (_I, [_P, C.POINTER(_I), _I, _I32P, _I, _I32P]),
     "pa_alloc_common_prefix": (_I, [_P, C.POINTER(_I), _I, C.POINTER(_I)]),

@@ -97,6 +97,11 @@ class BlockAllocator:
     def free_seq(self, seq: int):
         _chk(self._L.pa_alloc_free_seq(self._h, int(seq)), "pa_alloc_free_seq")
 
+    def compact(self, seq: int, first_token: int, n_tokens: int):
+        """``seq`` keeps ``n_tokens`` tokens, those from ``first_token`` on rewritten by ``ops.compact_kv`` (build the
+        tables it reads before this call); blocks behind are released."""
+        _chk(self._L.pa_alloc_compact(self._h, int(seq), int(first_token), int(n_tokens)), "pa_alloc_compact")
+
     def block_table(self, seq: int) -> list:
         n = C.c_int(0)
         self._L.pa_alloc_block_table(self._h, int(seq), None, 0, C.byref(n))

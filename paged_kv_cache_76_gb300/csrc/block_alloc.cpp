@@ -154,14 +154,17 @@ struct pa_alloc {
   // cached block leaves the cache here
   int32_t take() {
     const int32_t b = pop_front();
-    if (has_hash[b]) {
-      auto it = cached.find(hash[b]);
-      if (it != cached.end() && it->second == b) cached.erase(it);
-      has_hash[b] = 0;
-      ++evictions;
-    }
+    if (forget(b)) ++evictions;
     ref[b] = 1;
     return b;
+  }
+  // the block leaves the prefix cache; false: it was not in it
+  bool forget(int32_t b) {
+    if (!has_hash[b]) return false;
+    auto it = cached.find(hash[b]);
+    if (it != cached.end() && it->second == b) cached.erase(it);
+    has_hash[b] = 0;
+    return true;
   }
   // touch: one more reference; a free block leaves the queue
   void touch(int32_t b) {
@@ -328,6 +331,56 @@ int pa_alloc_free_seq(pa_alloc* a, int seq_id) {
     for (auto rit = no_hash.rbegin(); rit != no_hash.rend(); ++rit) a->push_front(*rit);
     for (int32_t b : with_hash) a->push_back(b);
     a->seqs.erase(it);
+    return PA_OK;
+  });
+}
+
+int pa_alloc_compact(pa_alloc* a, int seq_id, int64_t first_token, int64_t n_tokens) {
+  return pa_guarded([&]() -> int {
+    if (!a) return PA_ERR_INVALID;
+    Seq* s = a->find(seq_id);
+    if (!s || s->swapped || first_token < 0 || first_token > n_tokens || n_tokens > s->num_tokens)
+      return PA_ERR_INVALID;
+    const int64_t bs = a->block_size;
+    const int64_t kept = cdiv64(n_tokens, bs);
+    const int64_t rewritten = first_token < n_tokens ? first_token / bs : kept;  // blocks [rewritten, kept)
+    for (int64_t i = rewritten; i < kept; ++i)
+      if (a->ref[s->blocks[i]] > 1) return PA_ERR_SHARED_BLOCK;
+    std::vector<int32_t> no_hash, with_hash;
+    no_hash.reserve(s->blocks.size() - kept);
+    with_hash.reserve(s->blocks.size() - kept);
+    // contents change, or will with the next append: out of the prefix cache
+    for (int64_t i = rewritten; i < kept; ++i) a->forget(s->blocks[i]);
+    const bool cut = n_tokens % bs != 0 && n_tokens < s->num_tokens;
+    if (cut && a->ref[s->blocks[kept - 1]] == 1) a->forget(s->blocks[kept - 1]);
+    // where the hash chain goes on from
+    if (first_token < n_tokens) {
+      s->hashable = false;
+      s->pending.clear();
+    } else if (n_tokens == 0) {
+      s->parent = s->salt;
+      s->hashable = true;
+      s->pending.clear();
+    } else if (n_tokens / bs == s->num_tokens / bs) {  // inside the same partial block
+      if (s->hashable) s->pending.resize(n_tokens % bs);
+    } else if (n_tokens % bs == 0 && a->has_hash[s->blocks[kept - 1]]) {
+      s->parent = a->hash[s->blocks[kept - 1]];
+      s->hashable = true;
+      s->pending.clear();
+    } else {
+      s->hashable = false;
+      s->pending.clear();
+    }
+    // the blocks behind, released as pa_alloc_free_seq releases them
+    for (int64_t i = (int64_t)s->blocks.size() - 1; i >= kept; --i) {
+      const int32_t b = s->blocks[i];
+      a->ref[b] -= 1;
+      if (a->ref[b] == 0) (a->has_hash[b] ? with_hash : no_hash).push_back(b);
+    }
+    for (auto rit = no_hash.rbegin(); rit != no_hash.rend(); ++rit) a->push_front(*rit);
+    for (int32_t b : with_hash) a->push_back(b);
+    s->blocks.resize(kept);
+    s->num_tokens = n_tokens;
     return PA_OK;
   });
 }
