@@ -59,6 +59,7 @@
 // non-finite elements (tree.cuh).  A context may be cut into partitions of
 // split_tokens keys, a unit each, whose partials a merge combines.  A unit of
 // at most 128 rows leaves tile B alone: its issuer only frees the stages.
+// Blocks of 4 tokens (GATHER) are gathered without TMA (tree.cuh).
 #include <float.h>
 
 #include "pa_device.cuh"
@@ -197,7 +198,7 @@ __device__ __forceinline__ int tree_unit(const PrefillParams& p, const TreeParam
   return 0;
 }
 
-template <int D, int BSUB, typename T, bool TREE>
+template <int D, int BSUB, typename T, bool TREE, bool GATHER>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                     const PrefillParams p, const TreeParams tp) {
@@ -247,11 +248,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKStages; ++i) {
-      mbar_init(bar(B_KFULL + i), 1);
+      mbar_init(bar(B_KFULL + i), GATHER ? 32 : 1);
       mbar_init(bar(B_KEMPTY + i), 2);
     }
     for (int i = 0; i < kVStages; ++i) {
-      mbar_init(bar(B_VFULL + i), 1);
+      mbar_init(bar(B_VFULL + i), GATHER ? 32 : 1);
       mbar_init(bar(B_VEMPTY + i), 2);
     }
     for (int i = 0; i < 4; ++i) {
@@ -302,6 +303,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int ts = w.k0 + j * kKeys;
         const int nvalid = min(kKeys, w.kend - ts);
+        if constexpr (GATHER) {
+          gather4_tile<Tile, D, kKeys>(tp, isv ? tp.v_cache : tp.k_cache, trow, w.h, ts, nvalid,
+                                       base + s * Tile::BYTES, bar(full0 + s));
+          continue;
+        }
         const int nsub = (nvalid + BSUB - 1) / BSUB;
         if (lane == 0) mbar_arrive_expect_tx(bar(full0 + s), nsub * NH * Tile::BOX_BYTES);
         __syncwarp();
@@ -346,6 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   mbar_wait(bar(B_VFULL + vst), (t / kVStages) & 1)))
           return false;
         tc_fence_after();
+        if constexpr (GATHER) fence_proxy_async_smem();  // the copies' writes before the MMAs' reads
         const uint32_t vb = vbase + vst * Tile::BYTES;
 #pragma unroll
         for (int kk = 0; kk < PSTEPS; ++kk) {
@@ -397,6 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
+          if constexpr (GATHER) fence_proxy_async_smem();
           const uint32_t kb = kbase + sk * Tile::BYTES;
 #pragma unroll
           for (int ks = 0; ks < KSTEPS; ++ks) {
@@ -684,7 +692,7 @@ template <int D, int BSUB, typename T>
 cudaError_t launch_tc_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const PrefillParams& p,
                          cudaStream_t stream) {
   using L = TcSmem<D, BSUB>;
-  auto kern = attn_tc_kernel<D, BSUB, T, false>;
+  auto kern = attn_tc_kernel<D, BSUB, T, false, false>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -704,11 +712,11 @@ cudaError_t launch_tc_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const 
   return launch_pdl(kern, grid, dim3(kThreads), L::BYTES, stream, kmap, vmap, p, TreeParams{});
 }
 
-template <int D, int BSUB, typename T>
+template <int D, int BSUB, typename T, bool GATHER = false>
 cudaError_t launch_tree_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const PrefillParams& p,
                           const TreeParams& tp, cudaStream_t stream) {
   using L = TcSmem<D, BSUB>;
-  auto kern = attn_tc_kernel<D, BSUB, T, true>;
+  auto kern = attn_tc_kernel<D, BSUB, T, true, GATHER>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -727,6 +735,7 @@ template <int D, typename T>
 cudaError_t launch_tree_bs(const CUtensorMap& kmap, const CUtensorMap& vmap, const PrefillParams& p,
                            const TreeParams& tp, int bsub, cudaStream_t stream) {
   switch (bsub) {
+    case 4: return launch_tree_t<D, 16, T, true>(kmap, vmap, p, tp, stream);
     case 8: return launch_tree_t<D, 8, T>(kmap, vmap, p, tp, stream);
     case 16: return launch_tree_t<D, 16, T>(kmap, vmap, p, tp, stream);
     default: return cudaErrorInvalidValue;

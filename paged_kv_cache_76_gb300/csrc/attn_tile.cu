@@ -64,6 +64,7 @@
 // that zero V rows past the keys also clean the drafted V rows of non-finite
 // elements (tree.cuh).  A context may be cut into partitions of split_tokens
 // keys, a unit each, whose partials a merge combines.  One unit per CTA.
+// Blocks of 4 tokens (GATHER) are gathered without TMA (tree.cuh).
 #include <float.h>
 
 #include "pa_device.cuh"
@@ -187,7 +188,7 @@ __device__ __forceinline__ int tree_unit(const PrefillParams& p, const TreeParam
   return 0;
 }
 
-template <int D, int BSUB, typename T, bool SPREAD, bool TREE>
+template <int D, int BSUB, typename T, bool SPREAD, bool TREE, bool GATHER>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tile_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                    const PrefillParams p, const TreeParams tp) {
@@ -260,11 +261,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKStages; ++i) {
-      mbar_init(bar(B_KFULL + i), 1);
+      mbar_init(bar(B_KFULL + i), GATHER ? 32 : 1);
       mbar_init(bar(B_KEMPTY + i), 1);
     }
     for (int i = 0; i < kVStages; ++i) {
-      mbar_init(bar(B_VFULL + i), 1);
+      mbar_init(bar(B_VFULL + i), GATHER ? 32 : 1);
       mbar_init(bar(B_VEMPTY + i), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -315,6 +316,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int ts = w.k0 + j * kKeys;
         const int nvalid = min(kKeys, w.kend - ts);
+        if constexpr (GATHER) {
+          gather4_tile<Tile, D, kKeys>(tp, isv ? tp.v_cache : tp.k_cache, trow, w.h, ts, nvalid,
+                                       base + s * Tile::BYTES, bar(full0 + s));
+          continue;
+        }
         const int nsub = (nvalid + BSUB - 1) / BSUB;
         if (lane == 0) mbar_arrive_expect_tx(bar(full0 + s), nsub * NH * Tile::BOX_BYTES);
         __syncwarp();
@@ -356,6 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
+          if constexpr (GATHER) fence_proxy_async_smem();  // the copies' writes before the MMAs' reads
           const uint32_t kb = kbase + sk * Tile::BYTES;
 #pragma unroll
           for (int ks = 0; ks < KSTEPS; ++ks) {
@@ -392,6 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               break;
             }
             tc_fence_after();
+            if constexpr (GATHER) fence_proxy_async_smem();
 #pragma unroll
             for (int k4 = 0; k4 < 4; ++k4) {
               // A = P[128 rows x keys 16kk..16kk+15] in TMEM (8 columns); B = V rows 16kk.., MN-major.
@@ -876,7 +884,7 @@ template <int D, int BSUB, typename T, bool SPREAD>
 cudaError_t launch_tc_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const PrefillParams& p,
                          cudaStream_t stream) {
   using L = TcSmem<D, BSUB, SPREAD, false>;
-  auto kern = attn_tile_kernel<D, BSUB, T, SPREAD, false>;
+  auto kern = attn_tile_kernel<D, BSUB, T, SPREAD, false, false>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -899,10 +907,10 @@ cudaError_t launch_tc_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const 
   return launch_pdl(kern, grid, dim3(kThreads), L::BYTES, stream, kmap, vmap, p, TreeParams{});
 }
 
-template <int D, int BSUB, typename T, bool SPREAD>
+template <int D, int BSUB, typename T, bool SPREAD, bool GATHER = false>
 cudaError_t launch_tree_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& tp, cudaStream_t stream) {
   using L = TcSmem<D, BSUB, SPREAD, true>;
-  auto kern = attn_tile_kernel<D, BSUB, T, SPREAD, true>;
+  auto kern = attn_tile_kernel<D, BSUB, T, SPREAD, true, GATHER>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);
@@ -923,6 +931,8 @@ cudaError_t launch_tree_bs(const CUtensorMap& kmap, const CUtensorMap& vmap, con
                            cudaStream_t stream) {
   const bool spread = p.max_q_len * p.group <= 32;
   switch (bsub) {
+    case 4: return spread ? launch_tree_t<D, 16, T, true, true>(kmap, vmap, p, stream)
+                          : launch_tree_t<D, 16, T, false, true>(kmap, vmap, p, stream);
     case 8: return spread ? launch_tree_t<D, 8, T, true>(kmap, vmap, p, stream)
                           : launch_tree_t<D, 8, T, false>(kmap, vmap, p, stream);
     case 16: return spread ? launch_tree_t<D, 16, T, true>(kmap, vmap, p, stream)

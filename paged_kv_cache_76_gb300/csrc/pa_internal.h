@@ -219,7 +219,8 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, int head_dim, pa_dtype dt,
 // Attention of drafted trees (pa_verify_tree).
 struct TreeParams {
   const void* q;
-  const void* v_cache;  // for the rare nodes whose V is not finite
+  const void* k_cache;  // blocks of 4 tokens are gathered without tensor maps
+  const void* v_cache;  // ... and the rare nodes whose V is not finite
   const int32_t* q_start;
   const uint64_t* mask;  // [total_q]
   const int32_t* lens;
@@ -233,8 +234,8 @@ struct TreeParams {
   float* part_m;
   float* part_l;
 };
-// blocks of >= 8 tokens, no merge: the tcgen05 kernels of attn_tile.cu (128
-// rows per CTA) and attn_tc.cu (256)
+// without the merge: the tcgen05 kernels of attn_tile.cu (128 rows per CTA) and
+// attn_tc.cu (256)
 cudaError_t launch_tree_pair(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int head_dim,
                              int bsub, pa_dtype dt, cudaStream_t stream);
 cudaError_t launch_tree_tile(const CUtensorMap& kmap, const CUtensorMap& vmap, const TreeParams& p, int head_dim,

@@ -50,6 +50,40 @@ __device__ __forceinline__ int tree_request(const TreeParams& p, int r, TreeReq&
   return 0;
 }
 
+// Blocks of 4 tokens: a TMA box of 4 rows is half of the 8-row atom that the
+// tensor cores' 128-byte-swizzled layout is made of, so a producer warp gathers
+// the tile's rows with 16-byte asynchronous copies into the layout of 16-token
+// boxes instead, and signals the stage with one arrival per lane.  (The warp
+// takes about ten instructions per two rows of 128 elements, well inside the
+// time a tile takes.)  Rows past nvalid become zero.  Block ids of the tile are
+// one per lane (ROWS <= 128).
+template <typename Tile, int D, int ROWS>
+__device__ __forceinline__ void gather4_tile(const TreeParams& p, const void* cache, const int32_t* trow, int h, int ts,
+                                             int nvalid, uint32_t dst, uint32_t bar) {
+  constexpr int CH = D / 8;        // 16-byte chunks of a row
+  constexpr int RPI = 32 / CH;     // rows per step
+  const int lane = threadIdx.x & 31;
+  int id = 0;
+  if (4 * lane < nvalid) {
+    id = __ldg(trow + ts / 4 + lane);
+    if (id < 0 || id >= p.num_blocks) {
+      record_error(p.err, PA_DEVERR_BLOCK_ID);
+      id = -1;  // its rows become zero
+    }
+  }
+  const int c = lane % CH;
+  const char* base = static_cast<const char*>(cache) + ((size_t)h * D + 8 * c) * 2;
+  const size_t token = (size_t)p.kv_heads * D * 2;
+#pragma unroll 8
+  for (int r0 = 0; r0 < ROWS; r0 += RPI) {
+    const int row = r0 + lane / CH;
+    const int b = __shfl_sync(0xffffffffu, id, row >> 2);
+    const bool in = row < nvalid && b >= 0;
+    cp_async16(dst + Tile::offset(row, c), base + (in ? ((size_t)b * 4 + (row & 3)) * token : 0), in ? 16u : 0u);
+  }
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];\n" ::"r"(bar) : "memory");
+}
+
 // Which of the 64 keys from `rel` past the draft's start on (before it:
 // negative) a row with this mask sees.
 __device__ __forceinline__ uint64_t tree_window(uint64_t mask, int rel) {
