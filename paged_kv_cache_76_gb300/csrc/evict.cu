@@ -340,23 +340,22 @@ cudaError_t launch_select_t(EvictSelectParams& p, int cluster, int num_seqs, cud
 
 // ----------------------------------------------------------------------------
 // In-place compaction: destination i, source keep[i] >= i.  A cluster of CTAs
-// takes one 64-byte column of one head's K or V rows (or the head's scores)
-// and walks the entries in order, kMoveChunk per CTA and step: all loads of a
-// step, a barrier, its stores.  A store to place i can only overwrite a source
-// read by an entry <= i (sources are never before their destinations), which
-// is in this step or an earlier one, so no entry reads what another has
-// written; for the same reason the next step's loads may be under way.
+// takes one column (64 or 128 bytes) of one head's K or V rows and walks the
+// entries in order, a step at a time: all loads of a step, a barrier, its
+// stores.  A store to place i can only overwrite a source read by an entry
+// <= i (sources are never before their destinations), which is in this step or
+// an earlier one, so no entry reads what another has written; for the same
+// reason the next steps' loads may be under way.
 //
-// Bound by HBM (2 * 64 bytes per entry and column), and before that by the
-// chain of loads to an address: the entry, its block id, its row.  So the walk
-// is a pipeline: while step c is stored, the rows of c+1 and c+2 are on their
-// way into shared memory (cp.async: no registers, four CTAs on an SM), and the
-// block ids of c+3 and the entries of c+4 into registers.
-constexpr int kMoveThreads = 256;
-constexpr int kMoveLanes = 4;                          // 16-byte vectors of a column
-constexpr int kMoveRows = kMoveThreads / kMoveLanes;   // rows side by side
+// Bound by HBM (twice the column per entry), and before that by the chain of
+// loads to an address: the entry, its block id, its row.  So the walk is a
+// pipeline: while step c is stored, the rows of c+1 and c+2 are on their way
+// into shared memory (cp.async: no registers), and the block ids of c+3 and the
+// entries of c+4 into registers; every load is made a step before its value is
+// used.  Measured on GB300, 8 heads of 128: 8 lists of 8192 per head (537 MB)
+// 93 us, 0.85 of the copy rate; one 18 us.
+constexpr int kMoveThreads = 256;                      // of the one-step kernel
 constexpr int kMoveUnroll = 4;
-constexpr int kMoveChunk = kMoveRows * kMoveUnroll;    // entries of a CTA and step
 constexpr int kMoveStages = 3;
 constexpr int kMoveSmall = 64;                         // longest list of the one-step kernel
 
@@ -380,8 +379,13 @@ __device__ __forceinline__ bool move_range(const CompactParams& p, int r, MoveRa
   return true;
 }
 
-__global__ void __launch_bounds__(kMoveThreads, 4) compact_kv_kernel(const CompactParams p) {
-  __shared__ uint4 ring[kMoveStages][kMoveUnroll][kMoveThreads];
+template <int LANES, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) compact_kv_kernel(const CompactParams p) {
+  constexpr int kMoveThreads = THREADS, kMoveLanes = LANES;
+  constexpr int kMoveRows = kMoveThreads / kMoveLanes;   // rows side by side
+  constexpr int kMoveChunk = kMoveRows * kMoveUnroll;    // entries of a CTA and step
+  extern __shared__ uint4 smem_raw[];
+  uint4 (*ring)[kMoveUnroll][kMoveThreads] = reinterpret_cast<uint4 (*)[kMoveUnroll][kMoveThreads]>(smem_raw);
   griddep_wait();
   griddep_launch_dependents();
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
@@ -396,44 +400,6 @@ __global__ void __launch_bounds__(kMoveThreads, 4) compact_kv_kernel(const Compa
     if (C == 1) __syncthreads();
     else cluster_sync();
   };
-
-  if (part == 2 * p.columns) {  // the scores of this head
-    const int row = p.score_rows ? __ldg(p.score_rows + r) : r;
-    if (row < 0) return;
-    bool twice = false;
-    if (p.score_rows)
-      for (int i = tid; i < r; i += kMoveThreads) twice |= __ldg(p.score_rows + i) == row;
-    twice = __syncthreads_or(twice);
-    if (row >= p.num_rows || twice) {
-      if (tid == 0) record_error(p.err, PA_DEVERR_SCORE_ROW);
-      return;
-    }
-    if (m.L > p.score_len) {
-      if (tid == 0) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
-      return;
-    }
-    float* sc = p.scores + ((size_t)row * p.kv_heads + g) * p.score_len + m.base;
-    constexpr int U = 8;
-    const int step = C * U * kMoveThreads;
-    for (int64_t i0 = 0; i0 < m.n; i0 += step) {
-      float x[U];
-      bool ok[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int64_t i = i0 + (rank * U + u) * kMoveThreads + tid;
-        const int src = i < m.n ? __ldg(keep + i) : -1;
-        ok[u] = src >= i && src < room && i < m.n;
-        if (ok[u]) x[u] = sc[src];
-      }
-      meet();
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (ok[u]) sc[i0 + (rank * U + u) * kMoveThreads + tid] = x[u];
-    }
-    meet();  // every source has been read
-    for (int64_t i = (int64_t)m.n + rank * kMoveThreads + tid; i < room; i += C * kMoveThreads) sc[i] = 0.f;
-    return;
-  }
 
   const int is_v = part >= p.columns;
   const int col = (is_v ? part - p.columns : part) * kMoveLanes + tid % kMoveLanes;  // 16-byte vector of the head's row
@@ -526,6 +492,68 @@ __global__ void __launch_bounds__(kMoveThreads, 4) compact_kv_kernel(const Compa
   cp_async_wait_all();
 }
 
+// The scores of a (KV head, request), moved by the same rule, and zeros behind
+// them.  A launch of its own: inside the kernel above the columns that also
+// moved scores were the last to end (8 lists of 8192 per head over contexts of
+// 80000: 124 us; apart, 93 and 7).  A cluster shares a long row: one SM's stores
+// alone take 14 us for the zeros of a context of 131000.
+constexpr int kScoreThreads = 256;
+
+__global__ void __launch_bounds__(kScoreThreads) compact_scores_kernel(const CompactParams p) {
+  griddep_wait();
+  griddep_launch_dependents();
+  const int C = (int)cluster_size(), rank = (int)cluster_rank();
+  const int r = blockIdx.y, g = blockIdx.x / C, tid = threadIdx.x;
+  auto meet = [&] {
+    if (C == 1) __syncthreads();
+    else cluster_sync();
+  };
+  MoveRange m;
+  if (!move_range(p, r, m, false)) return;  // reported by the rows' kernel
+  const int row = p.score_rows ? __ldg(p.score_rows + r) : r;
+  if (row < 0) return;
+  bool twice = false;  // an earlier request has this row: its alone are moved
+  if (p.score_rows)
+    for (int i = tid; i < r; i += kScoreThreads) twice |= __ldg(p.score_rows + i) == row;
+  const bool bad = __syncthreads_or(twice) || row >= p.num_rows;
+  if (bad || m.L > p.score_len) {
+    if (tid == 0) record_error(p.err, bad ? PA_DEVERR_SCORE_ROW : PA_DEVERR_CONTEXT_LEN);
+    return;
+  }
+  const int32_t* keep = p.keep + ((size_t)r * p.keep_heads + (p.keep_heads == 1 ? 0 : g)) * p.max_keep;
+  const int room = m.L - m.base;
+  float* sc = p.scores + ((size_t)row * p.kv_heads + g) * p.score_len + m.base;
+  constexpr int U = 8;
+  for (int64_t c = 0; c < m.n; c += C * U * kScoreThreads) {
+    const int64_t i0 = c + rank * U * kScoreThreads + tid;
+    int src[U];
+    float x[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int64_t i = i0 + u * kScoreThreads;
+      src[u] = i < m.n ? __ldg(keep + i) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (src[u] < i0 + u * kScoreThreads || src[u] >= room) src[u] = -1;
+      if (src[u] >= 0) x[u] = sc[src[u]];
+    }
+    meet();  // all loads of the step before its stores
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (src[u] >= 0) sc[i0 + u * kScoreThreads] = x[u];
+  }
+  meet();  // every score has been read
+  // zeros on [n, room): single ones up to a 16-byte boundary, then vectors
+  const int t0 = rank * kScoreThreads + tid;
+  const int n4 = min(m.n + (int)((16 - (reinterpret_cast<uintptr_t>(sc + m.n) & 15)) / 4) % 4, room);
+  if (t0 < n4 - m.n) sc[m.n + t0] = 0.f;
+  const int vecs = (room - n4) / 4;
+  for (int64_t i = t0; i < vecs; i += C * kScoreThreads)
+    reinterpret_cast<float4*>(sc + n4)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (t0 < room - n4 - 4 * vecs) sc[n4 + 4 * vecs + t0] = 0.f;
+}
+
 // Lists of at most kMoveSmall entries (a tree's accepted path): a CTA takes a
 // head's K and V rows whole, all loads, a barrier, all stores.  Bound by the
 // launch and one chain of loads.
@@ -604,23 +632,56 @@ cudaError_t launch_evict_select(const EvictSelectParams& p0, int num_seqs, cudaS
                          : launch_select_t<1024>(p, cluster, num_seqs, stream);
 }
 
+template <int LANES, int THREADS>
+cudaError_t launch_move_t(CompactParams& p, int num_seqs, cudaStream_t stream) {
+  auto kern = compact_kv_kernel<LANES, THREADS>;
+  constexpr int SMEM = kMoveStages * kMoveUnroll * THREADS * 16;
+  constexpr int CHUNK = THREADS / LANES * kMoveUnroll;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && !attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, SMEM);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  p.columns = p.row_vecs / LANES;
+  // few sequences of long lists: clusters share a column, as long as that
+  // leaves no more than 1024 threads per SM and each CTA has a step to take
+  const int64_t threads = 2 * (int64_t)p.columns * p.kv_heads * num_seqs * THREADS;
+  const int64_t sms = num_sms() > 0 ? num_sms() : 152;
+  int cluster = 1;
+  while (cluster < 8 && threads * cluster * 2 <= 1024 * sms && (int64_t)cluster * CHUNK < p.max_keep) cluster *= 2;
+  return launch_pdl_cluster(kern, cluster, dim3((unsigned)(2 * p.columns * cluster), p.kv_heads, num_seqs),
+                            dim3(THREADS), SMEM, stream, p);
+}
+
 cudaError_t launch_compact_kv(const CompactParams& p0, int num_seqs, cudaStream_t stream) {
   if (num_seqs == 0) return cudaSuccess;
   CompactParams p = p0;
-  p.columns = p.row_vecs / kMoveLanes;
-  if (p.max_keep <= kMoveSmall && !p.scores)
-    return p.row_vecs == 16 ? launch_pdl(compact_small_kernel<16>, dim3(p.kv_heads, num_seqs), dim3(kMoveThreads), 0,
-                                         stream, p)
-                            : launch_pdl(compact_small_kernel<8>, dim3(p.kv_heads, num_seqs), dim3(kMoveThreads), 0,
-                                         stream, p);
-  const int parts = 2 * p.columns + (p.scores ? 1 : 0);
-  // few sequences of long lists: clusters share a column, as long as that
-  // leaves no more than four CTAs per SM and each has a step to take
-  const int64_t ctas = (int64_t)parts * p.kv_heads * num_seqs, sms = num_sms() > 0 ? num_sms() : 152;
+  cudaError_t e;
+  // 128-byte columns, whole lines, when they fill the GPU: 512 threads while
+  // every CTA fits at once (8 lists of 8192 per head: 93 us; 256 threads 112,
+  // 64-byte columns 102), 256 when they do not (64 lists of 1024: 86; 512
+  // threads 99, 64-byte columns 92).  Fewer: 64-byte columns, twice the CTAs
+  // (one list: 18; 128-byte columns 21 to 28).
+  const int64_t ctas = (int64_t)p.row_vecs / 4 * p.kv_heads * num_seqs, sms = num_sms() > 0 ? num_sms() : 152;
+  const dim3 lists(p.kv_heads, num_seqs);
+  if (p.max_keep <= kMoveSmall)
+    e = p.row_vecs == 16 ? launch_pdl(compact_small_kernel<16>, lists, dim3(kMoveThreads), 0, stream, p)
+                         : launch_pdl(compact_small_kernel<8>, lists, dim3(kMoveThreads), 0, stream, p);
+  else if (ctas <= sms)
+    e = launch_move_t<4, 256>(p, num_seqs, stream);
+  else if (ctas <= 2 * sms)
+    e = launch_move_t<8, 512>(p, num_seqs, stream);
+  else
+    e = launch_move_t<8, 256>(p, num_seqs, stream);
+  if (e != cudaSuccess || !p.scores) return e;
+  const int64_t rows = (int64_t)p.kv_heads * num_seqs;
   int cluster = 1;
-  while (cluster < 8 && ctas * cluster * 2 <= 4 * sms && (int64_t)cluster * kMoveChunk < p.max_keep) cluster *= 2;
-  return launch_pdl_cluster(compact_kv_kernel, cluster, dim3((unsigned)(parts * cluster), p.kv_heads, num_seqs),
-                            dim3(kMoveThreads), 0, stream, p);
+  while (cluster < 8 && rows * cluster * 2 <= 4 * sms && (int64_t)cluster * 8 * kScoreThreads < p.score_len) cluster *= 2;
+  return launch_pdl_cluster(compact_scores_kernel, cluster, dim3((unsigned)(p.kv_heads * cluster), num_seqs),
+                            dim3(kScoreThreads), 0, stream, p);
 }
 
 }  // namespace pa
