@@ -308,6 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     TcUnit w;
     for (int u = next_unit(cta0, w, false); u < nunits && !failed; u = next_unit(u + nctas, w, false)) {
       const int32_t* trow = p.tables + (size_t)w.r * p.maxblk;
+      int ids = 0;  // GATHER: block ids of the next tile
+      if constexpr (GATHER) ids = gather4_ids(trow, w.k0, w.kend - w.k0);
       for (int j = 0; j < w.ntiles; ++j, ++gt) {
         const int s = gt % nst;
         if (gt >= nst && !mbar_wait(bar(empty0 + s), ((gt / nst) - 1) & 1)) {
@@ -317,8 +319,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int ts = w.k0 + j * kKeys;
         const int nvalid = min(kKeys, w.kend - ts);
         if constexpr (GATHER) {
-          gather4_tile<Tile, D, kKeys>(tp, isv ? tp.v_cache : tp.k_cache, trow, w.h, ts, nvalid,
-                                       base + s * Tile::BYTES, bar(full0 + s));
+          gather4_tile<Tile, D, kKeys>(tp, isv ? tp.v_cache : tp.k_cache, ids, w.h, nvalid, base + s * Tile::BYTES,
+                                       bar(full0 + s));
+          ids = gather4_ids(trow, ts + kKeys, w.kend - ts - kKeys);
           continue;
         }
         const int nsub = (nvalid + BSUB - 1) / BSUB;

@@ -56,20 +56,21 @@ __device__ __forceinline__ int tree_request(const TreeParams& p, int r, TreeReq&
 // boxes instead, and signals the stage with one arrival per lane.  (The warp
 // takes about ten instructions per two rows of 128 elements, well inside the
 // time a tile takes.)  Rows past nvalid become zero.  Block ids of the tile are
-// one per lane (ROWS <= 128).
+// one per lane (ROWS <= 128), loaded a tile ahead (gather4_ids).
+__device__ __forceinline__ int gather4_ids(const int32_t* trow, int ts, int nvalid) {
+  const int lane = threadIdx.x & 31;
+  return 4 * lane < nvalid ? __ldg(trow + ts / 4 + lane) : 0;
+}
+
 template <typename Tile, int D, int ROWS>
-__device__ __forceinline__ void gather4_tile(const TreeParams& p, const void* cache, const int32_t* trow, int h, int ts,
-                                             int nvalid, uint32_t dst, uint32_t bar) {
+__device__ __forceinline__ void gather4_tile(const TreeParams& p, const void* cache, int id, int h, int nvalid,
+                                             uint32_t dst, uint32_t bar) {
   constexpr int CH = D / 8;        // 16-byte chunks of a row
   constexpr int RPI = 32 / CH;     // rows per step
   const int lane = threadIdx.x & 31;
-  int id = 0;
-  if (4 * lane < nvalid) {
-    id = __ldg(trow + ts / 4 + lane);
-    if (id < 0 || id >= p.num_blocks) {
-      record_error(p.err, PA_DEVERR_BLOCK_ID);
-      id = -1;  // its rows become zero
-    }
+  if (id < 0 || id >= p.num_blocks) {
+    record_error(p.err, PA_DEVERR_BLOCK_ID);
+    id = -1;  // its rows become zero
   }
   const int c = lane % CH;
   const char* base = static_cast<const char*>(cache) + ((size_t)h * D + 8 * c) * 2;
