@@ -29,9 +29,9 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 // from the owner.
 //
 // The keys are gone over three times: for the first digit; to list the keys of
-// the chosen first digit (a few in a hundred: the other digits, and the counts
-// of keys above and equal to the result, come from the list; should it not
-// hold them, from all keys); and to write the indices in order, by ballots,
+// the chosen first digit, each warp its own (a few in a hundred: the other
+// digits, and the counts of keys above and equal to the result, come from the
+// list; a warp whose list does not hold them goes over its keys); and to write the indices in order, by ballots,
 // each warp from the counts before it - of the equal keys the first ones.
 // Bound by the instructions and atomics per key and the latency of the steps
 // between (memory is 4 bytes per candidate): keys stay in shared memory as far
@@ -43,36 +43,33 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 constexpr int kSelBins = 2048;
 constexpr int kSelSlices = 16;
 constexpr int kSelSlice = kSelBins / kSelSlices;     // 128 digits, four per lane
-constexpr int kSelList = 1024;
 constexpr int kSelBatch = 8;                         // keys of a lane loaded together
 
-// Shared memory in words before the keys, for a cluster of C.
-__host__ __device__ constexpr int select_words(int C) {
-  return kSelBins + (C == 1 ? kSelBins : 3 * kSelBins / C) + 2 * kSelList;
-}
+// Shared memory in words before the lists and keys, for a cluster of C.
+__host__ __device__ constexpr int select_words(int C) { return kSelBins + (C == 1 ? kSelBins : 3 * kSelBins / C); }
 
 template <int THREADS>
-__global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictSelectParams p) {
+__global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictSelectParams p) {
   constexpr int NW = THREADS / 32;
   extern __shared__ uint4 smem_raw[];
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
+  const int lc = 31 - __clz(C);  // C is a power of two
   uint32_t* hist = reinterpret_cast<uint32_t*>(smem_raw);  // [kSelBins] this CTA's digits
   uint32_t* sums = hist + kSelBins;                        // the cluster's, of the slices it owns, per digit
-  const int sums_stride = C == 1 ? 0 : kSelBins / C;
-  uint2* list = reinterpret_cast<uint2*>(sums + (C == 1 ? kSelBins : 3 * sums_stride));  // (key, place in the run)
-  uint32_t* keys = reinterpret_cast<uint32_t*>(list + kSelList);                        // [p.held]
+  const int sums_stride = C == 1 ? 0 : kSelBins >> lc;
+  uint32_t* lists = hist + select_words(C);                // [NW][p.warp_list] listed keys
+  uint32_t* keys = lists + NW * p.warp_list;               // [NW][p.warp_held]
   __shared__ uint32_t slices[3][kSelSlices];               // the cluster's slice sums
   __shared__ __align__(16) uint32_t s_count[4];            // this CTA's keys above and equal to the result
   __shared__ uint32_t w_above[NW], w_equal[NW];
-  __shared__ uint32_t s_listed, s_want, s_prefix, s_before[2];
+  __shared__ uint32_t s_want, s_prefix, s_before[2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int zero = (kSelBins + (C == 1 ? 0 : 3 * sums_stride)) / 4;
   for (int i = tid; i < zero; i += THREADS) smem_raw[i] = make_uint4(0, 0, 0, 0);
   if (tid < 3 * kSelSlices) (&slices[0][0])[tid] = 0;
-  if (tid == 0) s_listed = 0;
   griddep_wait();
   griddep_launch_dependents();
-  const int r = blockIdx.y, g = blockIdx.x / C;
+  const int r = blockIdx.y, g = blockIdx.x >> lc;
   const int budget = p.sink + p.heavy + p.recent;
   int32_t* keep = p.keep + ((size_t)r * p.kv_heads + g) * budget;
   const int row = p.score_rows ? __ldg(p.score_rows + r) : r;
@@ -97,17 +94,37 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictSelect
   const float* sc = p.scores + ((size_t)row * p.kv_heads + g) * p.score_len + p.sink;
   const int n = L - p.sink - p.recent;  // > heavy
   // this CTA's run of candidates, and each warp's run of it (whole warps wide)
-  const int run = ((n - 1) / (C * THREADS) + 1) * THREADS;
+  const int run = (((n - 1) / THREADS >> lc) + 1) * THREADS;
   const int c0 = (int)min((int64_t)rank * run, (int64_t)n), m = min(run, n - c0);
   sc += c0;
   const int wrun = ((m + THREADS - 1) / THREADS) * 32;
   const int w0 = min(warp * wrun, m), w1 = min(w0 + wrun, m);
-  // a lane's keys i0 + lane + 32 u; behind the run's end 0
-  auto batch = [&](int i0, uint32_t (&k)[kSelBatch]) {
+  // the first keys of the run stay in shared memory, in multiples of a batch:
+  // every warp reads its share of the others again
+  uint32_t* held = keys + warp * p.warp_held - w0;
+  const int h1 = w0 + p.warp_held;
+  // f(k, place, in) for each key of the warp's run, 32 at a time, in order; the
+  // run's whole batches in shared memory take the short way (in: true)
+  auto each_key = [&](auto&& f) {
+    int i0 = w0;
+    const int fast = min(w1, h1) - 32 * kSelBatch;
+    for (; i0 <= fast; i0 += 32 * kSelBatch) {
+      uint32_t k[kSelBatch];
 #pragma unroll
-    for (int u = 0; u < kSelBatch; ++u) {
-      const int i = i0 + 32 * u + lane;
-      k[u] = i >= w1 ? 0u : i < p.held ? keys[i] : score_key(__ldg(sc + i));
+      for (int u = 0; u < kSelBatch; ++u) k[u] = held[i0 + 32 * u + lane];
+#pragma unroll
+      for (int u = 0; u < kSelBatch; ++u) f(k[u], i0 + 32 * u + lane, true);
+    }
+    for (; i0 < w1; i0 += 32 * kSelBatch) {
+      uint32_t k[kSelBatch];
+#pragma unroll
+      for (int u = 0; u < kSelBatch; ++u) {
+        const int i = i0 + 32 * u + lane;
+        k[u] = i >= w1 ? 0u : i < h1 ? held[i] : score_key(__ldg(sc + i));
+      }
+#pragma unroll
+      for (int u = 0; u < kSelBatch; ++u)
+        if (i0 + 32 * u < w1) f(k[u], i0 + 32 * u + lane, i0 + 32 * u + lane < w1);
     }
   };
   if (C == 1) __syncthreads();  // the counts are zero, in every CTA
@@ -116,58 +133,58 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictSelect
   // first digit while the keys come in
   for (int i0 = w0; i0 < w1; i0 += 32 * kSelBatch) {
     float x[kSelBatch];
+    if (i0 + 32 * kSelBatch <= min(w1, h1)) {
+#pragma unroll
+      for (int u = 0; u < kSelBatch; ++u) x[u] = __ldg(sc + i0 + 32 * u + lane);
+#pragma unroll
+      for (int u = 0; u < kSelBatch; ++u) {
+        const uint32_t k = score_key(x[u]);
+        held[i0 + 32 * u + lane] = k;
+        atomicAdd(&hist[k >> 21], 1u);
+      }
+      continue;
+    }
 #pragma unroll
     for (int u = 0; u < kSelBatch; ++u)
       if (i0 + 32 * u + lane < w1) x[u] = __ldg(sc + i0 + 32 * u + lane);
 #pragma unroll
     for (int u = 0; u < kSelBatch; ++u) {
-      if (i0 + 32 * u >= w1) break;
       const int i = i0 + 32 * u + lane;
+      if (i0 + 32 * u >= w1) break;
       if (i < w1) {
         const uint32_t k = score_key(x[u]);
-        if (i < p.held) keys[i] = k;
+        if (i < h1) held[i] = k;
         atomicAdd(&hist[k >> 21], 1u);
       }
     }
   }
   uint32_t prefix = 0, want = p.heavy;  // of the keys with this prefix, `want` are still to be chosen
   uint32_t gt = 0;                      // this lane's keys above the first digit
+  uint32_t* list = lists + warp * p.warp_list;
+  int listed = p.warp_list + 1;         // this warp's keys of the first digit; more than fit: not listed
 #pragma unroll 1
   for (int d = 0; d < 3; ++d) {
     const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bits = d == 2 ? 10 : 11;
-    const uint32_t digits = (1u << bits) - 1;
     if (d == 1) {
-      for (int i0 = w0; i0 < w1; i0 += 32 * kSelBatch) {
-        uint32_t k[kSelBatch];
-        batch(i0, k);
-#pragma unroll
-        for (int u = 0; u < kSelBatch; ++u) {
-          if (i0 + 32 * u >= w1) break;
-          const int i = i0 + 32 * u + lane;
-          gt += (k[u] >> 21) > prefix;  // a key behind the end is 0: not above anything
-          const bool same = i < w1 && (k[u] >> 21) == prefix;
-          const uint32_t eq = __ballot_sync(kAll, same);
-          if (eq) {
-            if (same) atomicAdd(&hist[(k[u] >> shift) & digits], 1u);
-            uint32_t at = 0;
-            if (lane == 0) at = atomicAdd(&s_listed, (uint32_t)__popc(eq));
-            at = __shfl_sync(kAll, at, 0) + __popc(eq & ((1u << lane) - 1));
-            if (same && at < kSelList) list[at] = make_uint2(k[u], i);
-          }
-        }
-      }
+      listed = 0;
+      each_key([&](uint32_t k, int, bool in) {
+        gt += (k >> 21) > prefix;  // a key behind the end is 0: not above anything
+        const bool same = in && (k >> 21) == prefix;
+        if (same) atomicAdd(&hist[(k >> 10) & 2047u], 1u);
+        const uint32_t eq = __ballot_sync(kAll, same);
+        const int at = listed + __popc(eq & ((1u << lane) - 1));
+        if (same && at < p.warp_list) list[at] = k;
+        listed += __popc(eq);
+      });
+      __syncwarp();
     } else if (d == 2) {
-      if (s_listed <= kSelList) {
-        for (int j = tid; j < (int)s_listed; j += THREADS)
-          if ((list[j].x >> 10) == prefix) atomicAdd(&hist[list[j].x & digits], 1u);
+      if (listed <= p.warp_list) {
+        for (int j = lane; j < listed; j += 32)
+          if ((list[j] >> 10) == prefix) atomicAdd(&hist[list[j] & 1023u], 1u);
       } else {
-        for (int i0 = w0; i0 < w1; i0 += 32 * kSelBatch) {
-          uint32_t k[kSelBatch];
-          batch(i0, k);
-#pragma unroll
-          for (int u = 0; u < kSelBatch; ++u)
-            if (i0 + 32 * u + lane < w1 && (k[u] >> 10) == prefix) atomicAdd(&hist[k[u] & digits], 1u);
-        }
+        each_key([&](uint32_t k, int, bool in) {
+          if (in && (k >> 10) == prefix) atomicAdd(&hist[k & 1023u], 1u);
+        });
       }
     }
     __syncthreads();
@@ -177,12 +194,12 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictSelect
       const uint4 v = *mine;
       *mine = make_uint4(0, 0, 0, 0);  // for the next digit
       const uint32_t sum = __reduce_add_sync(kAll, v.x + v.y + v.z + v.w);
-      uint32_t* total = sums + d * sums_stride + sl / C * kSelSlice + 4 * lane;
+      uint32_t* total = sums + d * sums_stride + (sl >> lc) * kSelSlice + 4 * lane;
       if (C == 1) {
         *reinterpret_cast<uint4*>(total) = v;
         if (lane == 0) slices[d][sl] = sum;
       } else {
-        const uint32_t at = smem_u32(total), owner = sl % C;
+        const uint32_t at = smem_u32(total), owner = sl & (C - 1);
         if (v.x) cluster_add(at, owner, v.x);
         if (v.y) cluster_add(at + 4, owner, v.y);
         if (v.z) cluster_add(at + 8, owner, v.z);
@@ -192,22 +209,22 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictSelect
     }
     if (C == 1) __syncthreads();
     else cluster_sync();
-    // one warp (all of them would meet at the slice's owner): lane l holds slice
-    // 15 - l, so that a scan counts from the top
+    // one warp (all of them would meet at the slice's owner), counting from the
+    // top: lane l has slices 15 .. 15 - l
     if (warp == 0) {
-      const uint32_t sl = lane < kSelSlices ? slices[d][kSelSlices - 1 - lane] : 0u;
-      uint32_t upto = sl;
+      uint32_t upto = 0, sl = 0;  // the keys of the first lane + 1 slices, of the last of them
 #pragma unroll
-      for (int o = 1; o < kSelSlices; o <<= 1) {
-        const uint32_t y = __shfl_up_sync(kAll, upto, o);
-        if (lane >= o) upto += y;
+      for (int j = 0; j < kSelSlices; ++j) {
+        const uint32_t x = slices[d][kSelSlices - 1 - j];
+        if (j <= lane) upto += x;
+        if (j == lane) sl = x;
       }
       const int hit = __ffs(__ballot_sync(kAll, upto >= want)) - 1;  // one of the 16: they hold all
       want -= __shfl_sync(kAll, upto - sl, hit);
       const int slice = kSelSlices - 1 - hit;
       // its digits, lane l: the four below 128 - 4 l
-      const uint32_t* from = sums + d * sums_stride + slice / C * kSelSlice + kSelSlice - 4 * (lane + 1);
-      const uint4 q = C == 1 ? *reinterpret_cast<const uint4*>(from) : cluster_ld4(smem_u32(from), slice % C);
+      const uint32_t* from = sums + d * sums_stride + (slice >> lc) * kSelSlice + kSelSlice - 4 * (lane + 1);
+      const uint4 q = C == 1 ? *reinterpret_cast<const uint4*>(from) : cluster_ld4(smem_u32(from), slice & (C - 1));
       const uint32_t four = q.x + q.y + q.z + q.w;
       upto = four;
 #pragma unroll
@@ -216,58 +233,45 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictSelect
         if (lane >= o) upto += y;
       }
       const int at = __ffs(__ballot_sync(kAll, upto >= want)) - 1;
-      uint32_t above = upto - four, digit = slice * kSelSlice + kSelSlice - 1 - 4 * lane;  // lane `at`'s are wanted
-      if (above + q.w < want) {
-        above += q.w;
-        --digit;
-        if (above + q.z < want) {
-          above += q.z;
-          --digit;
-          if (above + q.y < want) {
-            above += q.y;
-            --digit;
-          }
-        }
-      }
+      // which of its four digits, lane `at`'s is wanted (selects: a divergent
+      // branch before a shuffle costs a thousand clocks here)
+      const uint32_t a0 = upto - four, a1 = a0 + q.w, a2 = a1 + q.z, a3 = a2 + q.y;
+      const int e = (a1 < want) + (a2 < want) + (a3 < want);
+      const uint32_t above = e == 0 ? a0 : e == 1 ? a1 : e == 2 ? a2 : a3;
+      const uint32_t keys_of = e == 0 ? q.w : e == 1 ? q.z : e == 2 ? q.y : q.x;
+      const uint32_t next = (prefix << bits) | (uint32_t)(slice * kSelSlice + kSelSlice - 1 - 4 * lane - e);
+      // all keys of the digit are taken: the last key below them does for T, none equal to it taken
+      const bool all = want - above == keys_of;
       if (lane == at) {
-        s_want = want - above;
-        s_prefix = (prefix << bits) | digit;
+        s_want = all ? 0u : want - above;
+        s_prefix = all ? (next << shift) - 1 : next;
       }
     }
     __syncthreads();
     want = s_want;
     prefix = s_prefix;
+    if (want == 0) break;
   }
-  // prefix: the heavy-th largest key; `want` of the equal ones are taken
-  if (s_listed <= kSelList) {
+  // prefix: T, the heavy-th largest key, and `want` of the keys equal to it are
+  // taken (none, where it was enough to know the keys above)
+  uint32_t eq = 0;
+  if (listed <= p.warp_list) {
     gt = __reduce_add_sync(kAll, gt);
-    if (lane == 0) {
-      w_above[warp] = gt;
-      w_equal[warp] = 0;
-    }
-    __syncthreads();
-    for (int j = tid; j < (int)s_listed; j += THREADS) {
-      const uint2 e = list[j];
-      if (e.x > prefix) atomicAdd(&w_above[e.y / wrun], 1u);
-      if (e.x == prefix) atomicAdd(&w_equal[e.y / wrun], 1u);
+    for (int j0 = 0; j0 < listed; j0 += 32) {
+      const uint32_t k = list[min(j0 + lane, p.warp_list - 1)];
+      gt += __popc(__ballot_sync(kAll, j0 + lane < listed && k > prefix));
+      eq += __popc(__ballot_sync(kAll, j0 + lane < listed && k == prefix));
     }
   } else {
-    uint32_t eq = 0;
     gt = 0;
-    for (int i0 = w0; i0 < w1; i0 += 32 * kSelBatch) {
-      uint32_t k[kSelBatch];
-      batch(i0, k);
-#pragma unroll
-      for (int u = 0; u < kSelBatch; ++u) {
-        const bool in = i0 + 32 * u + lane < w1;
-        gt += __popc(__ballot_sync(kAll, in && k[u] > prefix));
-        eq += __popc(__ballot_sync(kAll, in && k[u] == prefix));
-      }
-    }
-    if (lane == 0) {
-      w_above[warp] = gt;
-      w_equal[warp] = eq;
-    }
+    each_key([&](uint32_t k, int, bool in) {
+      gt += __popc(__ballot_sync(kAll, in && k > prefix));
+      eq += __popc(__ballot_sync(kAll, in && k == prefix));
+    });
+  }
+  if (lane == 0) {
+    w_above[warp] = gt;
+    w_equal[warp] = eq;
   }
   __syncthreads();
   // keys before this warp's run: lane w holds warp w's, then lane q CTA q's
@@ -292,26 +296,20 @@ __global__ void __launch_bounds__(THREADS) evict_select_kernel(const EvictSelect
     above += s_before[0];
     equal += s_before[1];
   }
-  uint32_t out = above + min(equal, want);
+  const uint32_t out = above + min(equal, want);
   const uint32_t before = (1u << lane) - 1;
   int32_t* to = keep + p.sink;
-  for (int i0 = w0; i0 < w1; i0 += 32 * kSelBatch) {
-    uint32_t k[kSelBatch];
-    batch(i0, k);
-#pragma unroll
-    for (int u = 0; u < kSelBatch; ++u) {
-      if (i0 + 32 * u >= w1) break;
-      const int i = i0 + 32 * u + lane;
-      uint32_t bt = __ballot_sync(kAll, k[u] > prefix);
-      const uint32_t beq = __ballot_sync(kAll, i < w1 && k[u] == prefix);
-      if (beq) {  // the first ones of the equal keys
-        bt |= __ballot_sync(kAll, ((beq >> lane) & 1) && equal + __popc(beq & before) < want);
-        equal += __popc(beq);
-      }
-      if ((bt >> lane) & 1) to[out + __popc(bt & before)] = p.sink + c0 + i;
-      out += __popc(bt);
+  to += out;
+  each_key([&](uint32_t k, int i, bool in) {
+    uint32_t bt = __ballot_sync(kAll, in && k > prefix);
+    const uint32_t beq = __ballot_sync(kAll, in && k == prefix);
+    if (beq) {  // the first ones of the equal keys
+      bt |= __ballot_sync(kAll, ((beq >> lane) & 1) && equal + __popc(beq & before) < want);
+      equal += __popc(beq);
     }
-  }
+    if ((bt >> lane) & 1) to[__popc(bt & before)] = p.sink + c0 + i;
+    to += __popc(bt);
+  });
 }
 
 template <int THREADS>
@@ -330,10 +328,16 @@ cudaError_t launch_select_t(EvictSelectParams& p, int cluster, int num_seqs, cud
   const int64_t sms = num_sms() > 0 ? num_sms() : 152;
   int64_t per_sm = ((int64_t)p.kv_heads * num_seqs * cluster + sms - 1) / sms;
   if (per_sm > 2048 / THREADS) per_sm = 2048 / THREADS;
-  const int64_t room = (kMost / per_sm - 4096) / 4 - select_words(cluster);
-  const int64_t run = ((int64_t)p.score_len / ((int64_t)cluster * THREADS) + 1) * THREADS;
-  p.held = (int)(room < 0 ? 0 : run < room ? run : room);
-  const size_t smem = (size_t)(select_words(cluster) + p.held) * 4;
+  const int64_t run = ((int64_t)p.score_len / ((int64_t)cluster * THREADS) + 1) * THREADS;  // at most, of a CTA
+  // lists: a quarter of a warp's run and a little, 32 KB in all at most
+  constexpr int NW = THREADS / 32;
+  const int64_t quarter = run / (4 * NW) + 32;
+  p.warp_list = (int)(quarter < 8192 / NW ? quarter : 8192 / NW);
+  const int64_t room = (kMost / per_sm - 4096) / 4 - select_words(cluster) - NW * p.warp_list;
+  const int64_t batches = (run / NW + 32 * kSelBatch - 1) / (32 * kSelBatch);  // of a warp
+  const int64_t fit = room < 0 ? 0 : room / (NW * 32 * kSelBatch);
+  p.warp_held = (int)(batches < fit ? batches : fit) * 32 * kSelBatch;
+  const size_t smem = (size_t)(select_words(cluster) + NW * (p.warp_list + p.warp_held)) * 4;
   return launch_pdl_cluster(kern, cluster, dim3((unsigned)(p.kv_heads * cluster), num_seqs), dim3(THREADS), smem,
                             stream, p);
 }

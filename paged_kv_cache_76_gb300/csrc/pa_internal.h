@@ -251,7 +251,7 @@ struct EvictSelectParams {
   int32_t* keep_lens;
   int* err;
   int num_rows, kv_heads, score_len, sink, heavy, recent;
-  int held;  // set by the launcher: keys a CTA holds in shared memory
+  int warp_held, warp_list;  // set by the launcher: keys and listed keys a warp has room for in shared memory
 };
 cudaError_t launch_evict_select(const EvictSelectParams& p, int num_seqs, cudaStream_t stream);
 
