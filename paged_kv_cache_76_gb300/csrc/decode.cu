@@ -697,28 +697,34 @@ __device__ __forceinline__ void add_weights(const AccumulateParams& p, int part)
     }
   };
   load(t0);
-  const int G = p.group;
-  const int nsplit = (ctx + p.split_tokens - 1) / p.split_tokens;
-  for (int g = warp; g < GP; g += threads / 32) {
-    const size_t prow = ((size_t)r * p.q_heads + h * G + g) * p.max_splits;
-    float M = -INFINITY, l = 0.f;
-    if (g < G) {  // heads that pad the group weigh nothing
-      for (int c = lane; c < nsplit; c += 32) M = fmaxf(M, p.part_m[prow + c]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      if (M == -INFINITY) M = 0.f;
-      for (int c = lane; c < nsplit; c += 32) l += exp2f(p.part_m[prow + c] - M) * p.part_w[prow + c];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    }
-    if (lane == 0) {
-      s_m[g] = M;
-      s_inv[g] = l > 0.f ? 1.f / l : 0.f;
-    }
-  }
   bool twice = false;  // an earlier request has this row: it alone keeps score
   if (p.score_rows)
     for (int i = tid; i < r; i += threads) twice |= __ldg(p.score_rows + i) == row;
+  const int G = p.group;
+  const int nsplit = (ctx + p.split_tokens - 1) / p.split_tokens;
+  for (int g = warp; g < GP; g += threads / 32) {
+    // M and W of the head in one pass over its partitions: each lane the
+    // largest reference of its own and its sum brought to that, then the warp's
+    const size_t prow = ((size_t)r * p.q_heads + h * G + (g < G ? g : 0)) * p.max_splits;
+    float m = -INFINITY, l = 0.f;
+    for (int c = lane; c < nsplit; c += 32) {
+      const float mc = p.part_m[prow + c], wc = p.part_w[prow + c];
+      const float mn = fmaxf(m, mc);
+      if (mn != -INFINITY) l = l * exp2f(m - mn) + wc * exp2f(mc - mn);
+      m = mn;
+    }
+    float M = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    if (M == -INFINITY) M = 0.f;
+    l *= exp2f(m - M);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) {
+      s_m[g] = M;
+      s_inv[g] = l > 0.f && g < G ? 1.f / l : 0.f;  // heads that pad the group weigh nothing
+    }
+  }
   if (__syncthreads_or(twice)) {
     if (tid == 0) record_error(p.err, PA_DEVERR_SCORE_ROW);
     return;
