@@ -29,7 +29,9 @@
  *   or written only once the previous kernel has completed.  So those four
  *   inputs must be ready when the call is enqueued (they are if whatever writes
  *   them was enqueued earlier on the stream without allowing early launch of
- *   its successor, as plain kernels and copies do).
+ *   its successor, as plain kernels and copies do; pa_norm_rope_and_cache, whose
+ *   q_out is such an input, and pa_evict_select, whose keep_lens may be, do the
+ *   same).
  * - Errors: every call returns a pa_status.  Argument errors are caught on the
  *   host before anything is launched.  Data errors that only the device can
  *   see (a block id outside [0, num_blocks), a slot past the pool, a context
@@ -543,7 +545,7 @@ int pa_norm_rope_and_cache(const void* q, const void* k, const void* v, int64_t 
  * no rows.  pa_verify_decode is the chain (mask bits 0..j).
  *   q, out        [total_q][q_heads][head_dim]
  *   q_start       int32 [num_reqs + 1], non-decreasing, q_start[num_reqs] <= total_q
- *   tree_mask     uint64 [total_q]
+ *   tree_mask     uint64 [total_q]; read during set-up, like q and q_start
  *   max_q_len     host-side bound of n, 1..64 (sizes the grid and the scratch)
  *   split_tokens  0 = the library's choice; else a multiple of 128: the context
  *                 is attended in partitions of that size, merged by log-sum-exp

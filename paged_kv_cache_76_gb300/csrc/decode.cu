@@ -652,7 +652,10 @@ __global__ void __launch_bounds__(256) lse_merge_warp_kernel(const MergeParams p
 // are under way: each thread takes the logits of 16 / GP tokens at a time, and
 // its first ones while the CTA works out M and W.  A CTA takes p.chunk tokens,
 // enough that the partials it reads for M and W stay below a quarter of its
-// logits.
+// logits.  Measured on GB300: the whole call 107 us where pa_decode takes 91 (64
+// requests of 532..4027 tokens, 32/8 heads), 510 where it takes 421 (8 of
+// 44..128 thousand, 64/8 heads: 168 MB of logits written and read); 4 requests
+// of <= 1500 tokens 9.4.  8 logits a thread (more, smaller CTAs): 112 and 519.
 constexpr int kMaxGroup = 16;
 
 // GP: floats between tokens (the group rounded up to 1, 2 or a multiple of 4).

@@ -10,6 +10,10 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
+// Loads here are plain ones, not through the read-only path: scores, lists and
+// lengths may come from the kernel before, which may still run when a CTA of
+// these starts (they wait for it first).
+
 // Order-preserving map of fp32 to uint32 (-0 equals +0, NaN below everything).
 __device__ __forceinline__ uint32_t score_key(float x) {
   const uint32_t b = __float_as_uint(x + 0.f);  // -0 + 0 is +0
@@ -31,15 +35,15 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 // The keys are gone over three times: for the first digit; to list the keys of
 // the chosen first digit, each warp its own (a few in a hundred: the other
 // digits, and the counts of keys above and equal to the result, come from the
-// list; a warp whose list does not hold them goes over its keys); and to write the indices in order, by ballots,
-// each warp from the counts before it - of the equal keys the first ones.
+// list; a warp whose list does not hold them goes over its keys); and to write
+// the indices in order, by ballots, each warp from the counts before it - of
+// the equal keys the first ones.
 // Bound by the instructions and atomics per key and the latency of the steps
 // between (memory is 4 bytes per candidate): keys stay in shared memory as far
 // as that leaves every CTA resident at once, and the rest are read again from
-// L2.  Measured on GB300: 512 rows of 2300 keys 15.5 us, 64 of 85000 30 us, 8
-// of 131000 18 us.  A range for the threshold from a sample of the row, which
-// saves most atomics, measured slower (25, 36 and 21 us): the sample's own
-// steps cost more.
+// L2.  Measured on GB300: 512 rows of 2300 keys 8.6 us, 64 of 85000 21 us, 8 of
+// 131000 14 us.  A range for the threshold from a sample of the row, to save
+// most atomics, was slower: the sample's own steps cost more.
 constexpr int kSelBins = 2048;
 constexpr int kSelSlices = 16;
 constexpr int kSelSlice = kSelBins / kSelSlices;     // 128 digits, four per lane
@@ -67,13 +71,14 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictSel
   const int zero = (kSelBins + (C == 1 ? 0 : 3 * sums_stride)) / 4;
   for (int i = tid; i < zero; i += THREADS) smem_raw[i] = make_uint4(0, 0, 0, 0);
   if (tid < 3 * kSelSlices) (&slices[0][0])[tid] = 0;
+  // No early launch of the next kernel: keep_lens may be the context lengths
+  // that one reads in its set-up.
   griddep_wait();
-  griddep_launch_dependents();
   const int r = blockIdx.y, g = blockIdx.x >> lc;
   const int budget = p.sink + p.heavy + p.recent;
   int32_t* keep = p.keep + ((size_t)r * p.kv_heads + g) * budget;
-  const int row = p.score_rows ? __ldg(p.score_rows + r) : r;
-  const int L = __ldg(p.lens + r);
+  const int row = p.score_rows ? p.score_rows[r] : r;
+  const int L = p.lens[r];
   const int t0 = rank * THREADS + tid, tn = C * THREADS;  // this thread among the cluster's
   if (row < 0 || row >= p.num_rows || L < 0 || L > p.score_len) {
     if (t0 == 0) {
@@ -120,7 +125,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictSel
 #pragma unroll
       for (int u = 0; u < kSelBatch; ++u) {
         const int i = i0 + 32 * u + lane;
-        k[u] = i >= w1 ? 0u : i < h1 ? held[i] : score_key(__ldg(sc + i));
+        k[u] = i >= w1 ? 0u : i < h1 ? held[i] : score_key(sc[i]);
       }
 #pragma unroll
       for (int u = 0; u < kSelBatch; ++u)
@@ -135,7 +140,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictSel
     float x[kSelBatch];
     if (i0 + 32 * kSelBatch <= min(w1, h1)) {
 #pragma unroll
-      for (int u = 0; u < kSelBatch; ++u) x[u] = __ldg(sc + i0 + 32 * u + lane);
+      for (int u = 0; u < kSelBatch; ++u) x[u] = sc[i0 + 32 * u + lane];
 #pragma unroll
       for (int u = 0; u < kSelBatch; ++u) {
         const uint32_t k = score_key(x[u]);
@@ -146,7 +151,7 @@ __global__ void __launch_bounds__(THREADS, 1) evict_select_kernel(const EvictSel
     }
 #pragma unroll
     for (int u = 0; u < kSelBatch; ++u)
-      if (i0 + 32 * u + lane < w1) x[u] = __ldg(sc + i0 + 32 * u + lane);
+      if (i0 + 32 * u + lane < w1) x[u] = sc[i0 + 32 * u + lane];
 #pragma unroll
     for (int u = 0; u < kSelBatch; ++u) {
       const int i = i0 + 32 * u + lane;
@@ -369,9 +374,9 @@ struct MoveRange {
 
 // The request's range, checked; false: nothing is moved.
 __device__ __forceinline__ bool move_range(const CompactParams& p, int r, MoveRange& m, bool report) {
-  m.L = __ldg(p.lens + r);
-  m.n = __ldg(p.keep_lens + r);
-  m.base = p.base ? __ldg(p.base + r) : 0;
+  m.L = p.lens[r];
+  m.n = p.keep_lens[r];
+  m.base = p.base ? p.base[r] : 0;
   if (m.L < 0 || m.L > p.cap) {
     if (report) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
     return false;
@@ -420,7 +425,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) compact_kv_kernel(con
 #pragma unroll
     for (int u = 0; u < kMoveUnroll; ++u) {
       const int i = entry(c, u);
-      src[u] = c < steps && i < m.n ? __ldg(keep + i) : i;
+      src[u] = c < steps && i < m.n ? keep[i] : i;
     }
   };
   // block ids of the entries to move and of their places; `src` becomes -1
@@ -514,11 +519,11 @@ __global__ void __launch_bounds__(kScoreThreads) compact_scores_kernel(const Com
   };
   MoveRange m;
   if (!move_range(p, r, m, false)) return;  // reported by the rows' kernel
-  const int row = p.score_rows ? __ldg(p.score_rows + r) : r;
+  const int row = p.score_rows ? p.score_rows[r] : r;
   if (row < 0) return;
   bool twice = false;  // an earlier request has this row: its alone are moved
   if (p.score_rows)
-    for (int i = tid; i < r; i += kScoreThreads) twice |= __ldg(p.score_rows + i) == row;
+    for (int i = tid; i < r; i += kScoreThreads) twice |= p.score_rows[i] == row;
   const bool bad = __syncthreads_or(twice) || row >= p.num_rows;
   if (bad || m.L > p.score_len) {
     if (tid == 0) record_error(p.err, bad ? PA_DEVERR_SCORE_ROW : PA_DEVERR_CONTEXT_LEN);
@@ -535,7 +540,7 @@ __global__ void __launch_bounds__(kScoreThreads) compact_scores_kernel(const Com
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t i = i0 + u * kScoreThreads;
-      src[u] = i < m.n ? __ldg(keep + i) : -1;
+      src[u] = i < m.n ? keep[i] : -1;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
@@ -593,7 +598,7 @@ __global__ void __launch_bounds__(kMoveThreads) compact_small_kernel(const Compa
     const int i = u * ROWS + tid / VECS;
     to[u] = -1;
     if (i < m.n) {
-      const int src = __ldg(keep + i);
+      const int src = keep[i];
       if (src < i || src >= room) {
         record_error(p.err, PA_DEVERR_KEEP);
       } else if (src != i) {
@@ -623,10 +628,10 @@ cudaError_t launch_evict_select(const EvictSelectParams& p0, int num_seqs, cudaS
   EvictSelectParams p = p0;
   // One CTA per SM: clusters of up to 8 share a row while there are SMs for
   // them and a thousand keys for each CTA.  A second CTA on an SM only halves
-  // both (64 rows of 85000 keys: clusters of 2, 4, 8 of 1024 threads 30, 42, 80
-  // us; of 512 threads 41, 34, 56).  More rows than SMs: small CTAs, the steps
-  // between the keys cost what short rows do (512 rows of 2300: 256 threads
-  // 15.5 us, 512 17.2, 1024 32.3).
+  // both (an earlier form, 64 rows of 85000 keys: clusters of 2, 4, 8 of 1024
+  // threads 30, 42, 80 us; of 512 threads 41, 34, 56).  More rows than SMs: small
+  // CTAs, the steps between the keys cost what short rows do (512 rows of 2300:
+  // 256 threads 15.5 us, 512 17.2, 1024 32.3).
   const int64_t rows = (int64_t)p.kv_heads * num_seqs, sms = num_sms() > 0 ? num_sms() : 152;
   int cluster = 1;
   while (cluster < 8 && rows * cluster * 2 <= sms && (int64_t)cluster * 1024 < p.score_len) cluster *= 2;
