@@ -226,8 +226,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int nunits =
       row_tiles * p.kv_heads *
       (TREE ? p.num_reqs * tp.max_splits : p.causal ? p.num_reqs : (p.prefix_len + p.key_split - 1) / p.key_split);
-  const int cta0 = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
+  int cta0 = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
   const int nctas = gridDim.x * gridDim.y * gridDim.z;
+  if constexpr (TREE) {
+    if (tp.longest_first) {  // one partition: a request's units are next to one another
+      __shared__ int longest[kTreeWindow + 1];
+      const int per_r = row_tiles * p.kv_heads, r = cta0 / per_r;
+      cta0 += (tree_longest_first(tp, r, longest) - r) * per_r;
+    }
+  }
   auto unit = [&](int u, TcUnit& w) -> bool {
     if constexpr (TREE) return tree_unit(p, tp, u, row_tiles, w) == 0;
     return tc_unit(p, u, row_tiles, w);

@@ -217,8 +217,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   // CTA b (linear block index) takes units b, b + nctas, ...
   const int row_tiles = (p.max_q_len * G + kRows - 1) / kRows;
   const int nunits = row_tiles * p.kv_heads * p.num_reqs * (TREE ? tp.max_splits : 1);
-  const int cta0 = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
+  int cta0 = blockIdx.x + gridDim.x * (blockIdx.y + gridDim.y * blockIdx.z);
   const int nctas = gridDim.x * gridDim.y * gridDim.z;
+  if constexpr (TREE) {
+    if (tp.longest_first) {  // one partition: a request's units are next to one another
+      const int per_r = row_tiles * p.kv_heads, r = cta0 / per_r;
+      cta0 += (tree_longest_first(tp, r, reinterpret_cast<int*>(smem + L::L_OFF)) - r) * per_r;
+    }
+  }
   // the spread form keeps its epilogue's partial outputs in V stages that
   // the next unit's loads would overwrite: it takes one unit per CTA (the
   // host launches it so)

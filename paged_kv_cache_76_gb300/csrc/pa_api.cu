@@ -1149,7 +1149,8 @@ int tree_setup(int num_reqs, int total_q, int max_q_len, int q_heads, int kv_hea
     // SM two run whole: a partition's partials (a kilobyte written and read
     // per row) then cost more than the balance brings.  Measured on GB300, 64
     // requests of <= 4096 tokens, 8 KV heads: whole 132 us, 2048-token
-    // partitions 153 us (80..128 rows); 162 and 190 us (104..240 rows).  Fewer
+    // partitions 153 us (80..128 rows); 162 and 190 us (104..240 rows); whole
+    // and in order of length 127 and 143.  Fewer
     // units are cut into about four per SM, but no smaller than the partials
     // are worth (twice the rows): 8 contexts of 33..131 thousand tokens, 128
     // rows: 65536 tokens 649 us, 32768 568, 12288 462, 4096 507; one of 8060,
@@ -1240,6 +1241,10 @@ int pa_verify_tree(const void* q, const int32_t* q_start, const uint64_t* tree_m
   p.block_size = block_size;
   p.split_tokens = s.split;
   p.max_splits = s.max_splits;
+  // not for the few-row form, whose units are bound by latency and HBM alike:
+  // the order costs it more than the shorter end brings (see tree_longest_first)
+  p.longest_first =
+      s.max_splits == 1 && (int64_t)num_reqs * kv_heads > sm_count() && max_q_len * p.group > 32;
   p.scale_log2 = scale * 1.4426950408889634f;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   if (s.ws.bytes) {

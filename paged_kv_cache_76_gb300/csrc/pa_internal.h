@@ -229,6 +229,7 @@ struct TreeParams {
   int* err;
   int maxblk, num_reqs, total_q, max_q_len, q_heads, kv_heads, group, num_blocks, block_size;
   int split_tokens, max_splits;  // partitions of the context; one: no scratch
+  int longest_first;             // 1 (max_splits == 1 only): requests run in order of length (tree_longest_first)
   float scale_log2;
   float* part_o;  // [total_q * q_heads][max_splits][head_dim], as the decode partials
   float* part_m;

@@ -269,6 +269,48 @@ def test_streams_graphs_and_recordings():
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("nreq,max_n,bs", [(170, 9, 16), (130, 64, 16), (300, 20, 4)])
+def test_a_batch_of_many_lengths(nreq, max_n, bs):
+    """More units than the GPU runs at once, which then start in order of
+    length, 128 requests at a time: equal lengths, requests without queries or
+    context and refused ones, on both sides of the 128.  The order decides when
+    a unit runs, never what it computes: every request's rows are bit-identical
+    to the request's alone."""
+    from paged_kv_cache_76_gb300 import _lib
+    g = np.random.default_rng(41 + nreq)
+    nodes = g.integers(0, max_n + 1, nreq)
+    hist = np.where(g.integers(0, 3, nreq) > 0, g.integers(0, 1000, nreq), 500)
+    hist[[0, 5, 127, 128, nreq - 1]] = [1000, 0, 0, 1000, 1]
+    nodes[[0, 5, 127, 128, nreq - 1]] = [max_n, 0, 1, max_n, 1]
+    c = make(8, hist.tolist(), nodes.tolist(), 8, 2, 64, bs, "bf16")
+    whole = c["tables"].shape[1] * bs
+    whole += -whole % 128
+    got = call(c, split_tokens=whole)
+    assert ops().get_device_error() == 0
+    qs = c["q_start"].tolist()
+
+    def alone(r):
+        one = {**c, "q": c["q"][qs[r]:qs[r + 1]], "mask": c["mask"][qs[r]:qs[r + 1]], "lens": c["lens"][r:r + 1],
+               "tables": c["tables"][r:r + 1],
+               "q_start": torch.tensor([0, qs[r + 1] - qs[r]], dtype=torch.int32, device="cuda")}
+        return call(one, split_tokens=whole)
+
+    for r in range(nreq):
+        if qs[r] < qs[r + 1]:
+            assert torch.equal(got[qs[r]:qs[r + 1]], alone(r)), r
+    for r in (0, 127, 128, nreq - 1):
+        assert_request(c, got, r)
+    bad = c["lens"].clone()
+    bad[0], bad[128] = whole + 1, 2 ** 31 - 1   # past the table: refused, and first in the order
+    out = torch.full_like(c["q"], 7.0)
+    call({**c, "lens": bad}, out=out, split_tokens=whole)
+    assert ops().get_device_error() == _lib.PA_DEVERR_CONTEXT_LEN
+    skipped = torch.zeros(len(out), dtype=torch.bool, device="cuda")
+    for r in (0, 128):
+        skipped[qs[r]:qs[r + 1]] = True
+    assert bool((out[skipped] == 7.0).all()) and torch.equal(out[~skipped], got[~skipped])
+
+
 def test_empty_calls():
     c = make(7, [20], [3], 8, 2, 128, 16, "bf16")
     out = ops().verify_tree(c["q"][:0], c["q_start"][:1], c["mask"][:0], c["lens"][:0], c["kc"], c["vc"],
