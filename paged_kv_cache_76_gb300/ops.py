@@ -8,6 +8,7 @@ documented shapes; int32 index tensors live on the same device.
 from __future__ import annotations
 
 import ctypes as C
+import functools
 import math
 import threading
 
@@ -439,10 +440,67 @@ def chunked_prefill(q, q_start, context_lens, k_cache, v_cache, block_tables, sc
     return out
 
 
-def _check_current(t: torch.Tensor):
-    """The library launches on the current device: a tensor elsewhere would be another GPU's memory."""
-    if t.is_cuda and t.device.index != torch.cuda.current_device():
-        raise ValueError(f"tensors are on {t.device}, but the current device is cuda:{torch.cuda.current_device()}")
+# The calls below take microseconds on the GPU, so their checks are written for
+# few interpreter steps: a device is its index (-1: not a GPU's), a tensor is
+# checked and its pointer taken in one place, and pure functions of sizes are
+# remembered.
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _stream_on(dev: int, stream=None):
+    """The launch's stream; the library launches on the current device, where every tensor has to be."""
+    if dev < 0:
+        raise ValueError("the tensors must be CUDA tensors")
+    if dev != _current_device():
+        raise ValueError(f"the tensors are on cuda:{dev}, but the current device is cuda:{_current_device()}")
+    if stream is not None:
+        return stream.cuda_stream
+    return _raw_stream(dev) if _raw_stream is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _ptr(t: torch.Tensor, name: str, dev: int) -> int:
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not with the other tensors")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows_ptr(t: torch.Tensor, name: str, dev: int, rows: int) -> int:
+    """An int32 index tensor with `rows` leading entries."""
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    shape = t.shape
+    if not shape or shape[0] != rows:
+        raise ValueError(f"{name} has shape {tuple(shape)}: {rows} rows expected")
+    return _ptr(t, name, dev)
+
+
+def _table_ptr(t: torch.Tensor, dev: int, rows: int) -> int:
+    if t.dim() != 2:
+        raise ValueError("block_tables is [num_seqs, max_blocks_per_seq]")
+    return _rows_ptr(t, "block_tables", dev, rows)
+
+
+def _cache_ptrs(k_cache, v_cache, dev: int):
+    """(k, v) pointers of two caches of one shape and dtype."""
+    if k_cache.dim() != 4:
+        raise ValueError("caches are [num_blocks, block_size, kv_heads, head_dim]")
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must agree in shape, dtype and device")
+    return _ptr(k_cache, "k_cache", dev), _ptr(v_cache, "v_cache", dev)
+
+
+def _score_ptrs(scores, hkv: int, score_rows, num_seqs: int, dev: int, name="scores"):
+    """(scores, score_rows) pointers."""
+    shape = scores.shape
+    if len(shape) != 3 or shape[1] != hkv or scores.dtype != torch.float32:
+        raise ValueError(f"{name} is fp32 [rows, kv_heads, length]")
+    if score_rows is not None:
+        return _ptr(scores, name, dev), _rows_ptr(score_rows, "score_rows", dev, num_seqs)
+    if shape[0] < num_seqs:
+        raise ValueError(f"{name} has fewer rows than there are requests")
+    return _ptr(scores, name, dev), None
 
 
 def rope_table(max_position: int, rot_dim: int, base: float = 10000.0, device=None) -> torch.Tensor:
@@ -454,12 +512,12 @@ def rope_table(max_position: int, rot_dim: int, base: float = 10000.0, device=No
     return torch.cat([angle.cos(), angle.sin()], 1).to(torch.float32)
 
 
-def _token_rows(t: torch.Tensor, name: str, heads: int, d: int, dtype, device) -> int:
+def _token_rows(t: torch.Tensor, name: str, heads: int, d: int, dtype, dev: int) -> int:
     """Token stride (elements) of [num_tokens, heads, head_dim] whose heads are contiguous."""
     if t.dtype != dtype:
         raise TypeError(f"{name} ({t.dtype}) must have the cache's dtype ({dtype})")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, not {device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not with the other tensors")
     row = heads * d
     if t.is_contiguous():
         stride = row
@@ -468,7 +526,7 @@ def _token_rows(t: torch.Tensor, name: str, heads: int, d: int, dtype, device) -
         if s2 != 1 or (heads > 1 and s1 != d):
             raise ValueError(f"{name}: the heads of a token must be contiguous")
         stride = s0 if t.shape[0] > 1 else row
-    if stride < row or stride % 8:
+    if stride < row or stride & 7:
         raise ValueError(f"{name}: tokens must be at least a row, and a multiple of 8 elements, apart")
     return stride
 
@@ -483,23 +541,23 @@ def norm_rope_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
 
     ``q``/``k``/``v`` may be views of one projection's rows.  ``positions``: int32 [num_tokens], or
     [axes, num_tokens] with ``sections`` (pairs per axis).  ``out`` may be ``q`` if that is contiguous."""
-    nb, bs, hkv, d = _cache_dims(k_cache)
-    _check_caches(k_cache, v_cache)
-    dtype, device = k_cache.dtype, k_cache.device
+    dtype, dev = k_cache.dtype, k_cache.get_device()
+    kc, vc = _cache_ptrs(k_cache, v_cache, dev)
+    nb, bs, hkv, d = k_cache.shape
     if q.dim() != 3 or q.shape[2] != d:
         raise ValueError("q is [num_tokens, q_heads, head_dim] of the cache's head_dim")
-    T, hq, _ = q.shape
+    qshape = T, hq, _ = q.shape
     if k.shape != (T, hkv, d) or v.shape != (T, hkv, d):
         raise ValueError("k and v are [num_tokens, kv_heads, head_dim] of the cache, as many tokens as q")
-    qs = _token_rows(q, "q", hq, d, dtype, device)
-    ks = _token_rows(k, "k", hkv, d, dtype, device)
-    vs = _token_rows(v, "v", hkv, d, dtype, device)
+    qs = _token_rows(q, "q", hq, d, dtype, dev)
+    ks = _token_rows(k, "k", hkv, d, dtype, dev)
+    vs = _token_rows(v, "v", hkv, d, dtype, dev)
     pshape = positions.shape
     axes = 1 if len(pshape) == 1 else pshape[0] if len(pshape) == 2 else 0
-    if not 1 <= axes <= 3 or pshape[-1] != T or positions.device != device:
-        raise ValueError("positions is [num_tokens] or [1 to 3 axes, num_tokens] on q's device")
-    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32 or cos_sin.device != device:
-        raise ValueError("cos_sin is fp32 [max_position, rot_dim] on q's device")
+    if not 1 <= axes <= 3 or pshape[-1] != T:
+        raise ValueError("positions is [num_tokens] or [1 to 3 axes, num_tokens]")
+    if cos_sin.dim() != 2 or cos_sin.dtype != torch.float32:
+        raise ValueError("cos_sin is fp32 [max_position, rot_dim]")
     max_pos, rot = cos_sin.shape
     sec = None
     if sections is None:
@@ -509,30 +567,27 @@ def norm_rope_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
         raise ValueError(f"sections are {axes} counts of pairs, rot_dim / 2 = {rot // 2} together")
     else:
         sec = _Sections(*sections)
-    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None and (w.shape != (d,) or w.dtype != dtype or w.device != device):
-            raise ValueError(f"{n} is [head_dim] of q's dtype and device")
-    _check_index(k_cache, "slot_mapping", slot_mapping, T)
+    qw = kw = None
+    if q_weight is not None:
+        if q_weight.shape != (d,) or q_weight.dtype != dtype:
+            raise ValueError("q_weight is [head_dim] of q's dtype")
+        qw = _ptr(q_weight, "q_weight", dev)
+    if k_weight is not None:
+        if k_weight.shape != (d,) or k_weight.dtype != dtype:
+            raise ValueError("k_weight is [head_dim] of q's dtype")
+        kw = _ptr(k_weight, "k_weight", dev)
+    sl = _rows_ptr(slot_mapping, "slot_mapping", dev, T)
     if out is None:
-        out = torch.empty((T, hq, d), dtype=dtype, device=device)
-    elif out.shape != (T, hq, d) or out.dtype != dtype or out.device != device:
+        out = torch.empty(qshape, dtype=dtype, device=q.device)
+    elif out.shape != qshape or out.dtype != dtype:
         raise ValueError("out must have q's shape, dtype and device")
-    _check_current(q)
+    handle = _stream_on(dev, stream)
     _keep(out)
     _launch(
-        "pa_norm_rope_and_cache", _dev_rows(q, "q"), _dev_rows(k, "k"), _dev_rows(v, "v"), qs, ks, vs,
-        _dev(q_weight, "q_weight") if q_weight is not None else None,
-        _dev(k_weight, "k_weight") if k_weight is not None else None, eps, _i32(positions, "positions"), axes, sec,
-        _dev(cos_sin, "cos_sin"), max_pos, rot, 1 if interleaved else 0, _i32(slot_mapping, "slot_mapping"), T, hq,
-        _dev(out, "out"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), nb, bs, hkv, d, dtype_code(dtype),
-        _stream(stream))
+        "pa_norm_rope_and_cache", q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, qw, kw, eps,
+        _rows_ptr(positions, "positions", dev, pshape[0]), axes, sec, _ptr(cos_sin, "cos_sin", dev), max_pos, rot,
+        1 if interleaved else 0, sl, T, hq, _ptr(out, "out", dev), kc, vc, nb, bs, hkv, d, dtype_code(dtype), handle)
     return out
-
-
-def _dev_rows(t: torch.Tensor, name: str):
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.data_ptr()
 
 
 def tree_mask(parents) -> torch.Tensor:
@@ -559,37 +614,48 @@ def verify_tree_workspace_size(num_reqs, total_q, max_q_len, q_heads, kv_heads, 
                                                         max_blocks_per_seq, block_size, split_tokens))
 
 
+@functools.lru_cache(maxsize=4096)
+def _tree_workspace(dev, *sizes) -> int:  # dev: the choice depends on the current device
+    return verify_tree_workspace_size(*sizes)
+
+
 def verify_tree(q, q_start, tree_mask, context_lens, k_cache, v_cache, block_tables, scale, max_q_len, out=None,
                 split_tokens=0, workspace=None, stream=None):
     """pa_verify_tree: ``q`` is [total_q, q_heads, head_dim], packed by ``q_start``; bit m of ``tree_mask[i]`` (int64)
     lets row i see its request's node m.  Every row sees the context before the draft."""
-    nb, bs, hkv, d = _cache_dims(k_cache)
+    dtype, dev = q.dtype, q.get_device()
+    kc, vc = _cache_ptrs(k_cache, v_cache, dev)
+    nb, bs, hkv, d = k_cache.shape
     if q.dim() != 3 or q.shape[2] != d:
         raise ValueError("q is [total_q, q_heads, head_dim] of the cache's head_dim")
-    T, hq, _ = q.shape
-    R = int(context_lens.shape[0])
-    if out is None:
-        out = torch.empty_like(q)
-    _check_attention(q, k_cache, v_cache, out)
-    _check_index(q, "context_lens", context_lens, R)
-    _check_index(q, "q_start", q_start, R + 1)
-    _check_index(q, "block_tables", block_tables, R, table=True)
-    _check_index(q, "tree_mask", tree_mask, T)
+    qshape = T, hq, _ = q.shape
+    if k_cache.dtype != dtype or (out is not None and out.dtype != dtype):
+        raise TypeError(f"q ({dtype}), the caches ({k_cache.dtype}) and out must share a dtype")
+    R = context_lens.shape[0]
+    lens = _rows_ptr(context_lens, "context_lens", dev, R)
+    starts = _rows_ptr(q_start, "q_start", dev, R + 1)
+    tables = _table_ptr(block_tables, dev, R)
     if tree_mask.dtype != torch.int64:
         raise TypeError("tree_mask must be int64")
-    _check_current(q)
-    maxblk = int(block_tables.shape[1])
+    if tree_mask.dim() == 0 or tree_mask.shape[0] != T:
+        raise ValueError(f"tree_mask has shape {tuple(tree_mask.shape)}: {T} rows expected")
+    mask = _ptr(tree_mask, "tree_mask", dev)
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != qshape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, q {tuple(qshape)}")
+    handle = _stream_on(dev, stream)
+    maxblk = block_tables.shape[1]
+    max_q_len, split_tokens = int(max_q_len), int(split_tokens)
     if workspace is None:
-        n = verify_tree_workspace_size(R, T, int(max_q_len), hq, hkv, d, maxblk, bs, split_tokens)
+        n = _tree_workspace(dev, R, T, max_q_len, hq, hkv, d, maxblk, bs, split_tokens)
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
-    ws_ptr, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
+    ws_ptr, ws_bytes = (_ptr(workspace, "workspace", dev), workspace.numel() * workspace.element_size()) \
         if workspace is not None else (None, 0)
     _keep(out, workspace)
     _launch(
-        "pa_verify_tree", _dev(q, "q"), _i32(q_start, "q_start"), _dev(tree_mask, "tree_mask"),
-        _i32(context_lens, "context_lens"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-        _i32(block_tables, "block_tables"), maxblk, R, T, int(max_q_len), hq, hkv, d, bs, nb, float(scale),
-        int(split_tokens), ws_ptr, ws_bytes, _dev(out, "out"), dtype_code(q.dtype), _stream(stream))
+        "pa_verify_tree", _ptr(q, "q", dev), starts, mask, lens, kc, vc, tables, maxblk, R, T, max_q_len, hq, hkv, d,
+        bs, nb, float(scale), split_tokens, ws_ptr, ws_bytes, _ptr(out, "out", dev), dtype_code(dtype), handle)
     return out
 
 
@@ -606,13 +672,9 @@ def decode_accumulate_workspace_size(num_seqs, q_heads, kv_heads, head_dim, max_
                                                               max_blocks_per_seq, block_size, split_tokens))
 
 
-def _check_scores(ref, scores, hkv: int, score_rows, num_seqs: int, name="scores"):
-    if scores.dim() != 3 or scores.shape[1] != hkv or scores.dtype != torch.float32 or scores.device != ref.device:
-        raise ValueError(f"{name} is fp32 [rows, kv_heads, length] on {ref.device}")
-    if score_rows is not None:
-        _check_index(ref, "score_rows", score_rows, num_seqs)
-    elif scores.shape[0] < num_seqs:
-        raise ValueError(f"{name} has fewer rows than there are requests")
+@functools.lru_cache(maxsize=4096)
+def _accumulate_workspace(dev, *sizes) -> int:  # dev: the choice depends on the current device
+    return decode_accumulate_workspace_size(*sizes)
 
 
 def decode_accumulate(q, k_cache, v_cache, block_tables, context_lens, scale, scores, score_rows=None,
@@ -620,30 +682,38 @@ def decode_accumulate(q, k_cache, v_cache, block_tables, context_lens, scale, sc
     """pa_decode_accumulate: :func:`decode`, and each cached token's attention weight (summed over the query heads of
     its KV head) added to its score.  ``scores``: fp32 [rows, kv_heads, length], request r's row is ``score_rows[r]``
     (None: r; negative: no score).  ``scores_out`` None: in place.  Returns (out, scores_out)."""
-    nb, bs, hkv, d = _cache_dims(k_cache)
-    if out is None:
-        out = torch.empty_like(q)
-    _check_decode(q, k_cache, v_cache, block_tables, context_lens, out)
-    B, hq, _ = q.shape
+    dtype, dev = q.dtype, q.get_device()
+    kc, vc = _cache_ptrs(k_cache, v_cache, dev)
+    nb, bs, hkv, d = k_cache.shape
+    if q.dim() != 3 or q.shape[2] != d:
+        raise ValueError("q is [num_seqs, q_heads, head_dim] of the cache's head_dim")
+    qshape = B, hq, _ = q.shape
+    if k_cache.dtype != dtype or (out is not None and out.dtype != dtype):
+        raise TypeError(f"q ({dtype}), the caches ({k_cache.dtype}) and out must share a dtype")
+    tables = _table_ptr(block_tables, dev, B)
+    lens = _rows_ptr(context_lens, "context_lens", dev, B)
+    sc, rows = _score_ptrs(scores, hkv, score_rows, B, dev)
+    so = sc
     if scores_out is None:
         scores_out = scores
-    _check_scores(q, scores, hkv, score_rows, B)
-    if scores_out.shape != scores.shape:
-        raise ValueError("scores_out must have scores' shape")
-    _check_scores(q, scores_out, hkv, score_rows, B, "scores_out")
-    _check_current(q)
-    maxblk = int(block_tables.shape[1])
+    else:
+        if scores_out.shape != scores.shape:
+            raise ValueError("scores_out must have scores' shape")
+        so, _ = _score_ptrs(scores_out, hkv, None, 0, dev, "scores_out")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != qshape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, q {tuple(qshape)}")
+    handle = _stream_on(dev, stream)
+    maxblk, split_tokens = block_tables.shape[1], int(split_tokens)
     if workspace is None:
-        n = decode_accumulate_workspace_size(B, hq, hkv, d, maxblk, bs, split_tokens)
+        n = _accumulate_workspace(dev, B, hq, hkv, d, maxblk, bs, split_tokens)
         workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
     _keep(out, workspace)
     _launch(
-        "pa_decode_accumulate", _dev(q, "q"), _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"),
-        _i32(block_tables, "block_tables"), maxblk, _i32(context_lens, "context_lens"), B, hq, hkv, d, bs, nb,
-        float(scale), int(split_tokens), _dev(scores, "scores"),
-        _i32(score_rows, "score_rows") if score_rows is not None else None, int(scores.shape[0]),
-        int(scores.shape[2]), _dev(scores_out, "scores_out"), workspace.data_ptr(),
-        workspace.numel() * workspace.element_size(), _dev(out, "out"), dtype_code(q.dtype), _stream(stream))
+        "pa_decode_accumulate", _ptr(q, "q", dev), kc, vc, tables, maxblk, lens, B, hq, hkv, d, bs, nb, float(scale),
+        split_tokens, sc, rows, scores.shape[0], scores.shape[2], so, _ptr(workspace, "workspace", dev),
+        workspace.numel() * workspace.element_size(), _ptr(out, "out", dev), dtype_code(dtype), handle)
     return out, scores_out
 
 
@@ -653,25 +723,26 @@ def evict_select(scores, context_lens, sink, heavy, recent, score_rows=None, kee
     keep_lens int32 [num_seqs])."""
     if scores.dim() != 3:
         raise ValueError("scores is fp32 [rows, kv_heads, length]")
-    B, hkv = int(context_lens.shape[0]), int(scores.shape[1])
-    _check_scores(scores, scores, hkv, score_rows, B)
-    _check_index(scores, "context_lens", context_lens, B)
-    if min(sink, heavy, recent) < 0 or sink + heavy + recent < 1:
+    dev = scores.get_device()
+    nrows, hkv, length = scores.shape
+    B = context_lens.shape[0]
+    lens = _rows_ptr(context_lens, "context_lens", dev, B)
+    sc, rows = _score_ptrs(scores, hkv, score_rows, B, dev)
+    sink, heavy, recent = int(sink), int(heavy), int(recent)
+    budget = sink + heavy + recent
+    if sink < 0 or heavy < 0 or recent < 0 or budget < 1:
         raise ValueError("sink, heavy and recent are counts, at least one token together")
-    budget = int(sink) + int(heavy) + int(recent)
     if keep is None:
         keep = torch.empty((B, hkv, budget), dtype=torch.int32, device=scores.device)
-    elif keep.shape != (B, hkv, budget) or keep.device != scores.device:
-        raise ValueError(f"keep is [{B}, {hkv}, {budget}] on {scores.device}")
+    elif keep.shape != (B, hkv, budget):
+        raise ValueError(f"keep is int32 [{B}, {hkv}, {budget}]")
     if keep_lens is None:
         keep_lens = torch.empty(B, dtype=torch.int32, device=scores.device)
-    _check_index(scores, "keep_lens", keep_lens, B)
-    _check_current(scores)
+    handle = _stream_on(dev, stream)
     _keep(keep, keep_lens)
     _launch(
-        "pa_evict_select", _dev(scores, "scores"), _i32(score_rows, "score_rows") if score_rows is not None else None,
-        int(scores.shape[0]), hkv, int(scores.shape[2]), _i32(context_lens, "context_lens"), B, int(sink), int(heavy),
-        int(recent), _i32(keep, "keep"), _i32(keep_lens, "keep_lens"), _stream(stream))
+        "pa_evict_select", sc, rows, nrows, hkv, length, lens, B, sink, heavy, recent,
+        _rows_ptr(keep, "keep", dev, B), _rows_ptr(keep_lens, "keep_lens", dev, B), handle)
     return keep, keep_lens
 
 
@@ -680,31 +751,31 @@ def compact_kv(k_cache, v_cache, block_tables, context_lens, keep, keep_lens, ba
     """pa_compact_kv: token ``base[r] + i`` of each sequence becomes its token ``base[r] + keep[r, g, i]``, in place
     (``keep``: int32 [num_seqs, 1 or kv_heads, max_keep], ``i <= keep[i]``); with ``scores``, those too, and zeros
     behind them."""
-    nb, bs, hkv, d = _cache_dims(k_cache)
-    _check_caches(k_cache, v_cache)
-    B = int(context_lens.shape[0])
-    _check_index(k_cache, "block_tables", block_tables, B, table=True)
-    _check_index(k_cache, "context_lens", context_lens, B)
-    if keep.dim() != 3 or keep.shape[0] != B or keep.shape[1] not in (1, hkv) or keep.device != k_cache.device:
-        raise ValueError("keep is int32 [num_seqs, 1 or kv_heads, max_keep] on the cache's device")
-    _check_index(k_cache, "keep_lens", keep_lens, B)
-    if base is not None:
-        _check_index(k_cache, "base", base, B)
+    dev = k_cache.get_device()
+    kc, vc = _cache_ptrs(k_cache, v_cache, dev)
+    nb, bs, hkv, d = k_cache.shape
+    B = context_lens.shape[0]
+    tables = _table_ptr(block_tables, dev, B)
+    lens = _rows_ptr(context_lens, "context_lens", dev, B)
+    kshape = keep.shape
+    if len(kshape) != 3 or kshape[1] not in (1, hkv):
+        raise ValueError("keep is int32 [num_seqs, 1 or kv_heads, max_keep]")
+    lists = _rows_ptr(keep, "keep", dev, B)
+    nkeep = _rows_ptr(keep_lens, "keep_lens", dev, B)
+    first = _rows_ptr(base, "base", dev, B) if base is not None else None
+    sc = rows = None
+    nrows = length = 0
     if scores is not None:
-        _check_scores(k_cache, scores, hkv, score_rows, B)
-    _check_current(k_cache)
-    if keep.shape[2] == 0:
+        sc, rows = _score_ptrs(scores, hkv, score_rows, B, dev)
+        nrows, _, length = scores.shape
+    handle = _stream_on(dev, stream)
+    if kshape[2] == 0:
         if scores is not None:
             raise ValueError("keep has no entries")
         return
-    with_rows = scores is not None and score_rows is not None
     _launch(
-        "pa_compact_kv", _dev(k_cache, "k_cache"), _dev(v_cache, "v_cache"), _i32(block_tables, "block_tables"),
-        int(block_tables.shape[1]), _i32(context_lens, "context_lens"), _i32(keep, "keep"), int(keep.shape[1]),
-        int(keep.shape[2]), _i32(keep_lens, "keep_lens"), _i32(base, "base") if base is not None else None, B, nb, bs,
-        hkv, d, dtype_code(k_cache.dtype), _dev(scores, "scores") if scores is not None else None,
-        _i32(score_rows, "score_rows") if with_rows else None, int(scores.shape[0]) if scores is not None else 0,
-        int(scores.shape[2]) if scores is not None else 0, _stream(stream))
+        "pa_compact_kv", kc, vc, tables, block_tables.shape[1], lens, lists, kshape[1], kshape[2], nkeep, first, B, nb,
+        bs, hkv, d, dtype_code(k_cache.dtype), sc, rows, nrows, length, handle)
 
 
 def selftest_wait_timeout(wait_ms: int = 50, stream=None) -> None:
