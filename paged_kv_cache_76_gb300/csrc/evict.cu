@@ -372,11 +372,12 @@ struct MoveRange {
   int base, n, L;
 };
 
-// The request's range, checked; false: nothing is moved.
+// The request's range, checked; false: nothing is moved.  PAST_L1: see compact_scores_kernel.
+template <bool PAST_L1 = false>
 __device__ __forceinline__ bool move_range(const CompactParams& p, int r, MoveRange& m, bool report) {
-  m.L = p.lens[r];
-  m.n = p.keep_lens[r];
-  m.base = p.base ? p.base[r] : 0;
+  m.L = PAST_L1 ? __ldcg(p.lens + r) : p.lens[r];
+  m.n = PAST_L1 ? __ldcg(p.keep_lens + r) : p.keep_lens[r];
+  m.base = !p.base ? 0 : PAST_L1 ? __ldcg(p.base + r) : p.base[r];
   if (m.L < 0 || m.L > p.cap) {
     if (report) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
     return false;
@@ -508,9 +509,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) compact_kv_kernel(con
 // alone take 14 us for the zeros of a context of 131000.
 constexpr int kScoreThreads = 256;
 
-__global__ void __launch_bounds__(kScoreThreads) compact_scores_kernel(const CompactParams p) {
-  griddep_wait();
-  griddep_launch_dependents();
+__device__ __forceinline__ void move_scores(const CompactParams& p) {
   const int C = (int)cluster_size(), rank = (int)cluster_rank();
   const int r = blockIdx.y, g = blockIdx.x / C, tid = threadIdx.x;
   auto meet = [&] {
@@ -518,12 +517,12 @@ __global__ void __launch_bounds__(kScoreThreads) compact_scores_kernel(const Com
     else cluster_sync();
   };
   MoveRange m;
-  if (!move_range(p, r, m, false)) return;  // reported by the rows' kernel
-  const int row = p.score_rows ? p.score_rows[r] : r;
+  if (!move_range<true>(p, r, m, false)) return;  // reported by the rows' kernel
+  const int row = p.score_rows ? __ldcg(p.score_rows + r) : r;
   if (row < 0) return;
   bool twice = false;  // an earlier request has this row: its alone are moved
   if (p.score_rows)
-    for (int i = tid; i < r; i += kScoreThreads) twice |= p.score_rows[i] == row;
+    for (int i = tid; i < r; i += kScoreThreads) twice |= __ldcg(p.score_rows + i) == row;
   const bool bad = __syncthreads_or(twice) || row >= p.num_rows;
   if (bad || m.L > p.score_len) {
     if (tid == 0) record_error(p.err, bad ? PA_DEVERR_SCORE_ROW : PA_DEVERR_CONTEXT_LEN);
@@ -540,12 +539,12 @@ __global__ void __launch_bounds__(kScoreThreads) compact_scores_kernel(const Com
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int64_t i = i0 + u * kScoreThreads;
-      src[u] = i < m.n ? keep[i] : -1;
+      src[u] = i < m.n ? __ldcg(keep + i) : -1;
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (src[u] < i0 + u * kScoreThreads || src[u] >= room) src[u] = -1;
-      if (src[u] >= 0) x[u] = sc[src[u]];
+      if (src[u] >= 0) x[u] = __ldcg(sc + src[u]);
     }
     meet();  // all loads of the step before its stores
 #pragma unroll
@@ -561,6 +560,17 @@ __global__ void __launch_bounds__(kScoreThreads) compact_scores_kernel(const Com
   for (int64_t i = t0; i < vecs; i += C * kScoreThreads)
     reinterpret_cast<float4*>(sc + n4)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (t0 < room - n4 - 4 * vecs) sc[n4 + 4 * vecs + t0] = 0.f;
+}
+
+// Runs beside the rows' kernel, with which it shares nothing that either
+// writes: it starts when every CTA of that kernel has started (and so has
+// waited for all that came before), and waits for its end before its own, so
+// that what follows finds both done (8 lists of 8192: 101 us for both, 109 one
+// after the other; one list 20 and 25).  Its loads go past L1, whose lines may be
+// older than that.
+__global__ void __launch_bounds__(kScoreThreads) compact_scores_kernel(const CompactParams p) {
+  move_scores(p);
+  griddep_wait();
 }
 
 // Lists of at most kMoveSmall entries (a tree's accepted path): a CTA takes a
