@@ -652,10 +652,14 @@ __global__ void __launch_bounds__(256) lse_merge_warp_kernel(const MergeParams p
 // are under way: each thread takes the logits of 16 / GP tokens at a time, and
 // its first ones while the CTA works out M and W.  A CTA takes p.chunk tokens,
 // enough that the partials it reads for M and W stay below a quarter of its
-// logits.  Measured on GB300: the whole call 107 us where pa_decode takes 91 (64
-// requests of 532..4027 tokens, 32/8 heads), 510 where it takes 421 (8 of
-// 44..128 thousand, 64/8 heads: 168 MB of logits written and read); 4 requests
-// of <= 1500 tokens 9.4.  8 logits a thread (more, smaller CTAs): 112 and 519.
+// logits.  Measured on GB300: the whole call 104 us where pa_decode takes 91 (64
+// requests of 532..4027 tokens, 32/8 heads), 506 where it takes 421 (8 of
+// 44..128 thousand, 64/8 heads: 175 MB of logits written and read); 4 requests
+// of <= 1500 tokens 8.8.  Of that 64 registers (1024 threads an SM instead of
+// 768) bring 1.4 and 1, four partitions of a lane side by side 0.4 and 5.  8
+// logits a thread (more, smaller CTAs): 112 and 519; the next tokens' loads
+// before these tokens' sums: 109 and 527; the last requests' logits first,
+// since they are in L2: no difference.
 constexpr int kMaxGroup = 16;
 
 // GP: floats between tokens (the group rounded up to 1, 2 or a multiple of 4).
@@ -710,17 +714,29 @@ __device__ __forceinline__ void add_weights(const AccumulateParams& p, int part)
     // largest reference of its own and its sum brought to that, then the warp's
     const size_t prow = ((size_t)r * p.q_heads + h * G + (g < G ? g : 0)) * p.max_splits;
     float m = -INFINITY, l = 0.f;
-    for (int c = lane; c < nsplit; c += 32) {
-      const float mc = p.part_m[prow + c], wc = p.part_w[prow + c];
-      const float mn = fmaxf(m, mc);
-      if (mn != -INFINITY) l = l * exp2f(m - mn) + wc * exp2f(mc - mn);
+    constexpr int P = 4;  // partitions of a lane side by side
+    for (int c0 = lane; c0 < nsplit; c0 += 32 * P) {
+      float mc[P], wc[P], mn = m;
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        const int c = c0 + 32 * i;
+        mc[i] = c < nsplit ? p.part_m[prow + c] : -INFINITY;
+        wc[i] = c < nsplit ? p.part_w[prow + c] : 0.f;
+      }
+#pragma unroll
+      for (int i = 0; i < P; ++i) mn = fmaxf(mn, mc[i]);
+      if (mn != -INFINITY) {
+        l *= ex2_approx(m - mn);
+#pragma unroll
+        for (int i = 0; i < P; ++i) l += wc[i] * ex2_approx(mc[i] - mn);
+      }
       m = mn;
     }
     float M = m;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
     if (M == -INFINITY) M = 0.f;
-    l *= exp2f(m - M);
+    l *= ex2_approx(m - M);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
@@ -742,7 +758,7 @@ __device__ __forceinline__ void add_weights(const AccumulateParams& p, int part)
         float w = 0.f;
 #pragma unroll
         for (int g = 0; g < GP; ++g)
-          if (g < G) w += exp2f(x[u][g] - s_m[g]) * s_inv[g];
+          if (g < G) w += ex2_approx(x[u][g] - s_m[g]) * s_inv[g];
         p.scores_out[at + t] = old[u] + w;
       }
     }
@@ -751,7 +767,7 @@ __device__ __forceinline__ void add_weights(const AccumulateParams& p, int part)
 
 // THREADS 256: a warp per row (at most 32 partitions); 128: the CTA per row.
 template <int D, typename T, int THREADS>
-__global__ void __launch_bounds__(THREADS)
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
     merge_accumulate_kernel(const MergeParams mp, const AccumulateParams ap, int merge_ctas) {
   griddep_wait();
   griddep_launch_dependents();
