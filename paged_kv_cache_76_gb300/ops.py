@@ -531,7 +531,10 @@ def _token_rows(t: torch.Tensor, name: str, heads: int, d: int, dtype, dev: int)
     return stride
 
 
-_Sections = C.c_int32 * 3
+@functools.lru_cache(maxsize=256)
+def _sections(counts):
+    """(the C array, the counts' sum, the smallest)"""
+    return (C.c_int32 * 3)(*counts), sum(counts), min(counts)
 
 
 def norm_rope_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight=None, k_weight=None,
@@ -563,10 +566,10 @@ def norm_rope_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
     if sections is None:
         if axes > 1:
             raise ValueError("several axes need their sections")
-    elif len(sections) != axes or min(sections) < 0 or sum(sections) != rot // 2:
-        raise ValueError(f"sections are {axes} counts of pairs, rot_dim / 2 = {rot // 2} together")
     else:
-        sec = _Sections(*sections)
+        sec, pairs, least = _sections(tuple(sections)) if len(sections) == axes else (None, -1, -1)
+        if least < 0 or pairs != rot // 2:
+            raise ValueError(f"sections are {axes} counts of pairs, rot_dim / 2 = {rot // 2} together")
     qw = kw = None
     if q_weight is not None:
         if q_weight.shape != (d,) or q_weight.dtype != dtype:
