@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         if (ok && !issue_pv(gt - 1, w.ntiles - 1)) ok = false;  // the unit's last P.V
+        if constexpr (TREE) break;  // one unit per CTA
       }
       if (!ok && lane == 0) record_error(p.err, PA_DEVERR_TIMEOUT);
       tc_commit_warp(bar(B_MMADONE));
@@ -684,6 +685,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       tc_fence_before();  // O_x read out before the next unit's P.V overwrites it
+      if constexpr (TREE) break;
     }
     if (lane == 0 && !ok) record_error(p.err, PA_DEVERR_TIMEOUT);
   }

@@ -556,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (u < nunits) {
       stage_q(w);
       q_to_tmem();
-      un = next_unit(u + nctas, wn, false);
+      un = TREE ? nunits : next_unit(u + nctas, wn, false);
       if (un < nunits) stage_q(wn);  // in flight during this unit
     }
     while (ok && u < nunits) {
@@ -868,6 +868,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();  // O read out before the next unit's first P.V overwrites it
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_OFREE));
+      // one unit per CTA: without the next one's state 118 to 168 registers and
+      // no spills (8 long requests 470 -> 460 us, 4 short ones 13.3 -> 11.5)
+      if constexpr (TREE) break;
       u = un;
       w = wn;
       if (u < nunits) {
