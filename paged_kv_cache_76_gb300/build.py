@@ -1,17 +1,23 @@
 """Build ``libpa.so`` (the C ABI of ``include/pa.h``) in-tree for sm_103a.
 
 Each translation unit is compiled by nvcc in parallel, then linked into one
-shared library with the CUDA runtime linked statically.  Only sources or
-headers newer than their object are rebuilt.  Run ``python -m
+shared library with the CUDA runtime linked statically.  Beside it, ``_marshal``
+(``csrc/marshal.cpp``), the Python extension that passes torch tensors to some
+of its functions, is compiled by g++ against the installed torch and Python;
+without their headers it is left out and the calls take the longer way through
+ctypes.  Only sources or headers newer than their object are rebuilt.  Run ``python -m
 paged_kv_cache_76_gb300.build [--force] [--verbose]``.
 """
 from __future__ import annotations
 
 import argparse
+import importlib.metadata
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 HERE = os.path.dirname(os.path.abspath(__file__))
@@ -22,6 +28,8 @@ OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpa.so")
 SOURCES = ["pa_api.cu", "decode.cu", "prefill.cu", "cache_ops.cu", "block_alloc.cpp", "decode_noalloc.cu", "attn_tc.cu",
            "attn_tile.cu", "vkv.cpp", "rope.cu", "evict.cu", "tree.cu"]
+MARSHAL = os.path.join(HERE, "_marshal" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
+MARSHAL_STAMP = os.path.join(OBJDIR, "marshal.stamp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -45,10 +53,38 @@ def _stale(obj: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _marshal_job(nvcc: str, force: bool):
+    """(command, stamp) that compiles _marshal, or None: up to date, or torch's or Python's headers are missing."""
+    spec = importlib.util.find_spec("torch")
+    cxx = shutil.which(os.environ.get("CXX", "g++"))
+    if spec is None or not spec.submodule_search_locations or cxx is None:
+        return None
+    torch_dir = spec.submodule_search_locations[0]
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
+           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
+           os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")]
+    if not os.path.exists(os.path.join(inc[1], "Python.h")) or not os.path.isdir(inc[2]):
+        return None
+    src = os.path.join(CSRC, "marshal.cpp")
+    # built for one torch and one Python: another of either is another build
+    stamp = f"torch {importlib.metadata.version('torch')} python {sys.version}"
+    try:
+        with open(MARSHAL_STAMP) as f:
+            same = f.read() == stamp
+    except OSError:
+        same = False
+    if not force and same and not _stale(MARSHAL, [src, os.path.join(INCLUDE, "pa.h")]):
+        return None
+    lib = os.path.join(torch_dir, "lib")
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared"] + [x for i in inc for x in ("-I", i)] + [src, "-o", MARSHAL]
+    return cmd + ["-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], stamp
+
+
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link; returns the path of libpa.so."""
     nvcc = _nvcc()
     os.makedirs(OBJDIR, exist_ok=True)
+    marshal = _marshal_job(nvcc, force)
     headers = _headers()
     common = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
     jobs = []
@@ -69,13 +105,17 @@ def build(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
-    if jobs:
-        with ThreadPoolExecutor(max_workers=min(len(jobs), os.cpu_count() or 4)) as ex:
-            for cmd, r in ex.map(run, jobs):
+    every = jobs + ([marshal[0]] if marshal else [])
+    if every:
+        with ThreadPoolExecutor(max_workers=min(len(every), os.cpu_count() or 4)) as ex:
+            for cmd, r in ex.map(run, every):
                 if verbose or r.returncode:
                     sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
                 if r.returncode:
-                    raise RuntimeError(f"nvcc failed on {cmd[-3]}")
+                    raise RuntimeError("failed: compiling " + next(a for a in cmd if a.startswith(CSRC + os.sep)))
+    if marshal:
+        with open(MARSHAL_STAMP, "w") as f:
+            f.write(marshal[1])
     if force or jobs or _stale(LIB, objs):
         cmd = [nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", LIB] + objs
         r = subprocess.run(cmd, capture_output=True, text=True)

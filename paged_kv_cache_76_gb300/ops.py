@@ -3,12 +3,15 @@
 Every function passes ``data_ptr()`` values, sizes and the current CUDA
 stream to the function of the same name in ``include/pa.h``; all work runs in
 the library's kernels.  Tensors must be contiguous CUDA tensors of the
-documented shapes; int32 index tensors live on the same device.
+documented shapes; int32 index tensors live on the same device.  Calls that
+take microseconds on the GPU go through the extension of csrc/marshal.cpp when
+they are regular, which does the same in a third of the host time.
 """
 from __future__ import annotations
 
 import ctypes as C
 import functools
+import importlib
 import math
 import threading
 
@@ -101,6 +104,36 @@ class recording:
     def __exit__(self, *exc):
         _tls.rec = None
         return False
+
+
+# The functions of csrc/marshal.cpp: what they take, they check, allocate and
+# launch; None from them means that the call is not of the regular kind, and
+# nothing was done.
+_SHORT = ("pa_norm_rope_and_cache", "pa_verify_tree_workspace_size", "pa_verify_tree",
+          "pa_decode_accumulate_workspace_size", "pa_decode_accumulate", "pa_evict_select", "pa_compact_kv")
+_marshal = None  # the module; False: not built
+
+
+def _load_marshal():
+    global _marshal
+    try:
+        lib = _lib.lib()
+    except _lib.LibraryMissing:  # the long way says so
+        return False
+    try:
+        m = importlib.import_module("._marshal", __package__)
+        m.bind(*(C.cast(getattr(lib, name), C.c_void_p).value for name in _SHORT))
+        _marshal = m
+    except ImportError:
+        _marshal = False
+    return _marshal
+
+
+def _short_way(stream):
+    """May this call go through _marshal?  (A recording wants the marshalled C call.)"""
+    if stream is not None or getattr(_tls, "rec", None) is not None:
+        return False
+    return _marshal if _marshal is not None else _load_marshal()
 
 
 def _keep(*tensors) -> None:
@@ -544,6 +577,13 @@ def norm_rope_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
 
     ``q``/``k``/``v`` may be views of one projection's rows.  ``positions``: int32 [num_tokens], or
     [axes, num_tokens] with ``sections`` (pairs per axis).  ``out`` may be ``q`` if that is contiguous."""
+    if _short_way(stream):
+        r = _marshal.norm_rope(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps,
+                               sections, interleaved, out)
+        if r is not None:
+            if type(r) is int:
+                check(r, "pa_norm_rope_and_cache")
+            return r
     dtype, dev = k_cache.dtype, k_cache.get_device()
     kc, vc = _cache_ptrs(k_cache, v_cache, dev)
     nb, bs, hkv, d = k_cache.shape
@@ -626,6 +666,13 @@ def verify_tree(q, q_start, tree_mask, context_lens, k_cache, v_cache, block_tab
                 split_tokens=0, workspace=None, stream=None):
     """pa_verify_tree: ``q`` is [total_q, q_heads, head_dim], packed by ``q_start``; bit m of ``tree_mask[i]`` (int64)
     lets row i see its request's node m.  Every row sees the context before the draft."""
+    if workspace is None and _short_way(stream):
+        r = _marshal.verify_tree(q, q_start, tree_mask, context_lens, k_cache, v_cache, block_tables, scale, max_q_len,
+                                 out, split_tokens)
+        if r is not None:
+            if type(r) is int:
+                check(r, "pa_verify_tree")
+            return r
     dtype, dev = q.dtype, q.get_device()
     kc, vc = _cache_ptrs(k_cache, v_cache, dev)
     nb, bs, hkv, d = k_cache.shape
@@ -685,6 +732,13 @@ def decode_accumulate(q, k_cache, v_cache, block_tables, context_lens, scale, sc
     """pa_decode_accumulate: :func:`decode`, and each cached token's attention weight (summed over the query heads of
     its KV head) added to its score.  ``scores``: fp32 [rows, kv_heads, length], request r's row is ``score_rows[r]``
     (None: r; negative: no score).  ``scores_out`` None: in place.  Returns (out, scores_out)."""
+    if workspace is None and _short_way(stream):
+        r = _marshal.decode_accumulate(q, k_cache, v_cache, block_tables, context_lens, scale, scores, score_rows,
+                                       scores_out, out, split_tokens)
+        if r is not None:
+            if type(r) is int:
+                check(r, "pa_decode_accumulate")
+            return r
     dtype, dev = q.dtype, q.get_device()
     kc, vc = _cache_ptrs(k_cache, v_cache, dev)
     nb, bs, hkv, d = k_cache.shape
@@ -724,6 +778,12 @@ def evict_select(scores, context_lens, sink, heavy, recent, score_rows=None, kee
     """pa_evict_select: per request and KV head the tokens a budget of ``sink + heavy + recent`` keeps, ascending:
     the first, the last, and the best scored between.  Returns (keep int32 [num_seqs, kv_heads, budget], -1 behind;
     keep_lens int32 [num_seqs])."""
+    if keep is None and keep_lens is None and _short_way(stream):
+        r = _marshal.evict_select(scores, context_lens, sink, heavy, recent, score_rows)
+        if r is not None:
+            if type(r) is int:
+                check(r, "pa_evict_select")
+            return r
     if scores.dim() != 3:
         raise ValueError("scores is fp32 [rows, kv_heads, length]")
     dev = scores.get_device()
@@ -754,6 +814,11 @@ def compact_kv(k_cache, v_cache, block_tables, context_lens, keep, keep_lens, ba
     """pa_compact_kv: token ``base[r] + i`` of each sequence becomes its token ``base[r] + keep[r, g, i]``, in place
     (``keep``: int32 [num_seqs, 1 or kv_heads, max_keep], ``i <= keep[i]``); with ``scores``, those too, and zeros
     behind them."""
+    if _short_way(stream):
+        r = _marshal.compact_kv(k_cache, v_cache, block_tables, context_lens, keep, keep_lens, base, scores, score_rows)
+        if r is not None:
+            check(r, "pa_compact_kv")
+            return
     dev = k_cache.get_device()
     kc, vc = _cache_ptrs(k_cache, v_cache, dev)
     nb, bs, hkv, d = k_cache.shape
