@@ -51,7 +51,8 @@ struct Call {
 
   const at::Tensor* tensor(PyObject* o) {
     if (!need(THPVariable_CheckExact(o))) return nullptr;
-    return &THPVariable_Unpack(o);
+    const at::Tensor* t = &THPVariable_Unpack(o);
+    return need(t->defined() && t->layout() == at::kStrided) ? t : nullptr;
   }
   // the tensor that names the device
   const at::Tensor* first(PyObject* o) {
@@ -149,6 +150,17 @@ bool run(F&& f) {
   return done;
 }
 
+// A result's object; nullptr with an error set.  (The work is under way by
+// then: no going the long way any more.)
+PyObject* give(const at::Tensor& t) {
+  try {
+    return THPVariable_Wrap(t);
+  } catch (...) {
+    if (!PyErr_Occurred()) PyErr_NoMemory();
+    return nullptr;
+  }
+}
+
 // (q, k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps, sections, interleaved, out)
 PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   if (n != 14) Py_RETURN_NONE;
@@ -215,7 +227,7 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
       }))
     Py_RETURN_NONE;
   if (st != PA_OK) return PyLong_FromLong(st);
-  return mine ? THPVariable_Wrap(out) : Py_NewRef(a[13]);
+  return mine ? give(out) : Py_NewRef(a[13]);
 }
 
 // (q, q_start, tree_mask, context_lens, k_cache, v_cache, block_tables, scale, max_q_len, out, split_tokens)
@@ -252,7 +264,7 @@ PyObject* verify_tree(PyObject*, PyObject* const* a, Py_ssize_t n) {
       }))
     Py_RETURN_NONE;
   if (st != PA_OK) return PyLong_FromLong(st);
-  return mine ? THPVariable_Wrap(out) : Py_NewRef(a[9]);
+  return mine ? give(out) : Py_NewRef(a[9]);
 }
 
 // (q, k_cache, v_cache, block_tables, context_lens, scale, scores, score_rows, scores_out, out, split_tokens)
@@ -296,7 +308,7 @@ PyObject* decode_accumulate(PyObject*, PyObject* const* a, Py_ssize_t n) {
       }))
     Py_RETURN_NONE;
   if (st != PA_OK) return PyLong_FromLong(st);
-  PyObject* o = mine ? THPVariable_Wrap(out) : Py_NewRef(a[9]);
+  PyObject* o = mine ? give(out) : Py_NewRef(a[9]);
   if (!o) return nullptr;
   PyObject* r = PyTuple_Pack(2, o, sout);
   Py_DECREF(o);
@@ -327,7 +339,7 @@ PyObject* evict_select(PyObject*, PyObject* const* a, Py_ssize_t n) {
       }))
     Py_RETURN_NONE;
   if (st != PA_OK) return PyLong_FromLong(st);
-  PyObject *k = THPVariable_Wrap(keep), *l = THPVariable_Wrap(keep_lens);
+  PyObject *k = give(keep), *l = k ? give(keep_lens) : nullptr;
   PyObject* r = k && l ? PyTuple_Pack(2, k, l) : nullptr;
   Py_XDECREF(k);
   Py_XDECREF(l);
@@ -380,8 +392,20 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   Py_RETURN_NONE;
 }
 
+// What a tensor's own checks throw (one without storage, a wrapper) is the long
+// way's to refuse; nothing has been launched by then.
+template <PyObject* (*F)(PyObject*, PyObject* const*, Py_ssize_t)>
+PyObject* guarded(PyObject* self, PyObject* const* a, Py_ssize_t n) {
+  try {
+    return F(self, a, n);
+  } catch (...) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+}
+
 #define PA_METHOD(name) \
-  {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(name)), METH_FASTCALL, nullptr}
+  {#name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(guarded<name>)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {PA_METHOD(bind),
                          PA_METHOD(norm_rope),
                          PA_METHOD(verify_tree),

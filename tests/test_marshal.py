@@ -100,6 +100,19 @@ def test_what_is_on_the_host_is_left_to_the_long_way(name, taken):
     assert not any(taken)
 
 
+@pytest.mark.parametrize("name", NAMES)
+def test_tensors_that_are_not_plain_are_left_to_the_long_way(name, taken):
+    """Sparse and meta tensors, which have no storage to point at, and objects that are none."""
+    f, kw = calls("cpu")[name]
+    for key, t in kw.items():
+        if not isinstance(t, torch.Tensor):
+            continue
+        for w in (t.to_sparse(), t.to("meta"), t.cpu().numpy() if t.dtype != BF else [1], object()):
+            with pytest.raises((ValueError, TypeError, AttributeError, RuntimeError, NotImplementedError)):
+                f(**{**kw, key: w})
+    assert not any(taken)
+
+
 @pytest.mark.gpu
 @pytest.mark.parametrize("name", NAMES)
 def test_both_ways_give_the_same_bits(name, taken, monkeypatch):
@@ -160,9 +173,10 @@ def test_refusals_are_the_long_ways(name, taken):
             wrong = wrong[:2]
         if key in ("scores",):
             wrong = wrong[:2]                                    # more rows than requests are fine
+        wrong.append(t.to_sparse())
         if not (name == "norm_rope" and key in ("q", "k", "v")):
             wrong.append(torch.stack([t, t], -1)[..., 0])        # not contiguous
         for w in wrong:
-            with pytest.raises((ValueError, TypeError, PAError)):
+            with pytest.raises((ValueError, TypeError, RuntimeError, NotImplementedError, PAError)):
                 f(**{**kw, key: w})
     assert not any(taken) and ops.launch_count() == before
