@@ -1128,6 +1128,7 @@ namespace {
 constexpr int kTreeMaxNodes = 64;    // one mask word per node
 constexpr int kTreeSplitUnit = 128;  // partitions are whole key tiles
 constexpr int kTreeSplitMin = 256;
+constexpr int kTreeSplitLong = 4096;  // a short partition; above it, they are cut for balance
 
 struct TreeSetup {
   int split, max_splits;
@@ -1150,17 +1151,29 @@ int tree_setup(int num_reqs, int total_q, int max_q_len, int q_heads, int kv_hea
     // per row) then cost more than the balance brings.  Measured on GB300, 64
     // requests of <= 4096 tokens, 8 KV heads: whole 132 us, 2048-token
     // partitions 153 us (80..128 rows); 162 and 190 us (104..240 rows); whole
-    // and in order of length 127 and 143.  Fewer
-    // units are cut into about four per SM, but no smaller than the partials
-    // are worth (twice the rows): 8 contexts of 33..131 thousand tokens, 128
-    // rows: 65536 tokens 649 us, 32768 568, 12288 462, 4096 507; one of 8060,
-    // 240 rows: 1024 tokens 25.7 us, 512 24.0, 256 37.8.
+    // and in order of length 127 and 143.  Fewer units are cut until seven SMs
+    // in eight have one, where a partition then is short: starting and ending
+    // it takes 6 to 8 us, as much as 800 tokens (us at that and at four per SM:
+    // a context of 8000, 32 rows 15 and 23; one of 32000, 64 rows 30 and 62,
+    // and 36 with a unit on nearly every SM; 8 of <= 4000, 64 rows 25 and 36).
+    // Long ones are cut into about four per SM, which evens out contexts of
+    // different lengths (8 of 33..131 thousand, 128 rows: 65536 tokens 649 us,
+    // 32768 568, 12288 462, 4096 507), but not below kTreeSplitLong (12 of <=
+    // 8000, 64 rows: 4096 tokens 45, 2048 50, 1280 56).  No
+    // partition is smaller than its partials are worth, twice the rows (one of
+    // 8060, 240 rows: 1024 tokens 25.7 us, 512 24.0, 256 37.8).
     const int64_t rows = (int64_t)max_q_len * (q_heads / kv_heads);
-    const int64_t units = (int64_t)num_reqs * kv_heads * (rows <= 128 ? 1 : (rows + 255) / 256);
+    int64_t units = (int64_t)num_reqs * kv_heads * (rows <= 128 ? 1 : (rows + 255) / 256);
     const int64_t sms = sm_count() > 0 ? sm_count() : 152;
     split = whole;
     if (units < 2 * sms) {
-      split = cap * (units > 0 ? units : 1) / (4 * sms);
+      units = units > 0 ? units : 1;
+      const int64_t most = sms * 7 / 8, parts = units < most ? most / units : 1;
+      split = (cap + parts - 1) / parts;
+      if (split > kTreeSplitLong) {
+        split = cap * units / (4 * sms);
+        if (split < kTreeSplitLong) split = kTreeSplitLong;
+      }
       split = split > 2 * rows ? split : 2 * rows;
       split = (split + kTreeSplitUnit - 1) / kTreeSplitUnit * kTreeSplitUnit;
       if (split < kTreeSplitMin) split = kTreeSplitMin;

@@ -146,7 +146,8 @@ def test_c_calls_check_sizes_and_pointers(lib):
     assert tree(R=0) == ok and tree(T=0) == ok
     assert lib.pa_verify_tree_split_tokens(64, 60, 32, 8, 256, 16, 0) == 4096       # enough units: whole contexts
     assert lib.pa_verify_tree_split_tokens(1, 60, 32, 8, 504, 16, 0) == 512         # few: twice the 240 rows
-    assert lib.pa_verify_tree_split_tokens(1, 4, 8, 8, 504, 16, 0) == 256
+    assert lib.pa_verify_tree_split_tokens(1, 4, 8, 8, 504, 16, 0) == 512           # a unit on seven SMs in eight
+    assert lib.pa_verify_tree_split_tokens(2, 4, 8, 8, 32, 16, 0) == 256            # the smallest
     assert lib.pa_verify_tree_split_tokens(1, 4, 8, 8, 504, 16, 200) == inv
     assert lib.pa_verify_tree_workspace_size(64, 640, 10, 32, 8, 128, 256, 16, 0) == 0
     assert lib.pa_verify_tree_workspace_size(1, 10, 10, 32, 8, 128, 256, 16, 512) >= 8 * 10 * 32 * 130 * 4
