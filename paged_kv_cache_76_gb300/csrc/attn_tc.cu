@@ -59,7 +59,7 @@
 // non-finite elements (tree.cuh).  A context may be cut into partitions of
 // split_tokens keys, a unit each, whose partials a merge combines.  A unit of
 // at most 128 rows leaves tile B alone: its issuer only frees the stages.
-// Blocks of 4 tokens (GATHER) are gathered without TMA (tree.cuh).
+// Blocks of 4 tokens (QUAD) come in boxes of half a swizzle atom (tree.cuh).
 #include <float.h>
 
 #include "pa_device.cuh"
@@ -198,7 +198,7 @@ __device__ __forceinline__ int tree_unit(const PrefillParams& p, const TreeParam
   return 0;
 }
 
-template <int D, int BSUB, typename T, bool TREE, bool GATHER>
+template <int D, int BSUB, typename T, bool TREE, bool QUAD>
 __global__ void __launch_bounds__(kThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                     const PrefillParams p, const TreeParams tp) {
@@ -255,11 +255,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kKStages; ++i) {
-      mbar_init(bar(B_KFULL + i), GATHER ? 32 : 1);
+      mbar_init(bar(B_KFULL + i), 1);
       mbar_init(bar(B_KEMPTY + i), 2);
     }
     for (int i = 0; i < kVStages; ++i) {
-      mbar_init(bar(B_VFULL + i), GATHER ? 32 : 1);
+      mbar_init(bar(B_VFULL + i), 1);
       mbar_init(bar(B_VEMPTY + i), 2);
     }
     for (int i = 0; i < 4; ++i) {
@@ -302,8 +302,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       TcUnit w;
       if (!unit(u, w) || w.ntiles <= 0) continue;
       const int32_t* trow = p.tables + (size_t)w.r * p.maxblk;
-      int ids = 0;  // GATHER: block ids of the next tile
-      if constexpr (GATHER) ids = gather4_ids(trow, w.k0, w.kend - w.k0);
+      int ids = 0;  // QUAD: block ids of the next tile
+      if constexpr (QUAD) ids = quad_ids(trow, w.k0, w.kend - w.k0);
       for (int j = 0; j < w.ntiles; ++j, ++gt) {
         const int s = gt % nst;
         if (gt >= nst && !mbar_wait(bar(empty0 + s), ((gt / nst) - 1) & 1)) {
@@ -312,10 +312,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const int ts = w.k0 + j * kKeys;
         const int nvalid = min(kKeys, w.kend - ts);
-        if constexpr (GATHER) {
-          gather4_tile<Tile, D, kKeys>(tp, isv ? tp.v_cache : tp.k_cache, ids, w.h, nvalid, base + s * Tile::BYTES,
-                                       bar(full0 + s));
-          ids = gather4_ids(trow, ts + kKeys, w.kend - ts - kKeys);
+        if constexpr (QUAD) {
+          quad_tile<Tile, kKeys>(tp, map, ids, w.h, nvalid, base + s * Tile::BYTES, bar(full0 + s), pol);
+          ids = quad_ids(trow, ts + kKeys, w.kend - ts - kKeys);
           continue;
         }
         const int nsub = (nvalid + BSUB - 1) / BSUB;
@@ -362,7 +361,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                                   mbar_wait(bar(B_VFULL + vst), (t / kVStages) & 1)))
           return false;
         tc_fence_after();
-        if constexpr (GATHER) fence_proxy_async_smem();  // the copies' writes before the MMAs' reads
         const uint32_t vb = vbase + vst * Tile::BYTES;
 #pragma unroll
         for (int kk = 0; kk < PSTEPS; ++kk) {
@@ -414,7 +412,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             break;
           }
           tc_fence_after();
-          if constexpr (GATHER) fence_proxy_async_smem();
           const uint32_t kb = kbase + sk * Tile::BYTES;
 #pragma unroll
           for (int ks = 0; ks < KSTEPS; ++ks) {
@@ -724,11 +721,11 @@ cudaError_t launch_tc_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const 
   return launch_pdl(kern, grid, dim3(kThreads), L::BYTES, stream, kmap, vmap, p, TreeParams{});
 }
 
-template <int D, int BSUB, typename T, bool GATHER = false>
+template <int D, int BSUB, typename T, bool QUAD = false>
 cudaError_t launch_tree_t(const CUtensorMap& kmap, const CUtensorMap& vmap, const PrefillParams& p,
                           const TreeParams& tp, cudaStream_t stream) {
   using L = TcSmem<D, BSUB>;
-  auto kern = attn_tc_kernel<D, BSUB, T, true, GATHER>;
+  auto kern = attn_tc_kernel<D, BSUB, T, true, QUAD>;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaGetDevice(&dev);

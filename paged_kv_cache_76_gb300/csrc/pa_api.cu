@@ -1235,7 +1235,6 @@ int pa_verify_tree(const void* q, const int32_t* q_start, const uint64_t* tree_m
   if (!err) return PA_ERR_CUDA;
   TreeParams p{};
   p.q = q;
-  p.k_cache = k_cache;
   p.v_cache = v_cache;
   p.q_start = q_start;
   p.mask = tree_mask;

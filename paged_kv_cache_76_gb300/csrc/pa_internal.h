@@ -219,8 +219,7 @@ cudaError_t launch_norm_rope(const NormRopeParams& p, int head_dim, pa_dtype dt,
 // Attention of drafted trees (pa_verify_tree).
 struct TreeParams {
   const void* q;
-  const void* k_cache;  // blocks of 4 tokens are gathered without tensor maps
-  const void* v_cache;  // ... and the rare nodes whose V is not finite
+  const void* v_cache;  // read beside its tensor map for the rare nodes whose V is not finite
   const int32_t* q_start;
   const uint64_t* mask;  // [total_q]
   const int32_t* lens;
