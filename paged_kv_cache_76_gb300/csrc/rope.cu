@@ -18,10 +18,10 @@
 //    The thread keeps its four cosines and sines for the item's heads.
 //  * The chain slot/position -> table row runs ahead of the items: positions
 //    two items, cosines one.
-// Measured on GB300, bf16, norms, 8192 tokens of 32/8 heads of 128 (205 MB): 36.1
-// us, 0.84 of the copy rate.  2 KB items, 2 stages, 4 CTAs of 8 warps an SM; 3
-// stages 39.7, 4 with 3 CTAs 38.1, 1 KB items 52, 4 KB 38 to 46.  The same from
-// registers, a CTA per token: 50.
+// Measured on GB300, bf16, norms, 8192 tokens of 32/8 heads of 128 (205 MB): 35.3
+// us, 0.86 of the copy rate.  2 KB items, 2 stages, 4 CTAs of 8 warps an SM; when
+// that took 36.1: 3 stages 39.7, 4 with 3 CTAs 38.1, 1 KB items 52, 4 KB 38 to 46.
+// The same from registers, a CTA per token: 50.
 #include "pa_device.cuh"
 #include "pa_internal.h"
 
@@ -39,7 +39,10 @@ struct Place {
   int slot, pos[3];
 };
 
-template <int D, typename T, bool INTER>
+// PARTIAL: rot_dim < D.  Elements behind it are passed on, not turned by nothing (0
+// times an infinite neighbour is NaN).  The case of the figures above takes 37.0 us
+// with that choice, so the whole rotation goes without.
+template <int D, typename T, bool INTER, bool PARTIAL>
 __global__ void __launch_bounds__(32 * kRopeMaxWarps, 4) norm_rope_kernel(const NormRopeParams p) {
   constexpr int LPH = D / 8;                       // threads per head row
   constexpr int GROUPS = 32 / LPH;                 // head rows side by side
@@ -56,7 +59,7 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, 4) norm_rope_kernel(const 
   __syncwarp();
   const int sub = lane % LPH, group = lane / LPH;
   const int half = p.rot_dim / 2;
-  const bool rotated = sub < p.rot_dim / 8;
+  const bool rotated = !PARTIAL || sub < p.rot_dim / 8;
   // this thread's two runs of four elements; behind rot_dim, eight neighbours
   const int lo = INTER || !rotated ? 8 * sub : 4 * sub;
   const int hi = INTER || !rotated ? 8 * sub + 4 : half + 4 * sub;
@@ -218,8 +221,8 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, 4) norm_rope_kernel(const 
           float za[4], zb[4];
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            za[i] = a[i] * c[i] - bb[i] * sn[i];
-            zb[i] = bb[i] * c[i] + a[i] * sn[i];
+            za[i] = rotated ? a[i] * c[i] - bb[i] * sn[i] : a[i];
+            zb[i] = rotated ? bb[i] * c[i] + a[i] * sn[i] : bb[i];
           }
           if (row < n) {
             T* to = dst + row * D;
@@ -241,10 +244,10 @@ __global__ void __launch_bounds__(32 * kRopeMaxWarps, 4) norm_rope_kernel(const 
   }
 }
 
-template <int D, typename T, bool INTER>
-cudaError_t launch_t(const NormRopeParams& p, cudaStream_t stream) {
+template <int D, typename T, bool INTER, bool PARTIAL>
+cudaError_t launch_rot(const NormRopeParams& p, cudaStream_t stream) {
   constexpr int HEADS = kItemBytes / (2 * D);
-  auto kern = norm_rope_kernel<D, T, INTER>;
+  auto kern = norm_rope_kernel<D, T, INTER, PARTIAL>;
   auto bytes = [](int warps) { return warps * kRopeStages * (kItemBytes + 8); };
   static bool attr_set[64] = {};
   int dev = 0;
@@ -262,6 +265,11 @@ cudaError_t launch_t(const NormRopeParams& p, cudaStream_t stream) {
   const int64_t want = (items + warps - 1) / warps, cap = 4 * sms;
   const unsigned grid = (unsigned)(warps == 2 || want < cap ? want : cap);
   return launch_pdl(kern, dim3(grid), dim3(32 * warps), bytes(warps), stream, p);
+}
+
+template <int D, typename T, bool INTER>
+cudaError_t launch_t(const NormRopeParams& p, cudaStream_t stream) {
+  return p.rot_dim < D ? launch_rot<D, T, INTER, true>(p, stream) : launch_rot<D, T, INTER, false>(p, stream);
 }
 
 }  // namespace

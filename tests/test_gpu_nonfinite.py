@@ -1,0 +1,68 @@
+"""Infinities and NaN in the operators over moved caches: they decide exactly
+the results that the formulas give them, and no others."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+INF, NAN = float("inf"), float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    from paged_kv_cache_76_gb300 import _lib
+    try:
+        _lib.lib()
+    except _lib.LibraryMissing:
+        from paged_kv_cache_76_gb300 import build
+        build.build()
+    torch.cuda.init()
+
+
+def ops():
+    from paged_kv_cache_76_gb300 import ops as o
+    return o
+
+
+def i32(*x):
+    return torch.tensor(x, dtype=torch.int32, device="cuda")
+
+
+def same(a, b):
+    """The same bits, any NaN equal to any other."""
+    bits = torch.int16 if a.element_size() == 2 else torch.int32
+    return bool(((a.view(bits) == b.view(bits)) | (a.isnan() & b.isnan())).all())
+
+
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("d,rot,dtype", [(128, 64, torch.bfloat16), (128, 16, torch.float16), (64, 48, torch.bfloat16)])
+def test_elements_that_are_not_rotated_stay_apart(d, rot, dtype, interleaved, norm):
+    """Behind rot_dim an element meets no other one: an infinity or a NaN there stays where it is (with a norm, the
+    row's infinite or NaN factor makes the finite ones 0 or NaN, by the formula); in a rotated pair it stays in it."""
+    g = torch.Generator(device="cuda").manual_seed(11)
+    T, hq, hkv, bs = 13, 5, 2, 16
+    q, k, v = (torch.randn(T, h, d, generator=g, device="cuda").to(dtype) for h in (hq, hkv, hkv))
+    for x in (q, k):
+        x[0, 0, rot], x[1, 1, rot + 5], x[2, 0, d - 1], x[3, 1, rot + 3] = INF, -INF, NAN, -0.0
+        x[4, 0, 3], x[5, 1, rot // 2 + 1] = INF, NAN   # in a pair
+    pos, slots = torch.arange(T, dtype=torch.int32, device="cuda") + 1, torch.arange(T, dtype=torch.int32, device="cuda")
+    table = ops().rope_table(50, rot, device="cuda")
+    kc, vc = (torch.zeros(2, bs, hkv, d, dtype=dtype, device="cuda") for _ in range(2))
+    w = torch.ones(d, dtype=dtype, device="cuda") if norm else None
+    out = ops().norm_rope_and_cache(q, k, v, pos, table, slots, kc, vc, q_weight=w, k_weight=w, interleaved=interleaved)
+    assert ops().get_device_error() == 0
+    lo, hi = (np.arange(0, rot, 2), np.arange(1, rot, 2)) if interleaved else (np.arange(rot // 2),
+                                                                                np.arange(rot // 2, rot))
+    c, s = table[pos.long(), None, :rot // 2], table[pos.long(), None, rot // 2:]
+    for x, got in ((q, out), (k, kc.flatten(0, 1)[:T])):
+        y = x.float()
+        if norm:
+            y = y * torch.rsqrt((y * y).mean(-1, keepdim=True) + 1e-6)
+        z = y.clone()
+        z[..., lo], z[..., hi] = y[..., lo] * c - y[..., hi] * s, y[..., hi] * c + y[..., lo] * s
+        assert torch.equal(got.isnan(), z.isnan()) and torch.equal(got.isinf(), z.isinf())
+        assert torch.equal(got[got.isinf()].float(), z[z.isinf()])
+        if not norm:
+            assert same(got[..., rot:], x[..., rot:])
