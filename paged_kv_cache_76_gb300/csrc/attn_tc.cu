@@ -573,8 +573,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < 8; ++c)
                 *reinterpret_cast<uint4*>(vrow + hf * Tile::HALF + c * 16) = make_uint4(0, 0, 0, 0);
           } else if (TREE && row < kKeys && ts + row >= w.p0) {
-            // a drafted row loses its non-finite elements (both groups find
-            // and write the same, or the second finds none left)
+            // a drafted row loses its non-finite elements.  Both groups clean
+            // it; the second may find none left, so each writes the row itself
+            // (its P.V waits for its own group only) and reads `bad` after the
+            // barrier of both at the unit's end
             uint8_t* vrow = smem + L::V_OFF + s * Tile::BYTES + row * 128;
             bool any = false;
 #pragma unroll
@@ -583,10 +585,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               for (int c = 0; c < 8; ++c) {
                 uint4* at = reinterpret_cast<uint4*>(vrow + hf * Tile::HALF + c * 16);
                 uint4 v = *at;
-                if (scrub8<T>(v)) {
-                  *at = v;
-                  any = true;
-                }
+                any |= scrub8<T>(v);
+                *at = v;
               }
             const int node = ts + row - w.p0;
             if (any) atomicOr(&bad[node >> 5], 1u << (node & 31));
@@ -606,7 +606,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       const bool ofull = ok && mbar_wait(bar(B_OFULL + 2 * x + ((gt - 1) & 1)), ((gt - 1) >> 1) & 1);  // the unit's last P.V_x
-      ok = bar_red_and(1 + x, 128, ofull);
+      if (TREE && w.row0 + kRows < w.rows) ok = bar_red_and(1, 256, ofull);  // both tiles have rows
+      else ok = bar_red_and(1 + x, 128, ofull);
       if (!ok) break;
       tc_fence_after();
       if constexpr (TREE) {

@@ -66,3 +66,34 @@ def test_elements_that_are_not_rotated_stay_apart(d, rot, dtype, interleaved, no
         assert torch.equal(got[got.isinf()].float(), z[z.isinf()])
         if not norm:
             assert same(got[..., rot:], x[..., rot:])
+
+
+@pytest.mark.parametrize("nodes,hq,hkv,bs,split", [(40, 8, 2, 16, 0), (64, 12, 3, 4, 256), (33, 16, 2, 8, 128)])
+def test_every_row_of_both_tiles_learns_of_a_value(nodes, hq, hkv, bs, split):
+    """More than 128 rows per KV head, which two groups of warps share: each row is non-finite in a dimension exactly
+    where a node that it sees is, whichever group met the value first."""
+    d, reqs = 64, 24
+    rng = np.random.default_rng(14)
+    g = torch.Generator(device="cuda").manual_seed(14)
+    lens = [int(x) + nodes for x in rng.integers(0, 400, reqs)]
+    blocks = -(-max(lens) // bs)
+    tables = torch.arange(reqs * blocks, dtype=torch.int32, device="cuda").view(reqs, blocks)
+    kc, vc = (torch.randn(reqs * blocks, bs, hkv, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(reqs * nodes, hq, d, generator=g, device="cuda").to(torch.bfloat16)
+    trees = [[int(rng.integers(max(-1, i - 4), i)) for i in range(nodes)] for _ in range(reqs)]
+    mask = torch.cat([ops().tree_mask(t) for t in trees]).cuda()
+    v = vc.view(reqs, blocks * bs, hkv, d)
+    bad = torch.zeros(reqs, nodes, d, dtype=torch.bool)
+    for r, L in enumerate(lens):
+        for j in rng.permutation(nodes)[:5]:
+            e = int(rng.integers(d))
+            v[r, L - nodes + int(j), :, e] = (INF, -INF, NAN)[int(rng.integers(3))]
+            bad[r, int(j), e] = True
+    sees = (mask.view(reqs, nodes, 1).cpu() >> torch.arange(nodes)) & 1
+    want = torch.einsum("rij,rje->rie", sees.float(), bad.float()) > 0
+    for _ in range(10):
+        out = ops().verify_tree(q, i32(*range(0, reqs * nodes + 1, nodes)), mask, i32(*lens), kc, vc, tables, d ** -0.5,
+                                nodes, split_tokens=split)
+        assert ops().get_device_error() == 0
+        got = ~out.isfinite().cpu().view(reqs, nodes, hq, d)
+        assert torch.equal(got, want[:, :, None].expand_as(got))
