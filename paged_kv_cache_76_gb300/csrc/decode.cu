@@ -725,11 +725,11 @@ __device__ __forceinline__ void add_weights(const AccumulateParams& p, int part)
       }
 #pragma unroll
       for (int i = 0; i < P; ++i) mn = fmaxf(mn, mc[i]);
-      if (mn != -INFINITY) {
-        l *= ex2_approx(m - mn);
+      // partitions without a finite logit weigh nothing, or are NaN: so is l
+      const float ref = mn == -INFINITY ? 0.f : mn;
+      l *= ex2_approx(m - ref);
 #pragma unroll
-        for (int i = 0; i < P; ++i) l += wc[i] * ex2_approx(mc[i] - mn);
-      }
+      for (int i = 0; i < P; ++i) l += wc[i] * ex2_approx(mc[i] - ref);
       m = mn;
     }
     float M = m;
@@ -741,7 +741,7 @@ __device__ __forceinline__ void add_weights(const AccumulateParams& p, int part)
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     if (lane == 0) {
       s_m[g] = M;
-      s_inv[g] = l > 0.f && g < G ? 1.f / l : 0.f;  // heads that pad the group weigh nothing
+      s_inv[g] = l == 0.f || g >= G ? 0.f : 1.f / l;  // heads that pad the group weigh nothing; a NaN sum stays one
     }
   }
   if (__syncthreads_or(twice)) {

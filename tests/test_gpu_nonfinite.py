@@ -97,3 +97,35 @@ def test_every_row_of_both_tiles_learns_of_a_value(nodes, hq, hkv, bs, split):
         assert ops().get_device_error() == 0
         got = ~out.isfinite().cpu().view(reqs, nodes, hq, d)
         assert torch.equal(got, want[:, :, None].expand_as(got))
+
+
+@pytest.mark.parametrize("hq,hkv,split", [(8, 2, 0), (8, 2, 64), (14, 2, 0), (2, 2, 64)])
+def test_scores_of_a_softmax_that_is_not_a_number(hq, hkv, split):
+    """A NaN or a positively infinite logit makes its head's weights NaN for every token of the request, and so the
+    scores of its KV head; a negatively infinite one weighs nothing.  No other score changes."""
+    lens, d, bs = [300, 70, 1, 200], 128, 16
+    g = torch.Generator(device="cuda").manual_seed(12)
+    tables = torch.arange(4 * 20, dtype=torch.int32, device="cuda").view(4, 20)
+    kc, vc = (torch.randn(80, bs, hkv, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn(4, hq, d, generator=g, device="cuda").to(torch.bfloat16)
+    clean = torch.rand(4, hkv, 320, generator=g, device="cuda")
+    before = clean.clone()
+    ops().decode_accumulate(q, kc, vc, tables, i32(*lens), 0.09, clean, split_tokens=split)
+    keys = kc.view(4, 320, hkv, d)
+    keys[0, 299, 1, 7] = NAN         # one token of the last partition
+    keys[1, :, 0] = NAN              # every token
+    keys[2, 0, 0, 3] = NAN           # the only token
+    keys[3, 5, 0, 9] = INF           # by the sign of the query: a NaN, or a weight of nothing
+    got = before.clone()
+    ops().decode_accumulate(q, kc, vc, tables, i32(*lens), 0.09, got, split_tokens=split)
+    assert ops().get_device_error() == 0
+    for r, L in enumerate(lens):
+        k = keys[r, :L].double().repeat_interleave(hq // hkv, 1)
+        p = torch.softmax(torch.einsum("hd,thd->ht", q[r].double(), k) * 0.09, 1)
+        want = before[r, :, :L].double() + p.view(hkv, -1, L).sum(1)
+        assert torch.equal(got[r, :, :L].isnan(), want.isnan()), r
+        fine = ~want.isnan()
+        assert bool(((got[r, :, :L].double() - want)[fine].abs() < 1e-4).all())
+        assert torch.equal(got[r, :, L:], before[r, :, L:])
+    assert torch.equal(got[0, 0], clean[0, 0]) and torch.equal(got[1, 1], clean[1, 1])
+    assert torch.equal(got[2, 1], clean[2, 1]) and torch.equal(got[3, 1], clean[3, 1])
