@@ -625,7 +625,8 @@ int pa_decode_accumulate(const void* q, const void* k_cache, const void* v_cache
  *                 may repeat; a row outside [0, num_rows) records
  *                 PA_DEVERR_SCORE_ROW, a context outside [0, score_len]
  *                 PA_DEVERR_CONTEXT_LEN, and the request keeps nothing
- * sink, heavy, recent >= 0, budget >= 1.
+ * sink, heavy, recent >= 0, budget >= 1.  keep and keep_lens overlap neither one
+ * another nor an input (new lengths are another array: PA_ERR_INVALID).
  * ------------------------------------------------------------------------- */
 int pa_evict_select(const float* scores, const int32_t* score_rows, int num_rows, int kv_heads, int score_len,
                     const int32_t* context_lens, int num_seqs, int sink, int heavy, int recent, int32_t* keep,

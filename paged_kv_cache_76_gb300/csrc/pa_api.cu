@@ -136,6 +136,12 @@ bool kv_map(const void* base, int num_blocks, int block_size, int kv_heads, int 
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Do two arrays of an and bn elements of 4 bytes share any?
+bool overlap4(const void* a, int64_t an, const void* b, int64_t bn) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x < y ? y - x < 4 * (uintptr_t)an : x - y < 4 * (uintptr_t)bn;
+}
+
 int check_kv_shape(int num_blocks, int block_size, int kv_heads, int head_dim, pa_dtype dt) {
   if (dt != PA_FP16 && dt != PA_BF16) return PA_ERR_DTYPE;
   if (head_dim != 64 && head_dim != 128) return PA_ERR_INVALID;
@@ -1062,6 +1068,16 @@ int pa_evict_select(const float* scores, const int32_t* score_rows, int num_rows
   if (!score_rows && num_rows < num_seqs) return PA_ERR_INVALID;
   if (num_seqs == 0) return PA_OK;
   if (!scores || !context_lens || !keep || !keep_lens || !aligned16(scores) || !aligned16(keep)) return PA_ERR_INVALID;
+  // every CTA of a row reads the inputs while others write the outputs
+  const int64_t nkeep = (int64_t)num_seqs * kv_heads * budget, lists = (int64_t)num_rows * kv_heads;
+  if (lists > (int64_t(1) << 48) / score_len) return PA_ERR_INVALID;  // no address space holds it
+  const int64_t nscores = lists * score_len;
+  const struct { const void* p; int64_t n; } outs[] = {{keep, nkeep}, {keep_lens, num_seqs}};
+  for (const auto& o : outs)
+    if (overlap4(o.p, o.n, context_lens, num_seqs) || overlap4(o.p, o.n, scores, nscores) ||
+        (score_rows && overlap4(o.p, o.n, score_rows, num_seqs)))
+      return PA_ERR_INVALID;
+  if (overlap4(keep, nkeep, keep_lens, num_seqs)) return PA_ERR_INVALID;
   int* err = device_error_ptr();
   if (!err) return PA_ERR_CUDA;
   EvictSelectParams p{};

@@ -777,7 +777,7 @@ def decode_accumulate(q, k_cache, v_cache, block_tables, context_lens, scale, sc
 def evict_select(scores, context_lens, sink, heavy, recent, score_rows=None, keep=None, keep_lens=None, stream=None):
     """pa_evict_select: per request and KV head the tokens a budget of ``sink + heavy + recent`` keeps, ascending:
     the first, the last, and the best scored between.  Returns (keep int32 [num_seqs, kv_heads, budget], -1 behind;
-    keep_lens int32 [num_seqs])."""
+    keep_lens int32 [num_seqs]); neither may be an input's memory (``context_lens`` among them)."""
     if keep is None and keep_lens is None and _short_way(stream):
         r = _marshal.evict_select(scores, context_lens, sink, heavy, recent, score_rows)
         if r is not None:

@@ -189,3 +189,16 @@ def test_c_calls_check_sizes_and_pointers(lib):
                dict(keep=None)):
         assert com(**kw) == inv, kw
     assert com(R=0, keep=None) == ok
+
+
+def test_select_refuses_outputs_that_lie_in_its_inputs(lib):
+    """Every CTA of a row reads the lengths, rows and scores while others write the lists and their lengths."""
+    S, L, R, K, N = 1 << 20, 2 << 20, 3 << 20, 4 << 20, 5 << 20   # no call below reaches the GPU: it is refused first
+
+    def sel(s=S, lens=L, rows=R, keep=K, n=N, R=2, budget=6):
+        return lib.pa_evict_select(s, rows, 2, 2, 64, lens, R, 1, budget - 4, 3, keep, n, None)
+
+    for kw in (dict(n=L), dict(n=L + 4), dict(lens=L, n=L - 4), dict(n=R), dict(n=S + 1020), dict(keep=L),
+               dict(keep=L - 80), dict(keep=R), dict(keep=S), dict(keep=S + 1008), dict(n=K), dict(n=K + 92)):
+        assert sel(**kw) == _lib.PA_ERR_INVALID, kw
+    assert sel(R=0, n=L) == _lib.PA_OK
