@@ -10,6 +10,8 @@
 // order of length 132 and 162 us, and the latter 215 us as two row tiles of
 // the first (K and V once more through L2).  Before them a warp-MMA kernel took 347
 // and 509 us.
+#include <float.h>
+
 #include "pa_device.cuh"
 #include "pa_internal.h"
 #include "tree.cuh"
@@ -47,7 +49,9 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
   for (int i = 0; i < V; ++i) a[i] = 0.f;
 #pragma unroll 4
   for (int c = 0; c < nsplit; ++c) {
-    const float w = pm[c] == -INFINITY ? 0.f : exp2f(pm[c] - M);
+    // no smaller than the smallest normal number where the row sees a key: a value
+    // that is not finite decides the row however little it weighs
+    const float w = pm[c] == -INFINITY ? 0.f : fmaxf(exp2f(pm[c] - M), FLT_MIN);
     den += w * pl[c];
     const float* x = po + (size_t)c * D;
 #pragma unroll

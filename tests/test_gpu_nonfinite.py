@@ -129,3 +129,35 @@ def test_scores_of_a_softmax_that_is_not_a_number(hq, hkv, split):
         assert torch.equal(got[r, :, L:], before[r, :, L:])
     assert torch.equal(got[0, 0], clean[0, 0]) and torch.equal(got[1, 1], clean[1, 1])
     assert torch.equal(got[2, 1], clean[2, 1]) and torch.equal(got[3, 1], clean[3, 1])
+
+
+@pytest.mark.parametrize("nodes,hq,bs", [(7, 8, 16), (30, 16, 16), (64, 16, 16), (64, 16, 4)])
+def test_a_seen_value_decides_however_small_its_weight(nodes, hq, bs):
+    """A key of the first partition takes all the weight that 32 bits can hold, and a drafted node in the last one has
+    an infinity and a NaN among its values: the rows that see the node are infinite and NaN there, cut or whole."""
+    hkv, d, hist = 2, 128, 700
+    g = torch.Generator(device="cuda").manual_seed(13)
+    L = hist + nodes
+    nb = -(-L // bs)
+    tables = torch.arange(nb, dtype=torch.int32, device="cuda")[None]
+    kc, vc = (torch.randn(nb, bs, hkv, d, generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    along = torch.randn(d, generator=g, device="cuda").sign()
+    q = (along + 0.1 * torch.randn(nodes, hq, d, generator=g, device="cuda")).to(torch.bfloat16)
+    kc.view(-1, hkv, d)[3] = (30 * along).to(torch.bfloat16)     # logits of about 30 d / sqrt(d) = 340
+    mask = ops().tree_mask([-1] + [max(0, i - 3) if i != 2 else -1 for i in range(1, nodes)]).cuda()
+    args = (q, i32(0, nodes), mask, i32(L), kc, vc, tables, d ** -0.5, nodes)
+    clean = ops().verify_tree(*args, split_tokens=128)
+    v = vc.view(-1, hkv, d)
+    v[hist + 1, :, 5], v[hist + 1, :, 6], v[hist + 1, :, 7] = INF, NAN, -INF
+    seen = torch.tensor([bool((int(m) >> 1) & 1) for m in mask], device="cuda")
+    assert 0 < int(seen.sum()) < nodes
+    for split in (128, 256, -(-(nb * bs) // 128) * 128):
+        got = ops().verify_tree(*args, split_tokens=split)
+        assert ops().get_device_error() == 0
+        assert torch.equal(got[seen][..., 5], torch.full_like(got[seen][..., 5], INF))
+        assert torch.equal(got[seen][..., 7], torch.full_like(got[seen][..., 7], -INF))
+        assert bool(got[seen][..., 6].isnan().all())
+        rest = [i for i in range(d) if i not in (5, 6, 7)]
+        assert bool(got[~seen].isfinite().all()) and bool(got[..., rest].isfinite().all())
+        if split == 128:
+            assert torch.equal(got[~seen], clean[~seen]) and torch.equal(got[..., rest], clean[..., rest])
