@@ -784,8 +784,10 @@ int pa_alloc_get_stats(const pa_alloc* a, pa_alloc_stats* out);
  *    if they carry no hash (as above) and to the TAIL if they do, in release
  *    order, so cached blocks are evicted oldest-released first and a
  *    request's first block last.
- *  - A cached block loses its hash only when the free queue hands it out
- *    again (new block, CoW copy); its map entry is removed then.
+ *  - A cached block loses its hash, and the map its entry, when the free queue
+ *    hands it out again (new block, CoW copy), when pa_alloc_compact rewrites
+ *    it, and when the one sequence that holds it, in part (shared or cut inside
+ *    it), appends to it.
  *  - pa_alloc_share continues the hash chain into dst only when the shared
  *    part ends on a full, hashed block.
  * ------------------------------------------------------------------------- */

@@ -61,8 +61,10 @@ Automatic prefix caching ("Khám phá vLLM … phần 2", prefix caching;
 * a freed zero-count block with a hash goes to the tail of the free queue,
   without one to the head (the free_blocks rule above), so cached blocks are
   evicted in release order, the first block of a request last.
-* a cached block loses its hash only when the free queue hands it out again
-  (popleft): its map entry is removed then.
+* a cached block loses its hash when the free queue hands it out again
+  (popleft): its map entry is removed then.  It also does when its one owner
+  holds it in part (shared or cut inside it) and appends to it: the hash names
+  tokens that are overwritten then.
 
 Swapping ("2.1 PagedAttention" §7, preemption by swapping), when a swap pool
 of CPU blocks is set up:
@@ -420,6 +422,8 @@ class SequenceManager:
         if need > self.num_free():
             self.alloc_failures += 1
             raise NoFreeBlocks(f"need {need}, have {self.num_free()}")
+        if n > 0 and cur % bs != 0:
+            self._uncache(table[-1])
         table.extend(self.pool.get_new_blocks(need))
         slots = []
         for t in range(cur, cur + n):
@@ -467,6 +471,11 @@ class SequenceManager:
         self.cow_copies += 1
         return (b, nb)
 
+    def _uncache(self, b):
+        h, self.pool.block_hash[b] = self.pool.block_hash[b], None
+        if h is not None and self.pool.cached_block_hash_to_block.get(h) == b:
+            del self.pool.cached_block_hash_to_block[h]
+
     def compact(self, seq, first_token, n_tokens):
         self._resident(seq)
         L, bs = self.num_tokens[seq], self.block_size
@@ -481,9 +490,7 @@ class SequenceManager:
         if n_tokens % bs and n_tokens < L and self.pool.ref_cnt[table[kept - 1]] == 1:
             gone.add(table[kept - 1])
         for b in gone:
-            h, self.pool.block_hash[b] = self.pool.block_hash[b], None
-            if h is not None and self.pool.cached_block_hash_to_block.get(h) == b:
-                del self.pool.cached_block_hash_to_block[h]
+            self._uncache(b)
         if first_token < n_tokens:
             self.pending[seq] = None
         elif n_tokens == 0:

@@ -195,6 +195,9 @@ static int grow(pa_alloc* a, Seq* s, int n_tokens, int32_t* slots_out) {
     return PA_ERR_NO_FREE_BLOCKS;
   }
   if (need > 0) s->blocks.reserve(s->blocks.size() + (size_t)need);  // may throw: before any change
+  // a full, cached block that s holds in part (shared or cut there, and its own
+  // by now) is about to hold other tokens
+  if (n_tokens > 0 && cur % bs != 0) a->forget(s->blocks.back());
   for (int64_t i = 0; i < need; ++i) s->blocks.push_back(a->take());
   if (slots_out) {
     for (int64_t t = cur; t < cur + n_tokens; ++t)
