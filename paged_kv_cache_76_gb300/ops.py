@@ -166,6 +166,22 @@ def _stream(stream=None):
     return torch.cuda.current_stream().cuda_stream
 
 
+def _empty(shape, dtype, device, stream, returned=False):
+    """Memory for a launch on `stream` (None: the current one): of that stream's own, since what the current one frees
+    or is handed again may be in use there while the launch runs.  `returned`: the caller goes on with it on the
+    current stream."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if returned:
+        t.record_stream(current)
+    return t
+
+
 def _dev(t: torch.Tensor, name: str):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
@@ -303,22 +319,22 @@ def _decode_args(q, k_cache, v_cache, block_tables, context_lens, scale, out, sp
             ws_ptr, ws_bytes, _dev(out, "out"), dtype_code(q.dtype))
 
 
-def make_workspace(q, block_tables, block_size, split_tokens=0):
+def make_workspace(q, block_tables, block_size, split_tokens=0, stream=None):
     """Allocate (with torch) the scratch that :func:`decode` needs, or None."""
     B, hq, d = q.shape
     n = decode_workspace_size(B, hq, d, int(block_tables.shape[1]), block_size, split_tokens)
     if n == 0:
         return None
-    return torch.empty(n, dtype=torch.uint8, device=q.device)
+    return _empty(n, torch.uint8, q.device, stream)
 
 
 def decode(q, k_cache, v_cache, block_tables, context_lens, scale, out=None, split_tokens=0, workspace=None,
            stream=None):
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream, returned=True)
     _check_decode(q, k_cache, v_cache, block_tables, context_lens, out)
     if workspace is None:
-        workspace = make_workspace(q, block_tables, k_cache.shape[1], split_tokens)
+        workspace = make_workspace(q, block_tables, k_cache.shape[1], split_tokens, stream)
     args = _decode_args(q, k_cache, v_cache, block_tables, context_lens, scale, out, split_tokens, workspace)
     _keep(out, workspace)
     _launch("pa_decode", *args, _stream(stream))
@@ -362,7 +378,7 @@ def verify_decode(q, k_cache, v_cache, block_tables, context_lens, scale, out=No
         raise ValueError("q is [num_seqs, q_len, q_heads, head_dim]")
     B, ql, hq, dq = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream, returned=True)
     if dq != d:
         raise ValueError("head_dim mismatch")
     _check_attention(q, k_cache, v_cache, out)
@@ -371,7 +387,7 @@ def verify_decode(q, k_cache, v_cache, block_tables, context_lens, scale, out=No
     maxblk = int(block_tables.shape[1])
     if workspace is None:
         n = verify_workspace_size(B, ql, hq, d, maxblk, bs, split_tokens)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        workspace = _empty(n, torch.uint8, q.device, stream) if n else None
     ws_ptr, ws_bytes = (workspace.data_ptr(), workspace.numel() * workspace.element_size()) \
         if workspace is not None else (None, 0)
     _keep(out, workspace)
@@ -408,7 +424,7 @@ def decode_shared_prefix(q, k_cache, v_cache, prefix_blocks, prefix_len, block_t
     if dq != d:
         raise ValueError("head_dim mismatch")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream, returned=True)
     _check_attention(q, k_cache, v_cache, out)
     _check_index(q, "block_tables", block_tables, B, table=True)
     _check_index(q, "context_lens", context_lens, B)
@@ -417,7 +433,7 @@ def decode_shared_prefix(q, k_cache, v_cache, prefix_blocks, prefix_len, block_t
     maxblk = int(block_tables.shape[1])
     if workspace is None:
         n = decode_shared_prefix_workspace_size(B, hq, d, maxblk, bs, int(prefix_len), split_tokens)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(n, 1), torch.uint8, q.device, stream)
     _keep(out, workspace)
     _launch(
         "pa_decode_shared_prefix",
@@ -437,7 +453,7 @@ def verify_decode_tc(q, k_cache, v_cache, block_tables, context_lens, scale, out
     if dq != d:
         raise ValueError("head_dim mismatch")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream, returned=True)
     _check_attention(q, k_cache, v_cache, out)
     _check_index(q, "block_tables", block_tables, B, table=True)
     _check_index(q, "context_lens", context_lens, B)
@@ -458,7 +474,7 @@ def chunked_prefill(q, q_start, context_lens, k_cache, v_cache, block_tables, sc
         raise ValueError("head_dim mismatch")
     R = int(context_lens.shape[0])
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream, returned=True)
     _check_attention(q, k_cache, v_cache, out)
     _check_index(q, "context_lens", context_lens, R)
     _check_index(q, "q_start", q_start, R + 1)
@@ -621,7 +637,7 @@ def norm_rope_and_cache(q, k, v, positions, cos_sin, slot_mapping, k_cache, v_ca
         kw = _ptr(k_weight, "k_weight", dev)
     sl = _rows_ptr(slot_mapping, "slot_mapping", dev, T)
     if out is None:
-        out = torch.empty(qshape, dtype=dtype, device=q.device)
+        out = _empty(qshape, dtype, q.device, stream, returned=True)
     elif out.shape != qshape or out.dtype != dtype:
         raise ValueError("out must have q's shape, dtype and device")
     handle = _stream_on(dev, stream)
@@ -691,7 +707,7 @@ def verify_tree(q, q_start, tree_mask, context_lens, k_cache, v_cache, block_tab
         raise ValueError(f"tree_mask has shape {tuple(tree_mask.shape)}: {T} rows expected")
     mask = _ptr(tree_mask, "tree_mask", dev)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream, returned=True)
     elif out.shape != qshape:
         raise ValueError(f"out has shape {tuple(out.shape)}, q {tuple(qshape)}")
     handle = _stream_on(dev, stream)
@@ -699,7 +715,7 @@ def verify_tree(q, q_start, tree_mask, context_lens, k_cache, v_cache, block_tab
     max_q_len, split_tokens = int(max_q_len), int(split_tokens)
     if workspace is None:
         n = _tree_workspace(dev, R, T, max_q_len, hq, hkv, d, maxblk, bs, split_tokens)
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        workspace = _empty(n, torch.uint8, q.device, stream) if n else None
     ws_ptr, ws_bytes = (_ptr(workspace, "workspace", dev), workspace.numel() * workspace.element_size()) \
         if workspace is not None else (None, 0)
     _keep(out, workspace)
@@ -758,14 +774,14 @@ def decode_accumulate(q, k_cache, v_cache, block_tables, context_lens, scale, sc
             raise ValueError("scores_out must have scores' shape")
         so, _ = _score_ptrs(scores_out, hkv, None, 0, dev, "scores_out")
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream, returned=True)
     elif out.shape != qshape:
         raise ValueError(f"out has shape {tuple(out.shape)}, q {tuple(qshape)}")
     handle = _stream_on(dev, stream)
     maxblk, split_tokens = block_tables.shape[1], int(split_tokens)
     if workspace is None:
         n = _accumulate_workspace(dev, B, hq, hkv, d, maxblk, bs, split_tokens)
-        workspace = torch.empty(max(n, 1), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(n, 1), torch.uint8, q.device, stream)
     _keep(out, workspace)
     _launch(
         "pa_decode_accumulate", _ptr(q, "q", dev), kc, vc, tables, maxblk, lens, B, hq, hkv, d, bs, nb, float(scale),
@@ -796,11 +812,11 @@ def evict_select(scores, context_lens, sink, heavy, recent, score_rows=None, kee
     if sink < 0 or heavy < 0 or recent < 0 or budget < 1:
         raise ValueError("sink, heavy and recent are counts, at least one token together")
     if keep is None:
-        keep = torch.empty((B, hkv, budget), dtype=torch.int32, device=scores.device)
+        keep = _empty((B, hkv, budget), torch.int32, scores.device, stream, returned=True)
     elif keep.shape != (B, hkv, budget):
         raise ValueError(f"keep is int32 [{B}, {hkv}, {budget}]")
     if keep_lens is None:
-        keep_lens = torch.empty(B, dtype=torch.int32, device=scores.device)
+        keep_lens = _empty(B, torch.int32, scores.device, stream, returned=True)
     handle = _stream_on(dev, stream)
     _keep(keep, keep_lens)
     _launch(

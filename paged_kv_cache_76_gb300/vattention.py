@@ -11,7 +11,7 @@ import torch
 
 from . import _lib
 from ._lib import PA_ERR_NO_FREE_BLOCKS, PAError, check
-from .ops import _keep, _launch
+from .ops import _empty, _keep, _launch
 
 __all__ = ["VirtualKV", "NoPages", "decode_contiguous", "reshape_and_cache_slots"]
 
@@ -155,13 +155,13 @@ class VirtualKV:
                stream=None):
         B, hq, d = q.shape
         if out is None:
-            out = torch.empty_like(q)
+            out = _empty(q.shape, q.dtype, q.device, stream, returned=True)
         if d != self.head_dim or q.dtype != self.dtype or out.dtype != q.dtype or out.shape != q.shape:
             raise ValueError("q and out are [num_seqs, q_heads, head_dim] of the KV's head_dim and dtype")
         _rows(q, ("slot_ids", slot_ids, B), ("context_lens", context_lens, B), ("out", out, B))
         if workspace is None:
             n = int(self._L.pa_decode_workspace_size(B, hq, d, self.max_len // 16, 16, int(split_tokens)))
-            workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+            workspace = _empty(n, torch.uint8, q.device, stream) if n else None
         ws, wb = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
         _keep(out, workspace)
         _launch("pa_vkv_decode", self._h, int(layer), _dev(q, "q"), _i32(slot_ids, "slot_ids"),
@@ -185,7 +185,7 @@ def decode_contiguous(q, k_cache, v_cache, slot_ids, context_lens, scale, slot_t
     ns, L, hkv, d = k_cache.shape
     B, hq, dq = q.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(q.shape, q.dtype, q.device, stream, returned=True)
     _check_contiguous_kv(k_cache, v_cache, q.dtype, dq)
     if out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("out must have q's shape and dtype")
@@ -197,7 +197,7 @@ def decode_contiguous(q, k_cache, v_cache, slot_ids, context_lens, scale, slot_t
     lib = _lib.lib()
     if workspace is None:
         n = int(lib.pa_decode_workspace_size(B, hq, d, L // 16, 16, int(split_tokens)))
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device) if n else None
+        workspace = _empty(n, torch.uint8, q.device, stream) if n else None
     ws, wb = (workspace.data_ptr(), workspace.numel()) if workspace is not None else (None, 0)
     _keep(out, workspace)
     _launch(
