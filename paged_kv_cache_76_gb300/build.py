@@ -4,16 +4,16 @@ Each translation unit is compiled by nvcc in parallel, then linked into one
 shared library with the CUDA runtime linked statically.  Beside it, ``_marshal``
 (``csrc/marshal.cpp``), the Python extension that passes torch tensors to some
 of its functions, is compiled by g++ against the installed torch and Python;
-without their headers it is left out and the calls take the longer way through
-ctypes.  Only sources or headers newer than their object are rebuilt.  Run ``python -m
+where that cannot be done it is left out, with a word about it, and the calls
+take the longer way through ctypes.  Only sources or headers newer than their object are rebuilt.  Run ``python -m
 paged_kv_cache_76_gb300.build [--force] [--verbose]``.
 """
 from __future__ import annotations
 
 import argparse
-import importlib.metadata
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -53,38 +53,81 @@ def _stale(obj: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
-def _marshal_job(nvcc: str, force: bool):
-    """(command, stamp) that compiles _marshal, or None: up to date, or torch's or Python's headers are missing."""
+def _torch_version(torch_dir: str):
+    """torch.__version__ without importing torch; None if it is not where it always is."""
+    try:
+        with open(os.path.join(torch_dir, "version.py")) as f:
+            m = re.search(r"""^__version__ = ['"](.+)['"]$""", f.read(), re.M)
+    except OSError:
+        return None
+    return m and m.group(1)
+
+
+def _marshal_job(nvcc: str):
+    """(command up to the output's name, stamp) that compiles _marshal, or a text: why it cannot be."""
     spec = importlib.util.find_spec("torch")
     cxx = shutil.which(os.environ.get("CXX", "g++"))
-    if spec is None or not spec.submodule_search_locations or cxx is None:
-        return None
+    if spec is None or not spec.submodule_search_locations:
+        return "torch is not installed"
+    if cxx is None:
+        return "there is no C++ compiler"
     torch_dir = spec.submodule_search_locations[0]
     inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
            os.path.join(torch_dir, "include", "torch", "csrc", "api", "include"),
            os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "include")]
     if not os.path.exists(os.path.join(inc[1], "Python.h")) or not os.path.isdir(inc[2]):
-        return None
-    src = os.path.join(CSRC, "marshal.cpp")
+        return "torch's or Python's headers are missing"
+    version = _torch_version(torch_dir)
+    if version is None:
+        return "torch's version is not known"
+    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared"] + [x for i in inc for x in ("-I", i)]
+    cmd += [os.path.join(CSRC, "marshal.cpp"), "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu",
+            "-lc10", "-lc10_cuda", "-o"]
     # built for one torch and one Python: another of either is another build
-    stamp = f"torch {importlib.metadata.version('torch')} python {sys.version}"
+    return cmd, f"torch {version} python {sys.version}"
+
+
+def _marshal_fresh(stamp: str) -> bool:
     try:
         with open(MARSHAL_STAMP) as f:
             same = f.read() == stamp
     except OSError:
-        same = False
-    if not force and same and not _stale(MARSHAL, [src, os.path.join(INCLUDE, "pa.h")]):
-        return None
-    lib = os.path.join(torch_dir, "lib")
-    cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared"] + [x for i in inc for x in ("-I", i)] + [src, "-o", MARSHAL]
-    return cmd + ["-L", lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], stamp
+        return False
+    return same and not _stale(MARSHAL, [os.path.join(CSRC, "marshal.cpp"), os.path.join(INCLUDE, "pa.h")])
+
+
+def _remove(*paths) -> None:
+    for p in paths:
+        if os.path.exists(p):
+            os.remove(p)
+
+
+def _build_marshal(nvcc: str, force: bool, verbose: bool) -> None:
+    """Compile _marshal if it is not up to date.  It is optional: where that fails it is left out, an older one too."""
+    job = _marshal_job(nvcc)
+    if not isinstance(job, str):
+        cmd, stamp = job
+        if not force and _marshal_fresh(stamp):
+            return
+        new = MARSHAL + f".{os.getpid()}.tmp"
+        r = subprocess.run(cmd + [new], capture_output=True, text=True)
+        if verbose or r.returncode:
+            sys.stderr.write(" ".join(cmd + [new]) + "\n" + r.stdout + r.stderr)
+        if r.returncode == 0:
+            os.replace(new, MARSHAL)
+            with open(MARSHAL_STAMP, "w") as f:
+                f.write(stamp)
+            return
+        _remove(new)
+        job = "its compilation failed"
+    _remove(MARSHAL, MARSHAL_STAMP)
+    sys.stderr.write(f"_marshal is left out ({job}): its calls go through ctypes\n")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
     """Compile and link; returns the path of libpa.so."""
     nvcc = _nvcc()
     os.makedirs(OBJDIR, exist_ok=True)
-    marshal = _marshal_job(nvcc, force)
     headers = _headers()
     common = ["-O3", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
     jobs = []
@@ -105,17 +148,14 @@ def build(force: bool = False, verbose: bool = False) -> str:
         r = subprocess.run(cmd, capture_output=True, text=True)
         return cmd, r
 
-    every = jobs + ([marshal[0]] if marshal else [])
-    if every:
-        with ThreadPoolExecutor(max_workers=min(len(every), os.cpu_count() or 4)) as ex:
-            for cmd, r in ex.map(run, every):
-                if verbose or r.returncode:
-                    sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
-                if r.returncode:
-                    raise RuntimeError("failed: compiling " + next(a for a in cmd if a.startswith(CSRC + os.sep)))
-    if marshal:
-        with open(MARSHAL_STAMP, "w") as f:
-            f.write(marshal[1])
+    with ThreadPoolExecutor(max_workers=min(len(jobs) + 1, os.cpu_count() or 4)) as ex:
+        marshal = ex.submit(_build_marshal, nvcc, force, verbose)
+        for cmd, r in ex.map(run, jobs):
+            if verbose or r.returncode:
+                sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+            if r.returncode:
+                raise RuntimeError("nvcc failed on " + next(a for a in cmd if a.startswith(CSRC + os.sep)))
+        marshal.result()
     if force or jobs or _stale(LIB, objs):
         cmd = [nvcc] + ARCH + ["-shared", "-cudart", "static", "-o", LIB] + objs
         r = subprocess.run(cmd, capture_output=True, text=True)
