@@ -81,7 +81,7 @@ def _marshal_job(nvcc: str):
     if version is None:
         return "torch's version is not known"
     cmd = [cxx, "-O2", "-std=c++17", "-fPIC", "-shared"] + [x for i in inc for x in ("-I", i)]
-    cmd += [os.path.join(CSRC, "marshal.cpp"), "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu",
+    cmd += [f'-DPA_TORCH_VERSION="{version}"', os.path.join(CSRC, "marshal.cpp"), "-L", os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu",
             "-lc10", "-lc10_cuda", "-o"]
     # built for one torch and one Python: another of either is another build
     return cmd, f"torch {version} python {sys.version}"

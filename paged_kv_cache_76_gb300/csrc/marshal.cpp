@@ -417,4 +417,10 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, n
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__marshal() { return PyModule_Create(&module); }
+// torch_version: the torch whose headers, and so whose tensors' layout, this was
+// compiled with; it is used with that one alone (ops.py).
+PyMODINIT_FUNC PyInit__marshal() {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", PA_TORCH_VERSION) != 0) Py_CLEAR(m);
+  return m;
+}

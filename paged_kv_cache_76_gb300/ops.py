@@ -111,7 +111,7 @@ class recording:
 # nothing was done.
 _SHORT = ("pa_norm_rope_and_cache", "pa_verify_tree_workspace_size", "pa_verify_tree",
           "pa_decode_accumulate_workspace_size", "pa_decode_accumulate", "pa_evict_select", "pa_compact_kv")
-_marshal = None  # the module; False: not built
+_marshal = None  # the module; False: not built, or for another torch
 
 
 def _load_marshal():
@@ -122,9 +122,13 @@ def _load_marshal():
         return False
     try:
         m = importlib.import_module("._marshal", __package__)
+    except ImportError:
+        m = None
+    # it reads tensors by the layout of the torch it was compiled with
+    if getattr(m, "torch_version", None) == str(torch.__version__):
         m.bind(*(C.cast(getattr(lib, name), C.c_void_p).value for name in _SHORT))
         _marshal = m
-    except ImportError:
+    else:
         _marshal = False
     return _marshal
 

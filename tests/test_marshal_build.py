@@ -64,3 +64,34 @@ def test_a_build_with_it_replaces_the_old_one_and_then_rests(place, monkeypatch)
             assert f.read() == "new\n"
     assert (place / "ran").read_text() == "\n"           # once
     assert str(torch.__version__) in open(build.MARSHAL_STAMP).read()
+
+
+class Fake:
+    """Stands for the extension: bind must not be reached in one that was built for another torch."""
+
+    def __init__(self, version):
+        self.bound = 0
+        if version is not None:
+            self.torch_version = version
+
+    def bind(self, *addresses):
+        self.bound += 1
+
+
+@pytest.mark.parametrize("version,taken", [(str(torch.__version__), True), ("2.0.0", False), (None, False)])
+def test_an_extension_built_for_another_torch_is_not_used(monkeypatch, version, taken):
+    from paged_kv_cache_76_gb300 import ops
+    build.build()
+    fake = Fake(version)
+    monkeypatch.setattr(ops.importlib, "import_module", lambda name, package=None: fake)
+    monkeypatch.setattr(ops, "_marshal", None)
+    assert ops._load_marshal() is (fake if taken else False) and fake.bound == taken
+    assert ops._short_way(None) is (fake if taken else False) and fake.bound == taken     # not asked again
+
+
+def test_the_extension_knows_its_torch():
+    from paged_kv_cache_76_gb300 import ops
+    build.build()
+    if not os.path.exists(build.MARSHAL):
+        pytest.skip("the extension is not built here")
+    assert ops._load_marshal() and ops._marshal.torch_version == str(torch.__version__)
