@@ -551,6 +551,7 @@ int pa_norm_rope_and_cache(const void* q, const void* k, const void* v, int64_t 
  *                 is attended in partitions of that size, merged by log-sum-exp
  *   workspace     at least pa_verify_tree_workspace_size(...) bytes (may be NULL
  *                 when that is 0)
+ *   scale         positive (a normal fp32 number)
  * q_heads / kv_heads up to 16.  Rows of q past q_start[num_reqs] are left as
  * they were in out.  A q_start that decreases or passes total_q, n > max_q_len
  * or a context shorter than n records PA_DEVERR_QUERY_RANGE, a context past the

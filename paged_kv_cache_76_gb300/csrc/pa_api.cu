@@ -1230,7 +1230,8 @@ int pa_verify_tree(const void* q, const int32_t* q_start, const uint64_t* tree_m
                    pa_dtype dtype, pa_stream stream) {
   int st = check_kv_shape(num_blocks, block_size, kv_heads, head_dim, dtype);
   if (st != PA_OK) return st;
-  if (!std::isfinite(scale)) return PA_ERR_INVALID;
+  // masked logits are -inf and meet the scale: it must neither vanish nor turn their sign
+  if (!std::isnormal(scale) || scale < 0.f) return PA_ERR_INVALID;
   TreeSetup s;
   st = tree_setup(num_reqs, total_q, max_q_len, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size,
                   split_tokens, &s);

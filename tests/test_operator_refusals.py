@@ -202,3 +202,15 @@ def test_select_refuses_outputs_that_lie_in_its_inputs(lib):
                dict(keep=L - 80), dict(keep=R), dict(keep=S), dict(keep=S + 1008), dict(n=K), dict(n=K + 92)):
         assert sel(**kw) == _lib.PA_ERR_INVALID, kw
     assert sel(R=0, n=L) == _lib.PA_OK
+
+
+def test_tree_scale_is_positive(lib):
+    """Masked logits are -inf before they are scaled: a scale of zero or below would make them NaN or +inf."""
+    P = 16
+
+    def tree(scale, maxblk=8):
+        return lib.pa_verify_tree(P, P, P, P, P, P, P, maxblk, 1, 4, 4, 8, 2, 128, 16, 4, scale, 128, None, 0, P, 1, None)
+
+    for scale in (0.0, -0.0, -0.125, 1e-40, float("nan"), float("-inf")):
+        assert tree(scale) == _lib.PA_ERR_INVALID, scale
+    assert tree(1e-37, maxblk=64) == _lib.PA_ERR_WORKSPACE       # this far it gets with any other
