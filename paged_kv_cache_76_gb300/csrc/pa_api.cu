@@ -985,6 +985,9 @@ int pa_decode_accumulate(const void* q, const void* k_cache, const void* v_cache
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(scores) ||
       !aligned16(scores_out))
     return PA_ERR_INVALID;
+  const int64_t lists = (int64_t)num_rows * kv_heads;
+  if (lists > (int64_t(1) << 48) / score_len) return PA_ERR_INVALID;  // no address space holds it
+  if (scores != scores_out && overlap4(scores, lists * score_len, scores_out, lists * score_len)) return PA_ERR_INVALID;
   if (!workspace || workspace_bytes < s.bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
   CUtensorMap km, vm;
   if (!kv_map(k_cache, num_blocks, block_size, kv_heads, head_dim, dtype, &km) ||

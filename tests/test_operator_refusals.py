@@ -214,3 +214,18 @@ def test_tree_scale_is_positive(lib):
     for scale in (0.0, -0.0, -0.125, 1e-40, float("nan"), float("-inf")):
         assert tree(scale) == _lib.PA_ERR_INVALID, scale
     assert tree(1e-37, maxblk=64) == _lib.PA_ERR_WORKSPACE       # this far it gets with any other
+
+
+def test_accumulate_refuses_scores_that_overlap_in_part(lib):
+    """Each entry is read and written once, by the thread that owns it: in place or apart, not shifted."""
+    P, S = 16, 1 << 20
+    size = 2 * 2 * 128 * 4
+
+    def acc(s, so, rows=None, ws=P):
+        return lib.pa_decode_accumulate(P, P, P, P, 8, P, 2, 8, 2, 128, 16, 4, 0.1, 0, s, rows, 2, 128, so, ws, 64, P, 1,
+                                        None)
+
+    for so in (S + 16, S - 16, S + size - 16, S - size + 16):
+        assert acc(S, so) == _lib.PA_ERR_INVALID, so
+    for so in (S, S + size, S - size):                           # these get as far as the scratch's size
+        assert acc(S, so) == _lib.PA_ERR_WORKSPACE, so
