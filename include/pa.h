@@ -548,7 +548,10 @@ int pa_norm_rope_and_cache(const void* q, const void* k, const void* v, int64_t 
  *   tree_mask     uint64 [total_q]; read during set-up, like q and q_start
  *   max_q_len     host-side bound of n, 1..64 (sizes the grid and the scratch)
  *   split_tokens  0 = the library's choice; else a multiple of 128: the context
- *                 is attended in partitions of that size, merged by log-sum-exp
+ *                 is attended in partitions of that size, merged by log-sum-exp.
+ *                 The choice goes by the number of requests and heads: a large
+ *                 batch runs whole, so give a size (16384, say) where one of its
+ *                 contexts is far longer than the rest
  *   workspace     at least pa_verify_tree_workspace_size(...) bytes (may be NULL
  *                 when that is 0)
  *   scale         positive (a normal fp32 number)
@@ -582,6 +585,12 @@ int pa_verify_tree(const void* q, const int32_t* q_start, const uint64_t* tree_m
  * Entries of other rows and from context_lens[r] on are left as they were; a
  * token appended to a sequence must find zero there (a new sequence's row is
  * zeroed by the caller; pa_compact_kv leaves zeros behind what it keeps).
+ * Only this call keeps score: queries of pa_chunked_prefill, pa_verify_decode and
+ * pa_verify_tree add nothing, so right after a prompt every score is still what
+ * the caller set, and a selection by them would keep the lowest tokens (equal
+ * scores).  Decode some steps first, or set the scores of a prompt's tokens.
+ * A logit that is NaN or +infinity makes its head's weights, and the scores of
+ * all the request's tokens at its KV head, NaN: the softmax is.
  *   scores, scores_out  fp32 [num_rows][kv_heads][score_len]; the same array or
  *                 not overlapping; score_len >= max_blocks_per_seq * block_size
  *                 or at least every context (a longer one records
@@ -592,7 +601,13 @@ int pa_verify_tree(const void* q, const int32_t* q_start, const uint64_t* tree_m
  *                 request of the call has, records PA_DEVERR_SCORE_ROW and the
  *                 request keeps no score either.
  *   workspace     at least pa_decode_accumulate_workspace_size(...) bytes: the
- *                 partials, and the logits of the call
+ *                 partials, and the logits of the call: 4 bytes per request, KV
+ *                 head, query head of its group (their number rounded up to 1, 2
+ *                 or a multiple of 4) and token that the TABLE has room for; the
+ *                 second pass has a block of threads for each stretch of it, too.
+ *                 So cut the tables to the longest context: 64 requests of <= 4079
+ *                 tokens, 32/8 heads, take 45 MB and 96 us then, 1.1 GB and 341 us
+ *                 with tables for 131072
  *   split_tokens  as pa_decode; 0 = the library's choice for this call, which
  *                 also depends on num_seqs and kv_heads
  *                 (pa_decode_accumulate_split_tokens tells it)

@@ -47,7 +47,9 @@
 //               maximum m is raised only when a row maximum exceeds it by
 //               more than 2^8 (O is then rescaled in TMEM, once P.V_x(j-1)
 //               has completed); the final O / sum uses the same m, so this is
-//               exact.
+//               exact.  P is rounded to the type of V, as the MMA takes both
+//               operands in 16 bits: half a step of each weight; the sum is of
+//               the unrounded ones, in fp32.
 // Q and K are K-major and V is MN-major in the canonical 128-byte-swizzled
 // shared-memory layouts.  Every mbarrier wait is bounded.
 //
@@ -59,6 +61,9 @@
 // non-finite elements (tree.cuh).  A context may be cut into partitions of
 // split_tokens keys, a unit each, whose partials a merge combines.  A unit of
 // at most 128 rows leaves tile B alone: its issuer only frees the stages.
+// Measured on GB300, 64 equal contexts of 512 to 4096 tokens, 8 KV heads (four
+// rounds of units): 47 us plus 50 us per thousand tokens with 256 rows, 36 plus
+// 50 with 132, so about 12 us a unit to start and end, with nothing under it.
 // Blocks of 4 tokens (QUAD) come in boxes of half a swizzle atom (tree.cuh).
 #include <float.h>
 

@@ -32,7 +32,9 @@
 //               TMEM, all D columns by the warp of the low key half, before
 //               either half of the tile's P.V, each of which adds to every
 //               column, can start); the final O / sum uses the same m, so
-//               this is exact.
+//               this is exact.  P is rounded to the type of V, as the MMA
+//               takes both operands in 16 bits: half a step of each weight;
+//               the sum is of the unrounded ones, in fp32.
 //               A warp whose 32 rows are all past the unit's rows skips the
 //               arithmetic and only keeps the barrier phases.  The next
 //               unit's Q rows are staged in shared memory by cp.async.

@@ -41,8 +41,9 @@ __device__ __forceinline__ uint32_t score_key(float x) {
 // Bound by the instructions and atomics per key and the latency of the steps
 // between (memory is 4 bytes per candidate): keys stay in shared memory as far
 // as that leaves every CTA resident at once, and the rest are read again from
-// L2.  Measured on GB300: 512 rows of 2300 keys 8.6 us, 64 of 85000 21 us, 8 of
-// 131000 14 us.  A range for the threshold from a sample of the row, to save
+// L2.  Measured on GB300: 512 rows of 2300 keys 8.7 us, 64 of 85000 20 us, 8 of
+// 131000 13 us; 64 of 32768 to 131009, where the longest row's CTAs decide (every
+// row's cluster is the same), 34 us.  A range for the threshold from a sample of the row, to save
 // most atomics, was slower: the sample's own steps cost more.
 constexpr int kSelBins = 2048;
 constexpr int kSelSlices = 16;
@@ -641,7 +642,7 @@ cudaError_t launch_evict_select(const EvictSelectParams& p0, int num_seqs, cudaS
   // both (an earlier form, 64 rows of 85000 keys: clusters of 2, 4, 8 of 1024
   // threads 30, 42, 80 us; of 512 threads 41, 34, 56).  More rows than SMs: small
   // CTAs, the steps between the keys cost what short rows do (512 rows of 2300:
-  // 256 threads 15.5 us, 512 17.2, 1024 32.3).
+  // 256 threads 8.7 us, 512 12.7, 1024 22.5).
   const int64_t rows = (int64_t)p.kv_heads * num_seqs, sms = num_sms() > 0 ? num_sms() : 152;
   int cluster = 1;
   while (cluster < 8 && rows * cluster * 2 <= sms && (int64_t)cluster * 1024 < p.score_len) cluster *= 2;

@@ -1170,8 +1170,12 @@ int tree_setup(int num_reqs, int total_q, int max_q_len, int q_heads, int kv_hea
     // per row) then cost more than the balance brings.  Measured on GB300, 64
     // requests of <= 4096 tokens, 8 KV heads: whole 132 us, 2048-token
     // partitions 153 us (80..128 rows); 162 and 190 us (104..240 rows); whole
-    // and in order of length 127 and 143.  Fewer units are cut until seven SMs
-    // in eight have one, where a partition then is short: starting and ending
+    // and in order of length 127 and 143.  The number of units alone decides: a
+    // context far longer than the rest of such a batch is still walked whole, by
+    // one CTA per KV head (one of 131008 among 63 of 1000..3000, 26..60 nodes:
+    // whole 1610 us, 4096-token partitions 365, 16384 271; without it 136), and
+    // a caller that has one gives split_tokens.  Fewer units are cut until seven
+    // SMs in eight have one, where a partition then is short: starting and ending
     // it takes 6 to 8 us, as much as 800 tokens (us at that and at four per SM:
     // a context of 8000, 32 rows 15 and 23; one of 32000, 64 rows 30 and 62,
     // and 36 with a unit on nearly every SM; 8 of <= 4000, 64 rows 25 and 36).

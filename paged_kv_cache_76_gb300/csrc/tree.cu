@@ -6,7 +6,7 @@
 // (request, KV head) take attn_tile.cu's (128-key tiles; one Q tile), more
 // attn_tc.cu's (two Q tiles of 128 rows share every 64-key K/V tile).  Measured
 // on GB300, 64 requests of 509..4079 tokens, 32/8 heads: 20..32 nodes 125 us on
-// the first; 26..60 nodes 146 us on the second; before the requests ran in
+// the first; 26..60 nodes 147 us on the second; before the requests ran in
 // order of length 132 and 162 us, and the latter 215 us as two row tiles of
 // the first (K and V once more through L2).  Before them a warp-MMA kernel took 347
 // and 509 us.

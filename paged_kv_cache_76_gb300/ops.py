@@ -685,7 +685,8 @@ def _tree_workspace(dev, *sizes) -> int:  # dev: the choice depends on the curre
 def verify_tree(q, q_start, tree_mask, context_lens, k_cache, v_cache, block_tables, scale, max_q_len, out=None,
                 split_tokens=0, workspace=None, stream=None):
     """pa_verify_tree: ``q`` is [total_q, q_heads, head_dim], packed by ``q_start``; bit m of ``tree_mask[i]`` (int64)
-    lets row i see its request's node m.  Every row sees the context before the draft."""
+    lets row i see its request's node m.  Every row sees the context before the draft.  ``scale`` is positive.
+    ``split_tokens`` 0 runs large batches whole: give one (16384, say) where a context is far longer than the rest."""
     if workspace is None and _short_way(stream):
         r = _marshal.verify_tree(q, q_start, tree_mask, context_lens, k_cache, v_cache, block_tables, scale, max_q_len,
                                  out, split_tokens)
@@ -751,7 +752,10 @@ def decode_accumulate(q, k_cache, v_cache, block_tables, context_lens, scale, sc
                       scores_out=None, out=None, split_tokens=0, workspace=None, stream=None):
     """pa_decode_accumulate: :func:`decode`, and each cached token's attention weight (summed over the query heads of
     its KV head) added to its score.  ``scores``: fp32 [rows, kv_heads, length], request r's row is ``score_rows[r]``
-    (None: r; negative: no score).  ``scores_out`` None: in place.  Returns (out, scores_out)."""
+    (None: r; negative: no score).  ``scores_out`` None: in place.  Returns (out, scores_out).
+
+    Prompts and drafts keep no score: only this call's queries do.  The scratch and the second pass grow with the
+    width of ``block_tables``, so cut them to the longest context."""
     if workspace is None and _short_way(stream):
         r = _marshal.decode_accumulate(q, k_cache, v_cache, block_tables, context_lens, scale, scores, score_rows,
                                        scores_out, out, split_tokens)
