@@ -422,7 +422,8 @@ def decode_shared_prefix(q, k_cache, v_cache, prefix_blocks, prefix_len, block_t
 
     ``prefix_stream`` (a torch.cuda.Stream): run the prefix pass there,
     concurrently with the suffix pass; the caller orders it after the writes
-    of ``q``, the prefix's K/V and the previous use of ``workspace``."""
+    of ``q``, the prefix's K/V and the previous use of ``workspace`` (None:
+    after all that is under way on ``stream``, whose memory it is)."""
     nb, bs, hkv, d = _cache_dims(k_cache)
     B, hq, dq = q.shape
     if dq != d:
