@@ -677,6 +677,83 @@ int pa_compact_kv(void* k_cache, void* v_cache, const int32_t* block_tables, int
                   int kv_heads, int head_dim, pa_dtype dtype, float* scores, const int32_t* score_rows, int num_rows,
                   int score_len, pa_stream stream);
 
+/* ============================================================================
+ * A paged cache held in 4 bits.
+ *
+ * An element is one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 with a sign (e2m1), times the
+ * scale of its 16 neighbours along the head: a byte with five exponent bits and
+ * three of mantissa, bits 14..7 of the same number in fp16.  4.5 bits an
+ * element, 0.28 of the 16-bit cache; every element is exact in fp16 and bf16.
+ *
+ * Layout: k_cache and v_cache are byte arrays [num_blocks][kv_heads][page], a
+ * page (one block of one KV head) being block_size * head_dim * 9 / 16 bytes:
+ * block_size rows of head_dim / 2 bytes of codes (byte i: element 2i in the low
+ * four bits, 2i + 1 in the high; bit 3 of a code is its sign), then block_size
+ * rows of head_dim / 16 scales.  Blocks, Block Tables, slots and context lengths
+ * are those of the 16-bit cache; a block's bytes are contiguous, so
+ * pa_copy_pages moves them.  dtype below is that of k, v, q and out.
+ * ========================================================================== */
+
+/* ----------------------------------------------------------------------------
+ * pa_quantize_and_cache - pa_reshape_and_cache into a 4-bit cache.
+ *
+ * For each group of 16 elements x of a token's head
+ *     s = the scale nearest to max|x| / 6 (ties to the even byte; at most 10240,
+ *         2^-17 apart below 2^-14)
+ *     element = the level nearest to x / s (ties to the even code), times s
+ * both decided as by exact quotients.  Larger magnitudes than 61440 become
+ * that; a group whose scale rounds to 0 becomes zeros; a group with an element
+ * that is not finite is held as NaN (scale byte 0xFF).
+ *   k, v          [num_tokens][kv_heads][head_dim] with k_stride / v_stride
+ *                 elements between tokens (a multiple of 8, at least
+ *                 kv_heads * head_dim), so that both may be views of one
+ *                 projection's rows
+ * Other arguments and errors as pa_reshape_and_cache.
+ * ------------------------------------------------------------------------- */
+int pa_quantize_and_cache(const void* k, const void* v, int64_t k_stride, int64_t v_stride, const int32_t* slot_mapping,
+                          int num_tokens, void* k_cache, void* v_cache, int num_blocks, int block_size, int kv_heads,
+                          int head_dim, pa_dtype dtype, pa_stream stream);
+
+/* ----------------------------------------------------------------------------
+ * pa_dequantize_kv4 - tokens of a 4-bit cache in 16 bits (exactly).
+ *
+ *   slots         int32 [num_tokens], repeats allowed; a negative slot gives
+ *                 zeros, a slot past the pool zeros and PA_DEVERR_SLOT
+ *   k, v          [num_tokens][kv_heads][head_dim]
+ * ------------------------------------------------------------------------- */
+int pa_dequantize_kv4(const void* k_cache, const void* v_cache, const int32_t* slots, int num_tokens, int num_blocks,
+                      int block_size, int kv_heads, int head_dim, void* k, void* v, pa_dtype dtype, pa_stream stream);
+
+/* ----------------------------------------------------------------------------
+ * pa_decode_kv4 - pa_decode (q_len 1) and pa_verify_decode (q_len causal queries
+ * per request) over a 4-bit cache.
+ *
+ *   q, out        [num_seqs][q_len][q_heads][head_dim]; query i of request r sees
+ *                 tokens [0, context_lens[r] - (q_len-1-i)); one that sees none
+ *                 gives a zero row
+ *   q_len         >= 1, with (q_heads / kv_heads) * q_len <= 32 and a group of at
+ *                 most 16
+ *   split_tokens  0, or a multiple of 32 no larger than 256 * block_size;
+ *                 pa_decode_kv4_split_tokens returns the partition size such a
+ *                 call uses, or PA_ERR_INVALID
+ *   workspace     at least pa_decode_kv4_workspace_size(...) bytes (NULL where
+ *                 that is 0)
+ * Sums and softmax are fp32; weights are rounded to fp16 for the P.V product
+ * (relative error 2^-11), the cache's elements and q are not rounded.  A token
+ * that a query does not see leaves it as it is, whatever the token holds (NaN
+ * included).  A bad block id records PA_DEVERR_BLOCK_ID and reads as zeros.
+ * ------------------------------------------------------------------------- */
+int pa_decode_kv4_split_tokens(int num_seqs, int q_len, int q_heads, int kv_heads, int max_blocks_per_seq,
+                               int block_size, int split_tokens);
+
+size_t pa_decode_kv4_workspace_size(int num_seqs, int q_len, int q_heads, int kv_heads, int head_dim,
+                                    int max_blocks_per_seq, int block_size, int split_tokens);
+
+int pa_decode_kv4(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                  int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int q_len, int q_heads,
+                  int kv_heads, int head_dim, int block_size, int num_blocks, float scale, int split_tokens,
+                  void* workspace, size_t workspace_bytes, void* out, pa_dtype dtype, pa_stream stream);
+
 /* Read and clear the calling device's error word.  Synchronises `stream`.
  * *host_code receives the PA_DEVERR_* code (0 = none).  Returns
  * PA_ERR_DEVICE_CHECK if a code was recorded, PA_OK otherwise. */

@@ -111,6 +111,11 @@ PROTOTYPES = {
                                   _P, _I, _P]),
     "pa_evict_select": (_I, [_P, _P, _I, _I, _I, _P, _I, _I, _I, _I, _P, _P, _P]),
     "pa_compact_kv": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I, _I, _P]),
+    "pa_quantize_and_cache": (_I, [_P, _P, C.c_int64, C.c_int64, _P, _I, _P, _P, _I, _I, _I, _I, _I, _P]),
+    "pa_dequantize_kv4": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _P]),
+    "pa_decode_kv4_split_tokens": (_I, [_I, _I, _I, _I, _I, _I, _I]),
+    "pa_decode_kv4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "pa_decode_kv4": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P, _I, _P]),
     "pa_get_device_error": (_I, [_I32P, _P]),
     "pa_alloc_create": (_I, [_I, _I, _I32P, C.POINTER(_P)]),
     "pa_alloc_destroy": (None, [_P]),

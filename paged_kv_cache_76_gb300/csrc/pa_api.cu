@@ -43,19 +43,6 @@ int current_device() {
   return d;
 }
 
-// Device address of the error word on the current device (set up once).
-int* device_error_ptr() {
-  const int d = current_device();
-  if (d < 0 || d >= kMaxDevices) return nullptr;
-  std::lock_guard<std::mutex> lk(g_mu);
-  if (!g_err_ptr[d]) {
-    void* p = nullptr;
-    if (cudaGetSymbolAddress(&p, g_device_error) != cudaSuccess) return nullptr;
-    g_err_ptr[d] = static_cast<int*>(p);
-  }
-  return g_err_ptr[d];
-}
-
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
   std::lock_guard<std::mutex> lk(g_mu);
   if (!g_encode) {
@@ -275,6 +262,19 @@ int shared_prefix_setup(int num_seqs, int q_heads, int head_dim, int max_blocks_
 void note_launch(int n) { g_launches.fetch_add((uint64_t)n, std::memory_order_relaxed); }
 
 int num_sms() { return sm_count(); }
+
+// Device address of the error word on the current device (set up once).
+int* device_error_ptr() {
+  const int d = current_device();
+  if (d < 0 || d >= kMaxDevices) return nullptr;
+  std::lock_guard<std::mutex> lk(g_mu);
+  if (!g_err_ptr[d]) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_device_error) != cudaSuccess) return nullptr;
+    g_err_ptr[d] = static_cast<int*>(p);
+  }
+  return g_err_ptr[d];
+}
 
 }  // namespace pa
 

@@ -15,6 +15,9 @@ namespace pa {
 // Counts kernel launches (pa_launch_count).
 void note_launch(int n = 1);
 
+// Device address of the current device's error word; null if it cannot be had.
+int* device_error_ptr();
+
 // Launch with programmatic stream serialisation (programmatic dependent
 // launch): the kernel may start while the previous kernel on the stream is
 // finishing; it synchronises with griddepcontrol.wait before touching memory
@@ -288,5 +291,49 @@ struct AccumulateParams {
 };
 cudaError_t launch_merge_accumulate(const MergeParams& mp, const AccumulateParams& ap, int head_dim, pa_dtype dt,
                                     cudaStream_t stream);
+
+// 4-bit paged cache (kv4.cuh).
+struct Kv4WriteParams {
+  const void* k;
+  const void* v;
+  int64_t k_stride, v_stride;  // elements between tokens
+  const int32_t* slots;
+  void* k_cache;
+  void* v_cache;
+  int* err;
+  int64_t num_tokens, num_slots;
+  int kv_heads, block_size;
+};
+cudaError_t launch_quantize_and_cache(const Kv4WriteParams& p, int head_dim, pa_dtype dt, cudaStream_t stream);
+
+struct Kv4ReadParams {
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* slots;
+  void* k;  // [num_tokens][kv_heads][head_dim]
+  void* v;
+  int* err;
+  int64_t num_tokens, num_slots;
+  int kv_heads, block_size;
+};
+cudaError_t launch_dequantize_kv4(const Kv4ReadParams& p, int head_dim, pa_dtype dt, cudaStream_t stream);
+
+struct Kv4DecodeParams {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* tables;
+  const int32_t* lens;
+  void* out;
+  float* part_o;  // as DecodeParams
+  float* part_m;
+  float* part_l;
+  int* err;
+  int maxblk, num_seqs, q_len, q_heads, kv_heads, group, num_blocks, block_size, block_shift;
+  int split_tokens, max_splits, tab_entries;
+  float scale_log2;
+};
+// without the merge (launch_lse_merge)
+cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int head_dim, pa_dtype dt, cudaStream_t stream);
 
 }  // namespace pa

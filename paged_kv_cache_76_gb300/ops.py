@@ -47,6 +47,12 @@ __all__ = [
     "decode_accumulate_workspace_size",
     "evict_select",
     "compact_kv",
+    "kv4_cache",
+    "quantize_and_cache",
+    "dequantize_kv4",
+    "decode_kv4",
+    "decode_kv4_split_tokens",
+    "decode_kv4_workspace_size",
     "get_device_error",
     "selftest_wait_timeout",
     "launch_count",
@@ -869,6 +875,123 @@ def compact_kv(k_cache, v_cache, block_tables, context_lens, keep, keep_lens, ba
     _launch(
         "pa_compact_kv", kc, vc, tables, block_tables.shape[1], lens, lists, kshape[1], kshape[2], nkeep, first, B, nb,
         bs, hkv, d, dtype_code(k_cache.dtype), sc, rows, nrows, length, handle)
+
+
+# ----------------------------------------------------------------------------
+# a cache held in 4 bits
+# ----------------------------------------------------------------------------
+def kv4_cache(num_blocks, block_size, kv_heads, head_dim, device="cuda"):
+    """A cache of 4-bit elements, uint8 [num_blocks, kv_heads, block_size * head_dim * 9 / 16], all zeros: one of K or
+    of V.  The calls find block_size from its shape and the head_dim of the 16-bit tensors."""
+    if block_size not in (4, 8, 16, 32) or head_dim not in (64, 128):
+        raise ValueError("block_size is 4, 8, 16 or 32, head_dim 64 or 128")
+    return torch.zeros((num_blocks, kv_heads, block_size * head_dim * 9 // 16), dtype=torch.uint8, device=device)
+
+
+def _kv4_ptrs(k_cache, v_cache, dev: int, d: int):
+    """(k, v) pointers of two 4-bit caches and their (num_blocks, block_size, kv_heads)."""
+    shape = k_cache.shape
+    if len(shape) != 3 or k_cache.dtype != torch.uint8:
+        raise ValueError("4-bit caches are uint8 [num_blocks, kv_heads, page bytes]")
+    if v_cache.shape != shape or v_cache.dtype != torch.uint8:
+        raise ValueError("k_cache and v_cache must agree in shape, dtype and device")
+    bs, rest = divmod(shape[2] * 16, 9 * d) if d > 0 else (0, 1)
+    if rest or bs not in (4, 8, 16, 32):
+        raise ValueError(f"pages of {shape[2]} bytes are not those of blocks of 4, 8, 16 or 32 tokens of head_dim {d}")
+    return _ptr(k_cache, "k_cache", dev), _ptr(v_cache, "v_cache", dev), shape[0], bs, shape[1]
+
+
+def quantize_and_cache(k, v, slot_mapping, k_cache, v_cache, stream=None):
+    """pa_quantize_and_cache: :func:`reshape_and_cache` into a 4-bit cache.  ``k`` and ``v`` ([num_tokens, kv_heads,
+    head_dim]) may be views of one projection's rows."""
+    if k.dim() != 3 or v.shape != k.shape:
+        raise ValueError("k and v are [num_tokens, kv_heads, head_dim] of the cache")
+    dtype, dev = k.dtype, k.get_device()
+    T, hkv, d = k.shape
+    kc, vc, nb, bs, heads = _kv4_ptrs(k_cache, v_cache, dev, d)
+    if heads != hkv:
+        raise ValueError(f"the caches have {heads} heads, k and v {hkv}")
+    code = dtype_code(dtype)
+    ks = _token_rows(k, "k", hkv, d, dtype, dev)
+    vs = _token_rows(v, "v", hkv, d, dtype, dev)
+    sl = _rows_ptr(slot_mapping, "slot_mapping", dev, T)
+    _launch("pa_quantize_and_cache", k.data_ptr(), v.data_ptr(), ks, vs, sl, T, kc, vc, nb, bs, hkv, d, code,
+            _stream_on(dev, stream))
+
+
+def dequantize_kv4(k_cache, v_cache, slots, head_dim, dtype=torch.bfloat16, k=None, v=None, stream=None):
+    """pa_dequantize_kv4: K and V of the tokens at ``slots`` in 16 bits, each [num_tokens, kv_heads, head_dim] (exact;
+    zeros where a slot is negative)."""
+    dev, d, code = k_cache.get_device(), int(head_dim), dtype_code(dtype)
+    kc, vc, nb, bs, hkv = _kv4_ptrs(k_cache, v_cache, dev, d)
+    T = slots.shape[0] if slots.dim() == 1 else -1
+    sl = _rows_ptr(slots, "slots", dev, T)
+    handle = _stream_on(dev, stream)
+    shape = (T, hkv, d)
+    out = []
+    for name, t in (("k", k), ("v", v)):
+        if t is None:
+            t = _empty(shape, dtype, k_cache.device, stream, returned=True)
+        elif t.shape != shape or t.dtype != dtype:
+            raise ValueError(f"{name} is {dtype} {list(shape)}")
+        out.append(t)
+    _keep(*out)
+    _launch("pa_dequantize_kv4", kc, vc, sl, T, nb, bs, hkv, d, _ptr(out[0], "k", dev), _ptr(out[1], "v", dev), code,
+            handle)
+    return tuple(out)
+
+
+def decode_kv4_split_tokens(num_seqs, q_len, q_heads, kv_heads, max_blocks_per_seq, block_size, split_tokens=0) -> int:
+    """Partition size such a pa_decode_kv4 call uses (0: its automatic choice)."""
+    return check(_lib.lib().pa_decode_kv4_split_tokens(int(num_seqs), int(q_len), int(q_heads), int(kv_heads),
+                                                       int(max_blocks_per_seq), int(block_size), int(split_tokens)),
+                 "pa_decode_kv4_split_tokens")
+
+
+def decode_kv4_workspace_size(num_seqs, q_len, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size,
+                              split_tokens=0) -> int:
+    return int(_lib.lib().pa_decode_kv4_workspace_size(num_seqs, q_len, q_heads, kv_heads, head_dim,
+                                                       max_blocks_per_seq, block_size, split_tokens))
+
+
+@functools.lru_cache(maxsize=4096)
+def _kv4_workspace(dev, *sizes) -> int:  # dev: the choice depends on the current device
+    return decode_kv4_workspace_size(*sizes)
+
+
+def _scratch(workspace, n: int, device, dev: int, stream):
+    """(the workspace, its pointer and bytes): the caller's, or one of n bytes."""
+    if workspace is None:
+        if not n:
+            return None, None, 0
+        workspace = _empty(n, torch.uint8, device, stream)
+    return workspace, _ptr(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
+
+
+def decode_kv4(q, k_cache, v_cache, block_tables, context_lens, scale, out=None, split_tokens=0, workspace=None,
+               stream=None):
+    """pa_decode_kv4: :func:`decode` (``q`` [num_seqs, q_heads, head_dim]) or :func:`verify_decode` (``q`` [num_seqs,
+    q_len, q_heads, head_dim]) over a 4-bit cache."""
+    if q.dim() not in (3, 4):
+        raise ValueError("q is [num_seqs, q_heads, head_dim] or [num_seqs, q_len, q_heads, head_dim]")
+    dtype, dev, qshape = q.dtype, q.get_device(), q.shape
+    B, ql, hq, d = (qshape[0], 1, qshape[1], qshape[2]) if len(qshape) == 3 else qshape
+    kc, vc, nb, bs, hkv = _kv4_ptrs(k_cache, v_cache, dev, d)
+    code = dtype_code(dtype)
+    tables = _table_ptr(block_tables, dev, B)
+    lens = _rows_ptr(context_lens, "context_lens", dev, B)
+    if out is None:
+        out = _empty(qshape, dtype, q.device, stream, returned=True)
+    elif out.shape != qshape or out.dtype != dtype:
+        raise ValueError("out must have q's shape, dtype and device")
+    handle = _stream_on(dev, stream)
+    maxblk, split_tokens = block_tables.shape[1], int(split_tokens)
+    n = _kv4_workspace(dev, B, ql, hq, hkv, d, maxblk, bs, split_tokens) if workspace is None else 0
+    workspace, ws_ptr, ws_bytes = _scratch(workspace, n, q.device, dev, stream)
+    _keep(out, workspace)
+    _launch("pa_decode_kv4", _ptr(q, "q", dev), kc, vc, tables, maxblk, lens, B, ql, hq, hkv, d, bs, nb, float(scale),
+            split_tokens, ws_ptr, ws_bytes, _ptr(out, "out", dev), code, handle)
+    return out
 
 
 def selftest_wait_timeout(wait_ms: int = 50, stream=None) -> None:
