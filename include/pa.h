@@ -76,7 +76,9 @@ enum {
   PA_DEVERR_QUERY_RANGE = 5,  /* bad q_start / chunk length in chunked prefill          */
   PA_DEVERR_POSITION = 6,     /* rotary position outside [0, max_position)              */
   PA_DEVERR_SCORE_ROW = 7,    /* score row outside the score array, or used twice       */
-  PA_DEVERR_KEEP = 8          /* keep list: bad count, base, or an entry out of range   */
+  PA_DEVERR_KEEP = 8,         /* keep list: bad count, base, or an entry out of range   */
+  PA_DEVERR_FORK = 9,         /* fork: parent >= num_seqs, or growth outside [0, max]   */
+  PA_DEVERR_NO_BLOCKS = 10    /* fork: fewer free blocks than the new rows need         */
 };
 
 typedef struct CUstream_st* pa_stream; /* identical to cudaStream_t */
@@ -753,6 +755,71 @@ int pa_decode_kv4(const void* q, const void* k_cache, const void* v_cache, const
                   int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int q_len, int q_heads,
                   int kv_heads, int head_dim, int block_size, int num_blocks, float scale, int split_tokens,
                   void* workspace, size_t workspace_bytes, void* out, pa_dtype dtype, pa_stream stream);
+
+/* ----------------------------------------------------------------------------
+ * pa_fork_blocks - sequences that go on from others: tables, pages and slots of
+ * a batch's next step, worked out on the device.
+ *
+ * A step of beam search, several samples of one prompt, a batch that sequences
+ * leave and join: new row i goes on from row parents[i] of block_tables and
+ * grows by grow[i] tokens, without a copy of what it has read so far and
+ * without a trip to the host.  With L = context_lens[parents[i]] (0 for a new
+ * sequence) and bs = block_size:
+ *   - tables_out[i] holds the parent's ceil(L / bs) blocks, shared;
+ *   - if it grows and L % bs != 0 it goes on inside its last block, which no one
+ *     else may hold then: of the rows that go on inside one block the lowest
+ *     keeps it, if every row of the new batch that holds the block is one of
+ *     them and the block is not pinned; each other gets a fresh block there and
+ *     pairs[i] = (old, fresh), a copy for pa_copy_pages to make before anything
+ *     writes; otherwise pairs[i] = (-1, -1);
+ *   - fresh blocks follow for the tokens up to L + grow[i]; -1 behind them;
+ *   - lens_out[i] = L + grow[i], and slots[i][t] is the slot of token L + t for
+ *     t < grow[i], -1 for the others of max_grow.
+ * Fresh blocks are those that no row of the new batch shares and that are not
+ * pinned, in ascending order, given out row by row (a copy's first).  So the
+ * blocks of rows that nothing goes on from are free at once, and num_free
+ * [1] says how many are left.  The tables are all that says who holds a block:
+ * every sequence of the pool is in the batch, or its blocks are pinned.  Where
+ * the blocks do not suffice PA_DEVERR_NO_BLOCKS is recorded and the new batch is
+ * empty (tables, pairs and slots -1, lengths 0, num_free the free ones): nothing
+ * is lost, since the old tables are as they were.
+ *   parents       int32 [num_new]; -1: a new sequence; below: no sequence, an
+ *                 empty row that neither holds nor grows
+ *   grow          int32 [num_new], each in [0, max_grow]; NULL: max_grow for all
+ *   pinned        uint8 [num_blocks], not 0: never handed out nor written; NULL:
+ *                 none
+ *   max_blocks_out  columns of tables_out
+ *   workspace     at least pa_fork_blocks_workspace_size(...) bytes, 16-byte
+ *                 aligned; needs no initialisation
+ * Up to 65535 rows on either side.  Outputs and workspace overlap neither an
+ * input nor one another.  A parent >= num_seqs or a growth out of range records
+ * PA_DEVERR_FORK, a parent's length outside its table or a new one past
+ * max_blocks_out PA_DEVERR_CONTEXT_LEN, and the row is as one without a
+ * sequence.  A bad block id records PA_DEVERR_BLOCK_ID and stays in the table.
+ * ------------------------------------------------------------------------- */
+size_t pa_fork_blocks_workspace_size(int num_new, int num_blocks);
+
+int pa_fork_blocks(const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                   const int32_t* parents, int num_new, const int32_t* grow, int max_grow, const uint8_t* pinned,
+                   int num_blocks, int block_size, int32_t* tables_out, int max_blocks_out, int32_t* lens_out,
+                   int32_t* pairs, int32_t* slots, int32_t* num_free, void* workspace, size_t workspace_bytes,
+                   pa_stream stream);
+
+/* ----------------------------------------------------------------------------
+ * pa_copy_pages - block copies in any number of caches at once.
+ *
+ * In every cache c, block pairs[2p+1] becomes a bit-exact copy of block
+ * pairs[2p]; a pair whose source is negative is none.
+ *   caches        HOST array of num_caches device pointers, 16-byte aligned:
+ *                 caches of any type whose blocks are block_bytes contiguous
+ *                 bytes (a multiple of 16) - K and V of every layer, of 16 bits
+ *                 or 4
+ *   pairs         int32 [num_pairs][2], device memory, as pa_copy_blocks (pairs
+ *                 of pa_fork_blocks as they are)
+ * Ids outside [0, num_blocks) record PA_DEVERR_BLOCK_ID, the pair is skipped.
+ * ------------------------------------------------------------------------- */
+int pa_copy_pages(void* const* caches, int num_caches, const int32_t* pairs, int num_pairs, int num_blocks,
+                  int64_t block_bytes, pa_stream stream);
 
 /* Read and clear the calling device's error word.  Synchronises `stream`.
  * *host_code receives the PA_DEVERR_* code (0 = none).  Returns

@@ -35,6 +35,8 @@ PA_DEVERR_QUERY_RANGE = 5
 PA_DEVERR_POSITION = 6
 PA_DEVERR_SCORE_ROW = 7
 PA_DEVERR_KEEP = 8
+PA_DEVERR_FORK = 9
+PA_DEVERR_NO_BLOCKS = 10
 
 
 class LibraryMissing(RuntimeError):
@@ -116,6 +118,9 @@ PROTOTYPES = {
     "pa_decode_kv4_split_tokens": (_I, [_I, _I, _I, _I, _I, _I, _I]),
     "pa_decode_kv4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "pa_decode_kv4": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P, _I, _P]),
+    "pa_fork_blocks_workspace_size": (_SZ, [_I, _I]),
+    "pa_fork_blocks": (_I, [_P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "pa_copy_pages": (_I, [_P, _I, _P, _I, _I, C.c_int64, _P]),
     "pa_get_device_error": (_I, [_I32P, _P]),
     "pa_alloc_create": (_I, [_I, _I, _I32P, C.POINTER(_P)]),
     "pa_alloc_destroy": (None, [_P]),

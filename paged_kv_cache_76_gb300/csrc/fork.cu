@@ -1,0 +1,397 @@
+// Pages of the cache shared, copied, taken and given back on the device:
+// pa_fork_blocks (Block Tables of sequences that go on from others) and
+// pa_copy_pages (the copies it asks for, in any number of caches).
+//
+// fork_blocks keeps no counts from call to call.  What a page is, follows from
+// the tables that go on: state[b] of block b is
+//   kFree  no new row holds it;
+//   i >= 0 only rows that go on writing inside it hold it, i the first of them:
+//          row i keeps it, the others get copies;
+//   kHeld  some row holds it and does not write inside it: writers get copies.
+// A holder that does not write stores kHeld, a writer takes the minimum with its
+// row, so the order of either does not change what comes out, and nothing but
+// one word per writing row is atomic.  Then free pages (kFree and not pinned) go
+// to the rows in order of their number, so equal calls give equal tables.
+//
+//   clear   state = kFree
+//   mark    a warp per (old row, 512 columns): if a new row goes on from it, its
+//           blocks; the pages that new rows write in
+//   count   free pages of each warp's span of blocks; pages that each row needs,
+//           summed up
+//   list    the first free pages, as many as are needed, in order
+//   write   tables, lengths, pairs and slots
+//
+// The steps are dependent and small: a table of 64 sequences of 4096 tokens is
+// 64 KB.  So up to kFusedWork entries they are one launch of one cluster of
+// eight CTAs with its barrier between them; above it each step is a launch over
+// the whole GPU.
+#include "pa_device.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kFree = 0x7F7F7F7F;
+constexpr int kHeld = -1;
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kThreads = 512;
+constexpr int kWarpsPerCta = kThreads / 32;
+constexpr int kColumns = 512;  // of a row that a warp takes at a time
+constexpr int kCluster = 8;
+
+struct Row {
+  int parent;  // < 0: none
+  int len, have, want;  // tokens; pages of them, and with the new tokens
+  int grow;
+  int tail;    // page it goes on inside, or -1
+  int bad;     // error code of a row that is dropped
+};
+
+__device__ __forceinline__ Row fork_row(const ForkParams& p, int i) {
+  Row w{};
+  w.parent = -1;
+  w.tail = -1;
+  const int parent = __ldcg(p.parents + i);
+  if (parent < -1) return w;  // no sequence
+  if (parent >= p.num_old) {
+    w.bad = PA_DEVERR_FORK;
+    return w;
+  }
+  const int grow = p.grow ? __ldcg(p.grow + i) : p.max_grow;
+  if (grow < 0 || grow > p.max_grow) {
+    w.bad = PA_DEVERR_FORK;
+    return w;
+  }
+  const int len = parent < 0 ? 0 : __ldcg(p.lens + parent);
+  if (len < 0 || len > p.maxblk * p.block_size) {
+    w.bad = PA_DEVERR_CONTEXT_LEN;
+    return w;
+  }
+  const int have = (len + p.block_size - 1) >> p.block_shift;
+  const int64_t want = ((int64_t)len + grow + p.block_size - 1) >> p.block_shift;
+  if (want > p.maxblk_out) {
+    w.bad = PA_DEVERR_CONTEXT_LEN;
+    return w;
+  }
+  w.parent = parent;
+  w.len = len;
+  w.have = have;
+  w.want = (int)want;
+  w.grow = grow;
+  if (parent >= 0 && grow > 0 && (len & (p.block_size - 1))) {
+    const int b = __ldcg(p.tables + (size_t)parent * p.maxblk + have - 1);
+    if (b >= 0 && b < p.num_blocks) w.tail = b;
+  }
+  return w;
+}
+
+// Does row i, which goes on inside page w.tail, need a copy of it?
+__device__ __forceinline__ bool needs_copy(const ForkParams& p, const Row& w, int i) {
+  return w.tail >= 0 && (__ldcg(p.state + w.tail) != i || (p.pinned && __ldg(p.pinned + w.tail)));
+}
+
+__device__ __forceinline__ bool is_free(const ForkParams& p, int b) {
+  return __ldcg(p.state + b) == kFree && !(p.pinned && __ldg(p.pinned + b));
+}
+
+__device__ void step_clear(const ForkParams& p, int rank, int ranks) {
+  for (int b = rank * kThreads + threadIdx.x; b < p.num_blocks; b += ranks * kThreads) p.state[b] = kFree;
+}
+
+__device__ void step_mark(const ForkParams& p, int rank, int ranks) {
+  const int lane = threadIdx.x & 31;
+  const int chunks = (p.maxblk + kColumns - 1) / kColumns;
+  const int64_t items = (int64_t)p.num_old * chunks;
+  for (int64_t it = (int64_t)rank * kWarpsPerCta + (threadIdx.x >> 5); it < items;
+       it += (int64_t)ranks * kWarpsPerCta) {
+    const int old = (int)(it / chunks), c0 = (int)(it - (int64_t)old * chunks) * kColumns;
+    // the new rows that go on from this one: any at all, any that leaves its tail as it is
+    bool some = false, rests = false;
+    int have = 0;
+    for (int i = lane; i < p.num_new; i += 32) {
+      if (__ldcg(p.parents + i) != old) continue;
+      const Row w = fork_row(p, i);
+      if (w.parent < 0) continue;
+      some = true;
+      have = w.have;
+      if (w.tail >= 0) {
+        if (c0 == 0) atomicMin(p.state + w.tail, i);
+      } else {
+        rests = true;
+      }
+    }
+    some = __any_sync(kAll, some);
+    if (!some) continue;
+    rests = __any_sync(kAll, rests);
+    have = __reduce_max_sync(kAll, have);
+    const int end = min(have - (rests ? 0 : 1), c0 + kColumns);
+    const int32_t* row = p.tables + (size_t)old * p.maxblk;
+    bool bad = false;
+    for (int j = c0 + lane; j < end; j += 4 * 32) {
+      int b[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) b[k] = j + 32 * k < end ? __ldcg(row + j + 32 * k) : -1;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (j + 32 * k >= end) continue;
+        if (b[k] >= 0 && b[k] < p.num_blocks) p.state[b[k]] = kHeld;
+        else bad = true;
+      }
+    }
+    if (bad) record_error(p.err, PA_DEVERR_BLOCK_ID);
+  }
+}
+
+// Warp w of all takes blocks [w * span, (w + 1) * span).
+__device__ __forceinline__ int span_of(const ForkParams& p, int ranks) {
+  const int warps = ranks * kWarpsPerCta;
+  return ((p.num_blocks + warps - 1) / warps + 31) & ~31;
+}
+
+__device__ void step_count(const ForkParams& p, int rank, int ranks) {
+  const int warp = rank * kWarpsPerCta + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int span = span_of(p, ranks);
+  const int64_t b0 = (int64_t)warp * span;
+  const int b1 = (int)min((int64_t)p.num_blocks, b0 + span);
+  int n = 0;
+  for (int64_t b = b0 + lane; b < b1; b += 32) n += is_free(p, (int)b);
+  n = __reduce_add_sync(kAll, n);
+  if (lane == 0) p.warp_free[warp] = n;
+}
+
+// One CTA: where each row's pages start in the list, and how many are needed.
+__device__ void step_rows(const ForkParams& p) {
+  __shared__ int sums[kWarpsPerCta + 1];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int64_t before = 0;
+  for (int base = 0; base < p.num_new; base += kThreads) {
+    const int i = base + threadIdx.x;
+    int need = 0;
+    if (i < p.num_new) {
+      const Row w = fork_row(p, i);
+      if (w.bad) record_error(p.err, w.bad);
+      need = w.want - w.have + needs_copy(p, w, i);
+    }
+    int x = need;  // inclusive in the warp
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kAll, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) sums[warp] = x;
+    __syncthreads();
+    int64_t at = before + x - need;
+    for (int w = 0; w < kWarpsPerCta; ++w) {
+      if (w < warp) at += sums[w];
+      before += sums[w];
+    }
+    // more pages than there are blocks cannot be had: any such offset will do
+    if (i < p.num_new) p.row_start[i] = (int)min(at, (int64_t)INT32_MAX);
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) *p.needed = (int)min(before, (int64_t)INT32_MAX);
+}
+
+__device__ void step_list(const ForkParams& p, int rank, int ranks) {
+  __shared__ int part[kWarpsPerCta];
+  __shared__ int total;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int mine = rank * kWarpsPerCta + warp, warps = ranks * kWarpsPerCta;
+  // free pages before this CTA's spans, and of all
+  int before = 0, all = 0;
+  for (int w = threadIdx.x; w < warps; w += kThreads) {
+    const int n = __ldcg(p.warp_free + w);
+    all += n;
+    if (w < rank * kWarpsPerCta) before += n;
+  }
+  before = __reduce_add_sync(kAll, before);
+  all = __reduce_add_sync(kAll, all);
+  if (threadIdx.x == 0) total = 0;
+  __syncthreads();
+  if (lane == 0) {
+    part[warp] = before;
+    atomicAdd(&total, all);
+  }
+  __syncthreads();
+  int at = 0;
+#pragma unroll
+  for (int w = 0; w < kWarpsPerCta; ++w) at += part[w];
+  const int needed = __ldcg(p.needed);
+  if (rank == 0 && threadIdx.x == 0) {
+    const bool short_of = needed > total;
+    if (short_of) record_error(p.err, PA_DEVERR_NO_BLOCKS);
+    *p.num_free = short_of ? total : total - needed;
+    *p.refused = short_of;
+  }
+  for (int w = rank * kWarpsPerCta; w < mine; ++w) at += __ldcg(p.warp_free + w);
+  const int span = span_of(p, ranks);
+  const int64_t b0 = (int64_t)mine * span;
+  const int b1 = (int)min((int64_t)p.num_blocks, b0 + span);
+  for (int64_t b = b0; b < b1 && at < needed; b += 32) {
+    const bool f = b + lane < b1 && is_free(p, (int)b + lane);
+    const unsigned v = __ballot_sync(kAll, f);
+    const int k = at + __popc(v & ((1u << lane) - 1u));
+    if (f && k < needed) p.list[k] = (int)b + lane;  // at most num_blocks free pages: k < num_blocks
+    at += __popc(v);
+  }
+  __syncthreads();  // total and part may be used again
+}
+
+__device__ void step_write(const ForkParams& p, int rank, int ranks) {
+  const int lane = threadIdx.x & 31;
+  const int chunks = (p.maxblk_out + kColumns - 1) / kColumns;
+  const int64_t items = (int64_t)p.num_new * chunks;
+  const bool refused = __ldcg(p.refused) != 0;
+  for (int64_t it = (int64_t)rank * kWarpsPerCta + (threadIdx.x >> 5); it < items;
+       it += (int64_t)ranks * kWarpsPerCta) {
+    const int i = (int)(it / chunks), c0 = (int)(it - (int64_t)i * chunks) * kColumns;
+    const int end = min(p.maxblk_out, c0 + kColumns);
+    int32_t* dst = p.tables_out + (size_t)i * p.maxblk_out;
+    Row w = fork_row(p, i);
+    if (refused) {
+      w.parent = -1;
+      w.len = w.have = w.want = w.grow = 0;
+      w.tail = -1;
+    }
+    const bool copy = needs_copy(p, w, i);
+    const int32_t* src = p.tables + (size_t)max(w.parent, 0) * p.maxblk;
+    const int32_t* fresh = p.list + (w.want > w.have || copy ? __ldcg(p.row_start + i) : 0);
+    for (int j = c0 + lane; j < end; j += 4 * 32) {
+      int b[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = j + 32 * k;
+        b[k] = -1;
+        if (c < end && c < w.want)
+          b[k] = c >= w.have          ? __ldcg(fresh + copy + c - w.have)
+                 : copy && c == w.have - 1 ? __ldcg(fresh)
+                                           : __ldcg(src + c);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (j + 32 * k < end) dst[j + 32 * k] = b[k];
+    }
+    if (c0 == 0) {
+      if (lane == 0) {
+        p.lens_out[i] = w.len + w.grow;
+        p.pairs[2 * i] = copy ? w.tail : -1;
+        p.pairs[2 * i + 1] = copy ? __ldcg(fresh) : -1;
+      }
+      for (int t = lane; t < p.max_grow; t += 32) {
+        int slot = -1;
+        if (t < w.grow) {
+          const int pos = w.len + t, c = pos >> p.block_shift;
+          const int b = c >= w.have ? __ldcg(fresh + copy + c - w.have) : copy ? __ldcg(fresh) : __ldcg(src + c);
+          if (b >= 0 && b < p.num_blocks) slot = b * p.block_size + (pos & (p.block_size - 1));
+        }
+        p.slots[(size_t)i * p.max_grow + t] = slot;
+      }
+    }
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) fork_fused_kernel(const ForkParams p) {
+  griddep_wait();  // and no early start of the next kernel, which may read the tables before it waits
+  const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
+  step_clear(p, rank, ranks);
+  cluster_sync();
+  step_mark(p, rank, ranks);
+  cluster_sync();
+  if (rank == ranks - 1) step_rows(p);
+  step_count(p, rank, ranks);
+  cluster_sync();
+  step_list(p, rank, ranks);
+  cluster_sync();
+  step_write(p, rank, ranks);
+}
+
+template <int STEP>
+__global__ void __launch_bounds__(kThreads) fork_step_kernel(const ForkParams p) {
+  griddep_wait();
+  const int rank = blockIdx.x, ranks = gridDim.x;
+  if constexpr (STEP < 4) griddep_launch_dependents();
+  if constexpr (STEP == 0) step_clear(p, rank, ranks);
+  if constexpr (STEP == 1) step_mark(p, rank, ranks);
+  if constexpr (STEP == 2) {
+    if (rank == ranks - 1) step_rows(p);
+    step_count(p, rank, ranks);
+  }
+  if constexpr (STEP == 3) step_list(p, rank, ranks);
+  if constexpr (STEP == 4) step_write(p, rank, ranks);
+}
+
+// ----------------------------------------------------------------------------
+// copy_pages: blockIdx.z the cache, y strides over pairs, x over a block's 16-byte vectors
+// ----------------------------------------------------------------------------
+__global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__ CopyPagesParams p) {
+  constexpr int U = 4;  // vectors in flight per thread
+  griddep_wait();
+  griddep_launch_dependents();
+  uint4* cache = static_cast<uint4*>(p.caches[blockIdx.z]);
+  for (int pi = blockIdx.y; pi < p.num_pairs; pi += gridDim.y) {
+    const int src = __ldg(p.pairs + 2 * pi), dst = __ldg(p.pairs + 2 * pi + 1);
+    if (src < 0) continue;  // no copy
+    if (src >= p.num_blocks || dst < 0 || dst >= p.num_blocks) {
+      if (threadIdx.x == 0 && blockIdx.x == 0 && blockIdx.z == 0) record_error(p.err, PA_DEVERR_BLOCK_ID);
+      continue;
+    }
+    const uint4* s = cache + (int64_t)src * p.block_vecs;
+    uint4* d = cache + (int64_t)dst * p.block_vecs;
+    for (int64_t i0 = (int64_t)blockIdx.x * blockDim.x * U + threadIdx.x; i0 < p.block_vecs;
+         i0 += (int64_t)gridDim.x * blockDim.x * U) {
+      uint4 a[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * (int)blockDim.x < p.block_vecs) a[u] = s[i0 + u * (int)blockDim.x];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (i0 + u * (int)blockDim.x < p.block_vecs) d[i0 + u * (int)blockDim.x] = a[u];
+    }
+  }
+}
+
+int fork_ranks() {
+  const int sms = num_sms();
+  return 2 * (sms > 0 ? sms : 1);
+}
+
+}  // namespace
+
+// state, warp_free, row_start, list, needed, refused
+ForkWorkspace fork_workspace_layout(int num_new, int num_blocks) {
+  auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
+  ForkWorkspace w{};
+  w.state = 0;
+  w.list = al((size_t)num_blocks * 4);
+  w.row_start = w.list + al((size_t)num_blocks * 4);
+  w.warp_free = w.row_start + al((size_t)num_new * 4);
+  const int ranks = fork_ranks() > kCluster ? fork_ranks() : kCluster;
+  w.needed = w.warp_free + al((size_t)ranks * kWarpsPerCta * 4);
+  w.bytes = w.needed + 256;
+  return w;
+}
+
+cudaError_t launch_fork_blocks(const ForkParams& p, cudaStream_t stream) {
+  // Entries that the steps go over.
+  constexpr int64_t kFusedWork = 1 << 18;
+  const int64_t work = (int64_t)p.num_old * p.maxblk + (int64_t)p.num_new * p.maxblk_out + p.num_blocks;
+  if (work <= kFusedWork)
+    return launch_pdl_cluster(fork_fused_kernel, kCluster, dim3(kCluster), dim3(kThreads), 0, stream, p);
+  const dim3 grid(fork_ranks()), block(kThreads);
+  cudaError_t e = launch_pdl(fork_step_kernel<0>, grid, block, 0, stream, p);
+  if (e == cudaSuccess) e = launch_pdl(fork_step_kernel<1>, grid, block, 0, stream, p);
+  if (e == cudaSuccess) e = launch_pdl(fork_step_kernel<2>, grid, block, 0, stream, p);
+  if (e == cudaSuccess) e = launch_pdl(fork_step_kernel<3>, grid, block, 0, stream, p);
+  if (e == cudaSuccess) e = launch_pdl(fork_step_kernel<4>, grid, block, 0, stream, p);
+  return e;
+}
+
+cudaError_t launch_copy_pages(const CopyPagesParams& p, cudaStream_t stream) {
+  int64_t bx = (p.block_vecs + 1023) / 1024;
+  if (bx > 8) bx = 8;
+  const int by = p.num_pairs < 65535 ? p.num_pairs : 65535;
+  return launch_pdl(copy_pages_kernel, dim3((unsigned)bx, by, p.num_caches), dim3(256), 0, stream, p);
+}
+
+}  // namespace pa

@@ -336,4 +336,41 @@ struct Kv4DecodeParams {
 // without the merge (launch_lse_merge)
 cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int head_dim, pa_dtype dt, cudaStream_t stream);
 
+// Pages forked on the device (fork.cu).
+struct ForkParams {
+  const int32_t* tables;   // [num_old][maxblk]
+  const int32_t* lens;     // [num_old]
+  const int32_t* parents;  // [num_new]
+  const int32_t* grow;     // [num_new], or null: max_grow
+  const uint8_t* pinned;   // [num_blocks], or null
+  int32_t* tables_out;     // [num_new][maxblk_out]
+  int32_t* lens_out;
+  int32_t* pairs;          // [num_new][2]
+  int32_t* slots;          // [num_new][max_grow]
+  int32_t* num_free;
+  int32_t* state;          // scratch
+  int32_t* list;
+  int32_t* row_start;
+  int32_t* warp_free;
+  int32_t* needed;
+  int32_t* refused;
+  int* err;
+  int num_old, maxblk, num_new, maxblk_out, max_grow, num_blocks, block_size, block_shift;
+};
+struct ForkWorkspace {
+  size_t state, list, row_start, warp_free, needed, bytes;  // refused: the word behind needed
+};
+ForkWorkspace fork_workspace_layout(int num_new, int num_blocks);
+cudaError_t launch_fork_blocks(const ForkParams& p, cudaStream_t stream);
+
+constexpr int kMaxCopyCaches = 64;  // of a launch
+struct CopyPagesParams {
+  void* caches[kMaxCopyCaches];
+  const int32_t* pairs;
+  int* err;
+  int64_t block_vecs;  // 16-byte vectors of a block
+  int num_caches, num_pairs, num_blocks;
+};
+cudaError_t launch_copy_pages(const CopyPagesParams& p, cudaStream_t stream);
+
 }  // namespace pa

@@ -204,4 +204,99 @@ int pa_decode_kv4(const void* q, const void* k_cache, const void* v_cache, const
   return cuda_status(launch_lse_merge(mp, head_dim, dtype, to_stream(stream)));
 }
 
+size_t pa_fork_blocks_workspace_size(int num_new, int num_blocks) {
+  if (num_new < 0 || num_blocks <= 0) return 0;
+  return fork_workspace_layout(num_new, num_blocks).bytes;
+}
+
+int pa_fork_blocks(const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
+                   const int32_t* parents, int num_new, const int32_t* grow, int max_grow, const uint8_t* pinned,
+                   int num_blocks, int block_size, int32_t* tables_out, int max_blocks_out, int32_t* lens_out,
+                   int32_t* pairs, int32_t* slots, int32_t* num_free, void* workspace, size_t workspace_bytes,
+                   pa_stream stream) {
+  if (!block_size_ok(block_size) || num_blocks <= 0 || (int64_t)num_blocks * block_size > INT32_MAX)
+    return PA_ERR_INVALID;
+  if (num_seqs < 0 || num_seqs > 65535 || num_new < 0 || num_new > 65535 || max_blocks_per_seq <= 0 ||
+      max_blocks_out <= 0 || max_grow < 0 || (!grow && max_grow > max_blocks_out * (int64_t)block_size))
+    return PA_ERR_INVALID;
+  const int64_t most = INT32_MAX / 2;  // lengths, and lengths with what they grow by, are int32
+  if (max_blocks_per_seq > most / block_size || max_blocks_out > most / block_size || max_grow > most)
+    return PA_ERR_INVALID;
+  const int64_t n_out = (int64_t)num_new * max_blocks_out, n_slots = (int64_t)num_new * max_grow;
+  if (n_slots > (int64_t(1) << 40)) return PA_ERR_INVALID;
+  if (!num_free || (num_seqs > 0 && (!block_tables || !context_lens))) return PA_ERR_INVALID;
+  if (num_new > 0 && (!parents || !tables_out || !lens_out || !pairs || (!slots && max_grow > 0))) return PA_ERR_INVALID;
+  const ForkWorkspace w = fork_workspace_layout(num_new, num_blocks);
+  if (!workspace || workspace_bytes < w.bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+  // every warp reads the inputs while others write: outputs share no memory with them or one another
+  const struct { const void* p; int64_t bytes; } arrays[] = {
+      {tables_out, 4 * n_out}, {lens_out, 4 * (int64_t)num_new}, {pairs, 8 * (int64_t)num_new}, {slots, 4 * n_slots},
+      {num_free, 4}, {workspace, (int64_t)w.bytes},
+      {block_tables, 4 * (int64_t)num_seqs * max_blocks_per_seq}, {context_lens, 4 * (int64_t)num_seqs},
+      {parents, 4 * (int64_t)num_new}, {grow, 4 * (int64_t)num_new}, {pinned, num_blocks}};
+  constexpr int kOutputs = 6;
+  for (int a = 0; a < kOutputs; ++a)
+    for (int b = a + 1; b < (int)(sizeof(arrays) / sizeof(arrays[0])); ++b) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(arrays[a].p), y = reinterpret_cast<uintptr_t>(arrays[b].p);
+      if (!x || !y || arrays[a].bytes <= 0 || arrays[b].bytes <= 0) continue;
+      if (x < y ? y - x < (uintptr_t)arrays[a].bytes : x - y < (uintptr_t)arrays[b].bytes) return PA_ERR_INVALID;
+    }
+  int* err = device_error_ptr();
+  if (!err) return PA_ERR_CUDA;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  ForkParams p{};
+  p.tables = block_tables;
+  p.lens = context_lens;
+  p.parents = parents;
+  p.grow = grow;
+  p.pinned = pinned;
+  p.tables_out = tables_out;
+  p.lens_out = lens_out;
+  p.pairs = pairs;
+  p.slots = slots;
+  p.num_free = num_free;
+  p.state = reinterpret_cast<int32_t*>(ws + w.state);
+  p.list = reinterpret_cast<int32_t*>(ws + w.list);
+  p.row_start = reinterpret_cast<int32_t*>(ws + w.row_start);
+  p.warp_free = reinterpret_cast<int32_t*>(ws + w.warp_free);
+  p.needed = reinterpret_cast<int32_t*>(ws + w.needed);
+  p.refused = p.needed + 1;
+  p.err = err;
+  p.num_old = num_seqs;
+  p.maxblk = max_blocks_per_seq;
+  p.num_new = num_new;
+  p.maxblk_out = max_blocks_out;
+  p.max_grow = max_grow;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.block_shift = log2_of(block_size);
+  return cuda_status(launch_fork_blocks(p, to_stream(stream)));
+}
+
+int pa_copy_pages(void* const* caches, int num_caches, const int32_t* pairs, int num_pairs, int num_blocks,
+                  int64_t block_bytes, pa_stream stream) {
+  if (num_caches < 0 || num_pairs < 0 || num_blocks <= 0 || block_bytes <= 0 || block_bytes % 16 != 0 ||
+      block_bytes > INT64_MAX / 2 / num_blocks)
+    return PA_ERR_INVALID;
+  if (num_caches == 0 || num_pairs == 0) return PA_OK;
+  if (!caches || !pairs) return PA_ERR_INVALID;
+  for (int i = 0; i < num_caches; ++i)
+    if (!caches[i] || !aligned16(caches[i])) return PA_ERR_INVALID;
+  int* err = device_error_ptr();
+  if (!err) return PA_ERR_CUDA;
+  for (int i = 0; i < num_caches; i += kMaxCopyCaches) {
+    CopyPagesParams p{};
+    p.num_caches = num_caches - i < kMaxCopyCaches ? num_caches - i : kMaxCopyCaches;
+    for (int k = 0; k < p.num_caches; ++k) p.caches[k] = caches[i + k];
+    p.pairs = pairs;
+    p.err = err;
+    p.block_vecs = block_bytes / 16;
+    p.num_pairs = num_pairs;
+    p.num_blocks = num_blocks;
+    const int st = cuda_status(launch_copy_pages(p, to_stream(stream)));
+    if (st != PA_OK) return st;
+  }
+  return PA_OK;
+}
+
 }  // extern "C"

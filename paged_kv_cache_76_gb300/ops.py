@@ -53,6 +53,8 @@ __all__ = [
     "decode_kv4",
     "decode_kv4_split_tokens",
     "decode_kv4_workspace_size",
+    "fork_blocks",
+    "copy_pages",
     "get_device_error",
     "selftest_wait_timeout",
     "launch_count",
@@ -992,6 +994,83 @@ def decode_kv4(q, k_cache, v_cache, block_tables, context_lens, scale, out=None,
     _launch("pa_decode_kv4", _ptr(q, "q", dev), kc, vc, tables, maxblk, lens, B, ql, hq, hkv, d, bs, nb, float(scale),
             split_tokens, ws_ptr, ws_bytes, _ptr(out, "out", dev), code, handle)
     return out
+
+
+# ----------------------------------------------------------------------------
+# sequences that go on from others
+# ----------------------------------------------------------------------------
+@functools.lru_cache(maxsize=4096)
+def _fork_workspace(dev, num_new, num_blocks) -> int:  # dev: the size depends on the current device
+    return int(_lib.lib().pa_fork_blocks_workspace_size(num_new, num_blocks))
+
+
+def fork_blocks(block_tables, context_lens, parents, num_blocks, block_size, grow=1, max_grow=None, pinned=None,
+                max_blocks=None, workspace=None, stream=None):
+    """pa_fork_blocks: new row i goes on from row ``parents[i]`` (-1: a new sequence, below: none) and grows by ``grow``
+    tokens (a count, or int32 [num_new] of at most ``max_grow``).  Returns (tables int32 [num_new, max_blocks], lens
+    [num_new], pairs [num_new, 2] for :func:`copy_pages`, slots [num_new, max_grow], num_free [1]).
+
+    ``pinned`` (bool or uint8 [num_blocks]): blocks that others hold.  ``max_blocks``: columns of the new tables (None:
+    as many as ``block_tables`` has)."""
+    dev, num_blocks, block_size = block_tables.get_device(), int(num_blocks), int(block_size)
+    B, R = context_lens.shape[0], parents.shape[0]
+    tables = _table_ptr(block_tables, dev, B)
+    lens = _rows_ptr(context_lens, "context_lens", dev, B)
+    par = _rows_ptr(parents, "parents", dev, R)
+    gr = pin = None
+    if isinstance(grow, torch.Tensor):
+        if max_grow is None:
+            raise ValueError("a tensor of growths needs max_grow")
+        gr = _rows_ptr(grow, "grow", dev, R)
+        max_grow = int(max_grow)
+    else:
+        if max_grow is not None and int(max_grow) != int(grow):
+            raise ValueError("max_grow is for a tensor of growths")
+        max_grow = int(grow)
+    if max_grow < 0:
+        raise ValueError("growths are counts")
+    if pinned is not None:
+        if pinned.dtype not in (torch.bool, torch.uint8) or pinned.shape != (num_blocks,):
+            raise ValueError("pinned is bool or uint8 [num_blocks]")
+        pin = _ptr(pinned, "pinned", dev)
+    handle = _stream_on(dev, stream)
+    width = block_tables.shape[1] if max_blocks is None else int(max_blocks)
+    if width < 1:
+        raise ValueError("the new tables have no columns")
+
+    def new(*shape):
+        return _empty(shape, torch.int32, block_tables.device, stream, returned=True)
+    out = (new(R, width), new(R), new(R, 2), new(R, max_grow), new(1))
+    n = _fork_workspace(dev, R, num_blocks) if workspace is None else 0
+    workspace, ws_ptr, ws_bytes = _scratch(workspace, n, block_tables.device, dev, stream)
+    _keep(*out, workspace)
+    _launch("pa_fork_blocks", tables, block_tables.shape[1], lens, B, par, R, gr, max_grow, pin, num_blocks, block_size,
+            out[0].data_ptr(), width, out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(), out[4].data_ptr(), ws_ptr,
+            ws_bytes, handle)
+    return out
+
+
+def copy_pages(caches, pairs, stream=None):
+    """pa_copy_pages: in every cache (a list of tensors [num_blocks, ...] of one size, 16-bit or 4-bit) block
+    ``pairs[p, 1]`` becomes a copy of block ``pairs[p, 0]``; a negative source is no copy."""
+    caches = list(caches)
+    if not caches:
+        return
+    dev = caches[0].get_device()
+    nb = caches[0].shape[0] if caches[0].dim() else 0
+    size = caches[0].numel() * caches[0].element_size()
+    ptrs = []
+    for i, c in enumerate(caches):
+        if not c.dim() or c.shape[0] != nb or c.numel() * c.element_size() != size:
+            raise ValueError("the caches must agree in blocks and bytes")
+        ptrs.append(_ptr(c, f"caches[{i}]", dev))
+    if not nb or size // nb % 16:
+        raise ValueError("a block is a multiple of 16 bytes")
+    if pairs.dim() != 2 or pairs.shape[1] != 2:
+        raise ValueError("pairs is int32 [num_pairs, 2]")
+    pr = _rows_ptr(pairs, "pairs", dev, pairs.shape[0])
+    _launch("pa_copy_pages", (C.c_void_p * len(ptrs))(*ptrs), len(ptrs), pr, pairs.shape[0], nb, size // nb,
+            _stream_on(dev, stream))
 
 
 def selftest_wait_timeout(wait_ms: int = 50, stream=None) -> None:
