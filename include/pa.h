@@ -757,6 +757,36 @@ int pa_decode_kv4(const void* q, const void* k_cache, const void* v_cache, const
                   void* workspace, size_t workspace_bytes, void* out, pa_dtype dtype, pa_stream stream);
 
 /* ----------------------------------------------------------------------------
+ * pa_chunked_prefill_kv4 - pa_chunked_prefill over a 4-bit cache.
+ *
+ * The chunk's K and V are written first (pa_quantize_and_cache); query i of
+ * request r sees tokens [0, context_lens[r] - chunk + i].
+ *   q, out        [total_q][q_heads][head_dim], packed by q_start
+ *   q_start       int32 [num_reqs + 1], non-decreasing, q_start[num_reqs] <= total_q
+ *   max_q_len     host-side upper bound of any chunk length (sizes the grid)
+ *   scale         a normal number, of either sign
+ *   split_tokens  keys of a partition: 0, or a multiple of 64.  0 cuts contexts
+ *                 where there are fewer units of 256 (query, group head) rows of
+ *                 one (request, KV head) than SMs, by the width of block_tables.
+ *   workspace     at least pa_chunked_prefill_kv4_workspace_size(...) bytes (NULL
+ *                 where that is 0)
+ * Rounding, and tokens that are not numbers, as pa_decode_kv4; refused requests
+ * as pa_chunked_prefill (their rows of out, and rows behind the last chunk, stay
+ * as they are).
+ * ------------------------------------------------------------------------- */
+int pa_chunked_prefill_kv4_split_tokens(int num_reqs, int max_q_len, int q_heads, int kv_heads, int max_blocks_per_seq,
+                                        int block_size, int split_tokens);
+
+size_t pa_chunked_prefill_kv4_workspace_size(int num_reqs, int total_q, int max_q_len, int q_heads, int kv_heads,
+                                             int head_dim, int max_blocks_per_seq, int block_size, int split_tokens);
+
+int pa_chunked_prefill_kv4(const void* q, const int32_t* q_start, const int32_t* context_lens, const void* k_cache,
+                           const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq, int num_reqs,
+                           int total_q, int max_q_len, int q_heads, int kv_heads, int head_dim, int block_size,
+                           int num_blocks, float scale, int split_tokens, void* workspace, size_t workspace_bytes,
+                           void* out, pa_dtype dtype, pa_stream stream);
+
+/* ----------------------------------------------------------------------------
  * pa_fork_blocks - sequences that go on from others: tables, pages and slots of
  * a batch's next step, worked out on the device.
  *

@@ -118,6 +118,10 @@ PROTOTYPES = {
     "pa_decode_kv4_split_tokens": (_I, [_I, _I, _I, _I, _I, _I, _I]),
     "pa_decode_kv4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
     "pa_decode_kv4": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P, _I, _P]),
+    "pa_chunked_prefill_kv4_split_tokens": (_I, [_I, _I, _I, _I, _I, _I, _I]),
+    "pa_chunked_prefill_kv4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),
+    "pa_chunked_prefill_kv4": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P, _I,
+                                    _P]),
     "pa_fork_blocks_workspace_size": (_SZ, [_I, _I]),
     "pa_fork_blocks": (_I, [_P, _I, _P, _I, _P, _I, _P, _I, _P, _I, _I, _P, _I, _P, _P, _P, _P, _P, _SZ, _P]),
     "pa_copy_pages": (_I, [_P, _I, _P, _I, _I, C.c_int64, _P]),

@@ -27,7 +27,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OBJDIR = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libpa.so")
 SOURCES = ["pa_api.cu", "decode.cu", "prefill.cu", "cache_ops.cu", "block_alloc.cpp", "decode_noalloc.cu", "attn_tc.cu",
-           "attn_tile.cu", "vkv.cpp", "rope.cu", "evict.cu", "tree.cu", "pa_kv4.cu", "kv4_cache.cu", "kv4_decode.cu", "fork.cu"]
+           "attn_tile.cu", "vkv.cpp", "rope.cu", "evict.cu", "tree.cu", "pa_kv4.cu", "kv4_cache.cu", "kv4_decode.cu",
+           "kv4_prefill.cu", "fork.cu"]
 MARSHAL = os.path.join(HERE, "_marshal" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 MARSHAL_STAMP = os.path.join(OBJDIR, "marshal.stamp")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,0 +1,549 @@
+// Chunked prefill over a 4-bit paged cache (see kv4.cuh for the page) on the
+// 5th-generation tensor cores, sm_103a.
+//
+// The decomposition is attn_tc.cu's: a CTA owns two tiles of 128 rows (query,
+// head of the group) of one (request, KV head) and walks the keys they see 64
+// at a time; S_x = Q_x K^T into one of two tensor-memory buffers per tile, the
+// softmax in registers, P over the same buffer, O_x += P_x V with P from tensor
+// memory.  What differs:
+//
+//  * The two producer warps do not load K and V, they make them: pages come by
+//    bulk copy into a small ring, and a warp writes the fp16 tile in the
+//    128-byte-swizzled layout that the MMAs read (exact: kv4.cuh), a quarter of
+//    the shared-memory traffic that the MMAs cause.  A task is the 16 elements
+//    of a scale; lanes of the second half-row store their two 16-byte pieces in
+//    the other order, so that a store's eight lanes meet eight banks.
+//  * All operands are fp16 whatever the type of q (see kv4_decode.cu): a row of
+//    Q is brought to [2^13, 2^14) by a power of two that its softmax takes back.
+//  * V rows behind the last key are zeros; a V group that is not a number becomes
+//    zeros too, and the first such token of each group of elements is kept, so
+//    that the rows that see it get their NaN at the end and no other row does.
+//  * A context may be cut into partitions of split_tokens keys, a unit each,
+//    where there are few units; a merge joins them.
+//
+// Warps: 0, 1 MMA issuers of tiles A, B; 2 makes K, 3 makes V; 4..7 softmax of
+// tile A, 8..11 of tile B.  Every wait is bounded.
+#include <float.h>
+#include <limits.h>
+
+#include "kv4.cuh"
+#include "pa_internal.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kRows = 128;  // rows per Q tile
+constexpr int kKeys = 64;   // keys per K/V tile
+constexpr int kStages = 4;  // of K and of V, fp16
+constexpr int kRaw = 3;     // tiles of pages under way, of K and of V
+constexpr int kThreads = 32 * 12;
+constexpr uint32_t kTmem = 512;
+constexpr unsigned kAll = 0xffffffffu;
+constexpr float kRescale = 8.f;
+constexpr float kShift = 7.f;  // weights are 2^(s - m + kShift) <= 2^15
+
+template <int D>
+struct Kv4PrefillSmem {
+  using Tile = KvTile<D, 16, kKeys>;
+  static constexpr int QHALF = kRows * 128;
+  static constexpr int QTILE = D / 64 * QHALF;
+  static constexpr int RAW = kKeys * Kv4Row<D>::BYTES;
+  static constexpr int Q_OFF = 0;
+  static constexpr int K_OFF = Q_OFF + 2 * QTILE;
+  static constexpr int V_OFF = K_OFF + kStages * Tile::BYTES;
+  static constexpr int RAW_OFF = V_OFF + kStages * Tile::BYTES;  // K's ring, then V's
+  static constexpr int BAR_OFF = RAW_OFF + 2 * kRaw * RAW;
+  static constexpr int NBARS = 4 * kStages + 2 * kRaw + 15;
+  static constexpr int SLOT_OFF = BAR_OFF + NBARS * 8;
+  static constexpr int NAN_OFF = SLOT_OFF + 8;
+  static constexpr int BYTES = NAN_OFF + D / kKv4Group * 4 + 1024;
+  static_assert(BYTES <= 227 * 1024, "shared memory per CTA");
+};
+
+// barrier indices
+constexpr int B_KFULL = 0;                      // [kStages] the producer warp wrote K_j
+constexpr int B_KEMPTY = B_KFULL + kStages;     // [kStages] one commit per issuer after S_x(j)
+constexpr int B_VFULL = B_KEMPTY + kStages;
+constexpr int B_VEMPTY = B_VFULL + kStages;     // [kStages] one commit per issuer after P.V_x(j)
+constexpr int B_RAW = B_VEMPTY + kStages;       // [K, V][kRaw] pages landed
+constexpr int B_SFULL = B_RAW + 2 * kRaw;       // [2 Q tiles][2 S buffers]
+constexpr int B_PFULL = B_SFULL + 4;            // [2][2] four softmax warps
+constexpr int B_OFULL = B_PFULL + 4;            // [2][2] P.V_x(j) complete
+constexpr int B_QFULL = B_OFULL + 4;            // [2]
+constexpr int B_MMADONE = B_QFULL + 2;
+static_assert(B_MMADONE + 1 == 4 * kStages + 2 * kRaw + 15, "barrier count");
+
+struct Unit {
+  int r, h, row0, part, qs, chunk, p0, rows, k0, kend, ntiles;
+  int code;  // error of a refused request
+};
+
+// Units are numbered (request, partition), then row tile in reverse, then head:
+// the last row tiles of a chunk see the most keys.
+__device__ __forceinline__ Unit unit_of(const Kv4PrefillParams& p, int u) {
+  Unit w{};
+  const int per_z = p.row_tiles * p.kv_heads;
+  const int z = u / per_z, rem = u - z * per_z, rt = rem / p.kv_heads;
+  w.h = rem - rt * p.kv_heads;
+  w.row0 = (p.row_tiles - 1 - rt) * 2 * kRows;
+  w.r = z / p.max_splits;
+  w.part = z - w.r * p.max_splits;
+  w.qs = __ldg(p.q_start + w.r);
+  const int qe = __ldg(p.q_start + w.r + 1), ctx = __ldg(p.lens + w.r);
+  w.chunk = qe - w.qs;
+  w.p0 = ctx - w.chunk;
+  if (w.qs < 0 || qe < w.qs || qe > p.total_q || w.chunk > p.max_q_len || w.p0 < 0 || ctx > p.maxblk * p.block_size) {
+    w.code = PA_DEVERR_QUERY_RANGE;
+    return w;
+  }
+  w.rows = w.chunk * p.group;
+  if (w.row0 >= w.rows) return w;
+  const int last_row = min(w.row0 + 2 * kRows, w.rows) - 1;
+  w.k0 = w.part * p.split_tokens;
+  w.kend = min(w.p0 + last_row / p.group + 1, w.k0 + p.split_tokens);
+  if (w.k0 < w.kend) w.ntiles = (w.kend - w.k0 + kKeys - 1) / kKeys;
+  return w;
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4PrefillParams p) {
+  using L = Kv4PrefillSmem<D>;
+  using Tile = typename L::Tile;
+  using R = Kv4Row<D>;
+  constexpr int KSTEPS = D / 16;
+  constexpr int PSTEPS = kKeys / 16;
+  constexpr uint32_t O_COL = 4 * kKeys;
+  constexpr uint32_t IDESC_S = idesc_f16<__half>(kRows, kKeys, false);
+  constexpr uint32_t IDESC_O = idesc_f16<__half>(kRows, D, true);
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::SLOT_OFF);
+  int* first_nan = reinterpret_cast<int*>(smem + L::NAN_OFF);  // per group of elements: its first V token that is NaN
+  auto bar = [&](int i) { return smem_u32(&bars[i]); };
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = p.group;
+  const Unit w = unit_of(p, blockIdx.x);
+  if (w.code || w.ntiles == 0) {
+    griddep_wait();
+    if (w.code && w.h == 0 && w.row0 == 0 && w.part == 0 && threadIdx.x == 0) record_error(p.err, w.code);
+    return;
+  }
+  const int tiles = w.row0 + kRows < w.rows ? 2 : 1;  // Q tiles with rows
+
+  if (threadIdx.x < D / kKv4Group) first_nan[threadIdx.x] = INT_MAX;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(bar(B_KFULL + i), 1);
+      mbar_init(bar(B_KEMPTY + i), tiles);
+      mbar_init(bar(B_VFULL + i), 1);
+      mbar_init(bar(B_VEMPTY + i), tiles);
+    }
+    for (int i = 0; i < 2 * kRaw; ++i) mbar_init(bar(B_RAW + i), 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(bar(B_SFULL + i), 1);
+      mbar_init(bar(B_PFULL + i), 4);
+      mbar_init(bar(B_OFULL + i), 1);
+    }
+    mbar_init(bar(B_QFULL), 4);
+    mbar_init(bar(B_QFULL + 1), 4);
+    mbar_init(bar(B_MMADONE), tiles);
+    fence_mbar_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(smem_u32(tmem_slot), kTmem);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  griddep_launch_dependents();
+
+  if (warp == 2 || warp == 3) {
+    // ------------------------------------------------------------ K and V
+    const int isv = warp - 2;
+    const uint8_t* cache = static_cast<const uint8_t*>(isv ? p.v_cache : p.k_cache);
+    uint8_t* raw = smem + L::RAW_OFF + isv * kRaw * L::RAW;
+    uint8_t* tile0 = smem + (isv ? L::V_OFF : L::K_OFF);
+    const int full0 = isv ? B_VFULL : B_KFULL, empty0 = isv ? B_VEMPTY : B_KEMPTY, raw0 = B_RAW + isv * kRaw;
+    const int32_t* trow = p.tables + (size_t)w.r * p.maxblk;
+    const int bs = p.block_size, bsh = p.block_shift, page = bs * R::BYTES;
+    const uint64_t pol = p.row_tiles == 1 ? policy_evict_first() : policy_evict_last();  // other row tiles re-read them
+    griddep_wait();
+    auto issue = [&](int j) {
+      const int s = j % kRaw, ts = w.k0 + j * kKeys;
+      const int npages = (min(kKeys, w.kend - ts) + bs - 1) >> bsh;
+      const bool mine = lane < npages;
+      int b = mine ? __ldg(trow + (ts >> bsh) + lane) : -1;
+      if (mine && (b < 0 || b >= p.num_blocks)) {
+        record_error(p.err, PA_DEVERR_BLOCK_ID);
+        b = -1;
+      }
+      const int copies = __popc(__ballot_sync(kAll, b >= 0));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_expect_tx(bar(raw0 + s), copies * page);
+      __syncwarp();
+      if (mine) {
+        uint8_t* dst = raw + s * L::RAW + lane * page;
+        if (b >= 0) {
+          bulk_load_hint(smem_u32(dst), cache + ((size_t)b * p.kv_heads + w.h) * page, page, bar(raw0 + s), pol);
+        } else {  // a bad block id: zeros
+          for (int k = 0; k < page; k += 16) *reinterpret_cast<uint4*>(dst + k) = make_uint4(0, 0, 0, 0);
+        }
+      }
+    };
+    for (int j = 0; j < min(kRaw, w.ntiles); ++j) issue(j);
+    bool failed = false;
+    int j = 0;
+    for (; j < w.ntiles; ++j) {
+      const int s = j % kStages, rs = j % kRaw;
+      if (!mbar_wait(bar(raw0 + rs), (j / kRaw) & 1) ||
+          (j >= kStages && !mbar_wait(bar(empty0 + s), (j / kStages - 1) & 1))) {
+        failed = true;
+        break;
+      }
+      __syncwarp();
+      const int ts = w.k0 + j * kKeys;
+      const int nvalid = min(kKeys, w.kend - ts);
+      const uint8_t* src = raw + rs * L::RAW;
+      uint8_t* dst = tile0 + s * Tile::BYTES;
+      constexpr int PER_ROW = D / kKv4Group;
+#pragma unroll 4
+      for (int t = lane; t < kKeys * PER_ROW; t += 32) {
+        const int row = t / PER_ROW, g = t % PER_ROW;
+        const uint8_t* pg = src + (row >> bsh) * page;
+        const int o = row & (bs - 1);
+        const uint2 codes = *reinterpret_cast<const uint2*>(pg + o * R::CODES + 8 * g);
+        uint32_t byte = row < nvalid ? pg[bs * R::CODES + o * R::SCALES + g] : 0u;
+        if (isv && byte >= kKv4FirstInf) {
+          byte = 0;
+          atomicMin(&first_nan[g], ts + row);
+        }
+        const uint32_t s2 = kv4_scale2(byte);
+        uint32_t x[8];
+        kv4_unpack(codes.x, *reinterpret_cast<uint32_t(*)[4]>(&x[0]));
+        kv4_unpack(codes.y, *reinterpret_cast<uint32_t(*)[4]>(&x[4]));
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = hmul2_u(x[e], s2);
+        const uint4 c0 = make_uint4(x[0], x[1], x[2], x[3]), c1 = make_uint4(x[4], x[5], x[6], x[7]);
+        const int flip = g >> 2;
+        *reinterpret_cast<uint4*>(dst + Tile::offset(row, 2 * g + flip)) = flip ? c1 : c0;
+        *reinterpret_cast<uint4*>(dst + Tile::offset(row, 2 * g + (flip ^ 1))) = flip ? c0 : c1;
+      }
+      fence_proxy_async_smem();  // the tile before the MMAs, the pages before the next copies over them
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(full0 + s));
+      if (j + kRaw < w.ntiles) issue(j + kRaw);
+    }
+    if (failed) {
+      if (lane == 0) record_error(p.err, PA_DEVERR_TIMEOUT);
+      for (int t = j; t < w.ntiles && t < j + kRaw; ++t)  // copies in flight land before exit (bounded)
+        mbar_wait(bar(raw0 + t % kRaw), (t / kRaw) & 1);
+    }
+  } else if (warp < 2) {
+    // ------------------------------------------------------------ MMA issuers
+    const int x = warp;
+    if (x < tiles) {
+      bool ok = true;
+      const uint32_t kbase = smem_u32(smem + L::K_OFF), vbase = smem_u32(smem + L::V_OFF);
+      const uint32_t qa = smem_u32(smem + L::Q_OFF + x * L::QTILE);
+      const uint32_t sd = tmem + 2 * x * kKeys, od = tmem + O_COL + x * D;
+      auto issue_pv = [&](int t) -> bool {
+        const int pb = t & 1, vst = t % kStages;
+        if (!__all_sync(kAll, mbar_wait(bar(B_PFULL + 2 * x + pb), (t >> 1) & 1) &&
+                                  mbar_wait(bar(B_VFULL + vst), (t / kStages) & 1)))
+          return false;
+        tc_fence_after();
+        const uint32_t vb = vbase + vst * Tile::BYTES;
+#pragma unroll
+        for (int kk = 0; kk < PSTEPS; ++kk)
+          tc_mma_f16_ts_warp(od, sd + pb * kKeys + kk * 8, smem_desc_sw128(vb + kk * 2048, Tile::HALF, 1024), IDESC_O,
+                             (t > 0 || kk > 0) ? 1u : 0u);
+        tc_commit_warp(bar(B_OFULL + 2 * x + pb));
+        tc_commit_warp(bar(B_VEMPTY + vst));
+        return true;
+      };
+      ok = __all_sync(kAll, mbar_wait(bar(B_QFULL + x), 0));
+      // tile B starts half a key tile behind tile A, so that the two softmaxes alternate
+      if (ok && x == 1) ok = __all_sync(kAll, mbar_wait(bar(B_PFULL), 0));
+      for (int j = 0; ok && j < w.ntiles; ++j) {
+        const int s = j % kStages, b = j & 1;
+        // S_x(j) overwrites P_x(j - 2)
+        ok = __all_sync(kAll, mbar_wait(bar(B_KFULL + s), (j / kStages) & 1) &&
+                                  (j < 2 || mbar_wait(bar(B_OFULL + 2 * x + b), ((j - 2) >> 1) & 1)));
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t kb = kbase + s * Tile::BYTES;
+#pragma unroll
+        for (int ks = 0; ks < KSTEPS; ++ks)
+          tc_mma_f16_warp(sd + b * kKeys, smem_desc_sw128(qa + (ks >> 2) * L::QHALF + (ks & 3) * 32, 16, 1024),
+                          smem_desc_sw128(kb + (ks >> 2) * Tile::HALF + (ks & 3) * 32, 16, 1024), IDESC_S,
+                          ks > 0 ? 1u : 0u);
+        tc_commit_warp(bar(B_SFULL + 2 * x + b));
+        tc_commit_warp(bar(B_KEMPTY + s));
+        if (j > 0) ok = issue_pv(j - 1);
+      }
+      if (ok) ok = issue_pv(w.ntiles - 1);
+      if (!ok && lane == 0) record_error(p.err, PA_DEVERR_TIMEOUT);
+      tc_commit_warp(bar(B_MMADONE));
+    }
+  } else {
+    // ------------------------------------------------------------ softmax
+    const int x = (warp - 4) >> 2;
+    const int quarter = warp & 3, row = quarter * 32 + lane;
+    if (x < tiles) {
+      const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
+      const uint32_t scol0 = tmem + lane_addr + 2 * x * kKeys, ocol = tmem + lane_addr + O_COL + x * D;
+      const int grow = w.row0 + x * kRows + row;
+      const bool valid = grow < w.rows;
+      const int qi = grow / G, g = grow % G;
+      const int lim = valid ? w.p0 + qi : -1;  // last key this row sees
+      float sl2 = 0.f;
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
+                                                          ((size_t)(w.qs + qi) * p.q_heads + w.h * G + g) * D);
+        uint8_t* qt = smem + L::Q_OFF + x * L::QTILE;
+        float top = 0.f;
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(Elem<T>::lo(e[i])), fabsf(Elem<T>::hi(e[i]))));
+        }
+        int ex = top > 0.f && top < INFINITY ? ilogbf(top) - 13 : 0;
+        ex = max(ex, -126);
+        const float down = ldexpf(1.f, -ex);
+        // a masked score is -inf and must stay so: not below the smallest normal number
+        sl2 = fmaxf(p.scale_log2 * ldexpf(1.f, ex), FLT_MIN);
+#pragma unroll
+        for (int c = 0; c < D / 8; ++c) {
+          const uint4 v = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+          uint32_t y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = Elem<__half>::pack(Elem<T>::lo(e[i]) * down, Elem<T>::hi(e[i]) * down);
+          *reinterpret_cast<uint4*>(qt + (c >> 3) * L::QHALF + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
+              make_uint4(y[0], y[1], y[2], y[3]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_QFULL + x));
+      }
+      griddep_wait();  // before writing outputs
+
+      bool ok = true;
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < w.ntiles; ++j) {
+        const int sb = j & 1;
+        const uint32_t scol = scol0 + sb * kKeys;
+        if (!__all_sync(kAll, mbar_wait(bar(B_SFULL + 2 * x + sb), (j >> 1) & 1))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const int nvis = lim - (w.k0 + j * kKeys) + 1;  // keys of this tile the row sees
+        float sv[kKeys];
+#pragma unroll
+        for (int c = 0; c < kKeys / 32; ++c) tmem_ld32(scol + 32 * c, *reinterpret_cast<float(*)[32]>(&sv[32 * c]));
+        tmem_wait_ld();
+        // raw scores meet the scale's sign before the maximum
+        if (p.negative) {
+#pragma unroll
+          for (int e = 0; e < kKeys; ++e) sv[e] = -sv[e];
+        }
+        if (!__all_sync(kAll, nvis >= kKeys) || j == w.ntiles - 1) {
+          const int n = min(nvis, w.kend - (w.k0 + j * kKeys));
+#pragma unroll
+          for (int e = 0; e < kKeys; ++e) sv[e] = e < n ? sv[e] : -INFINITY;
+        }
+        float ma = -INFINITY, mb = -INFINITY, mc = -INFINITY, md = -INFINITY;
+#pragma unroll
+        for (int e = 0; e < kKeys; e += 8) {
+          ma = fmax3(ma, sv[e], sv[e + 1]);
+          mb = fmax3(mb, sv[e + 2], sv[e + 3]);
+          mc = fmax3(mc, sv[e + 4], sv[e + 5]);
+          md = fmax3(md, sv[e + 6], sv[e + 7]);
+        }
+        const float mx = fmax3(ma, mb, fmaxf(mc, md)) * sl2;
+        const bool raise = mx > m + kRescale;
+        const float alpha = (raise && m != -INFINITY) ? ex2_approx(m - mx) : 1.f;
+        const bool rescale = __any_sync(kAll, alpha != 1.f);
+        if (raise) {
+          l = m == -INFINITY ? 0.f : l * alpha;
+          m = mx;
+        }
+        const float neg_m = m == -INFINITY ? 0.f : kShift - m;
+        float sx[4] = {0.f, 0.f, 0.f, 0.f}, sy[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < kKeys / 32; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            float a0, a1;
+            ffma2(a0, a1, sv[32 * c + e], sv[32 * c + e + 1], sl2, sl2, neg_m, neg_m);
+            const float p0 = ex2_approx(a0), p1 = ex2_approx(a1);
+            const int k = (e >> 1) & 3;
+            fadd2(sx[k], sy[k], sx[k], sy[k], p0, p1);
+            pk[e >> 1] = Elem<__half>::pack(p0, p1);
+          }
+          tmem_st16u(scol + 16 * c, pk);
+        }
+        if (rescale) {
+          // O_x before P.V_x(j) starts, once P.V_x(j - 1) has completed
+          if (!mbar_wait(bar(B_OFULL + 2 * x + ((j - 1) & 1)), ((j - 1) >> 1) & 1)) ok = false;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < D / 16; ++c) {
+            float ov[16];
+            tmem_ld16(ocol + 16 * c, ov);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 16; ++e) ov[e] *= alpha;
+            tmem_st16u(ocol + 16 * c, *reinterpret_cast<const uint32_t(*)[16]>(ov));
+          }
+        }
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_PFULL + 2 * x + sb));
+        l += ((sx[0] + sy[0]) + (sx[1] + sy[1])) + ((sx[2] + sy[2]) + (sx[3] + sy[3]));
+        if (!__all_sync(kAll, ok)) {
+          ok = false;
+          break;
+        }
+      }
+      const int last = w.ntiles - 1;
+      // the unit's last P.V, and (for first_nan) the V producer's last arrival
+      if (ok)
+        ok = mbar_wait(bar(B_OFULL + 2 * x + (last & 1)), (last >> 1) & 1) &&
+             mbar_wait(bar(B_VFULL + last % kStages), (last / kStages) & 1);
+      if (__all_sync(kAll, ok)) {
+        tc_fence_after();
+        const size_t orow = (size_t)(w.qs + qi) * p.q_heads + w.h * G + g;
+        const size_t pr = orow * p.max_splits + w.part;
+        const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN sum stays one
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float ov[32];
+          tmem_ld32(ocol + 32 * c, ov);  // warp-collective
+          tmem_wait_ld();
+          if (!valid) continue;
+#pragma unroll
+          for (int e = 0; e < 32; ++e)
+            if (first_nan[2 * c + (e >> 4)] <= lim) ov[e] = NAN;
+          if (p.max_splits == 1) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + orow * D) + 4 * c;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              dst[q] = make_uint4(Elem<T>::pack(ov[8 * q] * inv, ov[8 * q + 1] * inv),
+                                  Elem<T>::pack(ov[8 * q + 2] * inv, ov[8 * q + 3] * inv),
+                                  Elem<T>::pack(ov[8 * q + 4] * inv, ov[8 * q + 5] * inv),
+                                  Elem<T>::pack(ov[8 * q + 6] * inv, ov[8 * q + 7] * inv));
+          } else {
+            float4* po = reinterpret_cast<float4*>(p.part_o + pr * D) + 8 * c;
+#pragma unroll
+            for (int q = 0; q < 8; ++q) po[q] = make_float4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+          }
+        }
+        if (valid && p.max_splits > 1) {
+          p.part_m[pr] = m;
+          p.part_l[pr] = l;
+        }
+        tc_fence_before();
+      } else if (lane == 0) {
+        record_error(p.err, PA_DEVERR_TIMEOUT);
+      }
+    }
+  }
+
+  if (warp == 0 && lane == 0) mbar_wait(bar(B_MMADONE), 0);  // the issuers' tcgen05 ops done (bounded)
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kTmem);
+  }
+}
+
+// One warp per row: the partitions its row tile has keys of, in order.
+// blockIdx.y: request; 8 rows per CTA.
+template <int D, typename T>
+__global__ void __launch_bounds__(256) kv4_prefill_merge_kernel(const Kv4PrefillParams p) {
+  constexpr int V = D / 32;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int r = blockIdx.y, lane = threadIdx.x & 31;
+  const int qs = __ldg(p.q_start + r), qe = __ldg(p.q_start + r + 1), ctx = __ldg(p.lens + r);
+  const int chunk = qe - qs, p0 = ctx - chunk, G = p.group;
+  if (qs < 0 || qe < qs || qe > p.total_q || chunk > p.max_q_len || p0 < 0 || ctx > p.maxblk * p.block_size) return;
+  const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);  // (query, head)
+  if (at >= (int64_t)chunk * p.q_heads) return;
+  const int qi = (int)(at / p.q_heads), head = (int)(at - (int64_t)qi * p.q_heads);
+  const int rows = chunk * G, grow = qi * G + head % G;
+  const int last_row = min((grow / (2 * kRows) + 1) * 2 * kRows, rows) - 1;  // of the row's tiles
+  const int nsplit = (p0 + last_row / G + p.split_tokens) / p.split_tokens;
+  const size_t orow = (size_t)(qs + qi) * p.q_heads + head;
+  const float* pm = p.part_m + orow * p.max_splits;
+  const float* pl = p.part_l + orow * p.max_splits;
+  const float* po = p.part_o + orow * p.max_splits * D + lane * V;
+  float M = -INFINITY;
+  for (int c = lane; c < nsplit; c += 32) M = fmaxf(M, pm[c]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
+  if (M == -INFINITY) M = 0.f;  // no finite score: sums are zero or not numbers
+  float a[V], den = 0.f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) a[i] = 0.f;
+#pragma unroll 4
+  for (int c = 0; c < nsplit; ++c) {
+    const float f = exp2f(pm[c] - M);
+    den += f * pl[c];
+    const float* x = po + (size_t)c * D;
+#pragma unroll
+    for (int i = 0; i < V; i += 2) {
+      const float2 v = *reinterpret_cast<const float2*>(x + i);
+      a[i] += f * v.x;
+      a[i + 1] += f * v.y;
+    }
+  }
+  const float inv = den == 0.f ? 0.f : 1.f / den;
+  T* o = static_cast<T*>(p.out) + orow * D + lane * V;
+#pragma unroll
+  for (int i = 0; i < V; i += 2)
+    *reinterpret_cast<uint32_t*>(o + i) = Elem<T>::pack(a[i] * inv, a[i + 1] * inv);
+}
+
+template <int D, typename T>
+cudaError_t launch_t(const Kv4PrefillParams& p, cudaStream_t stream) {
+  using L = Kv4PrefillSmem<D>;
+  auto kern = kv4_prefill_kernel<D, T>;
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && !attr_set[dev]) {
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+    if (e != cudaSuccess) return e;
+    attr_set[dev] = true;
+  }
+  const int64_t units = (int64_t)p.row_tiles * p.kv_heads * p.num_reqs * p.max_splits;
+  if (units > INT32_MAX) return cudaErrorInvalidValue;
+  cudaError_t e = launch_pdl(kern, dim3((unsigned)units), dim3(kThreads), L::BYTES, stream, p);
+  if (e != cudaSuccess || p.max_splits == 1) return e;
+  const unsigned gx = (unsigned)(((int64_t)p.max_q_len * p.q_heads + 7) / 8);
+  return launch_pdl(kv4_prefill_merge_kernel<D, T>, dim3(gx, p.num_reqs), dim3(256), 0, stream, p);
+}
+
+}  // namespace
+
+cudaError_t launch_kv4_prefill(const Kv4PrefillParams& p, int head_dim, pa_dtype dt, cudaStream_t stream) {
+  if (head_dim == 128) return dt == PA_BF16 ? launch_t<128, __nv_bfloat16>(p, stream) : launch_t<128, __half>(p, stream);
+  return dt == PA_BF16 ? launch_t<64, __nv_bfloat16>(p, stream) : launch_t<64, __half>(p, stream);
+}
+
+}  // namespace pa

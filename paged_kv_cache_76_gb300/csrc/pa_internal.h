@@ -336,6 +336,26 @@ struct Kv4DecodeParams {
 // without the merge (launch_lse_merge)
 cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int head_dim, pa_dtype dt, cudaStream_t stream);
 
+// Chunked prefill over a 4-bit cache (kv4_prefill.cu): the merge included.
+struct Kv4PrefillParams {
+  const void* q;
+  const void* k_cache;
+  const void* v_cache;
+  const int32_t* q_start;
+  const int32_t* lens;
+  const int32_t* tables;
+  void* out;
+  float* part_o;  // [total_q * q_heads][max_splits][head_dim], as the decode partials
+  float* part_m;
+  float* part_l;
+  int* err;
+  int maxblk, num_reqs, total_q, max_q_len, q_heads, kv_heads, group, num_blocks, block_size, block_shift;
+  int split_tokens, max_splits, row_tiles;
+  int negative;      // scores change their sign before the softmax
+  float scale_log2;  // of what is left
+};
+cudaError_t launch_kv4_prefill(const Kv4PrefillParams& p, int head_dim, pa_dtype dt, cudaStream_t stream);
+
 // Pages forked on the device (fork.cu).
 struct ForkParams {
   const int32_t* tables;   // [num_old][maxblk]

@@ -65,6 +65,49 @@ int kv4_decode_setup(int num_seqs, int q_len, int q_heads, int kv_heads, int hea
   return PA_OK;
 }
 
+constexpr int kKv4PrefillUnit = 64;  // a key tile of the kernel
+constexpr int kKv4PrefillMin = 512;
+
+struct Kv4PrefillSetup {
+  int split, max_splits, row_tiles;
+  DecodeWorkspace ws;
+};
+
+int kv4_prefill_setup(int num_reqs, int total_q, int max_q_len, int q_heads, int kv_heads, int head_dim,
+                      int max_blocks_per_seq, int block_size, int split_tokens, Kv4PrefillSetup* s) {
+  if (num_reqs < 0 || num_reqs > 65535 || total_q < 0 || max_q_len < 1 || q_heads <= 0 || kv_heads <= 0 ||
+      kv_heads > 1024 || q_heads % kv_heads != 0 || q_heads / kv_heads > 16 || head_dim <= 0 ||
+      max_blocks_per_seq <= 0 || !block_size_ok(block_size))
+    return PA_ERR_INVALID;
+  const int64_t cap = (int64_t)max_blocks_per_seq * block_size;
+  const int64_t rows = (int64_t)max_q_len * (q_heads / kv_heads);
+  if (cap > INT32_MAX - 4096 || (int64_t)total_q * q_heads > INT32_MAX || rows > INT32_MAX - 4096 ||
+      (int64_t)max_q_len * q_heads > INT32_MAX)
+    return PA_ERR_INVALID;
+  s->row_tiles = (int)((rows + 255) / 256);
+  const int64_t whole = (cap + kKv4PrefillUnit - 1) / kKv4PrefillUnit * kKv4PrefillUnit;
+  int64_t split = split_tokens;
+  if (split_tokens == 0) {
+    const int64_t sms = num_sms() > 0 ? num_sms() : 152;
+    const int64_t units = (int64_t)num_reqs * kv_heads * s->row_tiles;
+    split = whole;
+    if (units > 0 && units < sms) {
+      const int64_t parts = sms / units;
+      split = (cap + parts - 1) / parts;
+      split = (split + kKv4PrefillUnit - 1) / kKv4PrefillUnit * kKv4PrefillUnit;
+      if (split < kKv4PrefillMin) split = kKv4PrefillMin;
+    }
+  }
+  if (split <= 0 || split % kKv4PrefillUnit != 0) return PA_ERR_INVALID;
+  if (split > whole) split = whole;
+  s->split = (int)split;
+  s->max_splits = (int)((cap + split - 1) / split);
+  if ((int64_t)num_reqs * kv_heads * s->row_tiles * s->max_splits > INT32_MAX) return PA_ERR_INVALID;
+  s->ws = s->max_splits > 1 ? decode_workspace_layout(total_q, q_heads, head_dim, s->max_splits)
+                            : DecodeWorkspace{0, 0, 0, 0};
+  return PA_OK;
+}
+
 }  // namespace
 
 }  // namespace pa
@@ -202,6 +245,76 @@ int pa_decode_kv4(const void* q, const void* k_cache, const void* v_cache, const
   mp.cap = max_blocks_per_seq * block_size;
   mp.q_len = q_len;
   return cuda_status(launch_lse_merge(mp, head_dim, dtype, to_stream(stream)));
+}
+
+int pa_chunked_prefill_kv4_split_tokens(int num_reqs, int max_q_len, int q_heads, int kv_heads, int max_blocks_per_seq,
+                                        int block_size, int split_tokens) {
+  Kv4PrefillSetup s;
+  const int st = kv4_prefill_setup(num_reqs, 0, max_q_len, q_heads, kv_heads, 64, max_blocks_per_seq, block_size,
+                                   split_tokens, &s);
+  return st != PA_OK ? st : s.split;
+}
+
+size_t pa_chunked_prefill_kv4_workspace_size(int num_reqs, int total_q, int max_q_len, int q_heads, int kv_heads,
+                                             int head_dim, int max_blocks_per_seq, int block_size, int split_tokens) {
+  Kv4PrefillSetup s;
+  if (kv4_prefill_setup(num_reqs, total_q, max_q_len, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size,
+                        split_tokens, &s) != PA_OK)
+    return 0;
+  return s.ws.bytes;
+}
+
+int pa_chunked_prefill_kv4(const void* q, const int32_t* q_start, const int32_t* context_lens, const void* k_cache,
+                           const void* v_cache, const int32_t* block_tables, int max_blocks_per_seq, int num_reqs,
+                           int total_q, int max_q_len, int q_heads, int kv_heads, int head_dim, int block_size,
+                           int num_blocks, float scale, int split_tokens, void* workspace, size_t workspace_bytes,
+                           void* out, pa_dtype dtype, pa_stream stream) {
+  int st = check_kv4_shape(num_blocks, block_size, kv_heads, head_dim, dtype);
+  if (st != PA_OK) return st;
+  // masked scores are -inf before the scale meets them: it must not vanish
+  if (!std::isnormal(scale) || !std::isfinite(scale * 1.4426950408889634f)) return PA_ERR_INVALID;
+  Kv4PrefillSetup s;
+  st = kv4_prefill_setup(num_reqs, total_q, max_q_len, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size,
+                         split_tokens, &s);
+  if (st != PA_OK) return st;
+  if (num_reqs == 0 || total_q == 0) return PA_OK;
+  if (!q || !q_start || !context_lens || !k_cache || !v_cache || !block_tables || !out) return PA_ERR_INVALID;
+  if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return PA_ERR_INVALID;
+  if (s.ws.bytes > 0 && (!workspace || workspace_bytes < s.ws.bytes || !aligned16(workspace)))
+    return PA_ERR_WORKSPACE;
+  int* err = device_error_ptr();
+  if (!err) return PA_ERR_CUDA;
+  Kv4PrefillParams p{};
+  p.q = q;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.q_start = q_start;
+  p.lens = context_lens;
+  p.tables = block_tables;
+  p.out = out;
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (s.ws.bytes) {
+    p.part_o = reinterpret_cast<float*>(ws + s.ws.o_off);
+    p.part_m = reinterpret_cast<float*>(ws + s.ws.m_off);
+    p.part_l = reinterpret_cast<float*>(ws + s.ws.l_off);
+  }
+  p.err = err;
+  p.maxblk = max_blocks_per_seq;
+  p.num_reqs = num_reqs;
+  p.total_q = total_q;
+  p.max_q_len = max_q_len;
+  p.q_heads = q_heads;
+  p.kv_heads = kv_heads;
+  p.group = q_heads / kv_heads;
+  p.num_blocks = num_blocks;
+  p.block_size = block_size;
+  p.block_shift = log2_of(block_size);
+  p.split_tokens = s.split;
+  p.max_splits = s.max_splits;
+  p.row_tiles = s.row_tiles;
+  p.negative = scale < 0.f;
+  p.scale_log2 = std::fabs(scale) * 1.4426950408889634f;
+  return cuda_status(launch_kv4_prefill(p, head_dim, dtype, to_stream(stream)));
 }
 
 size_t pa_fork_blocks_workspace_size(int num_new, int num_blocks) {

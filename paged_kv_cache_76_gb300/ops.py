@@ -53,6 +53,9 @@ __all__ = [
     "decode_kv4",
     "decode_kv4_split_tokens",
     "decode_kv4_workspace_size",
+    "chunked_prefill_kv4",
+    "chunked_prefill_kv4_split_tokens",
+    "chunked_prefill_kv4_workspace_size",
     "fork_blocks",
     "copy_pages",
     "get_device_error",
@@ -993,6 +996,54 @@ def decode_kv4(q, k_cache, v_cache, block_tables, context_lens, scale, out=None,
     _keep(out, workspace)
     _launch("pa_decode_kv4", _ptr(q, "q", dev), kc, vc, tables, maxblk, lens, B, ql, hq, hkv, d, bs, nb, float(scale),
             split_tokens, ws_ptr, ws_bytes, _ptr(out, "out", dev), code, handle)
+    return out
+
+
+def chunked_prefill_kv4_split_tokens(num_reqs, max_q_len, q_heads, kv_heads, max_blocks_per_seq, block_size,
+                                     split_tokens=0) -> int:
+    """Partition size such a pa_chunked_prefill_kv4 call uses (0: its automatic choice)."""
+    return check(_lib.lib().pa_chunked_prefill_kv4_split_tokens(int(num_reqs), int(max_q_len), int(q_heads),
+                                                                int(kv_heads), int(max_blocks_per_seq),
+                                                                int(block_size), int(split_tokens)),
+                 "pa_chunked_prefill_kv4_split_tokens")
+
+
+def chunked_prefill_kv4_workspace_size(num_reqs, total_q, max_q_len, q_heads, kv_heads, head_dim, max_blocks_per_seq,
+                                       block_size, split_tokens=0) -> int:
+    return int(_lib.lib().pa_chunked_prefill_kv4_workspace_size(num_reqs, total_q, max_q_len, q_heads, kv_heads,
+                                                                head_dim, max_blocks_per_seq, block_size,
+                                                                split_tokens))
+
+
+@functools.lru_cache(maxsize=4096)
+def _kv4_prefill_workspace(dev, *sizes) -> int:  # dev: the choice depends on the current device
+    return chunked_prefill_kv4_workspace_size(*sizes)
+
+
+def chunked_prefill_kv4(q, q_start, context_lens, k_cache, v_cache, block_tables, scale, max_q_len, out=None,
+                        split_tokens=0, workspace=None, stream=None):
+    """pa_chunked_prefill_kv4: :func:`chunked_prefill` over a 4-bit cache.  ``scale`` is not zero."""
+    if q.dim() != 3:
+        raise ValueError("q is [total_q, q_heads, head_dim]")
+    dtype, dev, qshape = q.dtype, q.get_device(), q.shape
+    T, hq, d = qshape
+    kc, vc, nb, bs, hkv = _kv4_ptrs(k_cache, v_cache, dev, d)
+    code = dtype_code(dtype)
+    R = context_lens.shape[0]
+    lens = _rows_ptr(context_lens, "context_lens", dev, R)
+    starts = _rows_ptr(q_start, "q_start", dev, R + 1)
+    tables = _table_ptr(block_tables, dev, R)
+    if out is None:
+        out = _empty(qshape, dtype, q.device, stream, returned=True)
+    elif out.shape != qshape or out.dtype != dtype:
+        raise ValueError("out must have q's shape, dtype and device")
+    handle = _stream_on(dev, stream)
+    maxblk, max_q_len, split_tokens = block_tables.shape[1], int(max_q_len), int(split_tokens)
+    n = _kv4_prefill_workspace(dev, R, T, max_q_len, hq, hkv, d, maxblk, bs, split_tokens) if workspace is None else 0
+    workspace, ws_ptr, ws_bytes = _scratch(workspace, n, q.device, dev, stream)
+    _keep(out, workspace)
+    _launch("pa_chunked_prefill_kv4", _ptr(q, "q", dev), starts, lens, kc, vc, tables, maxblk, R, T, max_q_len, hq, hkv,
+            d, bs, nb, float(scale), split_tokens, ws_ptr, ws_bytes, _ptr(out, "out", dev), code, handle)
     return out
 
 

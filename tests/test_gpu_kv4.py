@@ -286,6 +286,94 @@ def test_bad_blocks_and_lengths(ops):
         assert torch.equal(out[1:], good[1:])
 
 
+def prefill_rows(lens, start):
+    def rows_of(r):
+        n = start[r + 1] - start[r]
+        return slice(start[r], start[r + 1]), [lens[r] - n + i + 1 for i in range(n)]
+    return rows_of
+
+
+CHUNKS = [(1, 1), (130, 7), (64, 64), (200, 33), (700, 0), (65, 65), (0, 0), (257, 1), (300, 129)]  # (context, chunk)
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs,dtype", [
+    (32, 8, 128, 16, BF), (28, 4, 128, 16, HF), (8, 1, 64, 4, BF), (12, 12, 64, 8, HF), (16, 1, 128, 32, BF),
+    (18, 2, 64, 32, BF), (8, 2, 128, 4, HF), (4, 2, 128, 8, BF)])
+@pytest.mark.parametrize("split", [0, 64, 256])
+def test_prefill(ops, hq, hkv, d, bs, dtype, split):
+    lens = [n for n, _ in CHUNKS]
+    start = np.concatenate([[0], np.cumsum([c for _, c in CHUNKS])])
+    b = Batch(ops, lens, hkv, d, bs, dtype)
+    q = b.q(int(start[-1]) + 2, hq)
+    scale = d ** -0.5
+    out = torch.full_like(q, 7.0)
+    ops.chunked_prefill_kv4(q, i32(start), b.ctx, b.kc, b.vc, b.tables, scale, 140, out=out, split_tokens=split)
+    assert ops.get_device_error() == 0
+    assert bool((out[-2:] == 7).all())  # rows behind the last chunk
+    b.check(out, q, scale, prefill_rows(lens, start))
+    again = ops.chunked_prefill_kv4(q, i32(start), b.ctx, b.kc, b.vc, b.tables, scale, 140, split_tokens=split)
+    assert torch.equal(out[:-2], again[:-2])
+
+
+@pytest.mark.parametrize("size,spread,scale", [(1e-30, 1.0, 0.09), (1e-30, 1.0, 1e-12), (3e4, 1.0, 1e-5), (2.0, 3e-3, 0.09),
+                                               (40.0, 5.0, 0.09), (2.0, 1.0, -0.09)])
+def test_prefill_of_any_size(ops, size, spread, scale):
+    b = Batch(ops, [400, 70], 2, 128, 16, BF, spread=spread)
+    q = b.q(100 + 70, 8, size=size)
+    for split in (0, 64):
+        out = ops.chunked_prefill_kv4(q, i32([0, 100, 170]), b.ctx, b.kc, b.vc, b.tables, scale, 100, split_tokens=split)
+        b.check(out, q, scale, prefill_rows([400, 70], [0, 100, 170]))
+    assert ops.get_device_error() == 0
+
+
+@pytest.mark.parametrize("split", [0, 64])
+def test_prefill_past_a_token_that_is_not_a_number(ops, split):
+    lens, hq, hkv, d, n = [150, 300], 8, 2, 128, 150
+    b = Batch(ops, lens, hkv, d, 16, BF)
+    start = [0, n, n + 100]
+    q = b.q(start[-1], hq)
+    args = (q, i32(start), b.ctx)
+    clean = ops.chunked_prefill_kv4(*args, b.kc, b.vc, b.tables, 0.1, n, split_tokens=split)
+
+    def slot(r, t):
+        return i32([int(b.tables[r, t // 16]) * 16 + t % 16])
+    keep = [ops.dequantize_kv4(b.kc, b.vc, slot(r, t), d) for r, t in ((0, 77), (1, 250))]
+    badv, badk = keep[0][1].clone(), keep[1][0].clone()  # but for one element what the cache holds: written as it is
+    badv[0, 1, 37], badk[0, 0, 5] = float("inf"), float("nan")
+    kc, vc = b.kc.clone(), b.vc.clone()
+    ops.quantize_and_cache(keep[0][0], badv, slot(0, 77), kc, vc)   # seen by queries 77 on
+    ops.quantize_and_cache(badk, keep[1][1], slot(1, 250), kc, vc)  # by queries 50 on of the second chunk
+    out = ops.chunked_prefill_kv4(*args, kc, vc, b.tables, 0.1, n, split_tokens=split)
+    nan = out.isnan()
+    assert bool(nan[77:n, 4:, 32:48].all()) and bool(nan[n + 50:, :4].all())
+    nan[77:n, 4:, 32:48] = False
+    nan[n + 50:, :4] = False
+    assert not bool(nan.any())
+    for got, want in ((out[:77], clean[:77]), (out[77:n, :4], clean[77:n, :4]), (out[n:n + 50], clean[n:n + 50]),
+                      (out[n + 50:, 4:], clean[n + 50:, 4:])):
+        assert torch.equal(got, want)
+
+
+def test_prefill_refuses_requests(ops):
+    b = Batch(ops, [60, 90, 40], 2, 128, 16, BF)
+    start = [0, 10, 30, 45]
+    q = b.q(45, 8)
+    good = ops.chunked_prefill_kv4(q, i32(start), b.ctx, b.kc, b.vc, b.tables, 0.1, 20)
+    assert ops.get_device_error() == 0
+    for lens, starts, most in [([60, 19, 40], start, 20), ([60, 10 ** 6, 40], start, 20), ([60, 90, 40], start, 17),
+                               ([60, 90, 40], [0, 10, 4, 45], 20), ([60, 90, 40], [0, 10, 60, 45], 20)]:
+        out = torch.full_like(q, 7.0)
+        ops.chunked_prefill_kv4(q, i32(starts), i32(lens), b.kc, b.vc, b.tables, 0.1, most, out=out)
+        assert ops.get_device_error() == 5
+        assert torch.equal(out[:10], good[:10])
+        assert bool((out[10:30] == 7).all()) or starts != start
+    t = b.tables.clone()
+    t[1, 1] = -3
+    out = ops.chunked_prefill_kv4(q, i32(start), b.ctx, b.kc, b.vc, t, 0.1, 20)
+    assert ops.get_device_error() == 1
+    assert torch.equal(out[:10], good[:10]) and torch.equal(out[30:], good[30:])
+
+
 def test_another_stream_a_capture_and_a_recording(ops):
     b = Batch(ops, [300, 5, 77], 2, 128, 16, BF)
     q = b.q(3, 8)
