@@ -7,12 +7,14 @@
 // softmax in registers, P over the same buffer, O_x += P_x V with P from tensor
 // memory.  What differs:
 //
-//  * The two producer warps do not load K and V, they make them: pages come by
-//    bulk copy into a small ring, and a warp writes the fp16 tile in the
-//    128-byte-swizzled layout that the MMAs read (exact: kv4.cuh), a quarter of
-//    the shared-memory traffic that the MMAs cause.  A task is the 16 elements
-//    of a scale; lanes of the second half-row store their two 16-byte pieces in
-//    the other order, so that a store's eight lanes meet eight banks.
+//  * K and V tiles are not loaded but made: pages come by bulk copy (their codes
+//    to one place and their scales to another, so that a token is found by its
+//    number whatever the block size), and a warp writes the fp16 tile in the
+//    128-byte-swizzled layout that the MMAs read (exact: kv4.cuh).  Three warps
+//    make K tiles in turn and three V tiles; a warp's next pages come while the
+//    others work.  A lane takes the 16 elements of a scale at a time; lanes of
+//    the second half-row store their two 16-byte pieces in the other order, so
+//    that a store's eight lanes meet eight banks.
 //  * All operands are fp16 whatever the type of q (see kv4_decode.cu): a row of
 //    Q is brought to [2^13, 2^14) by a power of two that its softmax takes back.
 //  * V rows behind the last key are zeros; a V group that is not a number becomes
@@ -21,8 +23,8 @@
 //  * A context may be cut into partitions of split_tokens keys, a unit each,
 //    where there are few units; a merge joins them.
 //
-// Warps: 0, 1 MMA issuers of tiles A, B; 2 makes K, 3 makes V; 4..7 softmax of
-// tile A, 8..11 of tile B.  Every wait is bounded.
+// Warps: 0, 1 MMA issuers of tiles A, B; 2..7 make K and V; 8..11 softmax of
+// tile A, 12..15 of tile B.  Every wait is bounded.
 #include <float.h>
 #include <limits.h>
 
@@ -36,8 +38,9 @@ namespace {
 constexpr int kRows = 128;  // rows per Q tile
 constexpr int kKeys = 64;   // keys per K/V tile
 constexpr int kStages = 4;  // of K and of V, fp16
-constexpr int kRaw = 3;     // tiles of pages under way, of K and of V
-constexpr int kThreads = 32 * 12;
+constexpr int kMakers = 3;  // warps that make K tiles, and V tiles, in turn
+constexpr int kThreads = 32 * 16;
+constexpr int kSoftmaxWarp0 = 8;
 constexpr uint32_t kTmem = 512;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr float kRescale = 8.f;
@@ -52,13 +55,14 @@ struct Kv4PrefillSmem {
   static constexpr int Q_OFF = 0;
   static constexpr int K_OFF = Q_OFF + 2 * QTILE;
   static constexpr int V_OFF = K_OFF + kStages * Tile::BYTES;
-  static constexpr int RAW_OFF = V_OFF + kStages * Tile::BYTES;  // K's ring, then V's
-  static constexpr int BAR_OFF = RAW_OFF + 2 * kRaw * RAW;
-  static constexpr int NBARS = 4 * kStages + 2 * kRaw + 15;
+  static constexpr int RAW_OFF = V_OFF + kStages * Tile::BYTES;  // a tile per maker: its codes, then its scales
+  static constexpr int BAR_OFF = RAW_OFF + 2 * kMakers * RAW;
+  static constexpr int NBARS = 4 * kStages + 2 * kMakers + 15;
   static constexpr int SLOT_OFF = BAR_OFF + NBARS * 8;
   static constexpr int NAN_OFF = SLOT_OFF + 8;
   static constexpr int BYTES = NAN_OFF + D / kKv4Group * 4 + 1024;
   static_assert(BYTES <= 227 * 1024, "shared memory per CTA");
+  static_assert(kMakers <= kStages, "the last tile of every maker is still the last of its stage at the end");
 };
 
 // barrier indices
@@ -66,13 +70,13 @@ constexpr int B_KFULL = 0;                      // [kStages] the producer warp w
 constexpr int B_KEMPTY = B_KFULL + kStages;     // [kStages] one commit per issuer after S_x(j)
 constexpr int B_VFULL = B_KEMPTY + kStages;
 constexpr int B_VEMPTY = B_VFULL + kStages;     // [kStages] one commit per issuer after P.V_x(j)
-constexpr int B_RAW = B_VEMPTY + kStages;       // [K, V][kRaw] pages landed
-constexpr int B_SFULL = B_RAW + 2 * kRaw;       // [2 Q tiles][2 S buffers]
+constexpr int B_RAW = B_VEMPTY + kStages;       // [maker] its pages landed
+constexpr int B_SFULL = B_RAW + 2 * kMakers;    // [2 Q tiles][2 S buffers]
 constexpr int B_PFULL = B_SFULL + 4;            // [2][2] four softmax warps
 constexpr int B_OFULL = B_PFULL + 4;            // [2][2] P.V_x(j) complete
 constexpr int B_QFULL = B_OFULL + 4;            // [2]
 constexpr int B_MMADONE = B_QFULL + 2;
-static_assert(B_MMADONE + 1 == 4 * kStages + 2 * kRaw + 15, "barrier count");
+static_assert(B_MMADONE + 1 == 4 * kStages + 2 * kMakers + 15, "barrier count");
 
 struct Unit {
   int r, h, row0, part, qs, chunk, p0, rows, k0, kend, ntiles;
@@ -142,7 +146,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
       mbar_init(bar(B_VFULL + i), 1);
       mbar_init(bar(B_VEMPTY + i), tiles);
     }
-    for (int i = 0; i < 2 * kRaw; ++i) mbar_init(bar(B_RAW + i), 1);
+    for (int i = 0; i < 2 * kMakers; ++i) mbar_init(bar(B_RAW + i), 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(bar(B_SFULL + i), 1);
       mbar_init(bar(B_PFULL + i), 4);
@@ -163,87 +167,86 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
   const uint32_t tmem = *tmem_slot;
   griddep_launch_dependents();
 
-  if (warp == 2 || warp == 3) {
+  if (warp >= 2 && warp < kSoftmaxWarp0) {
     // ------------------------------------------------------------ K and V
-    const int isv = warp - 2;
+    // warps 2, 4, 6 make K tiles, 3, 5, 7 V tiles, every kMakers-th each
+    const int maker = warp - 2, isv = maker & 1, first = maker >> 1;
     const uint8_t* cache = static_cast<const uint8_t*>(isv ? p.v_cache : p.k_cache);
-    uint8_t* raw = smem + L::RAW_OFF + isv * kRaw * L::RAW;
+    uint8_t* codes = smem + L::RAW_OFF + maker * L::RAW;
+    uint8_t* scales = codes + kKeys * R::CODES;
     uint8_t* tile0 = smem + (isv ? L::V_OFF : L::K_OFF);
-    const int full0 = isv ? B_VFULL : B_KFULL, empty0 = isv ? B_VEMPTY : B_KEMPTY, raw0 = B_RAW + isv * kRaw;
+    const int full0 = isv ? B_VFULL : B_KFULL, empty0 = isv ? B_VEMPTY : B_KEMPTY;
+    const uint32_t rawbar = bar(B_RAW + maker);
     const int32_t* trow = p.tables + (size_t)w.r * p.maxblk;
     const int bs = p.block_size, bsh = p.block_shift, page = bs * R::BYTES;
     const uint64_t pol = p.row_tiles == 1 ? policy_evict_first() : policy_evict_last();  // other row tiles re-read them
     griddep_wait();
+    // pages of tile j: lane 2i their i-th's codes, lane 2i + 1 its scales
     auto issue = [&](int j) {
-      const int s = j % kRaw, ts = w.k0 + j * kKeys;
+      const int ts = w.k0 + j * kKeys;
       const int npages = (min(kKeys, w.kend - ts) + bs - 1) >> bsh;
-      const bool mine = lane < npages;
-      int b = mine ? __ldg(trow + (ts >> bsh) + lane) : -1;
+      const int i = lane >> 1, part = lane & 1;
+      const bool mine = i < npages;
+      int b = mine ? __ldg(trow + (ts >> bsh) + i) : -1;
       if (mine && (b < 0 || b >= p.num_blocks)) {
         record_error(p.err, PA_DEVERR_BLOCK_ID);
         b = -1;
       }
-      const int copies = __popc(__ballot_sync(kAll, b >= 0));
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive_expect_tx(bar(raw0 + s), copies * page);
+      const int pages = __popc(__ballot_sync(kAll, b >= 0)) >> 1;
+      if (lane == 0) mbar_arrive_expect_tx(rawbar, pages * page);
       __syncwarp();
       if (mine) {
-        uint8_t* dst = raw + s * L::RAW + lane * page;
+        const int bytes = bs * (part ? R::SCALES : R::CODES);
+        uint8_t* dst = (part ? scales : codes) + i * bytes;
         if (b >= 0) {
-          bulk_load_hint(smem_u32(dst), cache + ((size_t)b * p.kv_heads + w.h) * page, page, bar(raw0 + s), pol);
+          bulk_load_hint(smem_u32(dst), cache + ((size_t)b * p.kv_heads + w.h) * page + (part ? bs * R::CODES : 0), bytes,
+                         rawbar, pol);
         } else {  // a bad block id: zeros
-          for (int k = 0; k < page; k += 16) *reinterpret_cast<uint4*>(dst + k) = make_uint4(0, 0, 0, 0);
+          for (int k = 0; k < bytes; k += 16) *reinterpret_cast<uint4*>(dst + k) = make_uint4(0, 0, 0, 0);
         }
       }
     };
-    for (int j = 0; j < min(kRaw, w.ntiles); ++j) issue(j);
+    if (first < w.ntiles) issue(first);
     bool failed = false;
-    int j = 0;
-    for (; j < w.ntiles; ++j) {
-      const int s = j % kStages, rs = j % kRaw;
-      if (!mbar_wait(bar(raw0 + rs), (j / kRaw) & 1) ||
-          (j >= kStages && !mbar_wait(bar(empty0 + s), (j / kStages - 1) & 1))) {
+    int n = 0;  // tiles made
+    for (int j = first; j < w.ntiles; j += kMakers, ++n) {
+      const int s = j % kStages;
+      if (!__all_sync(kAll, mbar_wait(rawbar, n & 1) &&
+                                (j < kStages || mbar_wait(bar(empty0 + s), (j / kStages - 1) & 1)))) {
         failed = true;
         break;
       }
-      __syncwarp();
       const int ts = w.k0 + j * kKeys;
       const int nvalid = min(kKeys, w.kend - ts);
-      const uint8_t* src = raw + rs * L::RAW;
       uint8_t* dst = tile0 + s * Tile::BYTES;
-      constexpr int PER_ROW = D / kKv4Group;
+      constexpr int PER_ROW = D / kKv4Group, STEP = 32 / PER_ROW;  // rows of a step
+      const int g = lane % PER_ROW, row0 = lane / PER_ROW, flip = g >> 2;
 #pragma unroll 4
-      for (int t = lane; t < kKeys * PER_ROW; t += 32) {
-        const int row = t / PER_ROW, g = t % PER_ROW;
-        const uint8_t* pg = src + (row >> bsh) * page;
-        const int o = row & (bs - 1);
-        const uint2 codes = *reinterpret_cast<const uint2*>(pg + o * R::CODES + 8 * g);
-        uint32_t byte = row < nvalid ? pg[bs * R::CODES + o * R::SCALES + g] : 0u;
+      for (int row = row0; row < kKeys; row += STEP) {
+        const uint2 c = *reinterpret_cast<const uint2*>(codes + row * R::CODES + 8 * g);
+        uint32_t byte = row < nvalid ? scales[row * R::SCALES + g] : 0u;
         if (isv && byte >= kKv4FirstInf) {
           byte = 0;
           atomicMin(&first_nan[g], ts + row);
         }
         const uint32_t s2 = kv4_scale2(byte);
         uint32_t x[8];
-        kv4_unpack(codes.x, *reinterpret_cast<uint32_t(*)[4]>(&x[0]));
-        kv4_unpack(codes.y, *reinterpret_cast<uint32_t(*)[4]>(&x[4]));
+        kv4_unpack(c.x, *reinterpret_cast<uint32_t(*)[4]>(&x[0]));
+        kv4_unpack(c.y, *reinterpret_cast<uint32_t(*)[4]>(&x[4]));
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = hmul2_u(x[e], s2);
         const uint4 c0 = make_uint4(x[0], x[1], x[2], x[3]), c1 = make_uint4(x[4], x[5], x[6], x[7]);
-        const int flip = g >> 2;
         *reinterpret_cast<uint4*>(dst + Tile::offset(row, 2 * g + flip)) = flip ? c1 : c0;
         *reinterpret_cast<uint4*>(dst + Tile::offset(row, 2 * g + (flip ^ 1))) = flip ? c0 : c1;
       }
       fence_proxy_async_smem();  // the tile before the MMAs, the pages before the next copies over them
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(full0 + s));
-      if (j + kRaw < w.ntiles) issue(j + kRaw);
+      if (j + kMakers < w.ntiles) issue(j + kMakers);
     }
     if (failed) {
       if (lane == 0) record_error(p.err, PA_DEVERR_TIMEOUT);
-      for (int t = j; t < w.ntiles && t < j + kRaw; ++t)  // copies in flight land before exit (bounded)
-        mbar_wait(bar(raw0 + t % kRaw), (t / kRaw) & 1);
+      mbar_wait(rawbar, n & 1);  // copies in flight land before exit (bounded)
     }
   } else if (warp < 2) {
     // ------------------------------------------------------------ MMA issuers
@@ -294,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
     }
   } else {
     // ------------------------------------------------------------ softmax
-    const int x = (warp - 4) >> 2;
+    const int x = (warp - kSoftmaxWarp0) >> 2;
     const int quarter = warp & 3, row = quarter * 32 + lane;
     if (x < tiles) {
       const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
@@ -419,10 +422,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
         }
       }
       const int last = w.ntiles - 1;
-      // the unit's last P.V, and (for first_nan) the V producer's last arrival
-      if (ok)
-        ok = mbar_wait(bar(B_OFULL + 2 * x + (last & 1)), (last >> 1) & 1) &&
-             mbar_wait(bar(B_VFULL + last % kStages), (last / kStages) & 1);
+      // the unit's last P.V, and (for first_nan) the V makers' last arrivals
+      if (ok) ok = mbar_wait(bar(B_OFULL + 2 * x + (last & 1)), (last >> 1) & 1);
+      for (int j = max(last - kMakers + 1, 0); j <= last; ++j)
+        ok = ok && mbar_wait(bar(B_VFULL + j % kStages), (j / kStages) & 1);
       if (__all_sync(kAll, ok)) {
         tc_fence_after();
         const size_t orow = (size_t)(w.qs + qi) * p.q_heads + w.h * G + g;
