@@ -34,6 +34,8 @@
 // the queries that do see such a token get their NaN at the end.
 #include <float.h>
 
+#include <type_traits>
+
 #include "kv4.cuh"
 #include "pa_internal.h"
 
@@ -50,17 +52,16 @@ constexpr unsigned kAll = 0xffffffffu;
 
 template <int D, int STAGES>
 struct Kv4DecodeSmem {
-  static constexpr int HALF = kStageTokens * Kv4Row<D>::BYTES;  // K or V of a stage
+  // of a stage: codes of K, its scales, codes of V, its scales
+  static constexpr int CODES = kStageTokens * Kv4Row<D>::CODES;
+  static constexpr int SCALES = kStageTokens * Kv4Row<D>::SCALES;
+  static constexpr int HALF = CODES + SCALES;
   static constexpr int STAGE = 2 * HALF;
   static constexpr int BAR_OFF = kWarps * STAGES * STAGE;
   static constexpr int NAN_OFF = BAR_OFF + kWarps * STAGES * 8;
   static constexpr int TAB_OFF = NAN_OFF + kWarps * (D / kKv4Group) * 4;
   static constexpr int bytes(int entries) { return TAB_OFF + kWarps * entries * 4; }
 };
-
-__device__ __forceinline__ float2 unpack_half2(uint32_t h) {
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
-}
 
 template <int D, int NT, int STAGES, typename T>
 __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4DecodeParams p) {
@@ -169,28 +170,30 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
   const int bsh = p.block_shift;
   const int page = bs * R::BYTES;
   const uint64_t pol = policy_evict_first();
-  // stage j: tokens [ts, ts + 32), 32 / bs pages of K, then of V (only those that hold tokens of the partition)
+  // stage j: tokens [ts, ts + 32); lane 4i + {0, 1, 2, 3} brings page i's codes and scales of K, of V (pages that
+  // hold tokens of the partition)
   auto issue = [&](int j) {
     const int s = j % STAGES;
     const int ts = tok0 + kStageTokens * j;
     const int npages = (min(kStageTokens, tok1 - ts) + bs - 1) >> bsh;
     const uint32_t bar = smem_u32(&bars[s]);
-    uint8_t* stage = ring + s * L::STAGE;
-    const int i = lane >> 1, isv = lane & 1;
-    const bool mine = i < npages;
+    const int i = lane >> 2;
+    const bool mine = i < npages, isv = lane & 2, part = lane & 1;
     const int b = mine ? tab[((ts - tok0) >> bsh) + i] : -1;
-    const int copies = __popc(__ballot_sync(kAll, mine && b >= 0));
+    const int copies = __popc(__ballot_sync(kAll, b >= 0)) >> 1;  // pages, of K and of V
     fence_proxy_async_smem();  // this stage's earlier reads and writes before the copies
     __syncwarp();
     if (lane == 0) mbar_arrive_expect_tx(bar, copies * page);
     __syncwarp();
     if (mine) {
-      uint8_t* dst = stage + isv * L::HALF + i * page;
+      const int bytes = bs * (part ? R::SCALES : R::CODES);
+      uint8_t* dst = ring + s * L::STAGE + (isv ? L::HALF : 0) + (part ? L::CODES : 0) + i * bytes;
       if (b >= 0) {
-        const uint8_t* src = static_cast<const uint8_t*>(isv ? p.v_cache : p.k_cache) + ((size_t)b * p.kv_heads + h) * page;
-        bulk_load_hint(smem_u32(dst), src, page, bar, pol);
+        const uint8_t* src = static_cast<const uint8_t*>(isv ? p.v_cache : p.k_cache) +
+                             ((size_t)b * p.kv_heads + h) * page + (part ? bs * R::CODES : 0);
+        bulk_load_hint(smem_u32(dst), src, bytes, bar, pol);
       } else {  // a bad block id: zeros
-        for (int k = 0; k < page; k += 16) *reinterpret_cast<uint4*>(dst + k) = make_uint4(0, 0, 0, 0);
+        for (int k = 0; k < bytes; k += 16) *reinterpret_cast<uint4*>(dst + k) = make_uint4(0, 0, 0, 0);
       }
     }
   };
@@ -209,7 +212,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
 #pragma unroll
     for (int mt = 0; mt < KSTEPS; ++mt) acc[nt][mt][0] = acc[nt][mt][1] = acc[nt][mt][2] = acc[nt][mt][3] = 0.f;
   }
-  const int causal0 = ctx - (p.q_len - 1);  // tokens from here on are hidden from some query
+  const int causal0 = ctx - (p.q_len - 1);  // tokens from here on are hidden from some query (q_len 1: from ctx on)
 
   for (int j = 0; j < min(nstages, STAGES); ++j) issue(j);
   const int pg = g ^ ((g >> 1) & 1);        // token row of this lane's K fragments
@@ -227,8 +230,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
     uint8_t* kst = ring + s * L::STAGE;
     uint8_t* vst = kst + L::HALF;
     // where token t of the stage has its codes and scales
-    auto code_at = [&](int t) { return (t >> bsh) * page + (t & (bs - 1)) * R::CODES; };
-    auto scale_at = [&](int t) { return (t >> bsh) * page + bs * R::CODES + (t & (bs - 1)) * R::SCALES; };
+    auto code_at = [](int t) { return t * R::CODES; };
+    auto scale_at = [](int t) { return L::CODES + t * R::SCALES; };
     __syncwarp();  // zeroed pages
     if (ts + kStageTokens > tok1) {
       const int t = lane;  // a token per lane
@@ -253,9 +256,9 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
       __syncwarp();
     }
 
-    const int tiles = (min(kStageTokens, tok1 - ts) + 15) >> 4;
-    for (int q = 0; q < tiles; ++q) {
-      const int tb = 16 * q;
+    // 16 tokens from tb on; `all`: every column sees all of them
+    auto tile = [&](const int tb, const auto all_t) {
+      constexpr bool all = decltype(all_t)::value;
       const int t0 = ts + tb + pg;  // this lane's score rows: tokens t0, t0 + 8
       float sacc[NT][4];
 #pragma unroll
@@ -297,10 +300,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
       uint32_t pb0[NT], pb1[NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float s0 = t0 < lim[nt][0] ? sacc[nt][0] * sl2[nt][0] : -INFINITY;
-        const float s1 = t0 < lim[nt][1] ? sacc[nt][1] * sl2[nt][1] : -INFINITY;
-        const float s2 = t0 + 8 < lim[nt][0] ? sacc[nt][2] * sl2[nt][0] : -INFINITY;
-        const float s3 = t0 + 8 < lim[nt][1] ? sacc[nt][3] * sl2[nt][1] : -INFINITY;
+        const float s0 = all || t0 < lim[nt][0] ? sacc[nt][0] * sl2[nt][0] : -INFINITY;
+        const float s1 = all || t0 < lim[nt][1] ? sacc[nt][1] * sl2[nt][1] : -INFINITY;
+        const float s2 = all || t0 + 8 < lim[nt][0] ? sacc[nt][2] * sl2[nt][0] : -INFINITY;
+        const float s3 = all || t0 + 8 < lim[nt][1] ? sacc[nt][3] * sl2[nt][1] : -INFINITY;
         // m is raised to the column's maximum only when a score passes it by
         // more than kRescale, so most tiles need no maximum across lanes: a
         // vote says that no lane has such a score
@@ -376,6 +379,14 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
           for (int nt = 0; nt < NT; ++nt) mma_16816<__half>(acc[nt][mt], a, pb0[nt], pb1[nt]);
         }
       }
+    };
+    if (ts + kStageTokens <= min(tok1, causal0)) {
+#pragma unroll
+      for (int q = 0; q < kStageTokens / 16; ++q) tile(16 * q, std::true_type{});
+    } else {
+      const int tiles = (min(kStageTokens, tok1 - ts) + 15) >> 4;
+#pragma unroll 1
+      for (int q = 0; q < tiles; ++q) tile(16 * q, std::false_type{});
     }
     __syncwarp();
     if (j + STAGES < nstages) issue(j + STAGES);
