@@ -735,7 +735,7 @@ int pa_dequantize_kv4(const void* k_cache, const void* v_cache, const int32_t* s
  *                 gives a zero row
  *   q_len         >= 1, with (q_heads / kv_heads) * q_len <= 32 and a group of at
  *                 most 16
- *   split_tokens  0, or a multiple of 32 no larger than 256 * block_size;
+ *   split_tokens  0, or a multiple of 32 no larger than 1024 * block_size;
  *                 pa_decode_kv4_split_tokens returns the partition size such a
  *                 call uses, or PA_ERR_INVALID
  *   workspace     at least pa_decode_kv4_workspace_size(...) bytes (NULL where

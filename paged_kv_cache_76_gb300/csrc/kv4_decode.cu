@@ -1,11 +1,11 @@
 // Decode attention over a 4-bit paged cache (see kv4.cuh for the page), one
 // query per request or a few causal ones, for sm_103a.
 //
-// As in decode.cu, one warp owns one (request r, KV head h, partition c) unit
-// and walks its tokens 16 at a time, every query head of the group on one read
-// of K and V, partitions joined by the log-sum-exp merge.  A page of a head is
-// contiguous, so each comes by one bulk copy, 32 tokens of K and V per stage of
-// the warp's own ring.
+// A CTA of four warps owns one (request r, KV head h, partition c) unit: warp w
+// takes the stages of 32 tokens w, w + 4, ..., every query head of the group on
+// one read of K and V; the warps' parts are joined in shared memory and the
+// partitions by the log-sum-exp merge.  The codes and the scales of a page are
+// contiguous, so each comes by a bulk copy into the warp's own ring.
 //
 // A cache element is exact in fp16, so the products are fp16 MMAs whatever the
 // type of q: a query row is brought to [2^13, 2^14) by a power of two (taken
@@ -45,27 +45,31 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kStageTokens = 32;
-constexpr int kMaxEntries = 256;  // Block Table entries of a partition
+constexpr int kMaxEntries = 1024;  // Block Table entries of a partition
 constexpr float kRescale = 8.f;   // a reference is raised when a score passes it by more (log2 units)
 constexpr float kShift = 7.f;     // weights are 2^(s - m + kShift) <= 2^15
 constexpr unsigned kAll = 0xffffffffu;
 
-template <int D, int STAGES>
+template <int D, int NT, int STAGES>
 struct Kv4DecodeSmem {
   // of a stage: codes of K, its scales, codes of V, its scales
   static constexpr int CODES = kStageTokens * Kv4Row<D>::CODES;
   static constexpr int SCALES = kStageTokens * Kv4Row<D>::SCALES;
   static constexpr int HALF = CODES + SCALES;
   static constexpr int STAGE = 2 * HALF;
-  static constexpr int BAR_OFF = kWarps * STAGES * STAGE;
+  static constexpr int RING = STAGES * STAGE;  // of a warp; at the end its outputs [NT * 8][ROW]
+  static constexpr int ROW = D + 4;            // floats, so that the lanes of a store spread over the banks
+  static constexpr int BAR_OFF = kWarps * RING;
   static constexpr int NAN_OFF = BAR_OFF + kWarps * STAGES * 8;
-  static constexpr int TAB_OFF = NAN_OFF + kWarps * (D / kKv4Group) * 4;
-  static constexpr int bytes(int entries) { return TAB_OFF + kWarps * entries * 4; }
+  static constexpr int SUM_OFF = NAN_OFF + D / kKv4Group * 4;  // m, then l: [kWarps][NT * 8]
+  static constexpr int TAB_OFF = SUM_OFF + 2 * kWarps * NT * 8 * 4;
+  static_assert(NT * 8 * ROW * 4 <= RING, "a warp's outputs take its ring's place");
+  static constexpr int bytes(int entries) { return TAB_OFF + entries * 4; }
 };
 
 template <int D, int NT, int STAGES, typename T>
 __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4DecodeParams p) {
-  using L = Kv4DecodeSmem<D, STAGES>;
+  using L = Kv4DecodeSmem<D, NT, STAGES>;
   using R = Kv4Row<D>;
   constexpr int KSTEPS = D / 16;
   constexpr int NW = D / 32;  // words of K codes a lane reads per token; of V codes: D / 64
@@ -73,32 +77,36 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
   extern __shared__ __align__(128) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c4 = lane & 3;
-  uint8_t* ring = smem + warp * STAGES * L::STAGE;
+  uint8_t* ring = smem + warp * L::RING;
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF) + warp * STAGES;
-  uint32_t* nan = reinterpret_cast<uint32_t*>(smem + L::NAN_OFF) + warp * (D / kKv4Group);
-  int32_t* tab = reinterpret_cast<int32_t*>(smem + L::TAB_OFF) + warp * p.tab_entries;
+  uint32_t* nan = reinterpret_cast<uint32_t*>(smem + L::NAN_OFF);
+  float* sums = reinterpret_cast<float*>(smem + L::SUM_OFF);
+  int32_t* tab = reinterpret_cast<int32_t*>(smem + L::TAB_OFF);
   if (lane == 0) {
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&bars[s]), 1);
     fence_mbar_init();
   }
-  if (lane < D / kKv4Group) nan[lane] = 0;
-  __syncwarp();
+  if (threadIdx.x < D / kKv4Group) nan[threadIdx.x] = 0;
   griddep_launch_dependents();
 
   const int r = blockIdx.y;
-  const int u = blockIdx.x * kWarps + warp;
-  const int h = u % p.kv_heads, c = u / p.kv_heads;
+  const int h = blockIdx.x % p.kv_heads, c = blockIdx.x / p.kv_heads;
   const int col0 = blockIdx.z * NT * 8;
   const int cap = p.maxblk * p.block_size;
   int ctx = __ldg(p.lens + r);
   const bool bad_len = ctx < 0 || ctx > cap;
   ctx = min(max(ctx, 0), cap);
   const int nsplit = (ctx + p.split_tokens - 1) / p.split_tokens;
-  const bool active = c < max(nsplit, 1);
   const int G = p.group, NC = G * p.q_len, qh0 = h * G;
+  if (c >= max(nsplit, 1)) {
+    griddep_wait();
+    if (bad_len && threadIdx.x == 0) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
+    return;
+  }
   const int tok0 = c * p.split_tokens, tok1 = min(tok0 + p.split_tokens, ctx);
-  const int nstages = active && tok1 > tok0 ? (tok1 - tok0 + kStageTokens - 1) / kStageTokens : 0;
+  const int nstages = (tok1 - tok0 + kStageTokens - 1) / kStageTokens;  // of the CTA: warp w takes w, w + kWarps, ...
+  const int mine = nstages > warp ? (nstages - warp + kWarps - 1) / kWarps : 0;
   const int blk0 = tok0 / p.block_size;
 
   // row of column n in q, out and the partials
@@ -113,7 +121,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
   if (nstages > 0) {
     const int nblk = (tok1 - 1) / p.block_size - blk0 + 1;
     const int32_t* trow = p.tables + (size_t)r * p.maxblk + blk0;
-    for (int i = lane; i < nblk; i += 32) {
+    for (int i = threadIdx.x; i < nblk; i += kWarps * 32) {
       int b = __ldg(trow + i);
       if (b < 0 || b >= p.num_blocks) {
         bad_id = true;
@@ -155,16 +163,15 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
     }
   }
   griddep_wait();
-  if (bad_len && lane == 0) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
+  if (bad_len && threadIdx.x == 0) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
   if (bad_id) record_error(p.err, PA_DEVERR_BLOCK_ID);
-  if (!active) return;
   T* out = static_cast<T*>(p.out);
+  const int ncols = min(NC - col0, NT * 8);  // of this CTA
   if (ctx == 0) {
-    const int ncw = max(0, min(NC - col0, NT * 8));
-    for (int i = lane; i < ncw * D; i += 32) out[row_of(col0 + i / D) * D + i % D] = Elem<T>::from(0.f);
+    for (int i = threadIdx.x; i < ncols * D; i += kWarps * 32) out[row_of(col0 + i / D) * D + i % D] = Elem<T>::from(0.f);
     return;
   }
-  __syncwarp();
+  __syncthreads();  // the table
 
   const int bs = p.block_size;
   const int bsh = p.block_shift;
@@ -172,20 +179,20 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
   const uint64_t pol = policy_evict_first();
   // stage j: tokens [ts, ts + 32); lane 4i + {0, 1, 2, 3} brings page i's codes and scales of K, of V (pages that
   // hold tokens of the partition)
-  auto issue = [&](int j) {
+  auto issue = [&](int j) {  // the warp's j-th stage
     const int s = j % STAGES;
-    const int ts = tok0 + kStageTokens * j;
+    const int ts = tok0 + kStageTokens * (j * kWarps + warp);
     const int npages = (min(kStageTokens, tok1 - ts) + bs - 1) >> bsh;
     const uint32_t bar = smem_u32(&bars[s]);
     const int i = lane >> 2;
-    const bool mine = i < npages, isv = lane & 2, part = lane & 1;
-    const int b = mine ? tab[((ts - tok0) >> bsh) + i] : -1;
+    const bool has = i < npages, isv = lane & 2, part = lane & 1;
+    const int b = has ? tab[((ts - tok0) >> bsh) + i] : -1;
     const int copies = __popc(__ballot_sync(kAll, b >= 0)) >> 1;  // pages, of K and of V
     fence_proxy_async_smem();  // this stage's earlier reads and writes before the copies
     __syncwarp();
     if (lane == 0) mbar_arrive_expect_tx(bar, copies * page);
     __syncwarp();
-    if (mine) {
+    if (has) {
       const int bytes = bs * (part ? R::SCALES : R::CODES);
       uint8_t* dst = ring + s * L::STAGE + (isv ? L::HALF : 0) + (part ? L::CODES : 0) + i * bytes;
       if (b >= 0) {
@@ -214,19 +221,19 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
   }
   const int causal0 = ctx - (p.q_len - 1);  // tokens from here on are hidden from some query (q_len 1: from ctx on)
 
-  for (int j = 0; j < min(nstages, STAGES); ++j) issue(j);
+  for (int j = 0; j < min(mine, STAGES); ++j) issue(j);
   const int pg = g ^ ((g >> 1) & 1);        // token row of this lane's K fragments
   const int t01[2] = {2 * c4 ^ (c4 & 1), (2 * c4 + 1) ^ (c4 & 1)};  // pi(2c), pi(2c + 1)
 
   bool failed = false;
   int j = 0;
-  for (; j < nstages; ++j) {
+  for (; j < mine; ++j) {
     const int s = j % STAGES;
     if (!mbar_wait(smem_u32(&bars[s]), (j / STAGES) & 1)) {
       failed = true;
       break;
     }
-    const int ts = tok0 + kStageTokens * j;
+    const int ts = tok0 + kStageTokens * (j * kWarps + warp);
     uint8_t* kst = ring + s * L::STAGE;
     uint8_t* vst = kst + L::HALF;
     // where token t of the stage has its codes and scales
@@ -389,16 +396,16 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
       for (int q = 0; q < tiles; ++q) tile(16 * q, std::false_type{});
     }
     __syncwarp();
-    if (j + STAGES < nstages) issue(j + STAGES);
+    if (j + STAGES < mine) issue(j + STAGES);
   }
 
   if (failed) {
     if (lane == 0) record_error(p.err, PA_DEVERR_TIMEOUT);
-    for (int k = j + 1; k < nstages && k < j + STAGES; ++k)  // copies in flight land before the warp leaves
+    for (int k = j + 1; k < mine && k < j + STAGES; ++k)  // copies in flight land before the warp goes on
       mbar_wait(smem_u32(&bars[k % STAGES]), (k / STAGES) & 1);
-    return;
   }
 
+  // the warps' parts of each column: brought to the largest reference, added up in order
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -407,41 +414,61 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
       x += __shfl_xor_sync(kAll, x, 4);
       x += __shfl_xor_sync(kAll, x, 8);
       x += __shfl_xor_sync(kAll, x, 16);
-      l[nt][e] = x;
-      const int n = col0 + nt * 8 + 2 * c4 + e;
-      if (n >= NC) continue;
-      // the lane's D/8 elements of column n: D/8 g + 2 mt + {0, 1}
-      const uint32_t seen = nan[D == 128 ? g : g >> 1];
-      const int nsee = min(max(lim[nt][e] - causal0, 0), 31);
-      const float add = seen & ((1u << nsee) - 1u) ? NAN : 0.f;
-      const size_t row = row_of(n);
-      if (nsplit == 1) {
-        const float inv = x == 0.f ? 0.f : 1.f / x;  // a NaN sum stays one
-        uint32_t o[KSTEPS];
-#pragma unroll
-        for (int mt = 0; mt < KSTEPS; ++mt)
-          o[mt] = Elem<T>::pack(acc[nt][mt][e] * inv + add, acc[nt][mt][2 + e] * inv + add);
-        uint4* dst = reinterpret_cast<uint4*>(out + row * D + (D / 8) * g);
-#pragma unroll
-        for (int i = 0; i < KSTEPS / 4; ++i) dst[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
-      } else {
-        float4* dst = reinterpret_cast<float4*>(p.part_o + (row * p.max_splits + c) * D + (D / 8) * g);
-#pragma unroll
-        for (int i = 0; i < KSTEPS / 2; ++i)
-          dst[i] = make_float4(acc[nt][2 * i][e] + add, acc[nt][2 * i][2 + e] + add, acc[nt][2 * i + 1][e] + add,
-                               acc[nt][2 * i + 1][2 + e] + add);
-        if (g == 0) {
-          p.part_m[row * p.max_splits + c] = m[nt][e];
-          p.part_l[row * p.max_splits + c] = x;
-        }
+      if (g == 0) {
+        const int n = nt * 8 + 2 * c4 + e;
+        sums[warp * NT * 8 + n] = m[nt][e];
+        sums[(kWarps + warp) * NT * 8 + n] = x;
       }
     }
+  float* po = reinterpret_cast<float*>(ring);  // every copy into the ring has landed and been read
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      // the lane's D/8 elements of column n: D/8 g + 2 mt + {0, 1}
+      float4* dst = reinterpret_cast<float4*>(po + (nt * 8 + 2 * c4 + e) * L::ROW + (D / 8) * g);
+#pragma unroll
+      for (int i = 0; i < KSTEPS / 2; ++i)
+        dst[i] = make_float4(acc[nt][2 * i][e], acc[nt][2 * i][2 + e], acc[nt][2 * i + 1][e], acc[nt][2 * i + 1][2 + e]);
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < ncols * (D / 4); i += kWarps * 32) {
+    const int n = i / (D / 4), d = 4 * (i % (D / 4));
+    float f[kWarps], M = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, f[w] = sums[w * NT * 8 + n]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    const float ref = M == -INFINITY ? 0.f : M;  // no finite score: sums are zero or not numbers
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const float a = ex2_approx(f[w] - ref);
+      const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * L::RING) + n * L::ROW + d);
+      o.x += a * x.x, o.y += a * x.y, o.z += a * x.z, o.w += a * x.w;
+      sum += a * sums[(kWarps + w) * NT * 8 + n];
+    }
+    // a token behind causal0 that is not a number, for the columns that see it
+    const int nsee = min(max(min(tok1, ctx - (p.q_len - 1 - (col0 + n) / G)) - causal0, 0), 31);
+    if (nan[d / kKv4Group] & ((1u << nsee) - 1u)) o = make_float4(NAN, NAN, NAN, NAN);
+    const size_t row = row_of(col0 + n);
+    if (nsplit == 1) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a NaN sum stays one
+      *reinterpret_cast<uint2*>(out + row * D + d) =
+          make_uint2(Elem<T>::pack(o.x * inv, o.y * inv), Elem<T>::pack(o.z * inv, o.w * inv));
+    } else {
+      *reinterpret_cast<float4*>(p.part_o + (row * p.max_splits + c) * D + d) = o;
+      if (d == 0) {
+        p.part_m[row * p.max_splits + c] = M;
+        p.part_l[row * p.max_splits + c] = sum;
+      }
+    }
+  }
 }
 
 template <int D, int NT, typename T>
 cudaError_t launch_t(const Kv4DecodeParams& p, cudaStream_t stream) {
   constexpr int STAGES = 3;
-  using L = Kv4DecodeSmem<D, STAGES>;
+  using L = Kv4DecodeSmem<D, NT, STAGES>;
   auto kern = kv4_decode_kernel<D, NT, STAGES, T>;
   static bool attr_set[64] = {};
   int dev = 0;
@@ -451,8 +478,7 @@ cudaError_t launch_t(const Kv4DecodeParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
-  const int64_t units = (int64_t)p.max_splits * p.kv_heads;
-  const dim3 grid((unsigned)((units + kWarps - 1) / kWarps), p.num_seqs, (p.group * p.q_len + NT * 8 - 1) / (NT * 8));
+  const dim3 grid((unsigned)(p.max_splits * p.kv_heads), p.num_seqs, (p.group * p.q_len + NT * 8 - 1) / (NT * 8));
   return launch_pdl(kern, grid, dim3(kWarps * 32), L::bytes(p.tab_entries), stream, p);
 }
 

@@ -44,15 +44,15 @@ int kv4_decode_setup(int num_seqs, int q_len, int q_heads, int kv_heads, int hea
   if (group > 16 || group * q_len > 32) return PA_ERR_INVALID;
   const int64_t cap = (int64_t)max_blocks_per_seq * block_size;
   if (cap > INT32_MAX - 4096 || (int64_t)num_seqs * q_len * q_heads > INT32_MAX - 8) return PA_ERR_INVALID;
-  const int most = 256 * block_size;
+  const int most = 1024 * block_size;
   int64_t split = split_tokens;
   if (split_tokens == 0) {
     const int64_t sms = num_sms() > 0 ? num_sms() : 152;
     const int64_t lists = (int64_t)num_seqs * kv_heads * ((group * q_len + 15) / 16);
-    const int64_t parts = lists > 0 ? (24 * sms + lists - 1) / lists : 1;
+    const int64_t parts = lists > 0 ? (8 * sms + lists - 1) / lists : 1;
     split = (cap + parts - 1) / parts;
     if (split < 128) split = 128;
-    if (split > 1024) split = 1024;
+    if (split > 4096) split = 4096;
     split = (split + kKv4SplitUnit - 1) / kKv4SplitUnit * kKv4SplitUnit;
     if (split > most) split = most;
   }
