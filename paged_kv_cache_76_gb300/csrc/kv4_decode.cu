@@ -2,10 +2,16 @@
 // query per request or a few causal ones, for sm_103a.
 //
 // A CTA of four warps owns one (request r, KV head h, partition c) unit: warp w
-// takes the stages of 32 tokens w, w + 4, ..., every query head of the group on
+// takes the tiles of 16 tokens w, w + 4, ..., every query head of the group on
 // one read of K and V; the warps' parts are joined in shared memory and the
-// partitions by the log-sum-exp merge.  The codes and the scales of a page are
-// contiguous, so each comes by a bulk copy into the warp's own ring.
+// partitions by the log-sum-exp merge.
+//
+// At 4.5 bits an element the instructions that turn a tile into MMA operands
+// take as long as its bytes, so the kernel is built for few of them.  Every lane
+// loads just what its fragments hold, straight into registers, one tile ahead:
+// 12 loads, no shared memory in between.  (Bulk copies into a ring took 378
+// instructions a tile where this takes XXX: the copies of a divergent warp are
+// issued one by one, 15 instructions each.)
 //
 // A cache element is exact in fp16, so the products are fp16 MMAs whatever the
 // type of q: a query row is brought to [2^13, 2^14) by a power of two (taken
@@ -16,14 +22,14 @@
 // sum of the unrounded weights.
 //
 // Per 16 tokens (m16n8k16, S^T = K Q^T and O^T += V^T P^T):
-//   K: lane (g, c) = (lane / 4, lane % 4) reads D/4 consecutive elements of
-//      tokens pi(g), pi(g) + 8, D/16 A fragments of both; which elements a
-//      fragment takes is free as long as Q's B fragments take the same.
-//   V: lane (g, c) reads D/8 elements of the four tokens that P's B fragments
-//      hold for it.  An A fragment wants two tokens side by side, so the codes
-//      of two tokens are interleaved before they are converted (four logical
-//      instructions for 16 elements, where 16 fp16 pairs would take 16).
-//   pi(i) = i ^ (i/2 & 1) puts neighbouring lanes' rows into different banks.
+//   K: lane (g, c) = (lane / 4, lane % 4) holds D/4 consecutive elements of
+//      tokens g and g + 8, D/16 A fragments of both; which elements a fragment
+//      takes is free as long as Q's B fragments take the same.
+//   V: lane (g, c) holds D/8 elements of the four tokens that P's B fragments
+//      hold for it, 2c, 2c + 1 and those + 8.  An A fragment wants two tokens
+//      side by side, so the codes of two tokens are interleaved before they are
+//      converted (four logical instructions for 16 elements, where 16 fp16 pairs
+//      would take 16).
 // Elements cost one conversion and one multiplication a pair (42 pairs per
 // clock and SM measured for the two together).
 //
@@ -44,56 +50,48 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kStageTokens = 32;
+constexpr int kTile = 16;
+constexpr int kDepth = 4;  // tiles of a warp's ring
 constexpr int kMaxEntries = 1024;  // Block Table entries of a partition
-constexpr float kRescale = 8.f;   // a reference is raised when a score passes it by more (log2 units)
-constexpr float kShift = 7.f;     // weights are 2^(s - m + kShift) <= 2^15
+constexpr float kRescale = 8.f;    // a reference is raised when a score passes it by more (log2 units)
+constexpr float kShift = 7.f;      // weights are 2^(s - m + kShift) <= 2^15
 constexpr unsigned kAll = 0xffffffffu;
 
-template <int D, int NT, int STAGES>
+template <int D, int NT>
 struct Kv4DecodeSmem {
-  // of a stage: codes of K, its scales, codes of V, its scales
-  static constexpr int CODES = kStageTokens * Kv4Row<D>::CODES;
-  static constexpr int SCALES = kStageTokens * Kv4Row<D>::SCALES;
-  static constexpr int HALF = CODES + SCALES;
-  static constexpr int STAGE = 2 * HALF;
-  static constexpr int RING = STAGES * STAGE;  // of a warp; at the end its outputs [NT * 8][ROW]
-  static constexpr int ROW = D + 4;            // floats, so that the lanes of a store spread over the banks
-  static constexpr int BAR_OFF = kWarps * RING;
-  static constexpr int NAN_OFF = BAR_OFF + kWarps * STAGES * 8;
-  static constexpr int SUM_OFF = NAN_OFF + D / kKv4Group * 4;  // m, then l: [kWarps][NT * 8]
-  static constexpr int TAB_OFF = SUM_OFF + 2 * kWarps * NT * 8 * 4;
-  static_assert(NT * 8 * ROW * 4 <= RING, "a warp's outputs take its ring's place");
+  static constexpr int TILE = 2 * kTile * Kv4Row<D>::BYTES;  // K, then V
+  static constexpr int RING = kDepth * TILE;                 // of a warp; at the end its outputs
+  static constexpr int ROW = D + 4;  // floats of a column's outputs, so that the lanes of a store spread over the banks
+  static constexpr int WARP = RING > NT * 8 * ROW * 4 ? RING : NT * 8 * ROW * 4;
+  static constexpr int SUM_OFF = kWarps * WARP;             // m, then l: [kWarps][NT * 8]
+  static constexpr int NAN_OFF = SUM_OFF + 2 * kWarps * NT * 8 * 4;
+  static constexpr int BAD_OFF = NAN_OFF + D / kKv4Group * 4;  // bits: bad block ids of the table
+  static constexpr int TAB_OFF = BAD_OFF + (kMaxEntries + 32) / 8;
   static constexpr int bytes(int entries) { return TAB_OFF + entries * 4; }
 };
 
-template <int D, int NT, int STAGES, typename T>
-__global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4DecodeParams p) {
-  using L = Kv4DecodeSmem<D, NT, STAGES>;
+template <int D, int NT, int BS>
+__global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_decode_kernel(const Kv4DecodeParams p) {
+  using L = Kv4DecodeSmem<D, NT>;
   using R = Kv4Row<D>;
   constexpr int KSTEPS = D / 16;
-  constexpr int NW = D / 32;  // words of K codes a lane reads per token; of V codes: D / 64
+  constexpr int NW = D / 32;  // words of K codes a lane has per token; of V codes: D / 64
+  constexpr int PAGE = BS * R::BYTES;
 
-  extern __shared__ __align__(128) uint8_t smem[];
+  extern __shared__ __align__(16) uint8_t smem[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c4 = lane & 3;
-  uint8_t* ring = smem + warp * L::RING;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF) + warp * STAGES;
-  uint32_t* nan = reinterpret_cast<uint32_t*>(smem + L::NAN_OFF);
   float* sums = reinterpret_cast<float*>(smem + L::SUM_OFF);
+  uint32_t* nan = reinterpret_cast<uint32_t*>(smem + L::NAN_OFF);
+  uint32_t* badbits = reinterpret_cast<uint32_t*>(smem + L::BAD_OFF);
   int32_t* tab = reinterpret_cast<int32_t*>(smem + L::TAB_OFF);
-  if (lane == 0) {
-#pragma unroll
-    for (int s = 0; s < STAGES; ++s) mbar_init(smem_u32(&bars[s]), 1);
-    fence_mbar_init();
-  }
   if (threadIdx.x < D / kKv4Group) nan[threadIdx.x] = 0;
   griddep_launch_dependents();
 
   const int r = blockIdx.y;
   const int h = blockIdx.x % p.kv_heads, c = blockIdx.x / p.kv_heads;
   const int col0 = blockIdx.z * NT * 8;
-  const int cap = p.maxblk * p.block_size;
+  const int cap = p.maxblk * BS;
   int ctx = __ldg(p.lens + r);
   const bool bad_len = ctx < 0 || ctx > cap;
   ctx = min(max(ctx, 0), cap);
@@ -105,9 +103,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
     return;
   }
   const int tok0 = c * p.split_tokens, tok1 = min(tok0 + p.split_tokens, ctx);
-  const int nstages = (tok1 - tok0 + kStageTokens - 1) / kStageTokens;  // of the CTA: warp w takes w, w + kWarps, ...
-  const int mine = nstages > warp ? (nstages - warp + kWarps - 1) / kWarps : 0;
-  const int blk0 = tok0 / p.block_size;
+  const int ntiles = (tok1 - tok0 + kTile - 1) / kTile;  // of the CTA
 
   // row of column n in q, out and the partials
   auto row_of = [&](int n) {
@@ -118,92 +114,114 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
   bool bad_id = false;
   uint32_t qf[NT][KSTEPS][2];
   float sl2[NT][2];  // softmax scale (log2 units) of the lane's two columns of each n-tile
-  if (nstages > 0) {
-    const int nblk = (tok1 - 1) / p.block_size - blk0 + 1;
-    const int32_t* trow = p.tables + (size_t)r * p.maxblk + blk0;
-    for (int i = threadIdx.x; i < nblk; i += kWarps * 32) {
-      int b = __ldg(trow + i);
-      if (b < 0 || b >= p.num_blocks) {
-        bad_id = true;
-        b = -1;
-      }
-      tab[i] = b;
+  {
+    const int nblk = (tok1 - tok0 + BS - 1) / BS;
+    const int entries = (ntiles * kTile + BS - 1) / BS;
+    const int32_t* trow = p.tables + (size_t)r * p.maxblk + tok0 / BS;
+    // a bad block, and one behind the last, is read as block 0 and counts as zeros
+    for (int i = threadIdx.x; i < (entries + 31 & ~31); i += kWarps * 32) {
+      int b = i < nblk ? __ldg(trow + i) : 0;
+      const bool bad = b < 0 || b >= p.num_blocks;
+      const uint32_t bits = __ballot_sync(kAll, bad);
+      if (lane == 0) badbits[i >> 5] = bits;
+      if (i < entries) tab[i] = bad ? 0 : b;
+      bad_id |= bad;
     }
     // Q^T as the B operand: lane (g, c) holds column g of each n-tile, elements
     // D/4 c + 4 ks + {0, 1} and {2, 3}
+    auto load_q = [&](auto type) {
+      using T = decltype(type);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int n = col0 + nt * 8 + g;
-      const uint2* src = reinterpret_cast<const uint2*>(static_cast<const T*>(p.q) + (n < NC ? row_of(n) : 0) * D + (D / 4) * c4);
-      float x[KSTEPS][4];
-      float top = 0.f;
+      for (int nt = 0; nt < NT; ++nt) {
+        const int n = col0 + nt * 8 + g;
+        const uint2* src = reinterpret_cast<const uint2*>(static_cast<const T*>(p.q) + (n < NC ? row_of(n) : 0) * D + (D / 4) * c4);
+        float x[KSTEPS][4];
+        float top = 0.f;
 #pragma unroll
-      for (int ks = 0; ks < KSTEPS; ++ks) {
-        const uint2 w = n < NC ? __ldg(src + ks) : make_uint2(0u, 0u);
-        x[ks][0] = Elem<T>::lo(w.x), x[ks][1] = Elem<T>::hi(w.x);
-        x[ks][2] = Elem<T>::lo(w.y), x[ks][3] = Elem<T>::hi(w.y);
+        for (int ks = 0; ks < KSTEPS; ++ks) {
+          const uint2 w = n < NC ? __ldg(src + ks) : make_uint2(0u, 0u);
+          x[ks][0] = Elem<T>::lo(w.x), x[ks][1] = Elem<T>::hi(w.x);
+          x[ks][2] = Elem<T>::lo(w.y), x[ks][3] = Elem<T>::hi(w.y);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(x[ks][e]));
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(x[ks][e]));
+        }
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+        // 2^e <= top < 2^(e + 1); rows of zeros and of values that are not finite stay as they are
+        int e = top > 0.f && top < INFINITY ? ilogbf(top) - 13 : 0;
+        e = max(e, -126);
+        const float down = ldexpf(1.f, -e);
+#pragma unroll
+        for (int ks = 0; ks < KSTEPS; ++ks) {
+          qf[nt][ks][0] = Elem<__half>::pack(x[ks][0] * down, x[ks][1] * down);
+          qf[nt][ks][1] = Elem<__half>::pack(x[ks][2] * down, x[ks][3] * down);
+        }
+        const float back = p.scale_log2 * ldexpf(1.f, e);
+        // accumulators hold columns 2c, 2c + 1 of the tile
+        sl2[nt][0] = __shfl_sync(kAll, back, 8 * c4);
+        sl2[nt][1] = __shfl_sync(kAll, back, 8 * c4 + 4);
       }
-      top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-      // 2^e <= top < 2^(e + 1); rows of zeros and of values that are not finite stay as they are
-      int e = top > 0.f && top < INFINITY ? ilogbf(top) - 13 : 0;
-      e = max(e, -126);
-      const float down = ldexpf(1.f, -e);
-#pragma unroll
-      for (int ks = 0; ks < KSTEPS; ++ks) {
-        qf[nt][ks][0] = Elem<__half>::pack(x[ks][0] * down, x[ks][1] * down);
-        qf[nt][ks][1] = Elem<__half>::pack(x[ks][2] * down, x[ks][3] * down);
-      }
-      const float back = p.scale_log2 * ldexpf(1.f, e);
-      // accumulators hold columns 2c, 2c + 1 of the tile
-      sl2[nt][0] = __shfl_sync(kAll, back, 8 * c4);
-      sl2[nt][1] = __shfl_sync(kAll, back, 8 * c4 + 4);
+    };
+    if (ntiles > 0) {
+      if (p.bf16) load_q(__nv_bfloat16{});
+      else load_q(__half{});
     }
   }
   griddep_wait();
   if (bad_len && threadIdx.x == 0) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
   if (bad_id) record_error(p.err, PA_DEVERR_BLOCK_ID);
-  T* out = static_cast<T*>(p.out);
   const int ncols = min(NC - col0, NT * 8);  // of this CTA
   if (ctx == 0) {
-    for (int i = threadIdx.x; i < ncols * D; i += kWarps * 32) out[row_of(col0 + i / D) * D + i % D] = Elem<T>::from(0.f);
+    uint16_t* out = static_cast<uint16_t*>(p.out);  // 0 in either type
+    for (int i = threadIdx.x; i < ncols * D; i += kWarps * 32) out[row_of(col0 + i / D) * D + i % D] = 0;
     return;
   }
-  __syncthreads();  // the table
+  const bool any_bad = __syncthreads_or(bad_id);  // and the table is complete
 
-  const int bs = p.block_size;
-  const int bsh = p.block_shift;
-  const int page = bs * R::BYTES;
-  const uint64_t pol = policy_evict_first();
-  // stage j: tokens [ts, ts + 32); lane 4i + {0, 1, 2, 3} brings page i's codes and scales of K, of V (pages that
-  // hold tokens of the partition)
-  auto issue = [&](int j) {  // the warp's j-th stage
-    const int s = j % STAGES;
-    const int ts = tok0 + kStageTokens * (j * kWarps + warp);
-    const int npages = (min(kStageTokens, tok1 - ts) + bs - 1) >> bsh;
-    const uint32_t bar = smem_u32(&bars[s]);
-    const int i = lane >> 2;
-    const bool has = i < npages, isv = lane & 2, part = lane & 1;
-    const int b = has ? tab[((ts - tok0) >> bsh) + i] : -1;
-    const int copies = __popc(__ballot_sync(kAll, b >= 0)) >> 1;  // pages, of K and of V
-    fence_proxy_async_smem();  // this stage's earlier reads and writes before the copies
-    __syncwarp();
-    if (lane == 0) mbar_arrive_expect_tx(bar, copies * page);
-    __syncwarp();
-    if (has) {
-      const int bytes = bs * (part ? R::SCALES : R::CODES);
-      uint8_t* dst = ring + s * L::STAGE + (isv ? L::HALF : 0) + (part ? L::CODES : 0) + i * bytes;
-      if (b >= 0) {
-        const uint8_t* src = static_cast<const uint8_t*>(isv ? p.v_cache : p.k_cache) +
-                             ((size_t)b * p.kv_heads + h) * page + (part ? bs * R::CODES : 0);
-        bulk_load_hint(smem_u32(dst), src, bytes, bar, pol);
-      } else {  // a bad block id: zeros
-        for (int k = 0; k < bytes; k += 16) *reinterpret_cast<uint4*>(dst + k) = make_uint4(0, 0, 0, 0);
+  // A tile is 2 * R::BYTES vectors of 16 bytes, K's and then V's, copied as they
+  // are in the pages (of blocks of 32: the tile's half of the codes, then of the
+  // scales); this lane copies vectors lane, lane + 32, ...
+  constexpr int VECS = R::BYTES, SLOTS = (2 * VECS + 31) / 32;
+  constexpr int PV = BS < kTile ? PAGE / 16 : VECS;  // vectors of a page in a tile
+  uint8_t* ring = smem + warp * L::WARP;
+  const uint32_t ring0 = smem_u32(ring) + 16 * lane;
+  const uint32_t block_bytes = (uint32_t)p.kv_heads * PAGE;
+  const uint8_t* src[SLOTS];
+#pragma unroll
+  for (int q = 0; q < SLOTS; ++q) {
+    const int id = lane + 32 * q, i = id % VECS;
+    const int codes = kTile * R::CODES / 16;  // vectors of them, blocks of 32
+    const int at = BS <= kTile || i < codes ? (i % PV) * 16 : BS * R::CODES + (i - codes) * 16;
+    src[q] = static_cast<const uint8_t*>(id < VECS ? p.k_cache : p.v_cache) + (int64_t)h * PAGE + at;
+  }
+  // entry of the table that holds a token of tile j
+  auto entry = [](int j, int token) { return BS >= kTile ? j * kTile / BS : j * (kTile / BS) + token / BS; };
+  auto issue = [&](int i) {  // the warp's i-th tile
+    const int j = warp + i * kWarps;
+    if (j < ntiles) {
+      const uint32_t dst = ring0 + (uint32_t)(i % kDepth) * L::TILE;
+#pragma unroll
+      for (int q = 0; q < SLOTS; ++q) {
+        const int id = lane + 32 * q, v = id % VECS;
+        const uint8_t* s = src[q] + (uint64_t)(uint32_t)tab[entry(j, v / PV * BS)] * block_bytes;
+        if (BS > kTile) s += (j * kTile & (BS - 1)) * (v < kTile * R::CODES / 16 ? R::CODES : R::SCALES);
+        if (32 * q + 32 <= 2 * VECS || id < 2 * VECS) cp_async16(dst + 512 * q, s, 16);
       }
     }
+    cp_async_commit();
   };
+  // Where this lane's elements are in a tile: K of token pi(g) (+ 8), V of pi(2c), pi(2c + 1) (+ 8)
+  auto code_at = [](int t) { return BS < kTile ? t / BS * PAGE + t % BS * R::CODES : t * R::CODES; };
+  auto scale_at = [](int t) {
+    return BS < kTile ? t / BS * PAGE + BS * R::CODES + t % BS * R::SCALES : kTile * R::CODES + t * R::SCALES;
+  };
+  constexpr int VOFF = kTile * R::BYTES;
+  const int pg = g ^ (g >> 1 & 1);
+  const int t01[2] = {2 * c4 ^ (c4 & 1), (2 * c4 + 1) ^ (c4 & 1)};
+  const int kcode = code_at(pg) + c4 * (4 * NW), kscale = scale_at(pg) + c4 * (NW / 2);
+  const int vcode[2] = {VOFF + code_at(t01[0]) + g * (D / 16), VOFF + code_at(t01[1]) + g * (D / 16)};
+  const int vscale[2] = {VOFF + scale_at(t01[0]) + (D == 128 ? g : g >> 1), VOFF + scale_at(t01[1]) + (D == 128 ? g : g >> 1)};
+  constexpr int CODE8 = BS < kTile ? 8 / BS * PAGE : 8 * R::CODES, SCALE8 = BS < kTile ? 8 / BS * PAGE : 8 * R::SCALES;
 
   float m[NT][2], l[NT][2], acc[NT][KSTEPS][4];
   int lim[NT][2];  // tokens [0, lim) are visible to the lane's columns
@@ -221,189 +239,159 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
   }
   const int causal0 = ctx - (p.q_len - 1);  // tokens from here on are hidden from some query (q_len 1: from ctx on)
 
-  for (int j = 0; j < min(mine, STAGES); ++j) issue(j);
-  const int pg = g ^ ((g >> 1) & 1);        // token row of this lane's K fragments
-  const int t01[2] = {2 * c4 ^ (c4 & 1), (2 * c4 + 1) ^ (c4 & 1)};  // pi(2c), pi(2c + 1)
-
-  bool failed = false;
-  int j = 0;
-  for (; j < mine; ++j) {
-    const int s = j % STAGES;
-    if (!mbar_wait(smem_u32(&bars[s]), (j / STAGES) & 1)) {
-      failed = true;
-      break;
+  // 16 tokens from ts on; `all`: every column sees all of them
+  auto compute = [&](const uint8_t* x, const int j, const auto all_t) {
+    constexpr bool all = decltype(all_t)::value;
+    const int ts = tok0 + j * kTile;
+    auto bad_block = [&](int token) {
+      const int i = entry(j, token);
+      return badbits[i >> 5] >> (i & 31) & 1;
+    };
+    float sacc[NT][2][4];  // even and odd steps: a chain of half the length
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) sacc[nt][k][0] = sacc[nt][k][1] = sacc[nt][k][2] = sacc[nt][k][3] = 0.f;
+    uint32_t kw[2][NW], ks[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      if constexpr (NW == 4) {
+        const uint4 w = *reinterpret_cast<const uint4*>(x + kcode + e * CODE8);
+        kw[e][0] = w.x, kw[e][1] = w.y, kw[e][2] = w.z, kw[e][3] = w.w;
+        ks[e] = *reinterpret_cast<const uint16_t*>(x + kscale + e * SCALE8);
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(x + kcode + e * CODE8);
+        kw[e][0] = w.x, kw[e][1] = w.y;
+        ks[e] = x[kscale + e * SCALE8];
+      }
     }
-    const int ts = tok0 + kStageTokens * (j * kWarps + warp);
-    uint8_t* kst = ring + s * L::STAGE;
-    uint8_t* vst = kst + L::HALF;
-    // where token t of the stage has its codes and scales
-    auto code_at = [](int t) { return t * R::CODES; };
-    auto scale_at = [](int t) { return L::CODES + t * R::SCALES; };
-    __syncwarp();  // zeroed pages
-    if (ts + kStageTokens > tok1) {
-      const int t = lane;  // a token per lane
-      if (ts + t >= tok1) {
 #pragma unroll
-        for (int i = 0; i < R::SCALES; i += 4) *reinterpret_cast<uint32_t*>(vst + scale_at(t) + i) = 0u;
-      }
-      __syncwarp();
-    }
-    if (ts + kStageTokens > causal0 && p.q_len > 1) {
-      const int t = lane;
-      if (ts + t >= causal0 && ts + t < tok1) {
+    for (int i = 0; i < NW; ++i) {
+      uint32_t y[2][4];
 #pragma unroll
-        for (int i = 0; i < R::SCALES; ++i) {
-          uint8_t* at = vst + scale_at(t) + i;
-          if (*at >= kKv4FirstInf) {
-            *at = 0;
-            atomicOr(&nan[i], 1u << (ts + t - causal0));
-          }
-        }
+      for (int e = 0; e < 2; ++e) {
+        kv4_unpack(kw[e][i], y[e]);
+        uint32_t s2 = kv4_scale2(NW == 4 && i >= 2 ? ks[e] >> 8 : ks[e] & 0xFFu);
+        if (!all && bad_block(pg + 8 * e)) s2 = 0;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[e][k] = hmul2_u(y[e][k], s2);
       }
-      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const uint32_t a[4] = {y[0][2 * k], y[1][2 * k], y[0][2 * k + 1], y[1][2 * k + 1]};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_16816<__half>(sacc[nt][k], a, qf[nt][2 * i + k][0], qf[nt][2 * i + k][1]);
+      }
     }
 
-    // 16 tokens from tb on; `all`: every column sees all of them
-    auto tile = [&](const int tb, const auto all_t) {
-      constexpr bool all = decltype(all_t)::value;
-      const int t0 = ts + tb + pg;  // this lane's score rows: tokens t0, t0 + 8
-      float sacc[NT][4];
+    const int t0 = ts + pg;  // the lane's score rows: tokens t0, t0 + 8
+    uint32_t pb0[NT], pb1[NT];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) sacc[nt][0] = sacc[nt][1] = sacc[nt][2] = sacc[nt][3] = 0.f;
-      {
-        uint32_t w[2][NW], sc[2];
+    for (int nt = 0; nt < NT; ++nt) {
+      const float s0 = all || t0 < lim[nt][0] ? (sacc[nt][0][0] + sacc[nt][1][0]) * sl2[nt][0] : -INFINITY;
+      const float s1 = all || t0 < lim[nt][1] ? (sacc[nt][0][1] + sacc[nt][1][1]) * sl2[nt][1] : -INFINITY;
+      const float s2 = all || t0 + 8 < lim[nt][0] ? (sacc[nt][0][2] + sacc[nt][1][2]) * sl2[nt][0] : -INFINITY;
+      const float s3 = all || t0 + 8 < lim[nt][1] ? (sacc[nt][0][3] + sacc[nt][1][3]) * sl2[nt][1] : -INFINITY;
+      // m is raised to the column's maximum only when a score passes it by
+      // more than kRescale, so most tiles need no maximum across lanes: a
+      // vote says that no lane has such a score
+      const bool up = fmaxf(s0, s2) > m[nt][0] + kRescale || fmaxf(s1, s3) > m[nt][1] + kRescale;
+      if (__any_sync(kAll, up)) {
+        float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const uint8_t* src = kst + code_at(tb + pg + 8 * e) + c4 * (4 * NW);
-          if constexpr (NW == 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(src);
-            w[e][0] = v.x, w[e][1] = v.y, w[e][2] = v.z, w[e][3] = v.w;
-            sc[e] = *reinterpret_cast<const uint16_t*>(kst + scale_at(tb + pg + 8 * e) + 2 * c4);
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(src);
-            w[e][0] = v.x, w[e][1] = v.y;
-            sc[e] = kst[scale_at(tb + pg + 8 * e) + c4];
-          }
+        for (int o = 4; o < 32; o <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(kAll, mx0, o));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(kAll, mx1, o));
         }
-#pragma unroll
-        for (int i = 0; i < NW; ++i) {
-          uint32_t x[2][4];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            kv4_unpack(w[e][i], x[e]);
-            const uint32_t s2 = kv4_scale2(NW == 4 && i >= 2 ? sc[e] >> 8 : sc[e] & 0xFFu);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[e][k] = hmul2_u(x[e][k], s2);
-          }
-#pragma unroll
-          for (int k = 0; k < 2; ++k) {
-            const uint32_t a[4] = {x[0][2 * k], x[1][2 * k], x[0][2 * k + 1], x[1][2 * k + 1]};
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_16816<__half>(sacc[nt], a, qf[nt][2 * i + k][0], qf[nt][2 * i + k][1]);
-          }
-        }
-      }
-
-      uint32_t pb0[NT], pb1[NT];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const float s0 = all || t0 < lim[nt][0] ? sacc[nt][0] * sl2[nt][0] : -INFINITY;
-        const float s1 = all || t0 < lim[nt][1] ? sacc[nt][1] * sl2[nt][1] : -INFINITY;
-        const float s2 = all || t0 + 8 < lim[nt][0] ? sacc[nt][2] * sl2[nt][0] : -INFINITY;
-        const float s3 = all || t0 + 8 < lim[nt][1] ? sacc[nt][3] * sl2[nt][1] : -INFINITY;
-        // m is raised to the column's maximum only when a score passes it by
-        // more than kRescale, so most tiles need no maximum across lanes: a
-        // vote says that no lane has such a score
-        const bool up = fmaxf(s0, s2) > m[nt][0] + kRescale || fmaxf(s1, s3) > m[nt][1] + kRescale;
-        if (__any_sync(kAll, up)) {
-          float mx0 = fmaxf(s0, s2), mx1 = fmaxf(s1, s3);
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) {
-            mx0 = fmaxf(mx0, __shfl_xor_sync(kAll, mx0, o));
-            mx1 = fmaxf(mx1, __shfl_xor_sync(kAll, mx1, o));
-          }
-          const bool up0 = mx0 > m[nt][0] + kRescale, up1 = mx1 > m[nt][1] + kRescale;
-          const float al0 = up0 ? ex2_approx(m[nt][0] - mx0) : 1.f;
-          const float al1 = up1 ? ex2_approx(m[nt][1] - mx1) : 1.f;
-          m[nt][0] = up0 ? mx0 : m[nt][0];
-          m[nt][1] = up1 ? mx1 : m[nt][1];
-          l[nt][0] *= al0;
-          l[nt][1] *= al1;
-#pragma unroll
-          for (int mt = 0; mt < KSTEPS; ++mt) {
-            acc[nt][mt][0] *= al0;
-            acc[nt][mt][1] *= al1;
-            acc[nt][mt][2] *= al0;
-            acc[nt][mt][3] *= al1;
-          }
-        }
-        // a column that has seen no token keeps m = -inf; its exponents then use 0
-        const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kShift;
-        const float b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kShift;
-        const float p0 = ex2_approx(s0 - b0), p1 = ex2_approx(s1 - b1);
-        const float p2 = ex2_approx(s2 - b0), p3 = ex2_approx(s3 - b1);
-        l[nt][0] += p0 + p2;
-        l[nt][1] += p1 + p3;
-        pb0[nt] = movmatrix_trans(Elem<__half>::pack(p0, p1));
-        pb1[nt] = movmatrix_trans(Elem<__half>::pack(p2, p3));
-      }
-
-      {
-        // V of tokens pi(2c), pi(2c+1) (pair 0) and those + 8 (pair 1), elements D/8 g ..
-        uint32_t x[2][D / 16][2];  // [pair][element pair][element of it]: two tokens each
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          uint32_t a[D / 64], b[D / 64];
-          const uint8_t* sa = vst + code_at(tb + t01[0] + 8 * e) + g * (D / 16);
-          const uint8_t* sb = vst + code_at(tb + t01[1] + 8 * e) + g * (D / 16);
-          if constexpr (D == 128) {
-            const uint2 va = *reinterpret_cast<const uint2*>(sa), vb = *reinterpret_cast<const uint2*>(sb);
-            a[0] = va.x, a[1] = va.y, b[0] = vb.x, b[1] = vb.y;
-          } else {
-            a[0] = *reinterpret_cast<const uint32_t*>(sa);
-            b[0] = *reinterpret_cast<const uint32_t*>(sb);
-          }
-          const int grp = D == 128 ? g : g >> 1;
-          const uint32_t s2 = kv4_scale_pair(vst[scale_at(tb + t01[0] + 8 * e) + grp], vst[scale_at(tb + t01[1] + 8 * e) + grp]);
-#pragma unroll
-          for (int i = 0; i < D / 64; ++i) {
-            const uint32_t lo = (a[i] & 0x0F0F0F0Fu) | ((b[i] << 4) & 0xF0F0F0F0u);
-            const uint32_t hi = ((a[i] >> 4) & 0x0F0F0F0Fu) | (b[i] & 0xF0F0F0F0u);
-            uint32_t y[4], z[4];
-            kv4_unpack(lo, y);
-            kv4_unpack(hi, z);
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              x[e][4 * i + k][0] = hmul2_u(y[k], s2);
-              x[e][4 * i + k][1] = hmul2_u(z[k], s2);
-            }
-          }
-        }
+        const bool up0 = mx0 > m[nt][0] + kRescale, up1 = mx1 > m[nt][1] + kRescale;
+        const float al0 = up0 ? ex2_approx(m[nt][0] - mx0) : 1.f;
+        const float al1 = up1 ? ex2_approx(m[nt][1] - mx1) : 1.f;
+        m[nt][0] = up0 ? mx0 : m[nt][0];
+        m[nt][1] = up1 ? mx1 : m[nt][1];
+        l[nt][0] *= al0;
+        l[nt][1] *= al1;
 #pragma unroll
         for (int mt = 0; mt < KSTEPS; ++mt) {
-          const uint32_t a[4] = {x[0][mt][0], x[0][mt][1], x[1][mt][0], x[1][mt][1]};
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_16816<__half>(acc[nt][mt], a, pb0[nt], pb1[nt]);
+          acc[nt][mt][0] *= al0;
+          acc[nt][mt][1] *= al1;
+          acc[nt][mt][2] *= al0;
+          acc[nt][mt][3] *= al1;
         }
       }
-    };
-    if (ts + kStageTokens <= min(tok1, causal0)) {
-#pragma unroll
-      for (int q = 0; q < kStageTokens / 16; ++q) tile(16 * q, std::true_type{});
-    } else {
-      const int tiles = (min(kStageTokens, tok1 - ts) + 15) >> 4;
-#pragma unroll 1
-      for (int q = 0; q < tiles; ++q) tile(16 * q, std::false_type{});
+      // a column that has seen no token keeps m = -inf; its exponents then use 0
+      const float b0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] - kShift;
+      const float b1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] - kShift;
+      const float p0 = ex2_approx(s0 - b0), p1 = ex2_approx(s1 - b1);
+      const float p2 = ex2_approx(s2 - b0), p3 = ex2_approx(s3 - b1);
+      l[nt][0] += p0 + p2;
+      l[nt][1] += p1 + p3;
+      pb0[nt] = movmatrix_trans(Elem<__half>::pack(p0, p1));
+      pb1[nt] = movmatrix_trans(Elem<__half>::pack(p2, p3));
     }
-    __syncwarp();
-    if (j + STAGES < mine) issue(j + STAGES);
-  }
 
-  if (failed) {
-    if (lane == 0) record_error(p.err, PA_DEVERR_TIMEOUT);
-    for (int k = j + 1; k < mine && k < j + STAGES; ++k)  // copies in flight land before the warp goes on
-      mbar_wait(smem_u32(&bars[k % STAGES]), (k / STAGES) & 1);
+    uint32_t y[2][D / 16][2];  // [e][element pair][element of it]: two tokens each
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      uint32_t vs[2], va[2][D / 64];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        vs[i] = x[vscale[i] + e * SCALE8];
+        if constexpr (D == 128) {
+          const uint2 w = *reinterpret_cast<const uint2*>(x + vcode[i] + e * CODE8);
+          va[i][0] = w.x, va[i][1] = w.y;
+        } else {
+          va[i][0] = *reinterpret_cast<const uint32_t*>(x + vcode[i] + e * CODE8);
+        }
+      }
+      if constexpr (!all) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int t = ts + t01[i] + 8 * e;
+          if (t >= causal0 && t < tok1 && vs[i] >= kKv4FirstInf) {
+            vs[i] = 0;
+            atomicOr(&nan[D == 128 ? g : g >> 1], 1u << (t - causal0));
+          }
+          if (t >= tok1 || bad_block(t01[i] + 8 * e)) vs[i] = 0;
+        }
+      }
+      const uint32_t s2 = kv4_scale_pair(vs[0], vs[1]);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const uint32_t a = va[0][i], b = va[1][i];
+        const uint32_t lo = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
+        const uint32_t hi = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
+        uint32_t u[4], z[4];
+        kv4_unpack(lo, u);
+        kv4_unpack(hi, z);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          y[e][4 * i + k][0] = hmul2_u(u[k], s2);
+          y[e][4 * i + k][1] = hmul2_u(z[k], s2);
+        }
+      }
+    }
+#pragma unroll
+    for (int mt = 0; mt < KSTEPS; ++mt) {
+      const uint32_t a[4] = {y[0][mt][0], y[0][mt][1], y[1][mt][0], y[1][mt][1]};
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) mma_16816<__half>(acc[nt][mt], a, pb0[nt], pb1[nt]);
+    }
+  };
+
+  const int nfull = any_bad ? 0 : min(max(min(tok1, causal0) - tok0, 0) / kTile, ntiles);  // seen whole by every column
+  for (int i = 0; i < kDepth - 1; ++i) issue(i);
+  int slot = 0;
+  for (int i = 0, j = warp; j < ntiles; ++i, j += kWarps) {
+    cp_async_wait<kDepth - 2>();
+    __syncwarp();  // every lane's part of tile i is there, and every lane is done with tile i - 1
+    issue(i + kDepth - 1);
+    const uint8_t* x = ring + slot * L::TILE;
+    slot = slot + 1 == kDepth ? 0 : slot + 1;
+    if (j < nfull) compute(x, j, std::true_type{});
+    else compute(x, j, std::false_type{});
   }
+  cp_async_wait_all();
+  __syncwarp();  // the ring becomes the outputs' place
 
   // the warps' parts of each column: brought to the largest reference, added up in order
 #pragma unroll
@@ -420,7 +408,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
         sums[(kWarps + warp) * NT * 8 + n] = x;
       }
     }
-  float* po = reinterpret_cast<float*>(ring);  // every copy into the ring has landed and been read
+  float* po = reinterpret_cast<float*>(ring);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -443,7 +431,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const float a = ex2_approx(f[w] - ref);
-      const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * L::RING) + n * L::ROW + d);
+      const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * L::WARP) + n * L::ROW + d);
       o.x += a * x.x, o.y += a * x.y, o.z += a * x.z, o.w += a * x.w;
       sum += a * sums[(kWarps + w) * NT * 8 + n];
     }
@@ -453,8 +441,10 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
     const size_t row = row_of(col0 + n);
     if (nsplit == 1) {
       const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a NaN sum stays one
-      *reinterpret_cast<uint2*>(out + row * D + d) =
-          make_uint2(Elem<T>::pack(o.x * inv, o.y * inv), Elem<T>::pack(o.z * inv, o.w * inv));
+      o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + d) =
+          p.bf16 ? make_uint2(Elem<__nv_bfloat16>::pack(o.x, o.y), Elem<__nv_bfloat16>::pack(o.z, o.w))
+                 : make_uint2(Elem<__half>::pack(o.x, o.y), Elem<__half>::pack(o.z, o.w));
     } else {
       *reinterpret_cast<float4*>(p.part_o + (row * p.max_splits + c) * D + d) = o;
       if (d == 0) {
@@ -465,34 +455,33 @@ __global__ void __launch_bounds__(kWarps * 32) kv4_decode_kernel(const Kv4Decode
   }
 }
 
-template <int D, int NT, typename T>
+template <int D, int NT, int BS>
 cudaError_t launch_t(const Kv4DecodeParams& p, cudaStream_t stream) {
-  constexpr int STAGES = 3;
-  using L = Kv4DecodeSmem<D, NT, STAGES>;
-  auto kern = kv4_decode_kernel<D, NT, STAGES, T>;
-  static bool attr_set[64] = {};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && !attr_set[dev]) {
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::bytes(kMaxEntries));
-    if (e != cudaSuccess) return e;
-    attr_set[dev] = true;
-  }
+  using L = Kv4DecodeSmem<D, NT>;
+  static_assert(L::bytes(kMaxEntries + 4) <= 48 * 1024, "no attribute needed");
   const dim3 grid((unsigned)(p.max_splits * p.kv_heads), p.num_seqs, (p.group * p.q_len + NT * 8 - 1) / (NT * 8));
-  return launch_pdl(kern, grid, dim3(kWarps * 32), L::bytes(p.tab_entries), stream, p);
+  return launch_pdl(kv4_decode_kernel<D, NT, BS>, grid, dim3(kWarps * 32), L::bytes(p.tab_entries + 4), stream, p);
 }
 
-template <int D, typename T>
+template <int D, int BS>
 cudaError_t launch_nt(const Kv4DecodeParams& p, cudaStream_t stream) {
-  return p.group * p.q_len <= 8 ? launch_t<D, 1, T>(p, stream) : launch_t<D, 2, T>(p, stream);
+  return p.group * p.q_len <= 8 ? launch_t<D, 1, BS>(p, stream) : launch_t<D, 2, BS>(p, stream);
+}
+
+template <int D>
+cudaError_t launch_bs(const Kv4DecodeParams& p, cudaStream_t stream) {
+  switch (p.block_size) {
+    case 4: return launch_nt<D, 4>(p, stream);
+    case 8: return launch_nt<D, 8>(p, stream);
+    case 16: return launch_nt<D, 16>(p, stream);
+    default: return launch_nt<D, 32>(p, stream);
+  }
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int head_dim, pa_dtype dt, cudaStream_t stream) {
-  if (head_dim == 128)
-    return dt == PA_BF16 ? launch_nt<128, __nv_bfloat16>(p, stream) : launch_nt<128, __half>(p, stream);
-  return dt == PA_BF16 ? launch_nt<64, __nv_bfloat16>(p, stream) : launch_nt<64, __half>(p, stream);
+cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int head_dim, cudaStream_t stream) {
+  return head_dim == 128 ? launch_bs<128>(p, stream) : launch_bs<64>(p, stream);
 }
 
 }  // namespace pa

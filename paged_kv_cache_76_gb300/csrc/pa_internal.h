@@ -329,12 +329,13 @@ struct Kv4DecodeParams {
   float* part_m;
   float* part_l;
   int* err;
-  int maxblk, num_seqs, q_len, q_heads, kv_heads, group, num_blocks, block_size, block_shift;
+  int maxblk, num_seqs, q_len, q_heads, kv_heads, group, num_blocks, block_size;
   int split_tokens, max_splits, tab_entries;
+  int bf16;  // q and out: bf16, or fp16
   float scale_log2;
 };
 // without the merge (launch_lse_merge)
-cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int head_dim, pa_dtype dt, cudaStream_t stream);
+cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int head_dim, cudaStream_t stream);
 
 // Chunked prefill over a 4-bit cache (kv4_prefill.cu): the merge included.
 struct Kv4PrefillParams {

@@ -225,12 +225,12 @@ int pa_decode_kv4(const void* q, const void* k_cache, const void* v_cache, const
   p.group = q_heads / kv_heads;
   p.num_blocks = num_blocks;
   p.block_size = block_size;
-  p.block_shift = log2_of(block_size);
   p.split_tokens = s.split;
   p.max_splits = s.max_splits;
   p.tab_entries = s.split / block_size;
+  p.bf16 = dtype == PA_BF16;
   p.scale_log2 = scale * 1.4426950408889634f;
-  st = cuda_status(launch_kv4_decode(p, head_dim, dtype, to_stream(stream)));
+  st = cuda_status(launch_kv4_decode(p, head_dim, to_stream(stream)));
   if (st != PA_OK || s.max_splits == 1) return st;
   MergeParams mp{};
   mp.part_o = p.part_o;
