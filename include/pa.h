@@ -735,23 +735,26 @@ int pa_dequantize_kv4(const void* k_cache, const void* v_cache, const int32_t* s
  *                 gives a zero row
  *   q_len         >= 1, with (q_heads / kv_heads) * q_len <= 32 and a group of at
  *                 most 16
- *   max_blocks_per_seq  at most 2^25 / block_size
- *   workspace     at least pa_decode_kv4_workspace_size(...) bytes
- * The tiles of all requests and heads are shared out evenly, so a request's sums
- * are cut where the batch's work is: equal batches give equal bits, the same
- * request in another batch may round otherwise.
+ *   split_tokens  0, or a multiple of 32 no larger than 1024 * block_size;
+ *                 pa_decode_kv4_split_tokens returns the partition size such a
+ *                 call uses, or PA_ERR_INVALID
+ *   workspace     at least pa_decode_kv4_workspace_size(...) bytes (NULL where
+ *                 that is 0)
  * Sums and softmax are fp32; weights are rounded to fp16 for the P.V product
  * (relative error 2^-11), the cache's elements and q are not rounded.  A token
  * that a query does not see leaves it as it is, whatever the token holds (NaN
  * included).  A bad block id records PA_DEVERR_BLOCK_ID and reads as zeros.
  * ------------------------------------------------------------------------- */
+int pa_decode_kv4_split_tokens(int num_seqs, int q_len, int q_heads, int kv_heads, int max_blocks_per_seq,
+                               int block_size, int split_tokens);
+
 size_t pa_decode_kv4_workspace_size(int num_seqs, int q_len, int q_heads, int kv_heads, int head_dim,
-                                    int max_blocks_per_seq, int block_size);
+                                    int max_blocks_per_seq, int block_size, int split_tokens);
 
 int pa_decode_kv4(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                   int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int q_len, int q_heads,
-                  int kv_heads, int head_dim, int block_size, int num_blocks, float scale, void* workspace,
-                  size_t workspace_bytes, void* out, pa_dtype dtype, pa_stream stream);
+                  int kv_heads, int head_dim, int block_size, int num_blocks, float scale, int split_tokens,
+                  void* workspace, size_t workspace_bytes, void* out, pa_dtype dtype, pa_stream stream);
 
 /* ----------------------------------------------------------------------------
  * pa_chunked_prefill_kv4 - pa_chunked_prefill over a 4-bit cache.

@@ -115,8 +115,9 @@ PROTOTYPES = {
     "pa_compact_kv": (_I, [_P, _P, _P, _I, _P, _P, _I, _I, _P, _P, _I, _I, _I, _I, _I, _I, _P, _P, _I, _I, _P]),
     "pa_quantize_and_cache": (_I, [_P, _P, C.c_int64, C.c_int64, _P, _I, _P, _P, _I, _I, _I, _I, _I, _P]),
     "pa_dequantize_kv4": (_I, [_P, _P, _P, _I, _I, _I, _I, _I, _P, _P, _I, _P]),
-    "pa_decode_kv4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I]),
-    "pa_decode_kv4": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _P, _SZ, _P, _I, _P]),
+    "pa_decode_kv4_split_tokens": (_I, [_I, _I, _I, _I, _I, _I, _I]),
+    "pa_decode_kv4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "pa_decode_kv4": (_I, [_P, _P, _P, _P, _I, _P, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P, _I, _P]),
     "pa_chunked_prefill_kv4_split_tokens": (_I, [_I, _I, _I, _I, _I, _I, _I]),
     "pa_chunked_prefill_kv4_workspace_size": (_SZ, [_I, _I, _I, _I, _I, _I, _I, _I, _I]),
     "pa_chunked_prefill_kv4": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, _I, _F, _I, _P, _SZ, _P, _I,

@@ -23,11 +23,10 @@
 //
 // Per 16 tokens (m16n8k16, S^T = K Q^T and O^T += V^T P^T):
 //   K: lane (g, c) = (lane / 4, lane % 4) holds D/4 consecutive elements of
-//      tokens pi(g) and pi(g) + 8, D/16 A fragments of both; which elements a
-//      fragment takes is free as long as Q's B fragments take the same.
+//      tokens g and g + 8, D/16 A fragments of both; which elements a fragment
+//      takes is free as long as Q's B fragments take the same.
 //   V: lane (g, c) holds D/8 elements of the four tokens that P's B fragments
-//      hold for it, pi(2c) = c, pi(2c + 1) = c + 4 and those + 8 (so that a
-//      load's lanes have rows of either parity).  An A fragment wants two tokens
+//      hold for it, 2c, 2c + 1 and those + 8.  An A fragment wants two tokens
 //      side by side, so the codes of two tokens are interleaved before they are
 //      converted (four logical instructions for 16 elements, where 16 fp16 pairs
 //      would take 16).
@@ -53,13 +52,12 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kTile = 16;
 constexpr int kDepth = 4;  // tiles of a warp's ring
-constexpr int kChunk = 256;  // tiles whose Block Table entries a CTA holds at a time
-constexpr int kMinShare = 8;  // tiles of a CTA at least: with fewer the merge costs more than they save
+constexpr int kMaxEntries = 1024;  // Block Table entries of a partition
 constexpr float kRescale = 8.f;    // a reference is raised when a score passes it by more (log2 units)
 constexpr float kShift = 7.f;      // weights are 2^(s - m + kShift) <= 2^15
 constexpr unsigned kAll = 0xffffffffu;
 
-template <int D, int NT, int BS>
+template <int D, int NT>
 struct Kv4DecodeSmem {
   static constexpr int TILE = 2 * kTile * Kv4Row<D>::BYTES;  // K, then V
   static constexpr int RING = kDepth * TILE;                 // of a warp; at the end its outputs
@@ -68,301 +66,183 @@ struct Kv4DecodeSmem {
   static constexpr int SUM_OFF = kWarps * WARP;             // m, then l: [kWarps][NT * 8]
   static constexpr int NAN_OFF = SUM_OFF + 2 * kWarps * NT * 8 * 4;
   static constexpr int BAD_OFF = NAN_OFF + D / kKv4Group * 4;  // bits: bad block ids of the table
-  static constexpr int ENTRIES = BS > kTile ? kChunk * kTile / BS + 1 : kChunk * (kTile / BS);
-  static constexpr int TAB_OFF = BAD_OFF + (ENTRIES + 31) / 32 * 4;
-  static constexpr int BYTES = TAB_OFF + ENTRIES * 4;
+  static constexpr int TAB_OFF = BAD_OFF + (kMaxEntries + 32) / 8;
+  static constexpr int bytes(int entries) { return TAB_OFF + entries * 4; }
 };
-
-// Shared memory at an address and a constant, after the wait that orders them
-// (volatile: they stay behind it).
-__device__ __forceinline__ uint4 lds4(uint32_t at, int off) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at + off));
-  return v;
-}
-__device__ __forceinline__ uint2 lds2(uint32_t at, int off) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at + off));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds1(uint32_t at, int off) {
-  uint32_t v;
-  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at + off));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u16(uint32_t at, int off) {
-  uint32_t v;
-  asm volatile("{\n .reg .u16 t;\n ld.shared.u16 t, [%1];\n cvt.u32.u16 %0, t;\n}" : "=r"(v) : "r"(at + off));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t at, int off) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at + off));
-  return v;
-}
-__device__ __forceinline__ void cp_async16_at(uint32_t dst, int off, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + off), "l"(src) : "memory");
-}
-
-// The work of a launch is one line of tiles: request after request, KV head
-// after KV head, each list's tiles in order.  CTA i takes tiles [i s, (i + 1) s)
-// of it, so that every CTA has as many, whatever the lengths.  A list that one
-// CTA holds whole is written by it; of any other, a CTA holds the end of one
-// (slot 0) and the beginning of one (slot 1) at most, as partials that the merge
-// joins.
-struct Line {
-  int64_t total;
-  uint32_t share;  // tiles of a CTA, a multiple of kWarps
-};
-__device__ __forceinline__ uint32_t div_line(int64_t a, uint32_t b) {
-  return (uint64_t)a >> 32 ? (uint32_t)((uint64_t)a / b) : (uint32_t)a / b;
-}
-__device__ __forceinline__ Line line_of(int64_t total, int grid) {
-  const uint32_t share = div_line(total + (int64_t)grid * kWarps - 1, (uint32_t)(grid * kWarps)) * kWarps;
-  return Line{total, max(share, (uint32_t)kMinShare)};
-}
-__device__ __forceinline__ int tiles_of(const Kv4DecodeParams& p, int r) {
-  return (min(max(__ldg(p.lens + r), 0), p.cap) + kTile - 1) / kTile;
-}
 
 template <int D, int NT, int BS>
 __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_decode_kernel(const Kv4DecodeParams p) {
-  using L = Kv4DecodeSmem<D, NT, BS>;
+  using L = Kv4DecodeSmem<D, NT>;
   using R = Kv4Row<D>;
   constexpr int KSTEPS = D / 16;
   constexpr int NW = D / 32;  // words of K codes a lane has per token; of V codes: D / 64
   constexpr int PAGE = BS * R::BYTES;
 
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ int64_t s_sum[kWarps];
-  __shared__ int s_chunk[kWarps];
-  __shared__ int64_t s_before;
-  __shared__ int s_request, s_len;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c4 = lane & 3;
   float* sums = reinterpret_cast<float*>(smem + L::SUM_OFF);
   uint32_t* nan = reinterpret_cast<uint32_t*>(smem + L::NAN_OFF);
   uint32_t* badbits = reinterpret_cast<uint32_t*>(smem + L::BAD_OFF);
   int32_t* tab = reinterpret_cast<int32_t*>(smem + L::TAB_OFF);
+  if (threadIdx.x < D / kKv4Group) nan[threadIdx.x] = 0;
   griddep_launch_dependents();
 
-  // this CTA's part of the line: tiles [at, end), from request r on, which has
-  // `before` tiles (of one head) before it
-  constexpr int THREADS = kWarps * 32;
-  const bool writes_before = blockIdx.x == 0 && blockIdx.y == 0;  // for the merge: tiles before each request's
-  bool bad_len = false;
-  int64_t total = 0;
-  if (p.num_seqs > THREADS) {
-    for (int r = threadIdx.x; r < p.num_seqs; r += THREADS) total += tiles_of(p, r);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
-    if (lane == 0) s_sum[warp] = total;
-    __syncthreads();
-    total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += s_sum[w];
+  const int r = blockIdx.y;
+  const int h = blockIdx.x % p.kv_heads, c = blockIdx.x / p.kv_heads;
+  const int col0 = blockIdx.z * NT * 8;
+  const int cap = p.maxblk * BS;
+  int ctx = __ldg(p.lens + r);
+  const bool bad_len = ctx < 0 || ctx > cap;
+  ctx = min(max(ctx, 0), cap);
+  const int nsplit = (ctx + p.split_tokens - 1) / p.split_tokens;
+  const int G = p.group, NC = G * p.q_len, qh0 = h * G;
+  if (c >= max(nsplit, 1)) {
+    griddep_wait();
+    if (bad_len && threadIdx.x == 0) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
+    return;
   }
-  int64_t sum = 0, at = 0, end = 0, before = 0;
-  int r = 0;
-  for (int r0 = 0; r0 < p.num_seqs; r0 += THREADS) {
-    const int mine = r0 + threadIdx.x, n = mine < p.num_seqs ? tiles_of(p, mine) : 0;
-    if (mine < p.num_seqs) {
-      const int len = __ldg(p.lens + mine);
-      bad_len |= len < 0 || len > p.cap;
+  const int tok0 = c * p.split_tokens, tok1 = min(tok0 + p.split_tokens, ctx);
+  const int ntiles = (tok1 - tok0 + kTile - 1) / kTile;  // of the CTA
+
+  // row of column n in q, out and the partials
+  auto row_of = [&](int n) {
+    const int qi = n / G;
+    return (size_t)(r * p.q_len + qi) * p.q_heads + qh0 + (n - qi * G);
+  };
+
+  bool bad_id = false;
+  uint32_t qf[NT][KSTEPS][2];
+  float sl2[NT][2];  // softmax scale (log2 units) of the lane's two columns of each n-tile
+  {
+    const int nblk = (tok1 - tok0 + BS - 1) / BS;
+    const int entries = (ntiles * kTile + BS - 1) / BS;
+    const int32_t* trow = p.tables + (size_t)r * p.maxblk + tok0 / BS;
+    // a bad block, and one behind the last, is read as block 0 and counts as zeros
+    for (int i = threadIdx.x; i < (entries + 31 & ~31); i += kWarps * 32) {
+      int b = i < nblk ? __ldg(trow + i) : 0;
+      const bool bad = b < 0 || b >= p.num_blocks;
+      const uint32_t bits = __ballot_sync(kAll, bad);
+      if (lane == 0) badbits[i >> 5] = bits;
+      if (i < entries) tab[i] = bad ? 0 : b;
+      bad_id |= bad;
     }
-    int x = n;  // inclusive in the warp
+    // Q^T as the B operand: lane (g, c) holds column g of each n-tile, elements
+    // D/4 c + 4 ks + {0, 1} and {2, 3}
+    auto load_q = [&](auto type) {
+      using T = decltype(type);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kAll, x, o);
-      if (lane >= o) x += y;
-    }
-    __syncthreads();
-    if (lane == 31) s_chunk[warp] = x;
-    __syncthreads();
-    int64_t first = sum + x - n;
+      for (int nt = 0; nt < NT; ++nt) {
+        const int n = col0 + nt * 8 + g;
+        const uint2* src = reinterpret_cast<const uint2*>(static_cast<const T*>(p.q) + (n < NC ? row_of(n) : 0) * D + (D / 4) * c4);
+        float x[KSTEPS][4];
+        float top = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) first += s_chunk[w];
-      sum += s_chunk[w];
+        for (int ks = 0; ks < KSTEPS; ++ks) {
+          const uint2 w = n < NC ? __ldg(src + ks) : make_uint2(0u, 0u);
+          x[ks][0] = Elem<T>::lo(w.x), x[ks][1] = Elem<T>::hi(w.x);
+          x[ks][2] = Elem<T>::lo(w.y), x[ks][3] = Elem<T>::hi(w.y);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(x[ks][e]));
+        }
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+        // 2^e <= top < 2^(e + 1); rows of zeros and of values that are not finite stay as they are
+        int e = top > 0.f && top < INFINITY ? ilogbf(top) - 13 : 0;
+        e = max(e, -126);
+        const float down = ldexpf(1.f, -e);
+#pragma unroll
+        for (int ks = 0; ks < KSTEPS; ++ks) {
+          qf[nt][ks][0] = Elem<__half>::pack(x[ks][0] * down, x[ks][1] * down);
+          qf[nt][ks][1] = Elem<__half>::pack(x[ks][2] * down, x[ks][3] * down);
+        }
+        const float back = p.scale_log2 * ldexpf(1.f, e);
+        // accumulators hold columns 2c, 2c + 1 of the tile
+        sl2[nt][0] = __shfl_sync(kAll, back, 8 * c4);
+        sl2[nt][1] = __shfl_sync(kAll, back, 8 * c4 + 4);
+      }
+    };
+    if (ntiles > 0) {
+      if (p.bf16) load_q(__nv_bfloat16{});
+      else load_q(__half{});
     }
-    if (r0 == 0) {
-      if (p.num_seqs <= THREADS) total = sum;
-      total *= p.kv_heads;
-      const Line line = line_of(total, gridDim.x);
-      at = (int64_t)line.share * blockIdx.x;
-      end = min(at + line.share, total);
-    }
-    if (n > 0 && first * p.kv_heads <= at && at < (first + n) * p.kv_heads) {
-      s_request = mine;
-      s_before = first;
-      s_len = min(max(__ldg(p.lens + mine), 0), p.cap);
-    }
-    if (writes_before) {
-      if (r0 == 0) griddep_wait();  // the workspace
-      if (mine < p.num_seqs) p.before[mine] = first * p.kv_heads;
-    } else if (sum * p.kv_heads > at) {
-      break;
-    }
-  }
-  if (writes_before && threadIdx.x == 0) p.before[p.num_seqs] = total;
-  if (at >= end && !writes_before) return;
-  __syncthreads();
-  int ctx = 0;  // of request r
-  if (at < end) {
-    r = s_request;
-    before = s_before;
-    ctx = s_len;
   }
   griddep_wait();
-  if (writes_before && bad_len) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
+  if (bad_len && threadIdx.x == 0) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
+  if (bad_id) record_error(p.err, PA_DEVERR_BLOCK_ID);
+  const int ncols = min(NC - col0, NT * 8);  // of this CTA
+  if (ctx == 0) {
+    uint16_t* out = static_cast<uint16_t*>(p.out);  // 0 in either type
+    for (int i = threadIdx.x; i < ncols * D; i += kWarps * 32) out[row_of(col0 + i / D) * D + i % D] = 0;
+    return;
+  }
+  const bool any_bad = __syncthreads_or(bad_id);  // and the table is complete
 
-  const int G = p.group, NC = G * p.q_len;
-  const int col0 = blockIdx.y * NT * 8, ncols = min(NC - col0, NT * 8);
-
-  // Where this lane's elements are in a tile: K of token pi(g) (+ 8), V of c and c + 4 (+ 8)
-  auto code_at = [](int t) { return BS < kTile ? t / BS * PAGE + t % BS * R::CODES : t * R::CODES; };
-  auto scale_at = [](int t) {
-    return BS < kTile ? t / BS * PAGE + BS * R::CODES + t % BS * R::SCALES : kTile * R::CODES + t * R::SCALES;
-  };
-  constexpr int VOFF = kTile * R::BYTES;
-  const int pg = (g >> 1) + 4 * (g & 1);
-  constexpr int CODE4 = BS < 8 ? PAGE : 4 * R::CODES, SCALE4 = BS < 8 ? PAGE : 4 * R::SCALES;  // to the token 4 behind
-  constexpr int CODE8 = BS < kTile ? 8 / BS * PAGE : 8 * R::CODES, SCALE8 = BS < kTile ? 8 / BS * PAGE : 8 * R::SCALES;
-  const uint32_t ring_at = smem_u32(smem + warp * L::WARP);
-  const uint32_t kcode = ring_at + code_at(pg) + c4 * (4 * NW), kscale = ring_at + scale_at(pg) + c4 * (NW / 2);
-  const uint32_t vcode = ring_at + VOFF + code_at(c4) + g * (D / 16);
-  const uint32_t vscale = ring_at + VOFF + scale_at(c4) + (D == 128 ? g : g >> 1);
   // A tile is 2 * R::BYTES vectors of 16 bytes, K's and then V's, copied as they
   // are in the pages (of blocks of 32: the tile's half of the codes, then of the
   // scales); this lane copies vectors lane, lane + 32, ...
   constexpr int VECS = R::BYTES, SLOTS = (2 * VECS + 31) / 32;
   constexpr int PV = BS < kTile ? PAGE / 16 : VECS;  // vectors of a page in a tile
   uint8_t* ring = smem + warp * L::WARP;
-  const uint32_t ring0 = ring_at + 16 * lane;
+  const uint32_t ring0 = smem_u32(ring) + 16 * lane;
   const uint32_t block_bytes = (uint32_t)p.kv_heads * PAGE;
-
-  while (at < end) {
-    // the next list, or the part of it that is this CTA's: tiles [first, first + count)
-    const int tiles = (ctx + kTile - 1) / kTile;
-    const uint32_t in_request = (uint32_t)(at - before * p.kv_heads);  // below 2^31: cap <= 2^25, 1024 heads
-    const int h = (int)(in_request / (uint32_t)tiles), first = (int)(in_request - (uint32_t)h * tiles);
-    const int count = (int)min(end - at, (int64_t)(tiles - first));
-    const int qh0 = h * G;
-    // row of column n in q and out
-    auto row_of = [&](int n) {
-      const int qi = n / G;
-      return (size_t)(r * p.q_len + qi) * p.q_heads + qh0 + (n - qi * G);
-    };
-    if (threadIdx.x < D / kKv4Group) nan[threadIdx.x] = 0;
-
-    const uint8_t* src[SLOTS];
+  const uint8_t* src[SLOTS];
 #pragma unroll
-    for (int q = 0; q < SLOTS; ++q) {
-      const int id = lane + 32 * q, i = id % VECS;
-      const int codes = kTile * R::CODES / 16;  // vectors of them, blocks of 32
-      const int off = BS <= kTile || i < codes ? (i % PV) * 16 : BS * R::CODES + (i - codes) * 16;
-      src[q] = static_cast<const uint8_t*>(id < VECS ? p.k_cache : p.v_cache) + (int64_t)h * PAGE + off;
+  for (int q = 0; q < SLOTS; ++q) {
+    const int id = lane + 32 * q, i = id % VECS;
+    const int codes = kTile * R::CODES / 16;  // vectors of them, blocks of 32
+    const int at = BS <= kTile || i < codes ? (i % PV) * 16 : BS * R::CODES + (i - codes) * 16;
+    src[q] = static_cast<const uint8_t*>(id < VECS ? p.k_cache : p.v_cache) + (int64_t)h * PAGE + at;
+  }
+  // entry of the table that holds a token of tile j
+  auto entry = [](int j, int token) { return BS >= kTile ? j * kTile / BS : j * (kTile / BS) + token / BS; };
+  auto issue = [&](int i) {  // the warp's i-th tile
+    const int j = warp + i * kWarps;
+    if (j < ntiles) {
+      const uint32_t dst = ring0 + (uint32_t)(i % kDepth) * L::TILE;
+#pragma unroll
+      for (int q = 0; q < SLOTS; ++q) {
+        const int id = lane + 32 * q, v = id % VECS;
+        const uint8_t* s = src[q] + (uint64_t)(uint32_t)tab[entry(j, v / PV * BS)] * block_bytes;
+        if (BS > kTile) s += (j * kTile & (BS - 1)) * (v < kTile * R::CODES / 16 ? R::CODES : R::SCALES);
+        if (32 * q + 32 <= 2 * VECS || id < 2 * VECS) cp_async16(dst + 512 * q, s, 16);
+      }
     }
-    // Q^T as the B operand: lane (g, c) holds column g of each n-tile, elements
-    // D/4 c + 4 ks + {0, 1} and {2, 3}
-    uint32_t qf[NT][KSTEPS][2];
-    float sl2[NT][2];  // softmax scale (log2 units) of the lane's two columns of each n-tile
-    auto convert_q = [&](auto type) {
-      using T = decltype(type);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int n = col0 + nt * 8 + g;
-        const uint2* q2 = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + (n < NC ? row_of(n) : 0) * D + (D / 4) * c4);
-        uint2 qw[KSTEPS];
-#pragma unroll
-        for (int ks = 0; ks < KSTEPS; ++ks) qw[ks] = n < NC ? __ldg(q2 + ks) : make_uint2(0u, 0u);
-        float top = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < KSTEPS; ++ks) {
-          const uint2 w = qw[ks];
-          top = fmaxf(top, fmaxf(fmaxf(fabsf(Elem<T>::lo(w.x)), fabsf(Elem<T>::hi(w.x))),
-                                 fmaxf(fabsf(Elem<T>::lo(w.y)), fabsf(Elem<T>::hi(w.y)))));
-        }
-        top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-        // 2^e <= top < 2^(e + 1); rows of zeros and of values that are not finite stay as they are
-        int e = (int)(__float_as_uint(top) >> 23) - 127;  // of a subnormal -127: it is brought up less
-        e = top > 0.f && top < INFINITY ? max(e - 13, -126) : 0;
-        const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-        for (int ks = 0; ks < KSTEPS; ++ks) {
-          const uint2 w = qw[ks];
-          qf[nt][ks][0] = Elem<__half>::pack(Elem<T>::lo(w.x) * down, Elem<T>::hi(w.x) * down);
-          qf[nt][ks][1] = Elem<__half>::pack(Elem<T>::lo(w.y) * down, Elem<T>::hi(w.y) * down);
-        }
-        const float back = p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
-        // accumulators hold columns 2c, 2c + 1 of the tile
-        sl2[nt][0] = __shfl_sync(kAll, back, 8 * c4);
-        sl2[nt][1] = __shfl_sync(kAll, back, 8 * c4 + 4);
-      }
-    };
+    cp_async_commit();
+  };
+  // Where this lane's elements are in a tile: K of token pi(g) (+ 8), V of pi(2c), pi(2c + 1) (+ 8)
+  auto code_at = [](int t) { return BS < kTile ? t / BS * PAGE + t % BS * R::CODES : t * R::CODES; };
+  auto scale_at = [](int t) {
+    return BS < kTile ? t / BS * PAGE + BS * R::CODES + t % BS * R::SCALES : kTile * R::CODES + t * R::SCALES;
+  };
+  constexpr int VOFF = kTile * R::BYTES;
+  const int pg = g ^ (g >> 1 & 1);
+  const int t01[2] = {2 * c4 ^ (c4 & 1), (2 * c4 + 1) ^ (c4 & 1)};
+  const int kcode = code_at(pg) + c4 * (4 * NW), kscale = scale_at(pg) + c4 * (NW / 2);
+  const int vcode[2] = {VOFF + code_at(t01[0]) + g * (D / 16), VOFF + code_at(t01[1]) + g * (D / 16)};
+  const int vscale[2] = {VOFF + scale_at(t01[0]) + (D == 128 ? g : g >> 1), VOFF + scale_at(t01[1]) + (D == 128 ? g : g >> 1)};
+  constexpr int CODE8 = BS < kTile ? 8 / BS * PAGE : 8 * R::CODES, SCALE8 = BS < kTile ? 8 / BS * PAGE : 8 * R::SCALES;
 
-    float m[NT][2], l[NT][2], acc[NT][KSTEPS][4];
-    int lim[NT][2];  // tokens [0, lim) are visible to the lane's columns
+  float m[NT][2], l[NT][2], acc[NT][KSTEPS][4];
+  int lim[NT][2];  // tokens [0, lim) are visible to the lane's columns
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+  for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m[nt][e] = -INFINITY;
-        l[nt][e] = 0.f;
-        const int n = col0 + nt * 8 + 2 * c4 + e;
-        lim[nt][e] = ctx - (p.q_len - 1 - (n < NC ? n / G : p.q_len - 1));
-      }
-#pragma unroll
-      for (int mt = 0; mt < KSTEPS; ++mt) acc[nt][mt][0] = acc[nt][mt][1] = acc[nt][mt][2] = acc[nt][mt][3] = 0.f;
+    for (int e = 0; e < 2; ++e) {
+      m[nt][e] = -INFINITY;
+      l[nt][e] = 0.f;
+      const int n = col0 + nt * 8 + 2 * c4 + e;
+      lim[nt][e] = min(tok1, ctx - (p.q_len - 1 - (n < NC ? n / G : p.q_len - 1)));
     }
-    const int causal0 = ctx - (p.q_len - 1);  // tokens from here on are hidden from some query (q_len 1: from ctx on)
-
-    for (int chunk = 0; chunk < count; chunk += kChunk) {
-    const int tile0 = first + chunk, ntiles = min(kChunk, count - chunk);  // of the list; of the chunk
-    const int entry0 = tile0 * kTile / BS;
-    // entry of the table that holds a token of the chunk's tile j
-    auto entry = [&](int j, int token) {
-      return BS > kTile ? (tile0 + j) * kTile / BS - entry0 : BS == kTile ? j : j * (kTile / BS) + token / BS;
-    };
-    bool any_bad;
-    {
-      // a bad block, and one behind the last, is read as block 0 and counts as zeros
-      const int nblk = (min((tile0 + ntiles) * kTile, ctx) + BS - 1) / BS - entry0;
-      const int entries = entry(ntiles - 1, kTile - 1) + 1;
-      const int32_t* trow = p.tables + (size_t)r * p.maxblk + entry0;
-      bool bad_id = false;
-      for (int i = threadIdx.x; i < (entries + 31 & ~31); i += kWarps * 32) {
-        int b = i < nblk ? __ldg(trow + i) : 0;
-        const bool bad = b < 0 || b >= p.num_blocks;
-        const uint32_t bits = __ballot_sync(kAll, bad);
-        if (lane == 0) badbits[i >> 5] = bits;
-        if (i < entries) tab[i] = bad ? 0 : b;
-        bad_id |= bad;
-      }
-      if (bad_id) record_error(p.err, PA_DEVERR_BLOCK_ID);
-      any_bad = __syncthreads_or(bad_id);  // and the table is complete
-    }
-    auto issue = [&](int j, uint32_t slot) {  // tile j of the chunk to a place of the ring
-      if (j < ntiles) {
-        const uint32_t dst = ring0 + slot * L::TILE;
-        const uint32_t block = (uint32_t)tab[entry(j, 0)];  // the only one, of blocks of 16 and 32
 #pragma unroll
-        for (int q = 0; q < SLOTS; ++q) {
-          const int id = lane + 32 * q, v = id % VECS;
-          const uint32_t b = BS >= kTile ? block : (uint32_t)tab[entry(j, v / PV * BS)];
-          const uint8_t* s = src[q] + (uint64_t)b * block_bytes;
-          if (BS > kTile) s += ((tile0 + j) * kTile & (BS - 1)) * (v < kTile * R::CODES / 16 ? R::CODES : R::SCALES);
-          if (32 * q + 32 <= 2 * VECS || id < 2 * VECS) cp_async16_at(dst, 512 * q, s);
-        }
-      }
-      cp_async_commit();
-    };
+    for (int mt = 0; mt < KSTEPS; ++mt) acc[nt][mt][0] = acc[nt][mt][1] = acc[nt][mt][2] = acc[nt][mt][3] = 0.f;
+  }
+  const int causal0 = ctx - (p.q_len - 1);  // tokens from here on are hidden from some query (q_len 1: from ctx on)
 
   // 16 tokens from ts on; `all`: every column sees all of them
-  auto compute = [&](const uint32_t x, const int j, const auto all_t) {  // x: the tile's place in the ring
+  auto compute = [&](const uint8_t* x, const int j, const auto all_t) {
     constexpr bool all = decltype(all_t)::value;
-    const int ts = (tile0 + j) * kTile;
+    const int ts = tok0 + j * kTile;
     auto bad_block = [&](int token) {
       const int i = entry(j, token);
       return badbits[i >> 5] >> (i & 31) & 1;
@@ -376,13 +256,13 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       if constexpr (NW == 4) {
-        const uint4 w = lds4(x + kcode, e * CODE8);
+        const uint4 w = *reinterpret_cast<const uint4*>(x + kcode + e * CODE8);
         kw[e][0] = w.x, kw[e][1] = w.y, kw[e][2] = w.z, kw[e][3] = w.w;
-        ks[e] = lds_u16(x + kscale, e * SCALE8);
+        ks[e] = *reinterpret_cast<const uint16_t*>(x + kscale + e * SCALE8);
       } else {
-        const uint2 w = lds2(x + kcode, e * CODE8);
+        const uint2 w = *reinterpret_cast<const uint2*>(x + kcode + e * CODE8);
         kw[e][0] = w.x, kw[e][1] = w.y;
-        ks[e] = lds_u8(x + kscale, e * SCALE8);
+        ks[e] = x[kscale + e * SCALE8];
       }
     }
 #pragma unroll
@@ -455,23 +335,23 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
       uint32_t vs[2], va[2][D / 64];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        vs[i] = lds_u8(x + vscale, e * SCALE8 + i * SCALE4);
+        vs[i] = x[vscale[i] + e * SCALE8];
         if constexpr (D == 128) {
-          const uint2 w = lds2(x + vcode, e * CODE8 + i * CODE4);
+          const uint2 w = *reinterpret_cast<const uint2*>(x + vcode[i] + e * CODE8);
           va[i][0] = w.x, va[i][1] = w.y;
         } else {
-          va[i][0] = lds1(x + vcode, e * CODE8 + i * CODE4);
+          va[i][0] = *reinterpret_cast<const uint32_t*>(x + vcode[i] + e * CODE8);
         }
       }
       if constexpr (!all) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          const int t = ts + c4 + 4 * i + 8 * e;
-          if (t >= causal0 && t < ctx && vs[i] >= kKv4FirstInf) {
+          const int t = ts + t01[i] + 8 * e;
+          if (t >= causal0 && t < tok1 && vs[i] >= kKv4FirstInf) {
             vs[i] = 0;
             atomicOr(&nan[D == 128 ? g : g >> 1], 1u << (t - causal0));
           }
-          if (t >= ctx || bad_block(c4 + 4 * i + 8 * e)) vs[i] = 0;
+          if (t >= tok1 || bad_block(t01[i] + 8 * e)) vs[i] = 0;
         }
       }
       const uint32_t s2 = kv4_scale_pair(vs[0], vs[1]);
@@ -498,197 +378,94 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
     }
   };
 
-    // tiles that every column sees whole
-    const int nfull = any_bad ? 0 : min(max(causal0, 0) / kTile - tile0, ntiles);
-#pragma unroll
-    for (int i = 0; i < kDepth - 1; ++i) issue(warp + i * kWarps, i);
-    if (chunk == 0) {  // while the first tiles come
-      if (p.bf16) convert_q(__nv_bfloat16{});
-      else convert_q(__half{});
-    }
-    uint32_t slot = 0;
-    for (int j = warp; j < ntiles; j += kWarps) {
-      cp_async_wait<kDepth - 2>();
-      __syncwarp();  // every lane's part of tile j is there, and every lane is done with the one before
-      issue(j + (kDepth - 1) * kWarps, slot == 0 ? kDepth - 1 : slot - 1);
-      const uint32_t x = slot * L::TILE;
-      slot = slot + 1 == kDepth ? 0 : slot + 1;
-      if (j < nfull) compute(x, j, std::true_type{});
-      else compute(x, j, std::false_type{});
-    }
-    cp_async_wait_all();
-    __syncthreads();  // the table, and the ring (the outputs' place) are done with
-    }
+  const int nfull = any_bad ? 0 : min(max(min(tok1, causal0) - tok0, 0) / kTile, ntiles);  // seen whole by every column
+  for (int i = 0; i < kDepth - 1; ++i) issue(i);
+  int slot = 0;
+  for (int i = 0, j = warp; j < ntiles; ++i, j += kWarps) {
+    cp_async_wait<kDepth - 2>();
+    __syncwarp();  // every lane's part of tile i is there, and every lane is done with tile i - 1
+    issue(i + kDepth - 1);
+    const uint8_t* x = ring + slot * L::TILE;
+    slot = slot + 1 == kDepth ? 0 : slot + 1;
+    if (j < nfull) compute(x, j, std::true_type{});
+    else compute(x, j, std::false_type{});
+  }
+  cp_async_wait_all();
+  __syncwarp();  // the ring becomes the outputs' place
 
-    // the warps' parts of each column: brought to the largest reference, added up in order
+  // the warps' parts of each column: brought to the largest reference, added up in order
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float x = l[nt][e];
-        x += __shfl_xor_sync(kAll, x, 4);
-        x += __shfl_xor_sync(kAll, x, 8);
-        x += __shfl_xor_sync(kAll, x, 16);
+    for (int e = 0; e < 2; ++e) {
+      float x = l[nt][e];
+      x += __shfl_xor_sync(kAll, x, 4);
+      x += __shfl_xor_sync(kAll, x, 8);
+      x += __shfl_xor_sync(kAll, x, 16);
+      if (g == 0) {
         const int n = nt * 8 + 2 * c4 + e;
-        if (g == 0) {
-          sums[warp * NT * 8 + n] = m[nt][e];
-          sums[(kWarps + warp) * NT * 8 + n] = x;
-        }
-        // the lane's D/8 elements of column n: D/8 g + 2 mt + {0, 1}
-        float4* dst = reinterpret_cast<float4*>(reinterpret_cast<float*>(ring) + n * L::ROW + (D / 8) * g);
-#pragma unroll
-        for (int i = 0; i < KSTEPS / 2; ++i)
-          dst[i] = make_float4(acc[nt][2 * i][e], acc[nt][2 * i][2 + e], acc[nt][2 * i + 1][e], acc[nt][2 * i + 1][2 + e]);
-      }
-    __syncthreads();
-    const bool whole = count == tiles;
-    const size_t part = (((size_t)blockIdx.y * gridDim.x + blockIdx.x) * 2 + (first == 0)) * (NT * 8);
-    for (int i = threadIdx.x; i < ncols * (D / 4); i += kWarps * 32) {
-      const int n = i / (D / 4), d = 4 * (i % (D / 4));
-      float f[kWarps], M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, f[w] = sums[w * NT * 8 + n]);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sum = 0.f;
-      const float ref = M == -INFINITY ? 0.f : M;  // no finite score: sums are zero or not numbers
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float a = ex2_approx(f[w] - ref);
-        const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * L::WARP) + n * L::ROW + d);
-        o.x += a * x.x, o.y += a * x.y, o.z += a * x.z, o.w += a * x.w;
-        sum += a * sums[(kWarps + w) * NT * 8 + n];
-      }
-      // a token behind causal0 that is not a number, for the columns that see it
-      const int nsee = min(max(ctx - (p.q_len - 1 - (col0 + n) / G) - causal0, 0), 31);
-      if (nan[d / kKv4Group] & ((1u << nsee) - 1u)) o = make_float4(NAN, NAN, NAN, NAN);
-      if (whole) {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a NaN sum stays one
-        o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row_of(col0 + n) * D + d) =
-            p.bf16 ? make_uint2(Elem<__nv_bfloat16>::pack(o.x, o.y), Elem<__nv_bfloat16>::pack(o.z, o.w))
-                   : make_uint2(Elem<__half>::pack(o.x, o.y), Elem<__half>::pack(o.z, o.w));
-      } else {
-        *reinterpret_cast<float4*>(p.part_o + (part + n) * D + d) = o;
-        if (d == 0) {
-          p.part_m[part + n] = M;
-          p.part_l[part + n] = sum;
-        }
+        sums[warp * NT * 8 + n] = m[nt][e];
+        sums[(kWarps + warp) * NT * 8 + n] = x;
       }
     }
-    __syncthreads();  // before the next list
-    at += count;
-    if (at < end && at == (before + tiles) * p.kv_heads) {  // the next request that has tokens
-      before += tiles;
-      do ctx = min(max(__ldg(p.lens + ++r), 0), p.cap);
-      while (ctx == 0);
-    }
-  }
-}
-
-// A CTA per list (request, KV head): the partials of one that several CTAs share,
-// in the CTAs' order; zeros for a request without tokens.
-template <int D>
-__global__ void __launch_bounds__(256) kv4_decode_merge_kernel(const Kv4DecodeParams p) {
-  constexpr int V = D / 4;  // float4s of a row
-  constexpr int CH = 4;     // partials of a thread under way
-  __shared__ float s_max[32], s_inv[32];
-  __shared__ float4 s_part[256];
-  griddep_wait();
-  griddep_launch_dependents();
-  const int h = blockIdx.x, r = blockIdx.y, tid = threadIdx.x;
-  const int64_t total = __ldcg(p.before + p.num_seqs), before = __ldcg(p.before + r);
-  const int tiles = tiles_of(p, r);
-  const int G = p.group, NC = G * p.q_len, width = p.cols;
-  auto store = [&](int col, int v, float4 x) {
-    const int qi = col / G;
-    const size_t row = (size_t)(r * p.q_len + qi) * p.q_heads + h * G + (col - qi * G);
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + 4 * v) =
-        p.bf16 ? make_uint2(Elem<__nv_bfloat16>::pack(x.x, x.y), Elem<__nv_bfloat16>::pack(x.z, x.w))
-               : make_uint2(Elem<__half>::pack(x.x, x.y), Elem<__half>::pack(x.z, x.w));
-  };
-  if (tiles == 0) {
-    for (int i = tid; i < NC * V; i += 256) store(i / V, i % V, make_float4(0.f, 0.f, 0.f, 0.f));
-    return;
-  }
-  const Line line = line_of(total, p.grid);
-  const int64_t t0 = before + (int64_t)h * tiles;
-  const int c0 = (int)div_line(t0, line.share), n = (int)div_line(t0 + tiles - 1, line.share) - c0 + 1;
-  if (n == 1) return;  // written by the CTA that holds it
-  // partial i: the beginning in slot 1 of CTA c0, then slot 0 of the next ones
-  auto part = [&](int i, int col) {
-    const int z = col / width;
-    return (((size_t)z * p.grid + c0 + i) * 2 + (i == 0)) * width + (col - z * width);
-  };
-  {
-    const int col = tid >> 3, lane8 = tid & 7;  // eight lanes per column
-    float M = -INFINITY, den = 0.f;
-    if (col < NC)
-      for (int i = lane8; i < n; i += 8) M = fmaxf(M, __ldcg(p.part_m + part(i, col)));
+  float* po = reinterpret_cast<float*>(ring);
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(kAll, M, o));
-    if (M == -INFINITY) M = 0.f;  // no finite score: sums are zero or not numbers
-    if (col < NC)
-      for (int i = lane8; i < n; i += 8) den += ex2_approx(__ldcg(p.part_m + part(i, col)) - M) * __ldcg(p.part_l + part(i, col));
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int o = 4; o > 0; o >>= 1) den += __shfl_xor_sync(kAll, den, o);
-    if (lane8 == 0) {
-      s_max[col] = M;
-      s_inv[col] = den == 0.f ? 0.f : 1.f / den;  // a NaN sum stays one
+    for (int e = 0; e < 2; ++e) {
+      // the lane's D/8 elements of column n: D/8 g + 2 mt + {0, 1}
+      float4* dst = reinterpret_cast<float4*>(po + (nt * 8 + 2 * c4 + e) * L::ROW + (D / 8) * g);
+#pragma unroll
+      for (int i = 0; i < KSTEPS / 2; ++i)
+        dst[i] = make_float4(acc[nt][2 * i][e], acc[nt][2 * i][2 + e], acc[nt][2 * i + 1][e], acc[nt][2 * i + 1][2 + e]);
     }
-  }
   __syncthreads();
-  // few elements: the threads share the partials too, in runs, added up in order
-  const int elems = NC * V, runs = elems <= 64 ? 4 : elems <= 128 ? 2 : 1, per = (n + runs - 1) / runs;
-  for (int e0 = 0; e0 < elems; e0 += 256 / runs) {
-    const int e = e0 + tid / runs, run = tid % runs;
-    const int col = min(e, elems - 1) / V, v = min(e, elems - 1) % V;
-    const float M = s_max[col];
-    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int end = min(n, (run + 1) * per);
-    for (int i0 = run * per; i0 < end; i0 += CH) {
-      float4 x[CH];
-      float f[CH];
+  for (int i = threadIdx.x; i < ncols * (D / 4); i += kWarps * 32) {
+    const int n = i / (D / 4), d = 4 * (i % (D / 4));
+    float f[kWarps], M = -INFINITY;
 #pragma unroll
-      for (int k = 0; k < CH; ++k)
-        if (i0 + k < end) {
-          const size_t at = part(i0 + k, col);
-          x[k] = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D) + v);
-          f[k] = ex2_approx(__ldcg(p.part_m + at) - M);
-        }
+    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, f[w] = sums[w * NT * 8 + n]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+    const float ref = M == -INFINITY ? 0.f : M;  // no finite score: sums are zero or not numbers
 #pragma unroll
-      for (int k = 0; k < CH; ++k)
-        if (i0 + k < end) a.x += f[k] * x[k].x, a.y += f[k] * x[k].y, a.z += f[k] * x[k].z, a.w += f[k] * x[k].w;
+    for (int w = 0; w < kWarps; ++w) {
+      const float a = ex2_approx(f[w] - ref);
+      const float4 x = *reinterpret_cast<const float4*>(reinterpret_cast<const float*>(smem + w * L::WARP) + n * L::ROW + d);
+      o.x += a * x.x, o.y += a * x.y, o.z += a * x.z, o.w += a * x.w;
+      sum += a * sums[(kWarps + w) * NT * 8 + n];
     }
-    if (runs > 1) {
-      s_part[tid] = a;
-      __syncthreads();
-      if (run == 0)
-        for (int k = 1; k < runs; ++k) {
-          const float4 x = s_part[tid + k];
-          a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
-        }
-      __syncthreads();
-    }
-    if (run == 0 && e < elems) {
-      const float inv = s_inv[col];
-      store(col, v, make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv));
+    // a token behind causal0 that is not a number, for the columns that see it
+    const int nsee = min(max(min(tok1, ctx - (p.q_len - 1 - (col0 + n) / G)) - causal0, 0), 31);
+    if (nan[d / kKv4Group] & ((1u << nsee) - 1u)) o = make_float4(NAN, NAN, NAN, NAN);
+    const size_t row = row_of(col0 + n);
+    if (nsplit == 1) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a NaN sum stays one
+      o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + d) =
+          p.bf16 ? make_uint2(Elem<__nv_bfloat16>::pack(o.x, o.y), Elem<__nv_bfloat16>::pack(o.z, o.w))
+                 : make_uint2(Elem<__half>::pack(o.x, o.y), Elem<__half>::pack(o.z, o.w));
+    } else {
+      *reinterpret_cast<float4*>(p.part_o + (row * p.max_splits + c) * D + d) = o;
+      if (d == 0) {
+        p.part_m[row * p.max_splits + c] = M;
+        p.part_l[row * p.max_splits + c] = sum;
+      }
     }
   }
 }
 
 template <int D, int NT, int BS>
 cudaError_t launch_t(const Kv4DecodeParams& p, cudaStream_t stream) {
-  using L = Kv4DecodeSmem<D, NT, BS>;
-  static_assert(L::BYTES <= 47 * 1024, "no attribute needed");
-  const cudaError_t e = launch_pdl(kv4_decode_kernel<D, NT, BS>, dim3(p.grid, (p.group * p.q_len + NT * 8 - 1) / (NT * 8)),
-                                   dim3(kWarps * 32), L::BYTES, stream, p);
-  if (e != cudaSuccess) return e;
-  return launch_pdl(kv4_decode_merge_kernel<D>, dim3(p.kv_heads, p.num_seqs), dim3(256), 0, stream, p);
+  using L = Kv4DecodeSmem<D, NT>;
+  static_assert(L::bytes(kMaxEntries + 4) <= 48 * 1024, "no attribute needed");
+  const dim3 grid((unsigned)(p.max_splits * p.kv_heads), p.num_seqs, (p.group * p.q_len + NT * 8 - 1) / (NT * 8));
+  return launch_pdl(kv4_decode_kernel<D, NT, BS>, grid, dim3(kWarps * 32), L::bytes(p.tab_entries + 4), stream, p);
 }
 
 template <int D, int BS>
 cudaError_t launch_nt(const Kv4DecodeParams& p, cudaStream_t stream) {
-  return p.cols == 8 ? launch_t<D, 1, BS>(p, stream) : launch_t<D, 2, BS>(p, stream);
+  return p.group * p.q_len <= 8 ? launch_t<D, 1, BS>(p, stream) : launch_t<D, 2, BS>(p, stream);
 }
 
 template <int D>
@@ -702,26 +479,6 @@ cudaError_t launch_bs(const Kv4DecodeParams& p, cudaStream_t stream) {
 }
 
 }  // namespace
-
-// As many CTAs as run at a time (by registers 3 or 4 on a SM); fewer where the
-// tables hold less than kMinShare tiles for each.
-Kv4DecodePlan kv4_decode_plan(int num_seqs, int q_len, int kv_heads, int group, int head_dim, int64_t cap) {
-  Kv4DecodePlan w{};
-  w.cols = group * q_len <= 8 ? 8 : 16;
-  const int z = (group * q_len + w.cols - 1) / w.cols;
-  const int sms = num_sms() > 0 ? num_sms() : 1;
-  const int64_t slots = (int64_t)sms * (head_dim == 128 && w.cols == 16 ? 3 : 4) / z;
-  const int64_t most = (cap + kTile - 1) / kTile * num_seqs;  // of one head; below 2^47
-  const int64_t want = (most * kv_heads + kMinShare - 1) / kMinShare;
-  w.grid = (int)(want < 1 ? 1 : want < slots ? want : slots);
-  auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
-  const size_t parts = (size_t)w.grid * z * 2 * w.cols;
-  w.m_off = al(parts * head_dim * sizeof(float));
-  w.l_off = w.m_off + al(parts * sizeof(float));
-  w.before_off = w.l_off + al(parts * sizeof(float));
-  w.bytes = w.before_off + al(((size_t)num_seqs + 1) * sizeof(int64_t));
-  return w;
-}
 
 cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int head_dim, cudaStream_t stream) {
   return head_dim == 128 ? launch_bs<128>(p, stream) : launch_bs<64>(p, stream);

@@ -325,22 +325,16 @@ struct Kv4DecodeParams {
   const int32_t* tables;
   const int32_t* lens;
   void* out;
-  float* part_o;    // [column tile][CTA][2][cols][head_dim]
+  float* part_o;  // as DecodeParams
   float* part_m;
   float* part_l;
-  int64_t* before;  // [num_seqs + 1] tiles of the requests before each
   int* err;
-  int maxblk, cap, num_seqs, q_len, q_heads, kv_heads, group, num_blocks, block_size;
-  int grid, cols;   // of the plan
-  int bf16;         // q and out: bf16, or fp16
+  int maxblk, num_seqs, q_len, q_heads, kv_heads, group, num_blocks, block_size;
+  int split_tokens, max_splits, tab_entries;
+  int bf16;  // q and out: bf16, or fp16
   float scale_log2;
 };
-struct Kv4DecodePlan {
-  int grid, cols;  // CTAs of a column tile, columns of it
-  size_t m_off, l_off, before_off, bytes;
-};
-Kv4DecodePlan kv4_decode_plan(int num_seqs, int q_len, int kv_heads, int group, int head_dim, int64_t cap);
-// the merge included
+// without the merge (launch_lse_merge)
 cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int head_dim, cudaStream_t stream);
 
 // Chunked prefill over a 4-bit cache (kv4_prefill.cu): the merge included.

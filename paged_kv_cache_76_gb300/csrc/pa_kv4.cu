@@ -28,14 +28,40 @@ int check_kv4_shape(int num_blocks, int block_size, int kv_heads, int head_dim, 
 
 int log2_of(int bs) { return bs == 4 ? 2 : bs == 8 ? 3 : bs == 16 ? 4 : 5; }
 
-int check_kv4_decode(int num_seqs, int q_len, int q_heads, int kv_heads, int max_blocks_per_seq, int block_size) {
+constexpr int kKv4SplitUnit = 32;  // a stage of the kernel
+
+struct Kv4DecodeSetup {
+  int split, max_splits;
+  DecodeWorkspace ws;
+};
+
+int kv4_decode_setup(int num_seqs, int q_len, int q_heads, int kv_heads, int head_dim, int max_blocks_per_seq,
+                     int block_size, int split_tokens, Kv4DecodeSetup* s) {
   if (num_seqs < 0 || num_seqs > 65535 || q_len < 1 || q_len > 32 || q_heads <= 0 || kv_heads <= 0 || kv_heads > 1024 ||
-      q_heads % kv_heads != 0 || max_blocks_per_seq <= 0 || !block_size_ok(block_size))
+      q_heads % kv_heads != 0 || head_dim <= 0 || max_blocks_per_seq <= 0 || !block_size_ok(block_size))
     return PA_ERR_INVALID;
   const int group = q_heads / kv_heads;
   if (group > 16 || group * q_len > 32) return PA_ERR_INVALID;
-  // a request's tiles over all heads are counted in 32 bits
-  if ((int64_t)max_blocks_per_seq * block_size > 1 << 25) return PA_ERR_INVALID;
+  const int64_t cap = (int64_t)max_blocks_per_seq * block_size;
+  if (cap > INT32_MAX - 4096 || (int64_t)num_seqs * q_len * q_heads > INT32_MAX - 8) return PA_ERR_INVALID;
+  const int most = 1024 * block_size;
+  int64_t split = split_tokens;
+  if (split_tokens == 0) {
+    const int64_t sms = num_sms() > 0 ? num_sms() : 152;
+    const int64_t lists = (int64_t)num_seqs * kv_heads * ((group * q_len + 15) / 16);
+    const int64_t parts = lists > 0 ? (8 * sms + lists - 1) / lists : 1;
+    split = (cap + parts - 1) / parts;
+    if (split < 128) split = 128;
+    if (split > 4096) split = 4096;
+    split = (split + kKv4SplitUnit - 1) / kKv4SplitUnit * kKv4SplitUnit;
+    if (split > most) split = most;
+  }
+  if (split <= 0 || split % kKv4SplitUnit != 0 || split > most) return PA_ERR_INVALID;
+  s->split = (int)split;
+  s->max_splits = (int)((cap + split - 1) / split);
+  if ((int64_t)s->max_splits * kv_heads > INT32_MAX - 8) return PA_ERR_INVALID;
+  s->ws = s->max_splits > 1 ? decode_workspace_layout(num_seqs * q_len, q_heads, head_dim, s->max_splits)
+                            : DecodeWorkspace{0, 0, 0, 0};
   return PA_OK;
 }
 
@@ -144,58 +170,81 @@ int pa_dequantize_kv4(const void* k_cache, const void* v_cache, const int32_t* s
   return cuda_status(launch_dequantize_kv4(p, head_dim, dtype, to_stream(stream)));
 }
 
+int pa_decode_kv4_split_tokens(int num_seqs, int q_len, int q_heads, int kv_heads, int max_blocks_per_seq,
+                               int block_size, int split_tokens) {
+  Kv4DecodeSetup s;
+  const int st = kv4_decode_setup(num_seqs, q_len, q_heads, kv_heads, 64, max_blocks_per_seq, block_size, split_tokens, &s);
+  return st != PA_OK ? st : s.split;
+}
+
 size_t pa_decode_kv4_workspace_size(int num_seqs, int q_len, int q_heads, int kv_heads, int head_dim,
-                                    int max_blocks_per_seq, int block_size) {
-  if (check_kv4_decode(num_seqs, q_len, q_heads, kv_heads, max_blocks_per_seq, block_size) != PA_OK ||
-      (head_dim != 64 && head_dim != 128))
+                                    int max_blocks_per_seq, int block_size, int split_tokens) {
+  Kv4DecodeSetup s;
+  if (kv4_decode_setup(num_seqs, q_len, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size, split_tokens,
+                       &s) != PA_OK)
     return 0;
-  return kv4_decode_plan(num_seqs, q_len, kv_heads, q_heads / kv_heads, head_dim, (int64_t)max_blocks_per_seq * block_size)
-      .bytes;
+  return s.ws.bytes;
 }
 
 int pa_decode_kv4(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
                   int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int q_len, int q_heads,
-                  int kv_heads, int head_dim, int block_size, int num_blocks, float scale, void* workspace,
-                  size_t workspace_bytes, void* out, pa_dtype dtype, pa_stream stream) {
+                  int kv_heads, int head_dim, int block_size, int num_blocks, float scale, int split_tokens,
+                  void* workspace, size_t workspace_bytes, void* out, pa_dtype dtype, pa_stream stream) {
   int st = check_kv4_shape(num_blocks, block_size, kv_heads, head_dim, dtype);
   if (st != PA_OK) return st;
-  st = check_kv4_decode(num_seqs, q_len, q_heads, kv_heads, max_blocks_per_seq, block_size);
-  if (st != PA_OK) return st;
   if (!std::isfinite(scale)) return PA_ERR_INVALID;
+  Kv4DecodeSetup s;
+  st = kv4_decode_setup(num_seqs, q_len, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size, split_tokens, &s);
+  if (st != PA_OK) return st;
   if (num_seqs == 0) return PA_OK;
   if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out) return PA_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return PA_ERR_INVALID;
-  Kv4DecodeParams p{};
-  p.cap = max_blocks_per_seq * block_size;
-  p.group = q_heads / kv_heads;
-  const Kv4DecodePlan plan = kv4_decode_plan(num_seqs, q_len, kv_heads, p.group, head_dim, p.cap);
-  if (!workspace || workspace_bytes < plan.bytes || !aligned16(workspace)) return PA_ERR_WORKSPACE;
+  if (s.ws.bytes > 0 && (!workspace || workspace_bytes < s.ws.bytes || !aligned16(workspace)))
+    return PA_ERR_WORKSPACE;
   int* err = device_error_ptr();
   if (!err) return PA_ERR_CUDA;
-  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  Kv4DecodeParams p{};
   p.q = q;
   p.k_cache = k_cache;
   p.v_cache = v_cache;
   p.tables = block_tables;
   p.lens = context_lens;
   p.out = out;
-  p.part_o = reinterpret_cast<float*>(ws);
-  p.part_m = reinterpret_cast<float*>(ws + plan.m_off);
-  p.part_l = reinterpret_cast<float*>(ws + plan.l_off);
-  p.before = reinterpret_cast<int64_t*>(ws + plan.before_off);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (s.ws.bytes) {
+    p.part_o = reinterpret_cast<float*>(ws + s.ws.o_off);
+    p.part_m = reinterpret_cast<float*>(ws + s.ws.m_off);
+    p.part_l = reinterpret_cast<float*>(ws + s.ws.l_off);
+  }
   p.err = err;
   p.maxblk = max_blocks_per_seq;
   p.num_seqs = num_seqs;
   p.q_len = q_len;
   p.q_heads = q_heads;
   p.kv_heads = kv_heads;
+  p.group = q_heads / kv_heads;
   p.num_blocks = num_blocks;
   p.block_size = block_size;
-  p.grid = plan.grid;
-  p.cols = plan.cols;
+  p.split_tokens = s.split;
+  p.max_splits = s.max_splits;
+  p.tab_entries = s.split / block_size;
   p.bf16 = dtype == PA_BF16;
   p.scale_log2 = scale * 1.4426950408889634f;
-  return cuda_status(launch_kv4_decode(p, head_dim, to_stream(stream)));
+  st = cuda_status(launch_kv4_decode(p, head_dim, to_stream(stream)));
+  if (st != PA_OK || s.max_splits == 1) return st;
+  MergeParams mp{};
+  mp.part_o = p.part_o;
+  mp.part_m = p.part_m;
+  mp.part_l = p.part_l;
+  mp.lens = context_lens;
+  mp.out = out;
+  mp.num_seqs = num_seqs;
+  mp.q_heads = q_heads;
+  mp.max_splits = s.max_splits;
+  mp.split_tokens = s.split;
+  mp.cap = max_blocks_per_seq * block_size;
+  mp.q_len = q_len;
+  return cuda_status(launch_lse_merge(mp, head_dim, dtype, to_stream(stream)));
 }
 
 int pa_chunked_prefill_kv4_split_tokens(int num_reqs, int max_q_len, int q_heads, int kv_heads, int max_blocks_per_seq,

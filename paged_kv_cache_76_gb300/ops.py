@@ -51,6 +51,7 @@ __all__ = [
     "quantize_and_cache",
     "dequantize_kv4",
     "decode_kv4",
+    "decode_kv4_split_tokens",
     "decode_kv4_workspace_size",
     "chunked_prefill_kv4",
     "chunked_prefill_kv4_split_tokens",
@@ -945,9 +946,17 @@ def dequantize_kv4(k_cache, v_cache, slots, head_dim, dtype=torch.bfloat16, k=No
     return tuple(out)
 
 
-def decode_kv4_workspace_size(num_seqs, q_len, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size) -> int:
+def decode_kv4_split_tokens(num_seqs, q_len, q_heads, kv_heads, max_blocks_per_seq, block_size, split_tokens=0) -> int:
+    """Partition size such a pa_decode_kv4 call uses (0: its automatic choice)."""
+    return check(_lib.lib().pa_decode_kv4_split_tokens(int(num_seqs), int(q_len), int(q_heads), int(kv_heads),
+                                                       int(max_blocks_per_seq), int(block_size), int(split_tokens)),
+                 "pa_decode_kv4_split_tokens")
+
+
+def decode_kv4_workspace_size(num_seqs, q_len, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size,
+                              split_tokens=0) -> int:
     return int(_lib.lib().pa_decode_kv4_workspace_size(num_seqs, q_len, q_heads, kv_heads, head_dim,
-                                                       max_blocks_per_seq, block_size))
+                                                       max_blocks_per_seq, block_size, split_tokens))
 
 
 @functools.lru_cache(maxsize=4096)
@@ -964,7 +973,8 @@ def _scratch(workspace, n: int, device, dev: int, stream):
     return workspace, _ptr(workspace, "workspace", dev), workspace.numel() * workspace.element_size()
 
 
-def decode_kv4(q, k_cache, v_cache, block_tables, context_lens, scale, out=None, workspace=None, stream=None):
+def decode_kv4(q, k_cache, v_cache, block_tables, context_lens, scale, out=None, split_tokens=0, workspace=None,
+               stream=None):
     """pa_decode_kv4: :func:`decode` (``q`` [num_seqs, q_heads, head_dim]) or :func:`verify_decode` (``q`` [num_seqs,
     q_len, q_heads, head_dim]) over a 4-bit cache."""
     if q.dim() not in (3, 4):
@@ -980,12 +990,12 @@ def decode_kv4(q, k_cache, v_cache, block_tables, context_lens, scale, out=None,
     elif out.shape != qshape or out.dtype != dtype:
         raise ValueError("out must have q's shape, dtype and device")
     handle = _stream_on(dev, stream)
-    maxblk = block_tables.shape[1]
-    n = _kv4_workspace(dev, B, ql, hq, hkv, d, maxblk, bs) if workspace is None else 0
+    maxblk, split_tokens = block_tables.shape[1], int(split_tokens)
+    n = _kv4_workspace(dev, B, ql, hq, hkv, d, maxblk, bs, split_tokens) if workspace is None else 0
     workspace, ws_ptr, ws_bytes = _scratch(workspace, n, q.device, dev, stream)
     _keep(out, workspace)
     _launch("pa_decode_kv4", _ptr(q, "q", dev), kc, vc, tables, maxblk, lens, B, ql, hq, hkv, d, bs, nb, float(scale),
-            ws_ptr, ws_bytes, _ptr(out, "out", dev), code, handle)
+            split_tokens, ws_ptr, ws_bytes, _ptr(out, "out", dev), code, handle)
     return out
 
 
