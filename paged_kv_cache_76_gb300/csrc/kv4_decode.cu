@@ -23,10 +23,11 @@
 //
 // Per 16 tokens (m16n8k16, S^T = K Q^T and O^T += V^T P^T):
 //   K: lane (g, c) = (lane / 4, lane % 4) holds D/4 consecutive elements of
-//      tokens g and g + 8, D/16 A fragments of both; which elements a fragment
-//      takes is free as long as Q's B fragments take the same.
+//      tokens pi(g) and pi(g) + 8, D/16 A fragments of both; which elements a
+//      fragment takes is free as long as Q's B fragments take the same.
 //   V: lane (g, c) holds D/8 elements of the four tokens that P's B fragments
-//      hold for it, 2c, 2c + 1 and those + 8.  An A fragment wants two tokens
+//      hold for it, pi(2c) = c, pi(2c + 1) = c + 4 and those + 8 (so that a
+//      load's lanes have rows of either parity).  An A fragment wants two tokens
 //      side by side, so the codes of two tokens are interleaved before they are
 //      converted (four logical instructions for 16 elements, where 16 fp16 pairs
 //      would take 16).
@@ -70,6 +71,37 @@ struct Kv4DecodeSmem {
   static constexpr int bytes(int entries) { return TAB_OFF + entries * 4; }
 };
 
+// Shared memory at an address and a constant, after the wait that orders them
+// (volatile: they stay behind it).
+__device__ __forceinline__ uint4 lds4(uint32_t at, int off) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at + off));
+  return v;
+}
+__device__ __forceinline__ uint2 lds2(uint32_t at, int off) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at + off));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds1(uint32_t at, int off) {
+  uint32_t v;
+  asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at + off));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u16(uint32_t at, int off) {
+  uint32_t v;
+  asm volatile("{\n .reg .u16 t;\n ld.shared.u16 t, [%1];\n cvt.u32.u16 %0, t;\n}" : "=r"(v) : "r"(at + off));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds_u8(uint32_t at, int off) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at + off));
+  return v;
+}
+__device__ __forceinline__ void cp_async16_at(uint32_t dst, int off, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + off), "l"(src) : "memory");
+}
+
 template <int D, int NT, int BS>
 __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_decode_kernel(const Kv4DecodeParams p) {
   using L = Kv4DecodeSmem<D, NT>;
@@ -111,9 +143,17 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
     return (size_t)(r * p.q_len + qi) * p.q_heads + qh0 + (n - qi * G);
   };
 
+  // Q^T as the B operand: lane (g, c) holds column g of each n-tile, elements
+  // D/4 c + 4 ks + {0, 1} and {2, 3}
+  uint2 raw[KSTEPS];
+  auto load_q = [&](int nt) {
+    const int n = col0 + nt * 8 + g;
+    const uint2* q2 = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + (n < NC ? row_of(n) : 0) * D + (D / 4) * c4);
+#pragma unroll
+    for (int ks = 0; ks < KSTEPS; ++ks) raw[ks] = n < NC ? __ldg(q2 + ks) : make_uint2(0u, 0u);
+  };
+  if (NT == 1) load_q(0);  // beside the table; more columns would take too many registers that long
   bool bad_id = false;
-  uint32_t qf[NT][KSTEPS][2];
-  float sl2[NT][2];  // softmax scale (log2 units) of the lane's two columns of each n-tile
   {
     const int nblk = (tok1 - tok0 + BS - 1) / BS;
     const int entries = (ntiles * kTile + BS - 1) / BS;
@@ -127,45 +167,6 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
       if (i < entries) tab[i] = bad ? 0 : b;
       bad_id |= bad;
     }
-    // Q^T as the B operand: lane (g, c) holds column g of each n-tile, elements
-    // D/4 c + 4 ks + {0, 1} and {2, 3}
-    auto load_q = [&](auto type) {
-      using T = decltype(type);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int n = col0 + nt * 8 + g;
-        const uint2* src = reinterpret_cast<const uint2*>(static_cast<const T*>(p.q) + (n < NC ? row_of(n) : 0) * D + (D / 4) * c4);
-        float x[KSTEPS][4];
-        float top = 0.f;
-#pragma unroll
-        for (int ks = 0; ks < KSTEPS; ++ks) {
-          const uint2 w = n < NC ? __ldg(src + ks) : make_uint2(0u, 0u);
-          x[ks][0] = Elem<T>::lo(w.x), x[ks][1] = Elem<T>::hi(w.x);
-          x[ks][2] = Elem<T>::lo(w.y), x[ks][3] = Elem<T>::hi(w.y);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(x[ks][e]));
-        }
-        top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
-        // 2^e <= top < 2^(e + 1); rows of zeros and of values that are not finite stay as they are
-        int e = top > 0.f && top < INFINITY ? ilogbf(top) - 13 : 0;
-        e = max(e, -126);
-        const float down = ldexpf(1.f, -e);
-#pragma unroll
-        for (int ks = 0; ks < KSTEPS; ++ks) {
-          qf[nt][ks][0] = Elem<__half>::pack(x[ks][0] * down, x[ks][1] * down);
-          qf[nt][ks][1] = Elem<__half>::pack(x[ks][2] * down, x[ks][3] * down);
-        }
-        const float back = p.scale_log2 * ldexpf(1.f, e);
-        // accumulators hold columns 2c, 2c + 1 of the tile
-        sl2[nt][0] = __shfl_sync(kAll, back, 8 * c4);
-        sl2[nt][1] = __shfl_sync(kAll, back, 8 * c4 + 4);
-      }
-    };
-    if (ntiles > 0) {
-      if (p.bf16) load_q(__nv_bfloat16{});
-      else load_q(__half{});
-    }
   }
   griddep_wait();
   if (bad_len && threadIdx.x == 0) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
@@ -178,50 +179,105 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
   }
   const bool any_bad = __syncthreads_or(bad_id);  // and the table is complete
 
+  // Where this lane's elements are in a tile: K of token pi(g) (+ 8), V of c and c + 4 (+ 8)
+  auto code_at = [](int t) { return BS < kTile ? t / BS * PAGE + t % BS * R::CODES : t * R::CODES; };
+  auto scale_at = [](int t) {
+    return BS < kTile ? t / BS * PAGE + BS * R::CODES + t % BS * R::SCALES : kTile * R::CODES + t * R::SCALES;
+  };
+  constexpr int VOFF = kTile * R::BYTES;
+  const int pg = (g >> 1) + 4 * (g & 1);
+  constexpr int CODE4 = BS < 8 ? PAGE : 4 * R::CODES, SCALE4 = BS < 8 ? PAGE : 4 * R::SCALES;  // to the token 4 behind
+  constexpr int CODE8 = BS < kTile ? 8 / BS * PAGE : 8 * R::CODES, SCALE8 = BS < kTile ? 8 / BS * PAGE : 8 * R::SCALES;
+  const uint32_t ring_at = smem_u32(smem + warp * L::WARP);
+  const uint32_t kcode = ring_at + code_at(pg) + c4 * (4 * NW), kscale = ring_at + scale_at(pg) + c4 * (NW / 2);
+  const uint32_t vcode = ring_at + VOFF + code_at(c4) + g * (D / 16);
+  const uint32_t vscale = ring_at + VOFF + scale_at(c4) + (D == 128 ? g : g >> 1);
   // A tile is 2 * R::BYTES vectors of 16 bytes, K's and then V's, copied as they
   // are in the pages (of blocks of 32: the tile's half of the codes, then of the
   // scales); this lane copies vectors lane, lane + 32, ...
   constexpr int VECS = R::BYTES, SLOTS = (2 * VECS + 31) / 32;
   constexpr int PV = BS < kTile ? PAGE / 16 : VECS;  // vectors of a page in a tile
   uint8_t* ring = smem + warp * L::WARP;
-  const uint32_t ring0 = smem_u32(ring) + 16 * lane;
+  const uint32_t ring0 = ring_at + 16 * lane;
   const uint32_t block_bytes = (uint32_t)p.kv_heads * PAGE;
-  const uint8_t* src[SLOTS];
+  // Where the lane's vectors are in a block.  Of blocks of 16 a tile is a run of
+  // K's bytes and one of V's: two addresses and constants.
+  constexpr bool RUN = BS == kTile;
+  const uint8_t* src[RUN ? 2 : SLOTS];
+  if constexpr (RUN) {
+    src[0] = static_cast<const uint8_t*>(p.k_cache) + (int64_t)h * PAGE + 16 * lane;
+    src[1] = static_cast<const uint8_t*>(p.v_cache) + (int64_t)h * PAGE + 16 * lane - 16 * VECS;
+  } else {
 #pragma unroll
-  for (int q = 0; q < SLOTS; ++q) {
-    const int id = lane + 32 * q, i = id % VECS;
-    const int codes = kTile * R::CODES / 16;  // vectors of them, blocks of 32
-    const int at = BS <= kTile || i < codes ? (i % PV) * 16 : BS * R::CODES + (i - codes) * 16;
-    src[q] = static_cast<const uint8_t*>(id < VECS ? p.k_cache : p.v_cache) + (int64_t)h * PAGE + at;
+    for (int q = 0; q < SLOTS; ++q) {
+      const int id = lane + 32 * q, i = id % VECS;
+      const int codes = kTile * R::CODES / 16;  // vectors of them, blocks of 32
+      const int off = BS <= kTile || i < codes ? (i % PV) * 16 : BS * R::CODES + (i - codes) * 16;
+      src[q] = static_cast<const uint8_t*>(id < VECS ? p.k_cache : p.v_cache) + (int64_t)h * PAGE + off;
+    }
   }
   // entry of the table that holds a token of tile j
   auto entry = [](int j, int token) { return BS >= kTile ? j * kTile / BS : j * (kTile / BS) + token / BS; };
-  auto issue = [&](int i) {  // the warp's i-th tile
-    const int j = warp + i * kWarps;
+  auto issue = [&](int j, uint32_t slot) {  // tile j of the CTA to a place of the ring
     if (j < ntiles) {
-      const uint32_t dst = ring0 + (uint32_t)(i % kDepth) * L::TILE;
+      const uint32_t dst = ring0 + slot * L::TILE;
+      const uint32_t block = (uint32_t)tab[entry(j, 0)];  // the only one, of blocks of 16 and 32
+      const uint64_t at_block = (uint64_t)block * block_bytes;
+      const uint8_t* kv[2];
+      if constexpr (RUN) kv[0] = src[0] + at_block, kv[1] = src[1] + at_block;
 #pragma unroll
       for (int q = 0; q < SLOTS; ++q) {
         const int id = lane + 32 * q, v = id % VECS;
-        const uint8_t* s = src[q] + (uint64_t)(uint32_t)tab[entry(j, v / PV * BS)] * block_bytes;
-        if (BS > kTile) s += (j * kTile & (BS - 1)) * (v < kTile * R::CODES / 16 ? R::CODES : R::SCALES);
-        if (32 * q + 32 <= 2 * VECS || id < 2 * VECS) cp_async16(dst + 512 * q, s, 16);
+        const uint8_t* s;
+        if constexpr (RUN) {
+          s = (32 * q + 32 <= VECS ? kv[0] : 32 * q >= VECS ? kv[1] : id < VECS ? kv[0] : kv[1]) + 512 * q;
+        } else {
+          s = src[q] + (BS > kTile ? at_block : (uint64_t)(uint32_t)tab[entry(j, v / PV * BS)] * block_bytes);
+          if (BS > kTile) s += (j * kTile & (BS - 1)) * (v < kTile * R::CODES / 16 ? R::CODES : R::SCALES);
+        }
+        if (32 * q + 32 <= 2 * VECS || id < 2 * VECS) cp_async16_at(dst, 512 * q, s);
       }
     }
     cp_async_commit();
   };
-  // Where this lane's elements are in a tile: K of token pi(g) (+ 8), V of pi(2c), pi(2c + 1) (+ 8)
-  auto code_at = [](int t) { return BS < kTile ? t / BS * PAGE + t % BS * R::CODES : t * R::CODES; };
-  auto scale_at = [](int t) {
-    return BS < kTile ? t / BS * PAGE + BS * R::CODES + t % BS * R::SCALES : kTile * R::CODES + t * R::SCALES;
+#pragma unroll
+  for (int i = 0; i < kDepth - 1; ++i) issue(warp + i * kWarps, i);
+  uint32_t slot = 0;
+
+  uint32_t qf[NT][KSTEPS][2];
+  float sl2[NT][2];  // softmax scale (log2 units) of the lane's two columns of each n-tile
+  auto convert_q = [&](auto type) {
+    using T = decltype(type);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      if (NT > 1) load_q(nt);
+      float top = 0.f;
+#pragma unroll
+      for (int ks = 0; ks < KSTEPS; ++ks) {
+        const uint2 w = raw[ks];
+        top = fmaxf(top, fmaxf(fmaxf(fabsf(Elem<T>::lo(w.x)), fabsf(Elem<T>::hi(w.x))),
+                               fmaxf(fabsf(Elem<T>::lo(w.y)), fabsf(Elem<T>::hi(w.y)))));
+      }
+      top = fmaxf(top, __shfl_xor_sync(kAll, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kAll, top, 2));
+      // 2^e <= top < 2^(e + 1); rows of zeros and of values that are not finite stay as they are
+      int e = (int)(__float_as_uint(top) >> 23) - 127;  // of a subnormal -127: it is brought up less
+      e = top > 0.f && top < INFINITY ? max(e - 13, -126) : 0;
+      const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+      for (int ks = 0; ks < KSTEPS; ++ks) {
+        const uint2 w = raw[ks];
+        qf[nt][ks][0] = Elem<__half>::pack(Elem<T>::lo(w.x) * down, Elem<T>::hi(w.x) * down);
+        qf[nt][ks][1] = Elem<__half>::pack(Elem<T>::lo(w.y) * down, Elem<T>::hi(w.y) * down);
+      }
+      const float back = p.scale_log2 * __uint_as_float((uint32_t)(127 + e) << 23);
+      // accumulators hold columns 2c, 2c + 1 of the tile
+      sl2[nt][0] = __shfl_sync(kAll, back, 8 * c4);
+      sl2[nt][1] = __shfl_sync(kAll, back, 8 * c4 + 4);
+    }
   };
-  constexpr int VOFF = kTile * R::BYTES;
-  const int pg = g ^ (g >> 1 & 1);
-  const int t01[2] = {2 * c4 ^ (c4 & 1), (2 * c4 + 1) ^ (c4 & 1)};
-  const int kcode = code_at(pg) + c4 * (4 * NW), kscale = scale_at(pg) + c4 * (NW / 2);
-  const int vcode[2] = {VOFF + code_at(t01[0]) + g * (D / 16), VOFF + code_at(t01[1]) + g * (D / 16)};
-  const int vscale[2] = {VOFF + scale_at(t01[0]) + (D == 128 ? g : g >> 1), VOFF + scale_at(t01[1]) + (D == 128 ? g : g >> 1)};
-  constexpr int CODE8 = BS < kTile ? 8 / BS * PAGE : 8 * R::CODES, SCALE8 = BS < kTile ? 8 / BS * PAGE : 8 * R::SCALES;
+  if (p.bf16) convert_q(__nv_bfloat16{});  // while the first tiles come
+  else convert_q(__half{});
 
   float m[NT][2], l[NT][2], acc[NT][KSTEPS][4];
   int lim[NT][2];  // tokens [0, lim) are visible to the lane's columns
@@ -240,7 +296,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
   const int causal0 = ctx - (p.q_len - 1);  // tokens from here on are hidden from some query (q_len 1: from ctx on)
 
   // 16 tokens from ts on; `all`: every column sees all of them
-  auto compute = [&](const uint8_t* x, const int j, const auto all_t) {
+  auto compute = [&](const uint32_t x, const int j, const auto all_t) {  // x: the tile's place in the ring
     constexpr bool all = decltype(all_t)::value;
     const int ts = tok0 + j * kTile;
     auto bad_block = [&](int token) {
@@ -256,13 +312,13 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       if constexpr (NW == 4) {
-        const uint4 w = *reinterpret_cast<const uint4*>(x + kcode + e * CODE8);
+        const uint4 w = lds4(x + kcode, e * CODE8);
         kw[e][0] = w.x, kw[e][1] = w.y, kw[e][2] = w.z, kw[e][3] = w.w;
-        ks[e] = *reinterpret_cast<const uint16_t*>(x + kscale + e * SCALE8);
+        ks[e] = lds_u16(x + kscale, e * SCALE8);
       } else {
-        const uint2 w = *reinterpret_cast<const uint2*>(x + kcode + e * CODE8);
+        const uint2 w = lds2(x + kcode, e * CODE8);
         kw[e][0] = w.x, kw[e][1] = w.y;
-        ks[e] = x[kscale + e * SCALE8];
+        ks[e] = lds_u8(x + kscale, e * SCALE8);
       }
     }
 #pragma unroll
@@ -329,63 +385,65 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
       pb1[nt] = movmatrix_trans(Elem<__half>::pack(p2, p3));
     }
 
-    uint32_t y[2][D / 16][2];  // [e][element pair][element of it]: two tokens each
+    uint32_t vs2[2];  // scales of the two tokens of each pair
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      uint32_t vs[2], va[2][D / 64];
+      uint32_t vs[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        vs[i] = x[vscale[i] + e * SCALE8];
-        if constexpr (D == 128) {
-          const uint2 w = *reinterpret_cast<const uint2*>(x + vcode[i] + e * CODE8);
-          va[i][0] = w.x, va[i][1] = w.y;
-        } else {
-          va[i][0] = *reinterpret_cast<const uint32_t*>(x + vcode[i] + e * CODE8);
-        }
-      }
-      if constexpr (!all) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const int t = ts + t01[i] + 8 * e;
+        vs[i] = lds_u8(x + vscale, e * SCALE8 + i * SCALE4);
+        if constexpr (!all) {
+          const int t = ts + c4 + 4 * i + 8 * e;
           if (t >= causal0 && t < tok1 && vs[i] >= kKv4FirstInf) {
             vs[i] = 0;
             atomicOr(&nan[D == 128 ? g : g >> 1], 1u << (t - causal0));
           }
-          if (t >= tok1 || bad_block(t01[i] + 8 * e)) vs[i] = 0;
+          if (t >= tok1 || bad_block(c4 + 4 * i + 8 * e)) vs[i] = 0;
         }
       }
-      const uint32_t s2 = kv4_scale_pair(vs[0], vs[1]);
+      vs2[e] = kv4_scale_pair(vs[0], vs[1]);
+    }
+    uint32_t va[2][2][D / 64];  // [e][token of the pair]
 #pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        const uint32_t a = va[0][i], b = va[1][i];
-        const uint32_t lo = (a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u);
-        const uint32_t hi = ((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u);
-        uint32_t u[4], z[4];
-        kv4_unpack(lo, u);
-        kv4_unpack(hi, z);
+    for (int e = 0; e < 2; ++e)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if constexpr (D == 128) {
+          const uint2 w = lds2(x + vcode, e * CODE8 + i * CODE4);
+          va[e][i][0] = w.x, va[e][i][1] = w.y;
+        } else {
+          va[e][i][0] = lds1(x + vcode, e * CODE8 + i * CODE4);
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      uint32_t u[2][4], z[2][4];  // even and odd elements of the word, two tokens each
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const uint32_t a = va[e][0][i], b = va[e][1][i];
+        kv4_unpack((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), u[e]);
+        kv4_unpack(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), z[e]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          y[e][4 * i + k][0] = hmul2_u(u[k], s2);
-          y[e][4 * i + k][1] = hmul2_u(z[k], s2);
+          u[e][k] = hmul2_u(u[e][k], vs2[e]);
+          z[e][k] = hmul2_u(z[e][k], vs2[e]);
         }
       }
-    }
 #pragma unroll
-    for (int mt = 0; mt < KSTEPS; ++mt) {
-      const uint32_t a[4] = {y[0][mt][0], y[0][mt][1], y[1][mt][0], y[1][mt][1]};
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t a[4] = {u[0][k], z[0][k], u[1][k], z[1][k]};
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) mma_16816<__half>(acc[nt][mt], a, pb0[nt], pb1[nt]);
+        for (int nt = 0; nt < NT; ++nt) mma_16816<__half>(acc[nt][4 * i + k], a, pb0[nt], pb1[nt]);
+      }
     }
   };
 
   const int nfull = any_bad ? 0 : min(max(min(tok1, causal0) - tok0, 0) / kTile, ntiles);  // seen whole by every column
-  for (int i = 0; i < kDepth - 1; ++i) issue(i);
-  int slot = 0;
-  for (int i = 0, j = warp; j < ntiles; ++i, j += kWarps) {
+  for (int j = warp; j < ntiles; j += kWarps) {
     cp_async_wait<kDepth - 2>();
-    __syncwarp();  // every lane's part of tile i is there, and every lane is done with tile i - 1
-    issue(i + kDepth - 1);
-    const uint8_t* x = ring + slot * L::TILE;
+    __syncwarp();  // every lane's part of tile j is there, and every lane is done with the one before
+    issue(j + (kDepth - 1) * kWarps, slot == 0 ? kDepth - 1 : slot - 1);
+    const uint32_t x = slot * L::TILE;
     slot = slot + 1 == kDepth ? 0 : slot + 1;
     if (j < nfull) compute(x, j, std::true_type{});
     else compute(x, j, std::false_type{});
