@@ -1,7 +1,8 @@
 // The short way from torch tensors to the calls whose GPU time is a few
 // microseconds: a Python extension that checks and passes the arguments of
 // pa_norm_rope_and_cache, pa_verify_tree, pa_decode_accumulate,
-// pa_evict_select and pa_compact_kv and allocates their outputs and scratch.
+// pa_evict_select, pa_compact_kv, the calls of the 4-bit cache, pa_fork_blocks
+// and pa_copy_pages and allocates their outputs and scratch.
 //
 // It takes regular calls only: plain tensors on the current device, of the
 // documented types and shapes, on the current stream.  For anything else a
@@ -39,6 +40,15 @@ struct {
   decltype(&pa_decode_accumulate) accumulate;
   decltype(&pa_evict_select) evict_select;
   decltype(&pa_compact_kv) compact;
+  decltype(&pa_quantize_and_cache) quantize;
+  decltype(&pa_dequantize_kv4) dequantize;
+  decltype(&pa_decode_kv4_workspace_size) decode4_workspace;
+  decltype(&pa_decode_kv4) decode4;
+  decltype(&pa_chunked_prefill_kv4_workspace_size) prefill4_workspace;
+  decltype(&pa_chunked_prefill_kv4) prefill4;
+  decltype(&pa_fork_blocks_workspace_size) fork_workspace;
+  decltype(&pa_fork_blocks) fork;
+  decltype(&pa_copy_pages) copy_pages;
 } pa;
 
 // One call's arguments: every function returns a value that may only be used
@@ -131,6 +141,50 @@ Scores scores(Call& c, const at::Tensor* t, int hkv, PyObject* rows, int num_seq
   return s;
 }
 
+// of the tokens of [T][heads][d], whose heads are contiguous
+int64_t token_stride(Call& c, const at::Tensor* t, int T, int heads, int d, at::ScalarType type) {
+  const int64_t row = (int64_t)heads * d;
+  if (!c.need(t->scalar_type() == type && t->dim() == 3 && t->size(0) == T && t->size(1) == heads && t->size(2) == d))
+    return 0;
+  int64_t s = row;
+  if (!t->is_contiguous()) {
+    c.need(t->stride(2) == 1 && (heads <= 1 || t->stride(1) == d));
+    if (T > 1) s = t->stride(0);
+  }
+  c.need(s >= row && s % 8 == 0);
+  return s;
+}
+
+// two 4-bit caches of one shape, for heads of d elements
+Caches kv4_caches(Call& c, PyObject* ko, PyObject* vo, int64_t d, bool names_device) {
+  Caches r;
+  const at::Tensor* k = names_device ? c.first(ko) : c.tensor(ko);
+  const at::Tensor* v = c.tensor(vo);
+  if (!c.ok || !c.need((d == 64 || d == 128) && k->dim() == 3 && v->sizes() == k->sizes() &&
+                       k->scalar_type() == at::kByte && v->scalar_type() == at::kByte))
+    return r;
+  const int64_t bs = k->size(2) * 16 / (9 * d);
+  c.need(bs * 9 * d == k->size(2) * 16 && (bs == 4 || bs == 8 || bs == 16 || bs == 32));
+  r.nb = c.size(k, 0), r.bs = (int)bs, r.hkv = c.size(k, 1), r.d = (int)d;
+  r.k = c.ptr(k), r.v = c.ptr(v);
+  return r;
+}
+
+// the type of q and of what comes with it
+pa_dtype half_type(Call& c, const at::Tensor* t) {
+  if (!c.ok) return PA_BF16;
+  c.need(t->scalar_type() == at::kBFloat16 || t->scalar_type() == at::kHalf);
+  return t->scalar_type() == at::kHalf ? PA_FP16 : PA_BF16;
+}
+
+// `o` as the output of q's shape and type, or none
+at::Tensor given(Call& c, PyObject* o, const at::Tensor* q) {
+  if (o == Py_None) return {};
+  const at::Tensor* t = c.tensor(o);
+  if (c.ok && c.need(t->sizes() == q->sizes() && t->scalar_type() == q->scalar_type()) && c.ptr(t), c.ok) return *t;
+  return {};
+}
+
 pa_stream current_stream(int64_t dev) {
   return reinterpret_cast<pa_stream>(c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)dev).stream());
 }
@@ -169,17 +223,7 @@ PyObject* norm_rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor *q = c.tensor(a[0]), *k = c.tensor(a[1]), *v = c.tensor(a[2]);
   if (!c.ok || !c.need(q->dim() == 3 && k->dim() == 3 && v->dim() == 3 && q->size(2) == kv.d)) Py_RETURN_NONE;
   const int T = c.size(q, 0), hq = c.size(q, 1);
-  auto stride = [&](const at::Tensor* t, int heads) -> int64_t {  // of the tokens, whose heads are contiguous
-    const int64_t row = (int64_t)heads * kv.d;
-    if (!c.need(t->scalar_type() == kv.type && t->size(0) == T && t->size(1) == heads && t->size(2) == kv.d)) return 0;
-    int64_t s = row;
-    if (!t->is_contiguous()) {
-      c.need(t->stride(2) == 1 && (heads <= 1 || t->stride(1) == kv.d));
-      if (T > 1) s = t->stride(0);
-    }
-    c.need(s >= row && s % 8 == 0);
-    return s;
-  };
+  auto stride = [&](const at::Tensor* t, int heads) { return token_stride(c, t, T, heads, kv.d, kv.type); };
   const int64_t qs = stride(q, hq), ks = stride(k, kv.hkv), vs = stride(v, kv.hkv);
   const at::Tensor *pos = c.tensor(a[3]), *table = c.tensor(a[4]);
   if (!c.ok || !c.need(pos->scalar_type() == at::kInt && (pos->dim() == 1 || pos->dim() == 2) &&
@@ -369,6 +413,199 @@ PyObject* compact_kv(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return PyLong_FromLong(st);
 }
 
+// (k, v, slot_mapping, k_cache, v_cache) -> PA_OK's 0, a status
+PyObject* quantize_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 5) Py_RETURN_NONE;
+  Call c;
+  const at::Tensor *k = c.first(a[0]), *v = c.tensor(a[1]);
+  if (!c.ok || !c.need(k->dim() == 3)) Py_RETURN_NONE;
+  const pa_dtype dtype = half_type(c, k);
+  const int T = c.size(k, 0);
+  const Caches kv = kv4_caches(c, a[3], a[4], k->size(2), false);
+  if (!c.ok) Py_RETURN_NONE;
+  const int64_t ks = token_stride(c, k, T, kv.hkv, kv.d, k->scalar_type());
+  const int64_t vs = token_stride(c, v, T, kv.hkv, kv.d, k->scalar_type());
+  const int32_t* slots = c.rows(a[2], T);
+  const void *kp = c.here(k), *vp = c.here(v);
+  if (!c.ok) Py_RETURN_NONE;
+  int st = PA_OK;
+  if (!run([&] {
+        st = pa.quantize(kp, vp, ks, vs, slots, T, kv.k, kv.v, kv.nb, kv.bs, kv.hkv, kv.d, dtype, current_stream(c.dev));
+      }))
+    Py_RETURN_NONE;
+  return PyLong_FromLong(st);
+}
+
+// (k_cache, v_cache, slots, head_dim, pa_dtype)
+PyObject* dequantize_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 5) Py_RETURN_NONE;
+  Call c;
+  const int d = c.integer(a[3]), dtype = c.integer(a[4]);
+  const Caches kv = kv4_caches(c, a[0], a[1], d, true);
+  const at::Tensor* slots = c.tensor(a[2]);
+  if (!c.ok || !c.need(slots->dim() == 1 && (dtype == PA_FP16 || dtype == PA_BF16))) Py_RETURN_NONE;
+  const int T = c.size(slots, 0);
+  const int32_t* sp = c.rows(a[2], T);
+  if (!c.ok) Py_RETURN_NONE;
+  at::Tensor k, v;
+  int st = PA_OK;
+  if (!run([&] {
+        const auto opt = slots->options().dtype(dtype == PA_FP16 ? at::kHalf : at::kBFloat16);
+        k = at::empty({T, kv.hkv, d}, opt);
+        v = at::empty({T, kv.hkv, d}, opt);
+        st = pa.dequantize(kv.k, kv.v, sp, T, kv.nb, kv.bs, kv.hkv, d, k.data_ptr(), v.data_ptr(), (pa_dtype)dtype,
+                           current_stream(c.dev));
+      }))
+    Py_RETURN_NONE;
+  if (st != PA_OK) return PyLong_FromLong(st);
+  PyObject *ko = give(k), *vo = ko ? give(v) : nullptr;
+  PyObject* r = ko && vo ? PyTuple_Pack(2, ko, vo) : nullptr;
+  Py_XDECREF(ko);
+  Py_XDECREF(vo);
+  return r;
+}
+
+// (q, k_cache, v_cache, block_tables, context_lens, scale, out, split_tokens)
+PyObject* decode_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 8) Py_RETURN_NONE;
+  Call c;
+  const at::Tensor *q = c.first(a[0]), *table = c.tensor(a[3]);
+  if (!c.ok || !c.need((q->dim() == 3 || q->dim() == 4) && table->dim() == 2)) Py_RETURN_NONE;
+  const pa_dtype dtype = half_type(c, q);
+  const int last = (int)q->dim() - 1;
+  const Caches kv = kv4_caches(c, a[1], a[2], q->size(last), false);
+  const int B = c.size(q, 0), ql = last == 2 ? 1 : c.size(q, 1), hq = c.size(q, last - 1), maxblk = c.size(table, 1);
+  const int32_t *tp = c.rows(a[3], B), *lp = c.rows(a[4], B);
+  const void* qp = c.ptr(q);
+  const float scale = c.real(a[5]);
+  const int split = c.integer(a[7]);
+  at::Tensor out = given(c, a[6], q), ws;
+  if (!c.ok) Py_RETURN_NONE;
+  const bool mine = !out.defined();
+  int st = PA_OK;
+  if (!run([&] {
+        if (mine) out = at::empty(q->sizes(), q->options());
+        const size_t bytes = pa.decode4_workspace(B, ql, hq, kv.hkv, kv.d, maxblk, kv.bs, split);
+        if (bytes) ws = at::empty({(int64_t)bytes}, q->options().dtype(at::kByte));
+        st = pa.decode4(qp, kv.k, kv.v, tp, maxblk, lp, B, ql, hq, kv.hkv, kv.d, kv.bs, kv.nb, scale, split,
+                        bytes ? ws.data_ptr() : nullptr, bytes, out.data_ptr(), dtype, current_stream(c.dev));
+      }))
+    Py_RETURN_NONE;
+  if (st != PA_OK) return PyLong_FromLong(st);
+  return mine ? give(out) : Py_NewRef(a[6]);
+}
+
+// (q, q_start, context_lens, k_cache, v_cache, block_tables, scale, max_q_len, out, split_tokens)
+PyObject* chunked_prefill_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 10) Py_RETURN_NONE;
+  Call c;
+  const at::Tensor *q = c.first(a[0]), *lens = c.tensor(a[2]), *table = c.tensor(a[5]);
+  if (!c.ok || !c.need(q->dim() == 3 && lens->dim() >= 1 && table->dim() == 2)) Py_RETURN_NONE;
+  const pa_dtype dtype = half_type(c, q);
+  const Caches kv = kv4_caches(c, a[3], a[4], q->size(2), false);
+  const int T = c.size(q, 0), hq = c.size(q, 1), R = c.size(lens, 0), maxblk = c.size(table, 1);
+  c.need(R < INT_MAX);
+  const int32_t *lp = c.rows(a[2], R), *sp = c.rows(a[1], c.ok ? R + 1 : 0), *tp = c.rows(a[5], R);
+  const void* qp = c.ptr(q);
+  const float scale = c.real(a[6]);
+  const int max_q = c.integer(a[7]), split = c.integer(a[9]);
+  at::Tensor out = given(c, a[8], q), ws;
+  if (!c.ok) Py_RETURN_NONE;
+  const bool mine = !out.defined();
+  int st = PA_OK;
+  if (!run([&] {
+        if (mine) out = at::empty(q->sizes(), q->options());
+        const size_t bytes = pa.prefill4_workspace(R, T, max_q, hq, kv.hkv, kv.d, maxblk, kv.bs, split);
+        if (bytes) ws = at::empty({(int64_t)bytes}, q->options().dtype(at::kByte));
+        st = pa.prefill4(qp, sp, lp, kv.k, kv.v, tp, maxblk, R, T, max_q, hq, kv.hkv, kv.d, kv.bs, kv.nb, scale, split,
+                         bytes ? ws.data_ptr() : nullptr, bytes, out.data_ptr(), dtype, current_stream(c.dev));
+      }))
+    Py_RETURN_NONE;
+  if (st != PA_OK) return PyLong_FromLong(st);
+  return mine ? give(out) : Py_NewRef(a[8]);
+}
+
+// (block_tables, context_lens, parents, num_blocks, block_size, grow, max_grow, pinned, max_blocks): grow a tensor and
+// max_grow its bound, or grow a count and max_grow None; pinned and max_blocks may be None
+PyObject* fork_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 9) Py_RETURN_NONE;
+  Call c;
+  const at::Tensor *table = c.first(a[0]), *lens = c.tensor(a[1]), *parents = c.tensor(a[2]);
+  if (!c.ok || !c.need(table->dim() == 2 && lens->dim() >= 1 && parents->dim() >= 1)) Py_RETURN_NONE;
+  const int B = c.size(lens, 0), R = c.size(parents, 0), maxblk = c.size(table, 1);
+  const int32_t *tp = c.rows(a[0], B), *lp = c.rows(a[1], B), *pp = c.rows(a[2], R), *gp = nullptr;
+  const int num_blocks = c.integer(a[3]), bs = c.integer(a[4]);
+  int most = 0;
+  if (a[6] == Py_None) {
+    most = c.integer(a[5]);
+  } else {
+    gp = c.rows(a[5], R);
+    most = c.integer(a[6]);
+  }
+  const uint8_t* pin = nullptr;
+  if (a[7] != Py_None) {
+    const at::Tensor* t = c.tensor(a[7]);
+    if (c.ok && c.need(t->dim() == 1 && t->size(0) == num_blocks &&
+                       (t->scalar_type() == at::kBool || t->scalar_type() == at::kByte)))
+      pin = static_cast<const uint8_t*>(c.ptr(t));
+  }
+  const int width = a[8] == Py_None ? maxblk : c.integer(a[8]);
+  if (!c.ok || !c.need(most >= 0 && width >= 1)) Py_RETURN_NONE;
+  at::Tensor out[5], ws;
+  int st = PA_OK;
+  if (!run([&] {
+        const auto opt = table->options();
+        out[0] = at::empty({R, width}, opt);
+        out[1] = at::empty({R}, opt);
+        out[2] = at::empty({R, 2}, opt);
+        out[3] = at::empty({R, most}, opt);
+        out[4] = at::empty({1}, opt);
+        int32_t* p[5];
+        for (int i = 0; i < 5; ++i) p[i] = static_cast<int32_t*>(out[i].data_ptr());
+        const size_t bytes = pa.fork_workspace(R, num_blocks);
+        ws = at::empty({(int64_t)bytes}, opt.dtype(at::kByte));
+        st = pa.fork(tp, maxblk, lp, B, pp, R, gp, most, pin, num_blocks, bs, p[0], width, p[1], p[2], p[3], p[4],
+                     ws.data_ptr(), bytes, current_stream(c.dev));
+      }))
+    Py_RETURN_NONE;
+  if (st != PA_OK) return PyLong_FromLong(st);
+  PyObject* r = PyTuple_New(5);
+  for (int i = 0; r && i < 5; ++i) {
+    PyObject* o = give(out[i]);
+    if (o) PyTuple_SET_ITEM(r, i, o);
+    else Py_CLEAR(r);
+  }
+  return r;
+}
+
+// (list of caches, pairs) -> PA_OK's 0, a status
+PyObject* copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  if (n != 2 || !PyList_CheckExact(a[0])) Py_RETURN_NONE;
+  const Py_ssize_t num = PyList_GET_SIZE(a[0]);
+  constexpr Py_ssize_t kMost = 512;  // longer lists go the long way
+  if (num < 1 || num > kMost) Py_RETURN_NONE;
+  Call c;
+  void* p[kMost];
+  int nb = 0;
+  int64_t bytes = 0;
+  for (Py_ssize_t i = 0; i < num; ++i) {
+    const at::Tensor* t = i ? c.tensor(PyList_GET_ITEM(a[0], i)) : c.first(PyList_GET_ITEM(a[0], i));
+    if (!c.ok || !c.need(t->dim() >= 1)) Py_RETURN_NONE;
+    const int64_t size = t->numel() * t->element_size();
+    if (i == 0) nb = c.size(t, 0), bytes = size;
+    c.need(nb > 0 && t->size(0) == nb && size == bytes);
+    p[i] = c.ptr(t);
+  }
+  const at::Tensor* pairs = c.tensor(a[1]);
+  if (!c.ok || !c.need(bytes / nb % 16 == 0 && pairs->dim() == 2 && pairs->size(1) == 2)) Py_RETURN_NONE;
+  const int np = c.size(pairs, 0);
+  const int32_t* pp = c.rows(a[1], np);
+  if (!c.ok) Py_RETURN_NONE;
+  int st = PA_OK;
+  if (!run([&] { st = pa.copy_pages(p, (int)num, pp, np, nb, bytes / nb, current_stream(c.dev)); })) Py_RETURN_NONE;
+  return PyLong_FromLong(st);
+}
+
 // (addresses in the order of `pa`)
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   constexpr int N = sizeof(pa) / sizeof(void*);
@@ -389,6 +626,15 @@ PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
   pa.accumulate = reinterpret_cast<decltype(pa.accumulate)>(f[4]);
   pa.evict_select = reinterpret_cast<decltype(pa.evict_select)>(f[5]);
   pa.compact = reinterpret_cast<decltype(pa.compact)>(f[6]);
+  pa.quantize = reinterpret_cast<decltype(pa.quantize)>(f[7]);
+  pa.dequantize = reinterpret_cast<decltype(pa.dequantize)>(f[8]);
+  pa.decode4_workspace = reinterpret_cast<decltype(pa.decode4_workspace)>(f[9]);
+  pa.decode4 = reinterpret_cast<decltype(pa.decode4)>(f[10]);
+  pa.prefill4_workspace = reinterpret_cast<decltype(pa.prefill4_workspace)>(f[11]);
+  pa.prefill4 = reinterpret_cast<decltype(pa.prefill4)>(f[12]);
+  pa.fork_workspace = reinterpret_cast<decltype(pa.fork_workspace)>(f[13]);
+  pa.fork = reinterpret_cast<decltype(pa.fork)>(f[14]);
+  pa.copy_pages = reinterpret_cast<decltype(pa.copy_pages)>(f[15]);
   Py_RETURN_NONE;
 }
 
@@ -412,6 +658,12 @@ PyMethodDef methods[] = {PA_METHOD(bind),
                          PA_METHOD(decode_accumulate),
                          PA_METHOD(evict_select),
                          PA_METHOD(compact_kv),
+                         PA_METHOD(quantize_and_cache),
+                         PA_METHOD(dequantize_kv4),
+                         PA_METHOD(decode_kv4),
+                         PA_METHOD(chunked_prefill_kv4),
+                         PA_METHOD(fork_blocks),
+                         PA_METHOD(copy_pages),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_marshal", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -121,7 +121,10 @@ class recording:
 # launch; None from them means that the call is not of the regular kind, and
 # nothing was done.
 _SHORT = ("pa_norm_rope_and_cache", "pa_verify_tree_workspace_size", "pa_verify_tree",
-          "pa_decode_accumulate_workspace_size", "pa_decode_accumulate", "pa_evict_select", "pa_compact_kv")
+          "pa_decode_accumulate_workspace_size", "pa_decode_accumulate", "pa_evict_select", "pa_compact_kv",
+          "pa_quantize_and_cache", "pa_dequantize_kv4", "pa_decode_kv4_workspace_size", "pa_decode_kv4",
+          "pa_chunked_prefill_kv4_workspace_size", "pa_chunked_prefill_kv4", "pa_fork_blocks_workspace_size",
+          "pa_fork_blocks", "pa_copy_pages")
 _marshal = None  # the module; False: not built, or for another torch
 
 
@@ -909,6 +912,11 @@ def _kv4_ptrs(k_cache, v_cache, dev: int, d: int):
 def quantize_and_cache(k, v, slot_mapping, k_cache, v_cache, stream=None):
     """pa_quantize_and_cache: :func:`reshape_and_cache` into a 4-bit cache.  ``k`` and ``v`` ([num_tokens, kv_heads,
     head_dim]) may be views of one projection's rows."""
+    if _short_way(stream):
+        r = _marshal.quantize_and_cache(k, v, slot_mapping, k_cache, v_cache)
+        if r is not None:
+            check(r, "pa_quantize_and_cache")
+            return
     if k.dim() != 3 or v.shape != k.shape:
         raise ValueError("k and v are [num_tokens, kv_heads, head_dim] of the cache")
     dtype, dev = k.dtype, k.get_device()
@@ -927,6 +935,12 @@ def quantize_and_cache(k, v, slot_mapping, k_cache, v_cache, stream=None):
 def dequantize_kv4(k_cache, v_cache, slots, head_dim, dtype=torch.bfloat16, k=None, v=None, stream=None):
     """pa_dequantize_kv4: K and V of the tokens at ``slots`` in 16 bits, each [num_tokens, kv_heads, head_dim] (exact;
     zeros where a slot is negative)."""
+    if k is None and v is None and _short_way(stream):
+        r = _marshal.dequantize_kv4(k_cache, v_cache, slots, head_dim, dtype_code(dtype))
+        if r is not None:
+            if type(r) is int:
+                check(r, "pa_dequantize_kv4")
+            return r
     dev, d, code = k_cache.get_device(), int(head_dim), dtype_code(dtype)
     kc, vc, nb, bs, hkv = _kv4_ptrs(k_cache, v_cache, dev, d)
     T = slots.shape[0] if slots.dim() == 1 else -1
@@ -977,6 +991,12 @@ def decode_kv4(q, k_cache, v_cache, block_tables, context_lens, scale, out=None,
                stream=None):
     """pa_decode_kv4: :func:`decode` (``q`` [num_seqs, q_heads, head_dim]) or :func:`verify_decode` (``q`` [num_seqs,
     q_len, q_heads, head_dim]) over a 4-bit cache."""
+    if workspace is None and _short_way(stream):
+        r = _marshal.decode_kv4(q, k_cache, v_cache, block_tables, context_lens, scale, out, split_tokens)
+        if r is not None:
+            if type(r) is int:
+                check(r, "pa_decode_kv4")
+            return r
     if q.dim() not in (3, 4):
         raise ValueError("q is [num_seqs, q_heads, head_dim] or [num_seqs, q_len, q_heads, head_dim]")
     dtype, dev, qshape = q.dtype, q.get_device(), q.shape
@@ -1023,6 +1043,13 @@ def _kv4_prefill_workspace(dev, *sizes) -> int:  # dev: the choice depends on th
 def chunked_prefill_kv4(q, q_start, context_lens, k_cache, v_cache, block_tables, scale, max_q_len, out=None,
                         split_tokens=0, workspace=None, stream=None):
     """pa_chunked_prefill_kv4: :func:`chunked_prefill` over a 4-bit cache.  ``scale`` is not zero."""
+    if workspace is None and _short_way(stream):
+        r = _marshal.chunked_prefill_kv4(q, q_start, context_lens, k_cache, v_cache, block_tables, scale, max_q_len, out,
+                                         split_tokens)
+        if r is not None:
+            if type(r) is int:
+                check(r, "pa_chunked_prefill_kv4")
+            return r
     if q.dim() != 3:
         raise ValueError("q is [total_q, q_heads, head_dim]")
     dtype, dev, qshape = q.dtype, q.get_device(), q.shape
@@ -1063,6 +1090,13 @@ def fork_blocks(block_tables, context_lens, parents, num_blocks, block_size, gro
 
     ``pinned`` (bool or uint8 [num_blocks]): blocks that others hold.  ``max_blocks``: columns of the new tables (None:
     as many as ``block_tables`` has)."""
+    if workspace is None and _short_way(stream):
+        r = _marshal.fork_blocks(block_tables, context_lens, parents, num_blocks, block_size, grow, max_grow, pinned,
+                                 max_blocks)
+        if r is not None:
+            if type(r) is int:
+                check(r, "pa_fork_blocks")
+            return r
     dev, num_blocks, block_size = block_tables.get_device(), int(num_blocks), int(block_size)
     B, R = context_lens.shape[0], parents.shape[0]
     tables = _table_ptr(block_tables, dev, B)
@@ -1104,6 +1138,11 @@ def fork_blocks(block_tables, context_lens, parents, num_blocks, block_size, gro
 def copy_pages(caches, pairs, stream=None):
     """pa_copy_pages: in every cache (a list of tensors [num_blocks, ...] of one size, 16-bit or 4-bit) block
     ``pairs[p, 1]`` becomes a copy of block ``pairs[p, 0]``; a negative source is no copy."""
+    if _short_way(stream):
+        r = _marshal.copy_pages(caches, pairs)
+        if r is not None:
+            check(r, "pa_copy_pages")
+            return
     caches = list(caches)
     if not caches:
         return
