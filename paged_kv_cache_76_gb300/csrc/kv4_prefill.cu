@@ -78,6 +78,10 @@ constexpr int B_QFULL = B_OFULL + 4;            // [2]
 constexpr int B_MMADONE = B_QFULL + 2;
 static_assert(B_MMADONE + 1 == 4 * kStages + 2 * kMakers + 15, "barrier count");
 
+__device__ __forceinline__ void st_shared4(uint32_t at, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 struct Unit {
   int r, h, row0, part, qs, chunk, p0, rows, k0, kend, ntiles;
   int code;  // error of a refused request
@@ -218,26 +222,45 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
       }
       const int ts = w.k0 + j * kKeys;
       const int nvalid = min(kKeys, w.kend - ts);
-      uint8_t* dst = tile0 + s * Tile::BYTES;
-      constexpr int PER_ROW = D / kKv4Group, STEP = 32 / PER_ROW;  // rows of a step
+      if (nvalid < kKeys) {
+        // rows behind the last key: their scales, which the copies are done with, become zeros
+        for (int row = nvalid + lane; row < kKeys; row += 32) {
+          uint32_t* at = reinterpret_cast<uint32_t*>(scales + row * R::SCALES);
+#pragma unroll
+          for (int i = 0; i < R::SCALES / 4; ++i) at[i] = 0u;
+        }
+        __syncwarp();
+      }
+      // The lane's row in step i is row0 + STEP i, so in the swizzle its 16-byte
+      // piece c is at c ^ (row % 8): row0 and a bit that alternates.
+      constexpr int PER_ROW = D / kKv4Group, STEP = 32 / PER_ROW;  // rows of a step: 4, or 8 of 64 elements
       const int g = lane % PER_ROW, row0 = lane / PER_ROW, flip = g >> 2;
-#pragma unroll 4
-      for (int row = row0; row < kKeys; row += STEP) {
-        const uint2 c = *reinterpret_cast<const uint2*>(codes + row * R::CODES + 8 * g);
-        uint32_t byte = row < nvalid ? scales[row * R::SCALES + g] : 0u;
+      const uint32_t place = smem_u32(tile0 + s * Tile::BYTES) + row0 * 128;
+      uint32_t at0[2], at1[2];  // of the first and the second store, even and odd steps
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int sw = (row0 + STEP * e) & 7, c = 2 * g + flip;
+        at0[e] = place + (c >> 3) * Tile::HALF + (((c & 7) ^ sw) << 4);
+        at1[e] = place + (c >> 3) * Tile::HALF + (((c & 7 ^ 1) ^ sw) << 4);
+      }
+      const uint8_t* code = codes + row0 * R::CODES + 8 * g;
+      const uint8_t* scale = scales + row0 * R::SCALES + g;
+#pragma unroll
+      for (int i = 0; i < kKeys / STEP; ++i) {
+        const uint2 c = *reinterpret_cast<const uint2*>(code + i * STEP * R::CODES);
+        uint32_t byte = scale[i * STEP * R::SCALES];
         if (isv && byte >= kKv4FirstInf) {
           byte = 0;
-          atomicMin(&first_nan[g], ts + row);
+          atomicMin(&first_nan[g], ts + row0 + i * STEP);
         }
         const uint32_t s2 = kv4_scale2(byte);
         uint32_t x[8];
-        kv4_unpack(c.x, *reinterpret_cast<uint32_t(*)[4]>(&x[0]));
-        kv4_unpack(c.y, *reinterpret_cast<uint32_t(*)[4]>(&x[4]));
+        kv4_unpack(flip ? c.y : c.x, *reinterpret_cast<uint32_t(*)[4]>(&x[0]));
+        kv4_unpack(flip ? c.x : c.y, *reinterpret_cast<uint32_t(*)[4]>(&x[4]));
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = hmul2_u(x[e], s2);
-        const uint4 c0 = make_uint4(x[0], x[1], x[2], x[3]), c1 = make_uint4(x[4], x[5], x[6], x[7]);
-        *reinterpret_cast<uint4*>(dst + Tile::offset(row, 2 * g + flip)) = flip ? c1 : c0;
-        *reinterpret_cast<uint4*>(dst + Tile::offset(row, 2 * g + (flip ^ 1))) = flip ? c0 : c1;
+        st_shared4(at0[i & 1] + i * STEP * 128, make_uint4(x[0], x[1], x[2], x[3]));
+        st_shared4(at1[i & 1] + i * STEP * 128, make_uint4(x[4], x[5], x[6], x[7]));
       }
       fence_proxy_async_smem();  // the tile before the MMAs, the pages before the next copies over them
       __syncwarp();
