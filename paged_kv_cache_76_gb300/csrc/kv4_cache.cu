@@ -1,9 +1,9 @@
 // Writing a 4-bit paged cache and reading it back (see kv4.cuh for the page).
 //
-// One thread takes the 16 elements of one scale: its largest magnitude, the
-// scale, and the codes need no other thread, and neighbouring threads read and
-// write neighbouring 32-byte pieces.  Both kernels are bound by memory: the
-// write reads 2 bytes an element and writes 9/16.
+// One thread takes the 16 elements of a scale, of K and of V: their largest
+// magnitude, the scale and the codes need no other thread, and neighbouring
+// threads read and write neighbouring 32-byte pieces.  Both kernels are bound by
+// memory: the write reads 2 bytes an element and writes 9/16.
 #include "kv4.cuh"
 #include "pa_internal.h"
 
@@ -57,98 +57,132 @@ __device__ __forceinline__ uint2 encode16(const float (&x)[16], uint32_t& byte) 
   return make_uint2(w[0], w[1]);
 }
 
+// Group i: its token, its place in the token's row of all heads, and where its
+// codes and its scale are in either cache.
+struct Place {
+  uint32_t token, at;
+  int32_t slot;
+  int64_t codes, scale;
+};
+template <int D>
+__device__ __forceinline__ Place place_of(uint32_t i, const int32_t* slots, uint32_t per_token, int64_t num_slots,
+                                          int kv_heads, int block_shift) {
+  constexpr uint32_t GROUPS = D / kKv4Group;
+  Place w;
+  w.token = i / per_token;
+  w.at = i - w.token * per_token;
+  w.slot = __ldg(slots + w.token);
+  const uint32_t h = w.at / GROUPS, g = w.at % GROUPS;
+  const uint32_t b = (uint32_t)w.slot >> block_shift, o = (uint32_t)w.slot & ((1u << block_shift) - 1u);
+  const int64_t page = ((int64_t)b * kv_heads + h) * ((int64_t)Kv4Row<D>::BYTES << block_shift);
+  w.codes = page + o * Kv4Row<D>::CODES + 8 * g;
+  w.scale = page + (Kv4Row<D>::CODES << block_shift) + o * GROUPS + g;
+  return w;
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(256) quantize_and_cache_kernel(const Kv4WriteParams p) {
-  constexpr int GROUPS = D / kKv4Group;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t per_token = (int64_t)p.kv_heads * GROUPS;
-  const int64_t total = 2 * p.num_tokens * per_token;
-  const int64_t page = (int64_t)p.block_size * Kv4Row<D>::BYTES;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t row = i / per_token;  // K of token 0, V of token 0, K of token 1, ...
-    const int at = (int)(i - row * per_token);
-    const int64_t tok = row >> 1;
-    const bool isv = row & 1;
-    const int32_t slot = __ldg(p.slots + tok);
-    if (slot < 0) continue;  // padding token
-    if (slot >= p.num_slots) {
-      if (at == 0) record_error(p.err, PA_DEVERR_SLOT);
-      continue;
-    }
-    const T* src = static_cast<const T*>(isv ? p.v : p.k) + tok * (isv ? p.v_stride : p.k_stride) + at * kKv4Group;
-    const uint4 v[2] = {__ldg(reinterpret_cast<const uint4*>(src)), __ldg(reinterpret_cast<const uint4*>(src) + 1)};
-    float x[16];
-    to_floats<T>(v, x);
-    uint32_t byte;
-    const uint2 codes = encode16(x, byte);
-    const int h = at / GROUPS, g = at - h * GROUPS;
-    const int b = slot / p.block_size, o = slot - b * p.block_size;
-    uint8_t* dst = static_cast<uint8_t*>(isv ? p.v_cache : p.k_cache) + ((int64_t)b * p.kv_heads + h) * page;
-    *reinterpret_cast<uint2*>(dst + o * Kv4Row<D>::CODES + 8 * g) = codes;
-    dst[p.block_size * Kv4Row<D>::CODES + o * GROUPS + g] = (uint8_t)byte;
+  const uint32_t per_token = p.kv_heads * (D / kKv4Group), total = (uint32_t)p.num_tokens * per_token;
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= total) return;
+  const Place w = place_of<D>(i, p.slots, per_token, p.num_slots, p.kv_heads, p.block_shift);
+  if (w.slot < 0) return;  // padding token
+  if (w.slot >= p.num_slots) {
+    if (w.at == 0) record_error(p.err, PA_DEVERR_SLOT);
+    return;
   }
+  const uint4* k = reinterpret_cast<const uint4*>(static_cast<const T*>(p.k) + w.token * p.k_stride + w.at * kKv4Group);
+  const uint4* v = reinterpret_cast<const uint4*>(static_cast<const T*>(p.v) + w.token * p.v_stride + w.at * kKv4Group);
+  const uint4 xk[2] = {__ldg(k), __ldg(k + 1)}, xv[2] = {__ldg(v), __ldg(v + 1)};
+  float x[16];
+  uint32_t byte;
+  to_floats<T>(xk, x);
+  uint2 codes = encode16(x, byte);
+  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.k_cache) + w.codes) = codes;
+  static_cast<uint8_t*>(p.k_cache)[w.scale] = (uint8_t)byte;
+  to_floats<T>(xv, x);
+  codes = encode16(x, byte);
+  *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.v_cache) + w.codes) = codes;
+  static_cast<uint8_t*>(p.v_cache)[w.scale] = (uint8_t)byte;
 }
 
 template <int D, typename T>
 __global__ void __launch_bounds__(256) dequantize_kernel(const Kv4ReadParams p) {
-  constexpr int GROUPS = D / kKv4Group;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t per_token = (int64_t)p.kv_heads * GROUPS;
-  const int64_t total = 2 * p.num_tokens * per_token;
-  const int64_t page = (int64_t)p.block_size * Kv4Row<D>::BYTES;
-  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
-    const int64_t row = i / per_token;
-    const int at = (int)(i - row * per_token);
-    const int64_t tok = row >> 1;
-    const bool isv = row & 1;
-    const int32_t slot = __ldg(p.slots + tok);
-    uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-    if (slot >= p.num_slots) {
-      if (at == 0) record_error(p.err, PA_DEVERR_SLOT);
-    } else if (slot >= 0) {
-      const int h = at / GROUPS, g = at - h * GROUPS;
-      const int b = slot / p.block_size, o = slot - b * p.block_size;
-      const uint8_t* src = static_cast<const uint8_t*>(isv ? p.v_cache : p.k_cache) + ((int64_t)b * p.kv_heads + h) * page;
-      const uint2 codes = *reinterpret_cast<const uint2*>(src + o * Kv4Row<D>::CODES + 8 * g);
-      const uint32_t s = kv4_scale2(src[p.block_size * Kv4Row<D>::CODES + o * GROUPS + g]);
-      uint32_t r[8];
-      kv4_unpack(codes.x, *reinterpret_cast<uint32_t(*)[4]>(&r[0]));
-      kv4_unpack(codes.y, *reinterpret_cast<uint32_t(*)[4]>(&r[4]));
+  const uint32_t per_token = p.kv_heads * (D / kKv4Group), total = (uint32_t)p.num_tokens * per_token;
+  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  if (i >= total) return;
+  const Place w = place_of<D>(i, p.slots, per_token, p.num_slots, p.kv_heads, p.block_shift);
+  const bool has = w.slot >= 0 && w.slot < p.num_slots;
+  if (w.slot >= p.num_slots && w.at == 0) record_error(p.err, PA_DEVERR_SLOT);
+  uint2 codes[2] = {make_uint2(0, 0), make_uint2(0, 0)};
+  uint32_t byte[2] = {0, 0};
+  if (has) {
+    codes[0] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.k_cache) + w.codes);
+    codes[1] = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.v_cache) + w.codes);
+    byte[0] = static_cast<const uint8_t*>(p.k_cache)[w.scale];
+    byte[1] = static_cast<const uint8_t*>(p.v_cache)[w.scale];
+  }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) r[e] = from_half2<T>(hmul2_u(r[e], s));
-      out[0] = make_uint4(r[0], r[1], r[2], r[3]);
-      out[1] = make_uint4(r[4], r[5], r[6], r[7]);
-    }
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(isv ? p.v : p.k) + (tok * per_token + at) * kKv4Group);
-    dst[0] = out[0];
-    dst[1] = out[1];
+  for (int e = 0; e < 2; ++e) {
+    const uint32_t s = kv4_scale2(byte[e]);
+    uint32_t r[8];
+    kv4_unpack(codes[e].x, *reinterpret_cast<uint32_t(*)[4]>(&r[0]));
+    kv4_unpack(codes[e].y, *reinterpret_cast<uint32_t(*)[4]>(&r[4]));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[k] = from_half2<T>(hmul2_u(r[k], s));
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(e ? p.v : p.k) + (int64_t)i * kKv4Group);
+    dst[0] = make_uint4(r[0], r[1], r[2], r[3]);
+    dst[1] = make_uint4(r[4], r[5], r[6], r[7]);
   }
 }
 
+// Tokens of a launch: groups are counted in 32 bits.
+int64_t tokens_at_once(int kv_heads, int head_dim) { return INT32_MAX / (kv_heads * (head_dim / kKv4Group)); }
+
 }  // namespace
 
-cudaError_t launch_quantize_and_cache(const Kv4WriteParams& p, int head_dim, pa_dtype dt, cudaStream_t stream) {
-  const int64_t total = 2 * p.num_tokens * p.kv_heads * (head_dim / kKv4Group);
-  if (total == 0) return cudaSuccess;
-  const dim3 grid(copy_grid(total)), block(256);
-  if (head_dim == 128)
-    return dt == PA_BF16 ? launch_pdl(quantize_and_cache_kernel<128, __nv_bfloat16>, grid, block, 0, stream, p)
-                         : launch_pdl(quantize_and_cache_kernel<128, __half>, grid, block, 0, stream, p);
-  return dt == PA_BF16 ? launch_pdl(quantize_and_cache_kernel<64, __nv_bfloat16>, grid, block, 0, stream, p)
-                       : launch_pdl(quantize_and_cache_kernel<64, __half>, grid, block, 0, stream, p);
+cudaError_t launch_quantize_and_cache(const Kv4WriteParams& all, int head_dim, pa_dtype dt, cudaStream_t stream) {
+  const int64_t most = tokens_at_once(all.kv_heads, head_dim);
+  cudaError_t e = cudaSuccess;
+  for (int64_t t = 0; t < all.num_tokens && e == cudaSuccess; t += most) {
+    Kv4WriteParams p = all;
+    p.num_tokens = all.num_tokens - t < most ? all.num_tokens - t : most;
+    p.k = static_cast<const uint16_t*>(all.k) + t * all.k_stride;
+    p.v = static_cast<const uint16_t*>(all.v) + t * all.v_stride;
+    p.slots = all.slots + t;
+    const dim3 grid((unsigned)((p.num_tokens * p.kv_heads * (head_dim / kKv4Group) + 255) / 256)), block(256);
+    if (head_dim == 128)
+      e = dt == PA_BF16 ? launch_pdl(quantize_and_cache_kernel<128, __nv_bfloat16>, grid, block, 0, stream, p)
+                        : launch_pdl(quantize_and_cache_kernel<128, __half>, grid, block, 0, stream, p);
+    else
+      e = dt == PA_BF16 ? launch_pdl(quantize_and_cache_kernel<64, __nv_bfloat16>, grid, block, 0, stream, p)
+                        : launch_pdl(quantize_and_cache_kernel<64, __half>, grid, block, 0, stream, p);
+  }
+  return e;
 }
 
-cudaError_t launch_dequantize_kv4(const Kv4ReadParams& p, int head_dim, pa_dtype dt, cudaStream_t stream) {
-  const int64_t total = 2 * p.num_tokens * p.kv_heads * (head_dim / kKv4Group);
-  if (total == 0) return cudaSuccess;
-  const dim3 grid(copy_grid(total)), block(256);
-  if (head_dim == 128)
-    return dt == PA_BF16 ? launch_pdl(dequantize_kernel<128, __nv_bfloat16>, grid, block, 0, stream, p)
-                         : launch_pdl(dequantize_kernel<128, __half>, grid, block, 0, stream, p);
-  return dt == PA_BF16 ? launch_pdl(dequantize_kernel<64, __nv_bfloat16>, grid, block, 0, stream, p)
-                       : launch_pdl(dequantize_kernel<64, __half>, grid, block, 0, stream, p);
+cudaError_t launch_dequantize_kv4(const Kv4ReadParams& all, int head_dim, pa_dtype dt, cudaStream_t stream) {
+  const int64_t most = tokens_at_once(all.kv_heads, head_dim), row = (int64_t)all.kv_heads * head_dim;
+  cudaError_t e = cudaSuccess;
+  for (int64_t t = 0; t < all.num_tokens && e == cudaSuccess; t += most) {
+    Kv4ReadParams p = all;
+    p.num_tokens = all.num_tokens - t < most ? all.num_tokens - t : most;
+    p.k = static_cast<uint16_t*>(all.k) + t * row;
+    p.v = static_cast<uint16_t*>(all.v) + t * row;
+    p.slots = all.slots + t;
+    const dim3 grid((unsigned)((p.num_tokens * p.kv_heads * (head_dim / kKv4Group) + 255) / 256)), block(256);
+    if (head_dim == 128)
+      e = dt == PA_BF16 ? launch_pdl(dequantize_kernel<128, __nv_bfloat16>, grid, block, 0, stream, p)
+                        : launch_pdl(dequantize_kernel<128, __half>, grid, block, 0, stream, p);
+    else
+      e = dt == PA_BF16 ? launch_pdl(dequantize_kernel<64, __nv_bfloat16>, grid, block, 0, stream, p)
+                        : launch_pdl(dequantize_kernel<64, __half>, grid, block, 0, stream, p);
+  }
+  return e;
 }
 
 }  // namespace pa

@@ -60,7 +60,8 @@ struct Kv4PrefillSmem {
   static constexpr int NBARS = 4 * kStages + 2 * kMakers + 15;
   static constexpr int SLOT_OFF = BAR_OFF + NBARS * 8;
   static constexpr int NAN_OFF = SLOT_OFF + 8;
-  static constexpr int BYTES = NAN_OFF + D / kKv4Group * 4 + 1024;
+  static constexpr int SCALE_OFF = NAN_OFF + D / kKv4Group * 4;  // softmax scale of each row
+  static constexpr int BYTES = SCALE_OFF + 2 * kRows * 4 + 1024;
   static_assert(BYTES <= 227 * 1024, "shared memory per CTA");
   static_assert(kMakers <= kStages, "the last tile of every maker is still the last of its stage at the end");
 };
@@ -114,6 +115,25 @@ __device__ __forceinline__ Unit unit_of(const Kv4PrefillParams& p, int u) {
   return w;
 }
 
+// Where units outnumber the SMs the last ones decide when the kernel ends, so
+// requests of one partition run longest first: the request of index r in that
+// order, ties by number, among the kWindow around it.  Every thread calls it.
+constexpr int kWindow = 128;
+__device__ __forceinline__ int longest_first(const Kv4PrefillParams& p, int r, int* scratch) {
+  const int w0 = r / kWindow * kWindow, n = min(kWindow, p.num_reqs - w0), t = threadIdx.x;
+  int len = 0;
+  if (t < n) scratch[t] = len = __ldg(p.lens + w0 + t);
+  __syncthreads();
+  if (t < n) {
+    int before = 0;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) before += scratch[i] > len || (scratch[i] == len && i < t);
+    if (before == r - w0) scratch[kWindow] = w0 + t;
+  }
+  __syncthreads();
+  return scratch[kWindow];
+}
+
 template <int D, typename T>
 __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4PrefillParams p) {
   using L = Kv4PrefillSmem<D>;
@@ -121,6 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
   using R = Kv4Row<D>;
   constexpr int KSTEPS = D / 16;
   constexpr int PSTEPS = kKeys / 16;
+  constexpr int ROW_BYTES = 2 * D;  // of a row of Q
   constexpr uint32_t O_COL = 4 * kKeys;
   constexpr uint32_t IDESC_S = idesc_f16<__half>(kRows, kKeys, false);
   constexpr uint32_t IDESC_O = idesc_f16<__half>(kRows, D, true);
@@ -130,11 +151,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + L::BAR_OFF);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::SLOT_OFF);
   int* first_nan = reinterpret_cast<int*>(smem + L::NAN_OFF);  // per group of elements: its first V token that is NaN
+  float* scales = reinterpret_cast<float*>(smem + L::SCALE_OFF);
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = p.group;
-  const Unit w = unit_of(p, blockIdx.x);
+  int u = blockIdx.x;
+  if (p.longest_first) {
+    __shared__ int longest[kWindow + 1];
+    const int per_r = p.row_tiles * p.kv_heads, r = u / per_r;
+    u += (longest_first(p, r, longest) - r) * per_r;
+  }
+  const Unit w = unit_of(p, u);
   if (w.code || w.ntiles == 0) {
     griddep_wait();
     if (w.code && w.h == 0 && w.row0 == 0 && w.part == 0 && threadIdx.x == 0) record_error(p.err, w.code);
@@ -177,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
     const int maker = warp - 2, isv = maker & 1, first = maker >> 1;
     const uint8_t* cache = static_cast<const uint8_t*>(isv ? p.v_cache : p.k_cache);
     uint8_t* codes = smem + L::RAW_OFF + maker * L::RAW;
-    uint8_t* scales = codes + kKeys * R::CODES;
+    uint8_t* raw_scales = codes + kKeys * R::CODES;
     uint8_t* tile0 = smem + (isv ? L::V_OFF : L::K_OFF);
     const int full0 = isv ? B_VFULL : B_KFULL, empty0 = isv ? B_VEMPTY : B_KEMPTY;
     const uint32_t rawbar = bar(B_RAW + maker);
@@ -201,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
       __syncwarp();
       if (mine) {
         const int bytes = bs * (part ? R::SCALES : R::CODES);
-        uint8_t* dst = (part ? scales : codes) + i * bytes;
+        uint8_t* dst = (part ? raw_scales : codes) + i * bytes;
         if (b >= 0) {
           bulk_load_hint(smem_u32(dst), cache + ((size_t)b * p.kv_heads + w.h) * page + (part ? bs * R::CODES : 0), bytes,
                          rawbar, pol);
@@ -225,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
       if (nvalid < kKeys) {
         // rows behind the last key: their scales, which the copies are done with, become zeros
         for (int row = nvalid + lane; row < kKeys; row += 32) {
-          uint32_t* at = reinterpret_cast<uint32_t*>(scales + row * R::SCALES);
+          uint32_t* at = reinterpret_cast<uint32_t*>(raw_scales + row * R::SCALES);
 #pragma unroll
           for (int i = 0; i < R::SCALES / 4; ++i) at[i] = 0u;
         }
@@ -244,7 +272,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
         at1[e] = place + (c >> 3) * Tile::HALF + (((c & 7 ^ 1) ^ sw) << 4);
       }
       const uint8_t* code = codes + row0 * R::CODES + 8 * g;
-      const uint8_t* scale = scales + row0 * R::SCALES + g;
+      const uint8_t* scale = raw_scales + row0 * R::SCALES + g;
 #pragma unroll
       for (int i = 0; i < kKeys / STEP; ++i) {
         const uint2 c = *reinterpret_cast<const uint2*>(code + i * STEP * R::CODES);
@@ -326,41 +354,57 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
       const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
       const uint32_t scol0 = tmem + lane_addr + 2 * x * kKeys, ocol = tmem + lane_addr + O_COL + x * D;
       const int grow = w.row0 + x * kRows + row;
-      const bool valid = grow < w.rows;
-      const int qi = grow / G, g = grow % G;
-      const int lim = valid ? w.p0 + qi : -1;  // last key this row sees
-      float sl2 = 0.f;
+      const int lim = grow < w.rows ? w.p0 + grow / G : -1;  // last key this row sees
+      // The warp's 32 rows of Q -> shared memory (K-major, 128-byte swizzle), a row
+      // by D/8 neighbouring lanes: a row per thread would touch 32 lines a load
+      // (measured: 5 us for the tile instead of 1)
+      constexpr int PIECES = D / 8, AT_ONCE = 32 / PIECES;  // 16-byte pieces of a row; rows a load takes
+      const int piece = lane % PIECES, row_in = lane / PIECES;
+      // row of q and out, in heads, of the warp's row `lane`; -1: a padding row.  The
+      // others' come by shuffles: a division each would cost more than the loads
+      auto own_row = [&](const Unit& w) {
+        const int n = w.row0 + x * kRows + row, i = n / G;
+        return n < w.rows ? (w.qs + i) * p.q_heads + w.h * G + (n - i * G) : -1;
+      };
+      uint8_t* qt = smem + L::Q_OFF + x * L::QTILE;
       {
-        const uint4* src = reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) +
-                                                          ((size_t)(w.qs + qi) * p.q_heads + w.h * G + g) * D);
-        uint8_t* qt = smem + L::Q_OFF + x * L::QTILE;
-        float top = 0.f;
+        constexpr int BATCH = 8;
+        const int own = own_row(w);
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+        for (int r0 = 0; r0 < 32; r0 += BATCH * AT_ONCE) {
+          uint4 v[BATCH];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) top = fmaxf(top, fmaxf(fabsf(Elem<T>::lo(e[i])), fabsf(Elem<T>::hi(e[i]))));
-        }
-        int ex = top > 0.f && top < INFINITY ? ilogbf(top) - 13 : 0;
-        ex = max(ex, -126);
-        const float down = ldexpf(1.f, -ex);
-        // a masked score is -inf and must stay so: not below the smallest normal number
-        sl2 = fmaxf(p.scale_log2 * ldexpf(1.f, ex), FLT_MIN);
+          for (int i = 0; i < BATCH; ++i) {
+            const int at = __shfl_sync(kAll, own, r0 + i * AT_ONCE + row_in);
+            v[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (int64_t)at * D) + piece)
+                           : make_uint4(0, 0, 0, 0);
+          }
 #pragma unroll
-        for (int c = 0; c < D / 8; ++c) {
-          const uint4 v = valid ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-          const uint32_t e[4] = {v.x, v.y, v.z, v.w};
-          uint32_t y[4];
+          for (int i = 0; i < BATCH; ++i) {
+            const int r = r0 + i * AT_ONCE + row_in, tr = quarter * 32 + r;
+            const uint32_t e[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            float top = 0.f;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) y[i] = Elem<__half>::pack(Elem<T>::lo(e[i]) * down, Elem<T>::hi(e[i]) * down);
-          *reinterpret_cast<uint4*>(qt + (c >> 3) * L::QHALF + row * 128 + (((c & 7) ^ (row & 7)) << 4)) =
-              make_uint4(y[0], y[1], y[2], y[3]);
+            for (int k = 0; k < 4; ++k) top = fmaxf(top, fmaxf(fabsf(Elem<T>::lo(e[k])), fabsf(Elem<T>::hi(e[k]))));
+#pragma unroll
+            for (int o = 1; o < PIECES; o <<= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+            int ex = (int)(__float_as_uint(top) >> 23) - 127;  // 2^ex <= top; of a subnormal -127: it is brought up less
+            ex = top > 0.f && top < INFINITY ? max(ex - 13, -126) : 0;
+            const float down = __uint_as_float((uint32_t)(127 - ex) << 23);
+            uint32_t y[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) y[k] = Elem<__half>::pack(Elem<T>::lo(e[k]) * down, Elem<T>::hi(e[k]) * down);
+            *reinterpret_cast<uint4*>(qt + (piece >> 3) * L::QHALF + tr * 128 + (((piece & 7) ^ (tr & 7)) << 4)) =
+                make_uint4(y[0], y[1], y[2], y[3]);
+            // a masked score is -inf and must stay so: not below the smallest normal number
+            if (piece == 0) scales[x * kRows + tr] = fmaxf(p.scale_log2 * __uint_as_float((uint32_t)(127 + ex) << 23), FLT_MIN);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_QFULL + x));
       }
+      const float sl2 = scales[x * kRows + row];
       griddep_wait();  // before writing outputs
 
       bool ok = true;
@@ -451,33 +495,66 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
         ok = ok && mbar_wait(bar(B_VFULL + j % kStages), (j / kStages) & 1);
       if (__all_sync(kAll, ok)) {
         tc_fence_after();
-        const size_t orow = (size_t)(w.qs + qi) * p.q_heads + w.h * G + g;
-        const size_t pr = orow * p.max_splits + w.part;
+        // the unit once more: kept through the loop above, its fields would spill
+        int again = u;
+        asm volatile("" : "+r"(again));
+        const Unit w = unit_of(p, again);
+        const int own = own_row(w);
         const float inv = l == 0.f ? 0.f : 1.f / l;  // a NaN sum stays one
+        // O through the Q tile's place (its MMAs have completed), 256 bytes of each
+        // of the warp's rows at a time, so that a store's lanes write whole rows
+        uint8_t* mine = smem + L::Q_OFF + x * L::QTILE + quarter * (L::QTILE / 4);
+        const bool whole = p.max_splits == 1;
+        auto put = [&](int c, uint4 v) {  // 16-byte piece c of this thread's row
+          *reinterpret_cast<uint4*>(mine + lane * ROW_BYTES + ((c ^ (lane & 7)) << 4)) = v;
+        };
+        auto get = [&](int r, int c) { return *reinterpret_cast<const uint4*>(mine + r * ROW_BYTES + ((c ^ (r & 7)) << 4)); };
 #pragma unroll
         for (int c = 0; c < D / 32; ++c) {
           float ov[32];
           tmem_ld32(ocol + 32 * c, ov);  // warp-collective
           tmem_wait_ld();
-          if (!valid) continue;
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (first_nan[2 * c + (e >> 4)] <= lim) ov[e] = NAN;
-          if (p.max_splits == 1) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + orow * D) + 4 * c;
+          for (int k = 0; k < 2; ++k) {
+            if (first_nan[2 * c + k] <= lim) {
+#pragma unroll
+              for (int e = 0; e < 16; ++e) ov[16 * k + e] = NAN;
+            }
+          }
+          if (whole) {
 #pragma unroll
             for (int q = 0; q < 4; ++q)
-              dst[q] = make_uint4(Elem<T>::pack(ov[8 * q] * inv, ov[8 * q + 1] * inv),
-                                  Elem<T>::pack(ov[8 * q + 2] * inv, ov[8 * q + 3] * inv),
-                                  Elem<T>::pack(ov[8 * q + 4] * inv, ov[8 * q + 5] * inv),
-                                  Elem<T>::pack(ov[8 * q + 6] * inv, ov[8 * q + 7] * inv));
+              put(4 * c + q, make_uint4(Elem<T>::pack(ov[8 * q] * inv, ov[8 * q + 1] * inv),
+                                        Elem<T>::pack(ov[8 * q + 2] * inv, ov[8 * q + 3] * inv),
+                                        Elem<T>::pack(ov[8 * q + 4] * inv, ov[8 * q + 5] * inv),
+                                        Elem<T>::pack(ov[8 * q + 6] * inv, ov[8 * q + 7] * inv)));
           } else {
-            float4* po = reinterpret_cast<float4*>(p.part_o + pr * D) + 8 * c;
+            // 32 fp32 columns: a quarter of the row (half, of 64 elements)
+            __syncwarp();
 #pragma unroll
-            for (int q = 0; q < 8; ++q) po[q] = make_float4(ov[4 * q], ov[4 * q + 1], ov[4 * q + 2], ov[4 * q + 3]);
+            for (int q = 0; q < 8; ++q)
+              put(q, make_uint4(__float_as_uint(ov[4 * q]), __float_as_uint(ov[4 * q + 1]), __float_as_uint(ov[4 * q + 2]),
+                                __float_as_uint(ov[4 * q + 3])));
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {  // four rows a store, 128 bytes each
+              const int r = 4 * i + (lane >> 3), at8 = lane & 7;
+              const int at = __shfl_sync(kAll, own, r);
+              if (at >= 0)
+                reinterpret_cast<uint4*>(p.part_o + ((size_t)at * p.max_splits + w.part) * D + 32 * c)[at8] = get(r, at8);
+            }
           }
         }
-        if (valid && p.max_splits > 1) {
+        if (whole) {
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 32 / AT_ONCE; ++i) {
+            const int r = i * AT_ONCE + row_in;
+            const int at = __shfl_sync(kAll, own, r);
+            if (at >= 0) reinterpret_cast<uint4*>(static_cast<T*>(p.out) + (int64_t)at * D)[piece] = get(r, piece);
+          }
+        } else if (own >= 0) {
+          const size_t pr = (size_t)own * p.max_splits + w.part;
           p.part_m[pr] = m;
           p.part_l[pr] = l;
         }

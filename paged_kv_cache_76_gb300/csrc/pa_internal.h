@@ -302,7 +302,7 @@ struct Kv4WriteParams {
   void* v_cache;
   int* err;
   int64_t num_tokens, num_slots;
-  int kv_heads, block_size;
+  int kv_heads, block_shift;
 };
 cudaError_t launch_quantize_and_cache(const Kv4WriteParams& p, int head_dim, pa_dtype dt, cudaStream_t stream);
 
@@ -314,7 +314,7 @@ struct Kv4ReadParams {
   void* v;
   int* err;
   int64_t num_tokens, num_slots;
-  int kv_heads, block_size;
+  int kv_heads, block_shift;
 };
 cudaError_t launch_dequantize_kv4(const Kv4ReadParams& p, int head_dim, pa_dtype dt, cudaStream_t stream);
 
@@ -352,6 +352,7 @@ struct Kv4PrefillParams {
   int* err;
   int maxblk, num_reqs, total_q, max_q_len, q_heads, kv_heads, group, num_blocks, block_size, block_shift;
   int split_tokens, max_splits, row_tiles;
+  int longest_first; // 1 (max_splits == 1 only): requests run in order of length
   int negative;      // scores change their sign before the softmax
   float scale_log2;  // of what is left
 };

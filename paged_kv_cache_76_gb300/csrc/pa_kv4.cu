@@ -66,7 +66,7 @@ int kv4_decode_setup(int num_seqs, int q_len, int q_heads, int kv_heads, int hea
 }
 
 constexpr int kKv4PrefillUnit = 64;  // a key tile of the kernel
-constexpr int kKv4PrefillMin = 512;
+constexpr int kKv4PrefillMin = 256;  // keys of a partition chosen here
 
 struct Kv4PrefillSetup {
   int split, max_splits, row_tiles;
@@ -88,14 +88,25 @@ int kv4_prefill_setup(int num_reqs, int total_q, int max_q_len, int q_heads, int
   const int64_t whole = (cap + kKv4PrefillUnit - 1) / kKv4PrefillUnit * kKv4PrefillUnit;
   int64_t split = split_tokens;
   if (split_tokens == 0) {
+    // Partitions that give the shortest time by this count, in quarters of a us:
+    // a key tile of a unit takes 3, starting and ending a unit 28, and a merge 20
+    // beside its partials' way to memory and back (8 bytes an element).  Units run
+    // in rounds of one per SM.  Measured on GB300: a chunk of 2048 over 34816
+    // tokens, 64/8 heads (512 units of 544 tiles, 3.4 rounds) whole 1752 us, in
+    // two partitions 1640; eight chunks of 257..768 over <= 4847 tokens whole 180,
+    // in two 250; four of 37..131 over <= 1632 whole 23, in two 23, in four 33.
     const int64_t sms = num_sms() > 0 ? num_sms() : 152;
-    const int64_t units = (int64_t)num_reqs * kv_heads * s->row_tiles;
-    split = whole;
-    if (units > 0 && units < sms) {
-      const int64_t parts = sms / units;
-      split = (cap + parts - 1) / parts;
-      split = (split + kKv4PrefillUnit - 1) / kKv4PrefillUnit * kKv4PrefillUnit;
-      if (split < kKv4PrefillMin) split = kKv4PrefillMin;
+    const int64_t units = (int64_t)num_reqs * kv_heads * s->row_tiles, tiles = whole / kKv4PrefillUnit;
+    const int64_t merge_bytes = (int64_t)num_reqs * max_q_len * q_heads * 128 * 8;  // at most
+    int64_t best = 0;
+    for (int64_t parts = 1; units > 0 && parts <= 64 && (parts == 1 || parts * kKv4PrefillMin <= cap); ++parts) {
+      const int64_t rounds = (units * parts + sms - 1) / sms;
+      const int64_t cost = rounds * (28 + 3 * ((tiles + parts - 1) / parts)) +
+                           (parts > 1 ? 20 + merge_bytes * parts / 1700000 : 0);
+      if (best == 0 || cost < best) {
+        best = cost;
+        split = (tiles + parts - 1) / parts * kKv4PrefillUnit;
+      }
     }
   }
   if (split <= 0 || split % kKv4PrefillUnit != 0) return PA_ERR_INVALID;
@@ -142,7 +153,7 @@ int pa_quantize_and_cache(const void* k, const void* v, int64_t k_stride, int64_
   p.num_tokens = num_tokens;
   p.num_slots = (int64_t)num_blocks * block_size;
   p.kv_heads = kv_heads;
-  p.block_size = block_size;
+  p.block_shift = log2_of(block_size);
   return cuda_status(launch_quantize_and_cache(p, head_dim, dtype, to_stream(stream)));
 }
 
@@ -166,7 +177,7 @@ int pa_dequantize_kv4(const void* k_cache, const void* v_cache, const int32_t* s
   p.num_tokens = num_tokens;
   p.num_slots = (int64_t)num_blocks * block_size;
   p.kv_heads = kv_heads;
-  p.block_size = block_size;
+  p.block_shift = log2_of(block_size);
   return cuda_status(launch_dequantize_kv4(p, head_dim, dtype, to_stream(stream)));
 }
 
@@ -312,6 +323,7 @@ int pa_chunked_prefill_kv4(const void* q, const int32_t* q_start, const int32_t*
   p.split_tokens = s.split;
   p.max_splits = s.max_splits;
   p.row_tiles = s.row_tiles;
+  p.longest_first = s.max_splits == 1 && num_reqs > 1 && (int64_t)num_reqs * kv_heads * s.row_tiles > num_sms();
   p.negative = scale < 0.f;
   p.scale_log2 = std::fabs(scale) * 1.4426950408889634f;
   return cuda_status(launch_kv4_prefill(p, head_dim, dtype, to_stream(stream)));
