@@ -22,9 +22,11 @@
 //   write   tables, lengths, pairs and slots
 //
 // The steps are dependent and small: a table of 64 sequences of 4096 tokens is
-// 64 KB.  So up to kFusedWork entries they are one launch of one cluster of
-// eight CTAs with its barrier between them; above it each step is a launch over
-// the whole GPU.
+// 64 KB.  So up to kClusterWork entries they are one launch of one cluster of
+// eight CTAs, with its barrier between them; above it one cooperative launch of
+// a CTA per SM.
+#include <cooperative_groups.h>
+
 #include "pa_device.cuh"
 #include "pa_internal.h"
 
@@ -40,50 +42,53 @@ constexpr int kWarpsPerCta = kThreads / 32;
 constexpr int kColumns = 512;  // of a row that a warp takes at a time
 constexpr int kCluster = 8;
 
+// A new row.  One without a sequence has parent kNone and nothing else, but for
+// the error code of a refused one (as a negative growth).
+constexpr int kNone = -2;
 struct Row {
-  int parent;  // < 0: none
-  int len, have, want;  // tokens; pages of them, and with the new tokens
-  int grow;
-  int tail;    // page it goes on inside, or -1
-  int bad;     // error code of a row that is dropped
+  int parent, len, grow;
+  int tail;  // page it goes on inside, or -1
 };
 
-__device__ __forceinline__ Row fork_row(const ForkParams& p, int i) {
-  Row w{};
-  w.parent = -1;
-  w.tail = -1;
+__device__ __forceinline__ int pages_of(const ForkParams& p, int tokens) {  // tokens below 2^31 - 32
+  return (tokens + p.block_size - 1) >> p.block_shift;
+}
+__device__ __forceinline__ int have_of(const ForkParams& p, const Row& w) { return pages_of(p, w.len); }
+__device__ __forceinline__ int want_of(const ForkParams& p, const Row& w) { return pages_of(p, w.len + max(w.grow, 0)); }
+
+__device__ __forceinline__ Row load_row(const ForkParams& p, int i) {
+  Row w{kNone, 0, 0, -1};
   const int parent = __ldcg(p.parents + i);
-  if (parent < -1) return w;  // no sequence
-  if (parent >= p.num_old) {
-    w.bad = PA_DEVERR_FORK;
-    return w;
-  }
+  if (parent < -1) return w;
   const int grow = p.grow ? __ldcg(p.grow + i) : p.max_grow;
-  if (grow < 0 || grow > p.max_grow) {
-    w.bad = PA_DEVERR_FORK;
+  if (parent >= p.num_old || grow < 0 || grow > p.max_grow) {
+    w.grow = -PA_DEVERR_FORK;
     return w;
   }
   const int len = parent < 0 ? 0 : __ldcg(p.lens + parent);
-  if (len < 0 || len > p.maxblk * p.block_size) {
-    w.bad = PA_DEVERR_CONTEXT_LEN;
-    return w;
-  }
-  const int have = (len + p.block_size - 1) >> p.block_shift;
-  const int64_t want = ((int64_t)len + grow + p.block_size - 1) >> p.block_shift;
-  if (want > p.maxblk_out) {
-    w.bad = PA_DEVERR_CONTEXT_LEN;
+  if (len < 0 || len > p.maxblk * p.block_size || ((int64_t)len + grow) > (int64_t)p.maxblk_out * p.block_size) {
+    w.grow = -PA_DEVERR_CONTEXT_LEN;
     return w;
   }
   w.parent = parent;
   w.len = len;
-  w.have = have;
-  w.want = (int)want;
   w.grow = grow;
   if (parent >= 0 && grow > 0 && (len & (p.block_size - 1))) {
-    const int b = __ldcg(p.tables + (size_t)parent * p.maxblk + have - 1);
+    const int b = __ldcg(p.tables + (size_t)parent * p.maxblk + (len >> p.block_shift));
     if (b >= 0 && b < p.num_blocks) w.tail = b;
   }
   return w;
+}
+
+// Every step asks for new rows, and to find out what one is takes three loads,
+// one behind the other: a CTA does that once, for as many as it has room for.
+constexpr int kHeldRows = 1024;
+__device__ void hold_rows(const ForkParams& p, Row* held) {
+  for (int i = threadIdx.x; i < min(p.num_new, kHeldRows); i += kThreads) held[i] = load_row(p, i);
+  __syncthreads();
+}
+__device__ __forceinline__ Row row_of(const ForkParams& p, const Row* held, int i) {
+  return i < kHeldRows ? held[i] : load_row(p, i);
 }
 
 // Does row i, which goes on inside page w.tail, need a copy of it?
@@ -99,7 +104,7 @@ __device__ void step_clear(const ForkParams& p, int rank, int ranks) {
   for (int b = rank * kThreads + threadIdx.x; b < p.num_blocks; b += ranks * kThreads) p.state[b] = kFree;
 }
 
-__device__ void step_mark(const ForkParams& p, int rank, int ranks) {
+__device__ void step_mark(const ForkParams& p, const Row* held, int rank, int ranks) {
   const int lane = threadIdx.x & 31;
   const int chunks = (p.maxblk + kColumns - 1) / kColumns;
   const int64_t items = (int64_t)p.num_old * chunks;
@@ -110,30 +115,29 @@ __device__ void step_mark(const ForkParams& p, int rank, int ranks) {
     bool some = false, rests = false;
     int have = 0;
     for (int i = lane; i < p.num_new; i += 32) {
-      if (__ldcg(p.parents + i) != old) continue;
-      const Row w = fork_row(p, i);
+      if ((i < kHeldRows ? held[i].parent : __ldcg(p.parents + i)) != old) continue;
+      const Row w = row_of(p, held, i);
       if (w.parent < 0) continue;
       some = true;
-      have = w.have;
+      have = have_of(p, w);
       if (w.tail >= 0) {
         if (c0 == 0) atomicMin(p.state + w.tail, i);
       } else {
         rests = true;
       }
     }
-    some = __any_sync(kAll, some);
-    if (!some) continue;
+    if (!__any_sync(kAll, some)) continue;
     rests = __any_sync(kAll, rests);
     have = __reduce_max_sync(kAll, have);
     const int end = min(have - (rests ? 0 : 1), c0 + kColumns);
     const int32_t* row = p.tables + (size_t)old * p.maxblk;
     bool bad = false;
-    for (int j = c0 + lane; j < end; j += 4 * 32) {
-      int b[4];
+    for (int j = c0 + lane; j < end; j += 8 * 32) {
+      int b[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) b[k] = j + 32 * k < end ? __ldcg(row + j + 32 * k) : -1;
+      for (int k = 0; k < 8; ++k) b[k] = j + 32 * k < end ? __ldcg(row + j + 32 * k) : -1;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 8; ++k) {
         if (j + 32 * k >= end) continue;
         if (b[k] >= 0 && b[k] < p.num_blocks) p.state[b[k]] = kHeld;
         else bad = true;
@@ -155,13 +159,14 @@ __device__ void step_count(const ForkParams& p, int rank, int ranks) {
   const int64_t b0 = (int64_t)warp * span;
   const int b1 = (int)min((int64_t)p.num_blocks, b0 + span);
   int n = 0;
+#pragma unroll 4
   for (int64_t b = b0 + lane; b < b1; b += 32) n += is_free(p, (int)b);
   n = __reduce_add_sync(kAll, n);
   if (lane == 0) p.warp_free[warp] = n;
 }
 
 // One CTA: where each row's pages start in the list, and how many are needed.
-__device__ void step_rows(const ForkParams& p) {
+__device__ void step_rows(const ForkParams& p, const Row* held) {
   __shared__ int sums[kWarpsPerCta + 1];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t before = 0;
@@ -169,9 +174,9 @@ __device__ void step_rows(const ForkParams& p) {
     const int i = base + threadIdx.x;
     int need = 0;
     if (i < p.num_new) {
-      const Row w = fork_row(p, i);
-      if (w.bad) record_error(p.err, w.bad);
-      need = w.want - w.have + needs_copy(p, w, i);
+      const Row w = row_of(p, held, i);
+      if (w.grow < 0) record_error(p.err, -w.grow);
+      need = want_of(p, w) - have_of(p, w) + needs_copy(p, w, i);
     }
     int x = need;  // inclusive in the warp
 #pragma unroll
@@ -238,7 +243,7 @@ __device__ void step_list(const ForkParams& p, int rank, int ranks) {
   __syncthreads();  // total and part may be used again
 }
 
-__device__ void step_write(const ForkParams& p, int rank, int ranks) {
+__device__ void step_write(const ForkParams& p, const Row* held, int rank, int ranks) {
   const int lane = threadIdx.x & 31;
   const int chunks = (p.maxblk_out + kColumns - 1) / kColumns;
   const int64_t items = (int64_t)p.num_new * chunks;
@@ -248,41 +253,35 @@ __device__ void step_write(const ForkParams& p, int rank, int ranks) {
     const int i = (int)(it / chunks), c0 = (int)(it - (int64_t)i * chunks) * kColumns;
     const int end = min(p.maxblk_out, c0 + kColumns);
     int32_t* dst = p.tables_out + (size_t)i * p.maxblk_out;
-    Row w = fork_row(p, i);
-    if (refused) {
-      w.parent = -1;
-      w.len = w.have = w.want = w.grow = 0;
-      w.tail = -1;
-    }
+    const Row w = refused ? Row{kNone, 0, 0, -1} : row_of(p, held, i);
+    const int have = have_of(p, w), want = want_of(p, w), grow = max(w.grow, 0);
     const bool copy = needs_copy(p, w, i);
     const int32_t* src = p.tables + (size_t)max(w.parent, 0) * p.maxblk;
-    const int32_t* fresh = p.list + (w.want > w.have || copy ? __ldcg(p.row_start + i) : 0);
-    for (int j = c0 + lane; j < end; j += 4 * 32) {
-      int b[4];
+    const int32_t* fresh = p.list + (want > have || copy ? __ldcg(p.row_start + i) : 0);
+    for (int j = c0 + lane; j < end; j += 8 * 32) {
+      int b[8];
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
+      for (int k = 0; k < 8; ++k) {
         const int c = j + 32 * k;
         b[k] = -1;
-        if (c < end && c < w.want)
-          b[k] = c >= w.have          ? __ldcg(fresh + copy + c - w.have)
-                 : copy && c == w.have - 1 ? __ldcg(fresh)
-                                           : __ldcg(src + c);
+        if (c < end && c < want)
+          b[k] = c >= have ? __ldcg(fresh + copy + c - have) : copy && c == have - 1 ? __ldcg(fresh) : __ldcg(src + c);
       }
 #pragma unroll
-      for (int k = 0; k < 4; ++k)
+      for (int k = 0; k < 8; ++k)
         if (j + 32 * k < end) dst[j + 32 * k] = b[k];
     }
     if (c0 == 0) {
       if (lane == 0) {
-        p.lens_out[i] = w.len + w.grow;
+        p.lens_out[i] = w.len + grow;
         p.pairs[2 * i] = copy ? w.tail : -1;
         p.pairs[2 * i + 1] = copy ? __ldcg(fresh) : -1;
       }
       for (int t = lane; t < p.max_grow; t += 32) {
         int slot = -1;
-        if (t < w.grow) {
+        if (t < grow) {
           const int pos = w.len + t, c = pos >> p.block_shift;
-          const int b = c >= w.have ? __ldcg(fresh + copy + c - w.have) : copy ? __ldcg(fresh) : __ldcg(src + c);
+          const int b = c >= have ? __ldcg(fresh + copy + c - have) : copy ? __ldcg(fresh) : __ldcg(src + c);
           if (b >= 0 && b < p.num_blocks) slot = b * p.block_size + (pos & (p.block_size - 1));
         }
         p.slots[(size_t)i * p.max_grow + t] = slot;
@@ -291,34 +290,30 @@ __device__ void step_write(const ForkParams& p, int rank, int ranks) {
   }
 }
 
-__global__ void __launch_bounds__(kThreads) fork_fused_kernel(const ForkParams p) {
-  griddep_wait();  // and no early start of the next kernel, which may read the tables before it waits
-  const int rank = (int)cluster_rank(), ranks = (int)cluster_size();
+// The steps, `sync` a barrier of all ranks' threads that makes their writes seen.
+template <typename Sync>
+__device__ __forceinline__ void fork_steps(const ForkParams& p, int rank, int ranks, Sync sync) {
+  __shared__ Row held[kHeldRows];
   step_clear(p, rank, ranks);
-  cluster_sync();
-  step_mark(p, rank, ranks);
-  cluster_sync();
-  if (rank == ranks - 1) step_rows(p);
+  hold_rows(p, held);
+  sync();
+  step_mark(p, held, rank, ranks);
+  sync();
+  if (rank == ranks - 1) step_rows(p, held);
   step_count(p, rank, ranks);
-  cluster_sync();
+  sync();
   step_list(p, rank, ranks);
-  cluster_sync();
-  step_write(p, rank, ranks);
+  sync();
+  step_write(p, held, rank, ranks);
 }
 
-template <int STEP>
-__global__ void __launch_bounds__(kThreads) fork_step_kernel(const ForkParams p) {
-  griddep_wait();
-  const int rank = blockIdx.x, ranks = gridDim.x;
-  if constexpr (STEP < 4) griddep_launch_dependents();
-  if constexpr (STEP == 0) step_clear(p, rank, ranks);
-  if constexpr (STEP == 1) step_mark(p, rank, ranks);
-  if constexpr (STEP == 2) {
-    if (rank == ranks - 1) step_rows(p);
-    step_count(p, rank, ranks);
-  }
-  if constexpr (STEP == 3) step_list(p, rank, ranks);
-  if constexpr (STEP == 4) step_write(p, rank, ranks);
+__global__ void __launch_bounds__(kThreads) fork_cluster_kernel(const ForkParams p) {
+  griddep_wait();  // and no early start of the next kernel, which may read the tables before it waits
+  fork_steps(p, (int)cluster_rank(), (int)cluster_size(), [] { cluster_sync(); });
+}
+
+__global__ void __launch_bounds__(kThreads) fork_grid_kernel(const ForkParams p) {
+  fork_steps(p, blockIdx.x, gridDim.x, [] { cooperative_groups::this_grid().sync(); });
 }
 
 // ----------------------------------------------------------------------------
@@ -353,7 +348,7 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__
 
 int fork_ranks() {
   const int sms = num_sms();
-  return 2 * (sms > 0 ? sms : 1);
+  return sms > 0 ? sms : 1;
 }
 
 }  // namespace
@@ -374,16 +369,21 @@ ForkWorkspace fork_workspace_layout(int num_new, int num_blocks) {
 
 cudaError_t launch_fork_blocks(const ForkParams& p, cudaStream_t stream) {
   // Entries that the steps go over.
-  constexpr int64_t kFusedWork = 1 << 18;
+  constexpr int64_t kClusterWork = 1 << 17;
   const int64_t work = (int64_t)p.num_old * p.maxblk + (int64_t)p.num_new * p.maxblk_out + p.num_blocks;
-  if (work <= kFusedWork)
-    return launch_pdl_cluster(fork_fused_kernel, kCluster, dim3(kCluster), dim3(kThreads), 0, stream, p);
-  const dim3 grid(fork_ranks()), block(kThreads);
-  cudaError_t e = launch_pdl(fork_step_kernel<0>, grid, block, 0, stream, p);
-  if (e == cudaSuccess) e = launch_pdl(fork_step_kernel<1>, grid, block, 0, stream, p);
-  if (e == cudaSuccess) e = launch_pdl(fork_step_kernel<2>, grid, block, 0, stream, p);
-  if (e == cudaSuccess) e = launch_pdl(fork_step_kernel<3>, grid, block, 0, stream, p);
-  if (e == cudaSuccess) e = launch_pdl(fork_step_kernel<4>, grid, block, 0, stream, p);
+  if (work <= kClusterWork)
+    return launch_pdl_cluster(fork_cluster_kernel, kCluster, dim3(kCluster), dim3(kThreads), 0, stream, p);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(fork_ranks());
+  cfg.blockDim = dim3(kThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, fork_grid_kernel, p);
+  if (e == cudaSuccess) note_launch();
   return e;
 }
 
