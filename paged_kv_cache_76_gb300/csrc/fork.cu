@@ -22,9 +22,9 @@
 //   write   tables, lengths, pairs and slots
 //
 // The steps are dependent and small: a table of 64 sequences of 4096 tokens is
-// 64 KB.  So up to kClusterWork entries they are one launch of one cluster of
-// eight CTAs, with its barrier between them; above it one cooperative launch of
-// a CTA per SM.
+// 64 KB, so what they cost is the barriers between them.  Small batches are one
+// CTA's, with the scratch in its shared memory; above that it is one cooperative
+// launch of a CTA per SM.
 #include <cooperative_groups.h>
 
 #include "pa_device.cuh"
@@ -37,10 +37,15 @@ namespace {
 constexpr int kFree = 0x7F7F7F7F;
 constexpr int kHeld = -1;
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kThreads = 512;
-constexpr int kWarpsPerCta = kThreads / 32;
+constexpr int kCtaThreads = 512;   // of the one CTA of small batches
+constexpr int kGridThreads = 256;  // of a CTA per SM
+constexpr int kMaxWarps = 16;
 constexpr int kColumns = 512;  // of a row that a warp takes at a time
-constexpr int kCluster = 8;
+
+__device__ __forceinline__ int warps_per_cta() { return (int)blockDim.x >> 5; }
+
+// Scratch that other CTAs write (or, of one CTA, shared memory): never from L1.
+__device__ __forceinline__ int ld_scratch(const int32_t* p) { return *reinterpret_cast<const volatile int32_t*>(p); }
 
 // A new row.  One without a sequence has parent kNone and nothing else, but for
 // the error code of a refused one (as a negative growth).
@@ -84,7 +89,7 @@ __device__ __forceinline__ Row load_row(const ForkParams& p, int i) {
 // one behind the other: a CTA does that once, for as many as it has room for.
 constexpr int kHeldRows = 1024;
 __device__ void hold_rows(const ForkParams& p, Row* held) {
-  for (int i = threadIdx.x; i < min(p.num_new, kHeldRows); i += kThreads) held[i] = load_row(p, i);
+  for (int i = threadIdx.x; i < min(p.num_new, kHeldRows); i += (int)blockDim.x) held[i] = load_row(p, i);
   __syncthreads();
 }
 __device__ __forceinline__ Row row_of(const ForkParams& p, const Row* held, int i) {
@@ -93,23 +98,23 @@ __device__ __forceinline__ Row row_of(const ForkParams& p, const Row* held, int 
 
 // Does row i, which goes on inside page w.tail, need a copy of it?
 __device__ __forceinline__ bool needs_copy(const ForkParams& p, const Row& w, int i) {
-  return w.tail >= 0 && (__ldcg(p.state + w.tail) != i || (p.pinned && __ldg(p.pinned + w.tail)));
+  return w.tail >= 0 && (ld_scratch(p.state + w.tail) != i || (p.pinned && __ldg(p.pinned + w.tail)));
 }
 
 __device__ __forceinline__ bool is_free(const ForkParams& p, int b) {
-  return __ldcg(p.state + b) == kFree && !(p.pinned && __ldg(p.pinned + b));
+  return ld_scratch(p.state + b) == kFree && !(p.pinned && __ldg(p.pinned + b));
 }
 
 __device__ void step_clear(const ForkParams& p, int rank, int ranks) {
-  for (int b = rank * kThreads + threadIdx.x; b < p.num_blocks; b += ranks * kThreads) p.state[b] = kFree;
+  for (int b = rank * (int)blockDim.x + threadIdx.x; b < p.num_blocks; b += ranks * (int)blockDim.x) p.state[b] = kFree;
 }
 
 __device__ void step_mark(const ForkParams& p, const Row* held, int rank, int ranks) {
   const int lane = threadIdx.x & 31;
   const int chunks = (p.maxblk + kColumns - 1) / kColumns;
   const int64_t items = (int64_t)p.num_old * chunks;
-  for (int64_t it = (int64_t)rank * kWarpsPerCta + (threadIdx.x >> 5); it < items;
-       it += (int64_t)ranks * kWarpsPerCta) {
+  for (int64_t it = (int64_t)rank * warps_per_cta() + (threadIdx.x >> 5); it < items;
+       it += (int64_t)ranks * warps_per_cta()) {
     const int old = (int)(it / chunks), c0 = (int)(it - (int64_t)old * chunks) * kColumns;
     // the new rows that go on from this one: any at all, any that leaves its tail as it is
     bool some = false, rests = false;
@@ -149,12 +154,12 @@ __device__ void step_mark(const ForkParams& p, const Row* held, int rank, int ra
 
 // Warp w of all takes blocks [w * span, (w + 1) * span).
 __device__ __forceinline__ int span_of(const ForkParams& p, int ranks) {
-  const int warps = ranks * kWarpsPerCta;
+  const int warps = ranks * warps_per_cta();
   return ((p.num_blocks + warps - 1) / warps + 31) & ~31;
 }
 
 __device__ void step_count(const ForkParams& p, int rank, int ranks) {
-  const int warp = rank * kWarpsPerCta + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  const int warp = rank * warps_per_cta() + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int span = span_of(p, ranks);
   const int64_t b0 = (int64_t)warp * span;
   const int b1 = (int)min((int64_t)p.num_blocks, b0 + span);
@@ -167,10 +172,10 @@ __device__ void step_count(const ForkParams& p, int rank, int ranks) {
 
 // One CTA: where each row's pages start in the list, and how many are needed.
 __device__ void step_rows(const ForkParams& p, const Row* held) {
-  __shared__ int sums[kWarpsPerCta + 1];
+  __shared__ int sums[kMaxWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int64_t before = 0;
-  for (int base = 0; base < p.num_new; base += kThreads) {
+  for (int base = 0; base < p.num_new; base += (int)blockDim.x) {
     const int i = base + threadIdx.x;
     int need = 0;
     if (i < p.num_new) {
@@ -187,7 +192,7 @@ __device__ void step_rows(const ForkParams& p, const Row* held) {
     if (lane == 31) sums[warp] = x;
     __syncthreads();
     int64_t at = before + x - need;
-    for (int w = 0; w < kWarpsPerCta; ++w) {
+    for (int w = 0; w < warps_per_cta(); ++w) {
       if (w < warp) at += sums[w];
       before += sums[w];
     }
@@ -199,16 +204,16 @@ __device__ void step_rows(const ForkParams& p, const Row* held) {
 }
 
 __device__ void step_list(const ForkParams& p, int rank, int ranks) {
-  __shared__ int part[kWarpsPerCta];
+  __shared__ int part[kMaxWarps];
   __shared__ int total;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int mine = rank * kWarpsPerCta + warp, warps = ranks * kWarpsPerCta;
+  const int mine = rank * warps_per_cta() + warp, warps = ranks * warps_per_cta();
   // free pages before this CTA's spans, and of all
   int before = 0, all = 0;
-  for (int w = threadIdx.x; w < warps; w += kThreads) {
-    const int n = __ldcg(p.warp_free + w);
+  for (int w = threadIdx.x; w < warps; w += (int)blockDim.x) {
+    const int n = ld_scratch(p.warp_free + w);
     all += n;
-    if (w < rank * kWarpsPerCta) before += n;
+    if (w < rank * warps_per_cta()) before += n;
   }
   before = __reduce_add_sync(kAll, before);
   all = __reduce_add_sync(kAll, all);
@@ -220,16 +225,15 @@ __device__ void step_list(const ForkParams& p, int rank, int ranks) {
   }
   __syncthreads();
   int at = 0;
-#pragma unroll
-  for (int w = 0; w < kWarpsPerCta; ++w) at += part[w];
-  const int needed = __ldcg(p.needed);
+  for (int w = 0; w < warps_per_cta(); ++w) at += part[w];
+  const int needed = ld_scratch(p.needed);
   if (rank == 0 && threadIdx.x == 0) {
     const bool short_of = needed > total;
     if (short_of) record_error(p.err, PA_DEVERR_NO_BLOCKS);
     *p.num_free = short_of ? total : total - needed;
     *p.refused = short_of;
   }
-  for (int w = rank * kWarpsPerCta; w < mine; ++w) at += __ldcg(p.warp_free + w);
+  for (int w = rank * warps_per_cta(); w < mine; ++w) at += ld_scratch(p.warp_free + w);
   const int span = span_of(p, ranks);
   const int64_t b0 = (int64_t)mine * span;
   const int b1 = (int)min((int64_t)p.num_blocks, b0 + span);
@@ -247,9 +251,9 @@ __device__ void step_write(const ForkParams& p, const Row* held, int rank, int r
   const int lane = threadIdx.x & 31;
   const int chunks = (p.maxblk_out + kColumns - 1) / kColumns;
   const int64_t items = (int64_t)p.num_new * chunks;
-  const bool refused = __ldcg(p.refused) != 0;
-  for (int64_t it = (int64_t)rank * kWarpsPerCta + (threadIdx.x >> 5); it < items;
-       it += (int64_t)ranks * kWarpsPerCta) {
+  const bool refused = ld_scratch(p.refused) != 0;
+  for (int64_t it = (int64_t)rank * warps_per_cta() + (threadIdx.x >> 5); it < items;
+       it += (int64_t)ranks * warps_per_cta()) {
     const int i = (int)(it / chunks), c0 = (int)(it - (int64_t)i * chunks) * kColumns;
     const int end = min(p.maxblk_out, c0 + kColumns);
     int32_t* dst = p.tables_out + (size_t)i * p.maxblk_out;
@@ -257,7 +261,7 @@ __device__ void step_write(const ForkParams& p, const Row* held, int rank, int r
     const int have = have_of(p, w), want = want_of(p, w), grow = max(w.grow, 0);
     const bool copy = needs_copy(p, w, i);
     const int32_t* src = p.tables + (size_t)max(w.parent, 0) * p.maxblk;
-    const int32_t* fresh = p.list + (want > have || copy ? __ldcg(p.row_start + i) : 0);
+    const int32_t* fresh = p.list + (want > have || copy ? ld_scratch(p.row_start + i) : 0);
     for (int j = c0 + lane; j < end; j += 8 * 32) {
       int b[8];
 #pragma unroll
@@ -265,7 +269,7 @@ __device__ void step_write(const ForkParams& p, const Row* held, int rank, int r
         const int c = j + 32 * k;
         b[k] = -1;
         if (c < end && c < want)
-          b[k] = c >= have ? __ldcg(fresh + copy + c - have) : copy && c == have - 1 ? __ldcg(fresh) : __ldcg(src + c);
+          b[k] = c >= have ? ld_scratch(fresh + copy + c - have) : copy && c == have - 1 ? ld_scratch(fresh) : __ldcg(src + c);
       }
 #pragma unroll
       for (int k = 0; k < 8; ++k)
@@ -275,13 +279,13 @@ __device__ void step_write(const ForkParams& p, const Row* held, int rank, int r
       if (lane == 0) {
         p.lens_out[i] = w.len + grow;
         p.pairs[2 * i] = copy ? w.tail : -1;
-        p.pairs[2 * i + 1] = copy ? __ldcg(fresh) : -1;
+        p.pairs[2 * i + 1] = copy ? ld_scratch(fresh) : -1;
       }
       for (int t = lane; t < p.max_grow; t += 32) {
         int slot = -1;
         if (t < grow) {
           const int pos = w.len + t, c = pos >> p.block_shift;
-          const int b = c >= have ? __ldcg(fresh + copy + c - have) : copy ? __ldcg(fresh) : __ldcg(src + c);
+          const int b = c >= have ? ld_scratch(fresh + copy + c - have) : copy ? ld_scratch(fresh) : __ldcg(src + c);
           if (b >= 0 && b < p.num_blocks) slot = b * p.block_size + (pos & (p.block_size - 1));
         }
         p.slots[(size_t)i * p.max_grow + t] = slot;
@@ -307,12 +311,21 @@ __device__ __forceinline__ void fork_steps(const ForkParams& p, int rank, int ra
   step_write(p, held, rank, ranks);
 }
 
-__global__ void __launch_bounds__(kThreads) fork_cluster_kernel(const ForkParams p) {
+// One CTA, its scratch in shared memory: a step is a barrier, not a trip to L2.
+__global__ void __launch_bounds__(kCtaThreads) fork_cta_kernel(const ForkParams p0) {
+  extern __shared__ __align__(16) int32_t scratch[];
   griddep_wait();  // and no early start of the next kernel, which may read the tables before it waits
-  fork_steps(p, (int)cluster_rank(), (int)cluster_size(), [] { cluster_sync(); });
+  ForkParams p = p0;
+  p.state = scratch;
+  p.list = p.state + p.num_blocks;
+  p.row_start = p.list + p.num_blocks;
+  p.warp_free = p.row_start + p.num_new;
+  p.needed = p.warp_free + kMaxWarps;
+  p.refused = p.needed + 1;
+  fork_steps(p, 0, 1, [] { __syncthreads(); });
 }
 
-__global__ void __launch_bounds__(kThreads) fork_grid_kernel(const ForkParams p) {
+__global__ void __launch_bounds__(kGridThreads) fork_grid_kernel(const ForkParams p) {
   fork_steps(p, blockIdx.x, gridDim.x, [] { cooperative_groups::this_grid().sync(); });
 }
 
@@ -346,6 +359,9 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__
   }
 }
 
+constexpr int kCtaBlocks = 16384;
+int cta_scratch(int num_blocks, int num_new) { return (2 * num_blocks + num_new + kMaxWarps + 2) * 4; }
+
 int fork_ranks() {
   const int sms = num_sms();
   return sms > 0 ? sms : 1;
@@ -361,21 +377,33 @@ ForkWorkspace fork_workspace_layout(int num_new, int num_blocks) {
   w.list = al((size_t)num_blocks * 4);
   w.row_start = w.list + al((size_t)num_blocks * 4);
   w.warp_free = w.row_start + al((size_t)num_new * 4);
-  const int ranks = fork_ranks() > kCluster ? fork_ranks() : kCluster;
-  w.needed = w.warp_free + al((size_t)ranks * kWarpsPerCta * 4);
+  w.needed = w.warp_free + al((size_t)fork_ranks() * (kGridThreads / 32) * 4);
   w.bytes = w.needed + 256;
   return w;
 }
 
 cudaError_t launch_fork_blocks(const ForkParams& p, cudaStream_t stream) {
-  // Entries that the steps go over.
-  constexpr int64_t kClusterWork = 1 << 17;
+  // Entries that the steps go over, up to which one CTA is the faster: it needs no
+  // barrier of the whole grid, about two microseconds each.  Measured on GB300 (us,
+  // one CTA and a CTA per SM): 16 rows of <= 95 blocks 5.7 and 12; 512 of <= 256
+  // 70 and 15.8; 64 of <= 8190 (more blocks than it has room for) 16.1.
+  constexpr int64_t kCtaWork = 48 << 10;
   const int64_t work = (int64_t)p.num_old * p.maxblk + (int64_t)p.num_new * p.maxblk_out + p.num_blocks;
-  if (work <= kClusterWork)
-    return launch_pdl_cluster(fork_cluster_kernel, kCluster, dim3(kCluster), dim3(kThreads), 0, stream, p);
+  if (p.num_blocks <= kCtaBlocks && p.num_new <= kHeldRows && work <= kCtaWork) {
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev < 64 && !attr_set[dev]) {
+      const cudaError_t e = cudaFuncSetAttribute(fork_cta_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                 cta_scratch(kCtaBlocks, kHeldRows));
+      if (e != cudaSuccess) return e;
+      attr_set[dev] = true;
+    }
+    return launch_pdl(fork_cta_kernel, dim3(1), dim3(kCtaThreads), cta_scratch(p.num_blocks, p.num_new), stream, p);
+  }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(fork_ranks());
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(kGridThreads);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeCooperative;
