@@ -98,6 +98,13 @@ __device__ __forceinline__ uint32_t lds_u8(uint32_t at, int off) {
   asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(at + off));
   return v;
 }
+// The low four bits of every byte of a, the high four of b (one instruction;
+// written as & and | it became two).
+__device__ __forceinline__ uint32_t low_halves(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xCA;" : "=r"(r) : "r"(0x0F0F0F0Fu), "r"(a), "r"(b));
+  return r;
+}
 __device__ __forceinline__ void cp_async16_at(uint32_t dst, int off, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + off), "l"(src) : "memory");
 }
@@ -421,8 +428,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const uint32_t a = va[e][0][i], b = va[e][1][i];
-        kv4_unpack((a & 0x0F0F0F0Fu) | ((b << 4) & 0xF0F0F0F0u), u[e]);
-        kv4_unpack(((a >> 4) & 0x0F0F0F0Fu) | (b & 0xF0F0F0F0u), z[e]);
+        kv4_unpack(low_halves(a, b << 4), u[e]);
+        kv4_unpack(low_halves(a >> 4, b), z[e]);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           u[e][k] = hmul2_u(u[e][k], vs2[e]);
