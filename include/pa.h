@@ -30,8 +30,8 @@
  *   inputs must be ready when the call is enqueued (they are if whatever writes
  *   them was enqueued earlier on the stream without allowing early launch of
  *   its successor, as plain kernels and copies do; pa_norm_rope_and_cache, whose
- *   q_out is such an input, and pa_evict_select, whose keep_lens may be, do the
- *   same).
+ *   q_out is such an input, pa_evict_select, whose keep_lens may be, and
+ *   pa_fork_blocks, whose tables and lengths are, do the same).
  * - Errors: every call returns a pa_status.  Argument errors are caught on the
  *   host before anything is launched.  Data errors that only the device can
  *   see (a block id outside [0, num_blocks), a slot past the pool, a context

@@ -207,3 +207,35 @@ def test_captured_and_on_another_stream(ops):
         assert all(torch.equal(a, b) for a, b in zip(out, want))
         assert torch.equal(after, cache)
     assert ops.get_device_error() == 0
+
+
+def test_a_large_batch_captured_and_two_at_once(ops):
+    """The cooperative form in a graph, and two calls on two streams."""
+    rng = np.random.default_rng(9)
+    batches = []
+    for seed in range(2):
+        tables, lens = batch(rng, 300, 4, 900, 90000, 0.7)
+        batches.append((i32(tables), i32(lens), i32(rng.integers(-1, 300, 400))))
+    want = [ops.fork_blocks(*b, 90000, 4, grow=2, max_blocks=226) for b in batches]
+    graphs, outs = [], []
+    for b in batches:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(ops.fork_blocks(*b, 90000, 4, grow=2, max_blocks=226))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for o in outs:
+            for x in o:
+                x.fill_(-9)
+        torch.cuda.synchronize()
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert all(torch.equal(x, y) for x, y in zip(o, w))
+    ws = torch.empty(8 << 20, dtype=torch.uint8, device="cuda")
+    again = ops.fork_blocks(*batches[0], 90000, 4, grow=2, max_blocks=226, workspace=ws)
+    assert all(torch.equal(x, y) for x, y in zip(again, want[0]))
+    assert ops.get_device_error() == 0

@@ -402,6 +402,61 @@ def test_another_stream_a_capture_and_a_recording(ops):
     assert ops.get_device_error() == 0
 
 
+def test_two_calls_at_once_and_a_given_workspace(ops):
+    b = Batch(ops, [700, 5, 300], 2, 128, 16, BF)
+    q, qp = b.q(3, 8), b.q(60, 8)
+    start = i32([0, 30, 35, 60])
+    want = ops.decode_kv4(q, b.kc, b.vc, b.tables, b.ctx, 0.1)
+    wantp = ops.chunked_prefill_kv4(qp, start, b.ctx, b.kc, b.vc, b.tables, 0.1, 30, split_tokens=64)
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(4)], []
+    for _ in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                if i % 2:
+                    got.append((ops.decode_kv4(q, b.kc, b.vc, b.tables, b.ctx, 0.1), want))
+                else:
+                    got.append((ops.chunked_prefill_kv4(qp, start, b.ctx, b.kc, b.vc, b.tables, 0.1, 30,
+                                                        split_tokens=64), wantp))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, w) for g, w in got)
+    ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
+    for _ in range(3):  # one scratch for calls in order
+        assert torch.equal(ops.decode_kv4(q, b.kc, b.vc, b.tables, b.ctx, 0.1, workspace=ws), want)
+        assert torch.equal(ops.chunked_prefill_kv4(qp, start, b.ctx, b.kc, b.vc, b.tables, 0.1, 30, split_tokens=64,
+                                                   workspace=ws), wantp)
+    from paged_kv_cache_76_gb300 import PAError
+    with pytest.raises(PAError):
+        ops.decode_kv4(q, b.kc, b.vc, b.tables, b.ctx, 0.1, workspace=ws[:256])
+    assert ops.get_device_error() == 0
+
+
+def test_wide_tables_and_many_requests(ops):
+    """Tables wider than the contexts, and as many requests as a call takes in one dimension of its grid."""
+    b = Batch(ops, [33, 0, 61], 1, 64, 16, BF)
+    q = b.q(3, 4)
+    wide = torch.full((3, 5000), -1, dtype=torch.int32, device="cuda")
+    wide[:, :b.tables.shape[1]] = b.tables
+    out = ops.decode_kv4(q, b.kc, b.vc, wide, b.ctx, 0.1)
+    b.check(out, q, 0.1, decode_rows(b.lens, 1))
+    n = 65535
+    big = b.tables[[0, 2]].repeat(n // 2 + 1, 1)[:n].contiguous()
+    lens = b.ctx[[0, 2]].repeat(n // 2 + 1)[:n].contiguous()
+    qs = q[[0, 2]].repeat(n // 2 + 1, 1, 1)[:n].contiguous()
+    got = ops.decode_kv4(qs, b.kc, b.vc, big, lens, 0.1)
+    for i in range(2):
+        mine = got[i::2]
+        assert torch.equal(mine, mine[:1].expand_as(mine))
+        assert float((mine[0].float() - out[2 * i].float()).abs().max()) < 0.01
+    start = torch.arange(n + 1, dtype=torch.int32, device="cuda")
+    pre = ops.chunked_prefill_kv4(qs, start, lens, b.kc, b.vc, big, 0.1, 1)
+    for i in range(2):
+        mine = pre[i::2]
+        assert torch.equal(mine, mine[:1].expand_as(mine))
+        assert float((mine[0].float() - out[2 * i].float()).abs().max()) < 0.01
+    assert ops.get_device_error() == 0
+
+
 def test_a_cache_past_two_gigabytes(ops):
     """Pages whose byte offset passes 32 bits."""
     hkv, d, bs = 8, 128, 16
