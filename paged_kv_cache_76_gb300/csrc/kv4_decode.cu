@@ -7,11 +7,26 @@
 // partitions by the log-sum-exp merge.
 //
 // At 4.5 bits an element the instructions that turn a tile into MMA operands
-// take as long as its bytes, so the kernel is built for few of them.  Every lane
-// loads just what its fragments hold, straight into registers, one tile ahead:
-// 12 loads, no shared memory in between.  (Bulk copies into a ring took 378
-// instructions a tile where this takes XXX: the copies of a divergent warp are
-// issued one by one, 15 instructions each.)
+// take about as long as its bytes, so the kernel is built for few of them.  The
+// tensor and 16-bit floating-point pipe is the one that counts: an MMA holds it
+// for 8 cycles of a quarter SM, a conversion of a pair for 1.5, a multiplication
+// for 1, so a tile costs 105 cycles of an SM if nothing waits, and its bytes 98.
+// Measured on GB300, in us: 64 requests of 509..4079 tokens, 32/8 heads (floor
+// 25), and 8 of 32768..131009, 64/8 heads (floor 116):
+//   a warp per unit, bulk copies of pages into its ring      52   197
+//   codes and scales copied apart, two tiles unrolled        48   178
+//   a CTA's four warps share a unit                          51   179
+//   16-byte asynchronous copies, block size a constant       46   162
+//   shared memory at constant offsets, copies before q       41   144
+// What was tried and left: loads straight into registers, a tile ahead (47 and
+// 184: too few bytes under way; with a prefetch to L2 six tiles ahead 50 and
+// 171); the batch's tiles shared out evenly over as many CTAs as run at a time
+// (50 and 154: CTAs that hold ends of two lists take their latencies twice, and
+// the merge has more to find out); five CTAs an SM at 96 registers (56 and 161);
+// rings of 3 or 6 tiles (no difference); first partitions of all requests first
+// (41 and 152).  A copy of a page by the bulk engine is issued lane by lane, 15
+// instructions each, which is why 16-byte copies win: 334 instructions a tile
+// against 378.
 //
 // A cache element is exact in fp16, so the products are fp16 MMAs whatever the
 // type of q: a query row is brought to [2^13, 2^14) by a power of two (taken
@@ -31,8 +46,6 @@
 //      side by side, so the codes of two tokens are interleaved before they are
 //      converted (four logical instructions for 16 elements, where 16 fp16 pairs
 //      would take 16).
-// Elements cost one conversion and one multiplication a pair (42 pairs per
-// clock and SM measured for the two together).
 //
 // Tokens past the context: their K scores become -inf by selection, and their V
 // scales 0 (codes are always finite), so nothing they hold reaches the output.

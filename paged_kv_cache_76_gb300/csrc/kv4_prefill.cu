@@ -23,6 +23,19 @@
 //  * A context may be cut into partitions of split_tokens keys, a unit each,
 //    where there are few units; a merge joins them.
 //
+// Measured on GB300 in us, a chunk of 2048 queries over 34816 tokens, 64/8 heads
+// (floor 1179 at the measured bf16 rate), and eight chunks of 257..768 over 509..
+// 4079 tokens more, 32/8 (floor 97):
+//   one warp makes K, one V                                4508   413
+//   three each, codes and scales apart                     2193   234
+//   a lane's addresses worked out once, scales as zeros    1752   198
+//   Q and outputs by whole lines, longest requests first   1752   180
+//   two partitions where rounds of units fill the SMs      1639   180
+// What is left: about 9 us to start and end a unit of 256 rows (barriers and
+// tensor memory 1, table and first pages 1.8, their tile and Q 2.5, outputs 3),
+// with nothing under them, a fifth of the second case; the MMAs of a tile at the
+// measured rate are 0.66 us of its 0.75.
+//
 // Warps: 0, 1 MMA issuers of tiles A, B; 2..7 make K and V; 8..11 softmax of
 // tile A, 12..15 of tile B.  Every wait is bounded.
 #include <float.h>

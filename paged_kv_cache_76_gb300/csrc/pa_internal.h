@@ -303,6 +303,7 @@ struct Kv4WriteParams {
   int* err;
   int64_t num_tokens, num_slots;
   int kv_heads, block_shift;
+  int wide;  // set by the launcher: every token's k and v are aligned to 32 bytes
 };
 cudaError_t launch_quantize_and_cache(const Kv4WriteParams& p, int head_dim, pa_dtype dt, cudaStream_t stream);
 
@@ -315,6 +316,7 @@ struct Kv4ReadParams {
   int* err;
   int64_t num_tokens, num_slots;
   int kv_heads, block_shift;
+  int wide;  // set by the launcher: k and v are aligned to 32 bytes
 };
 cudaError_t launch_dequantize_kv4(const Kv4ReadParams& p, int head_dim, pa_dtype dt, cudaStream_t stream);
 

@@ -47,6 +47,12 @@ int kv4_decode_setup(int num_seqs, int q_len, int q_heads, int kv_heads, int hea
   const int most = 1024 * block_size;
   int64_t split = split_tokens;
   if (split_tokens == 0) {
+    // Two rounds of the four CTAs that an SM holds, between 128 tokens (a partition
+    // below it costs more to start, end and merge than it saves) and 4096.
+    // Measured on GB300, us: 4 requests of <= 1501 tokens, 28/4 heads: 64 tokens
+    // 6.0, 128 5.5, 256 5.6, 512 6.9; 64 of <= 4079, 32/8: 512 44.6, 1024 41.9,
+    // 1376 (chosen) 41.5, 2048 44.1, 4096 52; with 4 queries each 512 79, 1024 66.5,
+    // 1376 66, 1536 65, 2048 68; 8 of <= 131009, 64/8: 1024 162, 2048 146, 4096 144.
     const int64_t sms = num_sms() > 0 ? num_sms() : 152;
     const int64_t lists = (int64_t)num_seqs * kv_heads * ((group * q_len + 15) / 16);
     const int64_t parts = lists > 0 ? (8 * sms + lists - 1) / lists : 1;
@@ -93,8 +99,9 @@ int kv4_prefill_setup(int num_reqs, int total_q, int max_q_len, int q_heads, int
     // beside its partials' way to memory and back (8 bytes an element).  Units run
     // in rounds of one per SM.  Measured on GB300: a chunk of 2048 over 34816
     // tokens, 64/8 heads (512 units of 544 tiles, 3.4 rounds) whole 1752 us, in
-    // two partitions 1640; eight chunks of 257..768 over <= 4847 tokens whole 180,
-    // in two 250; four of 37..131 over <= 1632 whole 23, in two 23, in four 33.
+    // two partitions 1639; eight chunks of 257..768 over <= 4847 tokens whole 180
+    // (in two 317, before the last steps, when whole took 235); four of 37..131
+    // over <= 1632 whole 23, in two 23 to 26, in five 22.
     const int64_t sms = num_sms() > 0 ? num_sms() : 152;
     const int64_t units = (int64_t)num_reqs * kv_heads * s->row_tiles, tiles = whole / kKv4PrefillUnit;
     const int64_t merge_bytes = (int64_t)num_reqs * max_q_len * q_heads * 128 * 8;  // at most

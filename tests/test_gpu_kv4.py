@@ -87,6 +87,23 @@ def test_written_as_defined(ops, bs, hkv, d, dtype, T):
     check_written(ops, k.contiguous(), v.contiguous(), bs, seed=1)
 
 
+@pytest.mark.parametrize("T,extra,first", [(37, 8, 0), (37, 16, 8), (1, 8, 8), (21, 24, 8)])
+def test_rows_that_begin_between_32_byte_lines(ops, T, extra, first):
+    hkv, d = 3, 64
+    row = torch.randn(T, 2 * hkv * d + extra, generator=torch.Generator(device="cuda").manual_seed(1), device="cuda").to(HF)
+    k, v = (row[:, first + i * hkv * d:first + (i + 1) * hkv * d].unflatten(1, (hkv, d)) for i in range(2))
+    check_written(ops, k, v, 8)
+    kc, vc = caches(ops, T // 8 + 1, 8, hkv, d)
+    slots = i32(np.arange(T))
+    ops.quantize_and_cache(k, v, slots, kc, vc)
+    want = ops.dequantize_kv4(kc, vc, slots, d, dtype=HF)
+    room = torch.zeros(2, T * hkv * d + 16, dtype=HF, device="cuda")
+    got = ops.dequantize_kv4(kc, vc, slots, d, dtype=HF, k=room[0, 8:8 + T * hkv * d].view(T, hkv, d),
+                             v=room[1, 8:8 + T * hkv * d].view(T, hkv, d))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.count_nonzero(room[:, :8]) == 0 and torch.count_nonzero(room[:, 8 + T * hkv * d:]) == 0
+
+
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_ties_ends_and_values_that_are_not_finite(ops, dtype):
     d = 64
