@@ -34,7 +34,7 @@
 // What is left: about 9 us to start and end a unit of 256 rows (barriers and
 // tensor memory 1, table and first pages 1.8, their tile and Q 2.5, outputs 3),
 // with nothing under them, a fifth of the second case; the MMAs of a tile at the
-// measured rate are 0.66 us of its 0.75.
+// measured rate are 0.66 us of its 0.79.
 //
 // Warps: 0, 1 MMA issuers of tiles A, B; 2..7 make K and V; 8..11 softmax of
 // tile A, 12..15 of tile B.  Every wait is bounded.
