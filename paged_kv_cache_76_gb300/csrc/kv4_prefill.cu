@@ -115,7 +115,7 @@ __device__ __forceinline__ Unit unit_of(const Kv4PrefillParams& p, int u) {
   const int qe = __ldg(p.q_start + w.r + 1), ctx = __ldg(p.lens + w.r);
   w.chunk = qe - w.qs;
   w.p0 = ctx - w.chunk;
-  if (w.qs < 0 || qe < w.qs || qe > p.total_q || w.chunk > p.max_q_len || w.p0 < 0 || ctx > p.maxblk * p.block_size) {
+  if (w.qs < 0 || qe < w.qs || qe > p.total_q || w.chunk > p.max_q_len || ctx < w.chunk || ctx > p.maxblk * p.block_size) {
     w.code = PA_DEVERR_QUERY_RANGE;
     return w;
   }
@@ -250,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
           for (int k = 0; k < bytes; k += 16) *reinterpret_cast<uint4*>(dst + k) = make_uint4(0, 0, 0, 0);
         }
       }
+      __syncwarp();  // the zeros before other lanes read them
     };
     if (first < w.ntiles) issue(first);
     bool failed = false;
@@ -597,7 +598,7 @@ __global__ void __launch_bounds__(256) kv4_prefill_merge_kernel(const Kv4Prefill
   const int r = blockIdx.y, lane = threadIdx.x & 31;
   const int qs = __ldg(p.q_start + r), qe = __ldg(p.q_start + r + 1), ctx = __ldg(p.lens + r);
   const int chunk = qe - qs, p0 = ctx - chunk, G = p.group;
-  if (qs < 0 || qe < qs || qe > p.total_q || chunk > p.max_q_len || p0 < 0 || ctx > p.maxblk * p.block_size) return;
+  if (qs < 0 || qe < qs || qe > p.total_q || chunk > p.max_q_len || ctx < chunk || ctx > p.maxblk * p.block_size) return;
   const int64_t at = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);  // (query, head)
   if (at >= (int64_t)chunk * p.q_heads) return;
   const int qi = (int)(at / p.q_heads), head = (int)(at - (int64_t)qi * p.q_heads);

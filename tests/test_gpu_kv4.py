@@ -391,6 +391,19 @@ def test_prefill_refuses_requests(ops):
     assert torch.equal(out[:10], good[:10]) and torch.equal(out[30:], good[30:])
 
 
+@pytest.mark.parametrize("split", [0, 64])
+def test_prefill_refuses_the_most_negative_length(ops, split):
+    b = Batch(ops, [60, 90], 2, 128, 16, BF)
+    q = b.q(30, 8)
+    good = ops.chunked_prefill_kv4(q, i32([0, 10, 30]), b.ctx, b.kc, b.vc, b.tables, 0.1, 20, split_tokens=split)
+    for length in (-2 ** 31, -2 ** 31 + 19, -1):  # the first two less 20 do not fit 32 bits
+        out = torch.full_like(q, 7.0)
+        ops.chunked_prefill_kv4(q, i32([0, 10, 30]), i32([60, length]), b.kc, b.vc, b.tables, 0.1, 20, out=out,
+                                split_tokens=split)
+        assert ops.get_device_error() == 5
+        assert torch.equal(out[:10], good[:10]) and bool((out[10:] == 7).all())
+
+
 def test_another_stream_a_capture_and_a_recording(ops):
     b = Batch(ops, [300, 5, 77], 2, 128, 16, BF)
     q = b.q(3, 8)
