@@ -4,7 +4,14 @@
 // A CTA of four warps owns one (request r, KV head h, partition c) unit: warp w
 // takes the tiles of 16 tokens w, w + 4, ..., every query head of the group on
 // one read of K and V; the warps' parts are joined in shared memory and the
-// partitions by the log-sum-exp merge.
+// partitions by the log-sum-exp merge, or, where all CTAs run at the same time
+// and a list has 16 partitions at most, in a cluster: each CTA writes its parts to
+// the ones that join them, all at once, and one barrier later every CTA has a
+// share of the list's outputs to write.  No partials, no second kernel (1 request
+// of 2048 tokens, 32/8 heads, in 16 partitions 5.0 -> 4.5 us, 16 in four 14 -> 11;
+// 4 of <= 1501, 28/4 heads 5.3 -> 5.0, and a call from Python 8.2 -> 5.5).  Past
+// that the CTAs of a cluster wait for one another in places that others could
+// have (64 requests below 41 -> 46).
 //
 // At 4.5 bits an element the instructions that turn a tile into MMA operands
 // take about as long as its bytes, so the kernel is built for few of them.  The
@@ -64,6 +71,7 @@ namespace pa {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kMaxCluster = kKv4Cluster;  // partitions that join their parts in one another's shared memory
 constexpr int kTile = 16;
 constexpr int kDepth = 4;  // tiles of a warp's ring
 constexpr int kMaxEntries = 1024;  // Block Table entries of a partition
@@ -80,8 +88,14 @@ struct Kv4DecodeSmem {
   static constexpr int SUM_OFF = kWarps * WARP;             // m, then l: [kWarps][NT * 8]
   static constexpr int NAN_OFF = SUM_OFF + 2 * kWarps * NT * 8 * 4;
   static constexpr int BAD_OFF = NAN_OFF + D / kKv4Group * 4;  // bits: bad block ids of the table
-  static constexpr int TAB_OFF = BAD_OFF + (kMaxEntries + 32) / 8;
-  static constexpr int bytes(int entries) { return TAB_OFF + entries * 4; }
+  // from each partition of a cluster: m, then l, of every column; the outputs that this CTA joins
+  static constexpr int PART_SUM_OFF = BAD_OFF + (kMaxEntries + 32) / 8;
+  static constexpr int PART_OFF = (PART_SUM_OFF + 2 * kMaxCluster * NT * 8 * 4 + 15) & ~15;
+  static constexpr int PART = (NT * 8 * D / 4 + kMaxCluster) * 16;
+  // then the Block Table; a call without clusters has it in the parts' place
+  static constexpr int bytes(int entries, bool cluster) {
+    return (cluster ? PART_OFF + PART : PART_SUM_OFF) + entries * 4;
+  }
 };
 
 // Shared memory at an address and a constant, after the wait that orders them
@@ -122,7 +136,8 @@ __device__ __forceinline__ void cp_async16_at(uint32_t dst, int off, const void*
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + off), "l"(src) : "memory");
 }
 
-template <int D, int NT, int BS>
+// JOIN: the partitions of a list are a cluster
+template <int D, int NT, int BS, bool JOIN>
 __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_decode_kernel(const Kv4DecodeParams p) {
   using L = Kv4DecodeSmem<D, NT>;
   using R = Kv4Row<D>;
@@ -136,12 +151,14 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
   float* sums = reinterpret_cast<float*>(smem + L::SUM_OFF);
   uint32_t* nan = reinterpret_cast<uint32_t*>(smem + L::NAN_OFF);
   uint32_t* badbits = reinterpret_cast<uint32_t*>(smem + L::BAD_OFF);
-  int32_t* tab = reinterpret_cast<int32_t*>(smem + L::TAB_OFF);
+  int32_t* tab = reinterpret_cast<int32_t*>(smem + (JOIN ? L::PART_OFF + L::PART : L::PART_SUM_OFF));
   if (threadIdx.x < D / kKv4Group) nan[threadIdx.x] = 0;
   griddep_launch_dependents();
 
   const int r = blockIdx.y;
-  const int h = blockIdx.x % p.kv_heads, c = blockIdx.x / p.kv_heads;
+  // a list's partitions side by side where they are a cluster
+  const int h = JOIN ? blockIdx.x / p.max_splits : blockIdx.x % p.kv_heads;
+  const int c = JOIN ? blockIdx.x - h * p.max_splits : blockIdx.x / p.kv_heads;
   const int col0 = blockIdx.z * NT * 8;
   const int cap = p.maxblk * BS;
   int ctx = __ldg(p.lens + r);
@@ -154,6 +171,8 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
     if (bad_len && threadIdx.x == 0) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
     return;
   }
+  const bool joins = JOIN && nsplit > 1;
+  if (joins) cluster_arrive();  // CTAs without tokens have left, and no one writes to them
   const int tok0 = c * p.split_tokens, tok1 = min(tok0 + p.split_tokens, ctx);
   const int ntiles = (tok1 - tok0 + kTile - 1) / kTile;  // of the CTA
 
@@ -498,6 +517,17 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
         dst[i] = make_float4(acc[nt][2 * i][e], acc[nt][2 * i][2 + e], acc[nt][2 * i + 1][e], acc[nt][2 * i + 1][2 + e]);
     }
   __syncthreads();
+  // a cluster's outputs are joined by all of its CTAs, `per` vectors of four each
+  float* parts = reinterpret_cast<float*>(smem + L::PART_SUM_OFF);
+  const int per = joins ? (ncols * (D / 4) + nsplit - 1) / nsplit : 0;
+  if (joins) cluster_wait();  // every CTA has begun
+  auto put_out = [&](size_t row, int d, float4 o, float sum) {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a NaN sum stays one
+    o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + d) =
+        p.bf16 ? make_uint2(Elem<__nv_bfloat16>::pack(o.x, o.y), Elem<__nv_bfloat16>::pack(o.z, o.w))
+               : make_uint2(Elem<__half>::pack(o.x, o.y), Elem<__half>::pack(o.z, o.w));
+  };
   for (int i = threadIdx.x; i < ncols * (D / 4); i += kWarps * 32) {
     const int n = i / (D / 4), d = 4 * (i % (D / 4));
     float f[kWarps], M = -INFINITY;
@@ -518,11 +548,15 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
     if (nan[d / kKv4Group] & ((1u << nsee) - 1u)) o = make_float4(NAN, NAN, NAN, NAN);
     const size_t row = row_of(col0 + n);
     if (nsplit == 1) {
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a NaN sum stays one
-      o.x *= inv, o.y *= inv, o.z *= inv, o.w *= inv;
-      *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + row * D + d) =
-          p.bf16 ? make_uint2(Elem<__nv_bfloat16>::pack(o.x, o.y), Elem<__nv_bfloat16>::pack(o.z, o.w))
-                 : make_uint2(Elem<__half>::pack(o.x, o.y), Elem<__half>::pack(o.z, o.w));
+      put_out(row, d, o, sum);
+    } else if (joins) {
+      const int to = i / per;
+      cluster_st4(smem_u32(smem + L::PART_OFF) + (c * per + i - to * per) * 16, to, o);
+      const int w = d / 4;  // a lane per CTA: the column's sums
+      if (w < nsplit) {
+        cluster_st(smem_u32(parts + c * NT * 8 + n), w, M);
+        cluster_st(smem_u32(parts + (kMaxCluster + c) * NT * 8 + n), w, sum);
+      }
     } else {
       *reinterpret_cast<float4*>(p.part_o + (row * p.max_splits + c) * D + d) = o;
       if (d == 0) {
@@ -531,14 +565,50 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
       }
     }
   }
+  if (!joins) return;
+
+  // this CTA's outputs, from the parts that the partitions have written to it
+  cluster_sync();
+  for (int j = threadIdx.x; j < per; j += kWarps * 32) {
+    const int i = c * per + j;
+    if (i >= ncols * (D / 4)) break;
+    const int n = i / (D / 4), d = 4 * (i % (D / 4));
+    float M = -INFINITY;
+    for (int w = 0; w < nsplit; ++w) M = fmaxf(M, parts[w * NT * 8 + n]);
+    const float ref = M == -INFINITY ? 0.f : M;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float sum = 0.f;
+#pragma unroll 4
+    for (int w = 0; w < nsplit; ++w) {
+      const float a = ex2_approx(parts[w * NT * 8 + n] - ref);
+      const float4 x = *reinterpret_cast<const float4*>(smem + L::PART_OFF + (w * per + j) * 16);
+      o.x += a * x.x, o.y += a * x.y, o.z += a * x.z, o.w += a * x.w;
+      sum += a * parts[(kMaxCluster + w) * NT * 8 + n];
+    }
+    put_out(row_of(col0 + n), d, o, sum);
+  }
 }
 
 template <int D, int NT, int BS>
 cudaError_t launch_t(const Kv4DecodeParams& p, cudaStream_t stream) {
   using L = Kv4DecodeSmem<D, NT>;
-  static_assert(L::bytes(kMaxEntries + 4) <= 48 * 1024, "no attribute needed");
+  static_assert(L::bytes(kMaxEntries + 4, false) <= 48 * 1024 && L::bytes(kKv4ClusterEntries + 4, true) <= 48 * 1024,
+                "no attribute needed");
   const dim3 grid((unsigned)(p.max_splits * p.kv_heads), p.num_seqs, (p.group * p.q_len + NT * 8 - 1) / (NT * 8));
-  return launch_pdl(kv4_decode_kernel<D, NT, BS>, grid, dim3(kWarps * 32), L::bytes(p.tab_entries + 4), stream, p);
+  const int smem = L::bytes(p.tab_entries + 4, p.cluster);
+  if (p.cluster) {
+    auto kern = kv4_decode_kernel<D, NT, BS, true>;
+    static bool attr_set[64] = {};
+    int dev = 0;
+    cudaGetDevice(&dev);
+    if (dev >= 64 || !attr_set[dev]) {
+      const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      if (dev < 64) attr_set[dev] = true;
+    }
+    return launch_pdl_cluster(kern, p.max_splits, grid, dim3(kWarps * 32), smem, stream, p);
+  }
+  return launch_pdl(kv4_decode_kernel<D, NT, BS, false>, grid, dim3(kWarps * 32), smem, stream, p);
 }
 
 template <int D, int BS>

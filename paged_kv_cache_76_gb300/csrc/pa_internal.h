@@ -333,9 +333,12 @@ struct Kv4DecodeParams {
   int* err;
   int maxblk, num_seqs, q_len, q_heads, kv_heads, group, num_blocks, block_size;
   int split_tokens, max_splits, tab_entries;
-  int bf16;  // q and out: bf16, or fp16
+  int cluster;  // the partitions of a list are a cluster, which joins them: no partials
+  int bf16;     // q and out: bf16, or fp16
   float scale_log2;
 };
+constexpr int kKv4Cluster = 16;          // partitions of a cluster, at most
+constexpr int kKv4ClusterEntries = 256;  // Block Table entries of a partition, at most
 // without the merge (launch_lse_merge)
 cudaError_t launch_kv4_decode(const Kv4DecodeParams& p, int head_dim, cudaStream_t stream);
 

@@ -32,6 +32,7 @@ constexpr int kKv4SplitUnit = 32;  // a stage of the kernel
 
 struct Kv4DecodeSetup {
   int split, max_splits;
+  bool cluster;
   DecodeWorkspace ws;
 };
 
@@ -45,28 +46,51 @@ int kv4_decode_setup(int num_seqs, int q_len, int q_heads, int kv_heads, int hea
   const int64_t cap = (int64_t)max_blocks_per_seq * block_size;
   if (cap > INT32_MAX - 4096 || (int64_t)num_seqs * q_len * q_heads > INT32_MAX - 8) return PA_ERR_INVALID;
   const int most = 1024 * block_size;
+  const int64_t sms = num_sms() > 0 ? num_sms() : 152;
+  const int64_t lists = (int64_t)num_seqs * kv_heads * ((group * q_len + 15) / 16);
   int64_t split = split_tokens;
+  // Partitions of a list that run at the same time may be a cluster, which joins
+  // its parts without a second kernel; more than twelve CTAs find no place in a
+  // part of the chip that others already share.
+  const int resident = group * q_len <= 8 ? 4 : 3;  // CTAs an SM holds
+  auto clusters = [&](int64_t parts, int64_t tokens) {
+    return parts > 1 && parts <= kKv4Cluster && tokens / block_size <= kKv4ClusterEntries &&
+           lists * parts <= (parts > 12 ? 2 : resident) * sms;
+  };
   if (split_tokens == 0) {
-    // Two rounds of the four CTAs that an SM holds, between 128 tokens (a partition
-    // below it costs more to start, end and merge than it saves) and 4096.
-    // Measured on GB300, us: 4 requests of <= 1501 tokens, 28/4 heads: 64 tokens
-    // 6.0, 128 5.5, 256 5.6, 512 6.9; 64 of <= 4079, 32/8: 512 44.6, 1024 41.9,
-    // 1376 (chosen) 41.5, 2048 44.1, 4096 52; with 4 queries each 512 79, 1024 66.5,
-    // 1376 66, 1536 65, 2048 68; 8 of <= 131009, 64/8: 1024 162, 2048 146, 4096 144.
-    const int64_t sms = num_sms() > 0 ? num_sms() : 152;
-    const int64_t lists = (int64_t)num_seqs * kv_heads * ((group * q_len + 15) / 16);
-    const int64_t parts = lists > 0 ? (8 * sms + lists - 1) / lists : 1;
-    split = (cap + parts - 1) / parts;
-    if (split < 128) split = 128;
-    if (split > 4096) split = 4096;
-    split = (split + kKv4SplitUnit - 1) / kKv4SplitUnit * kKv4SplitUnit;
-    if (split > most) split = most;
+    // The number of partitions that is the fastest by this count, in ns, of what
+    // was measured on GB300 for 1, 4 and 16 requests of 512..32768 tokens, 28/4 and
+    // 32/8 heads, one query and four, with 2..64 partitions (within 2 % of the
+    // fastest, on average): a CTA takes longer a token the more share its SM (a
+    // cluster's sooner, as they lie together); those after the first round start as
+    // others end; starting and ending cost what a count of CTAs does.
+    const bool wide = group * q_len > 8;
+    const int64_t first = (cap + 4095) / 4096 > (cap + most - 1) / most ? (cap + 4095) / 4096 : (cap + most - 1) / most;
+    int64_t best = 0;
+    for (int64_t parts = first; parts == first || (parts * 64 <= cap && parts <= first + 256);
+         parts += 1 + parts / 12) {
+      int64_t tokens = (cap + parts - 1) / parts;
+      tokens = (tokens + kKv4SplitUnit - 1) / kKv4SplitUnit * kKv4SplitUnit;
+      if (tokens > most) tokens = most;
+      const bool joined = clusters(parts, tokens);
+      const double x = (double)(lists * parts) / sms;
+      double k = joined ? 2.7 * x : std::ceil(x);
+      k = k < 1 ? 1 : k > resident ? resident : k;
+      const double rounds = x > resident ? 0.7 * x / resident + 0.5 : 1;  // contexts that are not all full
+      const double cost = 2200 + 570 * x + (double)tokens * (wide ? 4.7 + 3.7 * k : 3.9 + 2.1 * k) * rounds +
+                          (parts == 1 ? 0 : joined ? 720 + 12 * parts : 1230 + 35 * parts);
+      if (best == 0 || (int64_t)cost < best) {
+        best = (int64_t)cost;
+        split = tokens;
+      }
+    }
   }
   if (split <= 0 || split % kKv4SplitUnit != 0 || split > most) return PA_ERR_INVALID;
   s->split = (int)split;
   s->max_splits = (int)((cap + split - 1) / split);
   if ((int64_t)s->max_splits * kv_heads > INT32_MAX - 8) return PA_ERR_INVALID;
-  s->ws = s->max_splits > 1 ? decode_workspace_layout(num_seqs * q_len, q_heads, head_dim, s->max_splits)
+  s->cluster = clusters(s->max_splits, split);
+  s->ws = s->max_splits > 1 && !s->cluster ? decode_workspace_layout(num_seqs * q_len, q_heads, head_dim, s->max_splits)
                             : DecodeWorkspace{0, 0, 0, 0};
   return PA_OK;
 }
@@ -246,10 +270,11 @@ int pa_decode_kv4(const void* q, const void* k_cache, const void* v_cache, const
   p.split_tokens = s.split;
   p.max_splits = s.max_splits;
   p.tab_entries = s.split / block_size;
+  p.cluster = s.cluster;
   p.bf16 = dtype == PA_BF16;
   p.scale_log2 = scale * 1.4426950408889634f;
   st = cuda_status(launch_kv4_decode(p, head_dim, to_stream(stream)));
-  if (st != PA_OK || s.max_splits == 1) return st;
+  if (st != PA_OK || s.max_splits == 1 || s.cluster) return st;
   MergeParams mp{};
   mp.part_o = p.part_o;
   mp.part_m = p.part_m;

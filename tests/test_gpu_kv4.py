@@ -436,7 +436,8 @@ def test_two_calls_at_once_and_a_given_workspace(ops):
     b = Batch(ops, [700, 5, 300], 2, 128, 16, BF)
     q, qp = b.q(3, 8), b.q(60, 8)
     start = i32([0, 30, 35, 60])
-    want = ops.decode_kv4(q, b.kc, b.vc, b.tables, b.ctx, 0.1)
+    # split_tokens 32: partials and a merge; 64: twelve partitions, a cluster
+    want = {n: ops.decode_kv4(q, b.kc, b.vc, b.tables, b.ctx, 0.1, split_tokens=n) for n in (32, 64)}
     wantp = ops.chunked_prefill_kv4(qp, start, b.ctx, b.kc, b.vc, b.tables, 0.1, 30, split_tokens=64)
     torch.cuda.synchronize()
     streams, got = [torch.cuda.Stream() for _ in range(4)], []
@@ -444,7 +445,8 @@ def test_two_calls_at_once_and_a_given_workspace(ops):
         for i, s in enumerate(streams):
             with torch.cuda.stream(s):
                 if i % 2:
-                    got.append((ops.decode_kv4(q, b.kc, b.vc, b.tables, b.ctx, 0.1), want))
+                    n = 32 if i == 1 else 64
+                    got.append((ops.decode_kv4(q, b.kc, b.vc, b.tables, b.ctx, 0.1, split_tokens=n), want[n]))
                 else:
                     got.append((ops.chunked_prefill_kv4(qp, start, b.ctx, b.kc, b.vc, b.tables, 0.1, 30,
                                                         split_tokens=64), wantp))
@@ -452,13 +454,29 @@ def test_two_calls_at_once_and_a_given_workspace(ops):
     assert all(torch.equal(g, w) for g, w in got)
     ws = torch.empty(1 << 24, dtype=torch.uint8, device="cuda")
     for _ in range(3):  # one scratch for calls in order
-        assert torch.equal(ops.decode_kv4(q, b.kc, b.vc, b.tables, b.ctx, 0.1, workspace=ws), want)
+        assert torch.equal(ops.decode_kv4(q, b.kc, b.vc, b.tables, b.ctx, 0.1, split_tokens=32, workspace=ws), want[32])
         assert torch.equal(ops.chunked_prefill_kv4(qp, start, b.ctx, b.kc, b.vc, b.tables, 0.1, 30, split_tokens=64,
                                                    workspace=ws), wantp)
     from paged_kv_cache_76_gb300 import PAError
     with pytest.raises(PAError):
-        ops.decode_kv4(q, b.kc, b.vc, b.tables, b.ctx, 0.1, workspace=ws[:256])
+        ops.decode_kv4(q, b.kc, b.vc, b.tables, b.ctx, 0.1, split_tokens=32, workspace=ws[:256])
     assert ops.get_device_error() == 0
+
+
+@pytest.mark.parametrize("hq,hkv,d,bs,ql", [(8, 1, 128, 16, 1), (4, 1, 64, 4, 1), (16, 1, 128, 32, 2), (8, 2, 128, 8, 3)])
+@pytest.mark.parametrize("parts", [2, 5, 13, 16, 17])
+def test_partitions_that_join(ops, hq, hkv, d, bs, ql, parts):
+    """Clusters of every size beside the next that takes a merge; contexts that end in any of the partitions."""
+    most = 64 * parts - bs  # tables have a column more
+    lens = [most, 0, 1, 64, 65, 64 * (parts // 2) + 3]
+    b = Batch(ops, lens, hkv, d, bs, BF)
+    q = b.q(len(lens), ql, hq)
+    size = ops.decode_kv4_workspace_size(len(lens), ql, hq, hkv, d, b.tables.shape[1], bs, 64)
+    assert (size == 0) == (parts <= 16)
+    out = ops.decode_kv4(q, b.kc, b.vc, b.tables, b.ctx, 0.1, split_tokens=64)
+    assert ops.get_device_error() == 0
+    b.check(out, q, 0.1, decode_rows(lens, ql))
+    assert torch.equal(out, ops.decode_kv4(q, b.kc, b.vc, b.tables, b.ctx, 0.1, split_tokens=64))
 
 
 def test_wide_tables_and_many_requests(ops):

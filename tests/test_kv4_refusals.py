@@ -125,14 +125,15 @@ def test_c_calls_check_before_they_launch(lib):
     for bad in (dict(k=None), dict(v=8), dict(T=-1), dict(d=80)):
         assert r(**bad) == inv, bad
     d = lambda **k: lib.pa_decode_kv4(*{**dict(q=P, kc=P, vc=P, tab=P, mb=64, lens=P, B=2, ql=1, hq=8, h=2, d=128, bs=16,  # noqa: E731
-                                               nb=99, sc=0.1, sp=128, ws=P, wb=1 << 30, out=P, dt=1, st=None), **k}.values())
+                                               nb=99, sc=0.1, sp=32, ws=P, wb=1 << 30, out=P, dt=1, st=None), **k}.values())
     assert d(B=0) == _lib.PA_OK
     for bad in (dict(q=None), dict(out=8), dict(tab=None), dict(B=-1), dict(B=65536), dict(ql=0), dict(ql=9), dict(hq=9),
                 dict(hq=34, h=2), dict(sp=31), dict(sp=48), dict(sp=1 << 20), dict(sc=float("nan")),
                 dict(sc=float("inf")), dict(mb=0), dict(mb=2 ** 31 - 1)):
         assert d(**bad) == inv, bad
     assert d(wb=100) == ws and d(ws=None) == ws and d(ws=8) == ws
-    assert lib.pa_decode_kv4_workspace_size(2, 1, 8, 2, 128, 64, 16, 128) > 2 * 8 * 8 * 128 * 4
+    assert lib.pa_decode_kv4_workspace_size(2, 1, 8, 2, 128, 64, 16, 32) > 2 * 8 * 32 * 128 * 4
+    assert lib.pa_decode_kv4_workspace_size(2, 1, 8, 2, 128, 64, 16, 128) == 0  # eight partitions join without
     assert lib.pa_decode_kv4_workspace_size(2, 33, 8, 2, 128, 64, 16, 128) == 0
     assert lib.pa_decode_kv4_split_tokens(2, 1, 8, 2, 64, 16, 96) == 96
     assert lib.pa_decode_kv4_split_tokens(2, 1, 8, 2, 64, 16, 0) % 32 == 0
