@@ -14,8 +14,9 @@
 // Host time of a call (us, Grace host; the long way through ctypes and this
 // one): norm_rope_and_cache 22.4 and 5.4, verify_tree with scratch and two
 // launches 26.9 and 8.7, decode_accumulate 27.9 and 8.9, evict_select 20.4 and
-// 5.9, compact_kv 9.9 and 3.0.  Of a short one the launch is 2 to 3 us and an
-// allocation one.
+// 5.9, compact_kv 9.9 and 3.0; this one alone: quantize_and_cache 2.6,
+// dequantize_kv4 4.9, decode_kv4 4.6, fork_blocks 7, copy_pages 2.5.  Of a short
+// one the launch is 2 to 3 us and an allocation one.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
@@ -202,6 +203,15 @@ bool run(F&& f) {
   }
   PyEval_RestoreThread(s);
   return done;
+}
+
+// A contiguous tensor of `all`'s memory, from its element `at` on: small outputs
+// share one allocation, since at::empty is 1.2 of the microseconds that a call takes.
+at::Tensor piece(const at::Tensor& all, int64_t at, c10::IntArrayRef shape) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(all.storage()), all.key_set(), all.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(at);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous(shape);
+  return t;
 }
 
 // A result's object; nullptr with an error set.  (The work is under way by
@@ -451,8 +461,15 @@ PyObject* dequantize_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int st = PA_OK;
   if (!run([&] {
         const auto opt = slots->options().dtype(dtype == PA_FP16 ? at::kHalf : at::kBFloat16);
-        k = at::empty({T, kv.hkv, d}, opt);
-        v = at::empty({T, kv.hkv, d}, opt);
+        const int64_t n = (int64_t)T * kv.hkv * d;  // a multiple of 64
+        if (n <= (1 << 18)) {
+          const at::Tensor all = at::empty({2 * n}, opt);
+          k = piece(all, 0, {T, kv.hkv, d});
+          v = piece(all, n, {T, kv.hkv, d});
+        } else {  // so large that one may be let go before the other
+          k = at::empty({T, kv.hkv, d}, opt);
+          v = at::empty({T, kv.hkv, d}, opt);
+        }
         st = pa.dequantize(kv.k, kv.v, sp, T, kv.nb, kv.bs, kv.hkv, d, k.data_ptr(), v.data_ptr(), (pa_dtype)dtype,
                            current_stream(c.dev));
       }))
@@ -555,13 +572,19 @@ PyObject* fork_blocks(PyObject*, PyObject* const* a, Py_ssize_t n) {
   int st = PA_OK;
   if (!run([&] {
         const auto opt = table->options();
-        out[0] = at::empty({R, width}, opt);
-        out[1] = at::empty({R}, opt);
-        out[2] = at::empty({R, 2}, opt);
-        out[3] = at::empty({R, most}, opt);
-        out[4] = at::empty({1}, opt);
+        const std::initializer_list<int64_t> shapes[5] = {{R, width}, {R}, {R, 2}, {R, most}, {1}};
+        int64_t at[6] = {0};
+        for (int i = 0; i < 5; ++i) {
+          int64_t n = 1;
+          for (const int64_t x : shapes[i]) n *= x;
+          at[i + 1] = at[i] + (n + 63) / 64 * 64;
+        }
+        const at::Tensor all = at::empty({at[5]}, opt);
         int32_t* p[5];
-        for (int i = 0; i < 5; ++i) p[i] = static_cast<int32_t*>(out[i].data_ptr());
+        for (int i = 0; i < 5; ++i) {
+          out[i] = piece(all, at[i], shapes[i]);
+          p[i] = static_cast<int32_t*>(all.data_ptr()) + at[i];
+        }
         const size_t bytes = pa.fork_workspace(R, num_blocks);
         ws = at::empty({(int64_t)bytes}, opt.dtype(at::kByte));
         st = pa.fork(tp, maxblk, lp, B, pp, R, gp, most, pin, num_blocks, bs, p[0], width, p[1], p[2], p[3], p[4],
