@@ -31,6 +31,7 @@
 //   a lane's addresses worked out once, scales as zeros    1752   198
 //   Q and outputs by whole lines, longest requests first   1752   180
 //   two partitions where rounds of units fill the SMs      1639   180
+//   Q and the first table entries before the barriers      1638   180
 // What is left: about 9 us to start and end a unit of 256 rows (barriers and
 // tensor memory 1, table and first pages 1.8, their tile and Q 2.5, outputs 3),
 // with nothing under them, a fifth of the second case; the MMAs of a tile at the
@@ -70,7 +71,7 @@ struct Kv4PrefillSmem {
   static constexpr int V_OFF = K_OFF + kStages * Tile::BYTES;
   static constexpr int RAW_OFF = V_OFF + kStages * Tile::BYTES;  // a tile per maker: its codes, then its scales
   static constexpr int BAR_OFF = RAW_OFF + 2 * kMakers * RAW;
-  static constexpr int NBARS = 4 * kStages + 2 * kMakers + 15;
+  static constexpr int NBARS = 4 * kStages + 2 * kMakers + 16;
   static constexpr int SLOT_OFF = BAR_OFF + NBARS * 8;
   static constexpr int NAN_OFF = SLOT_OFF + 8;
   static constexpr int SCALE_OFF = NAN_OFF + D / kKv4Group * 4;  // softmax scale of each row
@@ -90,10 +91,21 @@ constexpr int B_PFULL = B_SFULL + 4;            // [2][2] four softmax warps
 constexpr int B_OFULL = B_PFULL + 4;            // [2][2] P.V_x(j) complete
 constexpr int B_QFULL = B_OFULL + 4;            // [2]
 constexpr int B_MMADONE = B_QFULL + 2;
-static_assert(B_MMADONE + 1 == 4 * kStages + 2 * kMakers + 15, "barrier count");
+constexpr int B_BEGUN = B_MMADONE + 1;          // tile A's first P is there (its B_PFULL may be a phase further by the time B looks)
+static_assert(B_BEGUN + 1 == 4 * kStages + 2 * kMakers + 16, "barrier count");
 
 __device__ __forceinline__ void st_shared4(uint32_t at, uint4 v) {
   asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// Named barriers of the start: of the warps that are no softmax warps, and of warp
+// 0 and those.
+constexpr int kSetUpBar = 1, kReadyBar = 2;
+__device__ __forceinline__ void named_sync(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ void named_arrive(int id, int threads) {
+  asm volatile("bar.arrive %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
 struct Unit {
@@ -200,17 +212,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
     mbar_init(bar(B_QFULL), 4);
     mbar_init(bar(B_QFULL + 1), 4);
     mbar_init(bar(B_MMADONE), tiles);
+    mbar_init(bar(B_BEGUN), 1);
     fence_mbar_init();
   }
   if (warp == 0) {
     tmem_alloc(smem_u32(tmem_slot), kTmem);
     tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
   griddep_launch_dependents();
+  // Barriers and tensor memory take about a microsecond: the softmax warps load Q
+  // meanwhile and meet warp 0 behind it, the makers have their first table entries.
+  tc_fence_before();
+  if (warp == 0) named_arrive(kReadyBar, 32 + 32 * (kThreads / 32 - kSoftmaxWarp0));
 
   if (warp >= 2 && warp < kSoftmaxWarp0) {
     // ------------------------------------------------------------ K and V
@@ -225,14 +238,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
     const int32_t* trow = p.tables + (size_t)w.r * p.maxblk;
     const int bs = p.block_size, bsh = p.block_shift, page = bs * R::BYTES;
     const uint64_t pol = p.row_tiles == 1 ? policy_evict_first() : policy_evict_last();  // other row tiles re-read them
-    griddep_wait();
     // pages of tile j: lane 2i their i-th's codes, lane 2i + 1 its scales
-    auto issue = [&](int j) {
+    auto entry = [&](int j) {
+      const int ts = w.k0 + j * kKeys, npages = (min(kKeys, w.kend - ts) + bs - 1) >> bsh;
+      return (lane >> 1) < npages ? __ldg(trow + (ts >> bsh) + (lane >> 1)) : -1;
+    };
+    auto issue = [&](int j, int b) {
       const int ts = w.k0 + j * kKeys;
       const int npages = (min(kKeys, w.kend - ts) + bs - 1) >> bsh;
       const int i = lane >> 1, part = lane & 1;
       const bool mine = i < npages;
-      int b = mine ? __ldg(trow + (ts >> bsh) + i) : -1;
       if (mine && (b < 0 || b >= p.num_blocks)) {
         record_error(p.err, PA_DEVERR_BLOCK_ID);
         b = -1;
@@ -252,7 +267,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
       }
       __syncwarp();  // the zeros before other lanes read them
     };
-    if (first < w.ntiles) issue(first);
+    const int b0 = first < w.ntiles ? entry(first) : -1;
+    named_sync(kSetUpBar, 32 * kSoftmaxWarp0);
+    griddep_wait();
+    if (first < w.ntiles) issue(first, b0);
     bool failed = false;
     int n = 0;  // tiles made
     for (int j = first; j < w.ntiles; j += kMakers, ++n) {
@@ -307,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
       fence_proxy_async_smem();  // the tile before the MMAs, the pages before the next copies over them
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(full0 + s));
-      if (j + kMakers < w.ntiles) issue(j + kMakers);
+      if (j + kMakers < w.ntiles) issue(j + kMakers, entry(j + kMakers));
     }
     if (failed) {
       if (lane == 0) record_error(p.err, PA_DEVERR_TIMEOUT);
@@ -315,6 +333,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
     }
   } else if (warp < 2) {
     // ------------------------------------------------------------ MMA issuers
+    named_sync(kSetUpBar, 32 * kSoftmaxWarp0);
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
     const int x = warp;
     if (x < tiles) {
       bool ok = true;
@@ -326,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
         if (!__all_sync(kAll, mbar_wait(bar(B_PFULL + 2 * x + pb), (t >> 1) & 1) &&
                                   mbar_wait(bar(B_VFULL + vst), (t / kStages) & 1)))
           return false;
+        if (x == 0 && t == 0 && lane == 0) mbar_arrive(bar(B_BEGUN));
         tc_fence_after();
         const uint32_t vb = vbase + vst * Tile::BYTES;
 #pragma unroll
@@ -338,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
       };
       ok = __all_sync(kAll, mbar_wait(bar(B_QFULL + x), 0));
       // tile B starts half a key tile behind tile A, so that the two softmaxes alternate
-      if (ok && x == 1) ok = __all_sync(kAll, mbar_wait(bar(B_PFULL), 0));
+      if (ok && x == 1) ok = __all_sync(kAll, mbar_wait(bar(B_BEGUN), 0));
       for (int j = 0; ok && j < w.ntiles; ++j) {
         const int s = j % kStages, b = j & 1;
         // S_x(j) overwrites P_x(j - 2)
@@ -364,9 +386,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
     // ------------------------------------------------------------ softmax
     const int x = (warp - kSoftmaxWarp0) >> 2;
     const int quarter = warp & 3, row = quarter * 32 + lane;
+    if (x >= tiles) named_sync(kReadyBar, 32 + 32 * (kThreads / 32 - kSoftmaxWarp0));
     if (x < tiles) {
-      const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16;
-      const uint32_t scol0 = tmem + lane_addr + 2 * x * kKeys, ocol = tmem + lane_addr + O_COL + x * D;
       const int grow = w.row0 + x * kRows + row;
       const int lim = grow < w.rows ? w.p0 + grow / G : -1;  // last key this row sees
       // The warp's 32 rows of Q -> shared memory (K-major, 128-byte swizzle), a row
@@ -415,9 +436,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
           }
         }
         fence_proxy_async_smem();
-        __syncwarp();
+        named_sync(kReadyBar, 32 + 32 * (kThreads / 32 - kSoftmaxWarp0));
         if (lane == 0) mbar_arrive(bar(B_QFULL + x));
       }
+      tc_fence_after();
+      const uint32_t lane_addr = (uint32_t)(quarter * 32) << 16, tmem = *tmem_slot;
+      const uint32_t scol0 = tmem + lane_addr + 2 * x * kKeys, ocol = tmem + lane_addr + O_COL + x * D;
       const float sl2 = scales[x * kRows + row];
       griddep_wait();  // before writing outputs
 
@@ -584,7 +608,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv4_prefill_kernel(const Kv4Prefi
   __syncthreads();
   if (warp == 0) {
     tc_fence_after();
-    tmem_dealloc(tmem, kTmem);
+    tmem_dealloc(*tmem_slot, kTmem);
   }
 }
 
