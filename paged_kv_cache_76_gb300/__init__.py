@@ -5,7 +5,9 @@ The compute path is ``libpa.so`` (hand-written CUDA behind the C ABI of
 
 * :mod:`.ops` - reshape_and_cache, copy_blocks, decode (partial + lse_merge),
   chunked_prefill, device error word; norm_rope_and_cache, verify_tree,
-  decode_accumulate, evict_select and compact_kv;
+  decode_accumulate, evict_select and compact_kv; a cache held in 4 bits
+  (quantize_and_cache, dequantize_kv4, decode_kv4, chunked_prefill_kv4);
+  fork_blocks and copy_pages;
 * :mod:`.allocator` - the C++ block allocator (free queue, refcounts, share,
   copy-on-write, release behind a compaction);
 * :mod:`.build` - compiles the library in-tree.
