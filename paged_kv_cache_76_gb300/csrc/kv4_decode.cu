@@ -9,7 +9,7 @@
 // the ones that join them, all at once, and one barrier later every CTA has a
 // share of the list's outputs to write.  No partials, no second kernel (1 request
 // of 2048 tokens, 32/8 heads, in 16 partitions 5.0 -> 4.5 us, 16 in four 14 -> 11;
-// 4 of <= 1501, 28/4 heads 5.3 -> 5.0, and a call from Python 8.2 -> 5.5).  Past
+// 4 of <= 1501, 28/4 heads 5.3 -> 5.0, and a call from Python 8..10 -> 6.5).  Past
 // that the CTAs of a cluster wait for one another in places that others could
 // have (64 requests below 41 -> 46).
 //
