@@ -36,6 +36,11 @@
 // tensor memory 1, table and first pages 1.8, their tile and Q 2.5, outputs 3),
 // with nothing under them, a fifth of the second case; the MMAs of a tile at the
 // measured rate are 0.66 us of its 0.79.
+// Tried and left: CTAs that take over further units (by cluster launch control),
+// whose makers are a unit ahead of the softmax (1680 and 183: the counters across
+// units take registers that the softmax has not, 3 % of every tile, as much as the
+// overlap gives; asked for at a unit's start instead of its end 1688 and 194, as
+// units are then held by busy CTAs while others have none).
 //
 // Warps: 0, 1 MMA issuers of tiles A, B; 2..7 make K and V; 8..11 softmax of
 // tile A, 12..15 of tile B.  Every wait is bounded.
