@@ -40,7 +40,10 @@
 // whose makers are a unit ahead of the softmax (1680 and 183: the counters across
 // units take registers that the softmax has not, 3 % of every tile, as much as the
 // overlap gives; asked for at a unit's start instead of its end 1688 and 194, as
-// units are then held by busy CTAs while others have none).
+// units are then held by busy CTAs while others have none); partitions joined in a
+// cluster, through the places of the K and V tiles (up to five, 64 KB and more a
+// CTA: four short chunks 22.6 in two, and where units go in rounds 1667 instead of
+// 1638 and worse).
 //
 // Warps: 0, 1 MMA issuers of tiles A, B; 2..7 make K and V; 8..11 softmax of
 // tile A, 12..15 of tile B.  Every wait is bounded.
