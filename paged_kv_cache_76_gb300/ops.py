@@ -934,7 +934,7 @@ def quantize_and_cache(k, v, slot_mapping, k_cache, v_cache, stream=None):
 
 def dequantize_kv4(k_cache, v_cache, slots, head_dim, dtype=torch.bfloat16, k=None, v=None, stream=None):
     """pa_dequantize_kv4: K and V of the tokens at ``slots`` in 16 bits, each [num_tokens, kv_heads, head_dim] (exact;
-    zeros where a slot is negative)."""
+    zeros where a slot is negative).  Small outputs share one allocation."""
     if k is None and v is None and _short_way(stream):
         r = _marshal.dequantize_kv4(k_cache, v_cache, slots, head_dim, dtype_code(dtype))
         if r is not None:
@@ -1089,7 +1089,7 @@ def fork_blocks(block_tables, context_lens, parents, num_blocks, block_size, gro
     [num_new], pairs [num_new, 2] for :func:`copy_pages`, slots [num_new, max_grow], num_free [1]).
 
     ``pinned`` (bool or uint8 [num_blocks]): blocks that others hold.  ``max_blocks``: columns of the new tables (None:
-    as many as ``block_tables`` has)."""
+    as many as ``block_tables`` has).  The outputs may share one allocation."""
     if workspace is None and _short_way(stream):
         r = _marshal.fork_blocks(block_tables, context_lens, parents, num_blocks, block_size, grow, max_grow, pinned,
                                  max_blocks)

@@ -155,3 +155,20 @@ def test_a_given_output_and_refusals_of_the_c_call(taken):
     with pytest.raises(PAError):
         f(**{**kw, "block_size": 5})
     assert taken == [True] * 5
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["fork", "dequantize"])
+@pytest.mark.parametrize("inference", [False, True])
+def test_outputs_of_one_allocation_are_tensors_of_their_own(name, inference, taken):
+    f, kw = calls("cuda")[name]
+    with torch.inference_mode(inference):
+        out = f(**kw)
+        assert taken == [True]
+        want = [t.clone() for t in out]
+        ends = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in out if t.numel())
+        assert all(a[1] <= b[0] for a, b in zip(ends, ends[1:]))
+        for i, t in enumerate(out):
+            assert t.is_contiguous() and t.data_ptr() % 16 == 0 and not t.requires_grad and t.is_inference() == inference
+            t.zero_()
+            assert all(torch.equal(a, b) for a, b in zip(out[i + 1:], want[i + 1:]))
