@@ -72,13 +72,11 @@ __device__ __forceinline__ uint2 encode16(const uint4 (&v)[2], uint32_t& byte) {
   uint32_t w[2] = {0u, 0u};
 #pragma unroll
   for (int i = 0; i < 16; i += 2) {
-    float y[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const float q = x[i + e] * r;
-      y[e] = fmaf(fmaf(-q, s, x[i + e]), r, q);
-    }
-    w[i >> 3] |= kv4_pack2(y[0], y[1]) << ((i & 7) * 4);
+    float q0, q1, y0, y1;
+    fmul2(q0, q1, x[i], x[i + 1], r, r);
+    ffma2(y0, y1, q0, q1, -s, -s, x[i], x[i + 1]);
+    ffma2(y0, y1, y0, y1, r, r, q0, q1);
+    w[i >> 3] |= kv4_pack2(y0, y1) << ((i & 7) * 4);
   }
   return make_uint2(w[0], w[1]);
 }

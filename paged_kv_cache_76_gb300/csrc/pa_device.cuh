@@ -374,7 +374,7 @@ __device__ __forceinline__ float ex2_approx(float x) {
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
-// Packed pairs of fp32 (one f32x2 instruction on sm_100+): d = a * b + c, d = a + b.
+// Packed pairs of fp32 (one f32x2 instruction on sm_100+): d = a * b + c, d = a + b, d = a * b.
 __device__ __forceinline__ void ffma2(float& dx, float& dy, float ax, float ay, float bx, float by, float cx,
                                       float cy) {
   asm("{\n .reg .b64 a, b, c, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n mov.b64 c, {%6, %7};\n"
@@ -385,6 +385,12 @@ __device__ __forceinline__ void ffma2(float& dx, float& dy, float ax, float ay, 
 __device__ __forceinline__ void fadd2(float& dx, float& dy, float ax, float ay, float bx, float by) {
   asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
       " add.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
+      : "=f"(dx), "=f"(dy)
+      : "f"(ax), "f"(ay), "f"(bx), "f"(by));
+}
+__device__ __forceinline__ void fmul2(float& dx, float& dy, float ax, float ay, float bx, float by) {
+  asm("{\n .reg .b64 a, b, d;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n"
+      " mul.rn.f32x2 d, a, b;\n mov.b64 {%0, %1}, d;\n}\n"
       : "=f"(dx), "=f"(dy)
       : "f"(ax), "f"(ay), "f"(bx), "f"(by));
 }
