@@ -4,8 +4,8 @@
 // magnitude, the scale and the codes need no other thread, and neighbouring
 // threads read and write neighbouring 32-byte pieces.  Both kernels are bound by
 // memory.  Measured on GB300: 8192 tokens (8 heads of 128, views of a fused
-// projection's rows) written to scattered slots 9.6 us (43 MB: 4.5 TB/s), a pool
-// of 10304 read back 8.3 (54 MB: 6.5 TB/s); 64 tokens 1.7.
+// projection's rows) written to scattered slots 8.9 us (43 MB: 4.8 TB/s), a pool
+// of 10304 read back 8.1 (54 MB: 6.6 TB/s); 64 tokens 1.5.
 #include "kv4.cuh"
 #include "pa_internal.h"
 
@@ -13,8 +13,12 @@ namespace pa {
 
 namespace {
 
+// Threads of a CTA (64: 9.3 us and 10.8 for the sizes above; 256: 9.35 and 8.3); of
+// those that write an SM holds twelve (eleven, in 44 registers: 9.0).
+constexpr int kThreads = 128;
+
 // 32 bytes at once, where they are aligned: two accesses of 16 each take half of
-// every sector (the read below 12.5 us instead of 8.3; the write 9.6 either way).
+// every sector (the read below 12.5 us instead of 8.3; the write the same either way).
 __device__ __forceinline__ void ld_32(const void* p, uint4 (&v)[2]) {
   asm volatile("ld.global.nc.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x), "=r"(v[1].y), "=r"(v[1].z),
@@ -95,11 +99,11 @@ __device__ __forceinline__ Place place_of(uint32_t at, int32_t slot, int kv_head
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(256) quantize_and_cache_kernel(const Kv4WriteParams p) {
+__global__ void __launch_bounds__(kThreads, 12) quantize_and_cache_kernel(const Kv4WriteParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t per_token = p.kv_heads * (D / kKv4Group), total = (uint32_t)p.num_tokens * per_token;
-  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
   if (i >= total) return;
   const uint32_t token = i / per_token, at = i - token * per_token;
   // k and v do not wait for the slot
@@ -130,11 +134,11 @@ __global__ void __launch_bounds__(256) quantize_and_cache_kernel(const Kv4WriteP
 }
 
 template <int D, typename T>
-__global__ void __launch_bounds__(256) dequantize_kernel(const Kv4ReadParams p) {
+__global__ void __launch_bounds__(kThreads) dequantize_kernel(const Kv4ReadParams p) {
   griddep_wait();
   griddep_launch_dependents();
   const uint32_t per_token = p.kv_heads * (D / kKv4Group), total = (uint32_t)p.num_tokens * per_token;
-  const uint32_t i = blockIdx.x * 256 + threadIdx.x;
+  const uint32_t i = blockIdx.x * kThreads + threadIdx.x;
   if (i >= total) return;
   const uint32_t token = i / per_token, at = i - token * per_token;
   const int32_t slot = __ldg(p.slots + token);
@@ -183,7 +187,8 @@ cudaError_t launch_quantize_and_cache(const Kv4WriteParams& all, int head_dim, p
     p.slots = all.slots + t;
     p.wide = ((reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) & 31u) == 0 &&
              p.k_stride % 16 == 0 && p.v_stride % 16 == 0;
-    const dim3 grid((unsigned)((p.num_tokens * p.kv_heads * (head_dim / kKv4Group) + 255) / 256)), block(256);
+    const dim3 grid((unsigned)((p.num_tokens * p.kv_heads * (head_dim / kKv4Group) + kThreads - 1) / kThreads)),
+        block(kThreads);
     if (head_dim == 128)
       e = dt == PA_BF16 ? launch_pdl(quantize_and_cache_kernel<128, __nv_bfloat16>, grid, block, 0, stream, p)
                         : launch_pdl(quantize_and_cache_kernel<128, __half>, grid, block, 0, stream, p);
@@ -204,7 +209,8 @@ cudaError_t launch_dequantize_kv4(const Kv4ReadParams& all, int head_dim, pa_dty
     p.v = static_cast<uint16_t*>(all.v) + t * row;
     p.slots = all.slots + t;
     p.wide = ((reinterpret_cast<uintptr_t>(p.k) | reinterpret_cast<uintptr_t>(p.v)) & 31u) == 0;
-    const dim3 grid((unsigned)((p.num_tokens * p.kv_heads * (head_dim / kKv4Group) + 255) / 256)), block(256);
+    const dim3 grid((unsigned)((p.num_tokens * p.kv_heads * (head_dim / kKv4Group) + kThreads - 1) / kThreads)),
+        block(kThreads);
     if (head_dim == 128)
       e = dt == PA_BF16 ? launch_pdl(dequantize_kernel<128, __nv_bfloat16>, grid, block, 0, stream, p)
                         : launch_pdl(dequantize_kernel<128, __half>, grid, block, 0, stream, p);
