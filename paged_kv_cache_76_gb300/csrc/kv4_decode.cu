@@ -31,7 +31,10 @@
 // (50 and 154: CTAs that hold ends of two lists take their latencies twice, and
 // the merge has more to find out); five CTAs an SM at 96 registers (56 and 161);
 // rings of 3 or 6 tiles (no difference); first partitions of all requests first
-// (41 and 152).  A copy of a page by the bulk engine is issued lane by lane, 15
+// (41 and 152); of 16 columns, Q's fragments in shared memory, which leaves four
+// CTAs an SM instead of three (4 queries for each of the 64: 66 us either way).
+// Over its active cycles an SM issues in 43 to 77 % of them at 64 requests: the last
+// of its partitions run with few beside them.  A copy of a page by the bulk engine is issued lane by lane, 15
 // instructions each, which is why 16-byte copies win: 334 instructions a tile
 // against 378.
 //
