@@ -4,7 +4,7 @@
 //
 // fork_blocks keeps no counts from call to call.  What a page is, follows from
 // the tables that go on: state[b] of block b is
-//   kFree  no new row holds it;
+//   kFree  no new row holds it (kPinned: and it is pinned);
 //   i >= 0 only rows that go on writing inside it hold it, i the first of them:
 //          row i keeps it, the others get copies;
 //   kHeld  some row holds it and does not write inside it: writers get copies.
@@ -18,8 +18,9 @@
 //           blocks; the pages that new rows write in
 //   count   free pages of each warp's span of blocks; pages that each row needs,
 //           summed up
-//   list    the first free pages, as many as are needed, in order
-//   write   tables, lengths, pairs and slots
+//   write   tables, lengths, pairs and slots; a row finds its free pages by the
+//           counts before each span and a vote in the span (a list of them all,
+//           made before, was one more barrier: 16.4 us for the last two below)
 //
 // The steps are dependent and small: a table of 64 sequences of 4096 tokens is
 // 64 KB, so what they cost is the barriers between them.  Small batches are one
@@ -36,11 +37,13 @@ namespace {
 
 constexpr int kFree = 0x7F7F7F7F;
 constexpr int kHeld = -1;
+constexpr int kPinned = -2;
 constexpr unsigned kAll = 0xffffffffu;
 constexpr int kCtaThreads = 512;   // of the one CTA of small batches
 constexpr int kGridThreads = 256;  // of a CTA per SM
 constexpr int kMaxWarps = 16;
-constexpr int kColumns = 512;  // of a row that a warp takes at a time
+constexpr int kMaxSpans = 2048;  // of blocks, a warp's each
+constexpr int kColumns = 512;    // of a row that a warp takes at a time
 
 __device__ __forceinline__ int warps_per_cta() { return (int)blockDim.x >> 5; }
 
@@ -101,9 +104,8 @@ __device__ __forceinline__ bool needs_copy(const ForkParams& p, const Row& w, in
   return w.tail >= 0 && (ld_scratch(p.state + w.tail) != i || (p.pinned && __ldg(p.pinned + w.tail)));
 }
 
-__device__ __forceinline__ bool is_free(const ForkParams& p, int b) {
-  return ld_scratch(p.state + b) == kFree && !(p.pinned && __ldg(p.pinned + b));
-}
+// after step_count
+__device__ __forceinline__ bool is_free(const ForkParams& p, int b) { return ld_scratch(p.state + b) == kFree; }
 
 __device__ void step_clear(const ForkParams& p, int rank, int ranks) {
   for (int b = rank * (int)blockDim.x + threadIdx.x; b < p.num_blocks; b += ranks * (int)blockDim.x) p.state[b] = kFree;
@@ -165,7 +167,11 @@ __device__ void step_count(const ForkParams& p, int rank, int ranks) {
   const int b1 = (int)min((int64_t)p.num_blocks, b0 + span);
   int n = 0;
 #pragma unroll 4
-  for (int64_t b = b0 + lane; b < b1; b += 32) n += is_free(p, (int)b);
+  for (int64_t b = b0 + lane; b < b1; b += 32) {
+    const bool pinned = p.pinned && __ldg(p.pinned + b), free = ld_scratch(p.state + b) == kFree;
+    if (free && pinned) p.state[b] = kPinned;
+    n += free && !pinned;
+  }
   n = __reduce_add_sync(kAll, n);
   if (lane == 0) p.warp_free[warp] = n;
 }
@@ -203,94 +209,138 @@ __device__ void step_rows(const ForkParams& p, const Row* held) {
   if (threadIdx.x == 0) *p.needed = (int)min(before, (int64_t)INT32_MAX);
 }
 
-__device__ void step_list(const ForkParams& p, int rank, int ranks) {
-  __shared__ int part[kMaxWarps];
-  __shared__ int total;
+// Free pages before each warp's span (before[warps]: of all), worked out by every
+// CTA for itself.
+__device__ void sum_up(const ForkParams& p, int rank, int ranks, int* before) {
+  __shared__ int sums[kMaxWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int mine = rank * warps_per_cta() + warp, warps = ranks * warps_per_cta();
-  // free pages before this CTA's spans, and of all
-  int before = 0, all = 0;
-  for (int w = threadIdx.x; w < warps; w += (int)blockDim.x) {
-    const int n = ld_scratch(p.warp_free + w);
-    all += n;
-    if (w < rank * warps_per_cta()) before += n;
+  const int warps = ranks * warps_per_cta(), per = (warps + (int)blockDim.x - 1) / (int)blockDim.x;
+  const int w0 = min((int)threadIdx.x * per, warps), w1 = min(w0 + per, warps);
+  int n = 0;
+  for (int w = w0; w < w1; ++w) {
+    const int f = ld_scratch(p.warp_free + w);
+    before[w] = f;
+    n += f;
   }
-  before = __reduce_add_sync(kAll, before);
-  all = __reduce_add_sync(kAll, all);
-  if (threadIdx.x == 0) total = 0;
+  int x = n;  // inclusive in the warp
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(kAll, x, o);
+    if (lane >= o) x += y;
+  }
+  if (lane == 31) sums[warp] = x;
   __syncthreads();
-  if (lane == 0) {
-    part[warp] = before;
-    atomicAdd(&total, all);
+  int at = x - n, total = 0;
+  for (int w = 0; w < warps_per_cta(); ++w) {
+    if (w < warp) at += sums[w];
+    total += sums[w];
   }
+  for (int w = w0; w < w1; ++w) {
+    const int f = before[w];
+    before[w] = at;
+    at += f;
+  }
+  if (threadIdx.x == 0) before[warps] = total;
   __syncthreads();
-  int at = 0;
-  for (int w = 0; w < warps_per_cta(); ++w) at += part[w];
-  const int needed = ld_scratch(p.needed);
-  if (rank == 0 && threadIdx.x == 0) {
-    const bool short_of = needed > total;
-    if (short_of) record_error(p.err, PA_DEVERR_NO_BLOCKS);
-    *p.num_free = short_of ? total : total - needed;
-    *p.refused = short_of;
+}
+
+// The warp writes free pages k, k + 1, ... to dst[0 .. n), the first of them to
+// `near` too: there are that many.
+constexpr int kNear = 32;
+__device__ void put_free(const ForkParams& p, int ranks, const int* before, int k, int n, int32_t* dst, int* near) {
+  const int lane = threadIdx.x & 31, span = span_of(p, ranks);
+  const int warps = ranks * warps_per_cta();
+  int lo = 0, hi = warps;  // before[lo] <= k < before[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (before[mid] <= k) lo = mid;
+    else hi = mid;
   }
-  for (int w = rank * warps_per_cta(); w < mine; ++w) at += ld_scratch(p.warp_free + w);
-  const int span = span_of(p, ranks);
-  const int64_t b0 = (int64_t)mine * span;
-  const int b1 = (int)min((int64_t)p.num_blocks, b0 + span);
-  for (int64_t b = b0; b < b1 && at < needed; b += 32) {
-    const bool f = b + lane < b1 && is_free(p, (int)b + lane);
-    const unsigned v = __ballot_sync(kAll, f);
-    const int k = at + __popc(v & ((1u << lane) - 1u));
-    if (f && k < needed) p.list[k] = (int)b + lane;  // at most num_blocks free pages: k < num_blocks
-    at += __popc(v);
+  for (int done = 0; done < n && lo < warps; ++lo) {
+    int at = before[lo];
+    if (before[lo + 1] == at) continue;
+    const int64_t b0 = (int64_t)lo * span;
+    const int b1 = (int)min((int64_t)p.num_blocks, b0 + span);
+    for (int64_t b = b0; b < b1 && done < n; b += 32) {
+      const bool f = b + lane < b1 && is_free(p, (int)b + lane);
+      const unsigned v = __ballot_sync(kAll, f);
+      const int j = at + __popc(v & ((1u << lane) - 1u)) - k;
+      if (f && j >= 0 && j < n) {
+        dst[j] = (int)b + lane;
+        if (j < kNear) near[j] = (int)b + lane;
+      }
+      at += __popc(v);
+      done = at - k;
+    }
   }
-  __syncthreads();  // total and part may be used again
 }
 
 __device__ void step_write(const ForkParams& p, const Row* held, int rank, int ranks) {
+  __shared__ int before[kMaxSpans + 1], nears[kMaxWarps][kNear];
+  int* near = nears[threadIdx.x >> 5];
+  sum_up(p, rank, ranks, before);
   const int lane = threadIdx.x & 31;
   const int chunks = (p.maxblk_out + kColumns - 1) / kColumns;
   const int64_t items = (int64_t)p.num_new * chunks;
-  const bool refused = ld_scratch(p.refused) != 0;
+  const int total = before[ranks * warps_per_cta()], needed = ld_scratch(p.needed);
+  const bool refused = needed > total;
+  if (rank == 0 && threadIdx.x == 0) {
+    if (refused) record_error(p.err, PA_DEVERR_NO_BLOCKS);
+    *p.num_free = refused ? total : total - needed;
+  }
   for (int64_t it = (int64_t)rank * warps_per_cta() + (threadIdx.x >> 5); it < items;
        it += (int64_t)ranks * warps_per_cta()) {
     const int i = (int)(it / chunks), c0 = (int)(it - (int64_t)i * chunks) * kColumns;
     const int end = min(p.maxblk_out, c0 + kColumns);
     int32_t* dst = p.tables_out + (size_t)i * p.maxblk_out;
     const Row w = refused ? Row{kNone, 0, 0, -1} : row_of(p, held, i);
-    const int have = have_of(p, w), want = want_of(p, w), grow = max(w.grow, 0);
+    const int want = want_of(p, w), grow = max(w.grow, 0);
     const bool copy = needs_copy(p, w, i);
+    const int shared = have_of(p, w) - copy;  // the parent's blocks, and fresh ones from here on
+    const int f0 = max(c0, shared), f1 = min(end, want);
     const int32_t* src = p.tables + (size_t)max(w.parent, 0) * p.maxblk;
-    const int32_t* fresh = p.list + (want > have || copy ? ld_scratch(p.row_start + i) : 0);
-    for (int j = c0 + lane; j < end; j += 8 * 32) {
-      int b[8];
+    int b[8];
+    auto load = [&](int j) {
+#pragma unroll
+      for (int k = 0; k < 8; ++k) b[k] = j + 32 * k < min(end, shared) ? __ldcg(src + j + 32 * k) : -1;
+    };
+    auto store = [&](int j) {
 #pragma unroll
       for (int k = 0; k < 8; ++k) {
         const int c = j + 32 * k;
-        b[k] = -1;
-        if (c < end && c < want)
-          b[k] = c >= have ? ld_scratch(fresh + copy + c - have) : copy && c == have - 1 ? ld_scratch(fresh) : __ldcg(src + c);
+        if (c < end && (c < shared || c >= want)) dst[c] = b[k];
       }
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if (j + 32 * k < end) dst[j + 32 * k] = b[k];
+    };
+    load(c0 + lane);  // on their way while free pages are looked for
+    if (f0 < f1) put_free(p, ranks, before, ld_scratch(p.row_start + i) + f0 - shared, f1 - f0, dst + f0, near);
+    store(c0 + lane);
+    for (int j = c0 + lane + 8 * 32; j < end; j += 8 * 32) {
+      load(j);
+      store(j);
     }
-    if (c0 == 0) {
-      if (lane == 0) {
-        p.lens_out[i] = w.len + grow;
+    __syncwarp();
+    auto page = [&](int c) {  // of a new token's column, as it has just been written
+      return c < shared ? w.tail : c - f0 < kNear ? near[c - f0] : ld_scratch(dst + c);
+    };
+    if (lane == 0) {
+      if (c0 == 0) p.lens_out[i] = w.len + grow;
+      if (copy ? shared >= c0 && shared < end : c0 == 0) {
         p.pairs[2 * i] = copy ? w.tail : -1;
-        p.pairs[2 * i + 1] = copy ? ld_scratch(fresh) : -1;
-      }
-      for (int t = lane; t < p.max_grow; t += 32) {
-        int slot = -1;
-        if (t < grow) {
-          const int pos = w.len + t, c = pos >> p.block_shift;
-          const int b = c >= have ? ld_scratch(fresh + copy + c - have) : copy ? ld_scratch(fresh) : __ldcg(src + c);
-          if (b >= 0 && b < p.num_blocks) slot = b * p.block_size + (pos & (p.block_size - 1));
-        }
-        p.slots[(size_t)i * p.max_grow + t] = slot;
+        p.pairs[2 * i + 1] = copy ? page(shared) : -1;
       }
     }
+    // slots of the new tokens in these columns; those of no token with the first
+    int32_t* slots = p.slots + (size_t)i * p.max_grow;
+    const int64_t bs = p.block_size;
+    const int t0 = (int)min((int64_t)grow, max(c0 * bs - w.len, (int64_t)0));
+    const int t1 = (int)min((int64_t)grow, max(end * bs - w.len, (int64_t)0));
+    for (int t = t0 + lane; t < t1; t += 32) {
+      const int pos = w.len + t, b = page(pos >> p.block_shift);
+      slots[t] = b >= 0 && b < p.num_blocks ? b * p.block_size + (pos & (p.block_size - 1)) : -1;
+    }
+    if (c0 == 0)
+      for (int t = grow + lane; t < p.max_grow; t += 32) slots[t] = -1;
+    __syncwarp();  // near is another row's next
   }
 }
 
@@ -306,8 +356,6 @@ __device__ __forceinline__ void fork_steps(const ForkParams& p, int rank, int ra
   if (rank == ranks - 1) step_rows(p, held);
   step_count(p, rank, ranks);
   sync();
-  step_list(p, rank, ranks);
-  sync();
   step_write(p, held, rank, ranks);
 }
 
@@ -317,11 +365,9 @@ __global__ void __launch_bounds__(kCtaThreads) fork_cta_kernel(const ForkParams 
   griddep_wait();  // and no early start of the next kernel, which may read the tables before it waits
   ForkParams p = p0;
   p.state = scratch;
-  p.list = p.state + p.num_blocks;
-  p.row_start = p.list + p.num_blocks;
+  p.row_start = p.state + p.num_blocks;
   p.warp_free = p.row_start + p.num_new;
   p.needed = p.warp_free + kMaxWarps;
-  p.refused = p.needed + 1;
   fork_steps(p, 0, 1, [] { __syncthreads(); });
 }
 
@@ -363,22 +409,21 @@ __global__ void __launch_bounds__(256) copy_pages_kernel(const __grid_constant__
 }
 
 constexpr int kCtaBlocks = 16384;
-int cta_scratch(int num_blocks, int num_new) { return (2 * num_blocks + num_new + kMaxWarps + 2) * 4; }
+int cta_scratch(int num_blocks, int num_new) { return (num_blocks + num_new + kMaxWarps + 1) * 4; }
 
 int fork_ranks() {
-  const int sms = num_sms();
-  return sms > 0 ? sms : 1;
+  const int sms = num_sms(), most = kMaxSpans / (kGridThreads / 32);
+  return sms > most ? most : sms > 0 ? sms : 1;
 }
 
 }  // namespace
 
-// state, warp_free, row_start, list, needed, refused
+// state, row_start, warp_free, needed
 ForkWorkspace fork_workspace_layout(int num_new, int num_blocks) {
   auto al = [](size_t x) { return (x + 255) & ~size_t(255); };
   ForkWorkspace w{};
   w.state = 0;
-  w.list = al((size_t)num_blocks * 4);
-  w.row_start = w.list + al((size_t)num_blocks * 4);
+  w.row_start = al((size_t)num_blocks * 4);
   w.warp_free = w.row_start + al((size_t)num_new * 4);
   w.needed = w.warp_free + al((size_t)fork_ranks() * (kGridThreads / 32) * 4);
   w.bytes = w.needed + 256;
@@ -387,9 +432,10 @@ ForkWorkspace fork_workspace_layout(int num_new, int num_blocks) {
 
 cudaError_t launch_fork_blocks(const ForkParams& p, cudaStream_t stream) {
   // Entries that the steps go over, up to which one CTA is the faster: it needs no
-  // barrier of the whole grid, about two microseconds each.  Measured on GB300 (us,
-  // one CTA and a CTA per SM): 16 rows of <= 95 blocks 5.7 and 12; 512 of <= 256
-  // 70 and 15.8; 64 of <= 8190 (more blocks than it has room for) 16.1.
+  // barrier of the whole grid, about two microseconds each.  Measured on GB300 with
+  // the list (us, one CTA and a CTA per SM): 16 rows of <= 95 blocks 5.7 and 12; 512
+  // of <= 256 70 and 15.8; 64 of <= 8190 (more blocks than it has room for) 16.1.
+  // Without it 6.4, 14.9 and 14.5 by the form that is taken.
   constexpr int64_t kCtaWork = 48 << 10;
   const int64_t work = (int64_t)p.num_old * p.maxblk + (int64_t)p.num_new * p.maxblk_out + p.num_blocks;
   if (p.num_blocks <= kCtaBlocks && p.num_new <= kHeldRows && work <= kCtaWork) {

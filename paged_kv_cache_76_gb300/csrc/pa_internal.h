@@ -376,16 +376,14 @@ struct ForkParams {
   int32_t* slots;          // [num_new][max_grow]
   int32_t* num_free;
   int32_t* state;          // scratch
-  int32_t* list;
   int32_t* row_start;
   int32_t* warp_free;
   int32_t* needed;
-  int32_t* refused;
   int* err;
   int num_old, maxblk, num_new, maxblk_out, max_grow, num_blocks, block_size, block_shift;
 };
 struct ForkWorkspace {
-  size_t state, list, row_start, warp_free, needed, bytes;  // refused: the word behind needed
+  size_t state, row_start, warp_free, needed, bytes;
 };
 ForkWorkspace fork_workspace_layout(int num_new, int num_blocks);
 cudaError_t launch_fork_blocks(const ForkParams& p, cudaStream_t stream);

@@ -413,11 +413,9 @@ int pa_fork_blocks(const int32_t* block_tables, int max_blocks_per_seq, const in
   p.slots = slots;
   p.num_free = num_free;
   p.state = reinterpret_cast<int32_t*>(ws + w.state);
-  p.list = reinterpret_cast<int32_t*>(ws + w.list);
   p.row_start = reinterpret_cast<int32_t*>(ws + w.row_start);
   p.warp_free = reinterpret_cast<int32_t*>(ws + w.warp_free);
   p.needed = reinterpret_cast<int32_t*>(ws + w.needed);
-  p.refused = p.needed + 1;
   p.err = err;
   p.num_old = num_seqs;
   p.maxblk = max_blocks_per_seq;

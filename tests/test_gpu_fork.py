@@ -151,6 +151,29 @@ def test_large_batches(ops, rows, new, width, num_blocks):
     check(ops, tables, lens, parents, rng.integers(0, 4, new).tolist(), num_blocks, bs, width + 1, 3)
 
 
+@pytest.mark.parametrize("num_blocks", [6000, 90000])
+def test_growth_by_whole_prompts(ops, num_blocks):
+    """Rows that take up to 1300 pages at a time, round scattered pinned ones, down to the last page of the pool."""
+    rng = np.random.default_rng(num_blocks)
+    bs, parents, grow = 4, [-1, 0, 0, -1, 1, -2, -1], [5200, 2049, 1, 130, 0, 0, 7]
+    lens = [2046, 9]
+    held = rng.permutation(num_blocks)[:515]
+    tables = np.full((2, 512), -1)
+    tables[0], tables[1, :3] = held[:512], held[512:]
+    free = np.setdiff1d(np.arange(num_blocks), held)
+    pinned = rng.permutation(free)[:len(free) // 3].tolist()
+    pinned += [int(held[0]), int(held[514])]
+    got = check(ops, tables, lens, parents, grow, num_blocks, bs, 1500, 5200, pinned)
+    left = int(got[4])
+    assert left > 0
+    # the same with all but the pages that it takes pinned: none left; with one more: too few
+    used = set(got[0].flatten().tolist()) - {-1}
+    rest = [int(b) for b in np.setdiff1d(free, list(used))]
+    check(ops, tables, lens, parents, grow, num_blocks, bs, 1500, 5200, sorted(set(pinned) | set(rest)))
+    last = max(used - set(held.tolist()))
+    check(ops, tables, lens, parents, grow, num_blocks, bs, 1500, 5200, sorted(set(pinned) | set(rest) | {last}), error=10)
+
+
 def test_many_rows(ops):
     rng = np.random.default_rng(5)
     rows, bs, num_blocks = 65535, 4, 70000
