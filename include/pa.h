@@ -763,7 +763,8 @@ int pa_decode_kv4(const void* q, const void* k_cache, const void* v_cache, const
  * request r sees tokens [0, context_lens[r] - chunk + i].
  *   q, out        [total_q][q_heads][head_dim], packed by q_start
  *   q_start       int32 [num_reqs + 1], non-decreasing, q_start[num_reqs] <= total_q
- *   max_q_len     host-side upper bound of any chunk length (sizes the grid)
+ *   max_q_len     host-side upper bound of any chunk length (sizes the grid); 0
+ *                 only in a batch without requests or queries, which is no work
  *   scale         a normal number, of either sign
  *   split_tokens  keys of a partition: 0, or a multiple of 64.  0 cuts contexts
  *                 where there are fewer units of 256 (query, group head) rows of

@@ -105,9 +105,11 @@ struct Kv4PrefillSetup {
 
 int kv4_prefill_setup(int num_reqs, int total_q, int max_q_len, int q_heads, int kv_heads, int head_dim,
                       int max_blocks_per_seq, int block_size, int split_tokens, Kv4PrefillSetup* s) {
-  if (num_reqs < 0 || num_reqs > 65535 || total_q < 0 || max_q_len < 1 || q_heads <= 0 || kv_heads <= 0 ||
-      kv_heads > 1024 || q_heads % kv_heads != 0 || q_heads / kv_heads > 16 || head_dim <= 0 ||
-      max_blocks_per_seq <= 0 || !block_size_ok(block_size))
+  // chunks of no query: only where there are none, or no requests
+  if (num_reqs < 0 || num_reqs > 65535 || total_q < 0 || max_q_len < 0 ||
+      (max_q_len == 0 && num_reqs > 0 && total_q > 0) || q_heads <= 0 || kv_heads <= 0 || kv_heads > 1024 ||
+      q_heads % kv_heads != 0 || q_heads / kv_heads > 16 || head_dim <= 0 || max_blocks_per_seq <= 0 ||
+      !block_size_ok(block_size))
     return PA_ERR_INVALID;
   const int64_t cap = (int64_t)max_blocks_per_seq * block_size;
   const int64_t rows = (int64_t)max_q_len * (q_heads / kv_heads);
@@ -130,6 +132,7 @@ int kv4_prefill_setup(int num_reqs, int total_q, int max_q_len, int q_heads, int
     const int64_t units = (int64_t)num_reqs * kv_heads * s->row_tiles, tiles = whole / kKv4PrefillUnit;
     const int64_t merge_bytes = (int64_t)num_reqs * max_q_len * q_heads * 128 * 8;  // at most
     int64_t best = 0;
+    split = whole;  // of no units
     for (int64_t parts = 1; units > 0 && parts <= 64 && (parts == 1 || parts * kKv4PrefillMin <= cap); ++parts) {
       const int64_t rounds = (units * parts + sms - 1) / sms;
       const int64_t cost = rounds * (28 + 3 * ((tiles + parts - 1) / parts)) +
@@ -320,7 +323,7 @@ int pa_chunked_prefill_kv4(const void* q, const int32_t* q_start, const int32_t*
   st = kv4_prefill_setup(num_reqs, total_q, max_q_len, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size,
                          split_tokens, &s);
   if (st != PA_OK) return st;
-  if (num_reqs == 0 || total_q == 0) return PA_OK;
+  if (num_reqs == 0 || max_q_len == 0 || total_q == 0) return PA_OK;
   if (!q || !q_start || !context_lens || !k_cache || !v_cache || !block_tables || !out) return PA_ERR_INVALID;
   if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out)) return PA_ERR_INVALID;
   if (s.ws.bytes > 0 && (!workspace || workspace_bytes < s.ws.bytes || !aligned16(workspace)))
