@@ -185,7 +185,7 @@ __device__ __forceinline__ int tree_unit(const PrefillParams& p, const TreeParam
   w.p0 = q.hist;
   w.rows = q.n * p.group;
   w.k0 = w.part * tp.split_tokens;
-  w.kend = min(q.ctx, w.k0 + tp.split_tokens);
+  w.kend = partition_end(w.k0, tp.split_tokens, q.ctx);
   if (w.row0 < w.rows && w.k0 < w.kend) w.ntiles = (w.kend - w.k0 + kKeys - 1) / kKeys;
   return 0;
 }

@@ -147,13 +147,13 @@ __global__ void __launch_bounds__(WARPS * 32)
     }
     if (ctx > mapped && !bad_slot) bad_len = true;
   }
-  const int nsplit = (ctx - p.tok_begin + p.split_tokens - 1) / p.split_tokens;
+  const int nsplit = partitions_of(ctx - p.tok_begin, p.split_tokens);
   const bool active = c < (nsplit > 0 ? nsplit : (p.always_partial ? 0 : 1));
   const int G = p.group;
   const int NC = G * p.q_len;  // columns: (query i, head) pairs, i-major
   const int qh0 = h * G;
   const int tok0 = p.tok_begin + c * p.split_tokens;
-  const int tok1 = min(tok0 + p.split_tokens, ctx);
+  const int tok1 = partition_end(tok0, p.split_tokens, ctx);
   const int load_end = min(tok1, mapped);  // == tok1 unless a contiguous slot is short of memory
   const int ntiles = active && load_end > tok0 ? (load_end - tok0 + 15) >> 4 : 0;
   const int blk0 = tok0 / p.block_size;
@@ -499,7 +499,7 @@ __device__ __forceinline__ void merge_row_by_cta(const MergeParams& p, int row) 
   const int r = row / (p.q_heads * p.q_len);
   int ctx = __ldg(p.lens + r);
   ctx = ctx < p.tok_begin ? p.tok_begin : (ctx > p.cap ? p.cap : ctx);
-  const int nsplit = p.extra_slots + (ctx - p.tok_begin + p.split_tokens - 1) / p.split_tokens;
+  const int nsplit = p.extra_slots + partitions_of(ctx - p.tok_begin, p.split_tokens);
   if (nsplit <= 1 && !p.always) return;  // pa_decode_partial wrote this row directly
   const float* pm = p.part_m + (size_t)row * p.max_splits;
   const float* pl = p.part_l + (size_t)row * p.max_splits;
@@ -564,7 +564,7 @@ __device__ __forceinline__ void merge_row_by_warp(const MergeParams& p, int row)
   const int r = row / (p.q_heads * p.q_len);
   int ctx = __ldg(p.lens + r);
   ctx = ctx < p.tok_begin ? p.tok_begin : (ctx > p.cap ? p.cap : ctx);
-  const int nsplit = p.extra_slots + (ctx - p.tok_begin + p.split_tokens - 1) / p.split_tokens;
+  const int nsplit = p.extra_slots + partitions_of(ctx - p.tok_begin, p.split_tokens);
   if (nsplit <= 1 && !p.always) return;  // pa_decode_partial wrote this row directly
   const float* pm = p.part_m + (size_t)row * p.max_splits;
   const float* pl = p.part_l + (size_t)row * p.max_splits;
@@ -708,7 +708,7 @@ __device__ __forceinline__ void add_weights(const AccumulateParams& p, int part)
   if (p.score_rows)
     for (int i = tid; i < r; i += threads) twice |= __ldg(p.score_rows + i) == row;
   const int G = p.group;
-  const int nsplit = (ctx + p.split_tokens - 1) / p.split_tokens;
+  const int nsplit = partitions_of(ctx, p.split_tokens);
   for (int g = warp; g < GP; g += threads / 32) {
     // M and W of the head in one pass over its partitions: each lane the
     // largest reference of its own and its sum brought to that, then the warp's

@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
   int ctx = __ldg(p.lens + r);
   const bool bad_len = ctx < 0 || ctx > cap;
   ctx = min(max(ctx, 0), cap);
-  const int nsplit = (ctx + p.split_tokens - 1) / p.split_tokens;
+  const int nsplit = partitions_of(ctx, p.split_tokens);
   const int G = p.group, NC = G * p.q_len, qh0 = h * G;
   if (c >= max(nsplit, 1)) {
     griddep_wait();
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(kWarps * 32, D == 128 && NT == 2 ? 3 : 4) kv4_
   }
   const bool joins = JOIN && nsplit > 1;
   if (joins) cluster_arrive();  // CTAs without tokens have left, and no one writes to them
-  const int tok0 = c * p.split_tokens, tok1 = min(tok0 + p.split_tokens, ctx);
+  const int tok0 = c * p.split_tokens, tok1 = partition_end(tok0, p.split_tokens, ctx);
   const int ntiles = (tok1 - tok0 + kTile - 1) / kTile;  // of the CTA
 
   // row of column n in q, out and the partials

@@ -143,7 +143,7 @@ __device__ __forceinline__ Unit unit_of(const Kv4PrefillParams& p, int u) {
   if (w.row0 >= w.rows) return w;
   const int last_row = min(w.row0 + 2 * kRows, w.rows) - 1;
   w.k0 = w.part * p.split_tokens;
-  w.kend = min(w.p0 + last_row / p.group + 1, w.k0 + p.split_tokens);
+  w.kend = partition_end(w.k0, p.split_tokens, w.p0 + last_row / p.group + 1);
   if (w.k0 < w.kend) w.ntiles = (w.kend - w.k0 + kKeys - 1) / kKeys;
   return w;
 }
@@ -636,7 +636,7 @@ __global__ void __launch_bounds__(256) kv4_prefill_merge_kernel(const Kv4Prefill
   const int qi = (int)(at / p.q_heads), head = (int)(at - (int64_t)qi * p.q_heads);
   const int rows = chunk * G, grow = qi * G + head % G;
   const int last_row = min((grow / (2 * kRows) + 1) * 2 * kRows, rows) - 1;  // of the row's tiles
-  const int nsplit = (p0 + last_row / G + p.split_tokens) / p.split_tokens;
+  const int nsplit = partitions_of(p0 + last_row / G + 1, p.split_tokens);
   const size_t orow = (size_t)(qs + qi) * p.q_heads + head;
   const float* pm = p.part_m + orow * p.max_splits;
   const float* pl = p.part_l + orow * p.max_splits;

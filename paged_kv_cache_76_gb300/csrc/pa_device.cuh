@@ -441,6 +441,19 @@ __device__ __forceinline__ void griddep_launch_dependents() {
 }
 
 // ----------------------------------------------------------------------------
+// partitions of a context
+// ----------------------------------------------------------------------------
+// How many partitions of `split` tokens n tokens make, and the end of the one
+// that begins at t0.  Neither is negative, but with a partition's size a length
+// may pass 2^31: the sums have no sign.
+__device__ __forceinline__ int partitions_of(int n, int split) {
+  return (int)(((uint32_t)n + (uint32_t)split - 1u) / (uint32_t)split);
+}
+__device__ __forceinline__ int partition_end(int t0, int split, int end) {
+  return (int)min((uint32_t)t0 + (uint32_t)split, (uint32_t)end);
+}
+
+// ----------------------------------------------------------------------------
 // thread-block clusters
 // ----------------------------------------------------------------------------
 __device__ __forceinline__ uint32_t cluster_rank() {

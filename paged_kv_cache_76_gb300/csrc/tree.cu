@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(256) tree_merge_kernel(const TreeParams p) {
   if (tree_request(p, r, rq)) return;
   const int row = blockIdx.x * 8 + (threadIdx.x >> 5);
   if (row >= rq.n * p.q_heads || rq.ctx <= p.split_tokens) return;
-  const int nsplit = (rq.ctx + p.split_tokens - 1) / p.split_tokens;
+  const int nsplit = partitions_of(rq.ctx, p.split_tokens);
   const size_t orow = (size_t)rq.qs * p.q_heads + row;
   const float* pm = p.part_m + orow * p.max_splits;
   const float* pl = p.part_l + orow * p.max_splits;
