@@ -677,7 +677,7 @@ __device__ __forceinline__ void add_weights(const AccumulateParams& p, int part)
     if (row >= p.num_rows && t0 == 0 && tid == 0) record_error(p.err, PA_DEVERR_SCORE_ROW);
     return;
   }
-  const int end = min(ctx, p.score_len), t1 = min(t0 + p.chunk, end);
+  const int end = min(ctx, p.score_len), t1 = partition_end(t0, p.chunk, end);
   const size_t at = ((size_t)row * p.kv_heads + h) * p.score_len;
   const float* lg = p.logits + ((size_t)r * p.kv_heads + h) * p.cap * GP;
   float x[U][GP], old[U];

@@ -103,3 +103,35 @@ def test_prefill_kv4_under_tables_of_two_billion_tokens(ops, split):
     ops.chunked_prefill_kv4(q, i32(start), b.ctx, b.kc, b.vc, tables, 0.125, 170, out=out, split_tokens=split)
     assert ops.get_device_error() == 0
     b.check(out, q, 0.125, prefill_rows(lens, start))
+
+
+def test_scores_of_two_billion_tokens(ops):
+    """decode_accumulate: the second pass gives a CTA a stretch of two million tokens, the last of which ends past 2^31.
+    A token's weight is 2^-23 off by each sum that its denominator goes through (8192 tokens, then as many partitions
+    of a lane) beside its score's error."""
+    nb, bs, d, split = 64, 32, 64, 8192
+    width = (2 ** 31 - 1 - 4096) // bs
+    n = width * bs
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("18 GB of scores and scratch")
+    k, v, q = inputs(nb, bs, 1, d)
+    table = (torch.arange(width, dtype=torch.int32, device="cuda") % nb)[None].contiguous()
+    scores = torch.zeros(1, 1, n, device="cuda")
+    out, _ = ops.decode_accumulate(q, k.view(nb, bs, 1, d), v.view(nb, bs, 1, d), table, i32([n]), d ** -0.5, scores,
+                                   split_tokens=split)
+    assert ops.get_device_error() == 0
+    repeated(out[0], q[0], k[:, 0].double(), v[:, 0].double(), d ** -0.5, n, 2.0 ** -8, split)
+    x = (q[0].double() @ k[:, 0].double().T)[0] * d ** -0.5
+    times = torch.full((nb * bs,), n // (nb * bs), dtype=torch.float64, device="cuda")
+    times[:n % (nb * bs)] += 1
+    w = torch.exp(x - x.max())
+    w /= (w * times).sum()
+    err = (d + 4) * 2.0 ** -24 * d ** -0.5 * float((q[0].double().abs() @ k[:, 0].double().abs().T).max())
+    tol = 2 * (2 * 8192 + 64) * 2.0 ** -23 + 4 * err + 2.0 ** -19
+    for first in (0, n // 2 // 2048 * 2048, n - 2 ** 22 - (n % 2048)):  # stretches of whole rounds of the 2048 tokens
+        got = scores[0, 0, first:first + 2 ** 21].double().view(-1, nb * bs)
+        assert float(((got / w - 1).abs()).max()) < tol
+    last = n % (nb * bs)
+    assert float((scores[0, 0, n - last:].double() / w[:last] - 1).abs().max()) < tol
+    del scores
+    torch.cuda.empty_cache()
