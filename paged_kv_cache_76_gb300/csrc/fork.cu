@@ -176,7 +176,10 @@ __device__ void step_count(const ForkParams& p, int rank, int ranks) {
   if (lane == 0) p.warp_free[warp] = n;
 }
 
-// One CTA: where each row's pages start in the list, and how many are needed.
+// One CTA: how many free pages the rows before each row need, and all of them.  A
+// warp's rows together may need more than 32 bits hold: past kMany, more than a
+// pool has blocks (2^29), their sum stays there, and the batch is refused.
+constexpr int kMany = (1 << 30) - 1;
 __device__ void step_rows(const ForkParams& p, const Row* held) {
   __shared__ int sums[kMaxWarps];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -193,7 +196,7 @@ __device__ void step_rows(const ForkParams& p, const Row* held) {
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int y = __shfl_up_sync(kAll, x, o);
-      if (lane >= o) x += y;
+      if (lane >= o) x = min(x + y, kMany);
     }
     if (lane == 31) sums[warp] = x;
     __syncthreads();
