@@ -103,7 +103,7 @@ struct TcSmem {
   static constexpr int K_OFF = Q_OFF + 2 * QTILE;
   static constexpr int V_OFF = K_OFF + kKStages * Tile::BYTES;
   static constexpr int BAR_OFF = V_OFF + kVStages * Tile::BYTES;
-  static constexpr int NBARS = 2 * kKStages + 2 * kVStages + 15;
+  static constexpr int NBARS = 2 * kKStages + 2 * kVStages + 16;
   static constexpr int SLOT_OFF = BAR_OFF + NBARS * 8;
   static constexpr int BAD_OFF = SLOT_OFF + 8;  // TREE: drafted nodes with non-finite V (2 words)
   static constexpr int BYTES = SLOT_OFF + 16 + 1024;
@@ -122,7 +122,8 @@ constexpr int B_PFULL = B_SFULL + 4;           // [2 Q tiles][2 S buffers] P_x(j
 constexpr int B_OFULL = B_PFULL + 4;           // [2 Q tiles][2 S buffers] P.V_x(j) complete (commit)
 constexpr int B_QFULL = B_OFULL + 4;            // [2] Q_x of the next work unit in smem (four softmax warps)
 constexpr int B_MMADONE = B_QFULL + 2;
-static_assert(B_MMADONE + 1 == 2 * kKStages + 2 * kVStages + 15, "barrier count");
+constexpr int B_BEGUN = B_MMADONE + 1;         // tile A's first P is there (four softmax warps): once in a CTA's life
+static_assert(B_BEGUN + 1 == 2 * kKStages + 2 * kVStages + 16, "barrier count");
 
 // One work unit: a tile of 2 x 128 rows of one (request, KV head) for the
 // causal prefill, or of one (prefix key range, KV head) for the shared-prefix
@@ -275,6 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(bar(B_QFULL), 4);
     mbar_init(bar(B_QFULL + 1), 4);
     mbar_init(bar(B_MMADONE), 2);  // the two MMA issuers' last commits
+    mbar_init(bar(B_BEGUN), 4);
     fence_mbar_init();
     prefetch_tensormap(&kmap);
     prefetch_tensormap(&vmap);
@@ -404,9 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         // Q_x of this unit is in smem; the softmax warps have also finished
         // the previous unit (its last P.V completed and O_x was read out).
         if (!__all_sync(kAll, mbar_wait(bar(B_QFULL + x), nu & 1))) { ok = false; break; }
-        // Tile B starts half a key tile behind tile A (once P_A(0) is being
-        // written), so that the two softmaxes alternate instead of overlapping.
-        if (x == 1 && nu == 0 && !__all_sync(kAll, mbar_wait(bar(B_PFULL), 0))) { ok = false; break; }
+        // Tile B starts half a key tile behind tile A (once P_A(0) is there), so
+        // that the two softmaxes alternate instead of overlapping.  Not on A's P
+        // barrier: were B's Q two key tiles late, it would be a phase further, and
+        // A would wait for the K stages that B has yet to read.
+        if (x == 1 && nu == 0 && !__all_sync(kAll, mbar_wait(bar(B_BEGUN), 0))) { ok = false; break; }
         ++nu;
         for (int j = 0; ok && j < w.ntiles; ++j, ++gt) {
           const int sk = gt % kKStages, b = gt & 1;
@@ -606,6 +610,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(B_PFULL + 2 * x + sb));
+        if (x == 0 && gt == 0 && lane == 0) mbar_arrive(bar(B_BEGUN));
         if (!vok) ok = false;
         l += ((sx[0] + sy[0]) + (sx[1] + sy[1])) + ((sx[2] + sy[2]) + (sx[3] + sy[3]));
         if (!ok) break;
