@@ -736,6 +736,7 @@ int pa_dequantize_kv4(const void* k_cache, const void* v_cache, const int32_t* s
  *                 gives a zero row
  *   q_len         >= 1, with (q_heads / kv_heads) * q_len <= 32 and a group of at
  *                 most 16
+ *   scale         finite, of either sign, as is scale / ln 2
  *   split_tokens  0, or a multiple of 32 no larger than 1024 * block_size;
  *                 pa_decode_kv4_split_tokens returns the partition size such a
  *                 call uses, or PA_ERR_INVALID
@@ -766,7 +767,7 @@ int pa_decode_kv4(const void* q, const void* k_cache, const void* v_cache, const
  *   q_start       int32 [num_reqs + 1], non-decreasing, q_start[num_reqs] <= total_q
  *   max_q_len     host-side upper bound of any chunk length (sizes the grid); 0
  *                 only in a batch without requests or queries, which is no work
- *   scale         a normal number, of either sign
+ *   scale         a normal number, of either sign; scale / ln 2 is finite
  *   split_tokens  keys of a partition: 0, or a multiple of 64.  0 cuts contexts
  *                 where there are fewer units of 256 (query, group head) rows of
  *                 one (request, KV head) than SMs, by the width of block_tables.

@@ -237,7 +237,8 @@ int pa_decode_kv4(const void* q, const void* k_cache, const void* v_cache, const
                   void* workspace, size_t workspace_bytes, void* out, pa_dtype dtype, pa_stream stream) {
   int st = check_kv4_shape(num_blocks, block_size, kv_heads, head_dim, dtype);
   if (st != PA_OK) return st;
-  if (!std::isfinite(scale)) return PA_ERR_INVALID;
+  // in log2 units, as the scores are
+  if (!std::isfinite(scale * 1.4426950408889634f)) return PA_ERR_INVALID;
   Kv4DecodeSetup s;
   st = kv4_decode_setup(num_seqs, q_len, q_heads, kv_heads, head_dim, max_blocks_per_seq, block_size, split_tokens, &s);
   if (st != PA_OK) return st;
