@@ -768,9 +768,12 @@ int pa_decode_kv4(const void* q, const void* k_cache, const void* v_cache, const
  *   max_q_len     host-side upper bound of any chunk length (sizes the grid); 0
  *                 only in a batch without requests or queries, which is no work
  *   scale         a normal number, of either sign; scale / ln 2 is finite
- *   split_tokens  keys of a partition: 0, or a multiple of 64.  0 cuts contexts
- *                 where there are fewer units of 256 (query, group head) rows of
- *                 one (request, KV head) than SMs, by the width of block_tables.
+ *   split_tokens  keys of a partition: 0, or a multiple of 64.  0 takes the
+ *                 number of partitions that is the fastest by a count of rounds
+ *                 (units of 256 (query, group head) rows of one (request, KV
+ *                 head) over the SMs), by the width of block_tables: contexts may
+ *                 be cut although there are more units than SMs.
+ *                 pa_chunked_prefill_kv4_split_tokens tells it
  *   workspace     at least pa_chunked_prefill_kv4_workspace_size(...) bytes (NULL
  *                 where that is 0)
  * Rounding, and tokens that are not numbers, as pa_decode_kv4; refused requests

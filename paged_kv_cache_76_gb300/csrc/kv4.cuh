@@ -8,9 +8,10 @@
 //
 // A page is one block of one KV head, contiguous: block_size rows of
 // head_dim / 2 bytes of codes (byte i: element 2i in the low half, 2i + 1 in
-// the high), then block_size rows of head_dim / 16 scales.  One bulk copy
-// brings it, and its size is a multiple of 16 for every block size and
-// head_dim.  A cache is [num_blocks][kv_heads][page].
+// the high), then block_size rows of head_dim / 16 scales.  Both parts are a
+// multiple of 16 bytes for every block size and head_dim, so pages are copied as
+// they are (prefill: a bulk copy of each part; decode: vectors of 16 bytes).  A
+// cache is [num_blocks][kv_heads][page].
 #pragma once
 
 #include "pa_device.cuh"

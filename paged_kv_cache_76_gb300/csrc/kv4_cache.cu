@@ -64,8 +64,11 @@ __device__ __forceinline__ float largest(const uint4 (&v)[2]) {
 // The quotient x / s is taken as x * (1 / s) and one Newton step on its
 // remainder: exact wherever x / s is representable, which is what decides a
 // tie between two levels (x has at most 11 significant bits and s four, so
-// every other quotient is at least 2^-12 of itself away from one).  Nothing
-// overflows: |x| is at most 6.4 s, or s is the largest scale.
+// every other quotient is at least 2^-12 of itself away from one).  Quotients
+// beyond 6 become the level 6, the nearest, by the conversion's saturation: up to
+// 6.4 where s is rounded down at three bits, below 9 for the smallest scales
+// (2^-17 apart, so the first stands for up to 1.5 times itself), any that fp32
+// holds above the largest.
 template <typename T>
 __device__ __forceinline__ uint2 encode16(const uint4 (&v)[2], uint32_t& byte) {
   byte = kv4_scale_byte(largest<T>(v));

@@ -28,7 +28,7 @@ int check_kv4_shape(int num_blocks, int block_size, int kv_heads, int head_dim, 
 
 int log2_of(int bs) { return bs == 4 ? 2 : bs == 8 ? 3 : bs == 16 ? 4 : 5; }
 
-constexpr int kKv4SplitUnit = 32;  // a stage of the kernel
+constexpr int kKv4SplitUnit = 32;  // partitions begin with a block, of any size, and with a tile of 16 tokens
 
 struct Kv4DecodeSetup {
   int split, max_splits;
