@@ -609,8 +609,7 @@ int pa_verify_tree(const void* q, const int32_t* q_start, const uint64_t* tree_m
  *                 second pass has a block of threads for each stretch of it, too.
  *                 So cut the tables to the longest context: 64 requests of <= 4079
  *                 tokens, 32/8 heads, take 45 MB and 96 us then, 1.1 GB and 341 us
- *                 with tables for 131072; wider than 2^31 - 4097 tokens they are
- *                 refused
+ *                 with tables for 131072
  *   split_tokens  as pa_decode; 0 = the library's choice for this call, which
  *                 also depends on num_seqs and kv_heads
  *                 (pa_decode_accumulate_split_tokens tells it)

@@ -677,15 +677,16 @@ __device__ __forceinline__ void add_weights(const AccumulateParams& p, int part)
     if (row >= p.num_rows && t0 == 0 && tid == 0) record_error(p.err, PA_DEVERR_SCORE_ROW);
     return;
   }
-  const int end = min(ctx, p.score_len), t1 = partition_end(t0, p.chunk, end);
+  const int n = partition_end(t0, p.chunk, min(ctx, p.score_len)) - t0;  // tokens of this CTA: t0 and the n - 1 behind it
   const size_t at = ((size_t)row * p.kv_heads + h) * p.score_len;
   const float* lg = p.logits + ((size_t)r * p.kv_heads + h) * p.cap * GP;
   float x[U][GP], old[U];
-  auto load = [&](int tb) {
+  auto load = [&](int first) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int t = tb + u * threads + tid;
-      if (t < t1) {
+      const int i = first + u * threads + tid;
+      if (i < n) {
+        const int t = t0 + i;
         const float* src = lg + (size_t)t * GP;
         old[u] = p.scores[at + t];
         if constexpr (GP >= 4) {
@@ -703,7 +704,7 @@ __device__ __forceinline__ void add_weights(const AccumulateParams& p, int part)
       }
     }
   };
-  load(t0);
+  load(0);
   bool twice = false;  // an earlier request has this row: it alone keeps score
   if (p.score_rows)
     for (int i = tid; i < r; i += threads) twice |= __ldg(p.score_rows + i) == row;
@@ -749,17 +750,17 @@ __device__ __forceinline__ void add_weights(const AccumulateParams& p, int part)
     return;
   }
   if (ctx > p.score_len && t0 == 0 && tid == 0) record_error(p.err, PA_DEVERR_CONTEXT_LEN);
-  for (int tb = t0; tb < t1; tb += U * threads) {
-    if (tb > t0) load(tb);
+  for (int first = 0; first < n; first += U * threads) {
+    if (first > 0) load(first);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int t = tb + u * threads + tid;
-      if (t < t1) {
+      const int i = first + u * threads + tid;
+      if (i < n) {
         float w = 0.f;
 #pragma unroll
         for (int g = 0; g < GP; ++g)
           if (g < G) w += ex2_approx(x[u][g] - s_m[g]) * s_inv[g];
-        p.scores_out[at + t] = old[u] + w;
+        p.scores_out[at + t0 + i] = old[u] + w;
       }
     }
   }

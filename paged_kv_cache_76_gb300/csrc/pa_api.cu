@@ -916,8 +916,6 @@ int accumulate_setup(int num_seqs, int q_heads, int kv_heads, int head_dim, int 
   if (group > 16) return PA_ERR_INVALID;
   int split = pa_decode_split_tokens(max_blocks_per_seq, block_size, split_tokens);
   if (split <= 0) return PA_ERR_INVALID;
-  // the second pass counts a CTA's rounds of tokens, up to 4096, behind the last one
-  if ((int64_t)max_blocks_per_seq * block_size > INT32_MAX - 4096) return PA_ERR_INVALID;
   if (split_tokens == 0) {
     // A warp takes a partition.  Too few of them leave SMs without their 12
     // warps each: 256, 128 or 64 tokens then.  More than about 54 per SM only

@@ -106,11 +106,11 @@ def test_prefill_kv4_under_tables_of_two_billion_tokens(ops, split):
 
 
 def test_scores_of_two_billion_tokens(ops):
-    """decode_accumulate: the second pass gives a CTA a stretch of two million tokens, the last of which ends past 2^31.
-    A token's weight is 2^-23 off by each sum that its denominator goes through (8192 tokens, then as many partitions
+    """decode_accumulate: the second pass gives a CTA a stretch of two million tokens, the last of which, and its
+    rounds of 2048, end past 2^31.  A token's weight is 2^-23 off by each sum that its denominator goes through (8192 tokens, then as many partitions
     of a lane) beside its score's error."""
     nb, bs, d, split = 64, 32, 64, 8192
-    width = (2 ** 31 - 1 - 4096) // bs
+    width = (2 ** 31 - 1) // bs
     n = width * bs
     if torch.cuda.mem_get_info()[0] < 24 << 30:
         pytest.skip("18 GB of scores and scratch")
@@ -128,7 +128,7 @@ def test_scores_of_two_billion_tokens(ops):
     w /= (w * times).sum()
     err = (d + 4) * 2.0 ** -24 * d ** -0.5 * float((q[0].double().abs() @ k[:, 0].double().abs().T).max())
     tol = 2 * (2 * 8192 + 64) * 2.0 ** -23 + 4 * err + 2.0 ** -19
-    for first in (0, n // 2 // 2048 * 2048, n - 2 ** 22 - (n % 2048)):  # stretches of whole rounds of the 2048 tokens
+    for first in (0, n // 2 // 2048 * 2048, n - 2 ** 21 - (n % 2048)):  # stretches of whole rounds of the 2048 tokens
         got = scores[0, 0, first:first + 2 ** 21].double().view(-1, nb * bs)
         assert float(((got / w - 1).abs()).max()) < tol
     last = n % (nb * bs)
